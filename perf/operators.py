@@ -221,11 +221,11 @@ def prepare_pages(c, seed):
         data = torch.randint(0, 256, (2 * layers, num, G * page * D * width), generator=g, device=DEV,
                              dtype=torch.uint8)
         s["data"] = data if width == 1 else data.view(torch.int16)
-        s["pools"] = [p.view(num, G, page, D) for p in s["data"]]
+        s["pools"] = [s["data"].view(2 * layers, num, G, page, D)]     # one tensor for all layers
         if c["kind"] == "fp8":
             s["scales"] = torch.randint(-9, -4, (2 * layers, num, G, blocks_of(page)), generator=g,
                                         device=DEV).float().exp2()
-            s["pools"] += list(s["scales"])
+            s["pools"].append(s["scales"])
     s["table_out"], s["refs_out"] = torch.empty_like(s["table"]), torch.empty_like(s["refs"])
     s["lens_out"] = torch.empty_like(s["lens"])
     s["counts"] = torch.empty(2, dtype=torch.int32, device=DEV)
@@ -338,7 +338,7 @@ def run_fork(s):
     if own:
         import grouped_query_decode_gb300 as gq
         gq.gqa_pages_fork(s["pools"], s["src"], s["table"], s["lens"], s["refs"], page, s["table_out"],
-                          s["lens_out"], s["refs_out"], s["counts"])
+                          s["lens_out"], s["refs_out"], s["counts"], page_dim=1)
     else:
         src, table, refs = s["src"].long(), s["table"], s["refs"]
         B, most = table.shape
@@ -357,7 +357,7 @@ def run_fork(s):
         out[~first[:, None] & (j[None, :] >= full[:, None])] = -1
         out[copies, full[copies].long()] = new.to(torch.int32)
         for pool in s["pools"]:
-            pool[new] = pool[old]
+            pool[:, new] = pool[:, old]
         count = refs.clone()
         count.index_add_(0, table[table >= 0].long(), torch.full_like(table[table >= 0], -1))
         count.index_add_(0, out[out >= 0].long(), torch.ones_like(out[out >= 0]))
@@ -371,7 +371,8 @@ def run_fork(s):
 def run_compact(s):
     if own:
         import grouped_query_decode_gb300 as gq
-        gq.gqa_pages_compact(s["pools"], s["table"], s["refs"], s["table_out"], s["refs_out"], s["counts"])
+        gq.gqa_pages_compact(s["pools"], s["table"], s["refs"], s["table_out"], s["refs_out"], s["counts"],
+                             page_dim=1)
     else:
         table, refs = s["table"], s["refs"]
         live = int((refs > 0).sum())
@@ -380,7 +381,7 @@ def run_compact(s):
         to = torch.arange(refs.numel(), device=DEV)
         to[moved] = holes
         for pool in s["pools"]:
-            pool[holes] = pool[moved]
+            pool[:, holes] = pool[:, moved]
         s["table_out"].copy_(torch.where(table >= 0, to[table.clamp_min(0).long()].to(torch.int32), table))
         s["refs_out"].copy_(refs)
         s["refs_out"][holes] = refs[moved]
