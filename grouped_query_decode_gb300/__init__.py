@@ -15,6 +15,7 @@ None. Calls are enqueued on the current torch CUDA stream (or `stream`).
 from __future__ import annotations
 
 import ctypes
+import functools
 import threading
 
 from . import build as _build
@@ -40,6 +41,11 @@ class GQADecodeError(RuntimeError):
         if status == GQA_ERR_CUDA and _lib is not None:
             msg += f" (cudaError {gqa_decode_last_cuda_error()})"
         super().__init__(f"{what}: {msg}" if what else msg)
+
+
+class PagePoolT(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_size_t),
+                ("layer_bytes", ctypes.c_size_t), ("layers", ctypes.c_int)]
 
 
 class PlanT(ctypes.Structure):
@@ -72,6 +78,25 @@ def load():
             lib.gqa_decode_fp8.restype = i32
             lib.gqa_prefill.argtypes = [vp, vp, vp, vp, f32, vp, vp, *shape, vp]
             lib.gqa_prefill.restype = i32
+            paged = [i32] * 8
+            lib.gqa_decode_paged_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, f32, vp, vp, *paged, vp, sz, vp]
+            lib.gqa_decode_paged_fp8.restype = i32
+            lib.gqa_decode_paged_fp8_workspace_bytes.argtypes = [i32] * 7
+            lib.gqa_decode_paged_fp8_workspace_bytes.restype = sz
+            lib.gqa_append_paged_fp8.argtypes = [vp] * 8 + [i32] * 7 + [vp]
+            lib.gqa_append_paged_fp8.restype = i32
+            lib.gqa_pages_workspace_bytes.argtypes = [i32, i32]
+            lib.gqa_pages_workspace_bytes.restype = sz
+            lib.gqa_pages_copy.argtypes = [vp, i32, vp, vp, i32, i32, vp]
+            lib.gqa_pages_copy.restype = i32
+            lib.gqa_pages_reserve.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, sz, vp]
+            lib.gqa_pages_reserve.restype = i32
+            lib.gqa_pages_fork.argtypes = [vp, i32] + [vp] * 8 + [i32] * 4 + [vp, sz, vp]
+            lib.gqa_pages_fork.restype = i32
+            lib.gqa_pages_free.argtypes = [vp, vp, vp, vp, i32, i32, i32, vp]
+            lib.gqa_pages_free.restype = i32
+            lib.gqa_pages_compact.argtypes = [vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, vp, sz, vp]
+            lib.gqa_pages_compact.restype = i32
             lib.gqa_decode_noalloc.argtypes = [vp, vp, vp, vp, f32, vp, vp, *shape, vp]
             lib.gqa_decode_noalloc.restype = i32
             lib.gqa_decode_workspace_bytes.argtypes = shape
@@ -268,6 +293,244 @@ def gqa_decode_fp8(q, k_codes, v_codes, k_scale, v_scale, seq_lens, scale, out, 
                B, sq, H, G, D, Tmax, _stream_handle(stream, dev))
     if rc != GQA_OK:
         raise GQADecodeError(rc, "gqa_decode_fp8")
+
+
+def _paged_fp8_cache(dev, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens):
+    """Checks the tensors of a paged 8-bit cache; returns B, num_pages, G,
+    page_size, D and max_pages_per_seq."""
+    import torch
+    u8, f32, i32 = torch.uint8, torch.float32, torch.int32
+    _check(dev, "k_pages", k_pages, u8)
+    _check(dev, "v_pages", v_pages, u8)
+    _check(dev, "k_scale", k_scale, f32)
+    _check(dev, "v_scale", v_scale, f32)
+    _check(dev, "block_table", block_table, i32)
+    _check(dev, "seq_lens", seq_lens, i32)
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages / v_pages must be [num_pages, G, page_size, D]")
+    num_pages, G, page_size, D = k_pages.shape
+    blocks = (num_pages, G, (page_size + 63) // 64)
+    if k_scale.shape != blocks or v_scale.shape != blocks:
+        raise ValueError("k_scale / v_scale must be [num_pages, G, ceil(page_size/64)]")
+    if block_table.dim() != 2 or seq_lens.shape != block_table.shape[:1]:
+        raise ValueError("block_table must be [B, max_pages_per_seq] and seq_lens [B]")
+    B, most = block_table.shape
+    return B, num_pages, G, page_size, D, most
+
+
+def _workspace(nbytes, dev, stream):
+    """A buffer for one call from torch's allocator, in the order of the
+    call's stream (inside a graph capture, the graph's own memory)."""
+    import torch
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
+
+
+def gqa_decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, scale, out, lse=None,
+                         stream=None, workspace=None):
+    """Attention over a paged 8-bit cache, for any number of new tokens sq:
+    k_pages/v_pages [num_pages, G, page_size, D] uint8 e4m3 codes, k_scale/
+    v_scale [num_pages, G, ceil(page_size/64)] float32, block_table [B,
+    max_pages_per_seq] int32. The workspace (a CUDA uint8 tensor of
+    gqa_decode_paged_fp8_workspace_bytes(...)) is taken from torch's allocator
+    when not given."""
+    import torch
+    dev = q.get_device()
+    _check(dev, "q", q, torch.bfloat16)
+    _check(dev, "out", out, torch.bfloat16)
+    Bt, num_pages, G, page_size, Dk, most = _paged_fp8_cache(dev, k_pages, v_pages, k_scale, v_scale,
+                                                             block_table, seq_lens)
+    if q.dim() != 4 or q.shape[0] != Bt or q.shape[3] != Dk:
+        raise ValueError("q must be [B, sq, H, D] with block_table's B and the pages' D")
+    B, sq, H, D = q.shape
+    if out.shape != q.shape:
+        raise ValueError("out must be [B, sq, H, D]")
+    _check_lse(dev, lse, B, sq, H)
+    handle = _stream_handle(stream, dev)
+    if workspace is None:
+        workspace = _workspace(gqa_decode_paged_fp8_workspace_bytes(B, sq, H, G, D, page_size, most, dev) or 256,
+                               dev, stream)
+    else:
+        _check(dev, "workspace", workspace, torch.uint8)
+    rc = _call(dev, load().gqa_decode_paged_fp8, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+               k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+               float(scale), out.data_ptr(), None if lse is None else lse.data_ptr(), B, sq, H, G, D,
+               page_size, num_pages, most, workspace.data_ptr(), workspace.numel(), handle)
+    if rc != GQA_OK:
+        raise GQADecodeError(rc, "gqa_decode_paged_fp8")
+
+
+@functools.lru_cache(maxsize=4096)
+def _paged_fp8_workspace_bytes(B, sq, H, G, D, page_size, most, device):
+    return int(_call(device, load().gqa_decode_paged_fp8_workspace_bytes, B, sq, H, G, D, page_size, most))
+
+
+def gqa_decode_paged_fp8_workspace_bytes(B, sq, H, G, D, page_size, max_pages_per_seq, device=None) -> int:
+    """Workspace bytes of gqa_decode_paged_fp8 on a device (0: unsupported sizes)."""
+    if device is None:
+        import torch
+        device = torch.cuda.current_device()
+    return _paged_fp8_workspace_bytes(B, sq, H, G, D, page_size, max_pages_per_seq, device)
+
+
+def gqa_append_paged_fp8(k_new, v_new, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, stream=None):
+    """Quantises the sq new tokens' K/V ([B, sq, G, D] bf16) into a paged
+    8-bit cache at positions seq_lens[b] - sq + s, with one power-of-two scale
+    per block of min(64, page_size) tokens and KV head."""
+    import torch
+    dev = k_new.get_device()
+    _check(dev, "k_new", k_new, torch.bfloat16)
+    _check(dev, "v_new", v_new, torch.bfloat16)
+    B, num_pages, G, page_size, D, most = _paged_fp8_cache(dev, k_pages, v_pages, k_scale, v_scale,
+                                                           block_table, seq_lens)
+    if k_new.dim() != 4 or k_new.shape[0] != B or tuple(k_new.shape[2:]) != (G, D) or v_new.shape != k_new.shape:
+        raise ValueError("k_new / v_new must be [B, sq, G, D]")
+    rc = _call(dev, load().gqa_append_paged_fp8, k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(),
+               v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
+               seq_lens.data_ptr(), B, k_new.shape[1], G, D, page_size, num_pages, most,
+               _stream_handle(stream, dev))
+    if rc != GQA_OK:
+        raise GQADecodeError(rc, "gqa_append_paged_fp8")
+
+
+def _page_pools(dev, pools, num_pages, page_dim):
+    """The pools of a page call as the library's array. Each is a tensor whose
+    dimension `page_dim` counts the pages; dimensions before it are layers
+    that share the page numbers."""
+    pools = list(pools)
+    arr = (PagePoolT * max(1, len(pools)))()
+    for i, t in enumerate(pools):
+        _check(dev, f"pools[{i}]", t, t.dtype)
+        if not 0 <= page_dim < t.dim() or t.shape[page_dim] != num_pages:
+            raise ValueError(f"pools[{i}] must count {num_pages} pages in dimension {page_dim}")
+        if t.numel() == 0:
+            raise ValueError(f"pools[{i}] is empty")
+        page = t.element_size()
+        for n in t.shape[page_dim + 1:]:
+            page *= n
+        layers = 1
+        for n in t.shape[:page_dim]:
+            layers *= n
+        arr[i].base, arr[i].page_bytes = t.data_ptr(), page
+        arr[i].layer_bytes, arr[i].layers = page * num_pages, layers
+    return arr, len(pools)
+
+
+def _page_state(dev, block_table, seq_lens, ref_counts, counts=None, suffix=""):
+    import torch
+    i32 = torch.int32
+    _check(dev, "block_table" + suffix, block_table, i32)
+    if seq_lens is not None:
+        _check(dev, "seq_lens" + suffix, seq_lens, i32)
+    _check(dev, "ref_counts" + suffix, ref_counts, i32)
+    if block_table.dim() != 2 or (seq_lens is not None and seq_lens.shape != block_table.shape[:1]):
+        raise ValueError("block_table must be [B, max_pages_per_seq] and seq_lens [B]")
+    if ref_counts.dim() != 1:
+        raise ValueError("ref_counts must be [num_pages]")
+    if counts is not None:
+        _check(dev, "counts", counts, i32)
+        if counts.shape != (2,):
+            raise ValueError("counts must be [2]")
+    return block_table.shape[0], block_table.shape[1], ref_counts.shape[0]
+
+
+def gqa_pages_workspace_bytes(B, num_pages) -> int:
+    return int(load().gqa_pages_workspace_bytes(B, num_pages))
+
+
+def gqa_pages_copy(pools, src, dst, num_pages, page_dim=0, stream=None):
+    """Copies page src[i] to page dst[i] (int32 [n]) in every pool: tensors
+    whose dimension page_dim counts the pages (dimensions before it: layers).
+    No page may be a source and a destination, or twice a destination."""
+    import torch
+    dev = src.get_device()
+    _check(dev, "src", src, torch.int32)
+    _check(dev, "dst", dst, torch.int32)
+    if src.dim() != 1 or dst.shape != src.shape:
+        raise ValueError("src and dst must be [n]")
+    arr, n = _page_pools(dev, pools, num_pages, page_dim)
+    rc = _call(dev, load().gqa_pages_copy, arr, n, src.data_ptr(), dst.data_ptr(), src.shape[0], num_pages,
+               _stream_handle(stream, dev))
+    if rc != GQA_OK:
+        raise GQADecodeError(rc, "gqa_pages_copy")
+
+
+def gqa_pages_reserve(block_table, seq_lens, ref_counts, page_size, counts, stream=None):
+    """Gives every sequence, in place, the pages that seq_lens[b] tokens need:
+    empty entries take the free pages (ref_counts <= 0) in ascending order.
+    counts (int32 [2]) = pages needed, pages that were free; nothing changes
+    if fewer are free than needed."""
+    dev = block_table.get_device()
+    B, most, num_pages = _page_state(dev, block_table, seq_lens, ref_counts, counts)
+    ws = _workspace(gqa_pages_workspace_bytes(B, num_pages) or 256, dev, stream)
+    rc = _call(dev, load().gqa_pages_reserve, block_table.data_ptr(), seq_lens.data_ptr(),
+               ref_counts.data_ptr(), counts.data_ptr(), B, most, page_size, num_pages, ws.data_ptr(),
+               ws.numel(), _stream_handle(stream, dev))
+    if rc != GQA_OK:
+        raise GQADecodeError(rc, "gqa_pages_reserve")
+
+
+def gqa_pages_fork(pools, src, block_table, seq_lens, ref_counts, page_size, block_table_out, seq_lens_out,
+                   ref_counts_out, counts, page_dim=0, stream=None):
+    """New row i goes on from old row src[i] (int32 [B]; outside [0, B): empty):
+    full pages are shared, the partly filled last page stays with the lowest
+    such row and is copied, in every pool, for the others; sequences that no
+    row goes on from give their pages back. The outputs are other tensors than
+    the inputs. counts (int32 [2]) = pages needed, pages that were free; the
+    outputs are copies of the inputs if fewer are free than needed."""
+    import torch
+    dev = block_table.get_device()
+    _check(dev, "src", src, torch.int32)
+    B, most, num_pages = _page_state(dev, block_table, seq_lens, ref_counts, counts)
+    if (B, most, num_pages) != _page_state(dev, block_table_out, seq_lens_out, ref_counts_out, None, "_out"):
+        raise ValueError("the outputs must have the inputs' shapes")
+    if src.shape != (B,):
+        raise ValueError("src must be [B]")
+    arr, n = _page_pools(dev, pools, num_pages, page_dim)
+    ws = _workspace(gqa_pages_workspace_bytes(B, num_pages) or 256, dev, stream)
+    rc = _call(dev, load().gqa_pages_fork, arr, n, src.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+               ref_counts.data_ptr(), block_table_out.data_ptr(), seq_lens_out.data_ptr(),
+               ref_counts_out.data_ptr(), counts.data_ptr(), B, most, page_size, num_pages, ws.data_ptr(),
+               ws.numel(), _stream_handle(stream, dev))
+    if rc != GQA_OK:
+        raise GQADecodeError(rc, "gqa_pages_fork")
+
+
+def gqa_pages_free(done, block_table, seq_lens, ref_counts, stream=None):
+    """Gives back the pages of every sequence with done[b] (bool or uint8 [B]),
+    in place: counts go down by one, rows become -1, lengths 0."""
+    import torch
+    dev = block_table.get_device()
+    _check(dev, "done", done, torch.bool if done.dtype == torch.bool else torch.uint8)
+    B, most, num_pages = _page_state(dev, block_table, seq_lens, ref_counts)
+    if done.shape != (B,):
+        raise ValueError("done must be [B]")
+    rc = _call(dev, load().gqa_pages_free, done.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+               ref_counts.data_ptr(), B, most, num_pages, _stream_handle(stream, dev))
+    if rc != GQA_OK:
+        raise GQADecodeError(rc, "gqa_pages_free")
+
+
+def gqa_pages_compact(pools, block_table, ref_counts, block_table_out, ref_counts_out, counts, page_dim=0,
+                      stream=None):
+    """Moves the live pages (ref_counts > 0) to the lowest page numbers, in
+    every pool; the block table and counts follow (the outputs may be the
+    input tensors themselves). counts (int32 [2]) = pages moved, pages live."""
+    dev = block_table.get_device()
+    B, most, num_pages = _page_state(dev, block_table, None, ref_counts, counts)
+    if (B, most, num_pages) != _page_state(dev, block_table_out, None, ref_counts_out, None, "_out"):
+        raise ValueError("the outputs must have the inputs' shapes")
+    arr, n = _page_pools(dev, pools, num_pages, page_dim)
+    ws = _workspace(gqa_pages_workspace_bytes(B, num_pages) or 256, dev, stream)
+    rc = _call(dev, load().gqa_pages_compact, arr, n, block_table.data_ptr(), ref_counts.data_ptr(),
+               block_table_out.data_ptr(), ref_counts_out.data_ptr(), counts.data_ptr(), B, most, num_pages,
+               ws.data_ptr(), ws.numel(), _stream_handle(stream, dev))
+    if rc != GQA_OK:
+        raise GQADecodeError(rc, "gqa_pages_compact")
 
 
 def gqa_decode_ex(q, k_cache, v_cache, seq_lens, scale, out, lse, workspace, stream=None):

@@ -610,6 +610,34 @@ const char* gqa_decode_strerror(int status) {
 
 namespace gqa {
 
+int remember_cuda_error(cudaError_t e) { return cuda_fail(e); }
+
+int current_device(int* sms, unsigned** status) {
+    DeviceInfo info;
+    const int st = device_info(&info);
+    if (st != GQA_OK) return st;
+    *sms = info.sms;
+    *status = info.status;
+    return GQA_OK;
+}
+
+void wait_knobs(unsigned long long* timeout_ns, int* skip_tile) { debug_knobs(timeout_ns, skip_tile); }
+
+int encode_byte_map(CUtensorMap* map, const void* base, long long slabs, int rows, int cols, int box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (!fn) return cuda_fail(cudaErrorNotSupported);
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)slabs};
+    cuuint64_t strides[2] = {(cuuint64_t)cols, (cuuint64_t)rows * cols};
+    cuuint32_t box[3] = {(cuuint32_t)cols, (cuuint32_t)box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
+    return GQA_OK;
+}
+
 template <template <int, int, bool> class F>
 int shape_query(int D, int mt, bool kv8) {
     if (kv8) return mt == 1 ? F<128, 1, true>::value : F<128, 2, true>::value;

@@ -1,0 +1,250 @@
+// gqa_append_paged_fp8: the new tokens' K/V, quantised into a paged e4m3 cache.
+//
+// One group of threads per (sequence, block of tokens, KV head, K or V):
+//   top    = max |x| over the block's finite new elements
+//   scale' = the block's scale, if it holds earlier tokens and top <= 448 scale;
+//            else the smallest 2^e >= top / 448
+//   codes  = e4m3(x / scale'); kept codes = e4m3(code * (scale / scale')) if it moved
+// The new elements are read once, into registers, where they wait for the
+// maximum. Nothing is shared between groups, so no order of execution changes
+// a result.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "gqa_decode.h"
+#include "gqa_device.cuh"
+#include "gqa_launch.h"
+
+namespace gqa {
+namespace {
+
+constexpr float kE4m3Max = 448.0f;
+constexpr int kBlockTokens = 64;   // most tokens that share a scale
+
+struct AppendParams {
+    const uint16_t* x_new[2];   // K, V: [B, sq, G, D] bf16
+    uint8_t* pages[2];          // [num_pages, G, page_size, D] codes
+    float* scale[2];            // [num_pages, G, blocks of a page]
+    const int32_t* table;
+    const int32_t* lens;
+    int B, sq, G, page_size, num_pages, max_pages;
+    int size;                   // tokens of a block: min(64, page_size)
+    int blocks;                 // blocks of a sequence that may receive tokens
+};
+
+// Smallest power of two >= top / 448 (448 = 0.875 * 2^9), 0 for 0, at least 2^-126.
+__device__ __forceinline__ float scale_for(float top) {
+    if (top == 0.f) return 0.f;
+    const uint32_t bits = __float_as_uint(top);
+    int e = (int)(bits >> 23) - 126;                     // top = m * 2^e, m in [0.5, 1)
+    e += (bits & 0x7fffffu) > 0x600000u ? -8 : -9;       // m > 0.875
+    if ((bits >> 23) == 0 || e < -126) e = -126;
+    return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// x / scale; for a power of two by its reciprocal, which is as exact.
+struct Divider {
+    float scale, inv;
+    bool pow2;
+    __device__ explicit Divider(float s) : scale(s) {
+        const uint32_t b = __float_as_uint(s);
+        pow2 = (b & 0x7fffffu) == 0 && (b >> 23) != 0 && (b >> 23) < 254;
+        inv = pow2 ? __uint_as_float((254u - (b >> 23)) << 23) : 0.f;   // 2^-e
+    }
+    __device__ float operator()(float x) const { return pow2 ? x * inv : (scale == 0.f ? 0.f : __fdiv_rn(x, scale)); }
+};
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float finite_or_nan(float x) {
+    return fabsf(x) <= 3.4028234664e38f ? x : __uint_as_float(0x7fffffffu);
+}
+
+// Eight bf16 values.
+__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+
+// TPI threads (a warp, or the CTA) per item; kChunks 8-element chunks of new
+// tokens per thread at most.
+template <int D, int TPI, int THREADS, int CHUNKS>
+__global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p) {
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    constexpr int kRowChunks = D / 8;
+    const int t = threadIdx.x % TPI;
+    const long long item = (long long)blockIdx.x * (THREADS / TPI) + threadIdx.x / TPI;
+    const long long items = 2ll * p.G * p.blocks * p.B;
+    if (item >= items) return;                       // whole groups leave
+    const int which = (int)(item & 1);
+    const int g = (int)((item >> 1) % p.G);
+    const long long rest = (item >> 1) / p.G;
+    const int b = (int)(rest / p.blocks);
+    const int T = clamp_len(p.lens[b], p.max_pages * p.page_size);
+    const int begin = T > p.sq ? T - p.sq : 0;       // first position that gets a new token
+    const long long block = begin / p.size + rest % p.blocks;
+    if (block * p.size >= T) return;
+    const int start = (int)block * p.size;
+    const int page = p.table[(size_t)b * p.max_pages + start / p.page_size];
+    if ((unsigned)page >= (unsigned)p.num_pages) return;
+    const int in_page = start % p.page_size;
+    const int lo = begin > start ? begin : start;
+    const int hi = T < start + p.size ? T : start + p.size;
+    const int kept = lo - start;
+    const size_t unit = (size_t)page * p.G + g;
+    uint8_t* rows = p.pages[which] + (unit * p.page_size + in_page) * D;
+    float* scale_at = p.scale[which] + unit * ((p.page_size + kBlockTokens - 1) / kBlockTokens) + in_page / kBlockTokens;
+    // New token s sits at position T - sq + s.
+    const int s0 = lo - (T - p.sq);
+    const uint16_t* x0 = p.x_new[which] + (((size_t)b * p.sq + s0) * p.G + g) * D;
+    const size_t row_step = (size_t)p.G * D;
+
+    const float held = kept > 0 ? *scale_at : 0.f;
+    uint4 v[CHUNKS];
+    float top = 0.f;
+    const int n = (hi - lo) * kRowChunks;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+        const int i = t + c * TPI;
+        v[c] = make_uint4(0, 0, 0, 0);
+        if (i < n)
+            v[c] = *reinterpret_cast<const uint4*>(x0 + (i / kRowChunks) * row_step + (i % kRowChunks) * 8);
+    }
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+        float x[8];
+        unpack8(v[c], x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float a = fabsf(x[e]);
+            top = fmaxf(top, a <= 3.4028234664e38f ? a : 0.f);
+        }
+    }
+    // Non-negative floats order as their bits do.
+    uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+    if constexpr (TPI > 32) {
+        __shared__ uint32_t part[TPI / 32];
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < TPI / 32; ++w) m = max(m, part[w]);
+    } else {
+        __syncwarp();                                // every lane has read the scale
+    }
+    top = __uint_as_float(m);
+    const float old = held > 0.f ? held : 0.f;
+    const float scale = old > 0.f && top <= kE4m3Max * old ? old : scale_for(top);
+    const Divider div(scale);
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+        const int i = t + c * TPI;
+        if (i < n) {
+            float x[8];
+            unpack8(v[c], x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = div(finite_or_nan(x[e]));
+            uint2 w;
+            w.x = e4m3x2(x[0], x[1]) | (e4m3x2(x[2], x[3]) << 16);
+            w.y = e4m3x2(x[4], x[5]) | (e4m3x2(x[6], x[7]) << 16);
+            *reinterpret_cast<uint2*>(rows + (size_t)kept * D + (size_t)i * 8) = w;
+        }
+    }
+    if (kept > 0 && scale != old) {
+        const float r = scale > 0.f ? __fdiv_rn(old, scale) : 0.f;
+        for (int i = t; i < kept * (D / 16); i += TPI) {
+            uint4* at = reinterpret_cast<uint4*>(rows) + i;
+            const uint4 c = *at;
+            const uint32_t in[4] = {c.x, c.y, c.z, c.w};
+            uint32_t out[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t y = 0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t f = e4m3x2_to_f16x2((uint16_t)(in[q] >> (16 * h)));
+                    const __half2 f2 = *reinterpret_cast<const __half2*>(&f);
+                    const float2 x = __half22float2(f2);
+                    y |= e4m3x2(x.x * r, x.y * r) << (16 * h);
+                }
+                out[q] = y;
+            }
+            *at = make_uint4(out[0], out[1], out[2], out[3]);
+        }
+    }
+    if (t == 0) *scale_at = scale;
+}
+
+template <int D, int TPI, int THREADS, int CHUNKS>
+cudaError_t launch_append(const AppendParams& p, cudaStream_t stream) {
+    const long long items = 2ll * p.G * p.blocks * p.B;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((items + THREADS / TPI - 1) / (THREADS / TPI)));
+    cfg.blockDim = dim3(THREADS);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, append_kernel<D, TPI, THREADS, CHUNKS>, p);
+}
+
+}  // namespace
+}  // namespace gqa
+
+using namespace gqa;
+
+extern "C" int gqa_append_paged_fp8(const void* k_new, const void* v_new, void* k_pages, void* v_pages,
+                                    float* k_scale, float* v_scale, const int32_t* block_table,
+                                    const int32_t* seq_lens, int B, int sq, int G, int D, int page_size,
+                                    int num_pages, int max_pages_per_seq, cudaStream_t stream) {
+    if (B <= 0 || sq <= 0 || G <= 0 || D <= 0 || page_size <= 0 || num_pages <= 0 || max_pages_per_seq <= 0)
+        return GQA_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return GQA_ERR_UNSUPPORTED;
+    if (page_size < 16 || page_size > 65536 || (page_size & (page_size - 1))) return GQA_ERR_UNSUPPORTED;
+    if (!k_new || !v_new || !k_pages || !v_pages || !k_scale || !v_scale || !block_table || !seq_lens)
+        return GQA_ERR_INVALID_ARG;
+    const uintptr_t wide = reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new) |
+                           reinterpret_cast<uintptr_t>(k_pages) | reinterpret_cast<uintptr_t>(v_pages);
+    const uintptr_t word = reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale) |
+                           reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(seq_lens);
+    if ((wide & 15u) || (word & 3u)) return GQA_ERR_MISALIGNED;
+    AppendParams p;
+    p.x_new[0] = static_cast<const uint16_t*>(k_new);
+    p.x_new[1] = static_cast<const uint16_t*>(v_new);
+    p.pages[0] = static_cast<uint8_t*>(k_pages);
+    p.pages[1] = static_cast<uint8_t*>(v_pages);
+    p.scale[0] = k_scale;
+    p.scale[1] = v_scale;
+    p.table = block_table;
+    p.lens = seq_lens;
+    p.B = B;
+    p.sq = sq;
+    p.G = G;
+    p.page_size = page_size;
+    p.num_pages = num_pages;
+    p.max_pages = max_pages_per_seq;
+    p.size = page_size < kBlockTokens ? page_size : kBlockTokens;
+    p.blocks = (int)(((long long)sq + p.size - 2) / p.size) + 1;
+    if ((long long)max_pages_per_seq * page_size >= (1ll << 31) - kBlockTokens ||
+        2ll * G * p.blocks * B >= (1ll << 31))
+        return GQA_ERR_UNSUPPORTED;
+    // Up to 8 new tokens a sequence: a warp per block holds them in registers;
+    // beyond that a CTA of 256 threads does.
+    cudaError_t e;
+    if (sq <= 8)
+        e = D == 64 ? launch_append<64, 32, 128, 2>(p, stream) : launch_append<128, 32, 128, 4>(p, stream);
+    else
+        e = D == 64 ? launch_append<64, 256, 256, 2>(p, stream) : launch_append<128, 256, 256, 4>(p, stream);
+    return e == cudaSuccess ? GQA_OK : remember_cuda_error(e);
+}

@@ -42,4 +42,12 @@ int splitkv_smem_bytes(int D, int row_tiles, bool kv8 = false);
 int splitkv_threads(int D, int row_tiles, bool kv8 = false);
 int splitkv_stages(int D, int row_tiles, bool kv8 = false);
 
+// Host services of api.cu for the entry points of the other translation units.
+int remember_cuda_error(cudaError_t e);                     // returns GQA_ERR_CUDA
+int current_device(int* sms, unsigned** status);            // SM count, status word
+void wait_knobs(unsigned long long* timeout_ns, int* skip_tile);
+// cuTensorMapEncodeTiled of a 3-D uint8 tensor [slabs][rows][cols] (dense) with
+// boxes of box_rows x cols bytes and the swizzle that `cols` (64 or 128) spans.
+int encode_byte_map(CUtensorMap* map, const void* base, long long slabs, int rows, int cols, int box_rows);
+
 }  // namespace gqa

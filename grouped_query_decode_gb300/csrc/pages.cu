@@ -1,0 +1,566 @@
+// Page management of a paged cache: which page belongs to which sequence
+// (block table, reference counts) and the copies of pages that follow from it.
+//
+// Every call is decided on the device, in one planning kernel, and carried out
+// by a second kernel over the whole GPU that reads the plan from the
+// workspace; the host never waits and a call can be captured into a graph.
+// All of it is integer work with one result: pages are taken in ascending
+// order, ranks come from scans, and the only atomics add to integer counts.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "gqa_decode.h"
+#include "gqa_launch.h"
+#include "ptx.cuh"
+
+namespace gqa {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kMoveThreads = 256;
+
+// Workspace, in ints: the header, then the copies' source and destination
+// pages (also the free pages of a reservation), then one new page per row.
+constexpr int kWsPairs = 0, kWsOk = 1, kWsLive = 2, kWsHeader = 64;
+struct PageWs {
+    int* head;
+    int* src;       // [num_pages]
+    int* dst;       // [num_pages]
+    int* row_page;  // [B]
+};
+__host__ __device__ inline PageWs page_ws(void* ws, int num_pages) {
+    int* p = static_cast<int*>(ws);
+    return {p, p + kWsHeader, p + kWsHeader + num_pages, p + kWsHeader + 2 * (size_t)num_pages};
+}
+
+struct PoolSet {
+    gqa_page_pool_t pool[GQA_MAX_POOLS];
+    int n;
+};
+
+struct PagesParams {
+    const int32_t* src_rows;
+    const int32_t* table;
+    const int32_t* lens;
+    const int32_t* refs;
+    int32_t* table_out;
+    int32_t* lens_out;
+    int32_t* refs_out;
+    int32_t* counts;
+    void* ws;
+    int B, max_pages, page_size, num_pages;
+};
+
+__device__ __forceinline__ bool is_page(int e, int num_pages) { return (unsigned)e < (unsigned)num_pages; }
+
+__device__ __forceinline__ int tokens_of(const PagesParams& p, int b) {
+    const long long most = (long long)p.max_pages * p.page_size;
+    const int t = p.lens[b];
+    return t < 0 ? 0 : (t > most ? (int)most : t);
+}
+
+// Exclusive sum of one value per thread of the CTA, and the total.
+__device__ int block_exclusive_sum(int v, int* total) {
+    __shared__ int warp_sum[kPlanWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int w = 0; w < kPlanWarps; ++w) {
+        const int s = warp_sum[w];
+        if (w < warp) before += s;
+        all += s;
+    }
+    *total = all;
+    return before + x - v;
+}
+
+// The free (or live) pages of [lo, hi), counted by the CTA: each warp takes a
+// contiguous range. Returns the number before this warp's range and the total.
+struct Ranks {
+    int lo, hi, before, total;
+};
+__device__ Ranks rank_pages(const int32_t* refs, int lo, int hi, bool live) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = ((hi - lo + kPlanWarps - 1) / kPlanWarps + 31) / 32 * 32;
+    Ranks r;
+    r.lo = min(hi, lo + warp * per);
+    r.hi = min(hi, r.lo + per);
+    int n = 0;
+    for (int i = r.lo + lane; i < r.hi; i += 32) n += (refs[i] > 0) == live;
+    n = __reduce_add_sync(0xffffffffu, n);
+    int before = block_exclusive_sum(lane == 0 ? n : 0, &r.total);
+    r.before = __shfl_sync(0xffffffffu, before, 0);
+    return r;
+}
+
+// list[k] = the k-th free (or live) page of the ranked range, k < limit.
+__device__ void list_pages(const int32_t* refs, const Ranks& r, bool live, int limit, int* list) {
+    const int lane = threadIdx.x & 31;
+    int at = r.before;
+    for (int i0 = r.lo; i0 < r.hi && at < limit; i0 += 32) {
+        const int i = i0 + lane;
+        const bool mine = i < r.hi && (refs[i] > 0) == live;
+        const unsigned m = __ballot_sync(0xffffffffu, mine);
+        const int k = at + __popc(m & ((1u << lane) - 1));
+        if (mine && k < limit) list[k] = i;
+        at += __popc(m);
+    }
+}
+
+// ------------------------------------------------------------------ planning
+
+__global__ void __launch_bounds__(kPlanThreads, 1) reserve_kernel(const PagesParams p) {
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    const PageWs ws = page_ws(p.ws, p.num_pages);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ int want[GQA_MAX_PAGE_ROWS];   // missing pages of each row, then those before it
+    for (int b = warp; b < p.B; b += kPlanWarps) {
+        const int n = (tokens_of(p, b) + p.page_size - 1) / p.page_size;
+        int missing = 0;
+        for (int j = lane; j < n; j += 32)
+            missing += !is_page(p.table_out[(size_t)b * p.max_pages + j], p.num_pages);
+        missing = __reduce_add_sync(0xffffffffu, missing);
+        if (lane == 0) want[b] = missing;
+    }
+    __syncthreads();
+    int need = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+        const int b = b0 + threadIdx.x;
+        const int v = b < p.B ? want[b] : 0;
+        int total;
+        const int before = block_exclusive_sum(v, &total);
+        if (b < p.B) want[b] = need + before;
+        need += total;
+    }
+    const Ranks r = rank_pages(p.refs_out, 0, p.num_pages, false);
+    if (threadIdx.x == 0) {
+        p.counts[0] = need;
+        p.counts[1] = r.total;
+    }
+    if (need > r.total) return;
+    list_pages(p.refs_out, r, false, need, ws.src);
+    __syncthreads();
+    for (int b = warp; b < p.B; b += kPlanWarps) {
+        const int n = (tokens_of(p, b) + p.page_size - 1) / p.page_size;
+        int at = want[b];
+        for (int j0 = 0; j0 < n; j0 += 32) {
+            const int j = j0 + lane;
+            int32_t* e = p.table_out + (size_t)b * p.max_pages + j;
+            const bool mine = j < n && !is_page(*e, p.num_pages);
+            const unsigned m = __ballot_sync(0xffffffffu, mine);
+            if (mine) {
+                const int page = ws.src[at + __popc(m & ((1u << lane) - 1))];
+                *e = page;
+                p.refs_out[page] = 1;
+            }
+            at += __popc(m);
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kPlanThreads, 1) fork_plan_kernel(const PagesParams p) {
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    const PageWs ws = page_ws(p.ws, p.num_pages);
+    __shared__ int first[GQA_MAX_PAGE_ROWS];   // the lowest row that goes on from each row
+    for (int b = threadIdx.x; b < p.B; b += kPlanThreads) first[b] = p.B;
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.B; i += kPlanThreads) {
+        const int s = p.src_rows[i];
+        if (s >= 0 && s < p.B) atomicMin(&first[s], i);
+    }
+    const Ranks r = rank_pages(p.refs, 0, p.num_pages, false);   // synchronises the CTA
+    for (int i = threadIdx.x; i < p.num_pages; i += kPlanThreads) p.refs_out[i] = p.refs[i];
+    int need = 0;
+    for (int i0 = 0; i0 < p.B; i0 += kPlanThreads) {
+        const int i = i0 + threadIdx.x;
+        int old = -1;
+        if (i < p.B) {
+            const int s = p.src_rows[i];
+            if (s >= 0 && s < p.B && first[s] != i) {
+                const int t = tokens_of(p, s);
+                if (t % p.page_size) old = p.table[(size_t)s * p.max_pages + t / p.page_size];
+            }
+        }
+        const bool copies = is_page(old, p.num_pages);
+        int total;
+        const int k = need + block_exclusive_sum(copies ? 1 : 0, &total);
+        // Row i's copy is pair k; the second kernel looks its new page up.
+        if (i < p.B) ws.row_page[i] = copies ? k : -1;
+        if (copies && k < p.num_pages) ws.src[k] = old;
+        need += total;
+    }
+    if (threadIdx.x == 0) {
+        p.counts[0] = need;
+        p.counts[1] = r.total;
+        ws.head[kWsPairs] = need <= r.total ? need : 0;
+        ws.head[kWsOk] = need <= r.total;
+    }
+    if (need <= r.total) list_pages(p.refs, r, false, need, ws.dst);
+    // The first row of each sequence takes its row as it is: marked -2.
+    for (int i = threadIdx.x; i < p.B; i += kPlanThreads) {
+        const int s = p.src_rows[i];
+        if (s >= 0 && s < p.B && first[s] == i) ws.row_page[i] = -2;
+    }
+}
+
+__global__ void __launch_bounds__(kPlanThreads, 1) compact_plan_kernel(const PagesParams p) {
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    const PageWs ws = page_ws(p.ws, p.num_pages);
+    const int live = rank_pages(p.refs, 0, p.num_pages, true).total;
+    const Ranks holes = rank_pages(p.refs, 0, live, false);
+    const Ranks movers = rank_pages(p.refs, live, p.num_pages, true);   // as many as there are holes
+    list_pages(p.refs, holes, false, holes.total, ws.dst);
+    list_pages(p.refs, movers, true, movers.total, ws.src);
+    if (threadIdx.x == 0) {
+        p.counts[0] = movers.total;
+        p.counts[1] = live;
+        ws.head[kWsPairs] = movers.total;
+        ws.head[kWsLive] = live;
+    }
+}
+
+// ------------------------------------------------------------ carrying it out
+
+template <class T>
+__device__ __forceinline__ void copy_bytes(char* dst, const char* src, size_t bytes, int lane) {
+    const size_t n = bytes / sizeof(T);
+    for (size_t i = lane; i < n; i += 32) reinterpret_cast<T*>(dst)[i] = reinterpret_cast<const T*>(src)[i];
+}
+
+// Pages src[k] -> dst[k], k < n, of every layer of every pool; one warp takes
+// one piece of a page at a time.
+constexpr size_t kPiece = 4096;
+__device__ void copy_pages(const PoolSet& pools, const int* src, const int* dst, int n, int num_pages) {
+    const int lane = threadIdx.x & 31;
+    const long long warp = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    const long long warps = (long long)gridDim.x * (blockDim.x >> 5);
+    for (int q = 0; q < pools.n; ++q) {
+        const gqa_page_pool_t pool = pools.pool[q];
+        const long long pieces = (long long)((pool.page_bytes + kPiece - 1) / kPiece);
+        const long long items = pieces * pool.layers * n;
+        for (long long it = warp; it < items; it += warps) {
+            const long long piece = it % pieces, rest = it / pieces;
+            const int k = (int)(rest / pool.layers), layer = (int)(rest % pool.layers);
+            const int a = src[k], b = dst[k];
+            if (!is_page(a, num_pages) || !is_page(b, num_pages)) continue;
+            char* base = static_cast<char*>(pool.base) + (size_t)layer * pool.layer_bytes + piece * kPiece;
+            const char* from = base + (size_t)a * pool.page_bytes;
+            char* to = base + (size_t)b * pool.page_bytes;
+            const size_t bytes = min(kPiece, pool.page_bytes - (size_t)piece * kPiece);
+            const uintptr_t bits = reinterpret_cast<uintptr_t>(from) | reinterpret_cast<uintptr_t>(to) | bytes;
+            if ((bits & 15) == 0)
+                copy_bytes<uint4>(to, from, bytes, lane);
+            else if ((bits & 3) == 0)
+                copy_bytes<unsigned>(to, from, bytes, lane);
+            else
+                copy_bytes<unsigned char>(to, from, bytes, lane);
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kMoveThreads) copy_kernel(const __grid_constant__ PoolSet pools,
+                                                            const int* src, const int* dst, int n,
+                                                            int num_pages) {
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    copy_pages(pools, src, dst, n, num_pages);
+}
+
+__global__ void __launch_bounds__(kMoveThreads) fork_kernel(const __grid_constant__ PoolSet pools,
+                                                            const PagesParams p) {
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    const PageWs ws = page_ws(p.ws, p.num_pages);
+    const bool ok = ws.head[kWsOk] != 0;
+    const long long entries = (long long)p.B * p.max_pages;
+    for (long long x = (long long)blockIdx.x * blockDim.x + threadIdx.x; x < entries;
+         x += (long long)gridDim.x * blockDim.x) {
+        const int i = (int)(x / p.max_pages), j = (int)(x % p.max_pages);
+        const int was = p.table[x];
+        int now = was;
+        if (ok) {
+            const int s = p.src_rows[i];
+            now = -1;
+            if (s >= 0 && s < p.B) {
+                const int t = tokens_of(p, s);
+                const int mark = ws.row_page[i];
+                if (mark == -2 || j < t / p.page_size)
+                    now = p.table[(size_t)s * p.max_pages + j];
+                else if (mark >= 0 && j == t / p.page_size)
+                    now = ws.dst[mark];
+            }
+            if (now != was) {
+                if (is_page(was, p.num_pages)) atomicAdd(&p.refs_out[was], -1);
+                if (is_page(now, p.num_pages)) atomicAdd(&p.refs_out[now], 1);
+            }
+        }
+        p.table_out[x] = now;
+        if (j == 0) {
+            const int s = p.src_rows[i];
+            p.lens_out[i] = !ok ? p.lens[i] : (s >= 0 && s < p.B ? tokens_of(p, s) : 0);
+        }
+    }
+    copy_pages(pools, ws.src, ws.dst, ws.head[kWsPairs], p.num_pages);
+}
+
+__global__ void __launch_bounds__(kMoveThreads) compact_kernel(const __grid_constant__ PoolSet pools,
+                                                               const PagesParams p) {
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    const PageWs ws = page_ws(p.ws, p.num_pages);
+    const int live = ws.head[kWsLive], pairs = ws.head[kWsPairs];
+    const long long stride = (long long)gridDim.x * blockDim.x;
+    const long long t0 = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    for (long long x = t0; x < (long long)p.B * p.max_pages; x += stride) {
+        int e = p.table[x];
+        if (is_page(e, p.num_pages) && e >= live) {
+            // The moved pages are listed in ascending order. An entry whose
+            // page has no reference is none of them and stays.
+            int lo = 0, hi = pairs;
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (ws.src[mid] < e) lo = mid + 1; else hi = mid;
+            }
+            if (lo < pairs && ws.src[lo] == e) e = ws.dst[lo];
+        }
+        p.table_out[x] = e;
+    }
+    // In place, the counts of a moved page's two ends belong to its own thread
+    // alone; every other thread may rewrite what it read.
+    for (long long k = t0; k < pairs; k += stride) {
+        const int a = ws.src[k], b = ws.dst[k], n = p.refs[a];
+        p.refs_out[b] = n;
+        p.refs_out[a] = 0;
+    }
+    if (p.refs_out != p.refs) {
+        for (long long i = t0; i < p.num_pages; i += stride) {
+            const int n = p.refs[i];
+            if ((n > 0) == (i < live)) p.refs_out[i] = n;
+        }
+    }
+    copy_pages(pools, ws.src, ws.dst, pairs, p.num_pages);
+}
+
+__global__ void __launch_bounds__(kMoveThreads) free_kernel(const uint8_t* done, const PagesParams p) {
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    const long long entries = (long long)p.B * p.max_pages;
+    for (long long x = (long long)blockIdx.x * blockDim.x + threadIdx.x; x < entries;
+         x += (long long)gridDim.x * blockDim.x) {
+        const int b = (int)(x / p.max_pages);
+        if (!done[b]) continue;
+        const int e = p.table_out[x];
+        if (is_page(e, p.num_pages) && atomicAdd(&p.refs_out[e], -1) <= 0) atomicAdd(&p.refs_out[e], 1);
+        p.table_out[x] = -1;
+        if (x % p.max_pages == 0) p.lens_out[b] = 0;
+    }
+}
+
+// ---------------------------------------------------------------------- host
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+template <class... KArgs, class... Args>
+int launch(void (*kernel)(KArgs...), unsigned grid, unsigned threads, cudaStream_t stream, Args... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e == cudaSuccess ? GQA_OK : remember_cuda_error(e);
+}
+
+int check_pools(const gqa_page_pool_t* pools, int num_pools, int num_pages, PoolSet* set) {
+    if (num_pools < 0 || (num_pools > 0 && !pools)) return GQA_ERR_INVALID_ARG;
+    if (num_pools > GQA_MAX_POOLS) return GQA_ERR_UNSUPPORTED;
+    for (int i = 0; i < num_pools; ++i) {
+        const gqa_page_pool_t& q = pools[i];
+        if (!q.base || q.page_bytes == 0 || q.layers <= 0 ||
+            (q.layers > 1 && q.layer_bytes / (size_t)num_pages < q.page_bytes))
+            return GQA_ERR_INVALID_ARG;
+        set->pool[i] = q;
+    }
+    set->n = num_pools;
+    return GQA_OK;
+}
+
+int check_sizes(int B, int max_pages, int page_size, int num_pages) {
+    if (B <= 0 || max_pages <= 0 || page_size <= 0 || num_pages <= 0) return GQA_ERR_INVALID_ARG;
+    if ((long long)max_pages * page_size >= (1ll << 31) || num_pages > (1 << 30)) return GQA_ERR_UNSUPPORTED;
+    return GQA_OK;
+}
+
+int check_ws(void* ws, size_t bytes, int B, int num_pages) {
+    if (!ws || bytes < gqa_pages_workspace_bytes(B, num_pages) || (reinterpret_cast<uintptr_t>(ws) & 255u))
+        return GQA_ERR_WORKSPACE;
+    return GQA_OK;
+}
+
+// Bytes that n copies of a page move at most, for the size of the grid.
+unsigned move_grid(const PoolSet& set, long long n, long long entries, int sms) {
+    long long warps = (entries + 31) / 32;
+    for (int i = 0; i < set.n; ++i)
+        warps += n * set.pool[i].layers * (long long)((set.pool[i].page_bytes + kPiece - 1) / kPiece);
+    const long long most = (long long)sms * 8, want = (warps * 32 + kMoveThreads - 1) / kMoveThreads;
+    return (unsigned)(want < 1 ? 1 : want < most ? want : most);
+}
+
+}  // namespace
+}  // namespace gqa
+
+using namespace gqa;
+
+extern "C" {
+
+size_t gqa_pages_workspace_bytes(int B, int num_pages) {
+    if (B <= 0 || num_pages <= 0) return 0;
+    return sizeof(int) * ((size_t)kWsHeader + 2 * (size_t)num_pages + (size_t)B);
+}
+
+int gqa_pages_copy(const gqa_page_pool_t* pools, int num_pools, const int32_t* src, const int32_t* dst, int n,
+                   int num_pages, cudaStream_t stream) {
+    if (n < 0 || num_pages <= 0) return GQA_ERR_INVALID_ARG;
+    PoolSet set;
+    int st = check_pools(pools, num_pools, num_pages, &set);
+    if (st != GQA_OK) return st;
+    if (n == 0 || num_pools == 0) return GQA_OK;
+    if (!src || !dst) return GQA_ERR_INVALID_ARG;
+    if (!aligned4(src) || !aligned4(dst)) return GQA_ERR_MISALIGNED;
+    int sms;
+    unsigned* status;
+    st = current_device(&sms, &status);
+    if (st != GQA_OK) return st;
+    return launch(copy_kernel, move_grid(set, n, 0, sms), kMoveThreads, stream, set, src, dst, n, num_pages);
+}
+
+int gqa_pages_reserve(int32_t* block_table, const int32_t* seq_lens, int32_t* ref_counts, int32_t* counts,
+                      int B, int max_pages_per_seq, int page_size, int num_pages, void* workspace,
+                      size_t workspace_bytes, cudaStream_t stream) {
+    int st = check_sizes(B, max_pages_per_seq, page_size, num_pages);
+    if (st != GQA_OK) return st;
+    if (B > GQA_MAX_PAGE_ROWS) return GQA_ERR_UNSUPPORTED;
+    if (!block_table || !seq_lens || !ref_counts || !counts) return GQA_ERR_INVALID_ARG;
+    if (!aligned4(block_table) || !aligned4(seq_lens) || !aligned4(ref_counts) || !aligned4(counts))
+        return GQA_ERR_MISALIGNED;
+    st = check_ws(workspace, workspace_bytes, B, num_pages);
+    if (st != GQA_OK) return st;
+    PagesParams p = {};
+    p.lens = seq_lens;
+    p.table_out = block_table;
+    p.refs_out = ref_counts;
+    p.counts = counts;
+    p.ws = workspace;
+    p.B = B;
+    p.max_pages = max_pages_per_seq;
+    p.page_size = page_size;
+    p.num_pages = num_pages;
+    return launch(reserve_kernel, 1, kPlanThreads, stream, p);
+}
+
+int gqa_pages_fork(const gqa_page_pool_t* pools, int num_pools, const int32_t* src, const int32_t* block_table,
+                   const int32_t* seq_lens, const int32_t* ref_counts, int32_t* table_out, int32_t* lens_out,
+                   int32_t* refs_out, int32_t* counts, int B, int max_pages_per_seq, int page_size,
+                   int num_pages, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    int st = check_sizes(B, max_pages_per_seq, page_size, num_pages);
+    if (st != GQA_OK) return st;
+    if (B > GQA_MAX_PAGE_ROWS) return GQA_ERR_UNSUPPORTED;
+    PoolSet set;
+    st = check_pools(pools, num_pools, num_pages, &set);
+    if (st != GQA_OK) return st;
+    if (!src || !block_table || !seq_lens || !ref_counts || !table_out || !lens_out || !refs_out || !counts)
+        return GQA_ERR_INVALID_ARG;
+    if (table_out == block_table || lens_out == seq_lens || refs_out == ref_counts) return GQA_ERR_INVALID_ARG;
+    if (!aligned4(src) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(ref_counts) ||
+        !aligned4(table_out) || !aligned4(lens_out) || !aligned4(refs_out) || !aligned4(counts))
+        return GQA_ERR_MISALIGNED;
+    st = check_ws(workspace, workspace_bytes, B, num_pages);
+    if (st != GQA_OK) return st;
+    int sms;
+    unsigned* status;
+    st = current_device(&sms, &status);
+    if (st != GQA_OK) return st;
+    const PagesParams p = {src, block_table, seq_lens, ref_counts, table_out, lens_out, refs_out, counts,
+                           workspace, B, max_pages_per_seq, page_size, num_pages};
+    st = launch(fork_plan_kernel, 1, kPlanThreads, stream, p);
+    if (st != GQA_OK) return st;
+    return launch(fork_kernel, move_grid(set, B, (long long)B * max_pages_per_seq, sms), kMoveThreads, stream,
+                  set, p);
+}
+
+int gqa_pages_free(const uint8_t* done, int32_t* block_table, int32_t* seq_lens, int32_t* ref_counts, int B,
+                   int max_pages_per_seq, int num_pages, cudaStream_t stream) {
+    const int st = check_sizes(B, max_pages_per_seq, 1, num_pages);
+    if (st != GQA_OK) return st;
+    if (!done || !block_table || !seq_lens || !ref_counts) return GQA_ERR_INVALID_ARG;
+    if (!aligned4(block_table) || !aligned4(seq_lens) || !aligned4(ref_counts)) return GQA_ERR_MISALIGNED;
+    int sms;
+    unsigned* status;
+    const int dv = current_device(&sms, &status);
+    if (dv != GQA_OK) return dv;
+    PagesParams p = {};
+    p.table_out = block_table;
+    p.lens_out = seq_lens;
+    p.refs_out = ref_counts;
+    p.B = B;
+    p.max_pages = max_pages_per_seq;
+    p.num_pages = num_pages;
+    PoolSet none;
+    none.n = 0;
+    return launch(free_kernel, move_grid(none, 0, (long long)B * max_pages_per_seq, sms), kMoveThreads, stream,
+                  done, p);
+}
+
+int gqa_pages_compact(const gqa_page_pool_t* pools, int num_pools, const int32_t* block_table,
+                      const int32_t* ref_counts, int32_t* table_out, int32_t* refs_out, int32_t* counts, int B,
+                      int max_pages_per_seq, int num_pages, void* workspace, size_t workspace_bytes,
+                      cudaStream_t stream) {
+    int st = check_sizes(B, max_pages_per_seq, 1, num_pages);
+    if (st != GQA_OK) return st;
+    PoolSet set;
+    st = check_pools(pools, num_pools, num_pages, &set);
+    if (st != GQA_OK) return st;
+    if (!block_table || !ref_counts || !table_out || !refs_out || !counts) return GQA_ERR_INVALID_ARG;
+    if (!aligned4(block_table) || !aligned4(ref_counts) || !aligned4(table_out) || !aligned4(refs_out) ||
+        !aligned4(counts))
+        return GQA_ERR_MISALIGNED;
+    st = check_ws(workspace, workspace_bytes, B, num_pages);
+    if (st != GQA_OK) return st;
+    int sms;
+    unsigned* status;
+    st = current_device(&sms, &status);
+    if (st != GQA_OK) return st;
+    PagesParams p = {};
+    p.table = block_table;
+    p.refs = ref_counts;
+    p.table_out = table_out;
+    p.refs_out = refs_out;
+    p.counts = counts;
+    p.ws = workspace;
+    p.B = B;
+    p.max_pages = max_pages_per_seq;
+    p.num_pages = num_pages;
+    st = launch(compact_plan_kernel, 1, kPlanThreads, stream, p);
+    if (st != GQA_OK) return st;
+    return launch(compact_kernel, move_grid(set, num_pages / 2, (long long)B * max_pages_per_seq, sms),
+                  kMoveThreads, stream, set, p);
+}
+
+}  // extern "C"

@@ -37,7 +37,7 @@
  * KV head, R = (H/G)*sq: up to 32 it runs the split-KV decode kernel, above
  * that the prefill kernel (see gqa_prefill, which also needs scale > 0). The
  * other decode entry points (workspace, plan, append, paged, fp8, no-alloc)
- * take R <= 32.
+ * take R <= 32; gqa_decode_paged_fp8 takes any R.
  * A row with no visible key (T_b - sq + s < 0) gets out = 0 and lse = -inf.
  *
  * Device: every pointer is device memory of the current CUDA device (the one
@@ -188,6 +188,154 @@ int gqa_decode_fp8(const void* q, const void* k_codes, const void* v_codes, cons
 int gqa_prefill(const void* q, const void* k_cache, const void* v_cache, const int32_t* seq_lens,
                 float scale, void* out, float* lse, int B, int sq, int H, int G, int D, int Tmax,
                 cudaStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Paged 8-bit cache: pages of e4m3 codes that are appended to, attended over,
+ * shared between sequences, copied and packed. One serving step is
+ * gqa_pages_reserve (pages for the new tokens), gqa_append_paged_fp8 (their
+ * K/V, quantised) and gqa_decode_paged_fp8 (attention); gqa_pages_fork,
+ * gqa_pages_free and gqa_pages_compact manage who holds which page.
+ *
+ *   k_pages, v_pages [num_pages, G, page_size, D]  e4m3 codes (uint8), as in
+ *                    gqa_decode_fp8; page_size a power of two, 16..65536
+ *   k_scale, v_scale [num_pages, G, ceil(page_size / 64)]  float32: one scale
+ *                    per block of min(64, page_size) tokens of a page and KV
+ *                    head; value = decode(code) * scale. Finite, |scale| < 2^60.
+ *   block_table      [B, max_pages_per_seq]  int32: the page of tokens
+ *                    [j*page_size, (j+1)*page_size) of sequence b; -1 for none
+ *
+ * Every workspace is the caller's (sizes from the *_workspace_bytes calls,
+ * 256-byte aligned, no initialisation): calls that may overlap on the GPU,
+ * replays of different captured graphs among them, take different ones.
+ */
+
+/*
+ * Decode attention over the paged 8-bit cache: the attention of gqa_decode_paged
+ * (same masks, outputs, empty rows, clamped lengths; a block-table entry
+ * outside [0, num_pages) reads as zeros), for D in {64, 128} and any number of
+ * query rows R = (H/G)*sq: single tokens, speculative tokens and the chunks of
+ * a prompt. Queries and codes enter the products exactly, probabilities rounded
+ * to fp16; sums and softmax statistics are fp32.
+ *
+ * A NaN code in K or V at a position a row sees makes that row NaN (in V with
+ * sq > 1 possibly in every column); codes at t >= seq_lens[b] are never used.
+ */
+int gqa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
+                         const float* v_scale, const int32_t* block_table, const int32_t* seq_lens,
+                         float scale, void* out, float* lse, int B, int sq, int H, int G, int D,
+                         int page_size, int num_pages, int max_pages_per_seq, void* workspace,
+                         size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes of gqa_decode_paged_fp8 on the current device (0: unsupported sizes). */
+size_t gqa_decode_paged_fp8_workspace_bytes(int B, int sq, int H, int G, int D, int page_size,
+                                            int max_pages_per_seq);
+
+/*
+ * Quantises the sq new tokens' K/V (k_new, v_new [B, sq, G, D] bf16, 16-byte
+ * aligned, D in {64, 128}) into the pages: new token s of sequence b goes to
+ * position T_b - sq + s as in gqa_decode_append (positions below 0, and
+ * positions whose block-table entry is outside [0, num_pages), are not
+ * written). Everything else in the pages stays as it is.
+ *
+ * Per block of min(64, page_size) tokens and KV head, for K and V apart: the
+ * block keeps its scale if it already holds earlier tokens of the sequence and
+ * every new element is within 448 * scale; otherwise its scale becomes the
+ * smallest power of two 2^e >= max|new| / 448 (e >= -126; 0 while all are 0),
+ * and codes it already holds are requantised. Powers of two leave e4m3's
+ * relative precision as it is and make requantising exact except for
+ * subnormals, so tokens appended one by one do not lose precision as their
+ * block outgrows its scale. Codes are round-to-nearest-even of x / scale; NaN
+ * and infinities are stored as NaN codes and leave the scale alone.
+ *
+ * A page that receives tokens must belong to one sequence only (gqa_pages_fork
+ * gives every sequence its own last page). No workspace.
+ */
+int gqa_append_paged_fp8(const void* k_new, const void* v_new, void* k_pages, void* v_pages,
+                         float* k_scale, float* v_scale, const int32_t* block_table,
+                         const int32_t* seq_lens, int B, int sq, int G, int D, int page_size,
+                         int num_pages, int max_pages_per_seq, cudaStream_t stream);
+
+/*
+ * Page management. ref_counts[p] (int32 [num_pages], device) counts the
+ * block-table entries that name page p, plus any holder outside the table; a
+ * page with a count <= 0 is free. Pages are always taken in ascending order
+ * from the free ones. seq_lens are clamped to [0, max_pages * page_size];
+ * entries outside [0, num_pages) count as no page. counts (int32 [2], device)
+ * reports what a call did, so the host need not wait for it.
+ *
+ * The data of a page is whatever `pools` lists: K and V pages, their scales,
+ * of any type and any number of layers.
+ */
+typedef struct gqa_page_pool_t {
+    void* base;          /* page 0 of layer 0, device */
+    size_t page_bytes;   /* bytes of one page; pages are dense within a layer */
+    size_t layer_bytes;  /* distance of the layers (>= num_pages * page_bytes) */
+    int layers;          /* layers that share the page numbers */
+} gqa_page_pool_t;
+#define GQA_MAX_POOLS 64      /* pools of one call */
+#define GQA_MAX_PAGE_ROWS 8192 /* rows B of gqa_pages_reserve and gqa_pages_fork */
+
+/* Workspace bytes of gqa_pages_reserve, gqa_pages_fork and gqa_pages_compact (host only). */
+size_t gqa_pages_workspace_bytes(int B, int num_pages);
+
+/*
+ * Copies page src[i] to page dst[i] in every layer of every pool, i < n. Pairs
+ * with a page outside [0, num_pages) are skipped. No page may be both a source
+ * and a destination or twice a destination (its contents are then undefined;
+ * nothing faults). src, dst: int32, device. n = 0 enqueues nothing.
+ */
+int gqa_pages_copy(const gqa_page_pool_t* pools, int num_pools, const int32_t* src, const int32_t* dst,
+                   int n, int num_pages, cudaStream_t stream);
+
+/*
+ * Gives every sequence the pages that seq_lens[b] tokens need: entries
+ * j < ceil(seq_lens[b] / page_size) of row b that hold no page take the free
+ * pages in ascending order, in the order (b, j), with a count of 1. In place.
+ * counts = {pages needed, pages that were free}; if fewer are free than needed,
+ * nothing is changed.
+ */
+int gqa_pages_reserve(int32_t* block_table, const int32_t* seq_lens, int32_t* ref_counts, int32_t* counts,
+                      int B, int max_pages_per_seq, int page_size, int num_pages, void* workspace,
+                      size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Row i of the new block table goes on from row src[i] of the old one (outside
+ * [0, B): an empty row): beam search, parallel samples, reordered or dropped
+ * sequences. Full pages are shared. The partly filled last page, and pages
+ * reserved behind it, stay with the lowest row that goes on from a sequence;
+ * every other such row gets a copy of the partly filled page in a free page, in
+ * the order of the rows. Sequences that no row goes on from give their pages
+ * back. table_out, lens_out, refs_out do not overlap the inputs.
+ * counts = {pages needed, pages that were free}; if fewer are free than needed,
+ * the outputs are copies of the inputs and no page is copied.
+ */
+int gqa_pages_fork(const gqa_page_pool_t* pools, int num_pools, const int32_t* src,
+                   const int32_t* block_table, const int32_t* seq_lens, const int32_t* ref_counts,
+                   int32_t* table_out, int32_t* lens_out, int32_t* refs_out, int32_t* counts, int B,
+                   int max_pages_per_seq, int page_size, int num_pages, void* workspace,
+                   size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Gives back the pages of every sequence b with done[b] != 0 (uint8 [B]): their
+ * counts go down by one (not below 0), row b becomes -1 and seq_lens[b] 0. In
+ * place; a row without pages is left empty.
+ */
+int gqa_pages_free(const uint8_t* done, int32_t* block_table, int32_t* seq_lens, int32_t* ref_counts, int B,
+                   int max_pages_per_seq, int num_pages, cudaStream_t stream);
+
+/*
+ * Moves the live pages to the lowest page numbers: with n pages live, the k-th
+ * live page at or above n moves to the k-th free page below n, in every pool,
+ * and the block table and counts follow. Pages n and above are free afterwards
+ * (their old contents stay). table_out / refs_out may be block_table /
+ * ref_counts themselves, but not overlap them otherwise.
+ * counts = {pages moved, pages live}.
+ */
+int gqa_pages_compact(const gqa_page_pool_t* pools, int num_pools, const int32_t* block_table,
+                      const int32_t* ref_counts, int32_t* table_out, int32_t* refs_out, int32_t* counts,
+                      int B, int max_pages_per_seq, int num_pages, void* workspace,
+                      size_t workspace_bytes, cudaStream_t stream);
 
 /*
  * Bytes of device workspace gqa_decode_ex needs for these sizes on the current

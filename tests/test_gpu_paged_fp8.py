@@ -1,0 +1,376 @@
+"""Attention over the paged 8-bit cache on the GPU, against the float64 oracle
+over the values the pages hold. Everything the call must not use holds NaN:
+pages of no sequence, rows past a length, and their blocks' scales.
+
+Bounds (arithmetic, for N(0,1)-sized values; vmax = max |v| that a row sees):
+  scores: fp32 sums of D <= 128 products, error at most D 2^-24 sum|q k| scale
+      <= 2^-14 for |scores| of a few units: taken as 2^-13, in natural units;
+  out: output rounding 2^-8 |out|; probabilities rounded to fp16, 2^-11 vmax,
+      or by at most 2^-24 of the largest one each, T 2^-24 vmax; the scores'
+      error twice (numerator and sum), 2^-12 vmax;
+  lse: the scores' error, fp32 sums of T terms T 2^-24, and its own rounding.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import grouped_query_decode_gb300 as gq
+import oracle
+import paged_fp8_model as model
+import synthetic as syn
+from gpu_helpers import _CANARY_BF16, _CANARY_F32, _PAD, bf16_to_f64, to_device_bf16
+
+pytestmark = pytest.mark.gpu
+
+
+class Case:
+    def __init__(self, seed, B, sq, H, G, D, page, lens, most=None, spread=1.0, extra=3, scale_spread=0):
+        rng = np.random.default_rng(seed)
+        self.lens = np.asarray(lens, dtype=np.int32)
+        self.most = most or max(1, -(-int(self.lens.max()) // page))
+        need = [-(-min(max(int(t), 0), self.most * page) // page) for t in self.lens]
+        num = sum(need) + extra
+        order = rng.permutation(num).astype(np.int32)
+        self.table = np.full((B, self.most), -1, np.int32)
+        self.shape = (B, sq, H, G, D, page)
+        self.q = syn.normal_bf16(seed, syn.STREAM_Q, (B, sq, H, D))
+        self.sm = 1 / math.sqrt(D)
+        nb = model.blocks_of(page)
+        self.codes, self.scales = [], []
+        for _ in range(2):
+            s = (0.5 + rng.random((num, G, nb))) / 100 * spread
+            s = (s * np.exp2(rng.integers(-scale_spread, scale_spread + 1, s.shape))).astype(np.float32)
+            c = model.nearest_codes(np.clip(rng.standard_normal((num, G, page, D)) * 80, -448, 448))
+            self.codes.append(c)
+            self.scales.append(s)
+        at, size = 0, model.block_tokens(page)
+        used = np.zeros((num, page), bool)
+        for b, n in enumerate(need):
+            self.table[b, :n] = order[at:at + n]
+            at += n
+            T = min(max(int(self.lens[b]), 0), self.most * page)
+            for j in range(n):
+                used[self.table[b, j], :max(0, min(page, T - j * page))] = True
+        for c, s in zip(self.codes, self.scales):
+            c.transpose(0, 2, 1, 3)[~used] = model.NAN_CODE
+            live = used.reshape(num, nb, size).any(2)
+            s.transpose(0, 2, 1)[~live] = np.nan
+
+    def reference(self):
+        B, sq, H, G, D, page = self.shape
+        tmax = self.most * page
+        with np.errstate(invalid="ignore"):
+            k, v = (model.logical(model.page_values(c, s), self.table, self.lens, tmax)
+                    for c, s in zip(self.codes, self.scales))
+        lens = np.clip(self.lens, 0, tmax)
+        out, lse = oracle.get().gqa_decode_kv(self.q, k, v, lens, self.sm, threads=8)
+        self.vmax = np.zeros((B, 1, H, 1))
+        for b in range(B):
+            if lens[b]:
+                top = np.abs(v[b, :, :lens[b]]).max((1, 2))
+                self.vmax[b, 0, :, 0] = np.repeat(top, H // G)
+        return out, lse
+
+    def device(self):
+        d = [to_device_bf16(self.q)]
+        d += [torch.from_numpy(x).cuda() for x in (*self.codes, *self.scales)]
+        d += [torch.from_numpy(self.table).cuda(), torch.from_numpy(self.lens).cuda()]
+        return d
+
+
+def guarded(shape, dtype, canary):
+    n = math.prod(shape)
+    buf = torch.empty(n + 2 * _PAD, dtype=dtype, device="cuda")
+    buf.view(torch.int16 if dtype == torch.bfloat16 else torch.int32).fill_(canary)
+    return buf, buf[_PAD:_PAD + n].view(shape)
+
+
+F32_CANARY = int(np.float32(_CANARY_F32).view(np.int32))
+BF_CANARY = int(np.uint16(_CANARY_BF16).view(np.int16))
+
+
+def run(case, dev=None, with_lse=True, **kw):
+    B, sq, H, G, D, page = case.shape
+    dev = dev or case.device()
+    obuf, out = guarded((B, sq, H, D), torch.bfloat16, BF_CANARY)
+    lbuf, lse = guarded((B, sq, H), torch.float32, F32_CANARY)
+    gq.gqa_decode_paged_fp8(*dev, case.sm, out, lse if with_lse else None, **kw)
+    torch.cuda.synchronize()
+    assert gq.gqa_decode_check_error() == gq.GQA_OK
+    for buf, c in ((obuf.view(torch.int16), BF_CANARY), (lbuf.view(torch.int32), F32_CANARY)):
+        assert (buf[:_PAD] == c).all() and (buf[-_PAD:] == c).all(), "guard words"
+    if not with_lse:
+        assert (lbuf.view(torch.int32) == F32_CANARY).all()
+    return bf16_to_f64(out), lse.cpu().numpy().astype(np.float64)
+
+
+def check(case, out, lse, ref=None, what=""):
+    ref_out, ref_lse = ref or case.reference()
+    empty = np.isneginf(ref_lse)
+    assert np.array_equal(np.isneginf(lse), empty), what
+    assert (out[empty] == 0).all(), what
+    T = max(1, int(np.clip(case.lens, 0, None).max()))
+    assert np.isfinite(out).all(), what
+    bound = 2.0 ** -8 * np.abs(ref_out) + (2.0 ** -11 + 2.0 ** -12 + T * 2.0 ** -24) * case.vmax
+    excess = np.abs(out - ref_out) - bound
+    assert excess.max() <= 0, (what, excess.max(), np.abs(out - ref_out).max())
+    lerr = np.abs(lse[~empty] - ref_lse[~empty])
+    lbound = 2.0 ** -13 + T * 2.0 ** -24 + 2.0 ** -23 * np.abs(ref_lse[~empty])
+    assert (lerr <= lbound).all(), (what, lerr.max())
+
+
+LENS = [1, 15, 64, 65, 127, 128, 129, 200, 511, 512, 0]
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H,G,sq", [(8, 8, 1), (32, 8, 1), (16, 2, 1), (24, 2, 1), (32, 1, 1), (64, 8, 4), (6, 2, 3)],
+                         ids=str)
+def test_matches_the_oracle(H, G, sq, D, page):
+    c = Case(100 + H + sq + D + page, len(LENS), sq, H, G, D, page, LENS)
+    check(c, *run(c))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H,G,sq,T", [(32, 8, 64, 300), (8, 2, 130, 257), (40, 1, 1, 300), (32, 1, 7, 140), (4, 4, 129, 129)],
+                         ids=str)
+def test_many_rows(H, G, sq, T, D):
+    """More than 32 rows per KV head: prompt chunks and wide groups."""
+    c = Case(300 + H + sq + D, 2, sq, H, G, D, 64, [T, max(1, T // 3)], most=5)
+    check(c, *run(c))
+
+
+@pytest.mark.parametrize("page,D,T", [(16, 128, 20000), (64, 64, 33333), (256, 128, 8192)])
+def test_long_and_split(page, D, T):
+    """One sequence split over every SM, next to a short one."""
+    c = Case(400 + page, 2, 1, 16, 2, D, page, [T, 130])
+    check(c, *run(c))
+
+
+@pytest.mark.parametrize("lens", [[1], [2], [3], [128], [127, 1, 0, 300]])
+@pytest.mark.parametrize("sq", [1, 4])
+def test_short_sequences_and_rows_without_a_key(lens, sq):
+    c = Case(500 + sq, len(lens), sq, 16, 4, 128, 16, lens)
+    check(c, *run(c))
+
+
+def test_lengths_are_clamped():
+    c = Case(510, 3, 1, 8, 2, 64, 16, [500, -3, 17], most=4)
+    check(c, *run(c))
+
+
+def test_many_sequences():
+    lens = np.random.default_rng(1).integers(0, 90, 700)
+    c = Case(520, 700, 1, 4, 2, 64, 32, lens)
+    check(c, *run(c))
+
+
+def test_lse_is_optional():
+    c = Case(530, 2, 1, 8, 2, 128, 64, [200, 77])
+    ref = c.reference()
+    out, _ = run(c, with_lse=False)
+    check(c, out, ref[1], ref)
+
+
+@pytest.mark.parametrize("page", [16, 64, 128])
+def test_entries_outside_the_pool_read_as_zeros(page):
+    c = Case(540 + page, 2, 1, 16, 4, 128, page, [300, 200])
+    c.table[0, 1] = c.codes[0].shape[0] + 7
+    c.table[1, 0] = -1
+    c.table[0, 0] = np.iinfo(np.int32).min
+    check(c, *run(c))
+
+
+def test_scales_of_unlike_size():
+    """Neighbouring blocks' scales up to 2^16 apart, in K within 2^4."""
+    c = Case(550, 3, 2, 16, 2, 128, 16, [900, 333, 64])
+    rng = np.random.default_rng(3)
+    c.scales[0] *= np.exp2(rng.integers(-2, 2, c.scales[0].shape)).astype(np.float32) / 4
+    c.scales[1] *= np.exp2(rng.integers(-8, 9, c.scales[1].shape)).astype(np.float32)
+    check(c, *run(c))
+
+
+def test_zero_scales():
+    c = Case(560, 2, 1, 8, 2, 64, 16, [200, 100])
+    rng = np.random.default_rng(4)
+    for s in c.scales:
+        s[rng.random(s.shape) < 0.4] = 0
+    check(c, *run(c))
+    for s in c.scales:
+        s[...] = 0
+    out, lse = run(c)
+    assert (out == 0).all()
+    check(c, out, lse)
+
+
+def test_large_and_tiny_queries():
+    """Rows of unlike magnitude in one group, and a zero row; the softmax scale
+    brings the scores back to a few units."""
+    c = Case(570, 1, 1, 16, 2, 128, 64, [400])
+    q = torch.from_numpy(c.q.view(np.int16)).view(torch.bfloat16).float()
+    q *= torch.exp2(torch.arange(16).float() - 15).view(1, 1, 16, 1)
+    q[0, 0, 3] = 0
+    c.q = (q * 2.0 ** 30).to(torch.bfloat16).view(torch.int16).numpy().view(np.uint16)
+    c.sm = 2.0 ** -30 / math.sqrt(128)
+    check(c, *run(c))
+
+
+def test_one_key_above_the_rest_and_a_long_tail():
+    """The first key holds half of the weight, 40000 equal keys the other
+    half: what each of them adds is 2^-17 of the first."""
+    T, D, page = 40000, 128, 64
+    c = Case(580, 1, 1, 2, 2, D, page, [T])
+    for x in range(2):
+        c.scales[x][...] = 1.0
+    c.codes[0][...] = 0
+    c.codes[1] &= 0x7F          # positive values: the tail does not average out
+    p0 = int(c.table[0, 0])
+    c.codes[0][p0, :, 0, 0] = model.nearest_codes(np.array(16.0))
+    c.q[...] = 0
+    c.q[..., 0] = int(torch.tensor([1.0]).to(torch.bfloat16).view(torch.int16))
+    c.sm = math.log(T) / 16
+    check(c, *run(c))
+
+
+def test_positive_and_negative_softmax_scales():
+    for sm in (0.0, -0.09, 1.5):
+        c = Case(590, 2, 2, 8, 2, 64, 32, [150, 40])
+        c.sm = sm
+        out, lse = run(c)
+        ref = c.reference()
+        if sm == 1.5:       # scores of up to ~60: their error grows with them
+            assert np.abs(out - ref[0]).max() <= 2.0 ** -6 * c.vmax.max()
+        else:
+            check(c, out, lse, ref)
+
+
+def test_nan_reaches_the_rows_that_see_it_and_no_other():
+    B, sq, H, G, D, page = 2, 4, 8, 2, 128, 16
+    base = Case(600, B, sq, H, G, D, page, [200, 90])
+    ref = run(base)
+    for which in (0, 1):                    # K, V
+        for pos in (50, 197, 198, 199):     # visible to all rows; the new tokens 1, 2, 3
+            c = Case(600, B, sq, H, G, D, page, [200, 90])
+            c.codes[which][c.table[0, pos // page], 1, pos % page, 7] = 0xFF
+            out, lse = run(c)
+            sees = np.zeros((B, sq, H), bool)
+            sees[0, [s for s in range(sq) if 200 - sq + s >= pos], H // G:] = True
+            assert np.isnan(out[sees]).any(axis=-1).all(), (which, pos)
+            assert np.array_equal(out[~sees], ref[0][~sees]) and np.array_equal(lse[~sees], ref[1][~sees])
+
+
+@pytest.mark.parametrize("bad", [np.inf, -np.inf, np.nan])
+def test_non_finite_queries_poison_their_own_row(bad):
+    base = Case(610, 1, 2, 8, 2, 64, 16, [100])
+    ref = run(base)
+    c = Case(610, 1, 2, 8, 2, 64, 16, [100])
+    c.q[0, 1, 5, 9] = int(torch.tensor([bad]).to(torch.bfloat16).view(torch.int16)) & 0xFFFF
+    out, lse = run(c)
+    assert np.isnan(out[0, 1, 5]).all() and np.isnan(lse[0, 1, 5])
+    keep = np.ones((1, 2, 8), bool)
+    keep[0, 1, 5] = False
+    assert np.array_equal(out[keep], ref[0][keep]) and np.array_equal(lse[keep], ref[1][keep])
+
+
+def test_matches_the_contiguous_fp8_cache():
+    """The same codes and scales in 64-token pages and in one contiguous cache."""
+    B, H, G, D, T = 2, 16, 4, 128, 512
+    c = Case(620, B, 1, H, G, D, 64, [T, T])
+    dev = c.device()
+    out, lse = run(c, dev)
+    t = dev[5].long()
+    k, v = (x[t].transpose(1, 2).reshape(B, G, T, D).contiguous() for x in dev[1:3])
+    ks, vs = (x[t][..., 0].transpose(1, 2).contiguous() for x in dev[3:5])
+    o2 = torch.empty(B, 1, H, D, dtype=torch.bfloat16, device="cuda")
+    l2 = torch.empty(B, 1, H, dtype=torch.float32, device="cuda")
+    gq.gqa_decode_fp8(dev[0], k, v, ks, vs, dev[6], c.sm, o2, l2)
+    check(c, bf16_to_f64(o2), l2.cpu().numpy().astype(np.float64))
+    assert np.abs(out - bf16_to_f64(o2)).max() <= 2.0 ** -7 * np.abs(out).max() + 2.0 ** -10 * c.vmax.max()
+
+
+def test_two_calls_agree_bit_for_bit():
+    c = Case(630, 3, 4, 64, 8, 128, 64, [3000, 700, 45])
+    dev = c.device()
+    a, b = run(c, dev), run(c, dev)
+    assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+
+
+def test_streams_graphs_and_dirty_workspaces():
+    """Two graphs with their own memory, replayed at once on two streams with
+    new lengths and queries; and a caller's workspace full of canary bytes."""
+    cases = [Case(640 + i, 3, 1, 32, 8, 128, 64, [2000, 1500 - 99 * i, 40]) for i in range(2)]
+    devs = [c.device() for c in cases]
+    refs = [run(c, d) for c, d in zip(cases, devs)]
+    outs, graphs = [], []
+    for c, d in zip(cases, devs):
+        B, sq, H, G, D, page = c.shape
+        o = torch.zeros(B, sq, H, D, dtype=torch.bfloat16, device="cuda")
+        l = torch.zeros(B, sq, H, dtype=torch.float32, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            gq.gqa_decode_paged_fp8(*d, c.sm, o, l)
+        outs.append((o, l))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for rep in range(3):
+        for o, l in outs:
+            o.zero_()
+            l.zero_()
+        torch.cuda.synchronize()
+        for _ in range(10):
+            for g, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    g.replay()
+        torch.cuda.synchronize()
+        for (o, l), ref in zip(outs, refs):
+            assert np.array_equal(bf16_to_f64(o), ref[0])
+            assert np.array_equal(l.cpu().numpy(), ref[1].astype(np.float32))
+    assert gq.gqa_decode_check_error() == gq.GQA_OK
+    n = gq.gqa_decode_paged_fp8_workspace_bytes(3, 1, 32, 8, 128, 64, cases[1].most)
+    ws = torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda")
+    got = run(cases[1], devs[1], workspace=ws)
+    assert np.array_equal(got[0], refs[1][0])
+    short = torch.empty(n - 1, dtype=torch.uint8, device="cuda")
+    with pytest.raises(gq.GQADecodeError) as e:
+        run(cases[1], devs[1], workspace=short)
+    assert e.value.status == gq.GQA_ERR_WORKSPACE
+
+
+def test_replay_with_new_lengths_and_pages():
+    c = Case(650, 2, 2, 16, 2, 64, 16, [400, 400])
+    d = c.device()
+    B, sq, H, G, D, page = c.shape
+    o = torch.zeros(B, sq, H, D, dtype=torch.bfloat16, device="cuda")
+    l = torch.zeros(B, sq, H, dtype=torch.float32, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        gq.gqa_decode_paged_fp8(*d, c.sm, o, l)
+    for lens in ([400, 400], [1, 399], [0, 64], [130, 0], [400, 16]):
+        c.lens = np.array(lens, np.int32)
+        c.table = c.table[::-1].copy()
+        d[6].copy_(torch.from_numpy(c.lens))
+        d[5].copy_(torch.from_numpy(c.table))
+        g.replay()
+        torch.cuda.synchronize()
+        check(c, bf16_to_f64(o), l.cpu().numpy().astype(np.float64), what=str(lens))
+
+
+def test_page_pool_past_2_31_codes():
+    """A pool of more than 2^31 codes: the last pages' bytes and scales."""
+    G, D, page = 8, 128, 64
+    num = (1 << 31) // (G * D * page) + 5
+    c = Case(670, 1, 1, 16, G, D, page, [600])
+    dev = c.device()
+    n = c.codes[0].shape[0]
+    for i, shape in ((1, (num, G, page, D)), (2, (num, G, page, D))):
+        big = torch.full(shape, model.NAN_CODE, dtype=torch.uint8, device="cuda")
+        big[num - n:] = dev[i]
+        dev[i] = big
+    for i in (3, 4):
+        big = torch.full((num, G, 1), float("nan"), device="cuda")
+        big[num - n:] = dev[i]
+        dev[i] = big
+    dev[5] = torch.where(dev[5] >= 0, dev[5] + (num - n), dev[5])
+    check(c, *run(c, dev))
