@@ -1,0 +1,1013 @@
+// Decode attention over a paged e4m3 cache on the 5th-generation tensor cores,
+// with the codes as operands: no K or V element is converted.
+//
+// A unit is (sequence, KV head, up to 32 query rows). Its keys are cut into
+// 128-token tiles; tokens sit on the products' M side, rows on the N side:
+//     S [128 tokens x 2 rows]  = K   [128 x D]   (smem, K-major)  x Q^T  (smem)
+//     O [D x 3 rows]          += V^T [D x 128]   (smem, MN-major) x P    (smem)
+// both kind::f8f6f4 with fp32 accumulators in tensor memory. Rows are few, so
+// each bf16 or fp32 number on the N side is spread over several e4m3 columns:
+//   q * 2^e = hi + lo / 16              (2^e brings the row's maximum to [128, 256))
+//   p * v_scale * 2^c = hi + mid / 16 + lo / 256, of the value rounded to fp16
+// e4m3 keeps 4 significant bits and each residual is an exact difference of at
+// most half a step, so hi + lo is every bf16 query down to 2^-13 of its row's
+// maximum (2^-21 of it absolutely below that), and hi + mid + lo the fp16
+// probability down to 2^-13 of the reference (2^-24 absolutely below). The
+// extra columns cost nothing: with N <= 96 the products are bound by reading
+// the K and V tiles from shared memory once each.
+//
+// Softmax, one thread per token: x = s * scale2 * k_scale (base 2), p = 2^(x - m)
+// with a reference m per row that moves only when a score exceeds it by more
+// than 2 (then O is rescaled in tensor memory), so that tiles need no maximum
+// across threads: one vote. The sum l is kept per thread until the end. v_scale enters
+// p through a power of two 2^c that follows the largest scale seen.
+//
+// Work: the tiles of all units, end to end, are shared equally by the CTAs
+// (one per SM); a unit that crosses CTAs leaves (O, m, l) per CTA in the
+// workspace for the merge kernel. Per CTA: two groups of four softmax warps
+// take alternate tiles, two warps bring K and V by TMA (a box per page, the
+// swizzle of the operand layout), one issues the products, one prepares Q.
+// Every wait is bounded, as in the other kernels.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "gqa_device.cuh"
+#include "gqa_paged_fp8.h"
+#include "tcgen05.cuh"
+
+namespace gqa {
+
+constexpr int kP8Threads = 384;
+constexpr float kP8Slack = 2.0f;          // p <= 2^2 before the reference moves
+constexpr float kP8ProbScale = 64.0f;     // p * v_scale * 2^-ev * 64 <= 4 * 1.75 * 64 = 448
+constexpr float kP8ScaleSlack = 1.75f;
+constexpr float kP8Unseen = -3.402823466e38f;   // reference of a row that has seen no key
+
+template <int D, int RP>
+struct P8Shape {
+    static constexpr int kTileBytes = kP8Tokens * D;              // K or V of one tile
+    static constexpr int kNs = 2 * RP;                            // columns of S: hi, lo
+    static constexpr int kNp = RP == 8 ? 32 : 3 * RP;             // columns of O: hi, mid, lo
+    static constexpr int kQBytes = kNs * D;
+    static constexpr int kPBytes = kP8Tokens * kNp;
+    static constexpr int kStageFloats = RP * D + 2 * RP;          // one group's (O, m, l)
+    // The ring takes what the rest leaves of 227 KB.
+    static constexpr int kStages = D == 128 ? (RP == 32 ? 5 : 6) : (RP == 32 ? 10 : 12);
+    static constexpr int kBars = 4 * kStages + 15;
+    static constexpr int kRowInfoBytes = 2 * RP * 16;
+    static constexpr int kRefBytes = 2 * RP * 4;
+    static constexpr int kWarpMaxBytes = 2 * 4 * (RP + 1) * 4;
+    static constexpr int kSumBytes = 2 * RP * 16;
+    static constexpr int kMiscBytes = 128;
+    static constexpr int kSmemBytes = 1024 + 2 * kStages * kTileBytes + 2 * kQBytes + 2 * kPBytes +
+                                      4 * kStageFloats + kRowInfoBytes + kRefBytes + kWarpMaxBytes + kSumBytes +
+                                      kMiscBytes + 8 * kBars;
+    static constexpr uint32_t kColS = 0, kColO = 2 * kNs;         // S_0 | S_1 | O_0 | O_1
+    static constexpr uint32_t kCols = 2 * kNs + 2 * kNp;
+    static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
+};
+
+// ------------------------------------------------------ tensor-core wrappers
+
+// Shared-memory matrix descriptor: as smem_desc_sw128, with the layout given
+// (2: 128-byte swizzle, 4: 64-byte swizzle, 0: none).
+__device__ __forceinline__ uint64_t p8_desc(uint32_t addr, uint32_t lbo, uint32_t sbo, uint64_t layout) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (layout << 61);
+}
+
+// Instruction descriptor of kind::f8f6f4: e4m3 A and B, fp32 accumulator.
+__host__ __device__ constexpr uint32_t p8_idesc(int M, int N, bool a_mn, bool b_mn) {
+    return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 16 fp32 columns of this thread's TMEM lane, waited on; and their store.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// ------------------------------------------------------------ e4m3 and fp16
+
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t v) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(v));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// (a - b) * 16, exact for b = a rounded to e4m3.
+__device__ __forceinline__ uint32_t residual16(uint32_t a, uint32_t b) {
+    const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    const __half2 s = __hmul2(d, __float2half2_rn(16.f));
+    return *reinterpret_cast<const uint32_t*>(&s);
+}
+
+// Floats to integers of the same order, and back.
+__device__ __forceinline__ int ordered(float x) {
+    const int i = __float_as_int(x);
+    return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }   // |e| <= 126
+
+// ---------------------------------------------------------------------- plan
+
+__device__ __forceinline__ int p8_len(const PagedFp8Params& p, int b) {
+    return clamp_len(p.lens[b], p.max_pages << p.page_shift);
+}
+
+// Tiles that the rows of entry (b, row tile) see.
+template <int RP>
+__device__ __forceinline__ int p8_tiles(const PagedFp8Params& p, int entry) {
+    const int b = entry / p.row_tiles, rt = entry - b * p.row_tiles;
+    const int last = min(p.R, (rt + 1) * RP) - 1;
+    const int lim = p8_len(p, b) - p.sq + last / p.heads_per_group;
+    return lim < 0 ? 0 : lim / kP8Tokens + 1;
+}
+
+// A CTA's share as a run of segments of units.
+struct P8Segment {
+    int entry, g, i0, i1, n;     // tiles [i0, i1) of the unit's n
+};
+template <int RP>
+struct P8Walk {
+    long long left;
+    int entry, g, off;
+    __device__ bool next(const PagedFp8Params& p, P8Segment& s) {
+        if (left <= 0) return false;
+        int n = p8_tiles<RP>(p, entry);
+        while (n == 0) n = p8_tiles<RP>(p, ++entry);
+        s.entry = entry;
+        s.g = g;
+        s.i0 = off;
+        s.i1 = (int)min((long long)n, off + left);
+        s.n = n;
+        left -= s.i1 - s.i0;
+        off = 0;
+        if (++g == p.G) {
+            g = 0;
+            ++entry;
+        }
+        return true;
+    }
+};
+
+struct P8Plan {
+    long long total, begin, end;   // tiles of the call, and this CTA's
+    int entry, g, off;             // where it begins
+    int ctas;                      // CTAs that share the tiles
+};
+
+// All threads: sums the tiles of all entries, each thread over a contiguous
+// range of them, and finds where this CTA's share begins.
+template <int RP>
+__device__ void p8_make_plan(const PagedFp8Params& p, P8Plan* plan, long long* warp_sum) {
+    const int entries = p.B * p.row_tiles;
+    const int per = (entries + kP8Threads - 1) / kP8Threads;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int e0 = min((long long)entries, (long long)threadIdx.x * per), e1 = min(entries, e0 + per);
+    long long mine = 0;
+    for (int e = e0; e < e1; ++e) mine += p8_tiles<RP>(p, e);
+    mine *= p.G;
+    long long x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    long long before = x - mine, total = 0;
+    for (int w = 0; w < kP8Threads / 32; ++w) {
+        if (w < warp) before += warp_sum[w];
+        total += warp_sum[w];
+    }
+    const long long most = total / p.min_tiles;
+    const int ctas = (int)max(1ll, min((long long)gridDim.x, most));
+    const int c = blockIdx.x;
+    const long long t0 = c < ctas ? total * c / ctas : total;
+    const long long t1 = c < ctas ? total * (c + 1) / ctas : total;
+    if (threadIdx.x == 0) {
+        plan->total = total;
+        plan->begin = t0;
+        plan->end = t1;
+        plan->ctas = ctas;
+        plan->entry = plan->g = plan->off = 0;
+    }
+    __syncthreads();
+    if (t0 < t1 && t0 >= before && t0 < before + mine) {
+        long long at = before;
+        int e = e0, n = p8_tiles<RP>(p, e);
+        while (at + (long long)n * p.G <= t0) {
+            at += (long long)n * p.G;
+            n = p8_tiles<RP>(p, ++e);
+        }
+        plan->entry = e;
+        plan->g = (int)((t0 - at) / n);
+        plan->off = (int)((t0 - at) % n);
+    }
+    __syncthreads();
+}
+
+// Sums v[r] of the warp's lanes; lane i returns row i % RP. v is overwritten.
+template <int RP>
+__device__ __forceinline__ float reduce_rows(float (&v)[RP], int lane) {
+#pragma unroll
+    for (int o = RP / 2; o >= 1; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float send = up ? v[i] : v[i + o];
+            const float keep = up ? v[i + o] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+    }
+    float s = v[0];
+#pragma unroll
+    for (int o = RP; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+
+// Query row r of entry (b, rt): its index in [B, sq, H], or -1 past the last.
+template <int RP>
+__device__ __forceinline__ int p8_out_row(const PagedFp8Params& p, int b, int rt, int g, int r, int* s_tok) {
+    const int rr = rt * RP + r;
+    if (rr >= p.R) return -1;
+    const int s = rr / p.heads_per_group;
+    *s_tok = s;
+    return (b * p.sq + s) * p.H + g * p.heads_per_group + (rr - s * p.heads_per_group);
+}
+
+// ------------------------------------------------------------------- kernel
+
+template <int D, int RP>
+__global__ void __launch_bounds__(kP8Threads, 1)
+    gqa_paged_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                         const PagedFp8Params p) {
+    using PS = P8Shape<D, RP>;
+    constexpr int S = PS::kStages;
+    constexpr uint32_t TB = PS::kTileBytes;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    const uint32_t k_s = base, v_s = k_s + S * TB, q_s = v_s + S * TB, p_s = q_s + 2 * PS::kQBytes;
+    unsigned char* gen = smem_raw + (p_s + 2 * PS::kPBytes - raw);
+    float* stage_o = reinterpret_cast<float*>(gen);                       // [RP][D], then m[RP], l[RP]
+    gen += 4 * PS::kStageFloats;
+    // Row of the unit in q buffer i: {scale2 * 2^-e, last visible key, output row}.
+    int4* row_info = reinterpret_cast<int4*>(gen);                        // [2][RP]
+    gen += PS::kRowInfoBytes;
+    float4* sums = reinterpret_cast<float4*>(gen);                        // [2][RP], one component a warp
+    gen += PS::kSumBytes;
+    float* neg_ref = reinterpret_cast<float*>(gen);                       // [2][RP]: -m
+    gen += PS::kRefBytes;
+    int* warp_max = reinterpret_cast<int*>(gen);                          // [2][4][RP + 1]
+    gen += PS::kWarpMaxBytes;
+    P8Plan* plan = reinterpret_cast<P8Plan*>(gen);                        // 40 bytes
+    int* vote = reinterpret_cast<int*>(gen + 64);                         // [2][2]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gen + 80);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(gen + 84);
+    gen += PS::kMiscBytes;
+    const uint32_t bar0 = smem_addr(gen);
+    const uint32_t k_full = bar0, k_empty = k_full + 8 * S, v_full = k_empty + 8 * S, v_empty = v_full + 8 * S;
+    const uint32_t q_full = v_empty + 8 * S, q_empty = q_full + 16;
+    const uint32_t s_full = q_empty + 16, p_full = s_full + 16, o_done = p_full + 16, grp = o_done + 16;
+    const uint32_t m_full = grp + 16, m_empty = m_full + 8, fin = m_empty + 8;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint64_t tmo = p.wait_timeout_ns;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(k_full + 8 * s, 1);
+            mbar_init(k_empty + 8 * s, 1);
+            mbar_init(v_full + 8 * s, 1);
+            mbar_init(v_empty + 8 * s, 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(q_full + 8 * x, 1);
+            mbar_init(q_empty + 8 * x, 9);     // eight softmax warps and the products
+            mbar_init(s_full + 8 * x, 1);
+            mbar_init(p_full + 8 * x, 4);
+            mbar_init(o_done + 8 * x, 1);
+            mbar_init(grp + 8 * x, 4);
+        }
+        mbar_init(m_full, 4);
+        mbar_init(m_empty, 4);
+        mbar_init(fin, 1);
+        *abort_flag = 0;
+        vote[0] = vote[1] = vote[2] = vote[3] = 0;
+        fence_barrier_init();
+    }
+    if (warp == 10) {
+        tmem_alloc(smem_addr(tmem_slot), PS::kTmemCols);
+        tmem_relinquish();
+    }
+    if (warp == 8 && lane == 0) tma_prefetch_desc(&tm_k);
+    if (warp == 9 && lane == 0) tma_prefetch_desc(&tm_v);
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    p8_make_plan<RP>(p, plan, reinterpret_cast<long long*>(stage_o));   // synchronises the CTA
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    P8Walk<RP> walk = {plan->end - plan->begin, plan->entry, plan->g, plan->off};
+    P8Segment seg;
+
+    if (warp == 8 || warp == 9) {
+        // -------------------------------------------------- K and V loaders
+        const bool is_v = warp == 9;
+        const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
+        const uint32_t full = is_v ? v_full : k_full, empty = is_v ? v_empty : k_empty;
+        const uint32_t ring = is_v ? v_s : k_s;
+        const int page_size = 1 << p.page_shift;
+        const int box = min(page_size, kP8Tokens);
+        const int boxes = kP8Tokens / box;
+        const uint64_t pol = l2_policy_evict_first();
+        int it = 0, issued = 0;
+        bool ok = true;
+        while (ok && walk.next(p, seg)) {
+            const int b = seg.entry / p.row_tiles;
+            const int T = p8_len(p, b);
+            const int32_t* row = p.table + (size_t)b * p.max_pages;
+            // This lane's page of a tile; looked up one tile ahead.
+            auto lookup = [&](int i) {
+                const int pos = i * kP8Tokens + lane * box;
+                return lane < boxes && i < seg.i1 && pos < T ? row[pos >> p.page_shift] : -1;
+            };
+            int page = lookup(seg.i0);
+            for (int i = seg.i0; i < seg.i1; ++i, ++it) {
+                const int s = it % S;
+                const int cur = page;
+                page = lookup(i + 1);
+                const int pos = i * kP8Tokens + lane * box;
+                const int here = min(boxes, (T - i * kP8Tokens + box - 1) / box);   // boxes that hold keys
+                ok = warp_wait(empty + 8 * s, ((it / S) & 1) ^ 1, abort_flag, p.status, tmo);
+                if (!ok) break;
+                if (!is_v && blockIdx.x == 0 && it == p.skip_tile) continue;   // injected fault: never loaded
+                if (lane == 0) mbar_arrive_expect_tx(full + 8 * s, here * box * D);
+                __syncwarp();
+                if (lane < here) {
+                    // A page outside the pool is a slab out of range: zeros.
+                    const int z = (unsigned)cur < (unsigned)p.num_pages ? cur * p.G + seg.g : -1;
+                    tma_load_3d_hint(ring + s * TB + lane * box * D, tm, full + 8 * s, 0, pos & (page_size - 1), z,
+                                     pol);
+                }
+                __syncwarp();
+                issued = it + 1;
+            }
+        }
+        // Leave only once the last copies have landed.
+        if (lane == 0)
+            for (int j = issued > S ? issued - S : 0; j < issued; ++j) {
+                if (!is_v && blockIdx.x == 0 && j == p.skip_tile) continue;
+                const uint64_t t0 = global_timer_ns();
+                while (!mbar_try_wait(full + 8 * (j % S), (j / S) & 1))
+                    if (global_timer_ns() - t0 > tmo) break;
+            }
+        __syncwarp();
+    } else if (warp == 10) {
+        // ------------------------------------------------------- products
+        constexpr uint64_t kLayout = D == 128 ? 2 : 4;
+        constexpr uint32_t kAtom = 8 * D;                                   // 8 rows of K, V or Q
+        constexpr uint32_t kIdescS = p8_idesc(kP8Tokens, PS::kNs, false, false);
+        constexpr uint32_t kIdescO = p8_idesc(D, PS::kNp, true, true);
+        bool ok = true, issued = false;
+        // S runs one tile ahead of O, across segments.
+        P8Walk<RP> ahead = walk;
+        P8Segment aseg;
+        bool have = ahead.next(p, aseg);
+        int ai = have ? aseg.i0 : 0, ait = 0, asg = 0;
+        auto issue_s = [&]() {
+            if (!have) return true;
+            if (ai == aseg.i0 && !warp_wait(q_full + 8 * (asg & 1), (asg >> 1) & 1, abort_flag, p.status, tmo))
+                return false;
+            const int s = ait % S, x = ait & 1;
+            if (!warp_wait(k_full + 8 * s, (ait / S) & 1, abort_flag, p.status, tmo)) return false;
+            const bool last = ai + 1 == aseg.i1;
+            if (lane == 0) {
+                tc_fence_after();
+                const uint32_t kt = k_s + s * TB, qt = q_s + (asg & 1) * PS::kQBytes;
+#pragma unroll
+                for (int kk = 0; kk < D / 32; ++kk)
+                    umma_f8(tmem + PS::kColS + x * PS::kNs, p8_desc(kt + kk * 32, 16, kAtom, kLayout),
+                            p8_desc(qt + kk * 32, 16, kAtom, kLayout), kIdescS, kk > 0 ? 1u : 0u);
+                umma_commit(s_full + 8 * x);
+                umma_commit(k_empty + 8 * s);
+                if (last) umma_commit(q_empty + 8 * (asg & 1));
+            }
+            __syncwarp();
+            issued = true;
+            ++ait;
+            if (last) {
+                have = ahead.next(p, aseg);
+                ai = aseg.i0;
+                ++asg;
+            } else {
+                ++ai;
+            }
+            return true;
+        };
+        ok = issue_s();
+        int it = 0;
+        uint32_t np[2] = {0, 0};
+        while (ok && walk.next(p, seg)) {
+            bool first[2] = {true, true};
+            for (int i = seg.i0; i < seg.i1; ++i, ++it) {
+                const int s = it % S, x = it & 1;
+                ok = issue_s() && warp_wait(v_full + 8 * s, (it / S) & 1, abort_flag, p.status, tmo) &&
+                     warp_wait(p_full + 8 * x, (x ? np[1] : np[0]) & 1, abort_flag, p.status, tmo);
+                if (!ok) break;
+                const bool fresh = x ? first[1] : first[0];
+                if (x) ++np[1], first[1] = false; else ++np[0], first[0] = false;
+                if (lane == 0) {
+                    tc_fence_after();
+                    const uint32_t vt = v_s + s * TB, pt = p_s + x * PS::kPBytes;
+#pragma unroll
+                    for (int kk = 0; kk < kP8Tokens / 32; ++kk)
+                        umma_f8(tmem + PS::kColO + x * PS::kNp, p8_desc(vt + kk * 32 * D, 16, kAtom, kLayout),
+                                p8_desc(pt + kk * 512, 128, 2048, 0), kIdescO, (!fresh || kk > 0) ? 1u : 0u);
+                    umma_commit(o_done + 8 * x);
+                    umma_commit(v_empty + 8 * s);
+                }
+                __syncwarp();
+            }
+        }
+        if (issued && lane == 0) {
+            umma_commit(fin);
+            const uint64_t t0 = global_timer_ns();
+            while (!mbar_try_wait(fin, 0))
+                if (global_timer_ns() - t0 > tmo) {
+                    atomicOr(p.status, kStatusTimeout);
+                    break;
+                }
+        }
+        __syncwarp();
+    } else if (warp == 11) {
+        // ------------------------------------------------------------ Q rows
+        PagedFp8Split split = {-1, 0, 0, 0};
+        long long at = plan->begin;
+        int sg = 0;
+        bool ok = true;
+        while (ok && walk.next(p, seg)) {
+            if (seg.i0 == 0 && seg.i1 < seg.n)
+                split = {seg.entry, seg.g, (int)(((at + seg.n) * plan->ctas - 1) / plan->total), 0};
+            at += seg.i1 - seg.i0;
+            const int buf = sg & 1;
+            ok = warp_wait(q_empty + 8 * buf, ((sg >> 1) & 1) ^ 1, abort_flag, p.status, tmo);
+            if (!ok) break;
+            const int b = seg.entry / p.row_tiles, rt = seg.entry - b * p.row_tiles;
+            const int T = p8_len(p, b);
+            const uint32_t qt = q_s + buf * PS::kQBytes;
+            constexpr int kPer = D / 32;          // elements of a row per lane
+#pragma unroll
+            for (int r0 = 0; r0 < RP; r0 += 8) {
+                uint32_t w[8][kPer / 2];
+                int orow[8], tok[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    tok[i] = 0;
+                    orow[i] = p8_out_row<RP>(p, b, rt, seg.g, r0 + i, &tok[i]);
+#pragma unroll
+                    for (int c = 0; c < kPer / 2; ++c) w[i][c] = 0;
+                    if (orow[i] >= 0) {
+                        const uint16_t* src = p.q + (size_t)orow[i] * D + lane * kPer;
+                        if constexpr (kPer == 4) {
+                            const uint2 v = *reinterpret_cast<const uint2*>(src);
+                            w[i][0] = v.x;
+                            w[i][1] = v.y;
+                        } else {
+                            w[i][0] = *reinterpret_cast<const uint32_t*>(src);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = r0 + i;
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int c = 0; c < kPer / 2; ++c)
+                        top = max(top, max(w[i][c] & 0x7fffu, (w[i][c] >> 16) & 0x7fffu));
+                    top = __reduce_max_sync(0xffffffffu, top);
+                    const bool bad = top >= 0x7f80u;              // an infinity or NaN: the whole row is NaN
+                    const int e = min(134 - max((int)(top >> 7), 1), 120);
+                    const float up = bad || top == 0 ? 0.f : pow2i(e);
+                    uint32_t hi = 0, lo = 0;
+#pragma unroll
+                    for (int c = 0; c < kPer / 2; ++c) {
+                        const float a = bad ? 0.f : __uint_as_float(w[i][c] << 16) * up;
+                        const float d = bad ? 0.f : __uint_as_float(w[i][c] & 0xffff0000u) * up;
+                        const uint32_t h = f32x2_to_e4m3x2(a, d);
+                        const uint32_t hf = e4m3x2_to_f16x2((uint16_t)h);
+                        const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hf));
+                        hi |= h << (16 * c);
+                        lo |= f32x2_to_e4m3x2((a - back.x) * 16.f, (d - back.y) * 16.f) << (16 * c);
+                    }
+                    const uint32_t at_byte = lane * kPer;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const uint32_t row = t * RP + r;
+                        const uint32_t sw = D == 128 ? (row & 7) : ((row >> 1) & 3);
+                        const uint32_t addr = qt + row * D + ((((at_byte >> 4) ^ sw) << 4) | (at_byte & 15));
+                        if constexpr (kPer == 4)
+                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(t ? lo : hi) : "memory");
+                        else
+                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"((uint16_t)(t ? lo : hi)) : "memory");
+                    }
+                    if (lane == 0) {
+                        const float f = orow[i] < 0 ? 0.f : bad ? __int_as_float(0x7fffffff)
+                                                                : p.scale_log2 * (top == 0 ? 1.f : pow2i(-e));
+                        row_info[buf * RP + r] =
+                            make_int4(__float_as_int(f), orow[i] < 0 ? -1 : T - p.sq + tok[i], orow[i], 0);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full + 8 * buf);
+            ++sg;
+        }
+        if (lane == 0) p.splits[blockIdx.x] = split;
+        // Entries none of whose rows sees a key own no tile: out = 0, lse = -inf.
+        for (int e = blockIdx.x; e < p.B * p.row_tiles; e += gridDim.x) {
+            if (p8_tiles<RP>(p, e) > 0) continue;
+            const int b = e / p.row_tiles, rt = e - b * p.row_tiles;
+            for (int x = 0; x < p.G * RP; ++x) {
+                int tok;
+                const int orow = p8_out_row<RP>(p, b, rt, x / RP, x % RP, &tok);
+                if (orow < 0) continue;
+                if (lane < D / 8) *reinterpret_cast<uint4*>(p.out + (size_t)orow * D + lane * 8) = make_uint4(0, 0, 0, 0);
+                if (p.lse && lane == 0) p.lse[orow] = -INFINITY;
+            }
+        }
+    } else {
+        // ----------------------------------------- softmax groups, one thread a token
+        const int x = warp >> 2, w4 = warp & 3;
+        const int tok = threadIdx.x & 127;
+        const uint32_t lane_base = tmem + ((uint32_t)(w4 * 32) << 16);
+        const uint32_t s_tm = lane_base + PS::kColS + x * PS::kNs;
+        const uint32_t o_tm = lane_base + PS::kColO + x * PS::kNp;
+        const uint32_t p_at = p_s + x * PS::kPBytes + tok * 16;
+        float* const my_ref = neg_ref + x * RP;
+        int* const my_max = warp_max + x * 4 * (RP + 1);
+        uint32_t n_grp = 0, n_tiles = 0, n_merge = 0;   // phases of grp, of s_full / o_done, of m_full
+        bool ok = true;
+        auto group_sync = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(grp + 8 * x);
+            const bool r = warp_wait(grp + 8 * x, n_grp & 1, abort_flag, p.status, tmo);
+            ++n_grp;
+            return r;
+        };
+        int it0 = 0, sg = 0;     // the CTA's tile number at the segment's start
+        while (ok && walk.next(p, seg)) {
+            const int b = seg.entry / p.row_tiles, rt = seg.entry - b * p.row_tiles;
+            const int T = p8_len(p, b);
+            const int32_t* table = p.table + (size_t)b * p.max_pages;
+            const int4* info = row_info + (sg & 1) * RP;
+            const int lim_min = T - p.sq + (rt * RP) / p.heads_per_group;   // every row sees keys up to here
+            const int first_i = seg.i0 + ((it0 & 1) != x ? 1 : 0);          // this group's first tile
+            auto page_of = [&](int i) {
+                const int pos = i * kP8Tokens + tok;
+                if (i >= seg.i1 || pos >= T) return -1;
+                const int e = table[pos >> p.page_shift];
+                return (unsigned)e < (unsigned)p.num_pages ? e : -1;
+            };
+            auto scales_of = [&](int page, int i, float& ks, float& vs) {
+                ks = vs = 0.f;
+                if (page >= 0) {
+                    const int pos = i * kP8Tokens + tok;
+                    const size_t at = ((size_t)page * p.G + seg.g) * p.blocks + ((pos & ((1 << p.page_shift) - 1)) >> 6);
+                    ks = p.k_scale[at];
+                    vs = p.v_scale[at];
+                }
+            };
+            float ks, vs, l[RP];
+            int ev = 0;
+#pragma unroll
+            for (int r = 0; r < RP; ++r) l[r] = 0.f;
+            scales_of(page_of(first_i), first_i, ks, vs);
+            int page_next = page_of(first_i + 2);
+            bool first = true;
+            // Also keeps a group without a tile here from running ahead.
+            ok = warp_wait(q_full + 8 * (sg & 1), (sg >> 1) & 1, abort_flag, p.status, tmo);
+            if (!ok) break;
+            for (int i = first_i; i < seg.i1; i += 2) {
+                const int it = it0 + i - seg.i0;
+                const int pos = i * kP8Tokens + tok;
+                // The next tile's scales, and the page of the one after it.
+                float ks_next, vs_next;
+                scales_of(page_next, i + 2, ks_next, vs_next);
+                page_next = page_of(i + 4);
+                const bool edge = (i + 1) * kP8Tokens - 1 > lim_min;        // some row does not see all of it
+
+                ok = warp_wait(s_full + 8 * x, n_tiles & 1, abort_flag, p.status, tmo);
+                if (!ok) break;
+                tc_fence_after();
+                float xs[RP];
+                {
+                    uint32_t h[RP], lo[RP];
+                    if constexpr (RP == 8) {
+                        uint32_t t[16];
+                        tmem_ld16(s_tm, t);
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) h[r] = t[r], lo[r] = t[8 + r];
+                    } else if constexpr (RP == 16) {
+                        tmem_ld16(s_tm, h);
+                        tmem_ld16(s_tm + 16, lo);
+                    } else {
+                        tmem_ld32(s_tm, h);
+                        tmem_ld32(s_tm + 32, lo);
+                    }
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int r = 0; r < RP; ++r) {
+                        const float f = __int_as_float(info[r].x) * ks;
+                        xs[r] = fmaf(__uint_as_float(lo[r]), 0.0625f, __uint_as_float(h[r])) * f;
+                        if (edge && pos > info[r].y) xs[r] = -INFINITY;
+                        if (!first) top = fmaxf(top, xs[r] + my_ref[r]);
+                    }
+                    // A NaN or infinite scale makes its block's values NaN.
+                    if (!(fabsf(vs) <= 3.402823466e38f)) vs = __int_as_float(0x7fffffff);
+                    const bool moves = first || top > kP8Slack || fabsf(vs) * pow2i(-ev) > kP8ScaleSlack;
+                    if (__any_sync(0xffffffffu, moves) && lane == 0) vote[2 * x + (n_tiles & 1)] = it + 1;
+                }
+                ok = group_sync();
+                if (!ok) break;
+                if (reinterpret_cast<volatile int*>(vote)[2 * x + (n_tiles & 1)] == it + 1) {
+                    // Move the references: rows whose tile maximum is out of range.
+                    int mine = 0;
+#pragma unroll
+                    for (int r = 0; r < RP; ++r) {
+                        const int m = __reduce_max_sync(0xffffffffu, ordered(xs[r]));
+                        if (lane == r) mine = m;
+                    }
+                    const uint32_t vb = __float_as_uint(fabsf(vs));
+                    const uint32_t vtop = __reduce_max_sync(0xffffffffu, vb <= 0x7f7fffffu ? vb : 0u);
+                    if (lane < RP) my_max[w4 * (RP + 1) + lane] = mine;
+                    if (lane == 0) my_max[w4 * (RP + 1) + RP] = (int)vtop;
+                    const float m_old = first || lane >= RP ? kP8Unseen : -my_ref[lane];
+                    ok = group_sync();
+                    if (!ok) break;
+                    float m_new = m_old;
+                    if (lane < RP) {
+                        const float m = unordered(max(max(my_max[lane], my_max[RP + 1 + lane]),
+                                                      max(my_max[2 * (RP + 1) + lane], my_max[3 * (RP + 1) + lane])));
+                        if (m > m_old + kP8Slack) m_new = m;
+                    }
+                    const int vm = max(max(my_max[RP], my_max[2 * RP + 1]), max(my_max[3 * RP + 2], my_max[4 * RP + 3]));
+                    // 2^-ev brings the largest scale to [0.5, 1).
+                    const int ev_top = min(max((vm >> 23) - 126, -60), 126);
+                    const int ev_new = first || __int_as_float(vm) * pow2i(-ev) > kP8ScaleSlack ? ev_top : ev;
+                    const float alpha = fast_exp2(m_old - m_new);
+                    const float alpha_o = first ? 0.f : alpha * pow2i(max(ev - ev_new, -126));
+                    if (w4 == 0 && lane < RP) my_ref[lane] = -m_new;
+                    ev = ev_new;
+#pragma unroll
+                    for (int r = 0; r < RP; ++r) l[r] *= __shfl_sync(0xffffffffu, alpha, r);
+                    if (!first) {
+                        // Every product of this group so far has completed.
+                        ok = warp_wait(o_done + 8 * x, (n_tiles - 1) & 1, abort_flag, p.status, tmo);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int c = 0; c < 3 * RP / 8; ++c) {
+                            uint32_t o[8];
+                            tmem_ld8(o_tm + 8 * c, o);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                o[k] = __float_as_uint(__uint_as_float(o[k]) *
+                                                       __shfl_sync(0xffffffffu, alpha_o, (8 * c + k) % RP));
+                            tmem_st8(o_tm + 8 * c, o);
+                        }
+                        tmem_st_wait();
+                    }
+                    ok = group_sync();
+                    if (!ok) break;
+                }
+                if (edge) {
+                    // Rows of V past the length may hold anything: zero them. A
+                    // NaN code in a key that only some rows see would reach the
+                    // others as 0 * NaN: its row is zeroed too, and the rows that
+                    // see it are made NaN through P.
+                    const int s = it % S;
+                    ok = warp_wait(v_full + 8 * s, (it / S) & 1, abort_flag, p.status, tmo);
+                    if (!ok) break;
+                    if (pos > lim_min) {
+                        const uint32_t at = v_s + s * TB + tok * D;
+                        bool clear = pos >= T;
+                        if (!clear) {
+                            uint32_t nan = 0;
+#pragma unroll
+                            for (int c = 0; c < D / 16; ++c) {
+                                uint32_t u[4];
+                                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                             : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+                                             : "r"(at + 16 * c));
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)   // a byte with its low seven bits set
+                                    nan |= ((u[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                            }
+                            clear = nan != 0;
+                            if (clear) vs = __int_as_float(0x7fffffff);
+                        }
+                        if (clear)
+#pragma unroll
+                            for (int c = 0; c < D / 16; ++c) st_shared_zero16(at + 16 * c);
+                    }
+                }
+                // P's operand is free once the group's previous product is done.
+                if (n_tiles > 0) ok = warp_wait(o_done + 8 * x, (n_tiles - 1) & 1, abort_flag, p.status, tmo);
+                if (!ok) break;
+                const float vw = vs * pow2i(-ev) * kP8ProbScale;
+                uint32_t packed[RP / 4][3];       // four rows: hi, mid, lo
+#pragma unroll
+                for (int r = 0; r < RP; r += 2) {
+                    float w[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float pr = fast_exp2(xs[r + k] + my_ref[r + k]);
+                        l[r + k] += pr;
+                        w[k] = pr * vw;
+                        if (edge && pos > info[r + k].y) w[k] = 0.f;
+                    }
+                    const uint32_t f = pack_f16x2(w[0], w[1]);
+                    const uint32_t hi = f16x2_to_e4m3x2(f);
+                    const uint32_t f1 = residual16(f, e4m3x2_to_f16x2((uint16_t)hi));
+                    const uint32_t mid = f16x2_to_e4m3x2(f1);
+                    const uint32_t f2 = residual16(f1, e4m3x2_to_f16x2((uint16_t)mid));
+                    const uint32_t lo = f16x2_to_e4m3x2(f2);
+                    if ((r & 2) == 0) {
+                        packed[r / 4][0] = hi;
+                        packed[r / 4][1] = mid;
+                        packed[r / 4][2] = lo;
+                    } else {
+                        packed[r / 4][0] |= hi << 16;
+                        packed[r / 4][1] |= mid << 16;
+                        packed[r / 4][2] |= lo << 16;
+                    }
+                }
+                // Column term * RP + r; 16 columns of a token are 16 bytes.
+                if constexpr (RP == 8) {
+                    st_shared_v4(p_at, make_uint4(packed[0][0], packed[1][0], packed[0][1], packed[1][1]));
+                    st_shared_v4(p_at + 2048, make_uint4(packed[0][2], packed[1][2], 0u, 0u));
+                } else {
+#pragma unroll
+                    for (int t = 0; t < 3; ++t)
+#pragma unroll
+                        for (int c = 0; c < RP / 16; ++c)
+                            st_shared_v4(p_at + (t * (RP / 16) + c) * 2048,
+                                         make_uint4(packed[4 * c][t], packed[4 * c + 1][t], packed[4 * c + 2][t],
+                                                    packed[4 * c + 3][t]));
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + 8 * x);
+                ++n_tiles;
+                first = false;
+                ks = ks_next;
+                vs = vs_next;
+            }
+            if (!ok) break;
+
+            // ------------------------------------------------ end of a segment
+            const int len = seg.i1 - seg.i0;
+            const int cnt0 = (len + ((it0 & 1) == 0 ? 1 : 0)) / 2, cnt1 = len - cnt0;
+            const int cnt = x ? cnt1 : cnt0;
+            const bool both = cnt0 > 0 && cnt1 > 0;
+            if (cnt > 0) {
+                const float sum = reduce_rows<RP>(l, lane);
+                if (lane < RP) reinterpret_cast<float*>(sums + x * RP + lane)[w4] = sum;
+                ok = group_sync() && warp_wait(o_done + 8 * x, (n_tiles - 1) & 1, abort_flag, p.status, tmo);
+                if (!ok) break;
+                tc_fence_after();
+                float o[RP];
+#pragma unroll
+                for (int r = 0; r < RP; ++r) o[r] = 0.f;
+#pragma unroll
+                for (int c = 0; c < 3 * RP / 8; ++c) {
+                    uint32_t t[8];
+                    tmem_ld8(o_tm + 8 * c, t);
+                    const float f = 8 * c < RP ? 1.f : 8 * c < 2 * RP ? 0.0625f : 0.00390625f;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) o[(8 * c + k) % RP] = fmaf(__uint_as_float(t[k]), f, o[(8 * c + k) % RP]);
+                }
+                tc_fence_before();
+                // D = 64 products keep 16 of their rows in each warp's 32 lanes.
+                const bool mine = D == 128 || lane < 16;
+                const int dim = D == 128 ? tok : w4 * 16 + lane;
+                const float unit = pow2i(ev) * (1.f / kP8ProbScale);
+                if (both && x == 1) {
+                    ok = warp_wait(m_empty, (n_merge & 1) ^ 1, abort_flag, p.status, tmo);
+                    if (!ok) break;
+#pragma unroll
+                    for (int r = 0; r < RP; ++r)
+                        if (mine) stage_o[r * D + dim] = o[r] * unit;
+                    if (tok < RP) {
+                        const float4 q = sums[x * RP + tok];
+                        stage_o[RP * D + tok] = -my_ref[tok];
+                        stage_o[RP * D + RP + tok] = q.x + q.y + q.z + q.w;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(m_full);
+                    ++n_merge;
+                } else {
+                    if (both) {
+                        ok = warp_wait(m_full, n_merge & 1, abort_flag, p.status, tmo);
+                        if (!ok) break;
+                    }
+                    const bool whole = seg.i0 == 0 && seg.i1 == seg.n;
+                    float* slot = p.part + ((size_t)blockIdx.x * 2 + (seg.i0 == 0 ? 1 : 0)) * p8_slot_floats(RP, D);
+#pragma unroll
+                    for (int r = 0; r < RP; ++r) {
+                        const float4 q = sums[x * RP + r];
+                        float m = -my_ref[r], ls = q.x + q.y + q.z + q.w, y = o[r] * unit;
+                        if (both) {
+                            const float m1 = stage_o[RP * D + r], l1 = stage_o[RP * D + RP + r];
+                            const float top = fmaxf(m, m1);
+                            const float a0 = fast_exp2(m - top), a1 = fast_exp2(m1 - top);
+                            m = top;
+                            ls = ls * a0 + l1 * a1;
+                            y = y * a0 + (mine ? stage_o[r * D + dim] : 0.f) * a1;
+                        }
+                        const int orow = info[r].z;
+                        if (orow < 0) continue;
+                        if (whole) {
+                            const bool some = ls > 0.f || ls != ls;
+                            if (mine)
+                                p.out[(size_t)orow * D + dim] =
+                                    (uint16_t)(pack_bf16x2(some ? y / ls : 0.f, 0.f) & 0xffffu);
+                            if (p.lse && tok == r)
+                                p.lse[orow] = some ? (m + log2f(ls)) * 0.6931471805599453f : -INFINITY;
+                        } else {
+                            if (mine) slot[r * D + dim] = y;
+                            if (tok == r) {
+                                slot[RP * D + r] = m;
+                                slot[RP * D + RP + r] = ls;
+                            }
+                        }
+                    }
+                    if (both) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(m_empty);
+                        ++n_merge;
+                    }
+                }
+                // The sums and references are read before the next segment writes them.
+                ok = group_sync();
+                if (!ok) break;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_empty + 8 * (sg & 1));
+            it0 += len;
+            ++sg;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 10) tmem_dealloc(tmem, PS::kTmemCols);
+}
+
+// Merges the partial results of the units that cross CTAs: one warp per row of
+// the unit that CTA blockIdx.x began,
+//     M = max m_c, L = sum l_c 2^(m_c - M), O = sum O_c 2^(m_c - M) / L.
+template <int D, int RP>
+__global__ void __launch_bounds__(128) gqa_paged_fp8_merge(const PagedFp8Params p) {
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    const PagedFp8Split s = p.splits[blockIdx.x];
+    if (s.entry < 0) return;
+    const int lane = threadIdx.x & 31, r = blockIdx.y * 4 + (threadIdx.x >> 5);
+    const int b = s.entry / p.row_tiles, rt = s.entry - b * p.row_tiles;
+    int tok;
+    const int orow = p8_out_row<RP>(p, b, rt, s.g, r, &tok);
+    if (orow < 0) return;
+    const int c0 = blockIdx.x, n = s.last_cta - c0 + 1;
+    const size_t slot = p8_slot_floats(RP, D);
+    // The first contributor's second slot, then every other's first.
+    auto at = [&](int i) { return p.part + ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * slot; };
+    float top = kP8Unseen;
+    for (int i = lane; i < n; i += 32) top = fmaxf(top, at(i)[RP * D + r]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float l = 0.f;
+    for (int i = lane; i < n; i += 32) l += at(i)[RP * D + RP + r] * fast_exp2(at(i)[RP * D + r] - top);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    constexpr int kPer = D / 32;
+    float y[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) y[k] = 0.f;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+        const float* src = at(i);
+        const float a = fast_exp2(src[RP * D + r] - top);
+        if constexpr (kPer == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(src + r * D + lane * 4);
+            y[0] = fmaf(v.x, a, y[0]);
+            y[1] = fmaf(v.y, a, y[1]);
+            y[2] = fmaf(v.z, a, y[2]);
+            y[3] = fmaf(v.w, a, y[3]);
+        } else {
+            const float2 v = *reinterpret_cast<const float2*>(src + r * D + lane * 2);
+            y[0] = fmaf(v.x, a, y[0]);
+            y[1] = fmaf(v.y, a, y[1]);
+        }
+    }
+    const bool some = l > 0.f || l != l;
+    const float inv = some ? 1.f / l : 0.f;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (size_t)orow * D + lane * kPer);
+#pragma unroll
+    for (int k = 0; k < kPer / 2; ++k) dst[k] = pack_bf16x2(some ? y[2 * k] * inv : 0.f, some ? y[2 * k + 1] * inv : 0.f);
+    if (p.lse && lane == 0) p.lse[orow] = some ? (top + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+template <int D, int RP>
+cudaError_t launch_paged_fp8(const PagedFp8Launch& a) {
+    using PS = P8Shape<D, RP>;
+    // The shared-memory opt-in is per function and per device.
+    static std::atomic<unsigned long long> attr_set_mask{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(attr_set_mask.load() & bit)) {
+        e = cudaFuncSetAttribute(gqa_paged_fp8_kernel<D, RP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 PS::kSmemBytes);
+        if (e != cudaSuccess) return e;
+        attr_set_mask.fetch_or(bit);
+    }
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.grid);
+    cfg.blockDim = dim3(kP8Threads);
+    cfg.dynamicSmemBytes = PS::kSmemBytes;
+    cfg.stream = a.stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, gqa_paged_fp8_kernel<D, RP>, a.tm_k, a.tm_v, a.p);
+    if (e != cudaSuccess || a.grid == 1) return e;
+    cfg.gridDim = dim3(a.grid, RP / 4);
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, gqa_paged_fp8_merge<D, RP>, a.p);
+}
+
+template <int D>
+cudaError_t launch_paged_fp8_rows(const PagedFp8Launch& a) {
+    switch (p8_rows(a.p.R)) {
+        case 8: return launch_paged_fp8<D, 8>(a);
+        case 16: return launch_paged_fp8<D, 16>(a);
+        default: return launch_paged_fp8<D, 32>(a);
+    }
+}
+
+}  // namespace gqa

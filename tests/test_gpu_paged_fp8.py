@@ -20,7 +20,7 @@ import grouped_query_decode_gb300 as gq
 import oracle
 import paged_fp8_model as model
 import synthetic as syn
-from gpu_helpers import _CANARY_BF16, _CANARY_F32, _PAD, bf16_to_f64, to_device_bf16
+from gpu_helpers import _CANARY_BF16, _CANARY_F32, _PAD, bf16_to_f64, env, to_device_bf16
 
 pytestmark = pytest.mark.gpu
 
@@ -355,6 +355,20 @@ def test_replay_with_new_lengths_and_pages():
         g.replay()
         torch.cuda.synchronize()
         check(c, bf16_to_f64(o), l.cpu().numpy().astype(np.float64), what=str(lens))
+
+
+def test_an_expired_wait_is_reported_and_the_context_survives():
+    c = Case(660, 2, 1, 16, 2, 128, 64, [2000, 900])
+    d = c.device()
+    ref = run(c, d)
+    B, sq, H, G, D, page = c.shape
+    o = torch.empty(B, sq, H, D, dtype=torch.bfloat16, device="cuda")
+    with env(GQA_DECODE_DEBUG_TIMEOUT_MS=200, GQA_DECODE_DEBUG_SKIP_TILE=0):
+        gq.gqa_decode_paged_fp8(*d, c.sm, o)
+        assert gq.gqa_decode_check_error() == gq.GQA_ERR_DEVICE_TIMEOUT
+    for _ in range(2):
+        got = run(c, d)
+        assert np.array_equal(got[0], ref[0]) and np.array_equal(got[1], ref[1])
 
 
 def test_page_pool_past_2_31_codes():
