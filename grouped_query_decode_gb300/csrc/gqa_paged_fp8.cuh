@@ -41,8 +41,9 @@
 namespace gqa {
 
 constexpr int kP8Threads = 384;
-constexpr float kP8Slack = 2.0f;          // p <= 2^2 before the reference moves
-constexpr float kP8ProbScale = 64.0f;     // p * v_scale * 2^-ev * 64 <= 4 * 1.75 * 64 = 448
+constexpr int kP8Terms = 4;               // e4m3 columns per probability
+constexpr float kP8Slack = 4.0f;          // p <= 2^4 before the reference moves
+constexpr float kP8ProbScale = 16.0f;     // p * v_scale * 2^-ev * 16 <= 16 * 1.75 * 16 = 448
 constexpr float kP8ScaleSlack = 1.75f;
 constexpr float kP8Unseen = -3.402823466e38f;   // reference of a row that has seen no key
 
@@ -50,21 +51,22 @@ template <int D, int RP>
 struct P8Shape {
     static constexpr int kTileBytes = kP8Tokens * D;              // K or V of one tile
     static constexpr int kNs = 2 * RP;                            // columns of S: hi, lo
-    static constexpr int kNp = RP == 8 ? 32 : 3 * RP;             // columns of O: hi, mid, lo
+    static constexpr int kNp = kP8Terms * RP;                     // columns of O
     static constexpr int kQBytes = kNs * D;
     static constexpr int kPBytes = kP8Tokens * kNp;
     static constexpr int kStageFloats = RP * D + 2 * RP;          // one group's (O, m, l)
     // The ring takes what the rest leaves of 227 KB.
-    static constexpr int kStages = D == 128 ? (RP == 32 ? 5 : 6) : (RP == 32 ? 10 : 12);
-    static constexpr int kBars = 4 * kStages + 15;
-    static constexpr int kRowInfoBytes = 2 * RP * 16;
+    static constexpr int kStages = (D == 128 ? 1 : 2) * (RP == 32 ? 4 : RP == 16 ? 5 : 6);
+    static constexpr int kBars = 3 * kStages + 14;
+    static constexpr int kRowInfoBytes = 2 * 3 * RP * 4;
     static constexpr int kRefBytes = 2 * RP * 4;
     static constexpr int kWarpMaxBytes = 2 * 4 * (RP + 1) * 4;
     static constexpr int kSumBytes = 2 * RP * 16;
-    static constexpr int kMiscBytes = 128;
+    static constexpr int kLenBytes = kP8Threads * 4;
+    static constexpr int kMiscBytes = 192;
     static constexpr int kSmemBytes = 1024 + 2 * kStages * kTileBytes + 2 * kQBytes + 2 * kPBytes +
                                       4 * kStageFloats + kRowInfoBytes + kRefBytes + kWarpMaxBytes + kSumBytes +
-                                      kMiscBytes + 8 * kBars;
+                                      kLenBytes + kMiscBytes + 8 * kBars;
     static constexpr uint32_t kColS = 0, kColO = 2 * kNs;         // S_0 | S_1 | O_0 | O_1
     static constexpr uint32_t kCols = 2 * kNs + 2 * kNp;
     static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
@@ -108,19 +110,13 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-        : "r"(taddr)
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
-}
-
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
-                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
 }
 
 // ------------------------------------------------------------ e4m3 and fp16
@@ -155,18 +151,28 @@ __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) 
 
 // ---------------------------------------------------------------------- plan
 
-__device__ __forceinline__ int p8_len(const PagedFp8Params& p, int b) {
-    return clamp_len(p.lens[b], p.max_pages << p.page_shift);
-}
-
-// Tiles that the rows of entry (b, row tile) see.
+// Lengths, from the CTA's copy where the batch fits it, and the tiles that the
+// rows of an entry (b, row tile) see: with one row tile, all of the sequence's.
 template <int RP>
-__device__ __forceinline__ int p8_tiles(const PagedFp8Params& p, int entry) {
-    const int b = entry / p.row_tiles, rt = entry - b * p.row_tiles;
-    const int last = min(p.R, (rt + 1) * RP) - 1;
-    const int lim = p8_len(p, b) - p.sq + last / p.heads_per_group;
-    return lim < 0 ? 0 : lim / kP8Tokens + 1;
-}
+struct P8Lens {
+    const PagedFp8Params& p;
+    const int* copy;
+    __device__ int global(int b) const { return clamp_len(p.lens[b], p.max_pages << p.page_shift); }
+    __device__ int tokens(int b) const { return p.B <= kP8Threads ? copy[b] : global(b); }
+    __device__ void split(int entry, int& b, int& rt) const {
+        b = p.row_tiles == 1 ? entry : entry / p.row_tiles;
+        rt = entry - b * p.row_tiles;
+    }
+    __device__ int tiles(int entry) const {
+        int b, rt;
+        split(entry, b, rt);
+        const int T = tokens(b);
+        if (p.row_tiles == 1) return (T + kP8Tokens - 1) / kP8Tokens;
+        const int last = min(p.R, (rt + 1) * RP) - 1;
+        const int lim = T - p.sq + last / p.heads_per_group;
+        return lim < 0 ? 0 : lim / kP8Tokens + 1;
+    }
+};
 
 // A CTA's share as a run of segments of units.
 struct P8Segment {
@@ -176,18 +182,18 @@ template <int RP>
 struct P8Walk {
     long long left;
     int entry, g, off;
-    __device__ bool next(const PagedFp8Params& p, P8Segment& s) {
+    __device__ bool next(const P8Lens<RP>& lens, P8Segment& s) {
         if (left <= 0) return false;
-        int n = p8_tiles<RP>(p, entry);
-        while (n == 0) n = p8_tiles<RP>(p, ++entry);
+        int n = lens.tiles(entry);
+        while (n == 0) n = lens.tiles(++entry);
         s.entry = entry;
         s.g = g;
         s.i0 = off;
-        s.i1 = (int)min((long long)n, off + left);
+        s.i1 = left < n - off ? off + (int)left : n;
         s.n = n;
         left -= s.i1 - s.i0;
         off = 0;
-        if (++g == p.G) {
+        if (++g == lens.p.G) {
             g = 0;
             ++entry;
         }
@@ -201,16 +207,30 @@ struct P8Plan {
     int ctas;                      // CTAs that share the tiles
 };
 
+// a * b / c for 64-bit a, in 32 bits where they do.
+__device__ __forceinline__ long long muldiv(long long a, int b, int c) {
+    const unsigned long long x = (unsigned long long)a * (unsigned)b;
+    return x >> 32 ? (long long)(x / (unsigned)c) : (long long)((unsigned)x / (unsigned)c);
+}
+
 // All threads: sums the tiles of all entries, each thread over a contiguous
-// range of them, and finds where this CTA's share begins.
+// range of them, and finds where this CTA's share begins. The caller
+// synchronises the CTA before anyone reads the plan.
 template <int RP>
-__device__ void p8_make_plan(const PagedFp8Params& p, P8Plan* plan, long long* warp_sum) {
+__device__ void p8_make_plan(const P8Lens<RP>& lens, int* len_copy, P8Plan* plan, long long* warp_sum) {
+    const PagedFp8Params& p = lens.p;
     const int entries = p.B * p.row_tiles;
     const int per = (entries + kP8Threads - 1) / kP8Threads;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int e0 = min((long long)entries, (long long)threadIdx.x * per), e1 = min(entries, e0 + per);
+    if (p.B <= kP8Threads && p.row_tiles > 1) {
+        if ((int)threadIdx.x < p.B) len_copy[threadIdx.x] = lens.global(threadIdx.x);
+        __syncthreads();
+    } else if ((int)threadIdx.x < p.B && p.B <= kP8Threads) {
+        len_copy[threadIdx.x] = lens.global(threadIdx.x);    // read back below by this thread only
+    }
+    const int e0 = (int)min((long long)entries, (long long)threadIdx.x * per), e1 = min(entries, e0 + per);
     long long mine = 0;
-    for (int e = e0; e < e1; ++e) mine += p8_tiles<RP>(p, e);
+    for (int e = e0; e < e1; ++e) mine += lens.tiles(e);
     mine *= p.G;
     long long x = mine;
 #pragma unroll
@@ -221,35 +241,35 @@ __device__ void p8_make_plan(const PagedFp8Params& p, P8Plan* plan, long long* w
     if (lane == 31) warp_sum[warp] = x;
     __syncthreads();
     long long before = x - mine, total = 0;
+#pragma unroll
     for (int w = 0; w < kP8Threads / 32; ++w) {
         if (w < warp) before += warp_sum[w];
         total += warp_sum[w];
     }
-    const long long most = total / p.min_tiles;
-    const int ctas = (int)max(1ll, min((long long)gridDim.x, most));
+    const long long most = total / kP8MinTiles;
+    const int ctas = most < 1 ? 1 : most < (long long)gridDim.x ? (int)most : (int)gridDim.x;
     const int c = blockIdx.x;
-    const long long t0 = c < ctas ? total * c / ctas : total;
-    const long long t1 = c < ctas ? total * (c + 1) / ctas : total;
-    if (threadIdx.x == 0) {
+    const long long t0 = c < ctas ? muldiv(total, c, ctas) : total;
+    const long long t1 = c < ctas ? muldiv(total, c + 1, ctas) : total;
+    if (t0 < t1 ? t0 >= before && t0 < before + mine : threadIdx.x == 0) {
         plan->total = total;
         plan->begin = t0;
         plan->end = t1;
         plan->ctas = ctas;
         plan->entry = plan->g = plan->off = 0;
-    }
-    __syncthreads();
-    if (t0 < t1 && t0 >= before && t0 < before + mine) {
-        long long at = before;
-        int e = e0, n = p8_tiles<RP>(p, e);
-        while (at + (long long)n * p.G <= t0) {
-            at += (long long)n * p.G;
-            n = p8_tiles<RP>(p, ++e);
+        if (t0 < t1) {
+            long long at = before;
+            int e = e0, n = lens.tiles(e);
+            while (at + (long long)n * p.G <= t0) {
+                at += (long long)n * p.G;
+                n = lens.tiles(++e);
+            }
+            const unsigned in = (unsigned)min(t0 - at, 0xffffffffll);   // below n * G
+            plan->entry = e;
+            plan->g = t0 - at > 0xffffffffll ? (int)((t0 - at) / n) : (int)(in / (unsigned)n);
+            plan->off = (int)(t0 - at - (long long)plan->g * n);
         }
-        plan->entry = e;
-        plan->g = (int)((t0 - at) / n);
-        plan->off = (int)((t0 - at) % n);
     }
-    __syncthreads();
 }
 
 // Sums v[r] of the warp's lanes; lane i returns row i % RP. v is overwritten.
@@ -283,6 +303,23 @@ __device__ __forceinline__ int p8_out_row(const PagedFp8Params& p, int b, int rt
 
 // ------------------------------------------------------------------- kernel
 
+// A group's 128 threads meet (and agree whether any of them votes). These are
+// the CTA's named barriers 1 and 2: no thread of a group ever leaves its loop
+// early, whatever a bounded wait reported, so the four warps always arrive.
+__device__ __forceinline__ void group_sync(int x) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(x + 1) : "memory"); }
+__device__ __forceinline__ bool group_any(int x, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(x + 1)
+        : "memory");
+    return r != 0;
+}
+
 template <int D, int RP>
 __global__ void __launch_bounds__(kP8Threads, 1)
     gqa_paged_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -297,8 +334,10 @@ __global__ void __launch_bounds__(kP8Threads, 1)
     unsigned char* gen = smem_raw + (p_s + 2 * PS::kPBytes - raw);
     float* stage_o = reinterpret_cast<float*>(gen);                       // [RP][D], then m[RP], l[RP]
     gen += 4 * PS::kStageFloats;
-    // Row of the unit in q buffer i: {scale2 * 2^-e, last visible key, output row}.
-    int4* row_info = reinterpret_cast<int4*>(gen);                        // [2][RP]
+    // Rows of the unit in q buffer i: scale2 * 2^-e, last visible key, output row.
+    float* row_scale = reinterpret_cast<float*>(gen);                     // [2][RP]
+    int* row_lim = reinterpret_cast<int*>(row_scale + 2 * RP);            // [2][RP]
+    int* row_out = row_lim + 2 * RP;                                      // [2][RP]
     gen += PS::kRowInfoBytes;
     float4* sums = reinterpret_cast<float4*>(gen);                        // [2][RP], one component a warp
     gen += PS::kSumBytes;
@@ -306,103 +345,112 @@ __global__ void __launch_bounds__(kP8Threads, 1)
     gen += PS::kRefBytes;
     int* warp_max = reinterpret_cast<int*>(gen);                          // [2][4][RP + 1]
     gen += PS::kWarpMaxBytes;
+    int* len_copy = reinterpret_cast<int*>(gen);
+    gen += PS::kLenBytes;
     P8Plan* plan = reinterpret_cast<P8Plan*>(gen);                        // 40 bytes
-    int* vote = reinterpret_cast<int*>(gen + 64);                         // [2][2]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gen + 80);
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(gen + 84);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gen + 64);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(gen + 68);
+    long long* warp_sum = reinterpret_cast<long long*>(gen + 80);         // [12]
     gen += PS::kMiscBytes;
     const uint32_t bar0 = smem_addr(gen);
-    const uint32_t k_full = bar0, k_empty = k_full + 8 * S, v_full = k_empty + 8 * S, v_empty = v_full + 8 * S;
-    const uint32_t q_full = v_empty + 8 * S, q_empty = q_full + 16;
-    const uint32_t s_full = q_empty + 16, p_full = s_full + 16, o_done = p_full + 16, grp = o_done + 16;
-    const uint32_t m_full = grp + 16, m_empty = m_full + 8, fin = m_empty + 8;
+    const uint32_t k_full = bar0, v_full = k_full + 8 * S, empty = v_full + 8 * S;
+    const uint32_t q_full = empty + 8 * S, q_empty = q_full + 16;
+    const uint32_t s_full = q_empty + 16, s_free = s_full + 16, p_full = s_free + 16;
+    const uint32_t m_full = p_full + 16, m_empty = m_full + 8, fin = m_empty + 8;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t tmo = p.wait_timeout_ns;
+    const P8Lens<RP> lens = {p, len_copy};
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(k_full + 8 * s, 1);
-            mbar_init(k_empty + 8 * s, 1);
             mbar_init(v_full + 8 * s, 1);
-            mbar_init(v_empty + 8 * s, 1);
+            mbar_init(empty + 8 * s, 1);       // the stage's last reader, P V, is done
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(q_full + 8 * x, 1);
             mbar_init(q_empty + 8 * x, 9);     // eight softmax warps and the products
             mbar_init(s_full + 8 * x, 1);
+            mbar_init(s_free + 8 * x, 4);
             mbar_init(p_full + 8 * x, 4);
-            mbar_init(o_done + 8 * x, 1);
-            mbar_init(grp + 8 * x, 4);
+            mbar_init(fin + 8 * x, 1);
         }
         mbar_init(m_full, 4);
         mbar_init(m_empty, 4);
-        mbar_init(fin, 1);
         *abort_flag = 0;
-        vote[0] = vote[1] = vote[2] = vote[3] = 0;
         fence_barrier_init();
     }
-    if (warp == 10) {
+    if (warp == 9) {
         tmem_alloc(smem_addr(tmem_slot), PS::kTmemCols);
         tmem_relinquish();
     }
-    if (warp == 8 && lane == 0) tma_prefetch_desc(&tm_k);
-    if (warp == 9 && lane == 0) tma_prefetch_desc(&tm_v);
+    if (warp == 8 && lane < 2) tma_prefetch_desc(lane ? &tm_v : &tm_k);
+    tc_fence_before();
     pdl_launch_dependents();
     pdl_wait_primary();
-    p8_make_plan<RP>(p, plan, reinterpret_cast<long long*>(stage_o));   // synchronises the CTA
-    tc_fence_before();
+    p8_make_plan<RP>(lens, len_copy, plan, warp_sum);
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     P8Walk<RP> walk = {plan->end - plan->begin, plan->entry, plan->g, plan->off};
     P8Segment seg;
+    // Bounded waits of one thread, and of a softmax warp: all its lanes poll,
+    // and all go on when the limit runs out.
+    auto wait = [&](uint32_t bar, uint32_t n) { return wait_phase(bar, n & 1, abort_flag, p.status, tmo); };
+    auto all_wait = [&](uint32_t bar, uint32_t n) {
+        if (!mbar_try_wait(bar, n & 1) && !*abort_flag) wait_phase(bar, n & 1, abort_flag, p.status, tmo);
+        __syncwarp();
+    };
 
-    if (warp == 8 || warp == 9) {
-        // -------------------------------------------------- K and V loaders
-        const bool is_v = warp == 9;
+    if (warp == 8) {
+        // ------------------------------------- loader: lanes 0-7 K, lanes 8-15 V
+        const bool is_v = lane >= 8;
+        const int box_of = lane & 7;
         const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
-        const uint32_t full = is_v ? v_full : k_full, empty = is_v ? v_empty : k_empty;
+        const uint32_t full = is_v ? v_full : k_full;
         const uint32_t ring = is_v ? v_s : k_s;
         const int page_size = 1 << p.page_shift;
         const int box = min(page_size, kP8Tokens);
         const int boxes = kP8Tokens / box;
         const uint64_t pol = l2_policy_evict_first();
-        int it = 0, issued = 0;
+        int it = 0, issued = 0, s = 0;
+        uint32_t ph = 1;
         bool ok = true;
-        while (ok && walk.next(p, seg)) {
-            const int b = seg.entry / p.row_tiles;
-            const int T = p8_len(p, b);
+        while (ok && walk.next(lens, seg)) {
+            int b, rt;
+            lens.split(seg.entry, b, rt);
+            const int T = lens.tokens(b);
             const int32_t* row = p.table + (size_t)b * p.max_pages;
             // This lane's page of a tile; looked up one tile ahead.
             auto lookup = [&](int i) {
-                const int pos = i * kP8Tokens + lane * box;
-                return lane < boxes && i < seg.i1 && pos < T ? row[pos >> p.page_shift] : -1;
+                const int pos = i * kP8Tokens + box_of * box;
+                return lane < 16 && box_of < boxes && i < seg.i1 && pos < T ? row[pos >> p.page_shift] : -1;
             };
             int page = lookup(seg.i0);
             for (int i = seg.i0; i < seg.i1; ++i, ++it) {
-                const int s = it % S;
                 const int cur = page;
                 page = lookup(i + 1);
-                const int pos = i * kP8Tokens + lane * box;
+                const int pos = i * kP8Tokens + box_of * box;
                 const int here = min(boxes, (T - i * kP8Tokens + box - 1) / box);   // boxes that hold keys
-                ok = warp_wait(empty + 8 * s, ((it / S) & 1) ^ 1, abort_flag, p.status, tmo);
+                ok = warp_wait(empty + 8 * s, ph, abort_flag, p.status, tmo);
                 if (!ok) break;
-                if (!is_v && blockIdx.x == 0 && it == p.skip_tile) continue;   // injected fault: never loaded
-                if (lane == 0) mbar_arrive_expect_tx(full + 8 * s, here * box * D);
+                const bool skip = blockIdx.x == 0 && it == p.skip_tile && !is_v;    // injected fault: never loaded
+                if ((lane & 7) == 0 && lane < 16 && !skip) mbar_arrive_expect_tx(full + 8 * s, here * box * D);
                 __syncwarp();
-                if (lane < here) {
+                if (lane < 16 && box_of < here && !skip) {
                     // A page outside the pool is a slab out of range: zeros.
                     const int z = (unsigned)cur < (unsigned)p.num_pages ? cur * p.G + seg.g : -1;
-                    tma_load_3d_hint(ring + s * TB + lane * box * D, tm, full + 8 * s, 0, pos & (page_size - 1), z,
+                    tma_load_3d_hint(ring + s * TB + box_of * box * D, tm, full + 8 * s, 0, pos & (page_size - 1), z,
                                      pol);
                 }
                 __syncwarp();
                 issued = it + 1;
+                if (++s == S) s = 0, ph ^= 1;
             }
         }
         // Leave only once the last copies have landed.
-        if (lane == 0)
+        if (lane == 0 || lane == 8)
             for (int j = issued > S ? issued - S : 0; j < issued; ++j) {
                 if (!is_v && blockIdx.x == 0 && j == p.skip_tile) continue;
                 const uint64_t t0 = global_timer_ns();
@@ -410,81 +458,73 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                     if (global_timer_ns() - t0 > tmo) break;
             }
         __syncwarp();
-    } else if (warp == 10) {
-        // ------------------------------------------------------- products
-        constexpr uint64_t kLayout = D == 128 ? 2 : 4;
-        constexpr uint32_t kAtom = 8 * D;                                   // 8 rows of K, V or Q
-        constexpr uint32_t kIdescS = p8_idesc(kP8Tokens, PS::kNs, false, false);
-        constexpr uint32_t kIdescO = p8_idesc(D, PS::kNp, true, true);
-        bool ok = true, issued = false;
-        // S runs one tile ahead of O, across segments.
-        P8Walk<RP> ahead = walk;
-        P8Segment aseg;
-        bool have = ahead.next(p, aseg);
-        int ai = have ? aseg.i0 : 0, ait = 0, asg = 0;
-        auto issue_s = [&]() {
-            if (!have) return true;
-            if (ai == aseg.i0 && !warp_wait(q_full + 8 * (asg & 1), (asg >> 1) & 1, abort_flag, p.status, tmo))
-                return false;
-            const int s = ait % S, x = ait & 1;
-            if (!warp_wait(k_full + 8 * s, (ait / S) & 1, abort_flag, p.status, tmo)) return false;
-            const bool last = ai + 1 == aseg.i1;
-            if (lane == 0) {
-                tc_fence_after();
-                const uint32_t kt = k_s + s * TB, qt = q_s + (asg & 1) * PS::kQBytes;
+    } else if (warp == 9 || warp == 10) {
+        // ----------------- products: S from one thread, O from another, so that
+        // neither waits behind the other's operands
+        if (lane == 0) {
+            constexpr uint64_t kLayout = D == 128 ? 2 : 4;
+            constexpr uint32_t kAtom = 8 * D;                               // 8 rows of K, V or Q
+            bool ok = true, any = false;
+            int s = 0, x = 0;
+            uint32_t ph = 0, np[2] = {0, 0};
+            if (warp == 9) {
+                constexpr uint32_t kIdesc = p8_idesc(kP8Tokens, PS::kNs, false, false);
+                const uint64_t k_desc = p8_desc(k_s, 16, kAtom, kLayout), q_desc = p8_desc(q_s, 16, kAtom, kLayout);
+                int sg = 0;
+                while (ok && walk.next(lens, seg)) {
+                    ok = wait(q_full + 8 * (sg & 1), sg >> 1);
+                    const uint64_t qd = q_desc + (sg & 1) * (PS::kQBytes >> 4);
+                    for (int i = seg.i0; ok && i < seg.i1; ++i) {
+                        // S_x of two tiles ago has been read.
+                        ok = wait(s_free + 8 * x, (x ? np[1] : np[0]) + 1) && wait(k_full + 8 * s, ph);
+                        if (!ok) break;
+                        if (x) ++np[1]; else ++np[0];
+                        tc_fence_after();
+                        const uint64_t kd = k_desc + s * (TB >> 4);
 #pragma unroll
-                for (int kk = 0; kk < D / 32; ++kk)
-                    umma_f8(tmem + PS::kColS + x * PS::kNs, p8_desc(kt + kk * 32, 16, kAtom, kLayout),
-                            p8_desc(qt + kk * 32, 16, kAtom, kLayout), kIdescS, kk > 0 ? 1u : 0u);
-                umma_commit(s_full + 8 * x);
-                umma_commit(k_empty + 8 * s);
-                if (last) umma_commit(q_empty + 8 * (asg & 1));
-            }
-            __syncwarp();
-            issued = true;
-            ++ait;
-            if (last) {
-                have = ahead.next(p, aseg);
-                ai = aseg.i0;
-                ++asg;
+                        for (int kk = 0; kk < D / 32; ++kk)
+                            umma_f8(tmem + PS::kColS + x * PS::kNs, kd + kk * 2, qd + kk * 2, kIdesc, kk > 0 ? 1u : 0u);
+                        umma_commit(s_full + 8 * x);
+                        any = true;
+                        x ^= 1;
+                        if (++s == S) s = 0, ph ^= 1;
+                    }
+                    if (ok) umma_commit(q_empty + 8 * (sg & 1));
+                    ++sg;
+                }
             } else {
-                ++ai;
-            }
-            return true;
-        };
-        ok = issue_s();
-        int it = 0;
-        uint32_t np[2] = {0, 0};
-        while (ok && walk.next(p, seg)) {
-            bool first[2] = {true, true};
-            for (int i = seg.i0; i < seg.i1; ++i, ++it) {
-                const int s = it % S, x = it & 1;
-                ok = issue_s() && warp_wait(v_full + 8 * s, (it / S) & 1, abort_flag, p.status, tmo) &&
-                     warp_wait(p_full + 8 * x, (x ? np[1] : np[0]) & 1, abort_flag, p.status, tmo);
-                if (!ok) break;
-                const bool fresh = x ? first[1] : first[0];
-                if (x) ++np[1], first[1] = false; else ++np[0], first[0] = false;
-                if (lane == 0) {
-                    tc_fence_after();
-                    const uint32_t vt = v_s + s * TB, pt = p_s + x * PS::kPBytes;
+                constexpr uint32_t kIdesc = p8_idesc(D, PS::kNp, true, true);
+                const uint64_t v_desc = p8_desc(v_s, 16, kAtom, kLayout), p_desc = p8_desc(p_s, 128, 2048, 0);
+                while (ok && walk.next(lens, seg)) {
+                    bool first[2] = {true, true};
+                    for (int i = seg.i0; i < seg.i1; ++i) {
+                        ok = wait(v_full + 8 * s, ph) && wait(p_full + 8 * x, x ? np[1] : np[0]);
+                        if (!ok) break;
+                        const bool fresh = x ? first[1] : first[0];
+                        if (x) ++np[1], first[1] = false; else ++np[0], first[0] = false;
+                        tc_fence_after();
+                        const uint64_t vd = v_desc + s * (TB >> 4), pd = p_desc + x * (PS::kPBytes >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < kP8Tokens / 32; ++kk)
-                        umma_f8(tmem + PS::kColO + x * PS::kNp, p8_desc(vt + kk * 32 * D, 16, kAtom, kLayout),
-                                p8_desc(pt + kk * 512, 128, 2048, 0), kIdescO, (!fresh || kk > 0) ? 1u : 0u);
-                    umma_commit(o_done + 8 * x);
-                    umma_commit(v_empty + 8 * s);
+                        for (int kk = 0; kk < kP8Tokens / 32; ++kk)
+                            umma_f8(tmem + PS::kColO + x * PS::kNp, vd + kk * (2 * D), pd + kk * 32, kIdesc,
+                                    (!fresh || kk > 0) ? 1u : 0u);
+                        umma_commit(empty + 8 * s);
+                        any = true;
+                        x ^= 1;
+                        if (++s == S) s = 0, ph ^= 1;
+                    }
                 }
-                __syncwarp();
             }
-        }
-        if (issued && lane == 0) {
-            umma_commit(fin);
-            const uint64_t t0 = global_timer_ns();
-            while (!mbar_try_wait(fin, 0))
-                if (global_timer_ns() - t0 > tmo) {
-                    atomicOr(p.status, kStatusTimeout);
-                    break;
-                }
+            if (any) {
+                const uint32_t bar = fin + 8 * (warp - 9);
+                umma_commit(bar);
+                const uint64_t t0 = global_timer_ns();
+                while (!mbar_try_wait(bar, 0))
+                    if (global_timer_ns() - t0 > tmo) {
+                        atomicOr(p.status, kStatusTimeout);
+                        break;
+                    }
+            }
         }
         __syncwarp();
     } else if (warp == 11) {
@@ -493,15 +533,16 @@ __global__ void __launch_bounds__(kP8Threads, 1)
         long long at = plan->begin;
         int sg = 0;
         bool ok = true;
-        while (ok && walk.next(p, seg)) {
+        while (ok && walk.next(lens, seg)) {
             if (seg.i0 == 0 && seg.i1 < seg.n)
                 split = {seg.entry, seg.g, (int)(((at + seg.n) * plan->ctas - 1) / plan->total), 0};
             at += seg.i1 - seg.i0;
             const int buf = sg & 1;
             ok = warp_wait(q_empty + 8 * buf, ((sg >> 1) & 1) ^ 1, abort_flag, p.status, tmo);
             if (!ok) break;
-            const int b = seg.entry / p.row_tiles, rt = seg.entry - b * p.row_tiles;
-            const int T = p8_len(p, b);
+            int b, rt;
+            lens.split(seg.entry, b, rt);
+            const int T = lens.tokens(b);
             const uint32_t qt = q_s + buf * PS::kQBytes;
             constexpr int kPer = D / 32;          // elements of a row per lane
 #pragma unroll
@@ -559,10 +600,10 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                             asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"((uint16_t)(t ? lo : hi)) : "memory");
                     }
                     if (lane == 0) {
-                        const float f = orow[i] < 0 ? 0.f : bad ? __int_as_float(0x7fffffff)
-                                                                : p.scale_log2 * (top == 0 ? 1.f : pow2i(-e));
-                        row_info[buf * RP + r] =
-                            make_int4(__float_as_int(f), orow[i] < 0 ? -1 : T - p.sq + tok[i], orow[i], 0);
+                        row_scale[buf * RP + r] = orow[i] < 0 ? 0.f : bad ? __int_as_float(0x7fffffff)
+                                                                        : p.scale_log2 * (top == 0 ? 1.f : pow2i(-e));
+                        row_lim[buf * RP + r] = orow[i] < 0 ? -1 : T - p.sq + tok[i];
+                        row_out[buf * RP + r] = orow[i];
                     }
                 }
             }
@@ -574,8 +615,9 @@ __global__ void __launch_bounds__(kP8Threads, 1)
         if (lane == 0) p.splits[blockIdx.x] = split;
         // Entries none of whose rows sees a key own no tile: out = 0, lse = -inf.
         for (int e = blockIdx.x; e < p.B * p.row_tiles; e += gridDim.x) {
-            if (p8_tiles<RP>(p, e) > 0) continue;
-            const int b = e / p.row_tiles, rt = e - b * p.row_tiles;
+            if (lens.tiles(e) > 0) continue;
+            int b, rt;
+            lens.split(e, b, rt);
             for (int x = 0; x < p.G * RP; ++x) {
                 int tok;
                 const int orow = p8_out_row<RP>(p, b, rt, x / RP, x % RP, &tok);
@@ -594,22 +636,19 @@ __global__ void __launch_bounds__(kP8Threads, 1)
         const uint32_t p_at = p_s + x * PS::kPBytes + tok * 16;
         float* const my_ref = neg_ref + x * RP;
         int* const my_max = warp_max + x * 4 * (RP + 1);
-        uint32_t n_grp = 0, n_tiles = 0, n_merge = 0;   // phases of grp, of s_full / o_done, of m_full
-        bool ok = true;
-        auto group_sync = [&]() {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(grp + 8 * x);
-            const bool r = warp_wait(grp + 8 * x, n_grp & 1, abort_flag, p.status, tmo);
-            ++n_grp;
-            return r;
-        };
-        int it0 = 0, sg = 0;     // the CTA's tile number at the segment's start
-        while (ok && walk.next(p, seg)) {
-            const int b = seg.entry / p.row_tiles, rt = seg.entry - b * p.row_tiles;
-            const int T = p8_len(p, b);
+        uint32_t n_tiles = 0, n_merge = 0;       // phases of s_full and p_full, of m_full
+        int it0 = 0, sg = 0;                     // the CTA's tile number at the segment's start
+        // The product of this group's tile `it` has completed.
+        auto wait_product = [&](int it) { all_wait(empty + 8 * (it % S), it / S); };
+        while (walk.next(lens, seg)) {
+            int b, rt;
+            lens.split(seg.entry, b, rt);
+            const int T = lens.tokens(b);
             const int32_t* table = p.table + (size_t)b * p.max_pages;
-            const int4* info = row_info + (sg & 1) * RP;
-            const int lim_min = T - p.sq + (rt * RP) / p.heads_per_group;   // every row sees keys up to here
+            const float4* scale4 = reinterpret_cast<const float4*>(row_scale + (sg & 1) * RP);
+            const int* lim = row_lim + (sg & 1) * RP;
+            const int lim_min =                                             // every row sees keys up to here
+                p.row_tiles == 1 ? T - p.sq : T - p.sq + (rt * RP) / p.heads_per_group;
             const int first_i = seg.i0 + ((it0 & 1) != x ? 1 : 0);          // this group's first tile
             auto page_of = [&](int i) {
                 const int pos = i * kP8Tokens + tok;
@@ -634,8 +673,7 @@ __global__ void __launch_bounds__(kP8Threads, 1)
             int page_next = page_of(first_i + 2);
             bool first = true;
             // Also keeps a group without a tile here from running ahead.
-            ok = warp_wait(q_full + 8 * (sg & 1), (sg >> 1) & 1, abort_flag, p.status, tmo);
-            if (!ok) break;
+            all_wait(q_full + 8 * (sg & 1), sg >> 1);
             for (int i = first_i; i < seg.i1; i += 2) {
                 const int it = it0 + i - seg.i0;
                 const int pos = i * kP8Tokens + tok;
@@ -645,10 +683,10 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                 page_next = page_of(i + 4);
                 const bool edge = (i + 1) * kP8Tokens - 1 > lim_min;        // some row does not see all of it
 
-                ok = warp_wait(s_full + 8 * x, n_tiles & 1, abort_flag, p.status, tmo);
-                if (!ok) break;
+                all_wait(s_full + 8 * x, n_tiles);
                 tc_fence_after();
                 float xs[RP];
+                bool moves = first;
                 {
                     uint32_t h[RP], lo[RP];
                     if constexpr (RP == 8) {
@@ -663,22 +701,27 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                         tmem_ld32(s_tm, h);
                         tmem_ld32(s_tm + 32, lo);
                     }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s_free + 8 * x);
                     float top = -INFINITY;
 #pragma unroll
-                    for (int r = 0; r < RP; ++r) {
-                        const float f = __int_as_float(info[r].x) * ks;
-                        xs[r] = fmaf(__uint_as_float(lo[r]), 0.0625f, __uint_as_float(h[r])) * f;
-                        if (edge && pos > info[r].y) xs[r] = -INFINITY;
-                        if (!first) top = fmaxf(top, xs[r] + my_ref[r]);
+                    for (int r = 0; r < RP; r += 4) {
+                        const float4 f = scale4[r / 4];
+                        const float4 m = *reinterpret_cast<const float4*>(my_ref + r);
+                        const float fs[4] = {f.x, f.y, f.z, f.w}, ms[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            xs[r + k] = fmaf(__uint_as_float(lo[r + k]), 0.0625f, __uint_as_float(h[r + k])) * (fs[k] * ks);
+                            if (edge && pos > lim[r + k]) xs[r + k] = -INFINITY;
+                            top = fmaxf(top, xs[r + k] + ms[k]);
+                        }
                     }
                     // A NaN or infinite scale makes its block's values NaN.
                     if (!(fabsf(vs) <= 3.402823466e38f)) vs = __int_as_float(0x7fffffff);
-                    const bool moves = first || top > kP8Slack || fabsf(vs) * pow2i(-ev) > kP8ScaleSlack;
-                    if (__any_sync(0xffffffffu, moves) && lane == 0) vote[2 * x + (n_tiles & 1)] = it + 1;
+                    moves |= top > kP8Slack || fabsf(vs) * pow2i(-ev) > kP8ScaleSlack;
                 }
-                ok = group_sync();
-                if (!ok) break;
-                if (reinterpret_cast<volatile int*>(vote)[2 * x + (n_tiles & 1)] == it + 1) {
+                if (group_any(x, moves)) {
                     // Move the references: rows whose tile maximum is out of range.
                     int mine = 0;
 #pragma unroll
@@ -691,8 +734,7 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                     if (lane < RP) my_max[w4 * (RP + 1) + lane] = mine;
                     if (lane == 0) my_max[w4 * (RP + 1) + RP] = (int)vtop;
                     const float m_old = first || lane >= RP ? kP8Unseen : -my_ref[lane];
-                    ok = group_sync();
-                    if (!ok) break;
+                    group_sync(x);
                     float m_new = m_old;
                     if (lane < RP) {
                         const float m = unordered(max(max(my_max[lane], my_max[RP + 1 + lane]),
@@ -710,24 +752,21 @@ __global__ void __launch_bounds__(kP8Threads, 1)
 #pragma unroll
                     for (int r = 0; r < RP; ++r) l[r] *= __shfl_sync(0xffffffffu, alpha, r);
                     if (!first) {
-                        // Every product of this group so far has completed.
-                        ok = warp_wait(o_done + 8 * x, (n_tiles - 1) & 1, abort_flag, p.status, tmo);
-                        if (!ok) break;
+                        wait_product(it - 2);     // and so every product of this group so far
                         tc_fence_after();
 #pragma unroll
-                        for (int c = 0; c < 3 * RP / 8; ++c) {
-                            uint32_t o[8];
-                            tmem_ld8(o_tm + 8 * c, o);
+                        for (int c = 0; c < PS::kNp / 16; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(o_tm + 16 * c, o);
 #pragma unroll
-                            for (int k = 0; k < 8; ++k)
+                            for (int k = 0; k < 16; ++k)
                                 o[k] = __float_as_uint(__uint_as_float(o[k]) *
-                                                       __shfl_sync(0xffffffffu, alpha_o, (8 * c + k) % RP));
-                            tmem_st8(o_tm + 8 * c, o);
+                                                       __shfl_sync(0xffffffffu, alpha_o, (16 * c + k) % RP));
+                            tmem_st16(o_tm + 16 * c, o);
                         }
                         tmem_st_wait();
                     }
-                    ok = group_sync();
-                    if (!ok) break;
+                    group_sync(x);
                 }
                 if (edge) {
                     // Rows of V past the length may hold anything: zero them. A
@@ -735,8 +774,7 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                     // others as 0 * NaN: its row is zeroed too, and the rows that
                     // see it are made NaN through P.
                     const int s = it % S;
-                    ok = warp_wait(v_full + 8 * s, (it / S) & 1, abort_flag, p.status, tmo);
-                    if (!ok) break;
+                    all_wait(v_full + 8 * s, it / S);
                     if (pos > lim_min) {
                         const uint32_t at = v_s + s * TB + tok * D;
                         bool clear = pos >= T;
@@ -760,49 +798,45 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                             for (int c = 0; c < D / 16; ++c) st_shared_zero16(at + 16 * c);
                     }
                 }
-                // P's operand is free once the group's previous product is done.
-                if (n_tiles > 0) ok = warp_wait(o_done + 8 * x, (n_tiles - 1) & 1, abort_flag, p.status, tmo);
-                if (!ok) break;
                 const float vw = vs * pow2i(-ev) * kP8ProbScale;
-                uint32_t packed[RP / 4][3];       // four rows: hi, mid, lo
+                uint32_t packed[RP / 4][kP8Terms];       // four rows: hi, mid, lo, last
 #pragma unroll
-                for (int r = 0; r < RP; r += 2) {
-                    float w[2];
+                for (int r = 0; r < RP; r += 4) {
+                    const float4 m = *reinterpret_cast<const float4*>(my_ref + r);
+                    const float ms[4] = {m.x, m.y, m.z, m.w};
+                    float w[4];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float pr = fast_exp2(xs[r + k] + my_ref[r + k]);
+                    for (int k = 0; k < 4; ++k) {
+                        const float pr = fast_exp2(xs[r + k] + ms[k]);
                         l[r + k] += pr;
                         w[k] = pr * vw;
-                        if (edge && pos > info[r + k].y) w[k] = 0.f;
+                        if (edge && pos > lim[r + k]) w[k] = 0.f;
                     }
-                    const uint32_t f = pack_f16x2(w[0], w[1]);
-                    const uint32_t hi = f16x2_to_e4m3x2(f);
-                    const uint32_t f1 = residual16(f, e4m3x2_to_f16x2((uint16_t)hi));
-                    const uint32_t mid = f16x2_to_e4m3x2(f1);
-                    const uint32_t f2 = residual16(f1, e4m3x2_to_f16x2((uint16_t)mid));
-                    const uint32_t lo = f16x2_to_e4m3x2(f2);
-                    if ((r & 2) == 0) {
-                        packed[r / 4][0] = hi;
-                        packed[r / 4][1] = mid;
-                        packed[r / 4][2] = lo;
-                    } else {
-                        packed[r / 4][0] |= hi << 16;
-                        packed[r / 4][1] |= mid << 16;
-                        packed[r / 4][2] |= lo << 16;
+                    uint32_t f0 = pack_f16x2(w[0], w[1]), f1 = pack_f16x2(w[2], w[3]);
+#pragma unroll
+                    for (int t = 0; t < kP8Terms; ++t) {
+                        const uint32_t c0 = f16x2_to_e4m3x2(f0), c1 = f16x2_to_e4m3x2(f1);
+                        packed[r / 4][t] = c0 | (c1 << 16);
+                        if (t + 1 < kP8Terms) {
+                            f0 = residual16(f0, e4m3x2_to_f16x2((uint16_t)c0));
+                            f1 = residual16(f1, e4m3x2_to_f16x2((uint16_t)c1));
+                        }
                     }
                 }
+                // P's operand is free once the group's previous product is done.
+                if (it >= 2) wait_product(it - 2);
                 // Column term * RP + r; 16 columns of a token are 16 bytes.
-                if constexpr (RP == 8) {
-                    st_shared_v4(p_at, make_uint4(packed[0][0], packed[1][0], packed[0][1], packed[1][1]));
-                    st_shared_v4(p_at + 2048, make_uint4(packed[0][2], packed[1][2], 0u, 0u));
-                } else {
 #pragma unroll
-                    for (int t = 0; t < 3; ++t)
-#pragma unroll
-                        for (int c = 0; c < RP / 16; ++c)
-                            st_shared_v4(p_at + (t * (RP / 16) + c) * 2048,
-                                         make_uint4(packed[4 * c][t], packed[4 * c + 1][t], packed[4 * c + 2][t],
-                                                    packed[4 * c + 3][t]));
+                for (int c = 0; c < PS::kNp / 16; ++c) {
+                    uint4 v;
+                    if constexpr (RP == 8)
+                        v = make_uint4(packed[0][2 * c], packed[1][2 * c], packed[0][2 * c + 1], packed[1][2 * c + 1]);
+                    else {
+                        constexpr int kHalf = RP / 16;
+                        const int t = c / kHalf, q = (c % kHalf) * 4;
+                        v = make_uint4(packed[q][t], packed[q + 1][t], packed[q + 2][t], packed[q + 3][t]);
+                    }
+                    st_shared_v4(p_at + c * 2048, v);
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -813,29 +847,32 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                 ks = ks_next;
                 vs = vs_next;
             }
-            if (!ok) break;
 
             // ------------------------------------------------ end of a segment
             const int len = seg.i1 - seg.i0;
             const int cnt0 = (len + ((it0 & 1) == 0 ? 1 : 0)) / 2, cnt1 = len - cnt0;
-            const int cnt = x ? cnt1 : cnt0;
             const bool both = cnt0 > 0 && cnt1 > 0;
-            if (cnt > 0) {
+            if ((x ? cnt1 : cnt0) > 0) {
                 const float sum = reduce_rows<RP>(l, lane);
                 if (lane < RP) reinterpret_cast<float*>(sums + x * RP + lane)[w4] = sum;
-                ok = group_sync() && warp_wait(o_done + 8 * x, (n_tiles - 1) & 1, abort_flag, p.status, tmo);
-                if (!ok) break;
+                group_sync(x);
+                // This group's last tile is the segment's last or the one before.
+                const int last = it0 + len - 1;
+                wait_product((last & 1) == x ? last : last - 1);
                 tc_fence_after();
                 float o[RP];
 #pragma unroll
                 for (int r = 0; r < RP; ++r) o[r] = 0.f;
 #pragma unroll
-                for (int c = 0; c < 3 * RP / 8; ++c) {
-                    uint32_t t[8];
-                    tmem_ld8(o_tm + 8 * c, t);
-                    const float f = 8 * c < RP ? 1.f : 8 * c < 2 * RP ? 0.0625f : 0.00390625f;
+                for (int c = 0; c < PS::kNp / 16; ++c) {
+                    uint32_t t[16];
+                    tmem_ld16(o_tm + 16 * c, t);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) o[(8 * c + k) % RP] = fmaf(__uint_as_float(t[k]), f, o[(8 * c + k) % RP]);
+                    for (int k = 0; k < 16; ++k) {
+                        const int n = 16 * c + k;
+                        const float f = n < RP ? 1.f : n < 2 * RP ? 0x1p-4f : n < 3 * RP ? 0x1p-8f : 0x1p-12f;
+                        o[n % RP] = fmaf(__uint_as_float(t[k]), f, o[n % RP]);
+                    }
                 }
                 tc_fence_before();
                 // D = 64 products keep 16 of their rows in each warp's 32 lanes.
@@ -843,8 +880,7 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                 const int dim = D == 128 ? tok : w4 * 16 + lane;
                 const float unit = pow2i(ev) * (1.f / kP8ProbScale);
                 if (both && x == 1) {
-                    ok = warp_wait(m_empty, (n_merge & 1) ^ 1, abort_flag, p.status, tmo);
-                    if (!ok) break;
+                    all_wait(m_empty, n_merge + 1);
 #pragma unroll
                     for (int r = 0; r < RP; ++r)
                         if (mine) stage_o[r * D + dim] = o[r] * unit;
@@ -857,10 +893,7 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                     if (lane == 0) mbar_arrive(m_full);
                     ++n_merge;
                 } else {
-                    if (both) {
-                        ok = warp_wait(m_full, n_merge & 1, abort_flag, p.status, tmo);
-                        if (!ok) break;
-                    }
+                    if (both) all_wait(m_full, n_merge);
                     const bool whole = seg.i0 == 0 && seg.i1 == seg.n;
                     float* slot = p.part + ((size_t)blockIdx.x * 2 + (seg.i0 == 0 ? 1 : 0)) * p8_slot_floats(RP, D);
 #pragma unroll
@@ -875,13 +908,13 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                             ls = ls * a0 + l1 * a1;
                             y = y * a0 + (mine ? stage_o[r * D + dim] : 0.f) * a1;
                         }
-                        const int orow = info[r].z;
+                        const int orow = row_out[(sg & 1) * RP + r];
                         if (orow < 0) continue;
                         if (whole) {
                             const bool some = ls > 0.f || ls != ls;
                             if (mine)
                                 p.out[(size_t)orow * D + dim] =
-                                    (uint16_t)(pack_bf16x2(some ? y / ls : 0.f, 0.f) & 0xffffu);
+                                    (uint16_t)(pack_bf16x2(some ? y * (1.f / ls) : 0.f, 0.f) & 0xffffu);
                             if (p.lse && tok == r)
                                 p.lse[orow] = some ? (m + log2f(ls)) * 0.6931471805599453f : -INFINITY;
                         } else {
@@ -899,8 +932,7 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                     }
                 }
                 // The sums and references are read before the next segment writes them.
-                ok = group_sync();
-                if (!ok) break;
+                group_sync(x);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(q_empty + 8 * (sg & 1));
@@ -911,7 +943,7 @@ __global__ void __launch_bounds__(kP8Threads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 10) tmem_dealloc(tmem, PS::kTmemCols);
+    if (warp == 9) tmem_dealloc(tmem, PS::kTmemCols);
 }
 
 // Merges the partial results of the units that cross CTAs: one warp per row of

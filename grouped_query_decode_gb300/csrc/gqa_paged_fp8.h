@@ -10,6 +10,7 @@
 namespace gqa {
 
 constexpr int kP8Tokens = 128;     // tokens per tile: one per thread of a softmax group, M of the products
+constexpr int kP8MinTiles = 2;     // fewest tiles worth a CTA
 constexpr int kP8MaxRows = 32;     // query rows of a unit; more are further units
 
 // One split unit: the CTA whose share starts it, recorded for the merge.
@@ -35,7 +36,6 @@ struct PagedFp8Params {
     float scale_log2;
     int B, sq, H, G, R, heads_per_group, row_tiles;
     int page_shift, num_pages, max_pages, blocks;
-    int min_tiles;             // fewest tiles worth a CTA
     int skip_tile;             // fault injection for tests (-1: off)
 };
 

@@ -23,15 +23,12 @@ int check_paged_fp8(int B, int sq, int H, int G, int D, int page_size, int max_p
     return GQA_OK;
 }
 
-// Fewest tiles worth a CTA of their own (a tile is 128 keys).
-constexpr int kMinTiles = 2;
-
 // CTAs of a call: one per SM, fewer if even full tables hold less work.
 int paged_fp8_grid(int B, int G, int R, int page_size, int max_pages, int sms) {
     const int rows = p8_rows(R);
     const long long units = (long long)B * G * ((R + rows - 1) / rows);
     const long long tiles = ((long long)max_pages * page_size + kP8Tokens - 1) / kP8Tokens;
-    const long long want = units * tiles / kMinTiles;
+    const long long want = units * tiles / kP8MinTiles;
     return (int)(want < 1 ? 1 : want < sms ? want : sms);
 }
 
@@ -111,7 +108,6 @@ int gqa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages
     p.num_pages = num_pages;
     p.max_pages = max_pages_per_seq;
     p.blocks = (page_size + 63) / 64;
-    p.min_tiles = kMinTiles;
     a.grid = grid;
     a.stream = stream;
     const cudaError_t e = D == 64 ? launch_paged_fp8_d64(a) : launch_paged_fp8_d128(a);
