@@ -4,17 +4,20 @@
 // A unit is (sequence, KV head, up to 32 query rows). Its keys are cut into
 // 128-token tiles; tokens sit on the products' M side, rows on the N side:
 //     S [128 tokens x 2 rows]  = K   [128 x D]   (smem, K-major)  x Q^T  (smem)
-//     O [D x 3 rows]          += V^T [D x 128]   (smem, MN-major) x P    (smem)
+//     O [D x 4 rows]          += V^T [D x 128]   (smem, MN-major) x P    (smem)
 // both kind::f8f6f4 with fp32 accumulators in tensor memory. Rows are few, so
-// each bf16 or fp32 number on the N side is spread over several e4m3 columns:
-//   q * 2^e = hi + lo / 16              (2^e brings the row's maximum to [128, 256))
-//   p * v_scale * 2^c = hi + mid / 16 + lo / 256, of the value rounded to fp16
-// e4m3 keeps 4 significant bits and each residual is an exact difference of at
-// most half a step, so hi + lo is every bf16 query down to 2^-13 of its row's
-// maximum (2^-21 of it absolutely below that), and hi + mid + lo the fp16
-// probability down to 2^-13 of the reference (2^-24 absolutely below). The
-// extra columns cost nothing: with N <= 96 the products are bound by reading
-// the K and V tiles from shared memory once each.
+// each bf16 or fp16 number on the N side is spread over several 8-bit columns:
+//   q * 2^e = hi + lo / 16, e4m3 (2^e brings the row's maximum to [128, 256)):
+//     4 significant bits each, the residual an exact difference, so every bf16
+//     query down to 2^-13 of its row's maximum, and 2^-21 of it below that;
+//   w = fp16(p * v_scale * 2^c) = t0 + t1 + t2 + t3, e5m2: a term is the upper
+//     byte of the fp16 residual (its first 3 significant bits), the next
+//     residual the exact difference, so 4 terms are all 11 bits of w down to
+//     2^-6, and w within 2^-16 below that, where w is 1024..2048 for p = 1. No
+//     conversion instruction is needed; an e4m3 split takes two per term and
+//     pair, and those, at a quarter of the rate, took half of a tile's time.
+// The extra columns cost nothing: up to N = 128 a product of M = 128 takes the
+// 64 cycles that reading its K or V rows takes.
 //
 // Softmax, one thread per token: x = s * scale2 * k_scale (base 2), p = 2^(x - m)
 // with a reference m per row that moves only when a score exceeds it by more
@@ -41,9 +44,9 @@
 namespace gqa {
 
 constexpr int kP8Threads = 384;
-constexpr int kP8Terms = 4;               // e4m3 columns per probability
+constexpr int kP8Terms = 4;               // e5m2 columns per probability
 constexpr float kP8Slack = 4.0f;          // p <= 2^4 before the reference moves
-constexpr float kP8ProbScale = 16.0f;     // p * v_scale * 2^-ev * 16 <= 16 * 1.75 * 16 = 448
+constexpr float kP8ProbScale = 2048.0f;   // p * v_scale * 2^-ev * 2048 <= 16 * 1.75 * 2048 = 57344
 constexpr float kP8ScaleSlack = 1.75f;
 constexpr float kP8Unseen = -3.402823466e38f;   // reference of a row that has seen no key
 
@@ -54,19 +57,23 @@ struct P8Shape {
     static constexpr int kNp = kP8Terms * RP;                     // columns of O
     static constexpr int kQBytes = kNs * D;
     static constexpr int kPBytes = kP8Tokens * kNp;
-    static constexpr int kStageFloats = RP * D + 2 * RP;          // one group's (O, m, l)
-    // The ring takes what the rest leaves of 227 KB.
-    static constexpr int kStages = (D == 128 ? 1 : 2) * (RP == 32 ? 4 : RP == 16 ? 5 : 6);
-    static constexpr int kBars = 3 * kStages + 14;
+    // The rings take what the rest leaves of 227 KB. A V tile is held from its
+    // copy to P V, a K tile only to S, so V gets more stages.
+    static constexpr int kStagesK = (D == 128 ? 1 : 2) * (RP == 32 ? 4 : 5);
+    static constexpr int kStagesV = (D == 128 ? 1 : 2) * (RP == 32 ? 5 : 7);
+    static constexpr int kBars = 2 * (kStagesK + kStagesV) + 15;
     static constexpr int kRowInfoBytes = 2 * 3 * RP * 4;
     static constexpr int kRefBytes = 2 * RP * 4;
     static constexpr int kWarpMaxBytes = 2 * 4 * (RP + 1) * 4;
     static constexpr int kSumBytes = 2 * RP * 16;
+    static constexpr int kMergeBytes = 3 * RP * 8;                // group 1's (m, l); each group's row factors
     static constexpr int kLenBytes = kP8Threads * 4;
     static constexpr int kMiscBytes = 192;
-    static constexpr int kSmemBytes = 1024 + 2 * kStages * kTileBytes + 2 * kQBytes + 2 * kPBytes +
-                                      4 * kStageFloats + kRowInfoBytes + kRefBytes + kWarpMaxBytes + kSumBytes +
+    static constexpr int kSmemBytes = 1024 + (kStagesK + kStagesV) * kTileBytes + 2 * kQBytes + 2 * kPBytes +
+                                      kRowInfoBytes + kRefBytes + kWarpMaxBytes + kSumBytes + kMergeBytes +
                                       kLenBytes + kMiscBytes + 8 * kBars;
+    // Group 1 hands its O over in its own P operand, which its last product has read.
+    static_assert(RP * D * 4 <= kPBytes, "O fits P");
     static constexpr uint32_t kColS = 0, kColO = 2 * kNs;         // S_0 | S_1 | O_0 | O_1
     static constexpr uint32_t kCols = 2 * kNs + 2 * kNp;
     static constexpr uint32_t kTmemCols = kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
@@ -82,9 +89,9 @@ __device__ __forceinline__ uint64_t p8_desc(uint32_t addr, uint32_t lbo, uint32_
            ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (layout << 61);
 }
 
-// Instruction descriptor of kind::f8f6f4: e4m3 A and B, fp32 accumulator.
-__host__ __device__ constexpr uint32_t p8_idesc(int M, int N, bool a_mn, bool b_mn) {
-    return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
+// Instruction descriptor of kind::f8f6f4: e4m3 A, e4m3 or e5m2 B, fp32 accumulator.
+__host__ __device__ constexpr uint32_t p8_idesc(int M, int N, bool a_mn, bool b_mn, bool b_e5m2) {
+    return (1u << 4) | ((b_e5m2 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
            ((uint32_t)(M >> 4) << 24);
 }
 
@@ -121,23 +128,17 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 
 // ------------------------------------------------------------ e4m3 and fp16
 
-__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t v) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(v));
-    return r;
-}
-
 __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
 
-// (a - b) * 16, exact for b = a rounded to e4m3.
-__device__ __forceinline__ uint32_t residual16(uint32_t a, uint32_t b) {
-    const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-    const __half2 s = __hmul2(d, __float2half2_rn(16.f));
-    return *reinterpret_cast<const uint32_t*>(&s);
+// What is left of two fp16 values without their first e5m2 terms (exact).
+__device__ __forceinline__ uint32_t e5m2_residual(uint32_t f) {
+    const uint32_t t = f & 0xff00ff00u;
+    const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&f), *reinterpret_cast<const __half2*>(&t));
+    return *reinterpret_cast<const uint32_t*>(&d);
 }
 
 // Floats to integers of the same order, and back.
@@ -325,15 +326,14 @@ __global__ void __launch_bounds__(kP8Threads, 1)
     gqa_paged_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const PagedFp8Params p) {
     using PS = P8Shape<D, RP>;
-    constexpr int S = PS::kStages;
+    constexpr int SK = PS::kStagesK, SV = PS::kStagesV;
     constexpr uint32_t TB = PS::kTileBytes;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
-    const uint32_t k_s = base, v_s = k_s + S * TB, q_s = v_s + S * TB, p_s = q_s + 2 * PS::kQBytes;
+    const uint32_t k_s = base, v_s = k_s + SK * TB, q_s = v_s + SV * TB, p_s = q_s + 2 * PS::kQBytes;
     unsigned char* gen = smem_raw + (p_s + 2 * PS::kPBytes - raw);
-    float* stage_o = reinterpret_cast<float*>(gen);                       // [RP][D], then m[RP], l[RP]
-    gen += 4 * PS::kStageFloats;
+    float* stage_o = reinterpret_cast<float*>(gen - PS::kPBytes);         // [RP][D], in group 1's P
     // Rows of the unit in q buffer i: scale2 * 2^-e, last visible key, output row.
     float* row_scale = reinterpret_cast<float*>(gen);                     // [2][RP]
     int* row_lim = reinterpret_cast<int*>(row_scale + 2 * RP);            // [2][RP]
@@ -343,6 +343,9 @@ __global__ void __launch_bounds__(kP8Threads, 1)
     gen += PS::kSumBytes;
     float* neg_ref = reinterpret_cast<float*>(gen);                       // [2][RP]: -m
     gen += PS::kRefBytes;
+    float2* other = reinterpret_cast<float2*>(gen);                       // [RP]: (m, l) of group 1
+    float2* factors = other + RP;                                         // [2][RP]: weights of the groups' O
+    gen += PS::kMergeBytes;
     int* warp_max = reinterpret_cast<int*>(gen);                          // [2][4][RP + 1]
     gen += PS::kWarpMaxBytes;
     int* len_copy = reinterpret_cast<int*>(gen);
@@ -353,8 +356,8 @@ __global__ void __launch_bounds__(kP8Threads, 1)
     long long* warp_sum = reinterpret_cast<long long*>(gen + 80);         // [12]
     gen += PS::kMiscBytes;
     const uint32_t bar0 = smem_addr(gen);
-    const uint32_t k_full = bar0, v_full = k_full + 8 * S, empty = v_full + 8 * S;
-    const uint32_t q_full = empty + 8 * S, q_empty = q_full + 16;
+    const uint32_t k_full = bar0, k_empty = k_full + 8 * SK, v_full = k_empty + 8 * SK, v_empty = v_full + 8 * SV;
+    const uint32_t q_full = v_empty + 8 * SV, q_empty = q_full + 16;
     const uint32_t s_full = q_empty + 16, s_free = s_full + 16, p_full = s_free + 16;
     const uint32_t m_full = p_full + 16, m_empty = m_full + 8, fin = m_empty + 8;
 
@@ -363,10 +366,13 @@ __global__ void __launch_bounds__(kP8Threads, 1)
     const P8Lens<RP> lens = {p, len_copy};
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < S; ++s) {
+        for (int s = 0; s < SK; ++s) {
             mbar_init(k_full + 8 * s, 1);
+            mbar_init(k_empty + 8 * s, 1);
+        }
+        for (int s = 0; s < SV; ++s) {
             mbar_init(v_full + 8 * s, 1);
-            mbar_init(empty + 8 * s, 1);       // the stage's last reader, P V, is done
+            mbar_init(v_empty + 8 * s, 1);
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(q_full + 8 * x, 1);
@@ -408,8 +414,9 @@ __global__ void __launch_bounds__(kP8Threads, 1)
         const bool is_v = lane >= 8;
         const int box_of = lane & 7;
         const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
-        const uint32_t full = is_v ? v_full : k_full;
+        const uint32_t full = is_v ? v_full : k_full, empty = is_v ? v_empty : k_empty;
         const uint32_t ring = is_v ? v_s : k_s;
+        const int S = is_v ? SV : SK;
         const int page_size = 1 << p.page_shift;
         const int box = min(page_size, kP8Tokens);
         const int boxes = kP8Tokens / box;
@@ -433,7 +440,8 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                 page = lookup(i + 1);
                 const int pos = i * kP8Tokens + box_of * box;
                 const int here = min(boxes, (T - i * kP8Tokens + box - 1) / box);   // boxes that hold keys
-                ok = warp_wait(empty + 8 * s, ph, abort_flag, p.status, tmo);
+                // Every lane waits for its own ring's stage.
+                ok = __all_sync(0xffffffffu, wait(empty + 8 * s, ph));
                 if (!ok) break;
                 const bool skip = blockIdx.x == 0 && it == p.skip_tile && !is_v;    // injected fault: never loaded
                 if ((lane & 7) == 0 && lane < 16 && !skip) mbar_arrive_expect_tx(full + 8 * s, here * box * D);
@@ -468,7 +476,7 @@ __global__ void __launch_bounds__(kP8Threads, 1)
             int s = 0, x = 0;
             uint32_t ph = 0, np[2] = {0, 0};
             if (warp == 9) {
-                constexpr uint32_t kIdesc = p8_idesc(kP8Tokens, PS::kNs, false, false);
+                constexpr uint32_t kIdesc = p8_idesc(kP8Tokens, PS::kNs, false, false, false);
                 const uint64_t k_desc = p8_desc(k_s, 16, kAtom, kLayout), q_desc = p8_desc(q_s, 16, kAtom, kLayout);
                 int sg = 0;
                 while (ok && walk.next(lens, seg)) {
@@ -485,15 +493,16 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                         for (int kk = 0; kk < D / 32; ++kk)
                             umma_f8(tmem + PS::kColS + x * PS::kNs, kd + kk * 2, qd + kk * 2, kIdesc, kk > 0 ? 1u : 0u);
                         umma_commit(s_full + 8 * x);
+                        umma_commit(k_empty + 8 * s);
                         any = true;
                         x ^= 1;
-                        if (++s == S) s = 0, ph ^= 1;
+                        if (++s == SK) s = 0, ph ^= 1;
                     }
                     if (ok) umma_commit(q_empty + 8 * (sg & 1));
                     ++sg;
                 }
             } else {
-                constexpr uint32_t kIdesc = p8_idesc(D, PS::kNp, true, true);
+                constexpr uint32_t kIdesc = p8_idesc(D, PS::kNp, true, true, true);
                 const uint64_t v_desc = p8_desc(v_s, 16, kAtom, kLayout), p_desc = p8_desc(p_s, 128, 2048, 0);
                 while (ok && walk.next(lens, seg)) {
                     bool first[2] = {true, true};
@@ -508,10 +517,10 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                         for (int kk = 0; kk < kP8Tokens / 32; ++kk)
                             umma_f8(tmem + PS::kColO + x * PS::kNp, vd + kk * (2 * D), pd + kk * 32, kIdesc,
                                     (!fresh || kk > 0) ? 1u : 0u);
-                        umma_commit(empty + 8 * s);
+                        umma_commit(v_empty + 8 * s);
                         any = true;
                         x ^= 1;
-                        if (++s == S) s = 0, ph ^= 1;
+                        if (++s == SV) s = 0, ph ^= 1;
                     }
                 }
             }
@@ -544,67 +553,69 @@ __global__ void __launch_bounds__(kP8Threads, 1)
             lens.split(seg.entry, b, rt);
             const int T = lens.tokens(b);
             const uint32_t qt = q_s + buf * PS::kQBytes;
-            constexpr int kPer = D / 32;          // elements of a row per lane
+            // Four lanes a row, eight rows at a time; the next rows are on
+            // their way while these are split.
+            constexpr int kVec = D / 32;          // 16-byte loads per lane: D / 4 elements
+            const int part = lane & 3;
+            uint4 next[kVec];
+            int orow_next, tok_next;
+            auto load_rows = [&](int r0) {
+                tok_next = 0;
+                orow_next = p8_out_row<RP>(p, b, rt, seg.g, r0 + (lane >> 2), &tok_next);
+                const uint4* src = reinterpret_cast<const uint4*>(p.q + (size_t)max(orow_next, 0) * D + part * (D / 4));
 #pragma unroll
+                for (int c = 0; c < kVec; ++c) next[c] = orow_next >= 0 ? src[c] : make_uint4(0, 0, 0, 0);
+            };
+            load_rows(0);
+#pragma unroll 1
             for (int r0 = 0; r0 < RP; r0 += 8) {
-                uint32_t w[8][kPer / 2];
-                int orow[8], tok[8];
+                uint4 v[kVec];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    tok[i] = 0;
-                    orow[i] = p8_out_row<RP>(p, b, rt, seg.g, r0 + i, &tok[i]);
+                for (int c = 0; c < kVec; ++c) v[c] = next[c];
+                const int orow = orow_next, tok = tok_next, r = r0 + (lane >> 2);
+                if (r0 + 8 < RP) load_rows(r0 + 8);
+                uint32_t top = 0;
 #pragma unroll
-                    for (int c = 0; c < kPer / 2; ++c) w[i][c] = 0;
-                    if (orow[i] >= 0) {
-                        const uint16_t* src = p.q + (size_t)orow[i] * D + lane * kPer;
-                        if constexpr (kPer == 4) {
-                            const uint2 v = *reinterpret_cast<const uint2*>(src);
-                            w[i][0] = v.x;
-                            w[i][1] = v.y;
-                        } else {
-                            w[i][0] = *reinterpret_cast<const uint32_t*>(src);
-                        }
-                    }
+                for (int c = 0; c < kVec; ++c) {
+                    const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
                 }
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const bool bad = top >= 0x7f80u;              // an infinity or NaN: the whole row is NaN
+                const int e = min(134 - max((int)(top >> 7), 1), 120);
+                const float up = bad || top == 0 ? 0.f : pow2i(e);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = r0 + i;
-                    uint32_t top = 0;
+                for (int c = 0; c < kVec; c += 2) {           // 16 elements: one 16-byte chunk of each row
+                    const uint32_t w[8] = {v[c].x, v[c].y, v[c].z, v[c].w,
+                                           v[c + 1].x, v[c + 1].y, v[c + 1].z, v[c + 1].w};
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int c = 0; c < kPer / 2; ++c)
-                        top = max(top, max(w[i][c] & 0x7fffu, (w[i][c] >> 16) & 0x7fffu));
-                    top = __reduce_max_sync(0xffffffffu, top);
-                    const bool bad = top >= 0x7f80u;              // an infinity or NaN: the whole row is NaN
-                    const int e = min(134 - max((int)(top >> 7), 1), 120);
-                    const float up = bad || top == 0 ? 0.f : pow2i(e);
-                    uint32_t hi = 0, lo = 0;
-#pragma unroll
-                    for (int c = 0; c < kPer / 2; ++c) {
-                        const float a = bad ? 0.f : __uint_as_float(w[i][c] << 16) * up;
-                        const float d = bad ? 0.f : __uint_as_float(w[i][c] & 0xffff0000u) * up;
+                    for (int k = 0; k < 8; ++k) {
+                        const float a = bad ? 0.f : __uint_as_float(w[k] << 16) * up;
+                        const float d = bad ? 0.f : __uint_as_float(w[k] & 0xffff0000u) * up;
                         const uint32_t h = f32x2_to_e4m3x2(a, d);
                         const uint32_t hf = e4m3x2_to_f16x2((uint16_t)h);
                         const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hf));
-                        hi |= h << (16 * c);
-                        lo |= f32x2_to_e4m3x2((a - back.x) * 16.f, (d - back.y) * 16.f) << (16 * c);
+                        const uint32_t lw = f32x2_to_e4m3x2((a - back.x) * 16.f, (d - back.y) * 16.f);
+                        if ((k & 1) == 0) hi[k / 2] = h, lo[k / 2] = lw;
+                        else hi[k / 2] |= h << 16, lo[k / 2] |= lw << 16;
                     }
-                    const uint32_t at_byte = lane * kPer;
+                    const uint32_t chunk = part * (D / 64) + c / 2;
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         const uint32_t row = t * RP + r;
                         const uint32_t sw = D == 128 ? (row & 7) : ((row >> 1) & 3);
-                        const uint32_t addr = qt + row * D + ((((at_byte >> 4) ^ sw) << 4) | (at_byte & 15));
-                        if constexpr (kPer == 4)
-                            asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(t ? lo : hi) : "memory");
-                        else
-                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"((uint16_t)(t ? lo : hi)) : "memory");
+                        const uint32_t* x = t ? lo : hi;
+                        st_shared_v4(qt + row * D + ((chunk ^ sw) << 4), make_uint4(x[0], x[1], x[2], x[3]));
                     }
-                    if (lane == 0) {
-                        row_scale[buf * RP + r] = orow[i] < 0 ? 0.f : bad ? __int_as_float(0x7fffffff)
-                                                                        : p.scale_log2 * (top == 0 ? 1.f : pow2i(-e));
-                        row_lim[buf * RP + r] = orow[i] < 0 ? -1 : T - p.sq + tok[i];
-                        row_out[buf * RP + r] = orow[i];
-                    }
+                }
+                if (part == 0) {
+                    row_scale[buf * RP + r] = orow < 0 ? 0.f : bad ? __int_as_float(0x7fffffff)
+                                                                 : p.scale_log2 * (top == 0 ? 1.f : pow2i(-e));
+                    row_lim[buf * RP + r] = orow < 0 ? -1 : T - p.sq + tok;
+                    row_out[buf * RP + r] = orow;
                 }
             }
             fence_proxy_async_smem();
@@ -635,11 +646,12 @@ __global__ void __launch_bounds__(kP8Threads, 1)
         const uint32_t o_tm = lane_base + PS::kColO + x * PS::kNp;
         const uint32_t p_at = p_s + x * PS::kPBytes + tok * 16;
         float* const my_ref = neg_ref + x * RP;
+        float2* const factor = factors + x * RP;
         int* const my_max = warp_max + x * 4 * (RP + 1);
         uint32_t n_tiles = 0, n_merge = 0;       // phases of s_full and p_full, of m_full
         int it0 = 0, sg = 0;                     // the CTA's tile number at the segment's start
         // The product of this group's tile `it` has completed.
-        auto wait_product = [&](int it) { all_wait(empty + 8 * (it % S), it / S); };
+        auto wait_product = [&](int it) { all_wait(v_empty + 8 * (it % SV), it / SV); };
         while (walk.next(lens, seg)) {
             int b, rt;
             lens.split(seg.entry, b, rt);
@@ -773,8 +785,8 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                     // NaN code in a key that only some rows see would reach the
                     // others as 0 * NaN: its row is zeroed too, and the rows that
                     // see it are made NaN through P.
-                    const int s = it % S;
-                    all_wait(v_full + 8 * s, it / S);
+                    const int s = it % SV;
+                    all_wait(v_full + 8 * s, it / SV);
                     if (pos > lim_min) {
                         const uint32_t at = v_s + s * TB + tok * D;
                         bool clear = pos >= T;
@@ -799,7 +811,7 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                     }
                 }
                 const float vw = vs * pow2i(-ev) * kP8ProbScale;
-                uint32_t packed[RP / 4][kP8Terms];       // four rows: hi, mid, lo, last
+                uint32_t packed[RP / 4][kP8Terms];       // a term of four rows
 #pragma unroll
                 for (int r = 0; r < RP; r += 4) {
                     const float4 m = *reinterpret_cast<const float4*>(my_ref + r);
@@ -815,16 +827,16 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                     uint32_t f0 = pack_f16x2(w[0], w[1]), f1 = pack_f16x2(w[2], w[3]);
 #pragma unroll
                     for (int t = 0; t < kP8Terms; ++t) {
-                        const uint32_t c0 = f16x2_to_e4m3x2(f0), c1 = f16x2_to_e4m3x2(f1);
-                        packed[r / 4][t] = c0 | (c1 << 16);
+                        packed[r / 4][t] = __byte_perm(f0, f1, 0x7531);      // the four upper bytes
                         if (t + 1 < kP8Terms) {
-                            f0 = residual16(f0, e4m3x2_to_f16x2((uint16_t)c0));
-                            f1 = residual16(f1, e4m3x2_to_f16x2((uint16_t)c1));
+                            f0 = e5m2_residual(f0);
+                            f1 = e5m2_residual(f1);
                         }
                     }
                 }
                 // P's operand is free once the group's previous product is done.
                 if (it >= 2) wait_product(it - 2);
+                if (x == 1 && first) all_wait(m_empty, n_merge + 1);      // and handed-over O is read
                 // Column term * RP + r; 16 columns of a token are 16 bytes.
 #pragma unroll
                 for (int c = 0; c < PS::kNp / 16; ++c) {
@@ -868,11 +880,7 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                     uint32_t t[16];
                     tmem_ld16(o_tm + 16 * c, t);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const int n = 16 * c + k;
-                        const float f = n < RP ? 1.f : n < 2 * RP ? 0x1p-4f : n < 3 * RP ? 0x1p-8f : 0x1p-12f;
-                        o[n % RP] = fmaf(__uint_as_float(t[k]), f, o[n % RP]);
-                    }
+                    for (int k = 0; k < 16; ++k) o[(16 * c + k) % RP] += __uint_as_float(t[k]);
                 }
                 tc_fence_before();
                 // D = 64 products keep 16 of their rows in each warp's 32 lanes.
@@ -880,14 +888,12 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                 const int dim = D == 128 ? tok : w4 * 16 + lane;
                 const float unit = pow2i(ev) * (1.f / kP8ProbScale);
                 if (both && x == 1) {
-                    all_wait(m_empty, n_merge + 1);
 #pragma unroll
                     for (int r = 0; r < RP; ++r)
                         if (mine) stage_o[r * D + dim] = o[r] * unit;
                     if (tok < RP) {
                         const float4 q = sums[x * RP + tok];
-                        stage_o[RP * D + tok] = -my_ref[tok];
-                        stage_o[RP * D + RP + tok] = q.x + q.y + q.z + q.w;
+                        other[tok] = make_float2(-my_ref[tok], q.x + q.y + q.z + q.w);
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(m_full);
@@ -896,34 +902,42 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                     if (both) all_wait(m_full, n_merge);
                     const bool whole = seg.i0 == 0 && seg.i1 == seg.n;
                     float* slot = p.part + ((size_t)blockIdx.x * 2 + (seg.i0 == 0 ? 1 : 0)) * p8_slot_floats(RP, D);
-#pragma unroll
-                    for (int r = 0; r < RP; ++r) {
-                        const float4 q = sums[x * RP + r];
-                        float m = -my_ref[r], ls = q.x + q.y + q.z + q.w, y = o[r] * unit;
+                    const int* rows_out = row_out + (sg & 1) * RP;
+                    if (tok < RP) {
+                        const float4 q = sums[x * RP + tok];
+                        float m = -my_ref[tok], ls = q.x + q.y + q.z + q.w, a0 = 1.f, a1 = 0.f;
                         if (both) {
-                            const float m1 = stage_o[RP * D + r], l1 = stage_o[RP * D + RP + r];
-                            const float top = fmaxf(m, m1);
-                            const float a0 = fast_exp2(m - top), a1 = fast_exp2(m1 - top);
+                            const float2 u = other[tok];
+                            const float top = fmaxf(m, u.x);
+                            a0 = fast_exp2(m - top);
+                            a1 = fast_exp2(u.x - top);
                             m = top;
-                            ls = ls * a0 + l1 * a1;
-                            y = y * a0 + (mine ? stage_o[r * D + dim] : 0.f) * a1;
+                            ls = ls * a0 + u.y * a1;
                         }
-                        const int orow = row_out[(sg & 1) * RP + r];
-                        if (orow < 0) continue;
                         if (whole) {
                             const bool some = ls > 0.f || ls != ls;
-                            if (mine)
-                                p.out[(size_t)orow * D + dim] =
-                                    (uint16_t)(pack_bf16x2(some ? y * (1.f / ls) : 0.f, 0.f) & 0xffffu);
-                            if (p.lse && tok == r)
-                                p.lse[orow] = some ? (m + log2f(ls)) * 0.6931471805599453f : -INFINITY;
+                            const float inv = some ? 1.f / ls : 0.f;
+                            a0 *= inv;
+                            a1 *= inv;
+                            if (p.lse && rows_out[tok] >= 0)
+                                p.lse[rows_out[tok]] = some ? (m + log2f(ls)) * 0.6931471805599453f : -INFINITY;
                         } else {
-                            if (mine) slot[r * D + dim] = y;
-                            if (tok == r) {
-                                slot[RP * D + r] = m;
-                                slot[RP * D + RP + r] = ls;
-                            }
+                            slot[RP * D + tok] = m;
+                            slot[RP * D + RP + tok] = ls;
                         }
+                        factor[tok] = make_float2(a0 * unit, a1);
+                    }
+                    group_sync(x);
+#pragma unroll
+                    for (int r = 0; r < RP; ++r) {
+                        const float2 f = factor[r];
+                        float y = o[r] * f.x;
+                        if (both && mine) y = fmaf(stage_o[r * D + dim], f.y, y);
+                        if (!mine) continue;
+                        if (!whole)
+                            slot[r * D + dim] = y;
+                        else if (rows_out[r] >= 0)
+                            p.out[(size_t)rows_out[r] * D + dim] = (uint16_t)(pack_bf16x2(y, 0.f) & 0xffffu);
                     }
                     if (both) {
                         __syncwarp();
