@@ -621,6 +621,8 @@ int current_device(int* sms, unsigned** status) {
     return GQA_OK;
 }
 
+unsigned long long call_tag() { return call_epoch(); }
+
 void wait_knobs(unsigned long long* timeout_ns, int* skip_tile) { debug_knobs(timeout_ns, skip_tile); }
 
 int encode_byte_map(CUtensorMap* map, const void* base, long long slabs, int rows, int cols, int box_rows) {

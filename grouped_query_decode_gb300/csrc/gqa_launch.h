@@ -45,6 +45,7 @@ int splitkv_stages(int D, int row_tiles, bool kv8 = false);
 // Host services of api.cu for the entry points of the other translation units.
 int remember_cuda_error(cudaError_t e);                     // returns GQA_ERR_CUDA
 int current_device(int* sms, unsigned** status);            // SM count, status word
+unsigned long long call_tag();                              // 48 bits, another for every call
 void wait_knobs(unsigned long long* timeout_ns, int* skip_tile);
 // cuTensorMapEncodeTiled of a 3-D uint8 tensor [slabs][rows][cols] (dense) with
 // boxes of box_rows x cols bytes and the swizzle that `cols` (64 or 128) spans.

@@ -26,11 +26,14 @@
 // p through a power of two 2^c that follows the largest scale seen.
 //
 // Work: the tiles of all units, end to end, are shared equally by the CTAs
-// (one per SM); a unit that crosses CTAs leaves (O, m, l) per CTA in the
-// workspace for the merge kernel. Per CTA: two groups of four softmax warps
-// take alternate tiles, two warps bring K and V by TMA (a box per page, the
-// swizzle of the operand layout), one issues the products, one prepares Q.
-// Every wait is bounded, as in the other kernels.
+// (one per SM). A unit that crosses CTAs leaves (O, m, l) per CTA in the
+// workspace; the CTA that arrives last merges them. Per CTA: two groups of four
+// softmax warps (with 32 rows two such pairs, 16 rows each) take alternate
+// tiles, a warp brings K and V (a TMA box per page, in the swizzle of the
+// operand layout), two threads issue the products, a warp splits Q and fetches
+// the blocks' scales up to 16 tiles ahead (behind a saturated HBM a lookup of
+// page and scale takes longer than a tile). Every wait is bounded, as in the
+// other kernels.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -43,7 +46,10 @@
 
 namespace gqa {
 
-constexpr int kP8Threads = 384;
+constexpr int kP8LenCopy = 384;           // sequences whose lengths a CTA keeps
+constexpr int kP8ScaleChunk = 4;          // tiles whose scales are fetched together,
+constexpr int kP8ScaleChunks = 4;         // and how many such chunks a CTA keeps
+constexpr int kP8SmallEntries = 128;      // entries that each warp plans by itself
 constexpr int kP8Terms = 4;               // e5m2 columns per probability
 constexpr float kP8Slack = 4.0f;          // p <= 2^4 before the reference moves
 constexpr float kP8ProbScale = 2048.0f;   // p * v_scale * 2^-ev * 2048 <= 16 * 1.75 * 2048 = 57344
@@ -53,6 +59,10 @@ constexpr float kP8Unseen = -3.402823466e38f;   // reference of a row that has s
 template <int D, int RP>
 struct P8Shape {
     static constexpr int kTileBytes = kP8Tokens * D;              // K or V of one tile
+    static constexpr int kParts = RP == 32 ? 2 : 1;               // row parts, each with its own warps
+    static constexpr int kRows = RP / kParts;                     // rows per softmax thread
+    static constexpr int kSoftWarps = 8 * kParts;
+    static constexpr int kThreads = (kSoftWarps + 4) * 32;
     static constexpr int kNs = 2 * RP;                            // columns of S: hi, lo
     static constexpr int kNp = kP8Terms * RP;                     // columns of O
     static constexpr int kQBytes = kNs * D;
@@ -61,17 +71,18 @@ struct P8Shape {
     // copy to P V, a K tile only to S, so V gets more stages.
     static constexpr int kStagesK = (D == 128 ? 1 : 2) * (RP == 32 ? 4 : 5);
     static constexpr int kStagesV = (D == 128 ? 1 : 2) * (RP == 32 ? 5 : 7);
-    static constexpr int kBars = 2 * (kStagesK + kStagesV) + 15;
+    static constexpr int kBars = 2 * (kStagesK + kStagesV) + 24;
     static constexpr int kRowInfoBytes = 2 * 3 * RP * 4;
     static constexpr int kRefBytes = 2 * RP * 4;
-    static constexpr int kWarpMaxBytes = 2 * 4 * (RP + 1) * 4;
+    static constexpr int kWarpMaxBytes = 2 * kParts * 4 * (kRows + 1) * 4;
     static constexpr int kSumBytes = 2 * RP * 16;
     static constexpr int kMergeBytes = 3 * RP * 8;                // group 1's (m, l); each group's row factors
-    static constexpr int kLenBytes = kP8Threads * 4;
-    static constexpr int kMiscBytes = 192;
+    static constexpr int kLenBytes = kP8LenCopy * 4;
+    static constexpr int kScaleBytes = kP8ScaleChunks * kP8ScaleChunk * 16 * 4;
+    static constexpr int kMiscBytes = 320;
     static constexpr int kSmemBytes = 1024 + (kStagesK + kStagesV) * kTileBytes + 2 * kQBytes + 2 * kPBytes +
                                       kRowInfoBytes + kRefBytes + kWarpMaxBytes + kSumBytes + kMergeBytes +
-                                      kLenBytes + kMiscBytes + 8 * kBars;
+                                      kLenBytes + kScaleBytes + kMiscBytes + 8 * kBars;
     // Group 1 hands its O over in its own P operand, which its last product has read.
     static_assert(RP * D * 4 <= kPBytes, "O fits P");
     static constexpr uint32_t kColS = 0, kColO = 2 * kNs;         // S_0 | S_1 | O_0 | O_1
@@ -117,6 +128,37 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(taddr)
+        : "memory");
+}
+
+// Two runs of 16 columns, one wait.
+__device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, uint32_t (&a)[16], uint32_t (&b)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+        "%28, %29, %30, %31}, [%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]),
+          "=r"(a[8]), "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]),
+          "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]),
+          "=r"(b[8]), "=r"(b[9]), "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15])
+        : "r"(ta), "r"(tb)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
@@ -124,6 +166,15 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&r)[N]) {
+    if constexpr (N == 8) tmem_ld8(taddr, r); else tmem_ld16(taddr, r);
+}
+template <int N>
+__device__ __forceinline__ void tmem_st_rows(uint32_t taddr, const uint32_t (&r)[N]) {
+    if constexpr (N == 8) tmem_st8(taddr, r); else tmem_st16(taddr, r);
 }
 
 // ------------------------------------------------------------ e4m3 and fp16
@@ -159,7 +210,7 @@ struct P8Lens {
     const PagedFp8Params& p;
     const int* copy;
     __device__ int global(int b) const { return clamp_len(p.lens[b], p.max_pages << p.page_shift); }
-    __device__ int tokens(int b) const { return p.B <= kP8Threads ? copy[b] : global(b); }
+    __device__ int tokens(int b) const { return p.B <= kP8LenCopy ? copy[b] : global(b); }
     __device__ void split(int entry, int& b, int& rt) const {
         b = p.row_tiles == 1 ? entry : entry / p.row_tiles;
         rt = entry - b * p.row_tiles;
@@ -206,7 +257,65 @@ struct P8Plan {
     long long total, begin, end;   // tiles of the call, and this CTA's
     int entry, g, off;             // where it begins
     int ctas;                      // CTAs that share the tiles
+    // The CTA whose share holds tile t of the call.
+    __device__ int owner(long long t) const {
+        const unsigned long long x = (unsigned long long)(t + 1) * (unsigned)ctas - 1;
+        return x >> 32 ? (int)(x / (unsigned long long)total) : (int)((unsigned)x / (unsigned)total);
+    }
 };
+
+// Up to 128 sequences of one row tile, and 32-bit products of tiles and CTAs:
+// every warp finds the CTA's share by itself, four entries a lane, so that no
+// warp waits for another. Each warp also writes the (same) copy of the lengths.
+template <int RP>
+__device__ __forceinline__ P8Plan p8_small_plan(const P8Lens<RP>& lens, int* len_copy) {
+    const PagedFp8Params& p = lens.p;
+    const int lane = threadIdx.x & 31;
+    unsigned n[4], mine = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int e = lane * 4 + k;
+        const int T = e < p.B ? lens.global(e) : 0;
+        if (e < p.B) len_copy[e] = T;
+        n[k] = (unsigned)(T + kP8Tokens - 1) / kP8Tokens;
+        mine += n[k];
+    }
+    mine *= (unsigned)p.G;
+    unsigned x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    const unsigned total = __shfl_sync(0xffffffffu, x, 31), before = x - mine;
+    const unsigned most = total / kP8MinTiles;
+    const unsigned ctas = most < 1 ? 1 : most < gridDim.x ? most : gridDim.x;
+    const unsigned c = blockIdx.x;
+    const unsigned t0 = c < ctas ? total * c / ctas : total, t1 = c < ctas ? total * (c + 1) / ctas : total;
+    // The lane whose entries hold tile t0, and where in them it lies.
+    const unsigned here = __ballot_sync(0xffffffffu, t0 >= before && t0 < before + mine);
+    int e = lane * 4;
+    unsigned at = before, ne = n[0];
+#pragma unroll
+    for (int k = 1; k < 4; ++k)
+        if (at + ne * p.G <= t0) {
+            at += ne * p.G;
+            ne = n[k];
+            ++e;
+        }
+    const unsigned in = t0 - at, g = ne ? in / ne : 0;
+    const int src = here ? __ffs(here) - 1 : 0;
+    P8Plan plan;
+    plan.total = total;
+    plan.begin = t0;
+    plan.end = t1;
+    plan.entry = __shfl_sync(0xffffffffu, e, src);
+    plan.g = __shfl_sync(0xffffffffu, (int)g, src);
+    plan.off = __shfl_sync(0xffffffffu, (int)(in - g * ne), src);
+    plan.ctas = (int)ctas;
+    __syncwarp();
+    return plan;
+}
 
 // a * b / c for 64-bit a, in 32 bits where they do.
 __device__ __forceinline__ long long muldiv(long long a, int b, int c) {
@@ -214,21 +323,18 @@ __device__ __forceinline__ long long muldiv(long long a, int b, int c) {
     return x >> 32 ? (long long)(x / (unsigned)c) : (long long)((unsigned)x / (unsigned)c);
 }
 
-// All threads: sums the tiles of all entries, each thread over a contiguous
-// range of them, and finds where this CTA's share begins. The caller
-// synchronises the CTA before anyone reads the plan.
-template <int RP>
-__device__ void p8_make_plan(const P8Lens<RP>& lens, int* len_copy, P8Plan* plan, long long* warp_sum) {
-    const PagedFp8Params& p = lens.p;
+// Any sizes, all threads: sums the tiles of all entries, each thread over a
+// contiguous range of them, and finds where this CTA's share begins. The
+// caller synchronises the CTA before anyone reads the plan.
+template <int RP, int THREADS>
+__device__ __noinline__ void p8_make_plan(const PagedFp8Params& p, int* len_copy, P8Plan* plan, long long* warp_sum) {
+    const P8Lens<RP> lens = {p, len_copy};
     const int entries = p.B * p.row_tiles;
-    const int per = (entries + kP8Threads - 1) / kP8Threads;
+    const int per = (entries + THREADS - 1) / THREADS;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (p.B <= kP8Threads && p.row_tiles > 1) {
-        if ((int)threadIdx.x < p.B) len_copy[threadIdx.x] = lens.global(threadIdx.x);
-        __syncthreads();
-    } else if ((int)threadIdx.x < p.B && p.B <= kP8Threads) {
-        len_copy[threadIdx.x] = lens.global(threadIdx.x);    // read back below by this thread only
-    }
+    if (p.B <= kP8LenCopy)
+        for (int b = threadIdx.x; b < p.B; b += THREADS) len_copy[b] = lens.global(b);
+    __syncthreads();
     const int e0 = (int)min((long long)entries, (long long)threadIdx.x * per), e1 = min(entries, e0 + per);
     long long mine = 0;
     for (int e = e0; e < e1; ++e) mine += lens.tiles(e);
@@ -242,8 +348,7 @@ __device__ void p8_make_plan(const P8Lens<RP>& lens, int* len_copy, P8Plan* plan
     if (lane == 31) warp_sum[warp] = x;
     __syncthreads();
     long long before = x - mine, total = 0;
-#pragma unroll
-    for (int w = 0; w < kP8Threads / 32; ++w) {
+    for (int w = 0; w < THREADS / 32; ++w) {
         if (w < warp) before += warp_sum[w];
         total += warp_sum[w];
     }
@@ -265,10 +370,9 @@ __device__ void p8_make_plan(const P8Lens<RP>& lens, int* len_copy, P8Plan* plan
                 at += (long long)n * p.G;
                 n = lens.tiles(++e);
             }
-            const unsigned in = (unsigned)min(t0 - at, 0xffffffffll);   // below n * G
             plan->entry = e;
-            plan->g = t0 - at > 0xffffffffll ? (int)((t0 - at) / n) : (int)(in / (unsigned)n);
-            plan->off = (int)(t0 - at - (long long)plan->g * n);
+            plan->g = (int)((t0 - at) / n);
+            plan->off = (int)((t0 - at) % n);
         }
     }
 }
@@ -302,13 +406,69 @@ __device__ __forceinline__ int p8_out_row(const PagedFp8Params& p, int b, int rt
     return (b * p.sq + s) * p.H + g * p.heads_per_group + (rr - s * p.heads_per_group);
 }
 
+// One group's merge of rows [r0, r0 + RH) of a unit that n CTAs from c0 on hold
+// parts of: a warp per row. The first CTA's part is in its second slot, every
+// other's in its first.
+template <int D, int RP, int RH>
+__device__ __noinline__ void p8_merge(const PagedFp8Params& p, int c0, int n, int r0, int w4, int lane,
+                                      const int* rows_out) {
+    constexpr int kPer = D / 32;
+    const size_t slot = p8_slot_floats(RP, D);
+    auto at = [&](int i) { return p.part + ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * slot; };
+    for (int k = w4; k < RH; k += 4) {
+        const int orow = rows_out[k], r = r0 + k;
+        if (orow < 0) continue;
+        float top = kP8Unseen;
+        for (int i = lane; i < n; i += 32) top = fmaxf(top, __ldcg(at(i) + RP * D + r));
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        float l = 0.f, y[kPer];
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) y[c] = 0.f;
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            float a = 0.f;
+            if (i0 + lane < n) {
+                a = fast_exp2(__ldcg(at(i0 + lane) + RP * D + r) - top);
+                l += __ldcg(at(i0 + lane) + RP * D + RP + r) * a;
+            }
+#pragma unroll 8
+            for (int i = 0; i < min(32, n - i0); ++i) {
+                const float w = __shfl_sync(0xffffffffu, a, i);
+                const float* src = at(i0 + i) + r * D + lane * kPer;
+                if constexpr (kPer == 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+                    y[0] = fmaf(v.x, w, y[0]);
+                    y[1] = fmaf(v.y, w, y[1]);
+                    y[2] = fmaf(v.z, w, y[2]);
+                    y[3] = fmaf(v.w, w, y[3]);
+                } else {
+                    const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+                    y[0] = fmaf(v.x, w, y[0]);
+                    y[1] = fmaf(v.y, w, y[1]);
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        const bool some = l > 0.f || l != l;
+        const float inv = some ? 1.f / l : 0.f;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (size_t)orow * D + lane * kPer);
+#pragma unroll
+        for (int c = 0; c < kPer / 2; ++c)
+            dst[c] = pack_bf16x2(some ? y[2 * c] * inv : 0.f, some ? y[2 * c + 1] * inv : 0.f);
+        if (p.lse && lane == 0) p.lse[orow] = some ? (top + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    }
+}
+
 // ------------------------------------------------------------------- kernel
 
-// A group's 128 threads meet (and agree whether any of them votes). These are
-// the CTA's named barriers 1 and 2: no thread of a group ever leaves its loop
-// early, whatever a bounded wait reported, so the four warps always arrive.
-__device__ __forceinline__ void group_sync(int x) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(x + 1) : "memory"); }
-__device__ __forceinline__ bool group_any(int x, bool v) {
+// The threads of a group meet (and agree whether any of them votes), on the
+// CTA's named barriers. No softmax thread leaves its loop early, whatever a
+// bounded wait reported, so all of a group's warps always arrive.
+__device__ __forceinline__ void named_sync(int id, int threads) {
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ bool named_any(int id, bool v) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
@@ -316,24 +476,53 @@ __device__ __forceinline__ bool group_any(int x, bool v) {
         "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)v), "r"(x + 1)
+        : "r"((uint32_t)v), "r"(id)
         : "memory");
     return r != 0;
 }
 
+// Counts one arrival on a counter that holds (tag << 16 | count); one with
+// another tag counts from zero. True for the last of n, which leaves a count
+// of zero: a captured call is replayed with its tag.
+__device__ __forceinline__ bool arrive_last(unsigned long long* counter, unsigned long long tag, unsigned n) {
+    const unsigned long long zero = tag << 16;
+    unsigned count;
+    const unsigned long long old = atomicAdd(counter, 1ull);
+    if (old >> 16 == tag) {
+        count = (unsigned)(old & 0xffffu) + 1;
+    } else {
+        unsigned long long seen = *reinterpret_cast<volatile unsigned long long*>(counter);
+        while (true) {
+            if (seen >> 16 == tag) {           // another arrival has tagged it: its count lacks this one
+                count = (unsigned)(atomicAdd(counter, 1ull) & 0xffffu) + 1;
+                break;
+            }
+            const unsigned long long was = atomicCAS(counter, seen, zero | 1ull);
+            if (was == seen) {
+                count = 1;
+                break;
+            }
+            seen = was;
+        }
+    }
+    if (count != n) return false;
+    atomicExch(counter, zero);
+    return true;
+}
+
 template <int D, int RP>
-__global__ void __launch_bounds__(kP8Threads, 1)
+__global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
     gqa_paged_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                         const PagedFp8Params p) {
+                         const __grid_constant__ PagedFp8Params p) {
     using PS = P8Shape<D, RP>;
-    constexpr int SK = PS::kStagesK, SV = PS::kStagesV;
+    constexpr int SK = PS::kStagesK, SV = PS::kStagesV, RH = PS::kRows, SW = PS::kSoftWarps;
     constexpr uint32_t TB = PS::kTileBytes;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     const uint32_t k_s = base, v_s = k_s + SK * TB, q_s = v_s + SV * TB, p_s = q_s + 2 * PS::kQBytes;
     unsigned char* gen = smem_raw + (p_s + 2 * PS::kPBytes - raw);
-    float* stage_o = reinterpret_cast<float*>(gen - PS::kPBytes);         // [RP][D], in group 1's P
+    float* const handed = reinterpret_cast<float*>(gen - PS::kPBytes);    // group 1's O, in its P
     // Rows of the unit in q buffer i: scale2 * 2^-e, last visible key, output row.
     float* row_scale = reinterpret_cast<float*>(gen);                     // [2][RP]
     int* row_lim = reinterpret_cast<int*>(row_scale + 2 * RP);            // [2][RP]
@@ -346,20 +535,24 @@ __global__ void __launch_bounds__(kP8Threads, 1)
     float2* other = reinterpret_cast<float2*>(gen);                       // [RP]: (m, l) of group 1
     float2* factors = other + RP;                                         // [2][RP]: weights of the groups' O
     gen += PS::kMergeBytes;
-    int* warp_max = reinterpret_cast<int*>(gen);                          // [2][4][RP + 1]
+    float* scale_ring = reinterpret_cast<float*>(gen);                    // [slots][8 of K, 8 of V]
+    gen += PS::kScaleBytes;
+    int* warp_max = reinterpret_cast<int*>(gen);                          // [2][parts][4][RH + 1]
     gen += PS::kWarpMaxBytes;
     int* len_copy = reinterpret_cast<int*>(gen);
     gen += PS::kLenBytes;
-    P8Plan* plan = reinterpret_cast<P8Plan*>(gen);                        // 40 bytes
+    P8Plan* plan_s = reinterpret_cast<P8Plan*>(gen);                      // 40 bytes
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gen + 64);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gen + 68);
-    long long* warp_sum = reinterpret_cast<long long*>(gen + 80);         // [12]
+    volatile int* last_flag = reinterpret_cast<volatile int*>(gen + 72);  // [4]
+    long long* warp_sum = reinterpret_cast<long long*>(gen + 96);         // [20]
     gen += PS::kMiscBytes;
     const uint32_t bar0 = smem_addr(gen);
     const uint32_t k_full = bar0, k_empty = k_full + 8 * SK, v_full = k_empty + 8 * SK, v_empty = v_full + 8 * SV;
     const uint32_t q_full = v_empty + 8 * SV, q_empty = q_full + 16;
     const uint32_t s_full = q_empty + 16, s_free = s_full + 16, p_full = s_free + 16;
-    const uint32_t m_full = p_full + 16, m_empty = m_full + 8, fin = m_empty + 8;
+    const uint32_t m_full = p_full + 16, m_empty = m_full + 16, fin = m_empty + 16;
+    const uint32_t sc_full = fin + 16, sc_free = sc_full + 8 * kP8ScaleChunks;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t tmo = p.wait_timeout_ns;
@@ -376,30 +569,41 @@ __global__ void __launch_bounds__(kP8Threads, 1)
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(q_full + 8 * x, 1);
-            mbar_init(q_empty + 8 * x, 9);     // eight softmax warps and the products
+            mbar_init(q_empty + 8 * x, SW + 1);         // the softmax warps and the products
             mbar_init(s_full + 8 * x, 1);
-            mbar_init(s_free + 8 * x, 4);
-            mbar_init(p_full + 8 * x, 4);
+            mbar_init(s_free + 8 * x, 4 * PS::kParts);
+            mbar_init(p_full + 8 * x, 4 * PS::kParts);
             mbar_init(fin + 8 * x, 1);
+            mbar_init(m_full + 8 * x, 4);
+            mbar_init(m_empty + 8 * x, 4);
         }
-        mbar_init(m_full, 4);
-        mbar_init(m_empty, 4);
+        for (int c = 0; c < kP8ScaleChunks; ++c) {
+            mbar_init(sc_full + 8 * c, 1);
+            mbar_init(sc_free + 8 * c, kP8ScaleChunk * PS::kParts);
+        }
         *abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == 9) {
+    if (warp == SW + 1) {
         tmem_alloc(smem_addr(tmem_slot), PS::kTmemCols);
         tmem_relinquish();
     }
-    if (warp == 8 && lane < 2) tma_prefetch_desc(lane ? &tm_v : &tm_k);
+    if (warp == SW && lane < 2) tma_prefetch_desc(lane ? &tm_v : &tm_k);
     tc_fence_before();
-    pdl_launch_dependents();
-    pdl_wait_primary();
-    p8_make_plan<RP>(lens, len_copy, plan, warp_sum);
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    P8Walk<RP> walk = {plan->end - plan->begin, plan->entry, plan->g, plan->off};
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    P8Plan plan;
+    if (p.small_plan) {
+        plan = p8_small_plan<RP>(lens, len_copy);
+    } else {
+        p8_make_plan<RP, PS::kThreads>(p, len_copy, plan_s, warp_sum);
+        __syncthreads();
+        plan = *plan_s;
+    }
+    P8Walk<RP> walk = {plan.end - plan.begin, plan.entry, plan.g, plan.off};
     P8Segment seg;
     // Bounded waits of one thread, and of a softmax warp: all its lanes poll,
     // and all go on when the limit runs out.
@@ -409,16 +613,16 @@ __global__ void __launch_bounds__(kP8Threads, 1)
         __syncwarp();
     };
 
-    if (warp == 8) {
+    if (warp == SW) {
         // ------------------------------------- loader: lanes 0-7 K, lanes 8-15 V
         const bool is_v = lane >= 8;
-        const int box_of = lane & 7;
+        const int sub = lane & 7;
         const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
         const uint32_t full = is_v ? v_full : k_full, empty = is_v ? v_empty : k_empty;
         const uint32_t ring = is_v ? v_s : k_s;
         const int S = is_v ? SV : SK;
         const int page_size = 1 << p.page_shift;
-        const int box = min(page_size, kP8Tokens);
+        const int box = min(page_size, kP8Tokens);              // rows of a copy
         const int boxes = kP8Tokens / box;
         const uint64_t pol = l2_policy_evict_first();
         int it = 0, issued = 0, s = 0;
@@ -429,29 +633,31 @@ __global__ void __launch_bounds__(kP8Threads, 1)
             lens.split(seg.entry, b, rt);
             const int T = lens.tokens(b);
             const int32_t* row = p.table + (size_t)b * p.max_pages;
-            // This lane's page of a tile; looked up one tile ahead.
-            auto lookup = [&](int i) {
-                const int pos = i * kP8Tokens + box_of * box;
-                return lane < 16 && box_of < boxes && i < seg.i1 && pos < T ? row[pos >> p.page_shift] : -1;
-            };
-            int page = lookup(seg.i0);
+            // The table is read 32 entries at a time, a lane each, and the
+            // next 32 are on their way.
+            int first = (seg.i0 * kP8Tokens) >> p.page_shift;
+            const int last = (min(T, seg.i1 * kP8Tokens) - 1) >> p.page_shift;
+            auto entries = [&](int e) { return e + lane <= last ? row[e + lane] : -1; };
+            int cur = entries(first), nxt = entries(first + 32);
             for (int i = seg.i0; i < seg.i1; ++i, ++it) {
-                const int cur = page;
-                page = lookup(i + 1);
-                const int pos = i * kP8Tokens + box_of * box;
+                if (((i * kP8Tokens) >> p.page_shift) - first >= 32) {
+                    first += 32;
+                    cur = nxt;
+                    nxt = entries(first + 32);
+                }
+                const int pos = i * kP8Tokens + sub * box;
+                const int page = __shfl_sync(0xffffffffu, cur, ((pos >> p.page_shift) - first) & 31);
                 const int here = min(boxes, (T - i * kP8Tokens + box - 1) / box);   // boxes that hold keys
                 // Every lane waits for its own ring's stage.
                 ok = __all_sync(0xffffffffu, wait(empty + 8 * s, ph));
                 if (!ok) break;
                 const bool skip = blockIdx.x == 0 && it == p.skip_tile && !is_v;    // injected fault: never loaded
-                if ((lane & 7) == 0 && lane < 16 && !skip) mbar_arrive_expect_tx(full + 8 * s, here * box * D);
+                if (sub == 0 && lane < 16 && !skip) mbar_arrive_expect_tx(full + 8 * s, here * box * D);
                 __syncwarp();
-                if (lane < 16 && box_of < here && !skip) {
+                if (lane < 16 && sub < here && !skip)
                     // A page outside the pool is a slab out of range: zeros.
-                    const int z = (unsigned)cur < (unsigned)p.num_pages ? cur * p.G + seg.g : -1;
-                    tma_load_3d_hint(ring + s * TB + box_of * box * D, tm, full + 8 * s, 0, pos & (page_size - 1), z,
-                                     pol);
-                }
+                    tma_load_3d_hint(ring + s * TB + sub * box * D, tm, full + 8 * s, 0, pos & (page_size - 1),
+                                     (unsigned)page < (unsigned)p.num_pages ? page * p.G + seg.g : -1, pol);
                 __syncwarp();
                 issued = it + 1;
                 if (++s == S) s = 0, ph ^= 1;
@@ -466,7 +672,7 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                     if (global_timer_ns() - t0 > tmo) break;
             }
         __syncwarp();
-    } else if (warp == 9 || warp == 10) {
+    } else if (warp == SW + 1 || warp == SW + 2) {
         // ----------------- products: S from one thread, O from another, so that
         // neither waits behind the other's operands
         if (lane == 0) {
@@ -475,7 +681,7 @@ __global__ void __launch_bounds__(kP8Threads, 1)
             bool ok = true, any = false;
             int s = 0, x = 0;
             uint32_t ph = 0, np[2] = {0, 0};
-            if (warp == 9) {
+            if (warp == SW + 1) {
                 constexpr uint32_t kIdesc = p8_idesc(kP8Tokens, PS::kNs, false, false, false);
                 const uint64_t k_desc = p8_desc(k_s, 16, kAtom, kLayout), q_desc = p8_desc(q_s, 16, kAtom, kLayout);
                 int sg = 0;
@@ -525,7 +731,7 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                 }
             }
             if (any) {
-                const uint32_t bar = fin + 8 * (warp - 9);
+                const uint32_t bar = fin + 8 * (warp - SW - 1);
                 umma_commit(bar);
                 const uint64_t t0 = global_timer_ns();
                 while (!mbar_try_wait(bar, 0))
@@ -536,16 +742,12 @@ __global__ void __launch_bounds__(kP8Threads, 1)
             }
         }
         __syncwarp();
-    } else if (warp == 11) {
+    } else if (warp == SW + 3) {
         // ------------------------------------------------------------ Q rows
-        PagedFp8Split split = {-1, 0, 0, 0};
-        long long at = plan->begin;
-        int sg = 0;
+        const int page_size = 1 << p.page_shift, block = min(page_size, 64);
+        int sg = 0, chunk = 0;
         bool ok = true;
         while (ok && walk.next(lens, seg)) {
-            if (seg.i0 == 0 && seg.i1 < seg.n)
-                split = {seg.entry, seg.g, (int)(((at + seg.n) * plan->ctas - 1) / plan->total), 0};
-            at += seg.i1 - seg.i0;
             const int buf = sg & 1;
             ok = warp_wait(q_empty + 8 * buf, ((sg >> 1) & 1) ^ 1, abort_flag, p.status, tmo);
             if (!ok) break;
@@ -622,8 +824,50 @@ __global__ void __launch_bounds__(kP8Threads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full + 8 * buf);
             ++sg;
+            // Scales of the segment's tiles, a chunk of four at a time: lane
+            // (tile, block); pages two chunks ahead, scales one.
+            const int32_t* table = p.table + (size_t)b * p.max_pages;
+            auto pos_of = [&](int i) {           // this lane's position in the chunk at tile i, -1: none
+                i += lane >> 3;
+                const int pos = i * kP8Tokens + (lane & 7) * block;
+                return i < seg.i1 && (lane & 7) * block < kP8Tokens && pos < T ? pos : -1;
+            };
+            auto page_of = [&](int pos) {
+                const int e = pos >= 0 ? table[pos >> p.page_shift] : -1;
+                return (unsigned)e < (unsigned)p.num_pages ? e : -1;
+            };
+            auto scale_of = [&](int pos, int page, float& ks, float& vs) {
+                ks = vs = 0.f;
+                if (page >= 0) {
+                    const size_t at = ((size_t)page * p.G + seg.g) * p.blocks + ((pos & (page_size - 1)) >> 6);
+                    ks = __ldg(p.k_scale + at);
+                    vs = __ldg(p.v_scale + at);
+                }
+            };
+            float ks, vs;
+            scale_of(pos_of(seg.i0), page_of(pos_of(seg.i0)), ks, vs);
+            int page_next = page_of(pos_of(seg.i0 + kP8ScaleChunk));
+            for (int i = seg.i0; i < seg.i1; i += kP8ScaleChunk, ++chunk) {
+                float ks_next, vs_next;
+                scale_of(pos_of(i + kP8ScaleChunk), page_next, ks_next, vs_next);
+                page_next = page_of(pos_of(i + 2 * kP8ScaleChunk));
+                const int slot = chunk % kP8ScaleChunks;
+                ok = warp_wait(sc_free + 8 * slot, ((chunk / kP8ScaleChunks) & 1) ^ 1, abort_flag, p.status, tmo);
+                if (!ok) break;
+                float* to = scale_ring + (slot * kP8ScaleChunk + (lane >> 3)) * 16 + (lane & 7);
+                to[0] = ks;
+                to[8] = vs;
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(sc_full + 8 * slot);
+                    // Tiles that the segment's last chunk lacks are read by nobody.
+                    for (int k = seg.i1 - i; k < kP8ScaleChunk; ++k)
+                        for (int y = 0; y < PS::kParts; ++y) mbar_arrive(sc_free + 8 * slot);
+                }
+                ks = ks_next;
+                vs = vs_next;
+            }
         }
-        if (lane == 0) p.splits[blockIdx.x] = split;
         // Entries none of whose rows sees a key own no tile: out = 0, lse = -inf.
         for (int e = blockIdx.x; e < p.B * p.row_tiles; e += gridDim.x) {
             if (lens.tiles(e) > 0) continue;
@@ -639,86 +883,77 @@ __global__ void __launch_bounds__(kP8Threads, 1)
         }
     } else {
         // ----------------------------------------- softmax groups, one thread a token
-        const int x = warp >> 2, w4 = warp & 3;
+        // (with 32 rows, one thread a token and half of the rows)
+        const int x = (warp >> 2) & 1, y = warp >> 3, w4 = warp & 3;
+        const int bar = 1 + x + 2 * y;
         const int tok = threadIdx.x & 127;
         const uint32_t lane_base = tmem + ((uint32_t)(w4 * 32) << 16);
-        const uint32_t s_tm = lane_base + PS::kColS + x * PS::kNs;
-        const uint32_t o_tm = lane_base + PS::kColO + x * PS::kNp;
-        const uint32_t p_at = p_s + x * PS::kPBytes + tok * 16;
-        float* const my_ref = neg_ref + x * RP;
-        float2* const factor = factors + x * RP;
-        int* const my_max = warp_max + x * 4 * (RP + 1);
+        const uint32_t s_tm = lane_base + PS::kColS + x * PS::kNs + y * RH;
+        const uint32_t o_tm = lane_base + PS::kColO + x * PS::kNp + y * RH;
+        const uint32_t p_at = p_s + x * PS::kPBytes + tok * 16 + y * 2048;
+        float* const my_ref = neg_ref + x * RP + y * RH;
+        float4* const my_sum = sums + x * RP + y * RH;
+        float2* const factor = factors + x * RP + y * RH;
+        int* const my_max = warp_max + (x * PS::kParts + y) * 4 * (RH + 1);
+        // Row r, column d of the O that group 1 hands over for this part.
+        auto handed_at = [&](int r, int d) -> float* {
+            if constexpr (PS::kParts == 1) return handed + r * D + d;
+            const int i = r * D + d;
+            return handed + ((i >> 9) * 2 + y) * 512 + (i & 511);
+        };
+        const int block_shift = min(p.page_shift, 6);
         uint32_t n_tiles = 0, n_merge = 0;       // phases of s_full and p_full, of m_full
         int it0 = 0, sg = 0;                     // the CTA's tile number at the segment's start
+        int chunk0 = 0;                          // and its chunk of scales
         // The product of this group's tile `it` has completed.
         auto wait_product = [&](int it) { all_wait(v_empty + 8 * (it % SV), it / SV); };
         while (walk.next(lens, seg)) {
             int b, rt;
             lens.split(seg.entry, b, rt);
             const int T = lens.tokens(b);
-            const int32_t* table = p.table + (size_t)b * p.max_pages;
-            const float4* scale4 = reinterpret_cast<const float4*>(row_scale + (sg & 1) * RP);
-            const int* lim = row_lim + (sg & 1) * RP;
+            const float4* scale4 = reinterpret_cast<const float4*>(row_scale + (sg & 1) * RP + y * RH);
+            const int* lim = row_lim + (sg & 1) * RP + y * RH;
             const int lim_min =                                             // every row sees keys up to here
                 p.row_tiles == 1 ? T - p.sq : T - p.sq + (rt * RP) / p.heads_per_group;
             const int first_i = seg.i0 + ((it0 & 1) != x ? 1 : 0);          // this group's first tile
-            auto page_of = [&](int i) {
-                const int pos = i * kP8Tokens + tok;
-                if (i >= seg.i1 || pos >= T) return -1;
-                const int e = table[pos >> p.page_shift];
-                return (unsigned)e < (unsigned)p.num_pages ? e : -1;
-            };
-            auto scales_of = [&](int page, int i, float& ks, float& vs) {
-                ks = vs = 0.f;
-                if (page >= 0) {
-                    const int pos = i * kP8Tokens + tok;
-                    const size_t at = ((size_t)page * p.G + seg.g) * p.blocks + ((pos & ((1 << p.page_shift) - 1)) >> 6);
-                    ks = p.k_scale[at];
-                    vs = p.v_scale[at];
-                }
-            };
-            float ks, vs, l[RP];
+            float l[RH];
             int ev = 0;
 #pragma unroll
-            for (int r = 0; r < RP; ++r) l[r] = 0.f;
-            scales_of(page_of(first_i), first_i, ks, vs);
-            int page_next = page_of(first_i + 2);
+            for (int r = 0; r < RH; ++r) l[r] = 0.f;
             bool first = true;
             // Also keeps a group without a tile here from running ahead.
             all_wait(q_full + 8 * (sg & 1), sg >> 1);
             for (int i = first_i; i < seg.i1; i += 2) {
                 const int it = it0 + i - seg.i0;
                 const int pos = i * kP8Tokens + tok;
-                // The next tile's scales, and the page of the one after it.
-                float ks_next, vs_next;
-                scales_of(page_next, i + 2, ks_next, vs_next);
-                page_next = page_of(i + 4);
                 const bool edge = (i + 1) * kP8Tokens - 1 > lim_min;        // some row does not see all of it
 
                 all_wait(s_full + 8 * x, n_tiles);
                 tc_fence_after();
-                float xs[RP];
+                const int chunk = chunk0 + (i - seg.i0) / kP8ScaleChunk, slot = chunk % kP8ScaleChunks;
+                all_wait(sc_full + 8 * slot, chunk / kP8ScaleChunks);
+                const float* sc = scale_ring + (slot * kP8ScaleChunk + (i - seg.i0) % kP8ScaleChunk) * 16 +
+                                  (tok >> block_shift);
+                const float ks = sc[0];
+                float vs = sc[8];
+                float xs[RH];
                 bool moves = first;
                 {
-                    uint32_t h[RP], lo[RP];
-                    if constexpr (RP == 8) {
+                    uint32_t h[RH], lo[RH];
+                    if constexpr (RH == 8) {
                         uint32_t t[16];
                         tmem_ld16(s_tm, t);
 #pragma unroll
                         for (int r = 0; r < 8; ++r) h[r] = t[r], lo[r] = t[8 + r];
-                    } else if constexpr (RP == 16) {
-                        tmem_ld16(s_tm, h);
-                        tmem_ld16(s_tm + 16, lo);
                     } else {
-                        tmem_ld32(s_tm, h);
-                        tmem_ld32(s_tm + 32, lo);
+                        tmem_ld16x2(s_tm, s_tm + RP, h, lo);
                     }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(s_free + 8 * x);
                     float top = -INFINITY;
 #pragma unroll
-                    for (int r = 0; r < RP; r += 4) {
+                    for (int r = 0; r < RH; r += 4) {
                         const float4 f = scale4[r / 4];
                         const float4 m = *reinterpret_cast<const float4*>(my_ref + r);
                         const float fs[4] = {f.x, f.y, f.z, f.w}, ms[4] = {m.x, m.y, m.z, m.w};
@@ -733,52 +968,53 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                     if (!(fabsf(vs) <= 3.402823466e38f)) vs = __int_as_float(0x7fffffff);
                     moves |= top > kP8Slack || fabsf(vs) * pow2i(-ev) > kP8ScaleSlack;
                 }
-                if (group_any(x, moves)) {
+                const bool any = named_any(bar, moves);
+                if (tok == 0) mbar_arrive(sc_free + 8 * slot);     // every thread has its scales
+                if (any) {
                     // Move the references: rows whose tile maximum is out of range.
                     int mine = 0;
 #pragma unroll
-                    for (int r = 0; r < RP; ++r) {
+                    for (int r = 0; r < RH; ++r) {
                         const int m = __reduce_max_sync(0xffffffffu, ordered(xs[r]));
                         if (lane == r) mine = m;
                     }
                     const uint32_t vb = __float_as_uint(fabsf(vs));
                     const uint32_t vtop = __reduce_max_sync(0xffffffffu, vb <= 0x7f7fffffu ? vb : 0u);
-                    if (lane < RP) my_max[w4 * (RP + 1) + lane] = mine;
-                    if (lane == 0) my_max[w4 * (RP + 1) + RP] = (int)vtop;
-                    const float m_old = first || lane >= RP ? kP8Unseen : -my_ref[lane];
-                    group_sync(x);
+                    if (lane < RH) my_max[w4 * (RH + 1) + lane] = mine;
+                    if (lane == 0) my_max[w4 * (RH + 1) + RH] = (int)vtop;
+                    const float m_old = first || lane >= RH ? kP8Unseen : -my_ref[lane];
+                    named_sync(bar, 128);
                     float m_new = m_old;
-                    if (lane < RP) {
-                        const float m = unordered(max(max(my_max[lane], my_max[RP + 1 + lane]),
-                                                      max(my_max[2 * (RP + 1) + lane], my_max[3 * (RP + 1) + lane])));
+                    if (lane < RH) {
+                        const float m = unordered(max(max(my_max[lane], my_max[RH + 1 + lane]),
+                                                      max(my_max[2 * (RH + 1) + lane], my_max[3 * (RH + 1) + lane])));
                         if (m > m_old + kP8Slack) m_new = m;
                     }
-                    const int vm = max(max(my_max[RP], my_max[2 * RP + 1]), max(my_max[3 * RP + 2], my_max[4 * RP + 3]));
+                    const int vm = max(max(my_max[RH], my_max[2 * RH + 1]), max(my_max[3 * RH + 2], my_max[4 * RH + 3]));
                     // 2^-ev brings the largest scale to [0.5, 1).
                     const int ev_top = min(max((vm >> 23) - 126, -60), 126);
                     const int ev_new = first || __int_as_float(vm) * pow2i(-ev) > kP8ScaleSlack ? ev_top : ev;
                     const float alpha = fast_exp2(m_old - m_new);
                     const float alpha_o = first ? 0.f : alpha * pow2i(max(ev - ev_new, -126));
-                    if (w4 == 0 && lane < RP) my_ref[lane] = -m_new;
+                    if (w4 == 0 && lane < RH) my_ref[lane] = -m_new;
                     ev = ev_new;
 #pragma unroll
-                    for (int r = 0; r < RP; ++r) l[r] *= __shfl_sync(0xffffffffu, alpha, r);
+                    for (int r = 0; r < RH; ++r) l[r] *= __shfl_sync(0xffffffffu, alpha, r);
                     if (!first) {
                         wait_product(it - 2);     // and so every product of this group so far
                         tc_fence_after();
+#pragma unroll 1
+                        for (int t = 0; t < kP8Terms; ++t) {
+                            uint32_t o[RH];
+                            tmem_ld_rows<RH>(o_tm + t * RP, o);
 #pragma unroll
-                        for (int c = 0; c < PS::kNp / 16; ++c) {
-                            uint32_t o[16];
-                            tmem_ld16(o_tm + 16 * c, o);
-#pragma unroll
-                            for (int k = 0; k < 16; ++k)
-                                o[k] = __float_as_uint(__uint_as_float(o[k]) *
-                                                       __shfl_sync(0xffffffffu, alpha_o, (16 * c + k) % RP));
-                            tmem_st16(o_tm + 16 * c, o);
+                            for (int k = 0; k < RH; ++k)
+                                o[k] = __float_as_uint(__uint_as_float(o[k]) * __shfl_sync(0xffffffffu, alpha_o, k));
+                            tmem_st_rows<RH>(o_tm + t * RP, o);
                         }
                         tmem_st_wait();
                     }
-                    group_sync(x);
+                    named_sync(bar, 128);
                 }
                 if (edge) {
                     // Rows of V past the length may hold anything: zero them. A
@@ -787,33 +1023,32 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                     // see it are made NaN through P.
                     const int s = it % SV;
                     all_wait(v_full + 8 * s, it / SV);
-                    if (pos > lim_min) {
-                        const uint32_t at = v_s + s * TB + tok * D;
-                        bool clear = pos >= T;
-                        if (!clear) {
-                            uint32_t nan = 0;
+                    const uint32_t at = v_s + s * TB + tok * D;
+                    bool clear = pos >= T;
+                    if (pos > lim_min && !clear) {
+                        uint32_t nan = 0;
 #pragma unroll
-                            for (int c = 0; c < D / 16; ++c) {
-                                uint32_t u[4];
-                                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                             : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
-                                             : "r"(at + 16 * c));
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t u[4];
+                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+                                         : "r"(at + 16 * c));
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)   // a byte with its low seven bits set
-                                    nan |= ((u[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                            }
-                            clear = nan != 0;
-                            if (clear) vs = __int_as_float(0x7fffffff);
+                            for (int k = 0; k < 4; ++k)   // a byte with its low seven bits set
+                                nan |= ((u[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
                         }
-                        if (clear)
-#pragma unroll
-                            for (int c = 0; c < D / 16; ++c) st_shared_zero16(at + 16 * c);
+                        clear = nan != 0;
+                        if (clear) vs = __int_as_float(0x7fffffff);
                     }
+                    if constexpr (PS::kParts > 1) named_sync(5 + x, 256);   // both parts have looked
+                    if (clear && y == 0)
+#pragma unroll
+                        for (int c = 0; c < D / 16; ++c) st_shared_zero16(at + 16 * c);
                 }
                 const float vw = vs * pow2i(-ev) * kP8ProbScale;
-                uint32_t packed[RP / 4][kP8Terms];       // a term of four rows
+                uint32_t packed[RH / 4][kP8Terms];       // a term of four rows
 #pragma unroll
-                for (int r = 0; r < RP; r += 4) {
+                for (int r = 0; r < RH; r += 4) {
                     const float4 m = *reinterpret_cast<const float4*>(my_ref + r);
                     const float ms[4] = {m.x, m.y, m.z, m.w};
                     float w[4];
@@ -836,19 +1071,16 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                 }
                 // P's operand is free once the group's previous product is done.
                 if (it >= 2) wait_product(it - 2);
-                if (x == 1 && first) all_wait(m_empty, n_merge + 1);      // and handed-over O is read
-                // Column term * RP + r; 16 columns of a token are 16 bytes.
+                if (x == 1 && first) all_wait(m_empty + 8 * y, n_merge + 1);      // and handed-over O is read
+                // Column term * RP + row; 16 columns of a token are 16 bytes.
+                if constexpr (RH == 8) {
+                    st_shared_v4(p_at, make_uint4(packed[0][0], packed[1][0], packed[0][1], packed[1][1]));
+                    st_shared_v4(p_at + 2048, make_uint4(packed[0][2], packed[1][2], packed[0][3], packed[1][3]));
+                } else {
 #pragma unroll
-                for (int c = 0; c < PS::kNp / 16; ++c) {
-                    uint4 v;
-                    if constexpr (RP == 8)
-                        v = make_uint4(packed[0][2 * c], packed[1][2 * c], packed[0][2 * c + 1], packed[1][2 * c + 1]);
-                    else {
-                        constexpr int kHalf = RP / 16;
-                        const int t = c / kHalf, q = (c % kHalf) * 4;
-                        v = make_uint4(packed[q][t], packed[q + 1][t], packed[q + 2][t], packed[q + 3][t]);
-                    }
-                    st_shared_v4(p_at + c * 2048, v);
+                    for (int t = 0; t < kP8Terms; ++t)
+                        st_shared_v4(p_at + t * (RP / 16) * 2048,
+                                     make_uint4(packed[0][t], packed[1][t], packed[2][t], packed[3][t]));
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -856,8 +1088,6 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                 if (lane == 0) mbar_arrive(p_full + 8 * x);
                 ++n_tiles;
                 first = false;
-                ks = ks_next;
-                vs = vs_next;
             }
 
             // ------------------------------------------------ end of a segment
@@ -865,22 +1095,22 @@ __global__ void __launch_bounds__(kP8Threads, 1)
             const int cnt0 = (len + ((it0 & 1) == 0 ? 1 : 0)) / 2, cnt1 = len - cnt0;
             const bool both = cnt0 > 0 && cnt1 > 0;
             if ((x ? cnt1 : cnt0) > 0) {
-                const float sum = reduce_rows<RP>(l, lane);
-                if (lane < RP) reinterpret_cast<float*>(sums + x * RP + lane)[w4] = sum;
-                group_sync(x);
+                const float sum = reduce_rows<RH>(l, lane);
+                if (lane < RH) reinterpret_cast<float*>(my_sum + lane)[w4] = sum;
+                named_sync(bar, 128);
                 // This group's last tile is the segment's last or the one before.
                 const int last = it0 + len - 1;
                 wait_product((last & 1) == x ? last : last - 1);
                 tc_fence_after();
-                float o[RP];
+                float o[RH];
 #pragma unroll
-                for (int r = 0; r < RP; ++r) o[r] = 0.f;
+                for (int r = 0; r < RH; ++r) o[r] = 0.f;
 #pragma unroll
-                for (int c = 0; c < PS::kNp / 16; ++c) {
-                    uint32_t t[16];
-                    tmem_ld16(o_tm + 16 * c, t);
+                for (int t = 0; t < kP8Terms; ++t) {
+                    uint32_t u[RH];
+                    tmem_ld_rows<RH>(o_tm + t * RP, u);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) o[(16 * c + k) % RP] += __uint_as_float(t[k]);
+                    for (int r = 0; r < RH; ++r) o[r] += __uint_as_float(u[r]);
                 }
                 tc_fence_before();
                 // D = 64 products keep 16 of their rows in each warp's 32 lanes.
@@ -889,25 +1119,26 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                 const float unit = pow2i(ev) * (1.f / kP8ProbScale);
                 if (both && x == 1) {
 #pragma unroll
-                    for (int r = 0; r < RP; ++r)
-                        if (mine) stage_o[r * D + dim] = o[r] * unit;
-                    if (tok < RP) {
-                        const float4 q = sums[x * RP + tok];
-                        other[tok] = make_float2(-my_ref[tok], q.x + q.y + q.z + q.w);
+                    for (int r = 0; r < RH; ++r)
+                        if (mine) *handed_at(r, dim) = o[r] * unit;
+                    if (tok < RH) {
+                        const float4 q = my_sum[tok];
+                        other[y * RH + tok] = make_float2(-my_ref[tok], q.x + q.y + q.z + q.w);
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(m_full);
+                    if (lane == 0) mbar_arrive(m_full + 8 * y);
                     ++n_merge;
                 } else {
-                    if (both) all_wait(m_full, n_merge);
+                    if (both) all_wait(m_full + 8 * y, n_merge);
                     const bool whole = seg.i0 == 0 && seg.i1 == seg.n;
-                    float* slot = p.part + ((size_t)blockIdx.x * 2 + (seg.i0 == 0 ? 1 : 0)) * p8_slot_floats(RP, D);
-                    const int* rows_out = row_out + (sg & 1) * RP;
-                    if (tok < RP) {
-                        const float4 q = sums[x * RP + tok];
+                    const size_t slot_floats = p8_slot_floats(RP, D);
+                    float* slot = p.part + ((size_t)blockIdx.x * 2 + (seg.i0 == 0 ? 1 : 0)) * slot_floats;
+                    const int* rows_out = row_out + (sg & 1) * RP + y * RH;
+                    if (tok < RH) {
+                        const float4 q = my_sum[tok];
                         float m = -my_ref[tok], ls = q.x + q.y + q.z + q.w, a0 = 1.f, a1 = 0.f;
                         if (both) {
-                            const float2 u = other[tok];
+                            const float2 u = other[y * RH + tok];
                             const float top = fmaxf(m, u.x);
                             a0 = fast_exp2(m - top);
                             a1 = fast_exp2(u.x - top);
@@ -922,96 +1153,58 @@ __global__ void __launch_bounds__(kP8Threads, 1)
                             if (p.lse && rows_out[tok] >= 0)
                                 p.lse[rows_out[tok]] = some ? (m + log2f(ls)) * 0.6931471805599453f : -INFINITY;
                         } else {
-                            slot[RP * D + tok] = m;
-                            slot[RP * D + RP + tok] = ls;
+                            slot[RP * D + y * RH + tok] = m;
+                            slot[RP * D + RP + y * RH + tok] = ls;
                         }
                         factor[tok] = make_float2(a0 * unit, a1);
                     }
-                    group_sync(x);
+                    named_sync(bar, 128);
 #pragma unroll
-                    for (int r = 0; r < RP; ++r) {
+                    for (int r = 0; r < RH; ++r) {
                         const float2 f = factor[r];
-                        float y = o[r] * f.x;
-                        if (both && mine) y = fmaf(stage_o[r * D + dim], f.y, y);
+                        float v = o[r] * f.x;
+                        if (both && mine) v = fmaf(*handed_at(r, dim), f.y, v);
                         if (!mine) continue;
                         if (!whole)
-                            slot[r * D + dim] = y;
+                            slot[(y * RH + r) * D + dim] = v;
                         else if (rows_out[r] >= 0)
-                            p.out[(size_t)rows_out[r] * D + dim] = (uint16_t)(pack_bf16x2(y, 0.f) & 0xffffu);
+                            p.out[(size_t)rows_out[r] * D + dim] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xffffu);
                     }
                     if (both) {
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(m_empty);
+                        if (lane == 0) mbar_arrive(m_empty + 8 * y);
                         ++n_merge;
+                    }
+                    if (!whole) {
+                        // The last of the unit's CTAs to arrive merges it:
+                        //   M = max m_c, L = sum l_c 2^(m_c - M), O = sum O_c 2^(m_c - M) / L.
+                        const long long unit0 = plan.begin + it0 - seg.i0;
+                        const int c0 = plan.owner(unit0), n = plan.owner(unit0 + seg.n - 1) - c0 + 1;
+                        __threadfence();
+                        named_sync(bar, 128);
+                        if (tok == 0)
+                            last_flag[bar - 1] = arrive_last(p.counters + (size_t)c0 * PS::kParts + y, p.tag, n);
+                        named_sync(bar, 128);
+                        if (last_flag[bar - 1]) {
+                            __threadfence();
+                            p8_merge<D, RP, RH>(p, c0, n, y * RH, w4, lane, rows_out);
+                        }
                     }
                 }
                 // The sums and references are read before the next segment writes them.
-                group_sync(x);
+                named_sync(bar, 128);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(q_empty + 8 * (sg & 1));
             it0 += len;
+            chunk0 += (len + kP8ScaleChunk - 1) / kP8ScaleChunk;
             ++sg;
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 9) tmem_dealloc(tmem, PS::kTmemCols);
-}
-
-// Merges the partial results of the units that cross CTAs: one warp per row of
-// the unit that CTA blockIdx.x began,
-//     M = max m_c, L = sum l_c 2^(m_c - M), O = sum O_c 2^(m_c - M) / L.
-template <int D, int RP>
-__global__ void __launch_bounds__(128) gqa_paged_fp8_merge(const PagedFp8Params p) {
-    pdl_launch_dependents();
-    pdl_wait_primary();
-    const PagedFp8Split s = p.splits[blockIdx.x];
-    if (s.entry < 0) return;
-    const int lane = threadIdx.x & 31, r = blockIdx.y * 4 + (threadIdx.x >> 5);
-    const int b = s.entry / p.row_tiles, rt = s.entry - b * p.row_tiles;
-    int tok;
-    const int orow = p8_out_row<RP>(p, b, rt, s.g, r, &tok);
-    if (orow < 0) return;
-    const int c0 = blockIdx.x, n = s.last_cta - c0 + 1;
-    const size_t slot = p8_slot_floats(RP, D);
-    // The first contributor's second slot, then every other's first.
-    auto at = [&](int i) { return p.part + ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * slot; };
-    float top = kP8Unseen;
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, at(i)[RP * D + r]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    float l = 0.f;
-    for (int i = lane; i < n; i += 32) l += at(i)[RP * D + RP + r] * fast_exp2(at(i)[RP * D + r] - top);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    constexpr int kPer = D / 32;
-    float y[kPer];
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) y[k] = 0.f;
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-        const float* src = at(i);
-        const float a = fast_exp2(src[RP * D + r] - top);
-        if constexpr (kPer == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(src + r * D + lane * 4);
-            y[0] = fmaf(v.x, a, y[0]);
-            y[1] = fmaf(v.y, a, y[1]);
-            y[2] = fmaf(v.z, a, y[2]);
-            y[3] = fmaf(v.w, a, y[3]);
-        } else {
-            const float2 v = *reinterpret_cast<const float2*>(src + r * D + lane * 2);
-            y[0] = fmaf(v.x, a, y[0]);
-            y[1] = fmaf(v.y, a, y[1]);
-        }
-    }
-    const bool some = l > 0.f || l != l;
-    const float inv = some ? 1.f / l : 0.f;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (size_t)orow * D + lane * kPer);
-#pragma unroll
-    for (int k = 0; k < kPer / 2; ++k) dst[k] = pack_bf16x2(some ? y[2 * k] * inv : 0.f, some ? y[2 * k + 1] * inv : 0.f);
-    if (p.lse && lane == 0) p.lse[orow] = some ? (top + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    if (warp == SW + 1) tmem_dealloc(tmem, PS::kTmemCols);
 }
 
 template <int D, int RP>
@@ -1034,17 +1227,12 @@ cudaError_t launch_paged_fp8(const PagedFp8Launch& a) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.grid);
-    cfg.blockDim = dim3(kP8Threads);
+    cfg.blockDim = dim3(PS::kThreads);
     cfg.dynamicSmemBytes = PS::kSmemBytes;
     cfg.stream = a.stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, gqa_paged_fp8_kernel<D, RP>, a.tm_k, a.tm_v, a.p);
-    if (e != cudaSuccess || a.grid == 1) return e;
-    cfg.gridDim = dim3(a.grid, RP / 4);
-    cfg.blockDim = dim3(128);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, gqa_paged_fp8_merge<D, RP>, a.p);
+    return cudaLaunchKernelEx(&cfg, gqa_paged_fp8_kernel<D, RP>, a.tm_k, a.tm_v, a.p);
 }
 
 template <int D>

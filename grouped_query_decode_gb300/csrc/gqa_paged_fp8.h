@@ -13,14 +13,6 @@ constexpr int kP8Tokens = 128;     // tokens per tile: one per thread of a softm
 constexpr int kP8MinTiles = 2;     // fewest tiles worth a CTA
 constexpr int kP8MaxRows = 32;     // query rows of a unit; more are further units
 
-// One split unit: the CTA whose share starts it, recorded for the merge.
-struct PagedFp8Split {
-    int entry;     // b * row_tiles + row tile, or -1
-    int g;
-    int last_cta;  // CTAs [this one, last_cta] hold its partial results
-    int pad;
-};
-
 struct PagedFp8Params {
     const uint16_t* q;         // [B, sq, H, D] bf16
     const float* k_scale;      // [num_pages, G, blocks]
@@ -29,13 +21,15 @@ struct PagedFp8Params {
     const int32_t* lens;       // [B]
     uint16_t* out;             // [B, sq, H, D] bf16
     float* lse;                // [B, sq, H] or nullptr
-    PagedFp8Split* splits;     // [grid]
+    unsigned long long* counters;   // [grid][2]: arrivals of the unit that a CTA's share starts
+    unsigned long long tag;    // of this call, in the counters (48 bits)
     float* part;               // [grid][2][slot]: O[rows][D], m[rows], l[rows]
     unsigned* status;
     unsigned long long wait_timeout_ns;
     float scale_log2;
     int B, sq, H, G, R, heads_per_group, row_tiles;
     int page_shift, num_pages, max_pages, blocks;
+    int small_plan;            // one row tile, up to 128 sequences, 32-bit tile arithmetic
     int skip_tile;             // fault injection for tests (-1: off)
 };
 

@@ -32,10 +32,10 @@ int paged_fp8_grid(int B, int G, int R, int page_size, int max_pages, int sms) {
     return (int)(want < 1 ? 1 : want < sms ? want : sms);
 }
 
-size_t split_bytes(int grid) { return (sizeof(PagedFp8Split) * (size_t)grid + 255) & ~size_t(255); }
+size_t counter_bytes(int grid) { return (sizeof(unsigned long long) * 2 * (size_t)grid + 255) & ~size_t(255); }
 
 size_t paged_fp8_ws_bytes(int grid, int R, int D) {
-    return split_bytes(grid) + sizeof(float) * 2 * (size_t)grid * p8_slot_floats(p8_rows(R), D);
+    return counter_bytes(grid) + sizeof(float) * 2 * (size_t)grid * p8_slot_floats(p8_rows(R), D);
 }
 
 }  // namespace
@@ -92,8 +92,9 @@ int gqa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages
     p.lens = seq_lens;
     p.out = static_cast<uint16_t*>(out);
     p.lse = lse;
-    p.splits = static_cast<PagedFp8Split*>(workspace);
-    p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + split_bytes(grid));
+    p.counters = static_cast<unsigned long long*>(workspace);
+    p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + counter_bytes(grid));
+    p.tag = call_tag();
     p.status = status;
     wait_knobs(&p.wait_timeout_ns, &p.skip_tile);
     p.scale_log2 = scale * 1.4426950408889634f;
@@ -108,6 +109,8 @@ int gqa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages
     p.num_pages = num_pages;
     p.max_pages = max_pages_per_seq;
     p.blocks = (page_size + 63) / 64;
+    const long long tiles = ((long long)max_pages_per_seq * page_size + kP8Tokens - 1) / kP8Tokens;
+    p.small_plan = p.row_tiles == 1 && B <= 128 && (long long)B * G * tiles * (grid + 1) < (1ll << 32);
     a.grid = grid;
     a.stream = stream;
     const cudaError_t e = D == 64 ? launch_paged_fp8_d64(a) : launch_paged_fp8_d128(a);
