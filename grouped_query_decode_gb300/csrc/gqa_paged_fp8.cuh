@@ -29,11 +29,12 @@
 // (one per SM). A unit that crosses CTAs leaves (O, m, l) per CTA in the
 // workspace; the CTA that arrives last merges them. Per CTA: two groups of four
 // softmax warps (with 32 rows two such pairs, 16 rows each) take alternate
-// tiles, a warp brings K and V (a TMA box per page, in the swizzle of the
-// operand layout), two threads issue the products, a warp splits Q and fetches
-// the blocks' scales up to 16 tiles ahead (behind a saturated HBM a lookup of
-// page and scale takes longer than a tile). Every wait is bounded, as in the
-// other kernels.
+// tiles. One warp brings K, another V (a TMA box per page, in the swizzle of
+// the operand layout; one warp issues a box in 65 cycles, two warps two), the
+// latter also splits Q and fetches the blocks' scales, ahead of V by a chunk of
+// tiles (behind a saturated HBM a lookup of page and scale takes longer than a
+// tile). Two warps issue the products. Every wait is bounded, as in the other
+// kernels.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -48,7 +49,7 @@ namespace gqa {
 
 constexpr int kP8LenCopy = 384;           // sequences whose lengths a CTA keeps
 constexpr int kP8ScaleChunk = 4;          // tiles whose scales are fetched together,
-constexpr int kP8ScaleChunks = 4;         // and how many such chunks a CTA keeps
+constexpr int kP8ScaleChunks = 8;         // and how many such chunks a CTA keeps
 constexpr int kP8SmallEntries = 128;      // entries that each warp plans by itself
 constexpr int kP8Terms = 4;               // e5m2 columns per probability
 constexpr float kP8Slack = 4.0f;          // p <= 2^4 before the reference moves
@@ -71,7 +72,7 @@ struct P8Shape {
     // copy to P V, a K tile only to S, so V gets more stages.
     static constexpr int kStagesK = (D == 128 ? 1 : 2) * (RP == 32 ? 4 : 5);
     static constexpr int kStagesV = (D == 128 ? 1 : 2) * (RP == 32 ? 5 : 7);
-    static constexpr int kBars = 2 * (kStagesK + kStagesV) + 24;
+    static constexpr int kBars = 2 * (kStagesK + kStagesV) + 16 + kP8ScaleChunks;
     static constexpr int kRowInfoBytes = 2 * 3 * RP * 4;
     static constexpr int kRefBytes = 2 * RP * 4;
     static constexpr int kWarpMaxBytes = 2 * kParts * 4 * (kRows + 1) * 4;
@@ -114,6 +115,17 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+
+// True in one thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
 }
 
 // 16 fp32 columns of this thread's TMEM lane, waited on; and their store.
@@ -289,7 +301,14 @@ __device__ __forceinline__ P8Plan p8_small_plan(const P8Lens<RP>& lens, int* len
     }
     const unsigned total = __shfl_sync(0xffffffffu, x, 31), before = x - mine;
     const unsigned most = total / kP8MinTiles;
-    const unsigned ctas = most < 1 ? 1 : most < gridDim.x ? most : gridDim.x;
+    unsigned ctas = most < 1 ? 1 : most < gridDim.x ? most : gridDim.x;
+    // Equal lengths: the host's grid that no unit crosses unevenly.
+    unsigned lo = 0xffffffffu, hi = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (lane * 4 + k < p.B) lo = min(lo, n[k]), hi = max(hi, n[k]);
+    if (__reduce_min_sync(0xffffffffu, lo) == __reduce_max_sync(0xffffffffu, hi) && (unsigned)p.even_ctas <= most)
+        ctas = (unsigned)p.even_ctas;
     const unsigned c = blockIdx.x;
     const unsigned t0 = c < ctas ? total * c / ctas : total, t1 = c < ctas ? total * (c + 1) / ctas : total;
     // The lane whose entries hold tile t0, and where in them it lies.
@@ -407,56 +426,74 @@ __device__ __forceinline__ int p8_out_row(const PagedFp8Params& p, int b, int rt
 }
 
 // One group's merge of rows [r0, r0 + RH) of a unit that n CTAs from c0 on hold
-// parts of: a warp per row. The first CTA's part is in its second slot, every
-// other's in its first.
+// parts of; the first CTA's part is in its second slot, every other's in its
+// first. A thread merges four columns of some rows, several parts at a time, all
+// of their loads under way at once.
 template <int D, int RP, int RH>
-__device__ __noinline__ void p8_merge(const PagedFp8Params& p, int c0, int n, int r0, int w4, int lane,
-                                      const int* rows_out) {
-    constexpr int kPer = D / 32;
+__device__ __noinline__ void p8_merge(const PagedFp8Params& p, int c0, int n, int r0, int tok, const int* rows_out) {
+    constexpr int kItems = RH * D / 4 / 128;      // 1 to 4
+    constexpr int kAtOnce = kItems > 2 ? 2 : 4;
     const size_t slot = p8_slot_floats(RP, D);
     auto at = [&](int i) { return p.part + ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * slot; };
-    for (int k = w4; k < RH; k += 4) {
-        const int orow = rows_out[k], r = r0 + k;
-        if (orow < 0) continue;
-        float top = kP8Unseen;
-        for (int i = lane; i < n; i += 32) top = fmaxf(top, __ldcg(at(i) + RP * D + r));
+    float top[kItems], l[kItems], y[kItems][4];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        float l = 0.f, y[kPer];
+    for (int j = 0; j < kItems; ++j) {
+        top[j] = kP8Unseen;
+        l[j] = y[j][0] = y[j][1] = y[j][2] = y[j][3] = 0.f;
+    }
+    for (int i0 = 0; i0 < n; i0 += kAtOnce) {
+        float m[kItems][kAtOnce], s[kItems][kAtOnce];
+        float4 v[kItems][kAtOnce];
 #pragma unroll
-        for (int c = 0; c < kPer; ++c) y[c] = 0.f;
-        for (int i0 = 0; i0 < n; i0 += 32) {
-            float a = 0.f;
-            if (i0 + lane < n) {
-                a = fast_exp2(__ldcg(at(i0 + lane) + RP * D + r) - top);
-                l += __ldcg(at(i0 + lane) + RP * D + RP + r) * a;
-            }
-#pragma unroll 8
-            for (int i = 0; i < min(32, n - i0); ++i) {
-                const float w = __shfl_sync(0xffffffffu, a, i);
-                const float* src = at(i0 + i) + r * D + lane * kPer;
-                if constexpr (kPer == 4) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-                    y[0] = fmaf(v.x, w, y[0]);
-                    y[1] = fmaf(v.y, w, y[1]);
-                    y[2] = fmaf(v.z, w, y[2]);
-                    y[3] = fmaf(v.w, w, y[3]);
-                } else {
-                    const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-                    y[0] = fmaf(v.x, w, y[0]);
-                    y[1] = fmaf(v.y, w, y[1]);
+        for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+            for (int j = 0; j < kItems; ++j) {
+                const int item = j * 128 + tok, r = r0 + item / (D / 4), d = item % (D / 4) * 4;
+                m[j][k] = kP8Unseen;
+                s[j][k] = 0.f;
+                v[j][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i0 + k < n) {
+                    const float* part = at(i0 + k);
+                    m[j][k] = __ldcg(part + RP * D + r);
+                    s[j][k] = __ldcg(part + RP * D + RP + r);
+                    v[j][k] = __ldcg(reinterpret_cast<const float4*>(part + r * D + d));
                 }
             }
+#pragma unroll
+        for (int j = 0; j < kItems; ++j) {
+            float t = top[j];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) t = fmaxf(t, m[j][k]);
+            const float a = fast_exp2(top[j] - t);
+            top[j] = t;
+            l[j] *= a;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) y[j][c] *= a;
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                if (i0 + k >= n) continue;
+                const float w = fast_exp2(m[j][k] - t);
+                l[j] = fmaf(s[j][k], w, l[j]);
+                y[j][0] = fmaf(v[j][k].x, w, y[j][0]);
+                y[j][1] = fmaf(v[j][k].y, w, y[j][1]);
+                y[j][2] = fmaf(v[j][k].z, w, y[j][2]);
+                y[j][3] = fmaf(v[j][k].w, w, y[j][3]);
+            }
         }
+    }
 #pragma unroll
-        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        const bool some = l > 0.f || l != l;
-        const float inv = some ? 1.f / l : 0.f;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (size_t)orow * D + lane * kPer);
-#pragma unroll
-        for (int c = 0; c < kPer / 2; ++c)
-            dst[c] = pack_bf16x2(some ? y[2 * c] * inv : 0.f, some ? y[2 * c + 1] * inv : 0.f);
-        if (p.lse && lane == 0) p.lse[orow] = some ? (top + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    for (int j = 0; j < kItems; ++j) {
+        const int item = j * 128 + tok, d = item % (D / 4) * 4, orow = rows_out[item / (D / 4)];
+        if (orow < 0) continue;
+        const bool some = l[j] > 0.f || l[j] != l[j];
+        const float inv = 1.f / l[j];
+        uint2 o = make_uint2(0, 0);
+        if (some) {
+            o.x = pack_bf16x2(y[j][0] * inv, y[j][1] * inv);
+            o.y = pack_bf16x2(y[j][2] * inv, y[j][3] * inv);
+        }
+        *reinterpret_cast<uint2*>(p.out + (size_t)orow * D + d) = o;
+        if (p.lse && d == 0) p.lse[orow] = some ? (top[j] + log2f(l[j])) * 0.6931471805599453f : -INFINITY;
     }
 }
 
@@ -552,7 +589,7 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
     const uint32_t q_full = v_empty + 8 * SV, q_empty = q_full + 16;
     const uint32_t s_full = q_empty + 16, s_free = s_full + 16, p_full = s_free + 16;
     const uint32_t m_full = p_full + 16, m_empty = m_full + 16, fin = m_empty + 16;
-    const uint32_t sc_full = fin + 16, sc_free = sc_full + 8 * kP8ScaleChunks;
+    const uint32_t sc_full = fin + 16;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t tmo = p.wait_timeout_ns;
@@ -577,10 +614,7 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
             mbar_init(m_full + 8 * x, 4);
             mbar_init(m_empty + 8 * x, 4);
         }
-        for (int c = 0; c < kP8ScaleChunks; ++c) {
-            mbar_init(sc_full + 8 * c, 1);
-            mbar_init(sc_free + 8 * c, kP8ScaleChunk * PS::kParts);
-        }
+        for (int c = 0; c < kP8ScaleChunks; ++c) mbar_init(sc_full + 8 * c, 1);
         *abort_flag = 0;
         fence_barrier_init();
     }
@@ -613,147 +647,202 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
         __syncwarp();
     };
 
-    if (warp == SW) {
-        // ------------------------------------- loader: lanes 0-7 K, lanes 8-15 V
-        const bool is_v = lane >= 8;
-        const int sub = lane & 7;
-        const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
-        const uint32_t full = is_v ? v_full : k_full, empty = is_v ? v_empty : k_empty;
-        const uint32_t ring = is_v ? v_s : k_s;
-        const int S = is_v ? SV : SK;
-        const int page_size = 1 << p.page_shift;
+    // One ring's copies of a segment's tiles, a lane per page; every lane of the
+    // calling warp takes part. `between` runs before each tile.
+    const int page_size = 1 << p.page_shift;
+    auto load_tiles = [&](const P8Segment& seg, int b, int T, const CUtensorMap* tm, uint32_t ring, int S, uint32_t full,
+                          uint32_t empty, int skip_tile, uint64_t pol, int& it, int& s, uint32_t& ph, auto between) {
         const int box = min(page_size, kP8Tokens);              // rows of a copy
         const int boxes = kP8Tokens / box;
-        const uint64_t pol = l2_policy_evict_first();
-        int it = 0, issued = 0, s = 0;
-        uint32_t ph = 1;
-        bool ok = true;
-        while (ok && walk.next(lens, seg)) {
-            int b, rt;
-            lens.split(seg.entry, b, rt);
-            const int T = lens.tokens(b);
-            const int32_t* row = p.table + (size_t)b * p.max_pages;
-            // The table is read 32 entries at a time, a lane each, and the
-            // next 32 are on their way.
-            int first = (seg.i0 * kP8Tokens) >> p.page_shift;
-            const int last = (min(T, seg.i1 * kP8Tokens) - 1) >> p.page_shift;
-            auto entries = [&](int e) { return e + lane <= last ? row[e + lane] : -1; };
-            int cur = entries(first), nxt = entries(first + 32);
-            for (int i = seg.i0; i < seg.i1; ++i, ++it) {
-                if (((i * kP8Tokens) >> p.page_shift) - first >= 32) {
-                    first += 32;
-                    cur = nxt;
-                    nxt = entries(first + 32);
-                }
-                const int pos = i * kP8Tokens + sub * box;
-                const int page = __shfl_sync(0xffffffffu, cur, ((pos >> p.page_shift) - first) & 31);
-                const int here = min(boxes, (T - i * kP8Tokens + box - 1) / box);   // boxes that hold keys
-                // Every lane waits for its own ring's stage.
-                ok = __all_sync(0xffffffffu, wait(empty + 8 * s, ph));
-                if (!ok) break;
-                const bool skip = blockIdx.x == 0 && it == p.skip_tile && !is_v;    // injected fault: never loaded
-                if (sub == 0 && lane < 16 && !skip) mbar_arrive_expect_tx(full + 8 * s, here * box * D);
-                __syncwarp();
-                if (lane < 16 && sub < here && !skip)
-                    // A page outside the pool is a slab out of range: zeros.
-                    tma_load_3d_hint(ring + s * TB + sub * box * D, tm, full + 8 * s, 0, pos & (page_size - 1),
-                                     (unsigned)page < (unsigned)p.num_pages ? page * p.G + seg.g : -1, pol);
-                __syncwarp();
-                issued = it + 1;
-                if (++s == S) s = 0, ph ^= 1;
+        const int32_t* row = p.table + (size_t)b * p.max_pages;
+        // The table is read 32 entries at a time, a lane each, and the next 32
+        // are on their way.
+        int first = (seg.i0 * kP8Tokens) >> p.page_shift;
+        const int last = (min(T, seg.i1 * kP8Tokens) - 1) >> p.page_shift;
+        auto entries = [&](int e) { return e + lane <= last ? row[e + lane] : -1; };
+        int cur = entries(first), nxt = entries(first + 32);
+        for (int i = seg.i0; i < seg.i1; ++i, ++it) {
+            if (((i * kP8Tokens) >> p.page_shift) - first >= 32) {
+                first += 32;
+                cur = nxt;
+                nxt = entries(first + 32);
             }
+            between(i);
+            const int pos = i * kP8Tokens + lane * box;
+            const int page = __shfl_sync(0xffffffffu, cur, ((pos >> p.page_shift) - first) & 31);
+            const int here = min(boxes, (T - i * kP8Tokens + box - 1) / box);   // boxes that hold keys
+            if (!warp_wait(empty + 8 * s, ph, abort_flag, p.status, tmo)) return false;
+            if (it != skip_tile) {
+                if (lane == 0) mbar_arrive_expect_tx(full + 8 * s, here * box * D);
+                __syncwarp();
+                if (lane < here)
+                    // A page outside the pool is a slab out of range: zeros.
+                    tma_load_3d_hint(ring + s * TB + lane * box * D, tm, full + 8 * s, 0, pos & (page_size - 1),
+                                     (unsigned)page < (unsigned)p.num_pages ? page * p.G + seg.g : -1, pol);
+            }
+            __syncwarp();
+            if (++s == S) s = 0, ph ^= 1;
         }
-        // Leave only once the last copies have landed.
-        if (lane == 0 || lane == 8)
+        return true;
+    };
+    // A loader leaves only once its last copies have landed.
+    auto drain = [&](uint32_t full, int S, int issued, int skip_tile) {
+        if (lane == 0)
             for (int j = issued > S ? issued - S : 0; j < issued; ++j) {
-                if (!is_v && blockIdx.x == 0 && j == p.skip_tile) continue;
+                if (j == skip_tile) continue;
                 const uint64_t t0 = global_timer_ns();
                 while (!mbar_try_wait(full + 8 * (j % S), (j / S) & 1))
                     if (global_timer_ns() - t0 > tmo) break;
             }
         __syncwarp();
+    };
+
+    if (warp == SW) {
+        // ---------------------------------------------------------- K loader
+        const int skip_tile = blockIdx.x == 0 ? p.skip_tile : -1;      // injected fault: never loaded
+        const uint64_t pol = l2_policy_evict_first();
+        int it = 0, s = 0;
+        uint32_t ph = 1;
+        bool ok = true;
+        while (ok && walk.next(lens, seg)) {
+            int b, rt;
+            lens.split(seg.entry, b, rt);
+            ok = load_tiles(seg, b, lens.tokens(b), &tm_k, k_s, SK, k_full, k_empty, skip_tile, pol, it, s, ph,
+                            [](int) {});
+        }
+        drain(k_full, SK, it, skip_tile);
     } else if (warp == SW + 1 || warp == SW + 2) {
-        // ----------------- products: S from one thread, O from another, so that
-        // neither waits behind the other's operands
-        if (lane == 0) {
-            constexpr uint64_t kLayout = D == 128 ? 2 : 4;
-            constexpr uint32_t kAtom = 8 * D;                               // 8 rows of K, V or Q
-            bool ok = true, any = false;
-            int s = 0, x = 0;
-            uint32_t ph = 0, np[2] = {0, 0};
-            if (warp == SW + 1) {
-                constexpr uint32_t kIdesc = p8_idesc(kP8Tokens, PS::kNs, false, false, false);
-                const uint64_t k_desc = p8_desc(k_s, 16, kAtom, kLayout), q_desc = p8_desc(q_s, 16, kAtom, kLayout);
-                int sg = 0;
-                while (ok && walk.next(lens, seg)) {
-                    ok = wait(q_full + 8 * (sg & 1), sg >> 1);
-                    const uint64_t qd = q_desc + (sg & 1) * (PS::kQBytes >> 4);
-                    for (int i = seg.i0; ok && i < seg.i1; ++i) {
-                        // S_x of two tiles ago has been read.
-                        ok = wait(s_free + 8 * x, (x ? np[1] : np[0]) + 1) && wait(k_full + 8 * s, ph);
-                        if (!ok) break;
-                        if (x) ++np[1]; else ++np[0];
-                        tc_fence_after();
-                        const uint64_t kd = k_desc + s * (TB >> 4);
+        // ----------------- products: S from one warp, O from another, so that
+        // neither waits behind the other's operands. The warp waits as a whole
+        // and one thread issues; what the instructions take is made uniform.
+        constexpr uint64_t kLayout = D == 128 ? 2 : 4;
+        constexpr uint32_t kAtom = 8 * D;                               // 8 rows of K, V or Q
+        bool ok = true, any = false;
+        int s = 0, x = 0;
+        uint32_t ph = 0, np[2] = {0, 0};
+        const uint32_t tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
+        auto wait_warp = [&](uint32_t bar, uint32_t n) {
+            return __all_sync(0xffffffffu, wait(bar, n)) != 0;
+        };
+        if (warp == SW + 1) {
+            constexpr uint32_t kIdesc = p8_idesc(kP8Tokens, PS::kNs, false, false, false);
+            const uint64_t k_desc = p8_desc(k_s, 16, kAtom, kLayout), q_desc = p8_desc(q_s, 16, kAtom, kLayout);
+            int sg = 0, chunk = 0;
+            while (ok && walk.next(lens, seg)) {
+                ok = wait_warp(q_full + 8 * (sg & 1), sg >> 1);
+                for (int i = seg.i0; ok && i < seg.i1; ++i) {
+                    // The scales of this tile and the next three are there, and
+                    // S_x of two tiles ago has been read.
+                    if ((i - seg.i0) % kP8ScaleChunk == 0) {
+                        ok = wait_warp(sc_full + 8 * (chunk % kP8ScaleChunks), chunk / kP8ScaleChunks);
+                        ++chunk;
+                    }
+                    ok = ok && wait_warp(s_free + 8 * x, (x ? np[1] : np[0]) + 1) && wait_warp(k_full + 8 * s, ph);
+                    if (!ok) break;
+                    if (x) ++np[1]; else ++np[0];
+                    tc_fence_after();
+                    const int su = __shfl_sync(0xffffffffu, s, 0), xu = __shfl_sync(0xffffffffu, x, 0);
+                    const int bu = __shfl_sync(0xffffffffu, sg & 1, 0);
+                    if (elect_one()) {
+                        const uint64_t kd = k_desc + su * (TB >> 4), qd = q_desc + bu * (PS::kQBytes >> 4);
 #pragma unroll
                         for (int kk = 0; kk < D / 32; ++kk)
-                            umma_f8(tmem + PS::kColS + x * PS::kNs, kd + kk * 2, qd + kk * 2, kIdesc, kk > 0 ? 1u : 0u);
-                        umma_commit(s_full + 8 * x);
-                        umma_commit(k_empty + 8 * s);
-                        any = true;
-                        x ^= 1;
-                        if (++s == SK) s = 0, ph ^= 1;
+                            umma_f8(tmem_u + PS::kColS + xu * PS::kNs, kd + kk * 2, qd + kk * 2, kIdesc, kk > 0 ? 1u : 0u);
+                        umma_commit(s_full + 8 * xu);
+                        umma_commit(k_empty + 8 * su);
+                        if (i + 1 == seg.i1) umma_commit(q_empty + 8 * bu);
                     }
-                    if (ok) umma_commit(q_empty + 8 * (sg & 1));
-                    ++sg;
+                    __syncwarp();
+                    any = true;
+                    x ^= 1;
+                    if (++s == SK) s = 0, ph ^= 1;
                 }
-            } else {
-                constexpr uint32_t kIdesc = p8_idesc(D, PS::kNp, true, true, true);
-                const uint64_t v_desc = p8_desc(v_s, 16, kAtom, kLayout), p_desc = p8_desc(p_s, 128, 2048, 0);
-                while (ok && walk.next(lens, seg)) {
-                    bool first[2] = {true, true};
-                    for (int i = seg.i0; i < seg.i1; ++i) {
-                        ok = wait(v_full + 8 * s, ph) && wait(p_full + 8 * x, x ? np[1] : np[0]);
-                        if (!ok) break;
-                        const bool fresh = x ? first[1] : first[0];
-                        if (x) ++np[1], first[1] = false; else ++np[0], first[0] = false;
-                        tc_fence_after();
-                        const uint64_t vd = v_desc + s * (TB >> 4), pd = p_desc + x * (PS::kPBytes >> 4);
+                ++sg;
+            }
+        } else {
+            constexpr uint32_t kIdesc = p8_idesc(D, PS::kNp, true, true, true);
+            const uint64_t v_desc = p8_desc(v_s, 16, kAtom, kLayout), p_desc = p8_desc(p_s, 128, 2048, 0);
+            while (ok && walk.next(lens, seg)) {
+                bool first[2] = {true, true};
+                for (int i = seg.i0; i < seg.i1; ++i) {
+                    ok = wait_warp(v_full + 8 * s, ph) && wait_warp(p_full + 8 * x, x ? np[1] : np[0]);
+                    if (!ok) break;
+                    const bool fresh = x ? first[1] : first[0];
+                    if (x) ++np[1], first[1] = false; else ++np[0], first[0] = false;
+                    tc_fence_after();
+                    const int su = __shfl_sync(0xffffffffu, s, 0), xu = __shfl_sync(0xffffffffu, x, 0);
+                    const int fu = __shfl_sync(0xffffffffu, fresh ? 1 : 0, 0);
+                    if (elect_one()) {
+                        const uint64_t vd = v_desc + su * (TB >> 4), pd = p_desc + xu * (PS::kPBytes >> 4);
 #pragma unroll
                         for (int kk = 0; kk < kP8Tokens / 32; ++kk)
-                            umma_f8(tmem + PS::kColO + x * PS::kNp, vd + kk * (2 * D), pd + kk * 32, kIdesc,
-                                    (!fresh || kk > 0) ? 1u : 0u);
-                        umma_commit(v_empty + 8 * s);
-                        any = true;
-                        x ^= 1;
-                        if (++s == SV) s = 0, ph ^= 1;
+                            umma_f8(tmem_u + PS::kColO + xu * PS::kNp, vd + kk * (2 * D), pd + kk * 32, kIdesc,
+                                    (fu == 0 || kk > 0) ? 1u : 0u);
+                        umma_commit(v_empty + 8 * su);
                     }
+                    __syncwarp();
+                    any = true;
+                    x ^= 1;
+                    if (++s == SV) s = 0, ph ^= 1;
                 }
             }
-            if (any) {
-                const uint32_t bar = fin + 8 * (warp - SW - 1);
-                umma_commit(bar);
-                const uint64_t t0 = global_timer_ns();
-                while (!mbar_try_wait(bar, 0))
-                    if (global_timer_ns() - t0 > tmo) {
-                        atomicOr(p.status, kStatusTimeout);
-                        break;
-                    }
-            }
+        }
+        // elect_one picks the same thread each time: its commit covers all of the warp's products.
+        if (any && elect_one()) {
+            const uint32_t bar = fin + 8 * (warp - SW - 1);
+            umma_commit(bar);
+            const uint64_t t0 = global_timer_ns();
+            while (!mbar_try_wait(bar, 0))
+                if (global_timer_ns() - t0 > tmo) {
+                    atomicOr(p.status, kStatusTimeout);
+                    break;
+                }
         }
         __syncwarp();
     } else if (warp == SW + 3) {
-        // ------------------------------------------------------------ Q rows
-        const int page_size = 1 << p.page_shift, block = min(page_size, 64);
-        int sg = 0, chunk = 0;
+        // ------------------------------------------------ Q rows, scales, V loader
+        const int block = min(page_size, 64);     // tokens of a scale
+        const uint64_t pol = l2_policy_evict_first();
+        int sg = 0, chunk = 0, it = 0, s = 0;
+        uint32_t ph = 1;
         bool ok = true;
         while (ok && walk.next(lens, seg)) {
             const int buf = sg & 1;
-            ok = warp_wait(q_empty + 8 * buf, ((sg >> 1) & 1) ^ 1, abort_flag, p.status, tmo);
-            if (!ok) break;
             int b, rt;
             lens.split(seg.entry, b, rt);
             const int T = lens.tokens(b);
+            // Scales of the segment's tiles, a chunk of four at a time: lane
+            // (tile, block); pages two chunks ahead, scales one.
+            const int32_t* table = p.table + (size_t)b * p.max_pages;
+            auto pos_of = [&](int i) {           // this lane's position in the chunk at tile i, -1: none
+                i += lane >> 3;
+                const int pos = i * kP8Tokens + (lane & 7) * block;
+                return i < seg.i1 && (lane & 7) * block < kP8Tokens && pos < T ? pos : -1;
+            };
+            auto page_of = [&](int pos) {
+                const int e = pos >= 0 ? table[pos >> p.page_shift] : -1;
+                return (unsigned)e < (unsigned)p.num_pages ? e : -1;
+            };
+            float ks, vs;
+            auto fetch_scales = [&](int pos, int page) {
+                ks = vs = 0.f;
+                if (page >= 0) {
+                    const size_t at = ((size_t)page * p.G + seg.g) * p.blocks + ((pos & (page_size - 1)) >> 6);
+                    ks = __ldg(p.k_scale + at);
+                    vs = __ldg(p.v_scale + at);
+                }
+            };
+            auto store_scales = [&]() {
+                float* to = scale_ring + ((chunk % kP8ScaleChunks) * kP8ScaleChunk + (lane >> 3)) * 16 + (lane & 7);
+                to[0] = ks;
+                to[8] = vs;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sc_full + 8 * (chunk % kP8ScaleChunks));
+                ++chunk;
+            };
+            const int page_first = page_of(pos_of(seg.i0));
+            ok = warp_wait(q_empty + 8 * buf, ((sg >> 1) & 1) ^ 1, abort_flag, p.status, tmo);
+            if (!ok) break;
             const uint32_t qt = q_s + buf * PS::kQBytes;
             // Four lanes a row, eight rows at a time; the next rows are on
             // their way while these are split.
@@ -769,6 +858,8 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
                 for (int c = 0; c < kVec; ++c) next[c] = orow_next >= 0 ? src[c] : make_uint4(0, 0, 0, 0);
             };
             load_rows(0);
+            fetch_scales(pos_of(seg.i0), page_first);
+            int page_next = page_of(pos_of(seg.i0 + kP8ScaleChunk));
 #pragma unroll 1
             for (int r0 = 0; r0 < RP; r0 += 8) {
                 uint4 v[kVec];
@@ -824,50 +915,21 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full + 8 * buf);
             ++sg;
-            // Scales of the segment's tiles, a chunk of four at a time: lane
-            // (tile, block); pages two chunks ahead, scales one.
-            const int32_t* table = p.table + (size_t)b * p.max_pages;
-            auto pos_of = [&](int i) {           // this lane's position in the chunk at tile i, -1: none
-                i += lane >> 3;
-                const int pos = i * kP8Tokens + (lane & 7) * block;
-                return i < seg.i1 && (lane & 7) * block < kP8Tokens && pos < T ? pos : -1;
-            };
-            auto page_of = [&](int pos) {
-                const int e = pos >= 0 ? table[pos >> p.page_shift] : -1;
-                return (unsigned)e < (unsigned)p.num_pages ? e : -1;
-            };
-            auto scale_of = [&](int pos, int page, float& ks, float& vs) {
-                ks = vs = 0.f;
-                if (page >= 0) {
-                    const size_t at = ((size_t)page * p.G + seg.g) * p.blocks + ((pos & (page_size - 1)) >> 6);
-                    ks = __ldg(p.k_scale + at);
-                    vs = __ldg(p.v_scale + at);
+            // Slots are reused eight chunks later: by then this warp, which is
+            // at most two segments and kStagesV tiles ahead of the products,
+            // has seen the tiles done whose scales they held.
+            store_scales();
+            fetch_scales(pos_of(seg.i0 + kP8ScaleChunk), page_next);
+            page_next = page_of(pos_of(seg.i0 + 2 * kP8ScaleChunk));
+            ok = load_tiles(seg, b, T, &tm_v, v_s, SV, v_full, v_empty, -1, pol, it, s, ph, [&](int i) {
+                if ((i - seg.i0) % kP8ScaleChunk == 0 && i + kP8ScaleChunk < seg.i1) {
+                    store_scales();                                     // of tiles i + 4 .. i + 7
+                    fetch_scales(pos_of(i + 2 * kP8ScaleChunk), page_next);
+                    page_next = page_of(pos_of(i + 3 * kP8ScaleChunk));
                 }
-            };
-            float ks, vs;
-            scale_of(pos_of(seg.i0), page_of(pos_of(seg.i0)), ks, vs);
-            int page_next = page_of(pos_of(seg.i0 + kP8ScaleChunk));
-            for (int i = seg.i0; i < seg.i1; i += kP8ScaleChunk, ++chunk) {
-                float ks_next, vs_next;
-                scale_of(pos_of(i + kP8ScaleChunk), page_next, ks_next, vs_next);
-                page_next = page_of(pos_of(i + 2 * kP8ScaleChunk));
-                const int slot = chunk % kP8ScaleChunks;
-                ok = warp_wait(sc_free + 8 * slot, ((chunk / kP8ScaleChunks) & 1) ^ 1, abort_flag, p.status, tmo);
-                if (!ok) break;
-                float* to = scale_ring + (slot * kP8ScaleChunk + (lane >> 3)) * 16 + (lane & 7);
-                to[0] = ks;
-                to[8] = vs;
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(sc_full + 8 * slot);
-                    // Tiles that the segment's last chunk lacks are read by nobody.
-                    for (int k = seg.i1 - i; k < kP8ScaleChunk; ++k)
-                        for (int y = 0; y < PS::kParts; ++y) mbar_arrive(sc_free + 8 * slot);
-                }
-                ks = ks_next;
-                vs = vs_next;
-            }
+            });
         }
+        drain(v_full, SV, it, -1);
         // Entries none of whose rows sees a key own no tile: out = 0, lse = -inf.
         for (int e = blockIdx.x; e < p.B * p.row_tiles; e += gridDim.x) {
             if (lens.tiles(e) > 0) continue;
@@ -930,15 +992,13 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
 
                 all_wait(s_full + 8 * x, n_tiles);
                 tc_fence_after();
-                const int chunk = chunk0 + (i - seg.i0) / kP8ScaleChunk, slot = chunk % kP8ScaleChunks;
-                all_wait(sc_full + 8 * slot, chunk / kP8ScaleChunks);
-                const float* sc = scale_ring + (slot * kP8ScaleChunk + (i - seg.i0) % kP8ScaleChunk) * 16 +
-                                  (tok >> block_shift);
+                const float* sc = scale_ring + ((chunk0 + (i - seg.i0) / kP8ScaleChunk) % kP8ScaleChunks * kP8ScaleChunk +
+                                                (i - seg.i0) % kP8ScaleChunk) * 16 + (tok >> block_shift);
                 const float ks = sc[0];
                 float vs = sc[8];
-                float xs[RH];
-                bool moves = first;
-                {
+                // z = x - m, -inf where the row does not see the key.
+                float sv[RH], z[RH];
+                auto load_s = [&]() {
                     uint32_t h[RH], lo[RH];
                     if constexpr (RH == 8) {
                         uint32_t t[16];
@@ -948,30 +1008,47 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
                     } else {
                         tmem_ld16x2(s_tm, s_tm + RP, h, lo);
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(s_free + 8 * x);
-                    float top = -INFINITY;
+#pragma unroll
+                    for (int r = 0; r < RH; ++r) sv[r] = fmaf(__uint_as_float(lo[r]), 0.0625f, __uint_as_float(h[r]));
+                };
+                auto subtract_refs = [&]() {
 #pragma unroll
                     for (int r = 0; r < RH; r += 4) {
                         const float4 f = scale4[r / 4];
                         const float4 m = *reinterpret_cast<const float4*>(my_ref + r);
-                        const float fs[4] = {f.x, f.y, f.z, f.w}, ms[4] = {m.x, m.y, m.z, m.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            xs[r + k] = fmaf(__uint_as_float(lo[r + k]), 0.0625f, __uint_as_float(h[r + k])) * (fs[k] * ks);
-                            if (edge && pos > lim[r + k]) xs[r + k] = -INFINITY;
-                            top = fmaxf(top, xs[r + k] + ms[k]);
-                        }
+                        z[r] = fmaf(sv[r], f.x * ks, m.x);
+                        z[r + 1] = fmaf(sv[r + 1], f.y * ks, m.y);
+                        z[r + 2] = fmaf(sv[r + 2], f.z * ks, m.z);
+                        z[r + 3] = fmaf(sv[r + 3], f.w * ks, m.w);
                     }
+                    if (edge) {
+#pragma unroll
+                        for (int r = 0; r < RH; ++r)
+                            if (pos > lim[r]) z[r] = -INFINITY;
+                    }
+                };
+                load_s();
+                subtract_refs();
+                bool moves = first;
+                {
+                    float top = fmax3(z[0], z[1], z[2]);
+#pragma unroll
+                    for (int r = 3; r + 1 < RH; r += 2) top = fmax3(top, z[r], z[r + 1]);
+                    top = fmaxf(top, z[RH - 1]);
                     // A NaN or infinite scale makes its block's values NaN.
                     if (!(fabsf(vs) <= 3.402823466e38f)) vs = __int_as_float(0x7fffffff);
                     moves |= top > kP8Slack || fabsf(vs) * pow2i(-ev) > kP8ScaleSlack;
                 }
-                const bool any = named_any(bar, moves);
-                if (tok == 0) mbar_arrive(sc_free + 8 * slot);     // every thread has its scales
-                if (any) {
+                if (named_any(bar, moves)) {
                     // Move the references: rows whose tile maximum is out of range.
+                    // S is read again, so that it need not be kept above.
+                    load_s();
+                    float xs[RH];
+#pragma unroll
+                    for (int r = 0; r < RH; ++r) {
+                        xs[r] = sv[r] * (row_scale[(sg & 1) * RP + y * RH + r] * ks);
+                        if (edge && pos > lim[r]) xs[r] = -INFINITY;
+                    }
                     int mine = 0;
 #pragma unroll
                     for (int r = 0; r < RH; ++r) {
@@ -1015,7 +1092,11 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
                         tmem_st_wait();
                     }
                     named_sync(bar, 128);
+                    subtract_refs();
                 }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_free + 8 * x);
                 if (edge) {
                     // Rows of V past the length may hold anything: zero them. A
                     // NaN code in a key that only some rows see would reach the
@@ -1049,15 +1130,17 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
                 uint32_t packed[RH / 4][kP8Terms];       // a term of four rows
 #pragma unroll
                 for (int r = 0; r < RH; r += 4) {
-                    const float4 m = *reinterpret_cast<const float4*>(my_ref + r);
-                    const float ms[4] = {m.x, m.y, m.z, m.w};
                     float w[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const float pr = fast_exp2(xs[r + k] + ms[k]);
+                        const float pr = fast_exp2(z[r + k]);
                         l[r + k] += pr;
                         w[k] = pr * vw;
-                        if (edge && pos > lim[r + k]) w[k] = 0.f;
+                    }
+                    if (edge) {          // 0 * NaN: of a scale, or of a value that other rows see
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (z[r + k] == -INFINITY) w[k] = 0.f;
                     }
                     uint32_t f0 = pack_f16x2(w[0], w[1]), f1 = pack_f16x2(w[2], w[3]);
 #pragma unroll
@@ -1187,7 +1270,7 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
                         named_sync(bar, 128);
                         if (last_flag[bar - 1]) {
                             __threadfence();
-                            p8_merge<D, RP, RH>(p, c0, n, y * RH, w4, lane, rows_out);
+                            p8_merge<D, RP, RH>(p, c0, n, y * RH, tok, rows_out);
                         }
                     }
                 }

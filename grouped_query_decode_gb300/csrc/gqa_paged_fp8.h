@@ -30,6 +30,7 @@ struct PagedFp8Params {
     int B, sq, H, G, R, heads_per_group, row_tiles;
     int page_shift, num_pages, max_pages, blocks;
     int small_plan;            // one row tile, up to 128 sequences, 32-bit tile arithmetic
+    int even_ctas;             // grid for equal lengths (small plans)
     int skip_tile;             // fault injection for tests (-1: off)
 };
 
