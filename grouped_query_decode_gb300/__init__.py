@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import threading
 
 from . import build as _build
@@ -295,39 +296,55 @@ def gqa_decode_fp8(q, k_codes, v_codes, k_scale, v_scale, seq_lens, scale, out, 
         raise GQADecodeError(rc, "gqa_decode_fp8")
 
 
-def _paged_fp8_cache(dev, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens):
-    """Checks the tensors of a paged 8-bit cache; returns B, num_pages, G,
+def _check_all(dev, named):
+    """dtype, device and contiguity of (name, tensor, dtype) triples: one pass
+    that is quick when all is well (a decode step is a few microseconds), then
+    the one that says what is wrong."""
+    for _, t, dt in named:
+        if not (t.dtype is dt and t.get_device() == dev and t.is_contiguous()):
+            break
+    else:
+        if dev >= 0:
+            return
+    for name, t, dt in named:
+        _check(dev, name, t, dt)
+
+
+def _raw_stream(stream, dev):
+    """The stream handle of a call: `stream`, or the device's current one."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream_handle(stream, dev)
+
+
+def _paged_fp8_cache(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens):
+    """Checks the shapes of a paged 8-bit cache; returns B, num_pages, G,
     page_size, D and max_pages_per_seq."""
-    import torch
-    u8, f32, i32 = torch.uint8, torch.float32, torch.int32
-    _check(dev, "k_pages", k_pages, u8)
-    _check(dev, "v_pages", v_pages, u8)
-    _check(dev, "k_scale", k_scale, f32)
-    _check(dev, "v_scale", v_scale, f32)
-    _check(dev, "block_table", block_table, i32)
-    _check(dev, "seq_lens", seq_lens, i32)
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+    shape = k_pages.shape
+    if len(shape) != 4 or v_pages.shape != shape:
         raise ValueError("k_pages / v_pages must be [num_pages, G, page_size, D]")
-    num_pages, G, page_size, D = k_pages.shape
+    num_pages, G, page_size, D = shape
     blocks = (num_pages, G, (page_size + 63) // 64)
     if k_scale.shape != blocks or v_scale.shape != blocks:
         raise ValueError("k_scale / v_scale must be [num_pages, G, ceil(page_size/64)]")
-    if block_table.dim() != 2 or seq_lens.shape != block_table.shape[:1]:
+    table = block_table.shape
+    if len(table) != 2 or seq_lens.shape != table[:1]:
         raise ValueError("block_table must be [B, max_pages_per_seq] and seq_lens [B]")
-    B, most = block_table.shape
-    return B, num_pages, G, page_size, D, most
+    return table[0], num_pages, G, page_size, D, table[1]
 
 
-def _workspace(nbytes, dev, stream):
-    """A buffer for one call from torch's allocator, in the order of the
-    call's stream (inside a graph capture, the graph's own memory)."""
+def _workspace(nbytes, like, stream):
+    """A buffer for one call from torch's allocator, on the device of `like`, in
+    the order of the call's stream (inside a graph capture, the graph's own
+    memory)."""
     import torch
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
 
 
 def gqa_decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, scale, out, lse=None,
@@ -340,26 +357,30 @@ def gqa_decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seq
     when not given."""
     import torch
     dev = q.get_device()
-    _check(dev, "q", q, torch.bfloat16)
-    _check(dev, "out", out, torch.bfloat16)
-    Bt, num_pages, G, page_size, Dk, most = _paged_fp8_cache(dev, k_pages, v_pages, k_scale, v_scale,
-                                                             block_table, seq_lens)
-    if q.dim() != 4 or q.shape[0] != Bt or q.shape[3] != Dk:
+    bf, u8, f32, i32 = torch.bfloat16, torch.uint8, torch.float32, torch.int32
+    named = [("q", q, bf), ("out", out, bf), ("k_pages", k_pages, u8), ("v_pages", v_pages, u8),
+             ("k_scale", k_scale, f32), ("v_scale", v_scale, f32), ("block_table", block_table, i32),
+             ("seq_lens", seq_lens, i32)]
+    if lse is not None:
+        named.append(("lse", lse, f32))
+    if workspace is not None:
+        named.append(("workspace", workspace, u8))
+    _check_all(dev, named)
+    Bt, num_pages, G, page_size, Dk, most = _paged_fp8_cache(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens)
+    shape = q.shape
+    if len(shape) != 4 or shape[0] != Bt or shape[3] != Dk:
         raise ValueError("q must be [B, sq, H, D] with block_table's B and the pages' D")
-    B, sq, H, D = q.shape
-    if out.shape != q.shape:
+    B, sq, H, D = shape
+    if out.shape != shape:
         raise ValueError("out must be [B, sq, H, D]")
-    _check_lse(dev, lse, B, sq, H)
-    handle = _stream_handle(stream, dev)
+    if lse is not None and lse.shape != (B, sq, H):
+        raise ValueError("lse must be [B, sq, H]")
     if workspace is None:
-        workspace = _workspace(gqa_decode_paged_fp8_workspace_bytes(B, sq, H, G, D, page_size, most, dev) or 256,
-                               dev, stream)
-    else:
-        _check(dev, "workspace", workspace, torch.uint8)
+        workspace = _workspace(_paged_fp8_workspace_bytes(B, sq, H, G, D, page_size, most, dev) or 256, q, stream)
     rc = _call(dev, load().gqa_decode_paged_fp8, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
                k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
                float(scale), out.data_ptr(), None if lse is None else lse.data_ptr(), B, sq, H, G, D,
-               page_size, num_pages, most, workspace.data_ptr(), workspace.numel(), handle)
+               page_size, num_pages, most, workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
     if rc != GQA_OK:
         raise GQADecodeError(rc, "gqa_decode_paged_fp8")
 
@@ -383,16 +404,17 @@ def gqa_append_paged_fp8(k_new, v_new, k_pages, v_pages, k_scale, v_scale, block
     per block of min(64, page_size) tokens and KV head."""
     import torch
     dev = k_new.get_device()
-    _check(dev, "k_new", k_new, torch.bfloat16)
-    _check(dev, "v_new", v_new, torch.bfloat16)
-    B, num_pages, G, page_size, D, most = _paged_fp8_cache(dev, k_pages, v_pages, k_scale, v_scale,
-                                                           block_table, seq_lens)
-    if k_new.dim() != 4 or k_new.shape[0] != B or tuple(k_new.shape[2:]) != (G, D) or v_new.shape != k_new.shape:
+    bf, u8, f32, i32 = torch.bfloat16, torch.uint8, torch.float32, torch.int32
+    _check_all(dev, (("k_new", k_new, bf), ("v_new", v_new, bf), ("k_pages", k_pages, u8), ("v_pages", v_pages, u8),
+                     ("k_scale", k_scale, f32), ("v_scale", v_scale, f32), ("block_table", block_table, i32),
+                     ("seq_lens", seq_lens, i32)))
+    B, num_pages, G, page_size, D, most = _paged_fp8_cache(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens)
+    shape = k_new.shape
+    if len(shape) != 4 or shape[0] != B or shape[2:] != (G, D) or v_new.shape != shape:
         raise ValueError("k_new / v_new must be [B, sq, G, D]")
     rc = _call(dev, load().gqa_append_paged_fp8, k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(),
                v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
-               seq_lens.data_ptr(), B, k_new.shape[1], G, D, page_size, num_pages, most,
-               _stream_handle(stream, dev))
+               seq_lens.data_ptr(), B, shape[1], G, D, page_size, num_pages, most, _raw_stream(stream, dev))
     if rc != GQA_OK:
         raise GQADecodeError(rc, "gqa_append_paged_fp8")
 
@@ -403,42 +425,35 @@ def _page_pools(dev, pools, num_pages, page_dim):
     that share the page numbers."""
     pools = list(pools)
     arr = (PagePoolT * max(1, len(pools)))()
+    _check_all(dev, [(f"pools[{i}]", t, t.dtype) for i, t in enumerate(pools)])
     for i, t in enumerate(pools):
-        _check(dev, f"pools[{i}]", t, t.dtype)
-        if not 0 <= page_dim < t.dim() or t.shape[page_dim] != num_pages:
+        shape = t.shape
+        if not 0 <= page_dim < len(shape) or shape[page_dim] != num_pages:
             raise ValueError(f"pools[{i}] must count {num_pages} pages in dimension {page_dim}")
-        if t.numel() == 0:
+        page, layers = t.element_size() * math.prod(shape[page_dim + 1:]), math.prod(shape[:page_dim])
+        if page * layers == 0:
             raise ValueError(f"pools[{i}] is empty")
-        page = t.element_size()
-        for n in t.shape[page_dim + 1:]:
-            page *= n
-        layers = 1
-        for n in t.shape[:page_dim]:
-            layers *= n
-        arr[i].base, arr[i].page_bytes = t.data_ptr(), page
-        arr[i].layer_bytes, arr[i].layers = page * num_pages, layers
+        arr[i] = (t.data_ptr(), page, page * num_pages, layers)
     return arr, len(pools)
 
 
-def _page_state(dev, block_table, seq_lens, ref_counts, counts=None, suffix=""):
-    import torch
-    i32 = torch.int32
-    _check(dev, "block_table" + suffix, block_table, i32)
-    if seq_lens is not None:
-        _check(dev, "seq_lens" + suffix, seq_lens, i32)
-    _check(dev, "ref_counts" + suffix, ref_counts, i32)
-    if block_table.dim() != 2 or (seq_lens is not None and seq_lens.shape != block_table.shape[:1]):
+def _page_sizes(block_table, seq_lens, ref_counts, counts=None):
+    """Checks the shapes of a block table and its counts; returns B,
+    max_pages_per_seq and num_pages."""
+    table, pages = block_table.shape, ref_counts.shape
+    if len(table) != 2 or (seq_lens is not None and seq_lens.shape != table[:1]):
         raise ValueError("block_table must be [B, max_pages_per_seq] and seq_lens [B]")
-    if ref_counts.dim() != 1:
+    if len(pages) != 1:
         raise ValueError("ref_counts must be [num_pages]")
-    if counts is not None:
-        _check(dev, "counts", counts, i32)
-        if counts.shape != (2,):
-            raise ValueError("counts must be [2]")
-    return block_table.shape[0], block_table.shape[1], ref_counts.shape[0]
+    if counts is not None and counts.shape != (2,):
+        raise ValueError("counts must be [2]")
+    return table[0], table[1], pages[0]
 
 
+@functools.lru_cache(maxsize=4096)
 def gqa_pages_workspace_bytes(B, num_pages) -> int:
+    """Workspace bytes of gqa_pages_reserve, gqa_pages_fork and
+    gqa_pages_compact (the functions here take one from torch's allocator)."""
     return int(load().gqa_pages_workspace_bytes(B, num_pages))
 
 
@@ -448,13 +463,12 @@ def gqa_pages_copy(pools, src, dst, num_pages, page_dim=0, stream=None):
     No page may be a source and a destination, or twice a destination."""
     import torch
     dev = src.get_device()
-    _check(dev, "src", src, torch.int32)
-    _check(dev, "dst", dst, torch.int32)
+    _check_all(dev, (("src", src, torch.int32), ("dst", dst, torch.int32)))
     if src.dim() != 1 or dst.shape != src.shape:
         raise ValueError("src and dst must be [n]")
     arr, n = _page_pools(dev, pools, num_pages, page_dim)
     rc = _call(dev, load().gqa_pages_copy, arr, n, src.data_ptr(), dst.data_ptr(), src.shape[0], num_pages,
-               _stream_handle(stream, dev))
+               _raw_stream(stream, dev))
     if rc != GQA_OK:
         raise GQADecodeError(rc, "gqa_pages_copy")
 
@@ -464,12 +478,15 @@ def gqa_pages_reserve(block_table, seq_lens, ref_counts, page_size, counts, stre
     empty entries take the free pages (ref_counts <= 0) in ascending order.
     counts (int32 [2]) = pages needed, pages that were free; nothing changes
     if fewer are free than needed."""
-    dev = block_table.get_device()
-    B, most, num_pages = _page_state(dev, block_table, seq_lens, ref_counts, counts)
-    ws = _workspace(gqa_pages_workspace_bytes(B, num_pages) or 256, dev, stream)
+    import torch
+    dev, i32 = block_table.get_device(), torch.int32
+    _check_all(dev, (("block_table", block_table, i32), ("seq_lens", seq_lens, i32), ("ref_counts", ref_counts, i32),
+                     ("counts", counts, i32)))
+    B, most, num_pages = _page_sizes(block_table, seq_lens, ref_counts, counts)
+    ws = _workspace(gqa_pages_workspace_bytes(B, num_pages) or 256, block_table, stream)
     rc = _call(dev, load().gqa_pages_reserve, block_table.data_ptr(), seq_lens.data_ptr(),
                ref_counts.data_ptr(), counts.data_ptr(), B, most, page_size, num_pages, ws.data_ptr(),
-               ws.numel(), _stream_handle(stream, dev))
+               ws.numel(), _raw_stream(stream, dev))
     if rc != GQA_OK:
         raise GQADecodeError(rc, "gqa_pages_reserve")
 
@@ -483,19 +500,23 @@ def gqa_pages_fork(pools, src, block_table, seq_lens, ref_counts, page_size, blo
     the inputs. counts (int32 [2]) = pages needed, pages that were free; the
     outputs are copies of the inputs if fewer are free than needed."""
     import torch
-    dev = block_table.get_device()
-    _check(dev, "src", src, torch.int32)
-    B, most, num_pages = _page_state(dev, block_table, seq_lens, ref_counts, counts)
-    if (B, most, num_pages) != _page_state(dev, block_table_out, seq_lens_out, ref_counts_out, None, "_out"):
+    dev, i32 = block_table.get_device(), torch.int32
+    _check_all(dev, (("src", src, i32), ("block_table", block_table, i32), ("seq_lens", seq_lens, i32),
+                     ("ref_counts", ref_counts, i32), ("block_table_out", block_table_out, i32),
+                     ("seq_lens_out", seq_lens_out, i32), ("ref_counts_out", ref_counts_out, i32),
+                     ("counts", counts, i32)))
+    B, most, num_pages = _page_sizes(block_table, seq_lens, ref_counts, counts)
+    if (block_table_out.shape != block_table.shape or seq_lens_out.shape != seq_lens.shape or
+            ref_counts_out.shape != ref_counts.shape):
         raise ValueError("the outputs must have the inputs' shapes")
     if src.shape != (B,):
         raise ValueError("src must be [B]")
     arr, n = _page_pools(dev, pools, num_pages, page_dim)
-    ws = _workspace(gqa_pages_workspace_bytes(B, num_pages) or 256, dev, stream)
+    ws = _workspace(gqa_pages_workspace_bytes(B, num_pages) or 256, block_table, stream)
     rc = _call(dev, load().gqa_pages_fork, arr, n, src.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
                ref_counts.data_ptr(), block_table_out.data_ptr(), seq_lens_out.data_ptr(),
                ref_counts_out.data_ptr(), counts.data_ptr(), B, most, page_size, num_pages, ws.data_ptr(),
-               ws.numel(), _stream_handle(stream, dev))
+               ws.numel(), _raw_stream(stream, dev))
     if rc != GQA_OK:
         raise GQADecodeError(rc, "gqa_pages_fork")
 
@@ -504,13 +525,14 @@ def gqa_pages_free(done, block_table, seq_lens, ref_counts, stream=None):
     """Gives back the pages of every sequence with done[b] (bool or uint8 [B]),
     in place: counts go down by one, rows become -1, lengths 0."""
     import torch
-    dev = block_table.get_device()
-    _check(dev, "done", done, torch.bool if done.dtype == torch.bool else torch.uint8)
-    B, most, num_pages = _page_state(dev, block_table, seq_lens, ref_counts)
+    dev, i32 = block_table.get_device(), torch.int32
+    _check_all(dev, (("done", done, torch.bool if done.dtype is torch.bool else torch.uint8),
+                     ("block_table", block_table, i32), ("seq_lens", seq_lens, i32), ("ref_counts", ref_counts, i32)))
+    B, most, num_pages = _page_sizes(block_table, seq_lens, ref_counts)
     if done.shape != (B,):
         raise ValueError("done must be [B]")
     rc = _call(dev, load().gqa_pages_free, done.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
-               ref_counts.data_ptr(), B, most, num_pages, _stream_handle(stream, dev))
+               ref_counts.data_ptr(), B, most, num_pages, _raw_stream(stream, dev))
     if rc != GQA_OK:
         raise GQADecodeError(rc, "gqa_pages_free")
 
@@ -520,15 +542,19 @@ def gqa_pages_compact(pools, block_table, ref_counts, block_table_out, ref_count
     """Moves the live pages (ref_counts > 0) to the lowest page numbers, in
     every pool; the block table and counts follow (the outputs may be the
     input tensors themselves). counts (int32 [2]) = pages moved, pages live."""
-    dev = block_table.get_device()
-    B, most, num_pages = _page_state(dev, block_table, None, ref_counts, counts)
-    if (B, most, num_pages) != _page_state(dev, block_table_out, None, ref_counts_out, None, "_out"):
+    import torch
+    dev, i32 = block_table.get_device(), torch.int32
+    _check_all(dev, (("block_table", block_table, i32), ("ref_counts", ref_counts, i32),
+                     ("block_table_out", block_table_out, i32), ("ref_counts_out", ref_counts_out, i32),
+                     ("counts", counts, i32)))
+    B, most, num_pages = _page_sizes(block_table, None, ref_counts, counts)
+    if block_table_out.shape != block_table.shape or ref_counts_out.shape != ref_counts.shape:
         raise ValueError("the outputs must have the inputs' shapes")
     arr, n = _page_pools(dev, pools, num_pages, page_dim)
-    ws = _workspace(gqa_pages_workspace_bytes(B, num_pages) or 256, dev, stream)
+    ws = _workspace(gqa_pages_workspace_bytes(B, num_pages) or 256, block_table, stream)
     rc = _call(dev, load().gqa_pages_compact, arr, n, block_table.data_ptr(), ref_counts.data_ptr(),
                block_table_out.data_ptr(), ref_counts_out.data_ptr(), counts.data_ptr(), B, most, num_pages,
-               ws.data_ptr(), ws.numel(), _stream_handle(stream, dev))
+               ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
     if rc != GQA_OK:
         raise GQADecodeError(rc, "gqa_pages_compact")
 

@@ -222,7 +222,7 @@ def test_binding_refuses_host_tensors_dtypes_and_shapes():
 
 
 def test_pool_array_counts_layers_and_bytes(monkeypatch):
-    monkeypatch.setattr(gq, "_check", lambda *a: None)
+    monkeypatch.setattr(gq, "_check_all", lambda *a: None)
     codes = torch.zeros(3, 2, 7, 4, 16, 64, dtype=torch.uint8)
     scales = torch.zeros(6, 7, 4, 1)
     arr, n = gq._page_pools(0, [codes], 7, 2)
