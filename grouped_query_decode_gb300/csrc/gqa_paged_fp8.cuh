@@ -276,21 +276,32 @@ struct P8Plan {
     }
 };
 
-// Up to 128 sequences of one row tile, and 32-bit products of tiles and CTAs:
-// every warp finds the CTA's share by itself, four entries a lane, so that no
-// warp waits for another. Each warp also writes the (same) copy of the lengths.
+// Up to 128 entries, and 32-bit products of tiles and CTAs: every warp finds
+// the CTA's share by itself, four entries a lane, so that no warp waits for
+// another. Each warp also writes the (same) copy of the lengths.
 template <int RP>
 __device__ __forceinline__ P8Plan p8_small_plan(const P8Lens<RP>& lens, int* len_copy) {
     const PagedFp8Params& p = lens.p;
     const int lane = threadIdx.x & 31;
+    const int entries = p.B * p.row_tiles;
     unsigned n[4], mine = 0;
+    if (p.row_tiles == 1) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int e = lane * 4 + k;
-        const int T = e < p.B ? lens.global(e) : 0;
-        if (e < p.B) len_copy[e] = T;
-        n[k] = (unsigned)(T + kP8Tokens - 1) / kP8Tokens;
-        mine += n[k];
+        for (int k = 0; k < 4; ++k) {
+            const int e = lane * 4 + k;
+            const int T = e < p.B ? lens.global(e) : 0;
+            if (e < p.B) len_copy[e] = T;
+            n[k] = (unsigned)(T + kP8Tokens - 1) / kP8Tokens;
+            mine += n[k];
+        }
+    } else {
+        for (int b = lane; b < p.B; b += 32) len_copy[b] = lens.global(b);
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            n[k] = lane * 4 + k < entries ? (unsigned)lens.tiles(lane * 4 + k) : 0;
+            mine += n[k];
+        }
     }
     mine *= (unsigned)p.G;
     unsigned x = mine;
@@ -306,7 +317,7 @@ __device__ __forceinline__ P8Plan p8_small_plan(const P8Lens<RP>& lens, int* len
     unsigned lo = 0xffffffffu, hi = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-        if (lane * 4 + k < p.B) lo = min(lo, n[k]), hi = max(hi, n[k]);
+        if (lane * 4 + k < entries) lo = min(lo, n[k]), hi = max(hi, n[k]);
     if (__reduce_min_sync(0xffffffffu, lo) == __reduce_max_sync(0xffffffffu, hi) && (unsigned)p.even_ctas <= most)
         ctas = (unsigned)p.even_ctas;
     const unsigned c = blockIdx.x;
@@ -605,7 +616,7 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
             mbar_init(v_empty + 8 * s, 1);
         }
         for (int x = 0; x < 2; ++x) {
-            mbar_init(q_full + 8 * x, 1);
+            mbar_init(q_full + 8 * x, RP / 8);          // eight rows a time
             mbar_init(q_empty + 8 * x, SW + 1);         // the softmax warps and the products
             mbar_init(s_full + 8 * x, 1);
             mbar_init(s_free + 8 * x, 4 * PS::kParts);
@@ -629,15 +640,19 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
     const uint32_t tmem = *tmem_slot;
     pdl_launch_dependents();
     pdl_wait_primary();
-    P8Plan plan;
+    P8Walk<RP> walk;
     if (p.small_plan) {
-        plan = p8_small_plan<RP>(lens, len_copy);
+        const P8Plan plan = p8_small_plan<RP>(lens, len_copy);
+        // Kept in shared memory (every warp writes the same) rather than in
+        // registers until a split unit's end needs it.
+        if (lane == 0) *plan_s = plan;
+        __syncwarp();
+        walk = {plan.end - plan.begin, plan.entry, plan.g, plan.off};
     } else {
         p8_make_plan<RP, PS::kThreads>(p, len_copy, plan_s, warp_sum);
         __syncthreads();
-        plan = *plan_s;
+        walk = {plan_s->end - plan_s->begin, plan_s->entry, plan_s->g, plan_s->off};
     }
-    P8Walk<RP> walk = {plan.end - plan.begin, plan.entry, plan.g, plan.off};
     P8Segment seg;
     // Bounded waits of one thread, and of a softmax warp: all its lanes poll,
     // and all go on when the limit runs out.
@@ -696,6 +711,85 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
             }
         __syncwarp();
     };
+
+    // Eight query rows of a unit at a time, by one warp, four lanes a row: their
+    // loads, and their split into q buffer `buf`, which arrives on its barrier.
+    constexpr int kVec = D / 32;                  // 16-byte loads per lane: D / 4 elements
+    struct QRows {
+        uint4 v[kVec];
+        int orow, tok;
+    };
+    auto load_rows = [&](int b, int rt, int g, int r0) {
+        QRows q;
+        q.tok = 0;
+        q.orow = p8_out_row<RP>(p, b, rt, g, r0 + (lane >> 2), &q.tok);
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (size_t)max(q.orow, 0) * D + (lane & 3) * (D / 4));
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) q.v[c] = q.orow >= 0 ? src[c] : make_uint4(0, 0, 0, 0);
+        return q;
+    };
+    auto split_rows = [&](const QRows& q, int T, int buf, int r0) {
+        const uint32_t qt = q_s + buf * PS::kQBytes;
+        const int part = lane & 3, r = r0 + (lane >> 2), orow = q.orow, tok = q.tok;
+        const uint4 (&v)[kVec] = q.v;
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) {
+            const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const bool bad = top >= 0x7f80u;          // an infinity or NaN: the whole row is NaN
+        const int e = min(134 - max((int)(top >> 7), 1), 120);
+        const float up = bad || top == 0 ? 0.f : pow2i(e);
+#pragma unroll
+        for (int c = 0; c < kVec; c += 2) {       // 16 elements: one 16-byte chunk of each row
+            const uint32_t w[8] = {v[c].x, v[c].y, v[c].z, v[c].w, v[c + 1].x, v[c + 1].y, v[c + 1].z, v[c + 1].w};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float a = bad ? 0.f : __uint_as_float(w[k] << 16) * up;
+                const float d = bad ? 0.f : __uint_as_float(w[k] & 0xffff0000u) * up;
+                const uint32_t h = f32x2_to_e4m3x2(a, d);
+                const uint32_t hf = e4m3x2_to_f16x2((uint16_t)h);
+                const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hf));
+                const uint32_t lw = f32x2_to_e4m3x2((a - back.x) * 16.f, (d - back.y) * 16.f);
+                if ((k & 1) == 0) hi[k / 2] = h, lo[k / 2] = lw;
+                else hi[k / 2] |= h << 16, lo[k / 2] |= lw << 16;
+            }
+            const uint32_t chunk = part * (D / 64) + c / 2;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const uint32_t row = t * RP + r;
+                const uint32_t sw = D == 128 ? (row & 7) : ((row >> 1) & 3);
+                const uint32_t* x = t ? lo : hi;
+                st_shared_v4(qt + row * D + ((chunk ^ sw) << 4), make_uint4(x[0], x[1], x[2], x[3]));
+            }
+        }
+        if (part == 0) {
+            row_scale[buf * RP + r] =
+                orow < 0 ? 0.f : bad ? __int_as_float(0x7fffffff) : p.scale_log2 * (top == 0 ? 1.f : pow2i(-e));
+            row_lim[buf * RP + r] = orow < 0 ? -1 : T - p.sq + tok;
+            row_out[buf * RP + r] = orow;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full + 8 * buf);
+    };
+
+    // The first segment's rows are split by softmax warps, which have nothing
+    // else to do yet, eight rows each (the loader warp would take them in turn,
+    // 1300 cycles each).
+    if (warp < RP / 8) {
+        P8Walk<RP> peek = walk;
+        if (peek.next(lens, seg)) {
+            int b, rt;
+            lens.split(seg.entry, b, rt);
+            split_rows(load_rows(b, rt, seg.g, warp * 8), lens.tokens(b), 0, warp * 8);
+        }
+    }
 
     if (warp == SW) {
         // ---------------------------------------------------------- K loader
@@ -843,77 +937,17 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
             const int page_first = page_of(pos_of(seg.i0));
             ok = warp_wait(q_empty + 8 * buf, ((sg >> 1) & 1) ^ 1, abort_flag, p.status, tmo);
             if (!ok) break;
-            const uint32_t qt = q_s + buf * PS::kQBytes;
-            // Four lanes a row, eight rows at a time; the next rows are on
-            // their way while these are split.
-            constexpr int kVec = D / 32;          // 16-byte loads per lane: D / 4 elements
-            const int part = lane & 3;
-            uint4 next[kVec];
-            int orow_next, tok_next;
-            auto load_rows = [&](int r0) {
-                tok_next = 0;
-                orow_next = p8_out_row<RP>(p, b, rt, seg.g, r0 + (lane >> 2), &tok_next);
-                const uint4* src = reinterpret_cast<const uint4*>(p.q + (size_t)max(orow_next, 0) * D + part * (D / 4));
-#pragma unroll
-                for (int c = 0; c < kVec; ++c) next[c] = orow_next >= 0 ? src[c] : make_uint4(0, 0, 0, 0);
-            };
-            load_rows(0);
-            fetch_scales(pos_of(seg.i0), page_first);
-            int page_next = page_of(pos_of(seg.i0 + kP8ScaleChunk));
+            if (sg > 0) {
+                QRows next = load_rows(b, rt, seg.g, 0);
 #pragma unroll 1
-            for (int r0 = 0; r0 < RP; r0 += 8) {
-                uint4 v[kVec];
-#pragma unroll
-                for (int c = 0; c < kVec; ++c) v[c] = next[c];
-                const int orow = orow_next, tok = tok_next, r = r0 + (lane >> 2);
-                if (r0 + 8 < RP) load_rows(r0 + 8);
-                uint32_t top = 0;
-#pragma unroll
-                for (int c = 0; c < kVec; ++c) {
-                    const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
-                }
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const bool bad = top >= 0x7f80u;              // an infinity or NaN: the whole row is NaN
-                const int e = min(134 - max((int)(top >> 7), 1), 120);
-                const float up = bad || top == 0 ? 0.f : pow2i(e);
-#pragma unroll
-                for (int c = 0; c < kVec; c += 2) {           // 16 elements: one 16-byte chunk of each row
-                    const uint32_t w[8] = {v[c].x, v[c].y, v[c].z, v[c].w,
-                                           v[c + 1].x, v[c + 1].y, v[c + 1].z, v[c + 1].w};
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float a = bad ? 0.f : __uint_as_float(w[k] << 16) * up;
-                        const float d = bad ? 0.f : __uint_as_float(w[k] & 0xffff0000u) * up;
-                        const uint32_t h = f32x2_to_e4m3x2(a, d);
-                        const uint32_t hf = e4m3x2_to_f16x2((uint16_t)h);
-                        const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hf));
-                        const uint32_t lw = f32x2_to_e4m3x2((a - back.x) * 16.f, (d - back.y) * 16.f);
-                        if ((k & 1) == 0) hi[k / 2] = h, lo[k / 2] = lw;
-                        else hi[k / 2] |= h << 16, lo[k / 2] |= lw << 16;
-                    }
-                    const uint32_t chunk = part * (D / 64) + c / 2;
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const uint32_t row = t * RP + r;
-                        const uint32_t sw = D == 128 ? (row & 7) : ((row >> 1) & 3);
-                        const uint32_t* x = t ? lo : hi;
-                        st_shared_v4(qt + row * D + ((chunk ^ sw) << 4), make_uint4(x[0], x[1], x[2], x[3]));
-                    }
-                }
-                if (part == 0) {
-                    row_scale[buf * RP + r] = orow < 0 ? 0.f : bad ? __int_as_float(0x7fffffff)
-                                                                 : p.scale_log2 * (top == 0 ? 1.f : pow2i(-e));
-                    row_lim[buf * RP + r] = orow < 0 ? -1 : T - p.sq + tok;
-                    row_out[buf * RP + r] = orow;
+                for (int r0 = 0; r0 < RP; r0 += 8) {
+                    const QRows q = next;
+                    if (r0 + 8 < RP) next = load_rows(b, rt, seg.g, r0 + 8);
+                    split_rows(q, T, buf, r0);
                 }
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_full + 8 * buf);
+            fetch_scales(pos_of(seg.i0), page_first);
+            int page_next = page_of(pos_of(seg.i0 + kP8ScaleChunk));
             ++sg;
             // Slots are reused eight chunks later: by then this warp, which is
             // at most two segments and kStagesV tiles ahead of the products,
@@ -1261,15 +1295,17 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
                     if (!whole) {
                         // The last of the unit's CTAs to arrive merges it:
                         //   M = max m_c, L = sum l_c 2^(m_c - M), O = sum O_c 2^(m_c - M) / L.
+                        const P8Plan plan = *plan_s;
                         const long long unit0 = plan.begin + it0 - seg.i0;
                         const int c0 = plan.owner(unit0), n = plan.owner(unit0 + seg.n - 1) - c0 + 1;
-                        __threadfence();
                         named_sync(bar, 128);
-                        if (tok == 0)
+                        if (tok == 0) {
+                            __threadfence();      // of the group's stores, which the barrier ordered before
                             last_flag[bar - 1] = arrive_last(p.counters + (size_t)c0 * PS::kParts + y, p.tag, n);
+                            __threadfence();
+                        }
                         named_sync(bar, 128);
                         if (last_flag[bar - 1]) {
-                            __threadfence();
                             p8_merge<D, RP, RH>(p, c0, n, y * RH, tok, rows_out);
                         }
                     }

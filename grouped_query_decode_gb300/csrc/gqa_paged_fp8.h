@@ -29,7 +29,7 @@ struct PagedFp8Params {
     float scale_log2;
     int B, sq, H, G, R, heads_per_group, row_tiles;
     int page_shift, num_pages, max_pages, blocks;
-    int small_plan;            // one row tile, up to 128 sequences, 32-bit tile arithmetic
+    int small_plan;            // up to 128 entries (b, row tile), 32-bit tile arithmetic
     int even_ctas;             // grid for equal lengths (small plans)
     int skip_tile;             // fault injection for tests (-1: off)
 };
