@@ -31,6 +31,7 @@ struct AppendParams {
     int B, sq, G, page_size, num_pages, max_pages;
     int size;                   // tokens of a block: min(64, page_size)
     int blocks;                 // blocks of a sequence that may receive tokens
+    int per, runs;              // blocks per item, items per sequence and head
 };
 
 // Smallest power of two >= top / 448 (448 = 0.875 * 2^9), 0 for 0, at least 2^-126.
@@ -75,118 +76,169 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
     }
 }
 
-// TPI threads (a warp, or the CTA) per item; kChunks 8-element chunks of new
-// tokens per thread at most.
+// TPI threads (a warp, or the CTA) per item; an item is a run of `per` blocks of
+// one (sequence, KV head, K or V). CHUNKS: 8-element chunks of a block's new
+// tokens per thread at most. A block's tokens are on their way while the one
+// before is quantised; what a block needs first (length, then page and tokens)
+// is two reads deep.
 template <int D, int TPI, int THREADS, int CHUNKS>
-__global__ void __launch_bounds__(THREADS) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_kernel(const __grid_constant__ AppendParams p) {
     pdl_launch_dependents();
     pdl_wait_primary();
     constexpr int kRowChunks = D / 8;
     const int t = threadIdx.x % TPI;
-    const long long item = (long long)blockIdx.x * (THREADS / TPI) + threadIdx.x / TPI;
-    const long long items = 2ll * p.G * p.blocks * p.B;
-    if (item >= items) return;                       // whole groups leave
-    const int which = (int)(item & 1);
-    const int g = (int)((item >> 1) % p.G);
-    const long long rest = (item >> 1) / p.G;
-    const int b = (int)(rest / p.blocks);
+    const unsigned item = blockIdx.x * (THREADS / TPI) + threadIdx.x / TPI;
+    const unsigned heads = 2u * p.G;
+    if (item >= heads * p.runs * p.B) return;        // whole groups leave
+    const unsigned rest = item / heads, head = item - rest * heads;
+    const int which = head & 1, g = head >> 1;
+    const int b = rest / p.runs, run = rest - b * p.runs;
     const int T = clamp_len(p.lens[b], p.max_pages * p.page_size);
     const int begin = T > p.sq ? T - p.sq : 0;       // first position that gets a new token
-    const long long block = begin / p.size + rest % p.blocks;
-    if (block * p.size >= T) return;
-    const int start = (int)block * p.size;
-    const int page = p.table[(size_t)b * p.max_pages + start / p.page_size];
-    if ((unsigned)page >= (unsigned)p.num_pages) return;
-    const int in_page = start % p.page_size;
-    const int lo = begin > start ? begin : start;
-    const int hi = T < start + p.size ? T : start + p.size;
-    const int kept = lo - start;
-    const size_t unit = (size_t)page * p.G + g;
-    uint8_t* rows = p.pages[which] + (unit * p.page_size + in_page) * D;
-    float* scale_at = p.scale[which] + unit * ((p.page_size + kBlockTokens - 1) / kBlockTokens) + in_page / kBlockTokens;
-    // New token s sits at position T - sq + s.
-    const int s0 = lo - (T - p.sq);
-    const uint16_t* x0 = p.x_new[which] + (((size_t)b * p.sq + s0) * p.G + g) * D;
+    const int block0 = begin / p.size + run * p.per;
+    const int block1 = min(block0 + p.per, min((T + p.size - 1) / p.size, begin / p.size + p.blocks));
+    const int shift = T - p.sq;                      // new token s sits at position shift + s
+    const uint16_t* x = p.x_new[which] + ((size_t)b * p.sq * p.G + g) * D;
     const size_t row_step = (size_t)p.G * D;
+    const int32_t* table = p.table + (size_t)b * p.max_pages;
 
-    const float held = kept > 0 ? *scale_at : 0.f;
-    uint4 v[CHUNKS];
-    float top = 0.f;
-    const int n = (hi - lo) * kRowChunks;
+    // The tokens and the page of a block.
+    uint4 next[CHUNKS];
+    int next_page = -1;
+    auto load = [&](int block) {
+        const int start = block * p.size;
+        const int lo = max(begin, start), hi = min(T, start + p.size);
+        next_page = table[start / p.page_size];
+        const uint16_t* x0 = x + (size_t)(lo - shift) * row_step;
+        const int n = (hi - lo) * kRowChunks;
 #pragma unroll
-    for (int c = 0; c < CHUNKS; ++c) {
-        const int i = t + c * TPI;
-        v[c] = make_uint4(0, 0, 0, 0);
-        if (i < n)
-            v[c] = *reinterpret_cast<const uint4*>(x0 + (i / kRowChunks) * row_step + (i % kRowChunks) * 8);
-    }
-#pragma unroll
-    for (int c = 0; c < CHUNKS; ++c) {
-        float x[8];
-        unpack8(v[c], x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float a = fabsf(x[e]);
-            top = fmaxf(top, a <= 3.4028234664e38f ? a : 0.f);
+        for (int c = 0; c < CHUNKS; ++c) {
+            const int i = t + c * TPI;
+            next[c] = make_uint4(0, 0, 0, 0);
+            if (i < n)
+                next[c] = *reinterpret_cast<const uint4*>(x0 + (i / kRowChunks) * row_step + (i % kRowChunks) * 8);
         }
-    }
-    // Non-negative floats order as their bits do.
-    uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-    if constexpr (TPI > 32) {
-        __shared__ uint32_t part[TPI / 32];
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
-        __syncthreads();
+    };
+    // Largest value of the group; every thread of it has passed its reads then.
+    int turn = 0;
+    auto group_max = [&](uint32_t m) {
+        m = __reduce_max_sync(0xffffffffu, m);
+        if constexpr (TPI > 32) {
+            __shared__ uint32_t part[2][TPI / 32];
+            uint32_t* mine = part[turn];             // the other half may still be read
+            turn ^= 1;
+            if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = m;
+            __syncthreads();
 #pragma unroll
-        for (int w = 0; w < TPI / 32; ++w) m = max(m, part[w]);
-    } else {
-        __syncwarp();                                // every lane has read the scale
-    }
-    top = __uint_as_float(m);
-    const float old = held > 0.f ? held : 0.f;
-    const float scale = old > 0.f && top <= kE4m3Max * old ? old : scale_for(top);
-    const Divider div(scale);
-#pragma unroll
-    for (int c = 0; c < CHUNKS; ++c) {
-        const int i = t + c * TPI;
-        if (i < n) {
-            float x[8];
-            unpack8(v[c], x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = div(finite_or_nan(x[e]));
-            uint2 w;
-            w.x = e4m3x2(x[0], x[1]) | (e4m3x2(x[2], x[3]) << 16);
-            w.y = e4m3x2(x[4], x[5]) | (e4m3x2(x[6], x[7]) << 16);
-            *reinterpret_cast<uint2*>(rows + (size_t)kept * D + (size_t)i * 8) = w;
+            for (int w = 0; w < TPI / 32; ++w) m = max(m, mine[w]);
+        } else {
+            __syncwarp();
         }
-    }
-    if (kept > 0 && scale != old) {
-        const float r = scale > 0.f ? __fdiv_rn(old, scale) : 0.f;
-        for (int i = t; i < kept * (D / 16); i += TPI) {
-            uint4* at = reinterpret_cast<uint4*>(rows) + i;
-            const uint4 c = *at;
-            const uint32_t in[4] = {c.x, c.y, c.z, c.w};
-            uint32_t out[4];
+        return m;
+    };
+    if (block0 < block1) load(block0);
+    for (int block = block0; block < block1; ++block) {
+        uint4 v[CHUNKS];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t y = 0;
+        for (int c = 0; c < CHUNKS; ++c) v[c] = next[c];
+        const int page = next_page;
+        if (block + 1 < block1) load(block + 1);
+        if ((unsigned)page >= (unsigned)p.num_pages) continue;       // the whole group goes on
+        const int start = block * p.size;
+        const int lo = max(begin, start), hi = min(T, start + p.size);
+        const int kept = lo - start, n = (hi - lo) * kRowChunks;
+        const int in_page = start % p.page_size;
+        const size_t unit = (size_t)page * p.G + g;
+        uint8_t* rows = p.pages[which] + (unit * p.page_size + in_page) * D;
+        float* scale_at =
+            p.scale[which] + unit * ((p.page_size + kBlockTokens - 1) / kBlockTokens) + in_page / kBlockTokens;
+        const float held = kept > 0 ? *scale_at : 0.f;
+        // Magnitudes order as their bits do, two at a time. Infinities and NaN
+        // do not count; blocks with one are rare and read their tokens again.
+        uint32_t m2 = 0;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t f = e4m3x2_to_f16x2((uint16_t)(in[q] >> (16 * h)));
-                    const __half2 f2 = *reinterpret_cast<const __half2*>(&f);
-                    const float2 x = __half22float2(f2);
-                    y |= e4m3x2(x.x * r, x.y * r) << (16 * h);
+        for (int c = 0; c < CHUNKS; ++c) {
+            m2 = __vmaxu2(m2, __vmaxu2(v[c].x & 0x7fff7fffu, v[c].y & 0x7fff7fffu));
+            m2 = __vmaxu2(m2, __vmaxu2(v[c].z & 0x7fff7fffu, v[c].w & 0x7fff7fffu));
+        }
+        const uint16_t* x0 = x + (size_t)(lo - shift) * row_step;
+        auto chunk_at = [&](int i) {
+            return *reinterpret_cast<const uint4*>(x0 + (i / kRowChunks) * row_step + (i % kRowChunks) * 8);
+        };
+        uint32_t m = group_max(max(m2 & 0xffffu, m2 >> 16));
+        const bool odd = m >= 0x7f80u;
+        if (odd) {
+            m = 0;
+#pragma unroll 1
+            for (int i = t; i < n; i += TPI) {
+                const uint4 u = chunk_at(i);
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t hi16 = (w[k] >> 16) & 0x7fffu, lo16 = w[k] & 0x7fffu;
+                    m = max(m, max(hi16 < 0x7f80u ? hi16 : 0u, lo16 < 0x7f80u ? lo16 : 0u));
                 }
-                out[q] = y;
             }
-            *at = make_uint4(out[0], out[1], out[2], out[3]);
+            m = group_max(m);
         }
+        const float top = __uint_as_float(m << 16);
+        const float old = held > 0.f ? held : 0.f;
+        const float scale = old > 0.f && top <= kE4m3Max * old ? old : scale_for(top);
+        const Divider div(scale);
+        if (div.pow2 && !odd) {
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c) {
+                const int i = t + c * TPI;
+                if (i < n) {
+                    float x8[8];
+                    unpack8(v[c], x8);
+                    uint2 w;
+                    w.x = e4m3x2(x8[0] * div.inv, x8[1] * div.inv) | (e4m3x2(x8[2] * div.inv, x8[3] * div.inv) << 16);
+                    w.y = e4m3x2(x8[4] * div.inv, x8[5] * div.inv) | (e4m3x2(x8[6] * div.inv, x8[7] * div.inv) << 16);
+                    *reinterpret_cast<uint2*>(rows + (size_t)kept * D + (size_t)i * 8) = w;
+                }
+            }
+        } else {
+#pragma unroll 1
+            for (int i = t; i < n; i += TPI) {
+                float x8[8];
+                unpack8(chunk_at(i), x8);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x8[e] = div(finite_or_nan(x8[e]));
+                uint2 w;
+                w.x = e4m3x2(x8[0], x8[1]) | (e4m3x2(x8[2], x8[3]) << 16);
+                w.y = e4m3x2(x8[4], x8[5]) | (e4m3x2(x8[6], x8[7]) << 16);
+                *reinterpret_cast<uint2*>(rows + (size_t)kept * D + (size_t)i * 8) = w;
+            }
+        }
+        if (kept > 0 && scale != old) {
+            const float r = scale > 0.f ? __fdiv_rn(old, scale) : 0.f;
+            for (int i = t; i < kept * (D / 16); i += TPI) {
+                uint4* at = reinterpret_cast<uint4*>(rows) + i;
+                const uint4 c = *at;
+                const uint32_t in[4] = {c.x, c.y, c.z, c.w};
+                uint32_t out[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t y = 0;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t f = e4m3x2_to_f16x2((uint16_t)(in[q] >> (16 * h)));
+                        const float2 f2 = __half22float2(*reinterpret_cast<const __half2*>(&f));
+                        y |= e4m3x2(f2.x * r, f2.y * r) << (16 * h);
+                    }
+                    out[q] = y;
+                }
+                *at = make_uint4(out[0], out[1], out[2], out[3]);
+            }
+        }
+        if (t == 0) *scale_at = scale;
     }
-    if (t == 0) *scale_at = scale;
 }
 
 template <int D, int TPI, int THREADS, int CHUNKS>
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream) {
-    const long long items = 2ll * p.G * p.blocks * p.B;
+    const long long items = 2ll * p.G * p.runs * p.B;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -236,11 +288,20 @@ extern "C" int gqa_append_paged_fp8(const void* k_new, const void* v_new, void* 
     p.max_pages = max_pages_per_seq;
     p.size = page_size < kBlockTokens ? page_size : kBlockTokens;
     p.blocks = (int)(((long long)sq + p.size - 2) / p.size) + 1;
-    if ((long long)max_pages_per_seq * page_size >= (1ll << 31) - kBlockTokens ||
+    if ((long long)max_pages_per_seq * page_size >= (1ll << 31) - kBlockTokens || sq >= (1 << 30) ||
         2ll * G * p.blocks * B >= (1ll << 31))
         return GQA_ERR_UNSUPPORTED;
     // Up to 8 new tokens a sequence: a warp per block holds them in registers;
-    // beyond that a CTA of 256 threads does.
+    // beyond that a CTA of 256 threads does, and enough blocks go to one CTA
+    // for all of them to be resident at once (four to an SM).
+    int sms;
+    unsigned* status;
+    const int st = current_device(&sms, &status);
+    if (st != GQA_OK) return st;
+    const long long blocks = 2ll * G * p.blocks * B;
+    p.per = sq <= 8 ? 1 : (int)((blocks + 4ll * sms - 1) / (4ll * sms));
+    if (p.per > p.blocks) p.per = p.blocks;
+    p.runs = (p.blocks + p.per - 1) / p.per;
     cudaError_t e;
     if (sq <= 8)
         e = D == 64 ? launch_append<64, 32, 128, 2>(p, stream) : launch_append<128, 32, 128, 4>(p, stream);
