@@ -3,9 +3,14 @@
 //
 // Every call is decided on the device, in one planning kernel, and carried out
 // by a second kernel over the whole GPU that reads the plan from the
-// workspace; the host never waits and a call can be captured into a graph.
+// workspace; the host never waits and a call can be captured into a graph. The
+// planning kernel is one cluster of eight CTAs: what it reads once (counts of
+// up to millions of pages) is shared by 256 warps, and what the warps need of
+// each other (how many free pages lie before mine) goes through distributed
+// shared memory in one exchange.
 // All of it is integer work with one result: pages are taken in ascending
 // order, ranks come from scans, and the only atomics add to integer counts.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -17,12 +22,16 @@
 namespace gqa {
 namespace {
 
+namespace cg = cooperative_groups;
+
+constexpr int kPlanCtas = 8;
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanWarps = kPlanThreads / 32;            // of a CTA
+constexpr int kAllWarps = kPlanCtas * kPlanWarps;
 constexpr int kMoveThreads = 256;
 
 // Workspace, in ints: the header, then the copies' source and destination
-// pages (also the free pages of a reservation), then one new page per row.
+// pages (also the free pages of a reservation), then one number per row.
 constexpr int kWsPairs = 0, kWsOk = 1, kWsLive = 2, kWsHeader = 64;
 struct PageWs {
     int* head;
@@ -84,77 +93,108 @@ __device__ int block_exclusive_sum(int v, int* total) {
     return before + x - v;
 }
 
-// The free (or live) pages of [lo, hi), counted by the CTA: each warp takes a
-// contiguous range. Returns the number before this warp's range and the total.
+// The cluster's warps share the pages in contiguous, ascending ranges. live:
+// pages with a count > 0 before this warp's range, and of all pages.
 struct Ranks {
-    int lo, hi, before, total;
+    int lo, hi, live_before, live;
 };
-__device__ Ranks rank_pages(const int32_t* refs, int lo, int hi, bool live) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int per = ((hi - lo + kPlanWarps - 1) / kPlanWarps + 31) / 32 * 32;
+// Every thread of the cluster, which has called announce_start(); synchronises it
+// (and so orders its global writes).
+__device__ __forceinline__ void announce_start() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ Ranks rank_pages(const int32_t* refs, int num_pages) {
+    __shared__ int warp_live[kPlanWarps];
+    __shared__ int cta_live[kPlanCtas];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = cluster.block_rank();
+    const int per = ((num_pages + kAllWarps - 1) / kAllWarps + 31) / 32 * 32;
     Ranks r;
-    r.lo = min(hi, lo + warp * per);
-    r.hi = min(hi, r.lo + per);
+    r.lo = (int)min((long long)num_pages, (long long)(cta * kPlanWarps + warp) * per);
+    r.hi = min(num_pages, r.lo + per);
     int n = 0;
-    for (int i = r.lo + lane; i < r.hi; i += 32) n += (refs[i] > 0) == live;
+#pragma unroll 8
+    for (int i = r.lo + lane; i < r.hi; i += 32) n += refs[i] > 0;
     n = __reduce_add_sync(0xffffffffu, n);
-    int before = block_exclusive_sum(lane == 0 ? n : 0, &r.total);
-    r.before = __shfl_sync(0xffffffffu, before, 0);
+    if (lane == 0) warp_live[warp] = n;
+    __syncthreads();
+    int before = 0, mine = 0;
+    for (int w = 0; w < kPlanWarps; ++w) {
+        if (w < warp) before += warp_live[w];
+        mine += warp_live[w];
+    }
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // all CTAs have started
+    if (threadIdx.x < kPlanCtas) cluster.map_shared_rank(cta_live, threadIdx.x)[cta] = mine;
+    cluster.sync();
+    r.live = 0;
+    for (int c = 0; c < kPlanCtas; ++c) {
+        if (c < cta) before += cta_live[c];
+        r.live += cta_live[c];
+    }
+    r.live_before = before;
     return r;
 }
 
-// list[k] = the k-th free (or live) page of the ranked range, k < limit.
-__device__ void list_pages(const int32_t* refs, const Ranks& r, bool live, int limit, int* list) {
+// Calls f(page, free pages before it) for the free pages of the warp's range,
+// those with at least `limit` before them excepted.
+template <class F>
+__device__ void each_free(const int32_t* refs, const Ranks& r, int limit, F f) {
     const int lane = threadIdx.x & 31;
-    int at = r.before;
+    int at = r.lo - r.live_before;
     for (int i0 = r.lo; i0 < r.hi && at < limit; i0 += 32) {
         const int i = i0 + lane;
-        const bool mine = i < r.hi && (refs[i] > 0) == live;
+        const bool mine = i < r.hi && refs[i] <= 0;
         const unsigned m = __ballot_sync(0xffffffffu, mine);
         const int k = at + __popc(m & ((1u << lane) - 1));
-        if (mine && k < limit) list[k] = i;
+        if (mine && k < limit) f(i, k);
         at += __popc(m);
     }
 }
 
 // ------------------------------------------------------------------ planning
 
-__global__ void __launch_bounds__(kPlanThreads, 1) reserve_kernel(const PagesParams p) {
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
+    reserve_kernel(const PagesParams p) {
+    announce_start();
     pdl_launch_dependents();
     pdl_wait_primary();
     const PageWs ws = page_ws(p.ws, p.num_pages);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    __shared__ int want[GQA_MAX_PAGE_ROWS];   // missing pages of each row, then those before it
-    for (int b = warp; b < p.B; b += kPlanWarps) {
+    cg::cluster_group cluster = cg::this_cluster();
+    const int lane = threadIdx.x & 31;
+    const int gw = cluster.block_rank() * kPlanWarps + (threadIdx.x >> 5);
+    __shared__ int want[GQA_MAX_PAGE_ROWS];   // missing pages of the rows before each
+    for (int b = gw; b < p.B; b += kAllWarps) {
         const int n = (tokens_of(p, b) + p.page_size - 1) / p.page_size;
         int missing = 0;
+#pragma unroll 4
         for (int j = lane; j < n; j += 32)
             missing += !is_page(p.table_out[(size_t)b * p.max_pages + j], p.num_pages);
         missing = __reduce_add_sync(0xffffffffu, missing);
-        if (lane == 0) want[b] = missing;
+        if (lane == 0) ws.row_page[b] = missing;
     }
-    __syncthreads();
+    const Ranks r = rank_pages(p.refs_out, p.num_pages);
     int need = 0;
     for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
         const int b = b0 + threadIdx.x;
-        const int v = b < p.B ? want[b] : 0;
+        const int v = b < p.B ? ws.row_page[b] : 0;
         int total;
         const int before = block_exclusive_sum(v, &total);
         if (b < p.B) want[b] = need + before;
         need += total;
     }
-    const Ranks r = rank_pages(p.refs_out, 0, p.num_pages, false);
-    if (threadIdx.x == 0) {
+    const int free = p.num_pages - r.live;
+    if (gw == 0 && lane == 0) {
         p.counts[0] = need;
-        p.counts[1] = r.total;
+        p.counts[1] = free;
     }
-    if (need > r.total) return;
-    list_pages(p.refs_out, r, false, need, ws.src);
-    __syncthreads();
-    for (int b = warp; b < p.B; b += kPlanWarps) {
+    if (need == 0 || need > free) return;    // the whole cluster
+    each_free(p.refs_out, r, need, [&](int page, int k) { ws.src[k] = page; });
+    cluster.sync();
+    for (int b = gw; b < p.B; b += kAllWarps) {
         const int n = (tokens_of(p, b) + p.page_size - 1) / p.page_size;
         int at = want[b];
-        for (int j0 = 0; j0 < n; j0 += 32) {
+        const int end = b + 1 < p.B ? want[b + 1] : need;
+        for (int j0 = 0; j0 < n && at < end; j0 += 32) {
             const int j = j0 + lane;
             int32_t* e = p.table_out + (size_t)b * p.max_pages + j;
             const bool mine = j < n && !is_page(*e, p.num_pages);
@@ -169,10 +209,13 @@ __global__ void __launch_bounds__(kPlanThreads, 1) reserve_kernel(const PagesPar
     }
 }
 
-__global__ void __launch_bounds__(kPlanThreads, 1) fork_plan_kernel(const PagesParams p) {
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
+    fork_plan_kernel(const PagesParams p) {
+    announce_start();
     pdl_launch_dependents();
     pdl_wait_primary();
     const PageWs ws = page_ws(p.ws, p.num_pages);
+    const bool writes = cg::this_cluster().block_rank() == 0;
     __shared__ int first[GQA_MAX_PAGE_ROWS];   // the lowest row that goes on from each row
     for (int b = threadIdx.x; b < p.B; b += kPlanThreads) first[b] = p.B;
     __syncthreads();
@@ -180,69 +223,107 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fork_plan_kernel(const PagesP
         const int s = p.src_rows[i];
         if (s >= 0 && s < p.B) atomicMin(&first[s], i);
     }
-    const Ranks r = rank_pages(p.refs, 0, p.num_pages, false);   // synchronises the CTA
-    for (int i = threadIdx.x; i < p.num_pages; i += kPlanThreads) p.refs_out[i] = p.refs[i];
+    const Ranks r = rank_pages(p.refs, p.num_pages);   // synchronises the CTA
+    for (int i = r.lo + (threadIdx.x & 31); i < r.hi; i += 32) p.refs_out[i] = p.refs[i];
+    // Every CTA counts the copies of all rows; the first one notes them.
     int need = 0;
     for (int i0 = 0; i0 < p.B; i0 += kPlanThreads) {
         const int i = i0 + threadIdx.x;
         int old = -1;
+        bool is_first = false;
         if (i < p.B) {
             const int s = p.src_rows[i];
-            if (s >= 0 && s < p.B && first[s] != i) {
+            if (s >= 0 && s < p.B) {
+                is_first = first[s] == i;
                 const int t = tokens_of(p, s);
-                if (t % p.page_size) old = p.table[(size_t)s * p.max_pages + t / p.page_size];
+                if (!is_first && t % p.page_size) old = p.table[(size_t)s * p.max_pages + t / p.page_size];
             }
         }
         const bool copies = is_page(old, p.num_pages);
         int total;
         const int k = need + block_exclusive_sum(copies ? 1 : 0, &total);
-        // Row i's copy is pair k; the second kernel looks its new page up.
-        if (i < p.B) ws.row_page[i] = copies ? k : -1;
-        if (copies && k < p.num_pages) ws.src[k] = old;
+        if (i < p.B && writes) {
+            // The first row of each sequence takes its row as it is: -2.
+            // Another row's copy is pair k, whose new page the second kernel
+            // looks up, or none: -1.
+            ws.row_page[i] = is_first ? -2 : copies ? k : -1;
+            if (copies && k < p.num_pages) ws.src[k] = old;
+        }
         need += total;
     }
-    if (threadIdx.x == 0) {
+    const int free = p.num_pages - r.live;
+    if (writes && threadIdx.x == 0) {
         p.counts[0] = need;
-        p.counts[1] = r.total;
-        ws.head[kWsPairs] = need <= r.total ? need : 0;
-        ws.head[kWsOk] = need <= r.total;
+        p.counts[1] = free;
+        ws.head[kWsPairs] = need <= free ? need : 0;
+        ws.head[kWsOk] = need <= free;
     }
-    if (need <= r.total) list_pages(p.refs, r, false, need, ws.dst);
-    // The first row of each sequence takes its row as it is: marked -2.
-    for (int i = threadIdx.x; i < p.B; i += kPlanThreads) {
-        const int s = p.src_rows[i];
-        if (s >= 0 && s < p.B && first[s] == i) ws.row_page[i] = -2;
-    }
+    if (need <= free) each_free(p.refs, r, need, [&](int page, int k) { ws.dst[k] = page; });
 }
 
-__global__ void __launch_bounds__(kPlanThreads, 1) compact_plan_kernel(const PagesParams p) {
+// With `live` live pages, the free pages below `live` and the live ones from
+// there on are as many, and the k-th of the one takes the k-th of the other. A
+// free page i has i - (live pages before it) free ones before it, so both
+// lists follow from the one exchange; the moved pages are listed in descending
+// order, since it is the live pages behind a page that a warp knows.
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
+    compact_plan_kernel(const PagesParams p) {
+    announce_start();
     pdl_launch_dependents();
     pdl_wait_primary();
     const PageWs ws = page_ws(p.ws, p.num_pages);
-    const int live = rank_pages(p.refs, 0, p.num_pages, true).total;
-    const Ranks holes = rank_pages(p.refs, 0, live, false);
-    const Ranks movers = rank_pages(p.refs, live, p.num_pages, true);   // as many as there are holes
-    list_pages(p.refs, holes, false, holes.total, ws.dst);
-    list_pages(p.refs, movers, true, movers.total, ws.src);
-    if (threadIdx.x == 0) {
-        p.counts[0] = movers.total;
-        p.counts[1] = live;
-        ws.head[kWsPairs] = movers.total;
-        ws.head[kWsLive] = live;
+    const int lane = threadIdx.x & 31;
+    const Ranks r = rank_pages(p.refs, p.num_pages);
+    int at = r.live_before;
+    for (int i0 = r.lo; i0 < r.hi; i0 += 32) {
+        const int i = i0 + lane;
+        const bool live = i < r.hi && p.refs[i] > 0;
+        const unsigned m = __ballot_sync(0xffffffffu, live);
+        const int before = at + __popc(m & ((1u << lane) - 1));
+        if (i < r.hi && !live && i < r.live) ws.dst[i - before] = i;
+        if (live && i >= r.live) ws.src[r.live - 1 - before] = i;
+        // The page before the boundary knows how many lie behind it.
+        if (i < r.hi && i == r.live - 1) {
+            const int moved = r.live - before - (live ? 1 : 0);
+            ws.head[kWsPairs] = moved;
+            p.counts[0] = moved;
+        }
+        at += __popc(m);
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        p.counts[1] = r.live;
+        ws.head[kWsLive] = r.live;
+        if (r.live == 0) ws.head[kWsPairs] = p.counts[0] = 0;
     }
 }
 
 // ------------------------------------------------------------ carrying it out
 
+// One warp's copy of at most kPiece bytes; 16-byte pieces load all before they
+// store, so that a warp has 4 KB under way.
+constexpr size_t kPiece = 4096;
 template <class T>
 __device__ __forceinline__ void copy_bytes(char* dst, const char* src, size_t bytes, int lane) {
-    const size_t n = bytes / sizeof(T);
-    for (size_t i = lane; i < n; i += 32) reinterpret_cast<T*>(dst)[i] = reinterpret_cast<const T*>(src)[i];
+    const int n = (int)(bytes / sizeof(T));
+    const T* from = reinterpret_cast<const T*>(src);
+    T* to = reinterpret_cast<T*>(dst);
+    if constexpr (sizeof(T) == 16) {
+        constexpr int kAtOnce = (int)(kPiece / 16 / 32);
+        T v[kAtOnce];
+#pragma unroll
+        for (int c = 0; c < kAtOnce; ++c)
+            if (lane + 32 * c < n) v[c] = __ldcs(from + lane + 32 * c);
+#pragma unroll
+        for (int c = 0; c < kAtOnce; ++c)
+            if (lane + 32 * c < n) __stcs(to + lane + 32 * c, v[c]);
+    } else {
+        for (int i = lane; i < n; i += 32) to[i] = from[i];
+    }
 }
 
 // Pages src[k] -> dst[k], k < n, of every layer of every pool; one warp takes
 // one piece of a page at a time.
-constexpr size_t kPiece = 4096;
+template <bool SRC_DESCENDING>
 __device__ void copy_pages(const PoolSet& pools, const int* src, const int* dst, int n, int num_pages) {
     const int lane = threadIdx.x & 31;
     const long long warp = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
@@ -254,7 +335,7 @@ __device__ void copy_pages(const PoolSet& pools, const int* src, const int* dst,
         for (long long it = warp; it < items; it += warps) {
             const long long piece = it % pieces, rest = it / pieces;
             const int k = (int)(rest / pool.layers), layer = (int)(rest % pool.layers);
-            const int a = src[k], b = dst[k];
+            const int a = src[SRC_DESCENDING ? n - 1 - k : k], b = dst[k];
             if (!is_page(a, num_pages) || !is_page(b, num_pages)) continue;
             char* base = static_cast<char*>(pool.base) + (size_t)layer * pool.layer_bytes + piece * kPiece;
             const char* from = base + (size_t)a * pool.page_bytes;
@@ -276,7 +357,7 @@ __global__ void __launch_bounds__(kMoveThreads) copy_kernel(const __grid_constan
                                                             int num_pages) {
     pdl_launch_dependents();
     pdl_wait_primary();
-    copy_pages(pools, src, dst, n, num_pages);
+    copy_pages<false>(pools, src, dst, n, num_pages);
 }
 
 __global__ void __launch_bounds__(kMoveThreads) fork_kernel(const __grid_constant__ PoolSet pools,
@@ -313,7 +394,7 @@ __global__ void __launch_bounds__(kMoveThreads) fork_kernel(const __grid_constan
             p.lens_out[i] = !ok ? p.lens[i] : (s >= 0 && s < p.B ? tokens_of(p, s) : 0);
         }
     }
-    copy_pages(pools, ws.src, ws.dst, ws.head[kWsPairs], p.num_pages);
+    copy_pages<false>(pools, ws.src, ws.dst, ws.head[kWsPairs], p.num_pages);
 }
 
 __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const __grid_constant__ PoolSet pools,
@@ -327,21 +408,21 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const __grid_cons
     for (long long x = t0; x < (long long)p.B * p.max_pages; x += stride) {
         int e = p.table[x];
         if (is_page(e, p.num_pages) && e >= live) {
-            // The moved pages are listed in ascending order. An entry whose
+            // The moved pages are listed in descending order. An entry whose
             // page has no reference is none of them and stays.
             int lo = 0, hi = pairs;
             while (lo < hi) {
                 const int mid = (lo + hi) >> 1;
-                if (ws.src[mid] < e) lo = mid + 1; else hi = mid;
+                if (ws.src[mid] > e) lo = mid + 1; else hi = mid;
             }
-            if (lo < pairs && ws.src[lo] == e) e = ws.dst[lo];
+            if (lo < pairs && ws.src[lo] == e) e = ws.dst[pairs - 1 - lo];
         }
         p.table_out[x] = e;
     }
     // In place, the counts of a moved page's two ends belong to its own thread
     // alone; every other thread may rewrite what it read.
     for (long long k = t0; k < pairs; k += stride) {
-        const int a = ws.src[k], b = ws.dst[k], n = p.refs[a];
+        const int a = ws.src[pairs - 1 - k], b = ws.dst[k], n = p.refs[a];
         p.refs_out[b] = n;
         p.refs_out[a] = 0;
     }
@@ -351,7 +432,7 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const __grid_cons
             if ((n > 0) == (i < live)) p.refs_out[i] = n;
         }
     }
-    copy_pages(pools, ws.src, ws.dst, pairs, p.num_pages);
+    copy_pages<true>(pools, ws.src, ws.dst, pairs, p.num_pages);
 }
 
 __global__ void __launch_bounds__(kMoveThreads) free_kernel(const uint8_t* done, const PagesParams p) {
@@ -472,7 +553,7 @@ int gqa_pages_reserve(int32_t* block_table, const int32_t* seq_lens, int32_t* re
     p.max_pages = max_pages_per_seq;
     p.page_size = page_size;
     p.num_pages = num_pages;
-    return launch(reserve_kernel, 1, kPlanThreads, stream, p);
+    return launch(reserve_kernel, kPlanCtas, kPlanThreads, stream, p);
 }
 
 int gqa_pages_fork(const gqa_page_pool_t* pools, int num_pools, const int32_t* src, const int32_t* block_table,
@@ -499,7 +580,7 @@ int gqa_pages_fork(const gqa_page_pool_t* pools, int num_pools, const int32_t* s
     if (st != GQA_OK) return st;
     const PagesParams p = {src, block_table, seq_lens, ref_counts, table_out, lens_out, refs_out, counts,
                            workspace, B, max_pages_per_seq, page_size, num_pages};
-    st = launch(fork_plan_kernel, 1, kPlanThreads, stream, p);
+    st = launch(fork_plan_kernel, kPlanCtas, kPlanThreads, stream, p);
     if (st != GQA_OK) return st;
     return launch(fork_kernel, move_grid(set, B, (long long)B * max_pages_per_seq, sms), kMoveThreads, stream,
                   set, p);
@@ -557,7 +638,7 @@ int gqa_pages_compact(const gqa_page_pool_t* pools, int num_pools, const int32_t
     p.B = B;
     p.max_pages = max_pages_per_seq;
     p.num_pages = num_pages;
-    st = launch(compact_plan_kernel, 1, kPlanThreads, stream, p);
+    st = launch(compact_plan_kernel, kPlanCtas, kPlanThreads, stream, p);
     if (st != GQA_OK) return st;
     return launch(compact_kernel, move_grid(set, num_pages / 2, (long long)B * max_pages_per_seq, sms),
                   kMoveThreads, stream, set, p);
