@@ -50,7 +50,6 @@ namespace gqa {
 constexpr int kP8LenCopy = 384;           // sequences whose lengths a CTA keeps
 constexpr int kP8ScaleChunk = 4;          // tiles whose scales are fetched together,
 constexpr int kP8ScaleChunks = 8;         // and how many such chunks a CTA keeps
-constexpr int kP8SmallEntries = 128;      // entries that each warp plans by itself
 constexpr int kP8Terms = 4;               // e5m2 columns per probability
 constexpr float kP8Slack = 4.0f;          // p <= 2^4 before the reference moves
 constexpr float kP8ProbScale = 2048.0f;   // p * v_scale * 2^-ev * 2048 <= 16 * 1.75 * 2048 = 57344
@@ -224,7 +223,7 @@ struct P8Lens {
     __device__ int global(int b) const { return clamp_len(p.lens[b], p.max_pages << p.page_shift); }
     __device__ int tokens(int b) const { return p.B <= kP8LenCopy ? copy[b] : global(b); }
     __device__ void split(int entry, int& b, int& rt) const {
-        b = p.row_tiles == 1 ? entry : entry / p.row_tiles;
+        b = p.by_row_tiles(entry);
         rt = entry - b * p.row_tiles;
     }
     __device__ int tiles(int entry) const {
@@ -233,7 +232,7 @@ struct P8Lens {
         const int T = tokens(b);
         if (p.row_tiles == 1) return (T + kP8Tokens - 1) / kP8Tokens;
         const int last = min(p.R, (rt + 1) * RP) - 1;
-        const int lim = T - p.sq + last / p.heads_per_group;
+        const int lim = T - p.sq + p.by_heads(last);
         return lim < 0 ? 0 : lim / kP8Tokens + 1;
     }
 };
@@ -249,7 +248,10 @@ struct P8Walk {
     __device__ bool next(const P8Lens<RP>& lens, P8Segment& s) {
         if (left <= 0) return false;
         int n = lens.tiles(entry);
-        while (n == 0) n = lens.tiles(++entry);
+        while (n == 0) {
+            if (++entry >= lens.p.B * lens.p.row_tiles) return false;   // not with one copy of the lengths
+            n = lens.tiles(entry);
+        }
         s.entry = entry;
         s.g = g;
         s.i0 = off;
@@ -277,31 +279,18 @@ struct P8Plan {
 };
 
 // Up to 128 entries, and 32-bit products of tiles and CTAs: every warp finds
-// the CTA's share by itself, four entries a lane, so that no warp waits for
-// another. Each warp also writes the (same) copy of the lengths.
+// the CTA's share by itself, four entries a lane, from the CTA's one copy of
+// the lengths (all warps have to walk the same tiles).
 template <int RP>
-__device__ __forceinline__ P8Plan p8_small_plan(const P8Lens<RP>& lens, int* len_copy) {
+__device__ __forceinline__ P8Plan p8_small_plan(const P8Lens<RP>& lens) {
     const PagedFp8Params& p = lens.p;
     const int lane = threadIdx.x & 31;
     const int entries = p.B * p.row_tiles;
     unsigned n[4], mine = 0;
-    if (p.row_tiles == 1) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int e = lane * 4 + k;
-            const int T = e < p.B ? lens.global(e) : 0;
-            if (e < p.B) len_copy[e] = T;
-            n[k] = (unsigned)(T + kP8Tokens - 1) / kP8Tokens;
-            mine += n[k];
-        }
-    } else {
-        for (int b = lane; b < p.B; b += 32) len_copy[b] = lens.global(b);
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            n[k] = lane * 4 + k < entries ? (unsigned)lens.tiles(lane * 4 + k) : 0;
-            mine += n[k];
-        }
+    for (int k = 0; k < 4; ++k) {
+        n[k] = lane * 4 + k < entries ? (unsigned)lens.tiles(lane * 4 + k) : 0;
+        mine += n[k];
     }
     mine *= (unsigned)p.G;
     unsigned x = mine;
@@ -311,15 +300,22 @@ __device__ __forceinline__ P8Plan p8_small_plan(const P8Lens<RP>& lens, int* len
         if (lane >= o) x += y;
     }
     const unsigned total = __shfl_sync(0xffffffffu, x, 31), before = x - mine;
-    const unsigned most = total / kP8MinTiles;
-    unsigned ctas = most < 1 ? 1 : most < gridDim.x ? most : gridDim.x;
-    // Equal lengths: the host's grid that no unit crosses unevenly.
+    // A CTA for every unit, or for every eight tiles.
+    const unsigned units = (unsigned)entries * p.G;
+    unsigned ctas = min(min(gridDim.x, max(units, total / kP8MinTiles)), max(total, 1u));
+    // Equal lengths: whole units per CTA, or the same number of CTAs per unit,
+    // where that keeps four fifths of them; no unit is then cut unevenly.
     unsigned lo = 0xffffffffu, hi = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         if (lane * 4 + k < entries) lo = min(lo, n[k]), hi = max(hi, n[k]);
-    if (__reduce_min_sync(0xffffffffu, lo) == __reduce_max_sync(0xffffffffu, hi) && (unsigned)p.even_ctas <= most)
-        ctas = (unsigned)p.even_ctas;
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lo == hi && hi > 0) {                     // the same in every lane, as all that follows
+        const unsigned per = (units + ctas - 1) / ctas;
+        const unsigned even = per > 1 ? (units % per == 0 ? units / per : 0) : units * (ctas / units);
+        if (5 * even >= 4 * ctas) ctas = even;
+    }
     const unsigned c = blockIdx.x;
     const unsigned t0 = c < ctas ? total * c / ctas : total, t1 = c < ctas ? total * (c + 1) / ctas : total;
     // The lane whose entries hold tile t0, and where in them it lies.
@@ -382,8 +378,8 @@ __device__ __noinline__ void p8_make_plan(const PagedFp8Params& p, int* len_copy
         if (w < warp) before += warp_sum[w];
         total += warp_sum[w];
     }
-    const long long most = total / kP8MinTiles;
-    const int ctas = most < 1 ? 1 : most < (long long)gridDim.x ? (int)most : (int)gridDim.x;
+    const long long most = max((long long)entries * p.G, total / kP8MinTiles);
+    const int ctas = (int)max(1ll, min(min((long long)gridDim.x, most), total));
     const int c = blockIdx.x;
     const long long t0 = c < ctas ? muldiv(total, c, ctas) : total;
     const long long t1 = c < ctas ? muldiv(total, c + 1, ctas) : total;
@@ -431,7 +427,7 @@ template <int RP>
 __device__ __forceinline__ int p8_out_row(const PagedFp8Params& p, int b, int rt, int g, int r, int* s_tok) {
     const int rr = rt * RP + r;
     if (rr >= p.R) return -1;
-    const int s = rr / p.heads_per_group;
+    const int s = p.by_heads(rr);
     *s_tok = s;
     return (b * p.sq + s) * p.H + g * p.heads_per_group + (rr - s * p.heads_per_group);
 }
@@ -642,7 +638,9 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
     pdl_wait_primary();
     P8Walk<RP> walk;
     if (p.small_plan) {
-        const P8Plan plan = p8_small_plan<RP>(lens, len_copy);
+        if ((int)threadIdx.x < p.B) len_copy[threadIdx.x] = lens.global(threadIdx.x);
+        __syncthreads();
+        const P8Plan plan = p8_small_plan<RP>(lens);
         // Kept in shared memory (every warp writes the same) rather than in
         // registers until a split unit's end needs it.
         if (lane == 0) *plan_s = plan;
@@ -1010,7 +1008,7 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
             const float4* scale4 = reinterpret_cast<const float4*>(row_scale + (sg & 1) * RP + y * RH);
             const int* lim = row_lim + (sg & 1) * RP + y * RH;
             const int lim_min =                                             // every row sees keys up to here
-                p.row_tiles == 1 ? T - p.sq : T - p.sq + (rt * RP) / p.heads_per_group;
+                T - p.sq + p.by_heads(rt * RP);
             const int first_i = seg.i0 + ((it0 & 1) != x ? 1 : 0);          // this group's first tile
             float l[RH];
             int ev = 0;
@@ -1301,8 +1299,9 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
                         named_sync(bar, 128);
                         if (tok == 0) {
                             __threadfence();      // of the group's stores, which the barrier ordered before
-                            last_flag[bar - 1] = arrive_last(p.counters + (size_t)c0 * PS::kParts + y, p.tag, n);
-                            __threadfence();
+                            const bool last = arrive_last(p.counters + (size_t)c0 * PS::kParts + y, p.tag, n);
+                            if (last) __threadfence();
+                            last_flag[bar - 1] = last;
                         }
                         named_sync(bar, 128);
                         if (last_flag[bar - 1]) {

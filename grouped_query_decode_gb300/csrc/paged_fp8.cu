@@ -28,19 +28,8 @@ int paged_fp8_grid(int B, int G, int R, int page_size, int max_pages, int sms) {
     const int rows = p8_rows(R);
     const long long units = (long long)B * G * ((R + rows - 1) / rows);
     const long long tiles = ((long long)max_pages * page_size + kP8Tokens - 1) / kP8Tokens;
-    const long long want = units * tiles / kP8MinTiles;
-    return (int)(want < 1 ? 1 : want < sms ? want : sms);
-}
-
-// CTAs for sequences of one length: whole units per CTA, or the same number of
-// CTAs per unit, where that keeps four fifths of the grid busy.
-int even_grid(long long units, int grid) {
-    if (units >= grid) {
-        const long long per = (units + grid - 1) / grid, even = (units + per - 1) / per;
-        return units % per == 0 && 5 * even >= 4ll * grid ? (int)even : grid;
-    }
-    const long long even = units * (grid / units);
-    return 5 * even >= 4ll * grid ? (int)even : grid;
+    const long long split = units * tiles / kP8MinTiles, want = split > units ? split : units;
+    return (int)(want < sms ? want : sms);
 }
 
 size_t counter_bytes(int grid) { return (sizeof(unsigned long long) * 2 * (size_t)grid + 255) & ~size_t(255); }
@@ -120,7 +109,8 @@ int gqa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages
     p.num_pages = num_pages;
     p.max_pages = max_pages_per_seq;
     p.blocks = (page_size + 63) / 64;
-    p.even_ctas = even_grid((long long)B * G * p.row_tiles, grid);
+    p.by_heads = FastDiv((unsigned)p.heads_per_group);
+    p.by_row_tiles = FastDiv((unsigned)p.row_tiles);
     const long long tiles = ((long long)max_pages_per_seq * page_size + kP8Tokens - 1) / kP8Tokens;
     p.small_plan = (long long)B * p.row_tiles <= 128 && (long long)B * p.row_tiles * G * tiles * (grid + 1) < (1ll << 32);
     a.grid = grid;

@@ -149,6 +149,15 @@ def test_long_and_split(page, D, T):
     check(c, *run(c))
 
 
+@pytest.mark.parametrize("B,H,G,T,page", [(16, 32, 8, 1100, 64), (5, 16, 16, 1500, 32), (64, 16, 1, 1030, 16), (38, 8, 8, 300, 64),
+                                          (128, 4, 2, 130, 16), (129, 4, 2, 130, 16), (400, 2, 1, 100, 32)], ids=str)
+def test_equal_lengths(B, H, G, T, page):
+    """Batches of one length, whose grid leaves SMs idle so that no unit is cut
+    unevenly; and batches on each side of the per-warp plan's size."""
+    c = Case(450 + B, B, 1, H, G, 128, page, [T] * B)
+    check(c, *run(c))
+
+
 @pytest.mark.parametrize("lens", [[1], [2], [3], [128], [127, 1, 0, 300]])
 @pytest.mark.parametrize("sq", [1, 4])
 def test_short_sequences_and_rows_without_a_key(lens, sq):
