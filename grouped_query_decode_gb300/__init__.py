@@ -334,13 +334,26 @@ def _paged_fp8_cache(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens):
     return table[0], num_pages, G, page_size, D, table[1]
 
 
-def _workspace(nbytes, like, stream):
-    """A buffer for one call from torch's allocator, on the device of `like`, in
-    the order of the call's stream (inside a graph capture, the graph's own
-    memory)."""
+# Workspaces of the calls that take theirs from torch's allocator, one per
+# (device, stream handle), grow-only: calls on a stream run in order.
+_workspaces = {}
+
+
+def _workspace(nbytes, like, dev, stream):
+    """A buffer for one call on the device of `like`, in the order of the call's
+    stream. A call on the current stream takes the stream's own, kept from call
+    to call; a call that is being captured takes new memory of its graph, which
+    no other graph shares; one on a stream passed as an argument takes new
+    memory too."""
     import torch
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        if torch._C._cuda_getDevice() != dev or torch._C._cuda_isCurrentStreamCapturing():
+            return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        key = (dev, torch._C._cuda_getCurrentRawStream(dev))
+        buf = _workspaces.get(key)
+        if buf is None or buf.shape[0] < nbytes:
+            buf = _workspaces[key] = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        return buf
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=like.device)
     with torch.cuda.stream(stream):
@@ -353,8 +366,9 @@ def gqa_decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seq
     k_pages/v_pages [num_pages, G, page_size, D] uint8 e4m3 codes, k_scale/
     v_scale [num_pages, G, ceil(page_size/64)] float32, block_table [B,
     max_pages_per_seq] int32. The workspace (a CUDA uint8 tensor of
-    gqa_decode_paged_fp8_workspace_bytes(...)) is taken from torch's allocator
-    when not given."""
+    gqa_decode_paged_fp8_workspace_bytes(...)) comes from torch's allocator when
+    not given: the stream's own, kept from call to call, or memory of the graph
+    being captured."""
     import torch
     dev = q.get_device()
     bf, u8, f32, i32 = torch.bfloat16, torch.uint8, torch.float32, torch.int32
@@ -376,7 +390,7 @@ def gqa_decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seq
     if lse is not None and lse.shape != (B, sq, H):
         raise ValueError("lse must be [B, sq, H]")
     if workspace is None:
-        workspace = _workspace(_paged_fp8_workspace_bytes(B, sq, H, G, D, page_size, most, dev) or 256, q, stream)
+        workspace = _workspace(_paged_fp8_workspace_bytes(B, sq, H, G, D, page_size, most, dev) or 256, q, dev, stream)
     rc = _call(dev, load().gqa_decode_paged_fp8, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
                k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
                float(scale), out.data_ptr(), None if lse is None else lse.data_ptr(), B, sq, H, G, D,
@@ -483,7 +497,7 @@ def gqa_pages_reserve(block_table, seq_lens, ref_counts, page_size, counts, stre
     _check_all(dev, (("block_table", block_table, i32), ("seq_lens", seq_lens, i32), ("ref_counts", ref_counts, i32),
                      ("counts", counts, i32)))
     B, most, num_pages = _page_sizes(block_table, seq_lens, ref_counts, counts)
-    ws = _workspace(gqa_pages_workspace_bytes(B, num_pages) or 256, block_table, stream)
+    ws = _workspace(gqa_pages_workspace_bytes(B, num_pages) or 256, block_table, dev, stream)
     rc = _call(dev, load().gqa_pages_reserve, block_table.data_ptr(), seq_lens.data_ptr(),
                ref_counts.data_ptr(), counts.data_ptr(), B, most, page_size, num_pages, ws.data_ptr(),
                ws.numel(), _raw_stream(stream, dev))
@@ -512,7 +526,7 @@ def gqa_pages_fork(pools, src, block_table, seq_lens, ref_counts, page_size, blo
     if src.shape != (B,):
         raise ValueError("src must be [B]")
     arr, n = _page_pools(dev, pools, num_pages, page_dim)
-    ws = _workspace(gqa_pages_workspace_bytes(B, num_pages) or 256, block_table, stream)
+    ws = _workspace(gqa_pages_workspace_bytes(B, num_pages) or 256, block_table, dev, stream)
     rc = _call(dev, load().gqa_pages_fork, arr, n, src.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
                ref_counts.data_ptr(), block_table_out.data_ptr(), seq_lens_out.data_ptr(),
                ref_counts_out.data_ptr(), counts.data_ptr(), B, most, page_size, num_pages, ws.data_ptr(),
@@ -551,7 +565,7 @@ def gqa_pages_compact(pools, block_table, ref_counts, block_table_out, ref_count
     if block_table_out.shape != block_table.shape or ref_counts_out.shape != ref_counts.shape:
         raise ValueError("the outputs must have the inputs' shapes")
     arr, n = _page_pools(dev, pools, num_pages, page_dim)
-    ws = _workspace(gqa_pages_workspace_bytes(B, num_pages) or 256, block_table, stream)
+    ws = _workspace(gqa_pages_workspace_bytes(B, num_pages) or 256, block_table, dev, stream)
     rc = _call(dev, load().gqa_pages_compact, arr, n, block_table.data_ptr(), ref_counts.data_ptr(),
                block_table_out.data_ptr(), ref_counts_out.data_ptr(), counts.data_ptr(), B, most, num_pages,
                ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
@@ -594,12 +608,14 @@ def gqa_decode_noalloc(q, k_cache, v_cache, seq_lens, scale, out, lse=None, stre
 
 
 def gqa_decode_release_workspace(stream=None, device=None) -> None:
-    """Frees the library-owned workspace of (device, stream) after the work
-    queued on the stream; the next call on that stream allocates again."""
+    """Frees the workspaces kept for (device, stream) after the work queued on
+    the stream; the next call on that stream allocates again."""
     import torch
     if device is None:
         device = stream.device_index if hasattr(stream, "device_index") else torch.cuda.current_device()
-    rc = _call(device, load().gqa_decode_release_workspace, _stream_handle(stream, device))
+    handle = _stream_handle(stream, device)
+    _workspaces.pop((device, handle.value or 0), None)
+    rc = _call(device, load().gqa_decode_release_workspace, handle)
     if rc != GQA_OK:
         raise GQADecodeError(rc, "gqa_decode_release_workspace")
 

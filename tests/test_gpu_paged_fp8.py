@@ -347,6 +347,26 @@ def test_streams_graphs_and_dirty_workspaces():
     assert e.value.status == gq.GQA_ERR_WORKSPACE
 
 
+def test_kept_workspaces_grow_and_are_released():
+    """Calls on one stream share a workspace that grows; releasing it, and calls
+    with streams as arguments, change no result."""
+    small = Case(645, 1, 1, 8, 2, 64, 16, [40])
+    large = Case(646, 4, 4, 64, 8, 128, 64, [3000, 2500, 17, 900])
+    devs = [small.device(), large.device()]
+    refs = [run(small, devs[0]), run(large, devs[1])]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for rep in range(3):
+        gq.gqa_decode_release_workspace()
+        for c, d, ref in zip((small, large, small), (devs[0], devs[1], devs[0]), (refs[0], refs[1], refs[0])):
+            for kw in ({}, dict(stream=side), dict(stream=side.cuda_stream)):
+                got = run(c, d, **kw)
+                assert np.array_equal(got[0], ref[0]) and np.array_equal(got[1], ref[1])
+        with torch.cuda.stream(side):
+            got = run(large, devs[1])
+        assert np.array_equal(got[0], refs[1][0])
+
+
 def test_replay_with_new_lengths_and_pages():
     c = Case(650, 2, 2, 16, 2, 64, 16, [400, 400])
     d = c.device()
