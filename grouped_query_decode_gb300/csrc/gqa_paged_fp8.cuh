@@ -287,11 +287,18 @@ __device__ __forceinline__ P8Plan p8_small_plan(const P8Lens<RP>& lens) {
     const int lane = threadIdx.x & 31;
     const int entries = p.B * p.row_tiles;
     unsigned n[4], mine = 0;
+    if (p.row_tiles == 1) {
+        const int4 T = reinterpret_cast<const int4*>(lens.copy)[lane];      // 0 past the batch
+        n[0] = ((unsigned)T.x + kP8Tokens - 1) / kP8Tokens;
+        n[1] = ((unsigned)T.y + kP8Tokens - 1) / kP8Tokens;
+        n[2] = ((unsigned)T.z + kP8Tokens - 1) / kP8Tokens;
+        n[3] = ((unsigned)T.w + kP8Tokens - 1) / kP8Tokens;
+    } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        n[k] = lane * 4 + k < entries ? (unsigned)lens.tiles(lane * 4 + k) : 0;
-        mine += n[k];
+        for (int k = 0; k < 4; ++k) n[k] = lane * 4 + k < entries ? (unsigned)lens.tiles(lane * 4 + k) : 0;
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mine += n[k];
     mine *= (unsigned)p.G;
     unsigned x = mine;
 #pragma unroll
@@ -493,14 +500,14 @@ __device__ __noinline__ void p8_merge(const PagedFp8Params& p, int c0, int n, in
         const int item = j * 128 + tok, d = item % (D / 4) * 4, orow = rows_out[item / (D / 4)];
         if (orow < 0) continue;
         const bool some = l[j] > 0.f || l[j] != l[j];
-        const float inv = 1.f / l[j];
+        const float inv = __fdividef(1.f, l[j]);
         uint2 o = make_uint2(0, 0);
         if (some) {
             o.x = pack_bf16x2(y[j][0] * inv, y[j][1] * inv);
             o.y = pack_bf16x2(y[j][2] * inv, y[j][3] * inv);
         }
         *reinterpret_cast<uint2*>(p.out + (size_t)orow * D + d) = o;
-        if (p.lse && d == 0) p.lse[orow] = some ? (top[j] + log2f(l[j])) * 0.6931471805599453f : -INFINITY;
+        if (p.lse && d == 0) p.lse[orow] = some ? (top[j] + __log2f(l[j])) * 0.6931471805599453f : -INFINITY;
     }
 }
 
@@ -552,6 +559,14 @@ __device__ __forceinline__ bool arrive_last(unsigned long long* counter, unsigne
     if (count != n) return false;
     atomicExch(counter, zero);
     return true;
+}
+
+// Gives a counter the call's tag ahead of its arrivals, which then take one
+// atomic each instead of three. No arrival is lost: one whose add this
+// overwrites finds the tag and adds again.
+__device__ __forceinline__ void tag_counter(unsigned long long* counter, unsigned long long tag) {
+    const unsigned long long seen = *reinterpret_cast<volatile unsigned long long*>(counter);
+    if (seen >> 16 != tag) atomicCAS(counter, seen, tag << 16);
 }
 
 template <int D, int RP>
@@ -638,7 +653,7 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
     pdl_wait_primary();
     P8Walk<RP> walk;
     if (p.small_plan) {
-        if ((int)threadIdx.x < p.B) len_copy[threadIdx.x] = lens.global(threadIdx.x);
+        if (threadIdx.x < 128) len_copy[threadIdx.x] = (int)threadIdx.x < p.B ? lens.global(threadIdx.x) : 0;
         __syncthreads();
         const P8Plan plan = p8_small_plan<RP>(lens);
         // Kept in shared memory (every warp writes the same) rather than in
@@ -852,6 +867,10 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
                 ++sg;
             }
         } else {
+            // This warp has nothing to do until the first P: the counters of the
+            // unit that this CTA may start.
+            if (lane < PS::kParts) tag_counter(p.counters + (size_t)blockIdx.x * PS::kParts + lane, p.tag);
+            __syncwarp();
             constexpr uint32_t kIdesc = p8_idesc(D, PS::kNp, true, true, true);
             const uint64_t v_desc = p8_desc(v_s, 16, kAtom, kLayout), p_desc = p8_desc(p_s, 128, 2048, 0);
             while (ok && walk.next(lens, seg)) {
@@ -1262,11 +1281,11 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
                         }
                         if (whole) {
                             const bool some = ls > 0.f || ls != ls;
-                            const float inv = some ? 1.f / ls : 0.f;
+                            const float inv = some ? __fdividef(1.f, ls) : 0.f;
                             a0 *= inv;
                             a1 *= inv;
                             if (p.lse && rows_out[tok] >= 0)
-                                p.lse[rows_out[tok]] = some ? (m + log2f(ls)) * 0.6931471805599453f : -INFINITY;
+                                p.lse[rows_out[tok]] = some ? (m + __log2f(ls)) * 0.6931471805599453f : -INFINITY;
                         } else {
                             slot[RP * D + y * RH + tok] = m;
                             slot[RP * D + RP + y * RH + tok] = ls;
