@@ -212,6 +212,33 @@ __device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((
 
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }   // |e| <= 126
 
+// Two fp32 operations in one instruction, each rounded as by itself.
+__device__ __forceinline__ float2 fma_x2(float2 a, float2 b, float2 c) {
+    unsigned long long x, y, z, d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c.x), "f"(c.y));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(d));
+    return a;
+}
+__device__ __forceinline__ float2 mul_x2(float2 a, float2 b) {
+    unsigned long long x, y, d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(d));
+    return a;
+}
+__device__ __forceinline__ float2 add_x2(float2 a, float2 b) {
+    unsigned long long x, y, d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(d));
+    return a;
+}
+
 // ---------------------------------------------------------------------- plan
 
 // Lengths, from the CTA's copy where the batch fits it, and the tiles that the
@@ -1060,17 +1087,28 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
                         tmem_ld16x2(s_tm, s_tm + RP, h, lo);
                     }
 #pragma unroll
-                    for (int r = 0; r < RH; ++r) sv[r] = fmaf(__uint_as_float(lo[r]), 0.0625f, __uint_as_float(h[r]));
+                    for (int r = 0; r < RH; r += 2) {
+                        const float2 v = fma_x2(make_float2(__uint_as_float(lo[r]), __uint_as_float(lo[r + 1])),
+                                                make_float2(0.0625f, 0.0625f),
+                                                make_float2(__uint_as_float(h[r]), __uint_as_float(h[r + 1])));
+                        sv[r] = v.x;
+                        sv[r + 1] = v.y;
+                    }
                 };
                 auto subtract_refs = [&]() {
 #pragma unroll
                     for (int r = 0; r < RH; r += 4) {
                         const float4 f = scale4[r / 4];
                         const float4 m = *reinterpret_cast<const float4*>(my_ref + r);
-                        z[r] = fmaf(sv[r], f.x * ks, m.x);
-                        z[r + 1] = fmaf(sv[r + 1], f.y * ks, m.y);
-                        z[r + 2] = fmaf(sv[r + 2], f.z * ks, m.z);
-                        z[r + 3] = fmaf(sv[r + 3], f.w * ks, m.w);
+                        const float2 kk = make_float2(ks, ks);
+                        const float2 a = fma_x2(make_float2(sv[r], sv[r + 1]), mul_x2(make_float2(f.x, f.y), kk),
+                                                make_float2(m.x, m.y));
+                        const float2 c = fma_x2(make_float2(sv[r + 2], sv[r + 3]), mul_x2(make_float2(f.z, f.w), kk),
+                                                make_float2(m.z, m.w));
+                        z[r] = a.x;
+                        z[r + 1] = a.y;
+                        z[r + 2] = c.x;
+                        z[r + 3] = c.y;
                     }
                     if (edge) {
 #pragma unroll
@@ -1183,10 +1221,14 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
                 for (int r = 0; r < RH; r += 4) {
                     float w[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float pr = fast_exp2(z[r + k]);
-                        l[r + k] += pr;
-                        w[k] = pr * vw;
+                    for (int k = 0; k < 4; k += 2) {
+                        const float2 pr = make_float2(fast_exp2(z[r + k]), fast_exp2(z[r + k + 1]));
+                        const float2 sum = add_x2(make_float2(l[r + k], l[r + k + 1]), pr);
+                        const float2 ww = mul_x2(pr, make_float2(vw, vw));
+                        l[r + k] = sum.x;
+                        l[r + k + 1] = sum.y;
+                        w[k] = ww.x;
+                        w[k + 1] = ww.y;
                     }
                     if (edge) {          // 0 * NaN: of a scale, or of a value that other rows see
 #pragma unroll
