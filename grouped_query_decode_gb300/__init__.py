@@ -339,6 +339,11 @@ def _paged_fp8_cache(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens):
 _workspaces = {}
 
 
+def _workspace_key(dev, handle):
+    # cudaStreamPerThread is another stream in every thread.
+    return (dev, handle) if handle != 2 else (dev, handle, threading.get_ident())
+
+
 def _workspace(nbytes, like, dev, stream):
     """A buffer for one call on the device of `like`, in the order of the call's
     stream. A call on the current stream takes the stream's own, kept from call
@@ -349,7 +354,7 @@ def _workspace(nbytes, like, dev, stream):
     if stream is None:
         if torch._C._cuda_getDevice() != dev or torch._C._cuda_isCurrentStreamCapturing():
             return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-        key = (dev, torch._C._cuda_getCurrentRawStream(dev))
+        key = _workspace_key(dev, torch._C._cuda_getCurrentRawStream(dev))
         buf = _workspaces.get(key)
         if buf is None or buf.shape[0] < nbytes:
             buf = _workspaces[key] = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
@@ -614,7 +619,8 @@ def gqa_decode_release_workspace(stream=None, device=None) -> None:
     if device is None:
         device = stream.device_index if hasattr(stream, "device_index") else torch.cuda.current_device()
     handle = _stream_handle(stream, device)
-    _workspaces.pop((device, handle.value or 0), None)
+    index = device if isinstance(device, int) else torch.device(device).index
+    _workspaces.pop(_workspace_key(torch.cuda.current_device() if index is None else index, handle.value or 0), None)
     rc = _call(device, load().gqa_decode_release_workspace, handle)
     if rc != GQA_OK:
         raise GQADecodeError(rc, "gqa_decode_release_workspace")

@@ -70,6 +70,10 @@ __device__ __forceinline__ int tokens_of(const PagesParams& p, int b) {
     return t < 0 ? 0 : (t > most ? (int)most : t);
 }
 
+__device__ __forceinline__ int pages_for(const PagesParams& p, int tokens) {
+    return tokens / p.page_size + (tokens % p.page_size != 0);
+}
+
 // Exclusive sum of one value per thread of the CTA, and the total.
 __device__ int block_exclusive_sum(int v, int* total) {
     __shared__ int warp_sum[kPlanWarps];
@@ -164,7 +168,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     const int gw = cluster.block_rank() * kPlanWarps + (threadIdx.x >> 5);
     __shared__ int want[GQA_MAX_PAGE_ROWS];   // missing pages of the rows before each
     for (int b = gw; b < p.B; b += kAllWarps) {
-        const int n = (tokens_of(p, b) + p.page_size - 1) / p.page_size;
+        const int n = pages_for(p, tokens_of(p, b));
         int missing = 0;
 #pragma unroll 4
         for (int j = lane; j < n; j += 32)
@@ -191,7 +195,7 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     each_free(p.refs_out, r, need, [&](int page, int k) { ws.src[k] = page; });
     cluster.sync();
     for (int b = gw; b < p.B; b += kAllWarps) {
-        const int n = (tokens_of(p, b) + p.page_size - 1) / p.page_size;
+        const int n = pages_for(p, tokens_of(p, b));
         int at = want[b];
         const int end = b + 1 < p.B ? want[b + 1] : need;
         for (int j0 = 0; j0 < n && at < end; j0 += 32) {
@@ -489,6 +493,21 @@ int check_sizes(int B, int max_pages, int page_size, int num_pages) {
     return GQA_OK;
 }
 
+// Whether any two of n ranges of memory share a byte.
+struct Range {
+    const void* at;
+    size_t bytes;
+};
+template <int N>
+bool overlap(const Range (&r)[N]) {
+    for (int i = 0; i < N; ++i)
+        for (int j = 0; j < i; ++j) {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(r[i].at), b = reinterpret_cast<uintptr_t>(r[j].at);
+            if (a < b + r[j].bytes && b < a + r[i].bytes) return true;
+        }
+    return false;
+}
+
 int check_ws(void* ws, size_t bytes, int B, int num_pages) {
     if (!ws || bytes < gqa_pages_workspace_bytes(B, num_pages) || (reinterpret_cast<uintptr_t>(ws) & 255u))
         return GQA_ERR_WORKSPACE;
@@ -537,12 +556,16 @@ int gqa_pages_reserve(int32_t* block_table, const int32_t* seq_lens, int32_t* re
                       size_t workspace_bytes, cudaStream_t stream) {
     int st = check_sizes(B, max_pages_per_seq, page_size, num_pages);
     if (st != GQA_OK) return st;
-    if (B > GQA_MAX_PAGE_ROWS) return GQA_ERR_UNSUPPORTED;
+    if (B > GQA_MAX_PAGE_ROWS || (long long)B * max_pages_per_seq >= (1ll << 31)) return GQA_ERR_UNSUPPORTED;
     if (!block_table || !seq_lens || !ref_counts || !counts) return GQA_ERR_INVALID_ARG;
     if (!aligned4(block_table) || !aligned4(seq_lens) || !aligned4(ref_counts) || !aligned4(counts))
         return GQA_ERR_MISALIGNED;
     st = check_ws(workspace, workspace_bytes, B, num_pages);
     if (st != GQA_OK) return st;
+    const size_t rows = 4 * (size_t)B, entries = rows * max_pages_per_seq, pages = 4 * (size_t)num_pages;
+    const Range all[] = {{block_table, entries}, {seq_lens, rows}, {ref_counts, pages}, {counts, 8},
+                         {workspace, gqa_pages_workspace_bytes(B, num_pages)}};
+    if (overlap(all)) return GQA_ERR_INVALID_ARG;
     PagesParams p = {};
     p.lens = seq_lens;
     p.table_out = block_table;
@@ -569,11 +592,16 @@ int gqa_pages_fork(const gqa_page_pool_t* pools, int num_pools, const int32_t* s
     if (!src || !block_table || !seq_lens || !ref_counts || !table_out || !lens_out || !refs_out || !counts)
         return GQA_ERR_INVALID_ARG;
     if (table_out == block_table || lens_out == seq_lens || refs_out == ref_counts) return GQA_ERR_INVALID_ARG;
+    const size_t rows = 4 * (size_t)B, entries = rows * max_pages_per_seq, pages = 4 * (size_t)num_pages;
+    const Range all[] = {{block_table, entries}, {seq_lens, rows}, {ref_counts, pages}, {src, rows},
+                         {table_out, entries}, {lens_out, rows}, {refs_out, pages}, {counts, 8},
+                         {workspace, gqa_pages_workspace_bytes(B, num_pages)}};
     if (!aligned4(src) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(ref_counts) ||
         !aligned4(table_out) || !aligned4(lens_out) || !aligned4(refs_out) || !aligned4(counts))
         return GQA_ERR_MISALIGNED;
     st = check_ws(workspace, workspace_bytes, B, num_pages);
     if (st != GQA_OK) return st;
+    if (overlap(all)) return GQA_ERR_INVALID_ARG;
     int sms;
     unsigned* status;
     st = current_device(&sms, &status);
@@ -592,6 +620,9 @@ int gqa_pages_free(const uint8_t* done, int32_t* block_table, int32_t* seq_lens,
     if (st != GQA_OK) return st;
     if (!done || !block_table || !seq_lens || !ref_counts) return GQA_ERR_INVALID_ARG;
     if (!aligned4(block_table) || !aligned4(seq_lens) || !aligned4(ref_counts)) return GQA_ERR_MISALIGNED;
+    const Range all[] = {{done, (size_t)B}, {block_table, 4 * (size_t)B * max_pages_per_seq}, {seq_lens, 4 * (size_t)B},
+                         {ref_counts, 4 * (size_t)num_pages}};
+    if (overlap(all)) return GQA_ERR_INVALID_ARG;
     int sms;
     unsigned* status;
     const int dv = current_device(&sms, &status);
@@ -624,6 +655,12 @@ int gqa_pages_compact(const gqa_page_pool_t* pools, int num_pools, const int32_t
         return GQA_ERR_MISALIGNED;
     st = check_ws(workspace, workspace_bytes, B, num_pages);
     if (st != GQA_OK) return st;
+    // In place is the same array; of two ranges that are one, the second is left out.
+    const size_t entries = 4 * (size_t)B * max_pages_per_seq, pages = 4 * (size_t)num_pages;
+    const Range all[] = {{block_table, entries}, {ref_counts, pages}, {table_out, table_out == block_table ? 0 : entries},
+                         {refs_out, refs_out == ref_counts ? 0 : pages}, {counts, 8},
+                         {workspace, gqa_pages_workspace_bytes(B, num_pages)}};
+    if (overlap(all)) return GQA_ERR_INVALID_ARG;
     int sms;
     unsigned* status;
     st = current_device(&sms, &status);

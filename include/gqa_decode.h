@@ -245,7 +245,8 @@ size_t gqa_decode_paged_fp8_workspace_bytes(int B, int sq, int H, int G, int D, 
  * and codes it already holds are requantised. Powers of two leave e4m3's
  * relative precision as it is and make requantising exact except for
  * subnormals, so tokens appended one by one do not lose precision as their
- * block outgrows its scale. Codes are round-to-nearest-even of x / scale; NaN
+ * block outgrows its scale. A scale that is not above 0 counts as 0, and so do
+ * the values that its block holds. Codes are round-to-nearest-even of x / scale; NaN
  * and infinities are stored as NaN codes and leave the scale alone.
  *
  * A page that receives tokens must belong to one sequence only (gqa_pages_fork
@@ -263,6 +264,10 @@ int gqa_append_paged_fp8(const void* k_new, const void* v_new, void* k_pages, vo
  * from the free ones. seq_lens are clamped to [0, max_pages * page_size];
  * entries outside [0, num_pages) count as no page. counts (int32 [2], device)
  * reports what a call did, so the host need not wait for it.
+ *
+ * The arrays of a call (the workspace among them) overlap nowhere, unless its
+ * description allows it: GQA_ERR_INVALID_ARG. gqa_pages_reserve takes block
+ * tables of less than 2^31 entries.
  *
  * The data of a page is whatever `pools` lists: K and V pages, their scales,
  * of any type and any number of layers.

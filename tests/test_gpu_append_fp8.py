@@ -147,6 +147,17 @@ def test_scales_that_are_no_powers_of_two():
         assert off.mean() < 1e-3 and (np.abs(a - b) <= np.maximum(np.abs(b) / 8, 2.0 ** -9)).all()
 
 
+def test_a_held_scale_that_is_not_positive_counts_as_zero():
+    p = Pool(111, 4, 2, 64, 64, 2)
+    for i, s in enumerate(p.scales):
+        odd = torch.from_numpy(s.copy())
+        odd[p.table[1, 0]], odd[p.table[2, 0]], odd[p.table[3, 0]] = -0.5, float("nan"), -0.0
+        p.dev[2 + i].copy_(odd)
+        s[p.table[1:, 0]] = 0.0
+    p.append(p.tokens(4, 3, 2, 64), p.tokens(4, 3, 2, 64), [10, 10, 33, 64])
+    p.check()
+
+
 def test_append_then_attend_serves_the_values(monkeypatch):
     """A prompt, then tokens one by one, through the public calls alone: the
     attention is the oracle's over the values the model quantised."""

@@ -81,6 +81,15 @@ def test_reserve(seed, B, most, ps, num):
     assert np.array_equal(t.cpu().numpy(), want[0]) and np.array_equal(r.cpu().numpy(), want[1])
 
 
+def test_reserve_for_the_longest_sequences():
+    """715827 pages of 3000 tokens: the last page ends past 2^31 tokens."""
+    most, ps, num = 715827, 3000, 50
+    t = torch.full((1, most), -1, dtype=torch.int32, device="cuda")
+    r, c = torch.zeros(num, dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    gq.gqa_pages_reserve(t, dev(np.array([2 ** 31 - 1], np.int32)), r, ps, c)
+    assert c.tolist() == [most, num] and bool((t == -1).all()) and not bool(r.any())
+
+
 @pytest.mark.parametrize("B,most,ps,num", SIZES, ids=str)
 @pytest.mark.parametrize("seed", range(4))
 def test_fork(seed, B, most, ps, num):

@@ -192,6 +192,39 @@ def test_pages_refuse():
     assert gq.gqa_pages_workspace_bytes(0, 8) == 0 and gq.gqa_pages_workspace_bytes(1, 0) == 0
 
 
+def test_pages_refuse_arrays_that_overlap():
+    """B = 4 rows of 4 entries (64 bytes), 8 pages (32 bytes)."""
+    lib = gq.load()
+    INV, big = gq.GQA_ERR_INVALID_ARG, 1 << 30
+    at = [A * (i + 1) for i in range(9)]
+
+    def fork(**kw):
+        x = dict(src=at[0], table=at[1], lens=at[2], refs=at[3], t_out=at[4], l_out=at[5], r_out=at[6], counts=at[7],
+                 ws=at[8])
+        x.update(kw)
+        return lib.gqa_pages_fork(_pool(), 1, x["src"], x["table"], x["lens"], x["refs"], x["t_out"], x["l_out"],
+                                  x["r_out"], x["counts"], 4, 4, 16, 8, x["ws"], big, None)
+
+    for kw in (dict(t_out=at[1] + 60), dict(t_out=at[1] - 60), dict(l_out=at[2] + 12), dict(r_out=at[3] - 28),
+               dict(t_out=at[3]), dict(l_out=at[0]), dict(counts=at[4] + 8), dict(r_out=at[4] + 32),
+               dict(ws=at[1]), dict(t_out=at[8] + 256)):
+        assert fork(**kw) == INV, kw
+    if not torch.cuda.is_available():       # ranges that only touch go on, to the missing device
+        for kw in ({}, dict(t_out=at[1] + 64), dict(t_out=at[1] - 64), dict(l_out=at[2] + 16)):
+            assert fork(**kw) not in (INV, gq.GQA_OK), kw
+    assert lib.gqa_pages_reserve(at[0], at[1], at[0] + 60, at[2], 4, 4, 16, 8, at[3], big, None) == INV
+    assert lib.gqa_pages_reserve(at[0], at[1], at[2], at[2] + 28, 4, 4, 16, 8, at[3], big, None) == INV
+    assert lib.gqa_pages_free(at[0], at[1], at[2], at[1] + 32, 4, 4, 8, None) == INV
+    assert lib.gqa_pages_compact(_pool(), 1, at[0], at[1], at[0] + 4, at[1], at[2], 4, 4, 8, at[3], big, None) == INV
+    assert lib.gqa_pages_compact(_pool(), 1, at[0], at[1], at[0], at[1] - 4, at[2], 4, 4, 8, at[3], big, None) == INV
+    assert lib.gqa_pages_compact(_pool(), 1, at[0], at[1], at[1], at[0], at[2], 4, 4, 8, at[3], big, None) == INV
+
+
+def test_reserve_refuses_tables_past_2_31_entries():
+    lib = gq.load()
+    assert lib.gqa_pages_reserve(A, A, A, A, 8192, 1 << 18, 16, 8, A, 1 << 30, None) == gq.GQA_ERR_UNSUPPORTED
+
+
 def test_binding_refuses_host_tensors_dtypes_and_shapes():
     bf, u8, f32, i32 = torch.bfloat16, torch.uint8, torch.float32, torch.int32
     q = torch.zeros(1, 1, 8, 64, dtype=bf)
