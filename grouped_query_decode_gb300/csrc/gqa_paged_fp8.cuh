@@ -559,23 +559,35 @@ __device__ __forceinline__ bool named_any(int id, bool v) {
     return r != 0;
 }
 
+__device__ __forceinline__ unsigned long long add_acq_rel(unsigned long long* at, unsigned long long v) {
+    unsigned long long old;
+    asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], %2;" : "=l"(old) : "l"(at), "l"(v) : "memory");
+    return old;
+}
+__device__ __forceinline__ unsigned long long cas_acq_rel(unsigned long long* at, unsigned long long seen,
+                                                          unsigned long long v) {
+    unsigned long long was;
+    asm volatile("atom.cas.acq_rel.gpu.global.b64 %0, [%1], %2, %3;" : "=l"(was) : "l"(at), "l"(seen), "l"(v) : "memory");
+    return was;
+}
+
 // Counts one arrival on a counter that holds (tag << 16 | count); one with
 // another tag counts from zero. True for the last of n, which leaves a count
 // of zero: a captured call is replayed with its tag.
 __device__ __forceinline__ bool arrive_last(unsigned long long* counter, unsigned long long tag, unsigned n) {
     const unsigned long long zero = tag << 16;
     unsigned count;
-    const unsigned long long old = atomicAdd(counter, 1ull);
+    const unsigned long long old = add_acq_rel(counter, 1ull);
     if (old >> 16 == tag) {
         count = (unsigned)(old & 0xffffu) + 1;
     } else {
         unsigned long long seen = *reinterpret_cast<volatile unsigned long long*>(counter);
         while (true) {
             if (seen >> 16 == tag) {           // another arrival has tagged it: its count lacks this one
-                count = (unsigned)(atomicAdd(counter, 1ull) & 0xffffu) + 1;
+                count = (unsigned)(add_acq_rel(counter, 1ull) & 0xffffu) + 1;
                 break;
             }
-            const unsigned long long was = atomicCAS(counter, seen, zero | 1ull);
+            const unsigned long long was = cas_acq_rel(counter, seen, zero | 1ull);
             if (was == seen) {
                 count = 1;
                 break;
@@ -1274,6 +1286,13 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
                 const float sum = reduce_rows<RH>(l, lane);
                 if (lane < RH) reinterpret_cast<float*>(my_sum + lane)[w4] = sum;
                 named_sync(bar, 128);
+                const bool whole = seg.i0 == 0 && seg.i1 == seg.n;
+                int c0 = 0, n = 1;                // the CTAs that share the unit
+                if (!whole) {
+                    const long long unit0 = plan_s->begin + it0 - seg.i0;
+                    c0 = plan_s->owner(unit0);
+                    n = plan_s->owner(unit0 + seg.n - 1) - c0 + 1;
+                }
                 // This group's last tile is the segment's last or the one before.
                 const int last = it0 + len - 1;
                 wait_product((last & 1) == x ? last : last - 1);
@@ -1306,7 +1325,6 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
                     ++n_merge;
                 } else {
                     if (both) all_wait(m_full + 8 * y, n_merge);
-                    const bool whole = seg.i0 == 0 && seg.i1 == seg.n;
                     const size_t slot_floats = p8_slot_floats(RP, D);
                     float* slot = p.part + ((size_t)blockIdx.x * 2 + (seg.i0 == 0 ? 1 : 0)) * slot_floats;
                     const int* rows_out = row_out + (sg & 1) * RP + y * RH;
@@ -1354,16 +1372,9 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
                     if (!whole) {
                         // The last of the unit's CTAs to arrive merges it:
                         //   M = max m_c, L = sum l_c 2^(m_c - M), O = sum O_c 2^(m_c - M) / L.
-                        const P8Plan plan = *plan_s;
-                        const long long unit0 = plan.begin + it0 - seg.i0;
-                        const int c0 = plan.owner(unit0), n = plan.owner(unit0 + seg.n - 1) - c0 + 1;
                         named_sync(bar, 128);
-                        if (tok == 0) {
-                            __threadfence();      // of the group's stores, which the barrier ordered before
-                            const bool last = arrive_last(p.counters + (size_t)c0 * PS::kParts + y, p.tag, n);
-                            if (last) __threadfence();
-                            last_flag[bar - 1] = last;
-                        }
+                        if (tok == 0)             // releases the group's stores, which the barrier ordered before
+                            last_flag[bar - 1] = arrive_last(p.counters + (size_t)c0 * PS::kParts + y, p.tag, n);
                         named_sync(bar, 128);
                         if (last_flag[bar - 1]) {
                             p8_merge<D, RP, RH>(p, c0, n, y * RH, tok, rows_out);
