@@ -29,7 +29,8 @@ struct AppendParams {
     const int32_t* table;
     const int32_t* lens;
     int B, sq, G, page_size, num_pages, max_pages;
-    int size;                   // tokens of a block: min(64, page_size)
+    int page_shift;             // log2 of page_size
+    int size, size_shift;       // tokens of a block: min(64, page_size)
     int blocks;                 // blocks of a sequence that may receive tokens
     int per, runs;              // blocks per item, items per sequence and head
 };
@@ -66,6 +67,17 @@ __device__ __forceinline__ float finite_or_nan(float x) {
     return fabsf(x) <= 3.4028234664e38f ? x : __uint_as_float(0x7fffffffu);
 }
 
+// e4m3 codes of two bf16 values times f, both products in one instruction.
+__device__ __forceinline__ uint32_t scaled_codes(uint32_t w, float f) {
+    unsigned long long x, y;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(w << 16), "r"(w & 0xffff0000u));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(y) : "f"(f));
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(y));
+    float lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+    return e4m3x2(lo, hi);
+}
+
 // Eight bf16 values.
 __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -95,11 +107,17 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_kernel(const _
     const int b = rest / p.runs, run = rest - b * p.runs;
     const int T = clamp_len(p.lens[b], p.max_pages * p.page_size);
     const int begin = T > p.sq ? T - p.sq : 0;       // first position that gets a new token
-    const int block0 = begin / p.size + run * p.per;
-    const int block1 = min(block0 + p.per, min((T + p.size - 1) / p.size, begin / p.size + p.blocks));
+    const int begin_block = begin >> p.size_shift;
+    const int block0 = begin_block + run * p.per;
+    const int block1 = min(block0 + p.per, min((T + p.size - 1) >> p.size_shift, begin_block + p.blocks));
     const int shift = T - p.sq;                      // new token s sits at position shift + s
     const uint16_t* x = p.x_new[which] + ((size_t)b * p.sq * p.G + g) * D;
     const size_t row_step = (size_t)p.G * D;
+    // This thread's chunks of a block: one column, every TPI / kRowChunks rows.
+    static_assert(TPI % kRowChunks == 0, "whole rows");
+    x += (t / kRowChunks) * row_step + (t % kRowChunks) * 8;
+    const size_t chunk_step = (TPI / kRowChunks) * row_step;
+    const int page_blocks = (p.page_size + kBlockTokens - 1) / kBlockTokens;
     const int32_t* table = p.table + (size_t)b * p.max_pages;
 
     // The tokens and the page of a block.
@@ -108,7 +126,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_kernel(const _
     auto load = [&](int block) {
         const int start = block * p.size;
         const int lo = max(begin, start), hi = min(T, start + p.size);
-        next_page = table[start / p.page_size];
+        next_page = table[start >> p.page_shift];
         const uint16_t* x0 = x + (size_t)(lo - shift) * row_step;
         const int n = (hi - lo) * kRowChunks;
 #pragma unroll
@@ -116,7 +134,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_kernel(const _
             const int i = t + c * TPI;
             next[c] = make_uint4(0, 0, 0, 0);
             if (i < n)
-                next[c] = *reinterpret_cast<const uint4*>(x0 + (i / kRowChunks) * row_step + (i % kRowChunks) * 8);
+                next[c] = *reinterpret_cast<const uint4*>(x0 + c * chunk_step);
         }
     };
     // Largest value of the group; every thread of it has passed its reads then.
@@ -124,13 +142,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_kernel(const _
     auto group_max = [&](uint32_t m) {
         m = __reduce_max_sync(0xffffffffu, m);
         if constexpr (TPI > 32) {
-            __shared__ uint32_t part[2][TPI / 32];
+            __shared__ __align__(16) uint32_t part[2][TPI / 32];
             uint32_t* mine = part[turn];             // the other half may still be read
             turn ^= 1;
             if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = m;
             __syncthreads();
 #pragma unroll
-            for (int w = 0; w < TPI / 32; ++w) m = max(m, mine[w]);
+            for (int w = 0; w < TPI / 32; w += 4) {
+                const uint4 u = *reinterpret_cast<const uint4*>(mine + w);
+                m = max(max(m, max(u.x, u.y)), max(u.z, u.w));
+            }
         } else {
             __syncwarp();
         }
@@ -147,11 +168,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_kernel(const _
         const int start = block * p.size;
         const int lo = max(begin, start), hi = min(T, start + p.size);
         const int kept = lo - start, n = (hi - lo) * kRowChunks;
-        const int in_page = start % p.page_size;
+        const int in_page = start & (p.page_size - 1);
         const size_t unit = (size_t)page * p.G + g;
         uint8_t* rows = p.pages[which] + (unit * p.page_size + in_page) * D;
         float* scale_at =
-            p.scale[which] + unit * ((p.page_size + kBlockTokens - 1) / kBlockTokens) + in_page / kBlockTokens;
+            p.scale[which] + unit * page_blocks + in_page / kBlockTokens;
         const float held = kept > 0 ? *scale_at : 0.f;
         // Magnitudes order as their bits do, two at a time. Infinities and NaN
         // do not count; blocks with one are rare and read their tokens again.
@@ -162,8 +183,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_kernel(const _
             m2 = __vmaxu2(m2, __vmaxu2(v[c].z & 0x7fff7fffu, v[c].w & 0x7fff7fffu));
         }
         const uint16_t* x0 = x + (size_t)(lo - shift) * row_step;
-        auto chunk_at = [&](int i) {
-            return *reinterpret_cast<const uint4*>(x0 + (i / kRowChunks) * row_step + (i % kRowChunks) * 8);
+        auto chunk_at = [&](int i) {             // i: t, t + TPI, ...
+            return *reinterpret_cast<const uint4*>(x0 + (i / TPI) * chunk_step);
         };
         uint32_t m = group_max(max(m2 & 0xffffu, m2 >> 16));
         const bool odd = m >= 0x7f80u;
@@ -190,11 +211,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_kernel(const _
             for (int c = 0; c < CHUNKS; ++c) {
                 const int i = t + c * TPI;
                 if (i < n) {
-                    float x8[8];
-                    unpack8(v[c], x8);
                     uint2 w;
-                    w.x = e4m3x2(x8[0] * div.inv, x8[1] * div.inv) | (e4m3x2(x8[2] * div.inv, x8[3] * div.inv) << 16);
-                    w.y = e4m3x2(x8[4] * div.inv, x8[5] * div.inv) | (e4m3x2(x8[6] * div.inv, x8[7] * div.inv) << 16);
+                    w.x = scaled_codes(v[c].x, div.inv) | (scaled_codes(v[c].y, div.inv) << 16);
+                    w.y = scaled_codes(v[c].z, div.inv) | (scaled_codes(v[c].w, div.inv) << 16);
                     *reinterpret_cast<uint2*>(rows + (size_t)kept * D + (size_t)i * 8) = w;
                 }
             }
@@ -287,6 +306,8 @@ extern "C" int gqa_append_paged_fp8(const void* k_new, const void* v_new, void* 
     p.num_pages = num_pages;
     p.max_pages = max_pages_per_seq;
     p.size = page_size < kBlockTokens ? page_size : kBlockTokens;
+    p.page_shift = __builtin_ctz((unsigned)page_size);
+    p.size_shift = __builtin_ctz((unsigned)p.size);
     p.blocks = (int)(((long long)sq + p.size - 2) / p.size) + 1;
     if ((long long)max_pages_per_seq * page_size >= (1ll << 31) - kBlockTokens || sq >= (1 << 30) ||
         2ll * G * p.blocks * B >= (1ll << 31))
