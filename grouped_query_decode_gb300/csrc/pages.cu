@@ -97,11 +97,30 @@ __device__ int block_exclusive_sum(int v, int* total) {
     return before + x - v;
 }
 
+// x = row * n + column, of 64-bit x; in 32 bits where they do (a third of the time).
+struct Entry {
+    int row, column;
+};
+__device__ __forceinline__ Entry entry_of(long long x, int n) {
+    if (x >> 32) return {(int)(x / n), (int)(x % n)};
+    const unsigned q = (unsigned)x / (unsigned)n;
+    return {(int)q, (int)((unsigned)x - q * (unsigned)n)};
+}
+
 // The cluster's warps share the pages in contiguous, ascending ranges. live:
-// pages with a count > 0 before this warp's range, and of all pages.
+// pages with a count > 0 before this warp's range, and of all pages. Lane k
+// keeps which of the range's k-th 32 pages are live, so that what follows the
+// exchange need not read the counts again (one round trip to L2 per 32 pages).
 struct Ranks {
     int lo, hi, live_before, live;
+    unsigned mask;
 };
+// The live pages among the 32 from lo + 32 k on.
+__device__ __forceinline__ unsigned live_mask(const int32_t* refs, const Ranks& r, int k) {
+    if (k < 32) return __shfl_sync(0xffffffffu, r.mask, k);
+    const int i = r.lo + 32 * k + (threadIdx.x & 31);
+    return __ballot_sync(0xffffffffu, i < r.hi && refs[i] > 0);
+}
 // Every thread of the cluster, which has called announce_start(); synchronises it
 // (and so orders its global writes).
 __device__ __forceinline__ void announce_start() {
@@ -117,9 +136,21 @@ __device__ Ranks rank_pages(const int32_t* refs, int num_pages) {
     r.lo = (int)min((long long)num_pages, (long long)(cta * kPlanWarps + warp) * per);
     r.hi = min(num_pages, r.lo + per);
     int n = 0;
-#pragma unroll 8
-    for (int i = r.lo + lane; i < r.hi; i += 32) n += refs[i] > 0;
-    n = __reduce_add_sync(0xffffffffu, n);
+    r.mask = 0;
+    for (int k0 = 0; r.lo + 32 * k0 < r.hi; k0 += 8) {
+        int count[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int i = r.lo + 32 * (k0 + k) + lane;
+            count[k] = i < r.hi ? refs[i] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const unsigned m = __ballot_sync(0xffffffffu, count[k] > 0);
+            n += __popc(m);
+            if (lane == k0 + k) r.mask = m;
+        }
+    }
     if (lane == 0) warp_live[warp] = n;
     __syncthreads();
     int before = 0, mine = 0;
@@ -145,12 +176,12 @@ template <class F>
 __device__ void each_free(const int32_t* refs, const Ranks& r, int limit, F f) {
     const int lane = threadIdx.x & 31;
     int at = r.lo - r.live_before;
-    for (int i0 = r.lo; i0 < r.hi && at < limit; i0 += 32) {
-        const int i = i0 + lane;
-        const bool mine = i < r.hi && refs[i] <= 0;
-        const unsigned m = __ballot_sync(0xffffffffu, mine);
+    for (int q = 0; r.lo + 32 * q < r.hi && at < limit; ++q) {
+        const int i = r.lo + 32 * q + lane;
+        const int here = min(32, r.hi - (r.lo + 32 * q));
+        const unsigned m = ~live_mask(refs, r, q) & (0xffffffffu >> (32 - here));
         const int k = at + __popc(m & ((1u << lane) - 1));
-        if (mine && k < limit) f(i, k);
+        if ((m >> lane & 1) && k < limit) f(i, k);
         at += __popc(m);
     }
 }
@@ -167,13 +198,21 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     const int lane = threadIdx.x & 31;
     const int gw = cluster.block_rank() * kPlanWarps + (threadIdx.x >> 5);
     __shared__ int want[GQA_MAX_PAGE_ROWS];   // missing pages of the rows before each
-    for (int b = gw; b < p.B; b += kAllWarps) {
+    // Lane k keeps the first missing entry of the warp's k-th row, and its pages.
+    static_assert(GQA_MAX_PAGE_ROWS <= 32 * kAllWarps, "a row a lane");
+    int first = 0, pages = 0;
+    for (int b = gw, k = 0; b < p.B; b += kAllWarps, ++k) {
         const int n = pages_for(p, tokens_of(p, b));
-        int missing = 0;
+        int missing = 0, at = n;
 #pragma unroll 4
         for (int j = lane; j < n; j += 32)
-            missing += !is_page(p.table_out[(size_t)b * p.max_pages + j], p.num_pages);
+            if (!is_page(p.table_out[(size_t)b * p.max_pages + j], p.num_pages)) {
+                ++missing;
+                at = min(at, j);
+            }
         missing = __reduce_add_sync(0xffffffffu, missing);
+        at = __reduce_min_sync(0xffffffffu, at);
+        if (lane == k) first = at, pages = n;
         if (lane == 0) ws.row_page[b] = missing;
     }
     const Ranks r = rank_pages(p.refs_out, p.num_pages);
@@ -194,11 +233,11 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     if (need == 0 || need > free) return;    // the whole cluster
     each_free(p.refs_out, r, need, [&](int page, int k) { ws.src[k] = page; });
     cluster.sync();
-    for (int b = gw; b < p.B; b += kAllWarps) {
-        const int n = pages_for(p, tokens_of(p, b));
+    for (int b = gw, k = 0; b < p.B; b += kAllWarps, ++k) {
+        const int n = __shfl_sync(0xffffffffu, pages, k), j1 = __shfl_sync(0xffffffffu, first, k);
         int at = want[b];
         const int end = b + 1 < p.B ? want[b + 1] : need;
-        for (int j0 = 0; j0 < n && at < end; j0 += 32) {
+        for (int j0 = j1; j0 < n && at < end; j0 += 32) {
             const int j = j0 + lane;
             int32_t* e = p.table_out + (size_t)b * p.max_pages + j;
             const bool mine = j < n && !is_page(*e, p.num_pages);
@@ -279,10 +318,10 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     const int lane = threadIdx.x & 31;
     const Ranks r = rank_pages(p.refs, p.num_pages);
     int at = r.live_before;
-    for (int i0 = r.lo; i0 < r.hi; i0 += 32) {
-        const int i = i0 + lane;
-        const bool live = i < r.hi && p.refs[i] > 0;
-        const unsigned m = __ballot_sync(0xffffffffu, live);
+    for (int q = 0; r.lo + 32 * q < r.hi; ++q) {
+        const int i = r.lo + 32 * q + lane;
+        const unsigned m = live_mask(p.refs, r, q);
+        const bool live = m >> lane & 1;
         const int before = at + __popc(m & ((1u << lane) - 1));
         if (i < r.hi && !live && i < r.live) ws.dst[i - before] = i;
         if (live && i >= r.live) ws.src[r.live - 1 - before] = i;
@@ -337,8 +376,19 @@ __device__ void copy_pages(const PoolSet& pools, const int* src, const int* dst,
         const long long pieces = (long long)((pool.page_bytes + kPiece - 1) / kPiece);
         const long long items = pieces * pool.layers * n;
         for (long long it = warp; it < items; it += warps) {
-            const long long piece = it % pieces, rest = it / pieces;
-            const int k = (int)(rest / pool.layers), layer = (int)(rest % pool.layers);
+            long long piece;
+            int k, layer;
+            if (items >> 32) {
+                const long long rest = it / pieces;
+                piece = it - rest * pieces;
+                k = (int)(rest / pool.layers);
+                layer = (int)(rest - (long long)k * pool.layers);
+            } else {
+                const unsigned rest = (unsigned)it / (unsigned)pieces;
+                piece = (unsigned)it - rest * (unsigned)pieces;
+                k = (int)(rest / (unsigned)pool.layers);
+                layer = (int)(rest - (unsigned)k * (unsigned)pool.layers);
+            }
             const int a = src[SRC_DESCENDING ? n - 1 - k : k], b = dst[k];
             if (!is_page(a, num_pages) || !is_page(b, num_pages)) continue;
             char* base = static_cast<char*>(pool.base) + (size_t)layer * pool.layer_bytes + piece * kPiece;
@@ -373,7 +423,8 @@ __global__ void __launch_bounds__(kMoveThreads) fork_kernel(const __grid_constan
     const long long entries = (long long)p.B * p.max_pages;
     for (long long x = (long long)blockIdx.x * blockDim.x + threadIdx.x; x < entries;
          x += (long long)gridDim.x * blockDim.x) {
-        const int i = (int)(x / p.max_pages), j = (int)(x % p.max_pages);
+        const Entry e = entry_of(x, p.max_pages);
+        const int i = e.row, j = e.column;
         const int was = p.table[x];
         int now = was;
         if (ok) {
@@ -445,12 +496,12 @@ __global__ void __launch_bounds__(kMoveThreads) free_kernel(const uint8_t* done,
     const long long entries = (long long)p.B * p.max_pages;
     for (long long x = (long long)blockIdx.x * blockDim.x + threadIdx.x; x < entries;
          x += (long long)gridDim.x * blockDim.x) {
-        const int b = (int)(x / p.max_pages);
-        if (!done[b]) continue;
+        const Entry at = entry_of(x, p.max_pages);
+        if (!done[at.row]) continue;
         const int e = p.table_out[x];
         if (is_page(e, p.num_pages) && atomicAdd(&p.refs_out[e], -1) <= 0) atomicAdd(&p.refs_out[e], 1);
         p.table_out[x] = -1;
-        if (x % p.max_pages == 0) p.lens_out[b] = 0;
+        if (at.column == 0) p.lens_out[at.row] = 0;
     }
 }
 

@@ -308,3 +308,54 @@ def test_a_serving_loop_of_every_call_in_a_graph():
         vmax = np.nanmax(np.abs(v)) if (lens > 0).any() else 0.0
         err = np.abs(out.float().cpu().numpy() - ref)
         assert (err <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * vmax).all(), (it, err.max())
+
+
+@pytest.mark.parametrize("num", [262144, 262145, 300001])
+def test_pools_of_many_pages(num):
+    """More pages than the planning kernel's warps keep in one mask a lane."""
+    s = State(70, 40, 6, 16, num)
+    some = s.rng.choice(num, num // 2, replace=False)       # pages that holders outside the table count
+    s.refs[some] += 1
+    pool = s.rng.integers(0, 2 ** 31, (num, 1)).astype(np.int32)
+    lens = np.full(40, 6 * 16, np.int32)
+    want = model.reserve(s.table, lens, s.refs, 16)
+    t, r, c = dev(s.table), dev(s.refs), torch.zeros(2, dtype=torch.int32, device="cuda")
+    gq.gqa_pages_reserve(t, dev(lens), r, 16, c)
+    assert c.tolist() == want[2]
+    assert np.array_equal(t.cpu().numpy(), want[0]) and np.array_equal(r.cpu().numpy(), want[1])
+
+    src = s.rng.integers(0, 40, 40).astype(np.int32)
+    want_t, want_l, want_r, counts, pairs = model.fork(src, s.table, s.lens, s.refs, 16)
+    d, t, l, r = dev(pool), dev(s.table), dev(s.lens), dev(s.refs)
+    outs = [torch.full_like(x, -77) for x in (t, l, r)]
+    gq.gqa_pages_fork([d], dev(src), t, l, r, 16, *outs, c)
+    assert c.tolist() == counts
+    for got, w in zip(outs, (want_t, want_l, want_r)):
+        assert np.array_equal(got.cpu().numpy(), w)
+    after = moved([pool[None]], pairs)[0][0]
+    assert np.array_equal(d.cpu().numpy(), after)
+
+    want_t, want_r, counts, pairs = model.compact(s.table, s.refs)
+    d, t, r = dev(pool), dev(s.table), dev(s.refs)
+    gq.gqa_pages_compact([d], t, r, t, r, c)
+    assert c.tolist() == counts
+    assert np.array_equal(t.cpu().numpy(), want_t) and np.array_equal(r.cpu().numpy(), want_r)
+    assert np.array_equal(d.cpu().numpy(), moved([pool[None]], pairs)[0][0])
+
+
+@pytest.mark.parametrize("B,most", [(3, 200), (700, 70), (8192, 3)])
+def test_reserve_fills_holes(B, most):
+    """Missing entries anywhere in a row, rows without any, entries outside the pool."""
+    rng = np.random.default_rng(71)
+    ps, num = 16, B * most + 7
+    table = rng.permutation(num)[:B * most].reshape(B, most).astype(np.int32)
+    holes = rng.random((B, most)) < rng.choice([0.0, 0.02, 0.7], (B, 1))
+    refs = np.zeros(num, np.int32)
+    refs[table[~holes]] = 1
+    table[holes] = rng.choice([-1, -5, num, 2 ** 31 - 1], holes.sum())
+    lens = rng.integers(0, most * ps + 1, B).astype(np.int32)
+    want = model.reserve(table, lens, refs, ps)
+    t, r, c = dev(table), dev(refs), torch.zeros(2, dtype=torch.int32, device="cuda")
+    gq.gqa_pages_reserve(t, dev(lens), r, ps, c)
+    assert c.tolist() == want[2]
+    assert np.array_equal(t.cpu().numpy(), want[0]) and np.array_equal(r.cpu().numpy(), want[1])
