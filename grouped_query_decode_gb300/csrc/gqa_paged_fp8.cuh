@@ -21,7 +21,7 @@
 //
 // Softmax, one thread per token: x = s * scale2 * k_scale (base 2), p = 2^(x - m)
 // with a reference m per row that moves only when a score exceeds it by more
-// than 2 (then O is rescaled in tensor memory), so that tiles need no maximum
+// than 4 (then O is rescaled in tensor memory), so that tiles need no maximum
 // across threads: one vote. The sum l is kept per thread until the end. v_scale enters
 // p through a power of two 2^c that follows the largest scale seen.
 //
@@ -30,11 +30,27 @@
 // workspace; the CTA that arrives last merges them. Per CTA: two groups of four
 // softmax warps (with 32 rows two such pairs, 16 rows each) take alternate
 // tiles. One warp brings K, another V (a TMA box per page, in the swizzle of
-// the operand layout; one warp issues a box in 65 cycles, two warps two), the
-// latter also splits Q and fetches the blocks' scales, ahead of V by a chunk of
-// tiles (behind a saturated HBM a lookup of page and scale takes longer than a
-// tile). Two warps issue the products. Every wait is bounded, as in the other
-// kernels.
+// the operand layout; one warp issues a box in 65 cycles, two warps two); the
+// latter also splits the queries of every segment but the first and fetches the
+// blocks' scales, ahead of V by a chunk of tiles (behind a saturated HBM a lookup
+// of page and scale takes longer than a tile). Two warps issue the products.
+// Every wait is bounded, as in the other kernels.
+//
+// What bounds it. Bytes: the cache, once. A tile of 8 rows takes 0.3 us, one of 32
+// rows 0.65 to 0.72 us (a softmax warp's chain of load, vote, exponentials and
+// four terms is 2400 cycles, two groups at a time), against 0.62 to 0.74 us for
+// a tile's 32 KB from HBM shared by 128 to 152 SMs. Around the tiles: 2 us of
+// launch, 1.5 us of plan, 2 us until the first softmax, and where a unit is
+// split 4 to 6 us for its parts (stores, one atomic, the last arriver's merge).
+// Measured on one GB300 (HBM copy 6.77 TB/s), B x H/G heads, tokens, page:
+//   16 x 32/8, D 128, 4096, 64           25.5 us, 5.3 TB/s (6.5 TB/s at 16384 tokens)
+//   64 x 32/1, D 128, 8192, 32           33.9 us, 4.0 TB/s
+//   1 x 64/8, D 128, 131072, 16          52.4 us, 5.1 TB/s
+//   64 x 64/8, 4 new tokens, D 128, up to 32768, 64    359 us, 6.1 TB/s
+//   1 x 32/8, 64 new tokens, D 64, 4096, 64            23.3 us (4.7 MB: latency)
+// Tried and slower: asking for a barrier's phase ahead of its wait (MQA end +0.3
+// us), running the merge once without effect to fetch its instructions (+0.7 us),
+// 152 CTAs with uneven shares where 128 share equal units evenly (+2.8 us).
 #pragma once
 
 #include <cuda_fp16.h>
