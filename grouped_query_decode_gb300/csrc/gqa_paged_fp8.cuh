@@ -860,15 +860,28 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
     }
 
     if (warp == SW) {
-        // ---------------------------------------------------------- K loader
+        // ------------------------------------------------ K loader, Q rows
         const int skip_tile = blockIdx.x == 0 ? p.skip_tile : -1;      // injected fault: never loaded
         const uint64_t pol = l2_policy_evict_first();
-        int it = 0, s = 0;
+        int it = 0, s = 0, sg = 0;
         uint32_t ph = 1;
         bool ok = true;
         while (ok && walk.next(lens, seg)) {
             int b, rt;
             lens.split(seg.entry, b, rt);
+            const int buf = sg & 1;
+            if (sg > 0) {                         // query rows of every segment but the first
+                QRows next = load_rows(b, rt, seg.g, 0);
+                ok = warp_wait(q_empty + 8 * buf, ((sg >> 1) & 1) ^ 1, abort_flag, p.status, tmo);
+                if (!ok) break;
+#pragma unroll 1
+                for (int r0 = 0; r0 < RP; r0 += 8) {
+                    const QRows q = next;
+                    if (r0 + 8 < RP) next = load_rows(b, rt, seg.g, r0 + 8);
+                    split_rows(q, lens.tokens(b), buf, r0);
+                }
+            }
+            ++sg;
             ok = load_tiles(seg, b, lens.tokens(b), &tm_k, k_s, SK, k_full, k_empty, skip_tile, pol, it, s, ph,
                             [](int) {});
         }
@@ -966,7 +979,7 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
         }
         __syncwarp();
     } else if (warp == SW + 3) {
-        // ------------------------------------------------ Q rows, scales, V loader
+        // --------------------------------------------------- scales, V loader
         const int block = min(page_size, 64);     // tokens of a scale
         const uint64_t pol = l2_policy_evict_first();
         int sg = 0, chunk = 0, it = 0, s = 0;
@@ -1009,15 +1022,6 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
             const int page_first = page_of(pos_of(seg.i0));
             ok = warp_wait(q_empty + 8 * buf, ((sg >> 1) & 1) ^ 1, abort_flag, p.status, tmo);
             if (!ok) break;
-            if (sg > 0) {
-                QRows next = load_rows(b, rt, seg.g, 0);
-#pragma unroll 1
-                for (int r0 = 0; r0 < RP; r0 += 8) {
-                    const QRows q = next;
-                    if (r0 + 8 < RP) next = load_rows(b, rt, seg.g, r0 + 8);
-                    split_rows(q, T, buf, r0);
-                }
-            }
             fetch_scales(pos_of(seg.i0), page_first);
             int page_next = page_of(pos_of(seg.i0 + kP8ScaleChunk));
             ++sg;
