@@ -93,7 +93,7 @@ struct P8Shape {
     static constexpr int kWarpMaxBytes = 2 * kParts * 4 * (kRows + 1) * 4;
     static constexpr int kSumBytes = 2 * RP * 16;
     static constexpr int kMergeBytes = 3 * RP * 8;                // group 1's (m, l); each group's row factors
-    static constexpr int kLenBytes = kP8LenCopy * 4;
+    static constexpr int kLenBytes = kP8LenCopy * 4 + 16;         // and the plan's padding
     static constexpr int kScaleBytes = kP8ScaleChunks * kP8ScaleChunk * 16 * 4;
     static constexpr int kMiscBytes = 320;
     static constexpr int kSmemBytes = 1024 + (kStagesK + kStagesV) * kTileBytes + 2 * kQBytes + 2 * kPBytes +
@@ -262,7 +262,7 @@ __device__ __forceinline__ float2 add_x2(float2 a, float2 b) {
 template <int RP>
 struct P8Lens {
     const PagedFp8Params& p;
-    const int* copy;
+    int* copy;
     __device__ int global(int b) const { return clamp_len(p.lens[b], p.max_pages << p.page_shift); }
     __device__ int tokens(int b) const { return p.B <= kP8LenCopy ? copy[b] : global(b); }
     __device__ void split(int entry, int& b, int& rt) const {
@@ -278,6 +278,8 @@ struct P8Lens {
         const int lim = T - p.sq + p.by_heads(last);
         return lim < 0 ? 0 : lim / kP8Tokens + 1;
     }
+    // Tiles that a unit counts beyond its own in the plan.
+    __device__ int pad() const { return copy[kP8LenCopy]; }
 };
 
 // A CTA's share as a run of segments of units.
@@ -286,7 +288,7 @@ struct P8Segment {
 };
 template <int RP>
 struct P8Walk {
-    long long left;
+    long long left;              // of the CTA's share, padding included
     int entry, g, off;
     __device__ bool next(const P8Lens<RP>& lens, P8Segment& s) {
         if (left <= 0) return false;
@@ -300,7 +302,7 @@ struct P8Walk {
         s.i0 = off;
         s.i1 = left < n - off ? off + (int)left : n;
         s.n = n;
-        left -= s.i1 - s.i0;
+        left -= s.i1 - s.i0 + lens.pad();
         off = 0;
         if (++g == lens.p.G) {
             g = 0;
@@ -311,9 +313,21 @@ struct P8Walk {
 };
 
 struct P8Plan {
-    long long total, begin, end;   // tiles of the call, and this CTA's
+    long long total, begin, end;   // tiles of the call, and this CTA's, padding included
+    long long left;                // of the latter from the first tile on
     int entry, g, off;             // where it begins
     int ctas;                      // CTAs that share the tiles
+    // A share that begins in a unit's padding begins with the next unit.
+    __device__ void skip_pad(int n, int pad, int G) {
+        left = end - begin;
+        if (off < n) return;
+        left -= n + pad - off;
+        off = 0;
+        if (++g == G) {
+            g = 0;
+            ++entry;
+        }
+    }
     // The CTA whose share holds tile t of the call.
     __device__ int owner(long long t) const {
         const unsigned long long x = (unsigned long long)(t + 1) * (unsigned)ctas - 1;
@@ -340,32 +354,49 @@ __device__ __forceinline__ P8Plan p8_small_plan(const P8Lens<RP>& lens) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) n[k] = lane * 4 + k < entries ? (unsigned)lens.tiles(lane * 4 + k) : 0;
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) mine += n[k];
-    mine *= (unsigned)p.G;
-    unsigned x = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    const unsigned total = __shfl_sync(0xffffffffu, x, 31), before = x - mine;
-    // A CTA for every unit, or for every eight tiles.
-    const unsigned units = (unsigned)entries * p.G;
-    unsigned ctas = min(min(gridDim.x, max(units, total / kP8MinTiles)), max(total, 1u));
-    // Equal lengths: whole units per CTA, or the same number of CTAs per unit,
-    // where that keeps four fifths of them; no unit is then cut unevenly.
     unsigned lo = 0xffffffffu, hi = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 4; ++k) {
+        mine += n[k];
         if (lane * 4 + k < entries) lo = min(lo, n[k]), hi = max(hi, n[k]);
+    }
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
-    if (lo == hi && hi > 0) {                     // the same in every lane, as all that follows
+    const bool equal = lo == hi;                  // the same in every lane, as all that follows
+    // A CTA for every unit, or for every eight tiles.
+    const unsigned tiles = __reduce_add_sync(0xffffffffu, mine) * (unsigned)p.G;
+    const unsigned units = (unsigned)entries * p.G;
+    unsigned ctas = min(min(gridDim.x, max(units, tiles / kP8MinTiles)), max(tiles, 1u));
+    // Equal lengths: whole units per CTA, or the same number of CTAs per unit,
+    // where that keeps four fifths of them; no unit is then cut unevenly.
+    if (equal && hi > 0) {
         const unsigned per = (units + ctas - 1) / ctas;
         const unsigned even = per > 1 ? (units % per == 0 ? units / per : 0) : units * (ctas / units);
         if (5 * even >= 4 * ctas) ctas = even;
     }
+    // Otherwise a unit counts some tiles more, for what its end costs a CTA.
+    const unsigned pad = equal ? 0 : p8_unit_pad(RP);
+    unsigned total, before;
+    if (equal) {
+        total = tiles;
+        before = (unsigned)min(lane * 4, entries) * hi * (unsigned)p.G;
+    } else {
+        mine = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (n[k]) n[k] += pad;
+            mine += n[k];
+        }
+        unsigned x = mine * (unsigned)p.G;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        total = __shfl_sync(0xffffffffu, x, 31);
+        before = x - mine * (unsigned)p.G;
+    }
+    mine *= (unsigned)p.G;
     const unsigned c = blockIdx.x;
     const unsigned t0 = c < ctas ? total * c / ctas : total, t1 = c < ctas ? total * (c + 1) / ctas : total;
     // The lane whose entries hold tile t0, and where in them it lies.
@@ -389,6 +420,8 @@ __device__ __forceinline__ P8Plan p8_small_plan(const P8Lens<RP>& lens) {
     plan.g = __shfl_sync(0xffffffffu, (int)g, src);
     plan.off = __shfl_sync(0xffffffffu, (int)(in - g * ne), src);
     plan.ctas = (int)ctas;
+    plan.skip_pad(__shfl_sync(0xffffffffu, (int)(ne - pad), src), (int)pad, p.G);
+    if (lane == 0) lens.copy[kP8LenCopy] = (int)pad;
     __syncwarp();
     return plan;
 }
@@ -410,10 +443,15 @@ __device__ __noinline__ void p8_make_plan(const PagedFp8Params& p, int* len_copy
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (p.B <= kP8LenCopy)
         for (int b = threadIdx.x; b < p.B; b += THREADS) len_copy[b] = lens.global(b);
+    if (threadIdx.x == 0) len_copy[kP8LenCopy] = p8_unit_pad(RP);
     __syncthreads();
     const int e0 = (int)min((long long)entries, (long long)threadIdx.x * per), e1 = min(entries, e0 + per);
     long long mine = 0;
-    for (int e = e0; e < e1; ++e) mine += lens.tiles(e);
+    auto padded = [&](int e) {
+        const int n = lens.tiles(e);
+        return n ? n + p8_unit_pad(RP) : 0;
+    };
+    for (int e = e0; e < e1; ++e) mine += padded(e);
     mine *= p.G;
     long long x = mine;
 #pragma unroll
@@ -439,16 +477,18 @@ __device__ __noinline__ void p8_make_plan(const PagedFp8Params& p, int* len_copy
         plan->end = t1;
         plan->ctas = ctas;
         plan->entry = plan->g = plan->off = 0;
+        plan->left = 0;
         if (t0 < t1) {
             long long at = before;
-            int e = e0, n = lens.tiles(e);
+            int e = e0, n = padded(e);
             while (at + (long long)n * p.G <= t0) {
                 at += (long long)n * p.G;
-                n = lens.tiles(++e);
+                n = padded(++e);
             }
             plan->entry = e;
             plan->g = (int)((t0 - at) / n);
             plan->off = (int)((t0 - at) % n);
+            plan->skip_pad(n - p8_unit_pad(RP), p8_unit_pad(RP), p.G);
         }
     }
 }
@@ -655,7 +695,7 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
     gen += PS::kWarpMaxBytes;
     int* len_copy = reinterpret_cast<int*>(gen);
     gen += PS::kLenBytes;
-    P8Plan* plan_s = reinterpret_cast<P8Plan*>(gen);                      // 40 bytes
+    P8Plan* plan_s = reinterpret_cast<P8Plan*>(gen);                      // 48 bytes
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gen + 64);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gen + 68);
     volatile int* last_flag = reinterpret_cast<volatile int*>(gen + 72);  // [4]
@@ -715,11 +755,11 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
         // registers until a split unit's end needs it.
         if (lane == 0) *plan_s = plan;
         __syncwarp();
-        walk = {plan.end - plan.begin, plan.entry, plan.g, plan.off};
+        walk = {plan.left, plan.entry, plan.g, plan.off};
     } else {
         p8_make_plan<RP, PS::kThreads>(p, len_copy, plan_s, warp_sum);
         __syncthreads();
-        walk = {plan_s->end - plan_s->begin, plan_s->entry, plan_s->g, plan_s->off};
+        walk = {plan_s->left, plan_s->entry, plan_s->g, plan_s->off};
     }
     P8Segment seg;
     // Bounded waits of one thread, and of a softmax warp: all its lanes poll,
@@ -1309,7 +1349,8 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
                 const bool whole = seg.i0 == 0 && seg.i1 == seg.n;
                 int c0 = 0, n = 1;                // the CTAs that share the unit
                 if (!whole) {
-                    const long long unit0 = plan_s->begin + it0 - seg.i0;
+                    // Of a unit that began in another CTA, or goes on in one.
+                    const long long unit0 = seg.i0 > 0 ? plan_s->begin - seg.i0 : plan_s->end - seg.i1;
                     c0 = plan_s->owner(unit0);
                     n = plan_s->owner(unit0 + seg.n - 1) - c0 + 1;
                 }

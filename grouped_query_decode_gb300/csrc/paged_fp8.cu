@@ -112,7 +112,7 @@ int gqa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages
     p.by_heads = FastDiv((unsigned)p.heads_per_group);
     p.by_row_tiles = FastDiv((unsigned)p.row_tiles);
     const long long tiles = ((long long)max_pages_per_seq * page_size + kP8Tokens - 1) / kP8Tokens;
-    p.small_plan = (long long)B * p.row_tiles <= 128 && (long long)B * p.row_tiles * G * tiles < (1ll << 32) / (grid + 1);
+    p.small_plan = (long long)B * p.row_tiles <= 128 && (long long)B * p.row_tiles * G * (tiles + p8_unit_pad(p8_rows(R))) < (1ll << 32) / (grid + 1);
     a.grid = grid;
     a.stream = stream;
     const cudaError_t e = D == 64 ? launch_paged_fp8_d64(a) : launch_paged_fp8_d128(a);
