@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
     const uint32_t base = (raw + 1023u) & ~1023u;
     const uint32_t k_s = base, v_s = k_s + SK * TB, q_s = v_s + SV * TB, p_s = q_s + 2 * PS::kQBytes;
     unsigned char* gen = smem_raw + (p_s + 2 * PS::kPBytes - raw);
-    float* const handed = reinterpret_cast<float*>(gen - PS::kPBytes);    // group 1's O, in its P
+    float* const handed = reinterpret_cast<float*>(gen - 2 * PS::kPBytes);   // O of each group, in its P
     // Rows of the unit in q buffer i: scale2 * 2^-e, last visible key, output row.
     float* row_scale = reinterpret_cast<float*>(gen);                     // [2][RP]
     int* row_lim = reinterpret_cast<int*>(row_scale + 2 * RP);            // [2][RP]
@@ -1107,14 +1107,17 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
         float4* const my_sum = sums + x * RP + y * RH;
         float2* const factor = factors + x * RP + y * RH;
         int* const my_max = warp_max + (x * PS::kParts + y) * 4 * (RH + 1);
-        // Row r, column d of the O that group 1 hands over for this part.
-        auto handed_at = [&](int r, int d) -> float* {
-            if constexpr (PS::kParts == 1) return handed + r * D + d;
+        // Row r, column d of this part's O that a group hands over, in its own P
+        // operand, which its last product has read.
+        auto handed_at = [&](int group, int r, int d) -> float* {
+            float* const base = handed + group * (PS::kPBytes / 4);
+            if constexpr (PS::kParts == 1) return base + r * D + d;
             const int i = r * D + d;
-            return handed + ((i >> 9) * 2 + y) * 512 + (i & 511);
+            return base + ((i >> 9) * 2 + y) * 512 + (i & 511);
         };
         const int block_shift = min(p.page_shift, 6);
         uint32_t n_tiles = 0, n_merge = 0;       // phases of s_full and p_full, of m_full
+        bool lent = false;                       // this group's P holds an O that it handed over
         int it0 = 0, sg = 0;                     // the CTA's tile number at the segment's start
         int chunk0 = 0;                          // and its chunk of scales
         // The product of this group's tile `it` has completed.
@@ -1319,7 +1322,10 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
                 }
                 // P's operand is free once the group's previous product is done.
                 if (it >= 2) wait_product(it - 2);
-                if (x == 1 && first) all_wait(m_empty + 8 * y, n_merge + 1);      // and handed-over O is read
+                if (lent) {                       // and handed-over O is read
+                    all_wait(m_empty + 8 * y, n_merge + 1);
+                    lent = false;
+                }
                 // Column term * RP + row; 16 columns of a token are 16 bytes.
                 if constexpr (RH == 8) {
                     st_shared_v4(p_at, make_uint4(packed[0][0], packed[1][0], packed[0][1], packed[1][1]));
@@ -1373,10 +1379,11 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
                 const bool mine = D == 128 || lane < 16;
                 const int dim = D == 128 ? tok : w4 * 16 + lane;
                 const float unit = pow2i(ev) * (1.f / kP8ProbScale);
-                if (both && x == 1) {
+                // Of two groups, the one without the last tile hands its O over.
+                if (both && x != (last & 1)) {
 #pragma unroll
                     for (int r = 0; r < RH; ++r)
-                        if (mine) *handed_at(r, dim) = o[r] * unit;
+                        if (mine) *handed_at(x, r, dim) = o[r] * unit;
                     if (tok < RH) {
                         const float4 q = my_sum[tok];
                         other[y * RH + tok] = make_float2(-my_ref[tok], q.x + q.y + q.z + q.w);
@@ -1384,6 +1391,7 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(m_full + 8 * y);
                     ++n_merge;
+                    lent = true;
                 } else {
                     if (both) all_wait(m_full + 8 * y, n_merge);
                     const size_t slot_floats = p8_slot_floats(RP, D);
@@ -1420,12 +1428,12 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
                     // instructions' fetch (8 rows, 128 x 4096 tokens: 25.7 -> 25.5 us).
                     // With 32 rows that lost to 2-byte stores (registers).
                     constexpr bool kGather = PS::kParts == 1;
-                    float* const own = handed + (x == 0 ? -(int)(PS::kPBytes / 4) : 0);
+                    float* const own = handed + x * (PS::kPBytes / 4);
 #pragma unroll
                     for (int r = 0; r < RH; ++r) {
                         const float2 f = factor[r];
                         float v = o[r] * f.x;
-                        if (both && mine) v = fmaf(*handed_at(r, dim), f.y, v);
+                        if (both && mine) v = fmaf(*handed_at(x ^ 1, r, dim), f.y, v);
                         if (!mine) continue;
                         if (!whole)
                             slot[(y * RH + r) * D + dim] = v;
