@@ -888,8 +888,12 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
     };
 
     // The first segment's rows are split by softmax warps, which have nothing
-    // else to do yet, eight rows each (the loader warp would take them in turn,
-    // 1300 cycles each).
+    // else to do yet, eight rows each; those of later segments by the K loader,
+    // which is ahead of the products, in turn, 1300 cycles per eight rows. With
+    // 32 rows that is too long for short segments: the softmax group that is
+    // done first with a segment takes them. 512 units of 1 to 4096 tokens, 32
+    // rows: loader 82, group 77 us; 8 rows: 58 and 66 us.
+    constexpr bool kLoaderSplits = RP < 32;
     if (warp < RP / 8) {
         P8Walk<RP> peek = walk;
         if (peek.next(lens, seg)) {
@@ -909,16 +913,15 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
         while (ok && walk.next(lens, seg)) {
             int b, rt;
             lens.split(seg.entry, b, rt);
-            const int buf = sg & 1;
-            if (sg > 0) {                         // query rows of every segment but the first
+            if (kLoaderSplits && sg > 0) {
                 QRows next = load_rows(b, rt, seg.g, 0);
-                ok = warp_wait(q_empty + 8 * buf, ((sg >> 1) & 1) ^ 1, abort_flag, p.status, tmo);
+                ok = warp_wait(q_empty + 8 * (sg & 1), ((sg >> 1) & 1) ^ 1, abort_flag, p.status, tmo);
                 if (!ok) break;
 #pragma unroll 1
                 for (int r0 = 0; r0 < RP; r0 += 8) {
                     const QRows q = next;
                     if (r0 + 8 < RP) next = load_rows(b, rt, seg.g, r0 + 8);
-                    split_rows(q, lens.tokens(b), buf, r0);
+                    split_rows(q, lens.tokens(b), sg & 1, r0);
                 }
             }
             ++sg;
@@ -1477,6 +1480,15 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(q_empty + 8 * (sg & 1));
+            if (!kLoaderSplits && x != ((it0 + len - 1) & 1) && y * 4 + w4 < RP / 8) {
+                P8Walk<RP> peek = walk;
+                if (peek.next(lens, seg)) {
+                    lens.split(seg.entry, b, rt);
+                    const QRows q = load_rows(b, rt, seg.g, (y * 4 + w4) * 8);
+                    all_wait(q_empty + 8 * ((sg + 1) & 1), ((sg + 1) >> 1) + 1);
+                    split_rows(q, lens.tokens(b), (sg + 1) & 1, (y * 4 + w4) * 8);
+                }
+            }
             it0 += len;
             chunk0 += (len + kP8ScaleChunk - 1) / kP8ScaleChunk;
             ++sg;
