@@ -26,31 +26,33 @@
 // p through a power of two 2^c that follows the largest scale seen.
 //
 // Work: the tiles of all units, end to end, are shared equally by the CTAs
-// (one per SM). A unit that crosses CTAs leaves (O, m, l) per CTA in the
+// (one per SM; units of unlike lengths count a few tiles more for their end). A unit that crosses CTAs leaves (O, m, l) per CTA in the
 // workspace; the CTA that arrives last merges them. Per CTA: two groups of four
 // softmax warps (with 32 rows two such pairs, 16 rows each) take alternate
 // tiles. One warp brings K, another V (a TMA box per page, in the swizzle of
 // the operand layout; one warp issues a box in 65 cycles, two warps two); the
-// latter also splits the queries of every segment but the first and fetches the
-// blocks' scales, ahead of V by a chunk of tiles (behind a saturated HBM a lookup
-// of page and scale takes longer than a tile). Two warps issue the products.
+// latter also fetches the blocks' scales, ahead of V by a chunk of tiles (behind
+// a saturated HBM a lookup of page and scale takes longer than a tile). Two warps issue the products.
 // Every wait is bounded, as in the other kernels.
 //
 // What bounds it. Bytes: the cache, once. A tile of 8 rows takes 0.3 us, one of 32
-// rows 0.65 to 0.72 us (a softmax warp's chain of load, vote, exponentials and
+// rows 0.65 to 0.70 us (a softmax warp's chain of load, vote, exponentials and
 // four terms is 2400 cycles, two groups at a time), against 0.62 to 0.74 us for
 // a tile's 32 KB from HBM shared by 128 to 152 SMs. Around the tiles: 2 us of
 // launch, 1.5 us of plan, 2 us until the first softmax, and where a unit is
 // split 4 to 6 us for its parts (stores, one atomic, the last arriver's merge).
 // Measured on one GB300 (HBM copy 6.77 TB/s), B x H/G heads, tokens, page:
-//   16 x 32/8, D 128, 4096, 64           25.5 us, 5.3 TB/s (6.5 TB/s at 16384 tokens)
-//   64 x 32/1, D 128, 8192, 32           33.9 us, 4.0 TB/s
-//   1 x 64/8, D 128, 131072, 16          52.4 us, 5.1 TB/s
-//   64 x 64/8, 4 new tokens, D 128, up to 32768, 64    359 us, 6.1 TB/s
-//   1 x 32/8, 64 new tokens, D 64, 4096, 64            23.3 us (4.7 MB: latency)
+//   16 x 32/8, D 128, 4096, 64           25.5 us, 5.3 TB/s (6.6 TB/s at 16384 tokens)
+//   64 x 32/1, D 128, 8192, 32           33.2 us, 4.1 TB/s
+//   1 x 64/8, D 128, 131072, 16          52.7 us, 5.1 TB/s
+//   64 x 64/8, 4 new tokens, D 128, 512 to 32768, 64   321 us, 6.8 TB/s
+//   64 x 64/8, 4 new tokens, D 128, up to 4096, 64     77 us, 3.3 TB/s (8 rows 58 us)
+//   1 x 32/8, 64 new tokens, D 64, 4096, 64            23.4 us (4.7 MB: latency)
 // Tried and slower: asking for a barrier's phase ahead of its wait (MQA end +0.3
 // us), running the merge once without effect to fetch its instructions (+0.7 us),
-// 152 CTAs with uneven shares where 128 share equal units evenly (+2.8 us).
+// 152 CTAs with uneven shares where 128 share equal units evenly (+2.8 us), the
+// next unit's queries split between this one's tiles (ragged +12 to +35 us: any
+// longer loader loop slows every tile), a stage more in each ring (no change).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -92,14 +94,14 @@ struct P8Shape {
     static constexpr int kRefBytes = 2 * RP * 4;
     static constexpr int kWarpMaxBytes = 2 * kParts * 4 * (kRows + 1) * 4;
     static constexpr int kSumBytes = 2 * RP * 16;
-    static constexpr int kMergeBytes = 3 * RP * 8;                // group 1's (m, l); each group's row factors
+    static constexpr int kMergeBytes = 3 * RP * 8;                // (m, l) handed over; each group's row factors
     static constexpr int kLenBytes = kP8LenCopy * 4 + 16;         // and the plan's padding
     static constexpr int kScaleBytes = kP8ScaleChunks * kP8ScaleChunk * 16 * 4;
     static constexpr int kMiscBytes = 320;
     static constexpr int kSmemBytes = 1024 + (kStagesK + kStagesV) * kTileBytes + 2 * kQBytes + 2 * kPBytes +
                                       kRowInfoBytes + kRefBytes + kWarpMaxBytes + kSumBytes + kMergeBytes +
                                       kLenBytes + kScaleBytes + kMiscBytes + 8 * kBars;
-    // Group 1 hands its O over in its own P operand, which its last product has read.
+    // A group hands its O over in its own P operand, which its last product has read.
     static_assert(RP * D * 4 <= kPBytes, "O fits P");
     static constexpr uint32_t kColS = 0, kColO = 2 * kNs;         // S_0 | S_1 | O_0 | O_1
     static constexpr uint32_t kCols = 2 * kNs + 2 * kNp;
@@ -686,7 +688,7 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
     gen += PS::kSumBytes;
     float* neg_ref = reinterpret_cast<float*>(gen);                       // [2][RP]: -m
     gen += PS::kRefBytes;
-    float2* other = reinterpret_cast<float2*>(gen);                       // [RP]: (m, l) of group 1
+    float2* other = reinterpret_cast<float2*>(gen);                       // [RP]: (m, l) handed over
     float2* factors = other + RP;                                         // [2][RP]: weights of the groups' O
     gen += PS::kMergeBytes;
     float* scale_ring = reinterpret_cast<float*>(gen);                    // [slots][8 of K, 8 of V]
