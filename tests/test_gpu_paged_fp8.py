@@ -176,6 +176,19 @@ def test_many_sequences():
     check(c, *run(c))
 
 
+@pytest.mark.parametrize("B", [90, 420])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H,G,sq", [(8, 2, 1), (32, 2, 1), (64, 2, 1), (8, 2, 8), (24, 2, 6)], ids=str)
+def test_many_units_of_unlike_lengths(H, G, sq, D, B):
+    """Many units to a CTA, of one tile to several, whole and cut: lengths of
+    zero, of whole tiles, and a few long ones among short ones."""
+    rng = np.random.default_rng(540 + H + sq + D + B)
+    lens = rng.choice([0, 1, 127, 128, 129, 256, 300, 900], B, p=[.1, .1, .1, .2, .15, .15, .15, .05])
+    lens[::7] = rng.integers(0, 700, lens[::7].size)
+    c = Case(540 + H + sq + D + B, B, sq, H, G, D, 64, lens)
+    check(c, *run(c))
+
+
 def test_lse_is_optional():
     c = Case(530, 2, 1, 8, 2, 128, 64, [200, 77])
     ref = c.reference()
