@@ -46,7 +46,7 @@
 //   64 x 32/1, D 128, 8192, 32           33.2 us, 4.1 TB/s
 //   1 x 64/8, D 128, 131072, 16          52.7 us, 5.1 TB/s
 //   64 x 64/8, 4 new tokens, D 128, 512 to 32768, 64   321 us, 6.8 TB/s
-//   64 x 64/8, 4 new tokens, D 128, up to 4096, 64     77 us, 3.3 TB/s (8 rows 58 us)
+//   64 x 64/8, 4 new tokens, D 128, up to 4096, 64     77 us, 3.3 TB/s (8 rows 52 us)
 //   1 x 32/8, 64 new tokens, D 64, 4096, 64            23.4 us (4.7 MB: latency)
 // Tried and slower: asking for a barrier's phase ahead of its wait (MQA end +0.3
 // us), running the merge once without effect to fetch its instructions (+0.7 us),
@@ -266,7 +266,15 @@ struct P8Lens {
     const PagedFp8Params& p;
     int* copy;
     __device__ int global(int b) const { return clamp_len(p.lens[b], p.max_pages << p.page_shift); }
-    __device__ int tokens(int b) const { return p.B <= kP8LenCopy ? copy[b] : global(b); }
+    // One copy for all warps: of all sequences, or of those from the first one of
+    // the CTA's share on. With 32 rows (and no register to spare) only the former:
+    // the latter took lengths up to 4096 from 76 to 83 us; with 8 rows 1500
+    // sequences gained, 777 to 659 us.
+    __device__ int tokens(int b) const {
+        if constexpr (RP == 32) return p.B <= kP8LenCopy ? copy[b] : global(b);
+        const unsigned i = (unsigned)(b - copy[kP8LenCopy + 1]);
+        return i < kP8LenCopy ? copy[i] : global(b);
+    }
     __device__ void split(int entry, int& b, int& rt) const {
         b = p.by_row_tiles(entry);
         rt = entry - b * p.row_tiles;
@@ -294,10 +302,20 @@ struct P8Walk {
     int entry, g, off;
     __device__ bool next(const P8Lens<RP>& lens, P8Segment& s) {
         if (left <= 0) return false;
-        int n = lens.tiles(entry);
-        while (n == 0) {
-            if (++entry >= lens.p.B * lens.p.row_tiles) return false;   // not with one copy of the lengths
+        int n;
+        if constexpr (RP == 32) {
             n = lens.tiles(entry);
+            while (n == 0) {
+                if (++entry >= lens.p.B * lens.p.row_tiles) return false;   // not while the lengths stay
+                n = lens.tiles(entry);
+            }
+        } else {                      // the same; 8 rows, lengths up to 4096: 55 -> 51 us
+            n = 0;
+            while (n == 0) {
+                if (entry >= lens.p.B * lens.p.row_tiles) return false;
+                n = lens.tiles(entry);
+                if (n == 0) ++entry;
+            }
         }
         s.entry = entry;
         s.g = g;
@@ -423,7 +441,7 @@ __device__ __forceinline__ P8Plan p8_small_plan(const P8Lens<RP>& lens) {
     plan.off = __shfl_sync(0xffffffffu, (int)(in - g * ne), src);
     plan.ctas = (int)ctas;
     plan.skip_pad(__shfl_sync(0xffffffffu, (int)(ne - pad), src), (int)pad, p.G);
-    if (lane == 0) lens.copy[kP8LenCopy] = (int)pad;
+    if (lane == 0) lens.copy[kP8LenCopy] = (int)pad;        // copy[kP8LenCopy + 1] is the caller's
     __syncwarp();
     return plan;
 }
@@ -445,7 +463,11 @@ __device__ __noinline__ void p8_make_plan(const PagedFp8Params& p, int* len_copy
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (p.B <= kP8LenCopy)
         for (int b = threadIdx.x; b < p.B; b += THREADS) len_copy[b] = lens.global(b);
-    if (threadIdx.x == 0) len_copy[kP8LenCopy] = p8_unit_pad(RP);
+    if (threadIdx.x == 0) {
+        len_copy[kP8LenCopy] = p8_unit_pad(RP);
+        len_copy[kP8LenCopy + 1] = p.B <= kP8LenCopy ? 0 : p.B;   // none yet
+        *plan = P8Plan{};
+    }
     __syncthreads();
     const int e0 = (int)min((long long)entries, (long long)threadIdx.x * per), e1 = min(entries, e0 + per);
     long long mine = 0;
@@ -492,6 +514,12 @@ __device__ __noinline__ void p8_make_plan(const PagedFp8Params& p, int* len_copy
             plan->off = (int)((t0 - at) % n);
             plan->skip_pad(n - p8_unit_pad(RP), p8_unit_pad(RP), p.G);
         }
+    }
+    if (RP < 32 && p.B > kP8LenCopy) {
+        __syncthreads();
+        const int first = p.by_row_tiles(plan->entry);
+        for (int i = threadIdx.x; i < kP8LenCopy && first + i < p.B; i += THREADS) len_copy[i] = lens.global(first + i);
+        if (threadIdx.x == 0) len_copy[kP8LenCopy + 1] = first;
     }
 }
 
@@ -751,6 +779,7 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
     P8Walk<RP> walk;
     if (p.small_plan) {
         if (threadIdx.x < 128) len_copy[threadIdx.x] = (int)threadIdx.x < p.B ? lens.global(threadIdx.x) : 0;
+        if (threadIdx.x == 0) len_copy[kP8LenCopy + 1] = 0;
         __syncthreads();
         const P8Plan plan = p8_small_plan<RP>(lens);
         // Kept in shared memory (every warp writes the same) rather than in

@@ -220,6 +220,7 @@ int gqa_prefill(const void* q, const void* k_cache, const void* v_cache, const i
  *
  * A NaN code in K or V at a position a row sees makes that row NaN (in V with
  * sq > 1 possibly in every column); codes at t >= seq_lens[b] are never used.
+ * seq_lens and block_table stay as they are until the call has finished.
  */
 int gqa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
                          const float* v_scale, const int32_t* block_table, const int32_t* seq_lens,
