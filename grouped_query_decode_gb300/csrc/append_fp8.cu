@@ -322,14 +322,29 @@ extern "C" int gqa_append_paged_fp8(const void* k_new, const void* v_new, void* 
         2ll * G * p.blocks * B >= (1ll << 31))
         return GQA_ERR_UNSUPPORTED;
     // Up to 8 new tokens a sequence: a warp per block holds them in registers;
-    // beyond that a CTA of 256 threads does, and enough blocks go to one CTA
-    // for all of them to be resident at once (four to an SM).
+    // beyond that a CTA of 256 threads does, four to an SM, with a run of blocks.
     int sms;
     unsigned* status;
     const int st = current_device(&sms, &status);
     if (st != GQA_OK) return st;
-    const long long blocks = 2ll * G * p.blocks * B;
-    p.per = sq <= 8 ? 1 : (int)((blocks + 4ll * sms - 1) / (4ll * sms));
+    p.per = 1;
+    if (sq > 8) {
+        // The run that ends first: a block's time each, half of one to start, and
+        // the CTAs beyond those that are resident at once take turns, half a run
+        // of which the others wait for. Runs of 1 | 2 | 3 | 4 | 6 blocks, us: 4 x 2048
+        // tokens 12.2 | 11.9 | 12.4 | 11.0 | 14.1; 3 x 777 4.0 | 5.1 | 6.5 | | 9.7; 8 x
+        // 8192 72.9 | 68.3 | 66.1 | | 64.8 (as few as fit at once, 28: 76.7).
+        const long long slots = 4ll * sms;
+        long long best = 0;
+        for (int per = 1; per <= 8; ++per) {
+            const long long ctas = 2ll * G * B * ((p.blocks + per - 1) / per);
+            const long long cost = ctas <= slots ? (2 * per + 1) * slots : ctas * (2 * per + 1) + per * slots;
+            if (best == 0 || cost < best) {
+                best = cost;
+                p.per = per;
+            }
+        }
+    }
     if (p.per > p.blocks) p.per = p.blocks;
     p.runs = (p.blocks + p.per - 1) / p.per;
     cudaError_t e;
