@@ -9,10 +9,10 @@
 // maximum. Nothing is shared between groups, so no order of execution changes
 // a result.
 //
-// Bytes: 2 read and 1 written per element. Blocks of 64 tokens by a CTA of 256
-// threads, a run of blocks each, the next block's tokens under way behind the
-// present one's maximum and conversion: 2048 tokens of four sequences, 8 KV
-// heads of 128 (50 MB), 11.0 us, 4.6 TB/s with the launch's 2 us. The schedulers
+// Bytes: 2 read and 1 written per element. Four threads a token of a block, a run
+// of blocks each, the next block's tokens under way behind the present one's
+// maximum and conversion: 2048 tokens of four sequences, 8 KV heads of 128 (50
+// MB), 11.0 us, 4.6 TB/s with the launch's 2 us (8 x 8192 tokens 65 us, 6.2 TB/s). The schedulers
 // issue 60 % of the time there, so instructions count: two products to an
 // instruction, packed maxima, no division by the page size (13.4 us without
 // these). Up to 8 new tokens a warp takes a block by itself: one token of 64
@@ -157,9 +157,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) append_kernel(const _
             if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = m;
             __syncthreads();
 #pragma unroll
-            for (int w = 0; w < TPI / 32; w += 4) {
-                const uint4 u = *reinterpret_cast<const uint4*>(mine + w);
-                m = max(max(m, max(u.x, u.y)), max(u.z, u.w));
+            for (int w = 0; w < TPI / 32; w += 2) {
+                const uint2 u = *reinterpret_cast<const uint2*>(mine + w);
+                m = max(m, max(u.x, u.y));
             }
         } else {
             __syncwarp();
@@ -322,7 +322,9 @@ extern "C" int gqa_append_paged_fp8(const void* k_new, const void* v_new, void* 
         2ll * G * p.blocks * B >= (1ll << 31))
         return GQA_ERR_UNSUPPORTED;
     // Up to 8 new tokens a sequence: a warp per block holds them in registers;
-    // beyond that a CTA of 256 threads does, four to an SM, with a run of blocks.
+    // beyond that a CTA of four threads per token of a block does, 1024 threads to
+    // an SM, with a run of blocks (4 x 2048 tokens in 16-token pages: 23.5 us with
+    // 256 threads a block, 11.0 with 64; 32-token pages 16.0 and 10.9).
     int sms;
     unsigned* status;
     const int st = current_device(&sms, &status);
@@ -334,7 +336,7 @@ extern "C" int gqa_append_paged_fp8(const void* k_new, const void* v_new, void* 
         // of which the others wait for. Runs of 1 | 2 | 3 | 4 | 6 blocks, us: 4 x 2048
         // tokens 12.2 | 11.9 | 12.4 | 11.0 | 14.1; 3 x 777 4.0 | 5.1 | 6.5 | | 9.7; 8 x
         // 8192 72.9 | 68.3 | 66.1 | | 64.8 (as few as fit at once, 28: 76.7).
-        const long long slots = 4ll * sms;
+        const long long slots = 1024ll / (4 * p.size) * sms;
         long long best = 0;
         for (int per = 1; per <= 8; ++per) {
             const long long ctas = 2ll * G * B * ((p.blocks + per - 1) / per);
@@ -350,6 +352,10 @@ extern "C" int gqa_append_paged_fp8(const void* k_new, const void* v_new, void* 
     cudaError_t e;
     if (sq <= 8)
         e = D == 64 ? launch_append<64, 32, 128, 2>(p, stream) : launch_append<128, 32, 128, 4>(p, stream);
+    else if (p.size == 16)
+        e = D == 64 ? launch_append<64, 64, 64, 2>(p, stream) : launch_append<128, 64, 64, 4>(p, stream);
+    else if (p.size == 32)
+        e = D == 64 ? launch_append<64, 128, 128, 2>(p, stream) : launch_append<128, 128, 128, 4>(p, stream);
     else
         e = D == 64 ? launch_append<64, 256, 256, 2>(p, stream) : launch_append<128, 256, 256, 4>(p, stream);
     return e == cudaSuccess ? GQA_OK : remember_cuda_error(e);
