@@ -12,10 +12,10 @@
 // Bytes: 2 read and 1 written per element. Four threads a token of a block, a run
 // of blocks each, the next block's tokens under way behind the present one's
 // maximum and conversion: 2048 tokens of four sequences, 8 KV heads of 128 (50
-// MB), 11.0 us, 4.6 TB/s with the launch's 2 us (8 x 8192 tokens 65 us, 6.2 TB/s). The schedulers
-// issue 60 % of the time there, so instructions count: two products to an
-// instruction, packed maxima, no division by the page size (13.4 us without
-// these). Up to 8 new tokens a warp takes a block by itself: one token of 64
+// MB), 11.0 us, 4.6 TB/s with the launch's 2 us (8 x 8192 tokens 65 us, 6.2
+// TB/s). The schedulers issue 60 % of the time there, so instructions count: two
+// products to an instruction, packed maxima, no division by the page size (13.4
+// us without these). Up to 8 new tokens a warp takes a block by itself: one token of 64
 // sequences 2.4 us, which is latency (length, then page and tokens, then codes).
 #include <cuda_runtime.h>
 
