@@ -35,6 +35,7 @@ namespace cg = cooperative_groups;
 constexpr int kPlanCtas = 8;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;            // of a CTA
+static_assert(kPlanWarps == 32, "a warp a lane");
 constexpr int kAllWarps = kPlanCtas * kPlanWarps;
 constexpr int kMoveThreads = 256;
 
@@ -95,14 +96,9 @@ __device__ int block_exclusive_sum(int v, int* total) {
     __syncthreads();
     if (lane == 31) warp_sum[warp] = x;
     __syncthreads();
-    int before = 0, all = 0;
-    for (int w = 0; w < kPlanWarps; ++w) {
-        const int s = warp_sum[w];
-        if (w < warp) before += s;
-        all += s;
-    }
-    *total = all;
-    return before + x - v;
+    const int s = warp_sum[lane];
+    *total = __reduce_add_sync(0xffffffffu, s);
+    return __reduce_add_sync(0xffffffffu, lane < warp ? s : 0) + x - v;
 }
 
 // x = row * n + column, of 64-bit x; in 32 bits where they do (a third of the time).
@@ -161,11 +157,9 @@ __device__ Ranks rank_pages(const int32_t* refs, int num_pages) {
     }
     if (lane == 0) warp_live[warp] = n;
     __syncthreads();
-    int before = 0, mine = 0;
-    for (int w = 0; w < kPlanWarps; ++w) {
-        if (w < warp) before += warp_live[w];
-        mine += warp_live[w];
-    }
+    const int of_lane = warp_live[lane];
+    const int mine = __reduce_add_sync(0xffffffffu, of_lane);
+    int before = __reduce_add_sync(0xffffffffu, lane < warp ? of_lane : 0);
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // all CTAs have started
     if (threadIdx.x < kPlanCtas) cluster.map_shared_rank(cta_live, threadIdx.x)[cta] = mine;
     cluster.sync();
