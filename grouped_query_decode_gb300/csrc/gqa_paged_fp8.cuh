@@ -42,10 +42,10 @@
 // launch, 1.5 us of plan, 2 us until the first softmax, and where a unit is
 // split 4 to 6 us for its parts (stores, one atomic, the last arriver's merge).
 // Measured on one GB300 (HBM copy 6.77 TB/s), B x H/G heads, tokens, page:
-//   16 x 32/8, D 128, 4096, 64           25.5 us, 5.3 TB/s (6.6 TB/s at 16384 tokens)
-//   64 x 32/1, D 128, 8192, 32           33.2 us, 4.1 TB/s
-//   1 x 64/8, D 128, 131072, 16          52.7 us, 5.1 TB/s
-//   64 x 64/8, 4 new tokens, D 128, 512 to 32768, 64   321 us, 6.8 TB/s
+//   16 x 32/8, D 128, 4096, 64           25.2 us, 5.3 TB/s (6.6 TB/s at 16384 tokens)
+//   64 x 32/1, D 128, 8192, 32           33.5 us, 4.0 TB/s
+//   1 x 64/8, D 128, 131072, 16          52.5 us, 5.1 TB/s
+//   64 x 64/8, 4 new tokens, D 128, 512 to 32768, 64   318 us, 6.9 TB/s
 //   64 x 64/8, 4 new tokens, D 128, up to 4096, 64     77 us, 3.3 TB/s (8 rows 52 us)
 //   1 x 32/8, 64 new tokens, D 64, 4096, 64            23.4 us (4.7 MB: latency)
 // Tried and slower: asking for a barrier's phase ahead of its wait (MQA end +0.3

@@ -9,11 +9,11 @@
 // each other (how many free pages lie before mine) goes through distributed
 // shared memory in one exchange.
 // What bounds it: the plan is latency (a cluster's start, one pass over the
-// counts, one exchange, one pass over what it kept of them: 4 to 5 us for 65536
+// counts, one exchange, one pass over what it kept of them: 3 to 5 us up to 65536
 // pages; one CTA took 13), the rest bytes. Measured: a fork of 32 beams, 1.3 MB of
-// pages, 8.5 us; one of 64 beams over 64 layers, 167 MB, 32 us, 5.2 TB/s; 1 GB
-// packed 161 us, 6.2 TB/s of 6.77 for a plain copy; pages reserved for 256
-// sequences and given back in a pool of 65536, 11.9 us with three copies of the
+// pages, 7.3 us; one of 64 beams over 64 layers, 167 MB, 31 us, 5.4 TB/s; 1 GB
+// packed 163 us, 6.2 TB/s of 6.77 for a plain copy; pages reserved for 256
+// sequences and given back in a pool of 65536, 11.1 us with three copies of the
 // table, the lengths and the counts between the calls.
 //
 // All of it is integer work with one result: pages are taken in ascending
