@@ -413,6 +413,65 @@ def test_an_expired_wait_is_reported_and_the_context_survives():
         assert np.array_equal(got[0], ref[0]) and np.array_equal(got[1], ref[1])
 
 
+def test_host_threads_with_a_stream_each():
+    """Four threads, attention and page management at once, each on its own
+    stream and so with its own kept workspace, results as without the others."""
+    import threading
+    cases = [Case(670 + i, 3, 1 + i, 16, 2, 64 if i % 2 else 128, 32, [1500 - 300 * i, 77, 640]) for i in range(4)]
+    refs, wrong = [run(c) for c in cases], []
+
+    def work(i):
+        try:
+            c = cases[i]
+            B, sq, H, G, D, page = c.shape
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                d = c.device()
+                o = [torch.empty(B, sq, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(20)]
+                lse = torch.empty(B, sq, H, device="cuda")
+                table = torch.full((B, 40), -1, dtype=torch.int32, device="cuda")
+                refs_, counts = torch.zeros(200, dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+                done = torch.ones(B, dtype=torch.bool, device="cuda")
+                for x in o:
+                    lens = torch.full((B,), 16 * (5 + i), dtype=torch.int32, device="cuda")
+                    gq.gqa_pages_reserve(table, lens, refs_, 16, counts)
+                    gq.gqa_decode_paged_fp8(*d, c.sm, x, lse)
+                    gq.gqa_pages_free(done, table, lens, refs_)
+                stream.synchronize()
+                same = all(np.array_equal(bf16_to_f64(x), refs[i][0]) for x in o)
+                if not (same and counts.tolist() == [B * (5 + i), 200] and not bool(refs_.any()) and bool((table == -1).all())):
+                    wrong.append(i)
+        except Exception as e:                    # a thread's failure is the test's
+            wrong.append((i, repr(e)))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not wrong and not any(t.is_alive() for t in threads), wrong
+
+
+@pytest.mark.parametrize("H,G,sq,D", [(64, 2, 1, 128), (8, 1, 4, 64), (32, 2, 1, 128)], ids=str)
+def test_an_expired_wait_with_more_rows_and_units(H, G, sq, D):
+    """16 and 32 rows, CTAs with parts of several units: the call ends, says so,
+    and leaves a workspace that the next calls use as if nothing had been."""
+    c = Case(661, 8, sq, H, G, D, 64, [3000, 1000, 129, 2500, 1, 700, 2048, 1500])
+    d = c.device()
+    n = gq.gqa_decode_paged_fp8_workspace_bytes(8, sq, H, G, D, 64, c.most)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    ref = run(c, d, workspace=ws)
+    check(c, *ref)
+    o = torch.empty(c.shape[0], sq, H, D, dtype=torch.bfloat16, device="cuda")
+    for tile in (0, 3):
+        with env(GQA_DECODE_DEBUG_TIMEOUT_MS=200, GQA_DECODE_DEBUG_SKIP_TILE=tile):
+            gq.gqa_decode_paged_fp8(*d, c.sm, o, workspace=ws)
+            assert gq.gqa_decode_check_error() == gq.GQA_ERR_DEVICE_TIMEOUT
+        for _ in range(2):
+            got = run(c, d, workspace=ws)
+            assert np.array_equal(got[0], ref[0]) and np.array_equal(got[1], ref[1])
+
+
 def test_page_pool_past_2_31_codes():
     """A pool of more than 2^31 codes: the last pages' bytes and scales."""
     G, D, page = 8, 128, 64
