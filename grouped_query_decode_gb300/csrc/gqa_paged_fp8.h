@@ -60,11 +60,13 @@ struct PagedFp8Launch {
 
 inline int p8_rows(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : kP8MaxRows; }
 // Tiles that a unit counts beyond its own where the units are not alike: what its
-// end (its output, the next one's queries) costs the CTA. Lengths of 512 to 32768
-// with 32 rows, GB/s at 0 | 4 | 8 | 12: 5820 | 6260 | 6460 | 6400; lengths up to
-// 4096: 1830 | 2460 | 2980 | 3060; with 8 rows 3210 | 4170 | 4300 | 4270, but 300
-// sequences, 64-dimensional heads: 6330, 2970 | 6570, 3010 | 6400, 2910 | 6230, 2830.
-__host__ __device__ constexpr int p8_unit_pad(int rows) { return rows == 32 ? 8 : 4; }
+// end (its output, the next one's queries) costs the CTA. GB/s with 512 units of
+// 512 to 32768 | of up to 4096 tokens, pad by pad: 32 rows 0: 5820 | 1830, 4: 6260 |
+// 2460, 8: 6460 | 2980, 12: 6400 | 3060; 16 rows 4: 6930 | 3260, 6: 6900 | 3550, 8: 6860 |
+// 3760; 8 rows 0: 6920 | 3210, 4: 7010 | 5150, 8: 6960 | 5130 (300 sequences 0:
+// 6330, 4: 6680, 8: 6460).
+__host__ __device__ constexpr int p8_unit_pad(int rows) { return rows == 32 ? 8 : rows == 16 ? 6 : 4; }
+
 __host__ __device__ inline size_t p8_slot_floats(int rows, int D) { return (size_t)rows * D + 2 * rows; }
 
 cudaError_t launch_paged_fp8_d64(const PagedFp8Launch& a);
