@@ -158,6 +158,25 @@ def test_a_held_scale_that_is_not_positive_counts_as_zero():
     p.check()
 
 
+@pytest.mark.parametrize("sq", [1, 20, 200])
+def test_positions_up_to_almost_2_31(sq):
+    """The last tokens of the widest table in the largest pages: as the last
+    tokens of a table of one page."""
+    page, most = 65536, 32000
+    x = [bf16(np.random.default_rng(112 + i).standard_normal((1, sq, 1, 64))).cuda() for i in range(2)]
+    got = []
+    for n in (1, most):
+        pool = [torch.zeros(2, 1, page, 64, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        scale = [torch.full((2, 1, 1024), 2.0 ** -9, device="cuda") for _ in range(2)]
+        table = torch.full((1, n), -1, dtype=torch.int32, device="cuda")
+        table[0, -1] = 1
+        lens = torch.tensor([n * page - 5], dtype=torch.int32, device="cuda")
+        gq.gqa_append_paged_fp8(*x, *pool, *scale, table, lens)
+        got.append(pool + scale)
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert all(bool(p[1, 0, page - 5 - sq:page - 5].any(1).all()) and not bool(p[1, 0, page - 5:].any()) for p in got[1][:2])
+
+
 def test_append_then_attend_serves_the_values(monkeypatch):
     """A prompt, then tokens one by one, through the public calls alone: the
     attention is the oracle's over the values the model quantised."""

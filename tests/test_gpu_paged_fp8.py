@@ -170,6 +170,18 @@ def test_lengths_are_clamped():
     check(c, *run(c))
 
 
+@pytest.mark.parametrize("H,sq", [(8, 1), (32, 1)])
+def test_table_for_almost_2_31_tokens(H, sq):
+    """Two sequences in the largest pages and the widest table: sizes whose
+    plan does not fit 32 bits, for few sequences."""
+    c = Case(515, 2, sq, H, 1, 64, 65536, [3000, 500], extra=0)
+    ref = c.reference()
+    d = c.device()
+    d[5] = torch.full((2, 32000), -1, dtype=torch.int32, device="cuda")
+    d[5][:, :1] = torch.from_numpy(c.table)
+    check(c, *run(c, d), ref)
+
+
 def test_many_sequences():
     lens = np.random.default_rng(1).integers(0, 90, 700)
     c = Case(520, 700, 1, 4, 2, 64, 32, lens)
