@@ -23,11 +23,10 @@ struct FastDiv {
         while ((1u << shift) < d) ++shift;
         mul = (unsigned)((((1ull << shift) - d) << 32) / d + 1);
     }
-#ifdef __CUDACC__
-    __device__ __forceinline__ int operator()(int n) const {
-        return (int)((__umulhi((unsigned)n, mul) + (unsigned)n) >> shift);
+    __host__ __device__ int operator()(int n) const {
+        const unsigned high = (unsigned)(((unsigned long long)(unsigned)n * mul) >> 32);
+        return (int)((high + (unsigned)n) >> shift);
     }
-#endif
 };
 
 struct PagedFp8Params {
@@ -66,6 +65,26 @@ inline int p8_rows(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : kP8MaxRows; }
 // 3760; 8 rows 0: 6920 | 3210, 4: 7010 | 5150, 8: 6960 | 5130 (300 sequences 0:
 // 6330, 4: 6680, 8: 6460).
 __host__ __device__ constexpr int p8_unit_pad(int rows) { return rows == 32 ? 8 : rows == 16 ? 6 : 4; }
+
+// CTAs of a call: one per SM, fewer if even full tables hold less work.
+inline long long p8_table_tiles(int page_size, int max_pages) {
+    return ((long long)max_pages * page_size + kP8Tokens - 1) / kP8Tokens;
+}
+inline int p8_grid(int B, int G, int R, int page_size, int max_pages, int sms) {
+    const int rows = p8_rows(R);
+    const long long units = (long long)B * G * ((R + rows - 1) / rows);
+    const long long split = units * p8_table_tiles(page_size, max_pages) / kP8MinTiles;
+    const long long want = split > units ? split : units;
+    return (int)(want < sms ? want : sms);
+}
+// Whether every warp plans by itself: up to 128 entries (b, row tile), and
+// products of tiles and CTAs that fit 32 bits.
+inline bool p8_small(int B, int G, int R, int page_size, int max_pages, int grid) {
+    const int rows = p8_rows(R);
+    const long long entries = (long long)B * ((R + rows - 1) / rows);
+    return entries <= 128 && entries * G * (p8_table_tiles(page_size, max_pages) + p8_unit_pad(rows)) <
+                                 (1ll << 32) / (grid + 1);
+}
 
 __host__ __device__ inline size_t p8_slot_floats(int rows, int D) { return (size_t)rows * D + 2 * rows; }
 

@@ -23,15 +23,6 @@ int check_paged_fp8(int B, int sq, int H, int G, int D, int page_size, int max_p
     return GQA_OK;
 }
 
-// CTAs of a call: one per SM, fewer if even full tables hold less work.
-int paged_fp8_grid(int B, int G, int R, int page_size, int max_pages, int sms) {
-    const int rows = p8_rows(R);
-    const long long units = (long long)B * G * ((R + rows - 1) / rows);
-    const long long tiles = ((long long)max_pages * page_size + kP8Tokens - 1) / kP8Tokens;
-    const long long split = units * tiles / kP8MinTiles, want = split > units ? split : units;
-    return (int)(want < sms ? want : sms);
-}
-
 size_t counter_bytes(int grid) { return (sizeof(unsigned long long) * 2 * (size_t)grid + 255) & ~size_t(255); }
 
 size_t paged_fp8_ws_bytes(int grid, int R, int D) {
@@ -49,7 +40,7 @@ size_t gqa_decode_paged_fp8_workspace_bytes(int B, int sq, int H, int G, int D, 
     unsigned* status;
     if (current_device(&sms, &status) != GQA_OK) return 0;
     const int R = H / G * sq;
-    return paged_fp8_ws_bytes(paged_fp8_grid(B, G, R, page_size, max_pages_per_seq, sms), R, D);
+    return paged_fp8_ws_bytes(p8_grid(B, G, R, page_size, max_pages_per_seq, sms), R, D);
 }
 
 int gqa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
@@ -74,7 +65,7 @@ int gqa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages
     st = current_device(&sms, &status);
     if (st != GQA_OK) return st;
     const int R = H / G * sq;
-    const int grid = paged_fp8_grid(B, G, R, page_size, max_pages_per_seq, sms);
+    const int grid = p8_grid(B, G, R, page_size, max_pages_per_seq, sms);
     if (!workspace || workspace_bytes < paged_fp8_ws_bytes(grid, R, D) ||
         (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return GQA_ERR_WORKSPACE;
@@ -111,8 +102,7 @@ int gqa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages
     p.blocks = (page_size + 63) / 64;
     p.by_heads = FastDiv((unsigned)p.heads_per_group);
     p.by_row_tiles = FastDiv((unsigned)p.row_tiles);
-    const long long tiles = ((long long)max_pages_per_seq * page_size + kP8Tokens - 1) / kP8Tokens;
-    p.small_plan = (long long)B * p.row_tiles <= 128 && (long long)B * p.row_tiles * G * (tiles + p8_unit_pad(p8_rows(R))) < (1ll << 32) / (grid + 1);
+    p.small_plan = p8_small(B, G, R, page_size, max_pages_per_seq, grid);
     a.grid = grid;
     a.stream = stream;
     const cudaError_t e = D == 64 ? launch_paged_fp8_d64(a) : launch_paged_fp8_d128(a);
