@@ -91,10 +91,11 @@ struct P8Plan {
     long long left;                // of the latter from the first tile on
     int entry, g, off;             // where it begins
     int ctas;                      // CTAs that share the tiles
-    // A share that begins in a unit's padding begins with the next unit.
+    // What is left of the share: nothing of an empty one, wherever it would begin;
+    // one that begins in a unit's padding begins with the next unit.
     __device__ void skip_pad(int n, int pad, int G) {
         left = end - begin;
-        if (off < n) return;
+        if (left <= 0 || off < n) return;
         left -= n + pad - off;
         off = 0;
         if (++g == G) {

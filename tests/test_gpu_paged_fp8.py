@@ -501,3 +501,20 @@ def test_page_pool_past_2_31_codes():
         dev[i] = big
     dev[5] = torch.where(dev[5] >= 0, dev[5] + (num - n), dev[5])
     check(c, *run(c, dev))
+
+
+@pytest.mark.parametrize("H,G,sq", [(32, 8, 1), (64, 2, 1), (8, 2, 9)], ids=str)
+@pytest.mark.parametrize("empty", [1, 3])
+def test_an_empty_sequence_before_many_units(empty, H, G, sq):
+    """A freed row among 16, tables wider than the lengths: the CTAs without a
+    share do nothing, and so repeated calls agree bit for bit."""
+    lens = [1024] * 16
+    lens[empty] = 0
+    lens[9:12] = [700, 1, 2000]
+    c = Case(700 + empty + sq, 16, sq, H, G, 128, 64, lens, most=64)
+    dev = c.device()
+    first = run(c, dev)
+    check(c, *first)
+    for rep in range(30):
+        again = run(c, dev)
+        assert np.array_equal(again[0], first[0]) and np.array_equal(again[1], first[1]), rep
