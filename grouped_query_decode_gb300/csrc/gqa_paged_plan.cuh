@@ -103,10 +103,11 @@ struct P8Plan {
             ++entry;
         }
     }
-    // The CTA whose share holds tile t of the call.
+    // The CTA whose share holds tile t of the call; in 32 bits where both sides fit.
     __device__ int owner(long long t) const {
         const unsigned long long x = (unsigned long long)(t + 1) * (unsigned)ctas - 1;
-        return x >> 32 ? (int)(x / (unsigned long long)total) : (int)((unsigned)x / (unsigned)total);
+        const unsigned long long of = (unsigned long long)total;
+        return (x | of) >> 32 ? (int)(x / of) : (int)((unsigned)x / (unsigned)of);
     }
     // The CTAs c0 .. c0 + n - 1 share the unit of a segment of this CTA's that is
     // not the whole of it: one that began in another CTA, or goes on in one.

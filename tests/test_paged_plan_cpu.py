@@ -96,3 +96,18 @@ def test_random_batches(plan, seed):
 def test_nothing_to_do(plan):
     check(plan, [0] * 5, 1, 8, 2, 64, 8)
     check(plan, [0] * 300, 1, 8, 2, 64, 8)
+
+
+def test_owner_of_a_tile_past_32_bits(plan):
+    """The CTA of a tile, ((t + 1) * ctas - 1) // total, whatever needs 64 bits:
+    the product, the number of tiles, both or neither."""
+    rng = np.random.default_rng(5)
+    totals = [1, 7, 152, (1 << 32) - 1, 1 << 32, (1 << 32) + 1, 3 << 32, 1 << 40]
+    totals += [int(x) for x in rng.integers(1 << 28, 1 << 45, 30)]
+    for total in totals:
+        for ctas in (1, 2, 151, 152):
+            if ctas > total:
+                continue
+            for t in [0, 1, total // 2, total - 1, *(int(x) for x in rng.integers(0, total, 20))]:
+                t = min(t, total - 1)
+                assert plan.plan_owner(total, ctas, t) == ((t + 1) * ctas - 1) // total, (total, ctas, t)
