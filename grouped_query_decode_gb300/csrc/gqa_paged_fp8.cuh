@@ -499,6 +499,9 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
         *abort_flag = 0;
         fence_barrier_init();
     }
+    // No output row yet: after an expired wait a segment may end whose rows were
+    // never split, and writes nothing then.
+    if (threadIdx.x < 2 * RP) row_out[threadIdx.x] = -1;
     if (warp == SW + 1) {
         tmem_alloc(smem_addr(tmem_slot), PS::kTmemCols);
         tmem_relinquish();

@@ -518,3 +518,31 @@ def test_an_empty_sequence_before_many_units(empty, H, G, sq):
     for rep in range(30):
         again = run(c, dev)
         assert np.array_equal(again[0], first[0]) and np.array_equal(again[1], first[1]), rep
+
+
+@pytest.mark.parametrize("H,G", [(8, 8), (64, 4)], ids=str)
+def test_an_expired_wait_writes_no_row_that_is_not_its_own(H, G):
+    """A CTA whose wait expires in its first unit ends its other units without
+    their queries: what shared memory held for them, rows of an earlier and
+    larger call, is no place to write to."""
+    B, T, D = 320 // G, 1024, 64
+    large = Case(720, 3 * B, 1, H, G, D, 64, [130] * (3 * B))
+    small = Case(721, B, 1, H, G, D, 64, [T] * B)
+    ds, dl = small.device(), large.device()
+    buf = torch.zeros(3 * B, 1, H, D, dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros(3 * B, 1, H, device="cuda")
+    gq.gqa_decode_paged_fp8(*ds, small.sm, buf[:B], lse[:B])
+    torch.cuda.synchronize()
+    ref = buf[:B].clone()
+    for rep in range(3):
+        gq.gqa_decode_paged_fp8(*dl, large.sm, buf, lse)
+        torch.cuda.synchronize()
+        buf.view(torch.int16).fill_(BF_CANARY)
+        lse.view(torch.int32).fill_(F32_CANARY)
+        with env(GQA_DECODE_DEBUG_TIMEOUT_MS=200, GQA_DECODE_DEBUG_SKIP_TILE=0):
+            gq.gqa_decode_paged_fp8(*ds, small.sm, buf[:B], lse[:B])
+            assert gq.gqa_decode_check_error() == gq.GQA_ERR_DEVICE_TIMEOUT
+        assert bool((buf[B:].view(torch.int16) == BF_CANARY).all()) and bool((lse[B:].view(torch.int32) == F32_CANARY).all())
+    gq.gqa_decode_paged_fp8(*ds, small.sm, buf[:B], lse[:B])
+    assert torch.equal(buf[:B], ref)
+    assert gq.gqa_decode_check_error() == gq.GQA_OK
