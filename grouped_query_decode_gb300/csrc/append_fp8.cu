@@ -63,7 +63,8 @@ struct Divider {
         pow2 = (b & 0x7fffffu) == 0 && (b >> 23) != 0 && (b >> 23) < 254;
         inv = pow2 ? __uint_as_float((254u - (b >> 23)) << 23) : 0.f;   // 2^-e
     }
-    __device__ float operator()(float x) const { return pow2 ? x * inv : (scale == 0.f ? 0.f : __fdiv_rn(x, scale)); }
+    // A scale of 0 comes with zeros and with NaN, which stays.
+    __device__ float operator()(float x) const { return pow2 ? x * inv : (scale == 0.f ? x * 0.f : __fdiv_rn(x, scale)); }
 };
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {

@@ -201,3 +201,40 @@ def test_append_then_attend_serves_the_values(monkeypatch):
         ref, _ = oracle.get().gqa_decode_kv(q.view(torch.int16).numpy().view(np.uint16), k, v, lens, sm)
         vmax = np.nanmax(np.abs(v))
         assert np.abs(out.float().cpu().numpy() - ref).max() <= 2.0 ** -8 * np.abs(ref).max() + 2.0 ** -10 * vmax
+
+
+NOT_FINITE = [float("nan"), float("inf"), float("-inf")]
+
+
+@pytest.mark.parametrize("sq", [1, 5, 20])
+@pytest.mark.parametrize("held", ["none", "zeros", "not positive"])
+@pytest.mark.parametrize("beside", ["alone", "zeros"])
+def test_nan_and_infinities_in_blocks_without_a_scale(beside, held, sq):
+    """No finite element above 0 and no scale held: the block's scale is 0, and
+    NaN and infinities are NaN codes all the same, so attention says NaN."""
+    B, G, D, page = 3, 2, 64, 64
+    p = Pool(130 + sq, B, G, D, page, 1)
+    kept = 0 if held == "none" else 7
+    if kept:
+        for i, s in enumerate(p.scales):
+            odd = torch.from_numpy(s.copy())
+            odd[p.table[:, 0]] = torch.tensor(0.0 if held == "zeros" else -0.5)
+            p.dev[2 + i].copy_(odd)
+            s[p.table[:, 0]] = 0.0
+    k, v = torch.zeros(B, sq, G, D), torch.zeros(B, sq, G, D)
+    for b in range(B):                              # sequence b: NaN, inf or -inf, in K head 0 and V head 1
+        if beside == "alone":
+            k[b, :, 0], v[b, :, 1] = NOT_FINITE[b], NOT_FINITE[b]
+        else:
+            k[b, sq // 2, 0, 3 + b], v[b, sq - 1, 1, 60 - b] = NOT_FINITE[b], NOT_FINITE[b]
+    lens = [kept + sq] * B
+    p.append(k.to(torch.bfloat16), v.to(torch.bfloat16), lens)
+    p.check()
+    at = p.table[:, 0]
+    want = ~np.isfinite(k.numpy().transpose(0, 2, 1, 3))
+    assert np.array_equal((p.dev[0].cpu().numpy()[at, :, kept:kept + sq] & 127) == 127, want)
+    out = torch.zeros(B, 1, 2, D, dtype=torch.bfloat16, device="cuda")
+    q = torch.ones(B, 1, 2, D, dtype=torch.bfloat16, device="cuda")
+    gq.gqa_decode_paged_fp8(q, *p.dev, torch.tensor(lens, dtype=torch.int32, device="cuda"), 1.0, out)
+    assert bool(out[:, :, 0].isnan().all())                              # a NaN score: the whole row
+    assert torch.equal(out[:, 0, 1].isnan().cpu(), torch.from_numpy(~np.isfinite(v.numpy()[:, :, 1])).any(1))
