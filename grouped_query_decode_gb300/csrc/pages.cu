@@ -303,7 +303,13 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         ws.head[kWsPairs] = need <= free ? need : 0;
         ws.head[kWsOk] = need <= free;
     }
-    if (need <= free) each_free(p.refs, r, need, [&](int page, int k) { ws.dst[k] = page; });
+    // A free page's count may lie below 0; the second kernel counts its new holder
+    // from 0. (The lane that copied the count above writes it again.)
+    if (need <= free)
+        each_free(p.refs, r, need, [&](int page, int k) {
+            ws.dst[k] = page;
+            p.refs_out[page] = 0;
+        });
 }
 
 // With `live` live pages, the free pages below `live` and the live ones from

@@ -359,3 +359,21 @@ def test_reserve_fills_holes(B, most):
     gq.gqa_pages_reserve(t, dev(lens), r, ps, c)
     assert c.tolist() == want[2]
     assert np.array_equal(t.cpu().numpy(), want[0]) and np.array_equal(r.cpu().numpy(), want[1])
+
+
+def test_a_forked_copy_is_held_whatever_its_free_page_counted():
+    """Counts below 0 are free pages too: the copies that take them count 1, and
+    no later reservation hands them out again."""
+    table = np.array([[0, 1], [0, 2], [-1, -1]], np.int32)
+    lens, refs = np.array([20, 20, 0], np.int32), np.array([2, 1, 1, -3, -1, 0, 1, -7], np.int32)
+    src = np.array([0, 0, 0], np.int32)
+    t, l, r = dev(table), dev(lens), dev(refs)
+    outs = [torch.zeros_like(x) for x in (t, l, r)]
+    c = torch.zeros(2, dtype=torch.int32, device="cuda")
+    gq.gqa_pages_fork([], dev(src), t, l, r, 16, *outs, c)
+    assert c.tolist() == [2, 4]
+    assert outs[0].tolist() == [[0, 1], [0, 3], [0, 4]] and outs[1].tolist() == [20, 20, 20]
+    assert outs[2].tolist() == [3, 1, 0, 1, 1, 0, 1, -7]
+    outs[1].copy_(dev(np.array([33, 20, 20], np.int32)))       # clamped to two pages: nothing to reserve
+    gq.gqa_pages_reserve(outs[0], outs[1], outs[2], 16, c)
+    assert c.tolist() == [0, 3]
