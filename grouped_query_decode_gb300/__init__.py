@@ -18,6 +18,7 @@ import ctypes
 import functools
 import math
 import threading
+import weakref
 
 from . import build as _build
 
@@ -334,30 +335,46 @@ def _paged_fp8_cache(k_pages, v_pages, k_scale, v_scale, block_table, seq_lens):
     return table[0], num_pages, G, page_size, D, table[1]
 
 
-# Workspaces of the calls that take theirs from torch's allocator, one per
-# (device, stream handle), grow-only: calls on a stream run in order.
-_workspaces = {}
+class _Workspaces:
+    """The workspaces that one host thread keeps, by (device, stream handle),
+    grow-only: a thread's calls on a stream run in order. Threads share none, also
+    on one stream: a call may be two launches, the second of which reads what the
+    first one wrote, and another thread's call may come in between. (So
+    cudaStreamPerThread, another stream in every thread, is a handle like any.)"""
+
+    def __init__(self):
+        self.by_stream = {}
 
 
-def _workspace_key(dev, handle):
-    # cudaStreamPerThread is another stream in every thread.
-    return (dev, handle) if handle != 2 else (dev, handle, threading.get_ident())
+_of_thread = threading.local()
+_of_all_threads = weakref.WeakSet()
+
+
+def _kept_workspaces():
+    try:
+        return _of_thread.workspaces.by_stream
+    except AttributeError:
+        mine = _of_thread.workspaces = _Workspaces()
+        with _lock:
+            _of_all_threads.add(mine)
+        return mine.by_stream
 
 
 def _workspace(nbytes, like, dev, stream):
     """A buffer for one call on the device of `like`, in the order of the call's
-    stream. A call on the current stream takes the stream's own, kept from call
-    to call; a call that is being captured takes new memory of its graph, which
+    stream. A call on the current stream takes the calling thread's own for that
+    stream, kept from call to call; a call that is being captured takes new memory of its graph, which
     no other graph shares; one on a stream passed as an argument takes new
     memory too."""
     import torch
     if stream is None:
         if torch._C._cuda_getDevice() != dev or torch._C._cuda_isCurrentStreamCapturing():
             return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-        key = _workspace_key(dev, torch._C._cuda_getCurrentRawStream(dev))
-        buf = _workspaces.get(key)
+        kept = _kept_workspaces()
+        key = (dev, torch._C._cuda_getCurrentRawStream(dev))
+        buf = kept.get(key)
         if buf is None or buf.shape[0] < nbytes:
-            buf = _workspaces[key] = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+            buf = kept[key] = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
         return buf
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=like.device)
@@ -372,8 +389,8 @@ def gqa_decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seq
     v_scale [num_pages, G, ceil(page_size/64)] float32, block_table [B,
     max_pages_per_seq] int32. The workspace (a CUDA uint8 tensor of
     gqa_decode_paged_fp8_workspace_bytes(...)) comes from torch's allocator when
-    not given: the stream's own, kept from call to call, or memory of the graph
-    being captured."""
+    not given: the calling thread's own for the stream, kept from call to call, or
+    memory of the graph being captured."""
     import torch
     dev = q.get_device()
     bf, u8, f32, i32 = torch.bfloat16, torch.uint8, torch.float32, torch.int32
@@ -613,14 +630,19 @@ def gqa_decode_noalloc(q, k_cache, v_cache, seq_lens, scale, out, lse=None, stre
 
 
 def gqa_decode_release_workspace(stream=None, device=None) -> None:
-    """Frees the workspaces kept for (device, stream) after the work queued on
-    the stream; the next call on that stream allocates again."""
+    """Frees the workspaces kept for (device, stream), those of every thread,
+    after the work queued on the stream; the next call on that stream allocates
+    again."""
     import torch
     if device is None:
         device = stream.device_index if hasattr(stream, "device_index") else torch.cuda.current_device()
     handle = _stream_handle(stream, device)
     index = device if isinstance(device, int) else torch.device(device).index
-    _workspaces.pop(_workspace_key(torch.cuda.current_device() if index is None else index, handle.value or 0), None)
+    key = (torch.cuda.current_device() if index is None else index, handle.value or 0)
+    with _lock:
+        everyone = list(_of_all_threads)
+    for w in everyone:
+        w.by_stream.pop(key, None)
     rc = _call(device, load().gqa_decode_release_workspace, handle)
     if rc != GQA_OK:
         raise GQADecodeError(rc, "gqa_decode_release_workspace")

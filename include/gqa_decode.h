@@ -207,7 +207,10 @@ int gqa_prefill(const void* q, const void* k_cache, const void* v_cache, const i
  *
  * Every workspace is the caller's (sizes from the *_workspace_bytes calls,
  * 256-byte aligned, no initialisation): calls that may overlap on the GPU,
- * replays of different captured graphs among them, take different ones.
+ * replays of different captured graphs among them, take different ones. So do
+ * calls that several host threads make on one stream: gqa_pages_fork and
+ * gqa_pages_compact are two launches, the second of which reads the plan that
+ * the first one left in the workspace, and another thread's may come in between.
  */
 
 /*

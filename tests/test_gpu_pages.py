@@ -377,3 +377,56 @@ def test_a_forked_copy_is_held_whatever_its_free_page_counted():
     outs[1].copy_(dev(np.array([33, 20, 20], np.int32)))       # clamped to two pages: nothing to reserve
     gq.gqa_pages_reserve(outs[0], outs[1], outs[2], 16, c)
     assert c.tolist() == [0, 3]
+
+
+def test_host_threads_fork_and_compact_on_one_stream():
+    """Three threads on one stream, each with its own table and pool: forks,
+    compactions, reservations and attention whose launches come in between each
+    other's, results as those of the models."""
+    import threading
+    n, reps, ps = 3, 60, 16
+    cases, errors = [], []
+    for i in range(n):
+        B, most, num = [(6, 5, 64), (33, 9, 500), (64, 40, 3000)][i]
+        s = State(80 + i, B, most, ps, num)
+        src = s.rng.integers(0, B, B).astype(np.int32)
+        pool = s.pools(("scale",))[0]
+        cases.append((s, src, pool, model.fork(src, s.table, s.lens, s.refs, ps)))
+    q = torch.ones(4, 1, 8, 64, dtype=torch.bfloat16, device="cuda")
+    pages, scale = torch.full((4, 2, ps, 64), 0x38, dtype=torch.uint8, device="cuda"), torch.ones(4, 2, 1, device="cuda")
+    short, some = dev(np.arange(4, dtype=np.int32)[:, None]), dev(np.full(4, ps, np.int32))
+    data = [(dev(src), dev(s.table), dev(s.lens), dev(s.refs), [dev(pool) for _ in range(reps)]) for s, src, pool, _ in cases]
+    torch.cuda.synchronize()
+    start = threading.Barrier(n)
+
+    def work(i):
+        try:
+            s, src, pool, (want_t, want_l, want_r, counts, pairs) = cases[i]
+            d_src, t, l, r, pools = data[i]
+            outs = [[torch.full_like(x, -77) for x in (t, l, r)] for _ in range(reps)]
+            after = [[torch.full_like(x, -77) for x in (t, r)] for _ in range(reps)]
+            c = [torch.zeros(2, dtype=torch.int32, device="cuda") for _ in range(2 * reps)]
+            o = torch.empty_like(q)
+            start.wait(60)
+            for k in range(reps):
+                gq.gqa_pages_fork([pools[k]], d_src, t, l, r, ps, *outs[k], c[2 * k], page_dim=1)
+                gq.gqa_decode_paged_fp8(q, pages, pages, scale, scale, short, some, 0.1, o)
+                gq.gqa_pages_compact([pools[k]], outs[k][0], outs[k][2], *after[k], c[2 * k + 1], page_dim=1)
+            torch.cuda.synchronize()
+            moved_once = moved([pool], pairs)[0]
+            final_t, final_r, final_c, final_pairs = model.compact(want_t, want_r)
+            want_pool = moved([moved_once], final_pairs)[0]
+            for k in range(reps):
+                assert c[2 * k].tolist() == counts and c[2 * k + 1].tolist() == final_c, k
+                for got, want in zip(outs[k] + after[k] + [pools[k]], (want_t, want_l, want_r, final_t, final_r, want_pool)):
+                    assert np.array_equal(got.cpu().numpy(), want), k
+            assert bool((o == 1).all())
+        except Exception as e:                    # a thread's failure is the test's
+            errors.append((i, repr(e)[:500]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(n)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(120)
+    assert not errors and not any(t.is_alive() for t in threads), errors

@@ -268,3 +268,48 @@ def test_pool_array_counts_layers_and_bytes(monkeypatch):
     with pytest.raises(ValueError, match="is empty"):
         gq._page_pools(0, [torch.zeros(7, 0)], 7, 0)
     assert ctypes.sizeof(gq.PagePoolT) == 32
+
+
+def test_host_threads_on_one_stream_do_not_share_a_workspace(monkeypatch):
+    """A call of two launches plans in its workspace and reads the plan back:
+    another thread's call that is enqueued in between, on the same stream, has a
+    workspace of its own. One thread keeps its buffer from call to call; a
+    release forgets those of every thread."""
+    import threading
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: False, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(gq, "_call", lambda *a: gq.GQA_OK)
+    monkeypatch.setattr(gq, "_stream_handle", lambda stream, device: ctypes.c_void_p(0))
+    like, n = torch.zeros(1), 3
+    got, turns, errors = [[] for _ in range(n)], threading.Barrier(n), []
+
+    def work(i):
+        try:
+            for _ in range(4):                    # every thread is within its call at once
+                got[i].append(gq._workspace(64, like, 0, None))
+                turns.wait(20)
+            if i == 0:
+                gq.gqa_decode_release_workspace()
+            turns.wait(20)
+            got[i].append(gq._workspace(64, like, 0, None))
+            got[i].append(gq._workspace(100, like, 0, None))
+            got[i].append(gq._workspace(64, like, 0, None))
+            turns.wait(20)
+        except Exception as e:
+            errors.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(n)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not errors
+    for mine in got:
+        assert all(b is mine[0] for b in mine[:4])              # kept
+        assert mine[4] is not mine[0]                           # released
+        assert mine[5].numel() >= 100 and mine[6] is mine[5]    # grown, then kept
+    for turn in range(7):
+        at = [mine[turn].data_ptr() for mine in got]
+        assert len(set(at)) == n, turn
