@@ -10,12 +10,16 @@
 //   q * 2^e = hi + lo / 16, e4m3 (2^e brings the row's maximum to [128, 256)):
 //     4 significant bits each, the residual an exact difference, so every bf16
 //     query down to 2^-13 of its row's maximum, and 2^-21 of it below that;
-//   w = fp16(p * v_scale * 2^c) = t0 + t1 + t2 + t3, e5m2: a term is the upper
-//     byte of the fp16 residual (its first 3 significant bits), the next
-//     residual the exact difference, so 4 terms are all 11 bits of w down to
-//     2^-6, and w within 2^-16 below that, where w is 1024..2048 for p = 1. No
-//     conversion instruction is needed; an e4m3 split takes two per term and
-//     pair, and those, at a quarter of the rate, took half of a tile's time.
+//   w = fp16(p * v_scale * 2^c) = t0 + t1 / 8 + t2 / 64 + t3 / 512, e5m2: a term
+//     is the upper byte of the fp16 residual (its first 3 significant bits), the
+//     next residual the exact difference times 8, which fits fp16 again. The 4
+//     terms are all of w, subnormals too: w is p * v_scale within half an fp16
+//     step, 2^-11 of itself or 2^-25, where w is 1024..2048 for p = 1 and the
+//     largest scale. (Without the factors what lies below e5m2's least step,
+//     2^-16, was dropped: 2^17 keys with a hundredth of the weight behind a key
+//     with the rest came out 3 % low, 2^20 of them 22 %.) No conversion instruction is needed; an e4m3 split takes two
+//     per term and pair, and those, at a quarter of the rate, took half of a
+//     tile's time.
 // The extra columns cost nothing: up to N = 128 a product of M = 128 takes the
 // 64 cycles that reading its K or V rows takes.
 //
@@ -214,11 +218,14 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
     return r;
 }
 
-// What is left of two fp16 values without their first e5m2 terms (exact).
+// 8 times what is left of two fp16 values without their first e5m2 terms: exact,
+// and at most 8 * (2^-2 - 2^-10) of the value's power of two, so in range.
+constexpr float kP8TermStep = 8.0f;
 __device__ __forceinline__ uint32_t e5m2_residual(uint32_t f) {
     const uint32_t t = f & 0xff00ff00u;
     const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&f), *reinterpret_cast<const __half2*>(&t));
-    return *reinterpret_cast<const uint32_t*>(&d);
+    const __half2 r = __hmul2(d, __float2half2_rn(kP8TermStep));
+    return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 // Floats to integers of the same order, and back.
@@ -1134,11 +1141,11 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
 #pragma unroll
                 for (int r = 0; r < RH; ++r) o[r] = 0.f;
 #pragma unroll
-                for (int t = 0; t < kP8Terms; ++t) {
+                for (int t = kP8Terms - 1; t >= 0; --t) {
                     uint32_t u[RH];
                     tmem_ld_rows<RH>(o_tm + t * RP, u);
 #pragma unroll
-                    for (int r = 0; r < RH; ++r) o[r] += __uint_as_float(u[r]);
+                    for (int r = 0; r < RH; ++r) o[r] = fmaf(o[r], 1.f / kP8TermStep, __uint_as_float(u[r]));
                 }
                 tc_fence_before();
                 // D = 64 products keep 16 of their rows in each warp's 32 lanes.

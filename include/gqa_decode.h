@@ -218,8 +218,13 @@ int gqa_prefill(const void* q, const void* k_cache, const void* v_cache, const i
  * (same masks, outputs, empty rows, clamped lengths; a block-table entry
  * outside [0, num_pages) reads as zeros), for D in {64, 128} and any number of
  * query rows R = (H/G)*sq: single tokens, speculative tokens and the chunks of
- * a prompt. Queries and codes enter the products exactly, probabilities rounded
- * to fp16; sums and softmax statistics are fp32.
+ * a prompt. Sums and softmax statistics are fp32. Codes enter the products
+ * exactly, queries too down to 2^-13 of their row's largest element (smaller ones
+ * within 2^-21 of it). A key's weight, its probability times its block's v_scale,
+ * is rounded to fp16, to nearest: within 2^-11 of itself, or, where that is more,
+ * within 2^-35 of the largest probability times the largest |v_scale| of the
+ * blocks read for the row. Small weights are rounded, never cut, so that the many
+ * of a long context do not come out low together.
  *
  * A NaN code in K or V at a position a row sees makes that row NaN (in V with
  * sq > 1 possibly in every column); codes at t >= seq_lens[b] are never used.

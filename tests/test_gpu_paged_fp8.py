@@ -546,3 +546,76 @@ def test_an_expired_wait_writes_no_row_that_is_not_its_own(H, G):
     gq.gqa_decode_paged_fp8(*ds, small.sm, buf[:B], lse[:B])
     assert torch.equal(buf[:B], ref)
     assert gq.gqa_decode_check_error() == gq.GQA_OK
+
+
+# Small weights. A key's weight, p times its block's V scale, is rounded to fp16
+# with the largest such product of the unit at 2^11 or a little above: by at
+# most 2^-11 of itself, or 2^-25, which is 2^-35 448 S a key, with S the largest
+# |v_scale| of the unit's blocks and the row's largest p at 1 or above:
+#   |out - exact| <= 2^-8 |out| + 2^-11 sum(p |v|) / l + n 2^-35 448 S / l
+# and the scores' error, 2^-13 in natural units, on numerator and sum.
+
+def weighted(pool_k, pool_v, pages, q, sm):
+    """Exact out of one row over `pages` (repeats allowed) of values [num, page, D];
+    also sum(p |v|) / l, and l with the largest p at 1."""
+    count = np.bincount(pages, minlength=len(pool_k)).astype(np.float64)
+    x = pool_k @ q * sm
+    m = x[count > 0].max()
+    w = np.exp(x - m) * count[:, None]
+    l = w.sum()
+    return (w.reshape(-1) @ pool_v.reshape(-1, pool_v.shape[-1]) / l,
+            w.reshape(-1) @ np.abs(pool_v).reshape(-1, pool_v.shape[-1]) / l, l)
+
+
+def run_weighted(codes, scales, pages, q, sm, H=2, page=64, B=1):
+    """B equal sequences over `pages`, one KV head, H equal query rows; what comes
+    out and how far it may be off."""
+    D, T = codes[0].shape[-1], len(pages) * page
+    d = [torch.from_numpy(x[:, None]).cuda() for x in (*codes, *scales)]
+    qs = torch.from_numpy(q).to(torch.bfloat16)
+    assert np.array_equal(qs.double().numpy(), q)
+    out = torch.zeros(B, 1, H, D, dtype=torch.bfloat16, device="cuda")
+    gq.gqa_decode_paged_fp8(qs.cuda().expand(B, 1, H, D).contiguous(), *d,
+                            torch.from_numpy(np.asarray(pages, np.int32)).cuda().expand(B, -1).contiguous(),
+                            torch.full((B,), T, dtype=torch.int32, device="cuda"), sm, out)
+    torch.cuda.synchronize()
+    assert gq.gqa_decode_check_error() == gq.GQA_OK
+    k, v = (model.page_values(c[:, None], s[:, None])[:, 0] for c, s in zip(codes, scales))
+    want, spread, l = weighted(k, v, pages, q, sm)
+    S = np.abs(scales[1][np.unique(pages)]).max()
+    bound = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -12) * spread + T * 2.0 ** -35 * 448 * S / l
+    return out.double().cpu().numpy()[:, 0], want, bound
+
+
+@pytest.mark.parametrize("T,rest", [(1 << 17, 0.5), (1 << 17, 0.1), (1 << 17, 0.01), (1 << 20, 0.1), (1 << 20, 0.01)])
+@pytest.mark.parametrize("H", [2, 12, 32])
+@pytest.mark.parametrize("B", [1, 304])
+def test_a_sink_and_a_long_tail(B, H, T, rest):
+    """A first key with most of the weight and a value of zero, the rest of the
+    weight spread over a long context whose values have one sign: split over the
+    SMs, each part with its own reference, and with whole sequences to an SM."""
+    rng = np.random.default_rng(T % 977 + H)
+    page, D, n = 64, 64, 40
+    codes = [np.zeros((n, page, D), np.uint8), model.nearest_codes(rng.uniform(40, 200, (n, page, D)))]
+    codes[0][..., 0] = model.nearest_codes(rng.uniform(-1, 1, (n, page)))
+    codes[0][0, 0, 0], codes[1][0, 0] = model.nearest_codes(np.array(16.0)), 0
+    scales = [np.ones((n, 1), np.float32), np.full((n, 1), 0.75 / 64, np.float32)]
+    pages = np.concatenate([[0], 1 + np.arange(T // page - 1) % (n - 1)])
+    q = np.zeros(D)
+    q[0] = 1.0
+    got, want, bound = run_weighted(codes, scales, pages, q, math.log(T / rest) / 16, H, B=B)
+    assert (np.abs(got - want) <= bound).all(), (np.abs(got / want - 1).max(), (np.abs(got - want) / bound).max())
+
+
+@pytest.mark.parametrize("ratio", [16, 20, 24, 26])
+def test_values_far_below_the_largest_scale(ratio):
+    """Equal weights; the values of a page with a large scale are zeros, those of
+    the others 2^-ratio of its scale."""
+    rng = np.random.default_rng(ratio)
+    page, D, n = 64, 128, 12
+    codes = [np.zeros((n, page, D), np.uint8), model.nearest_codes(rng.uniform(100, 448, (n, page, D)))]
+    scales = [np.ones((n, 1), np.float32), np.exp2(-ratio + rng.uniform(-0.5, 0.5, (n, 1))).astype(np.float32)]
+    codes[1][0], scales[1][0] = 0, 1.0
+    for pages in (np.arange(n), np.arange(n)[::-1], np.concatenate([np.zeros(1, int), 1 + np.arange(400) % (n - 1)])):
+        got, want, bound = run_weighted(codes, scales, pages, np.zeros(D), 1.0)
+        assert (np.abs(got - want) <= bound).all(), (np.abs(got / want - 1).max(), (np.abs(got - want) / bound).max())
