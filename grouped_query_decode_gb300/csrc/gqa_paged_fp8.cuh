@@ -1010,8 +1010,9 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
                         if (m > m_old + kP8Slack) m_new = m;
                     }
                     const int vm = max(max(my_max[RH], my_max[2 * RH + 1]), max(my_max[3 * RH + 2], my_max[4 * RH + 3]));
-                    // 2^-ev brings the largest scale to [0.5, 1).
-                    const int ev_top = min(max((vm >> 23) - 126, -60), 126);
+                    // 2^-ev brings the largest scale to [0.5, 1); where it is below
+                    // 2^-114 to 2^-13 at least, so that `unit` stays a normal number.
+                    const int ev_top = min(max((vm >> 23) - 126, -113), 126);
                     const int ev_new = first || __int_as_float(vm) * pow2i(-ev) > kP8ScaleSlack ? ev_top : ev;
                     const float alpha = fast_exp2(m_old - m_new);
                     const float alpha_o = first ? 0.f : alpha * pow2i(max(ev - ev_new, -126));
@@ -1148,15 +1149,19 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
                     for (int r = 0; r < RH; ++r) o[r] = fmaf(o[r], 1.f / kP8TermStep, __uint_as_float(u[r]));
                 }
                 tc_fence_before();
+                // In units of the values. By itself: times a row's factor as well it
+                // could fall below the normal numbers.
+                const float unit = pow2i(ev) * (1.f / kP8ProbScale);
+#pragma unroll
+                for (int r = 0; r < RH; ++r) o[r] *= unit;
                 // D = 64 products keep 16 of their rows in each warp's 32 lanes.
                 const bool mine = D == 128 || lane < 16;
                 const int dim = D == 128 ? tok : w4 * 16 + lane;
-                const float unit = pow2i(ev) * (1.f / kP8ProbScale);
                 // Of two groups, the one without the last tile hands its O over.
                 if (both && x != (last & 1)) {
 #pragma unroll
                     for (int r = 0; r < RH; ++r)
-                        if (mine) *handed_at(x, r, dim) = o[r] * unit;
+                        if (mine) *handed_at(x, r, dim) = o[r];
                     if (tok < RH) {
                         const float4 q = my_sum[tok];
                         other[y * RH + tok] = make_float2(-my_ref[tok], q.x + q.y + q.z + q.w);
@@ -1192,7 +1197,7 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
                             slot[RP * D + y * RH + tok] = m;
                             slot[RP * D + RP + y * RH + tok] = ls;
                         }
-                        factor[tok] = make_float2(a0 * unit, a1);
+                        factor[tok] = make_float2(a0, a1);
                     }
                     named_sync(bar, 128);
                     // With up to 16 rows whole outputs are gathered in the group's own

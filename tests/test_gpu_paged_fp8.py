@@ -619,3 +619,18 @@ def test_values_far_below_the_largest_scale(ratio):
     for pages in (np.arange(n), np.arange(n)[::-1], np.concatenate([np.zeros(1, int), 1 + np.arange(400) % (n - 1)])):
         got, want, bound = run_weighted(codes, scales, pages, np.zeros(D), 1.0)
         assert (np.abs(got - want) <= bound).all(), (np.abs(got / want - 1).max(), (np.abs(got - want) / bound).max())
+
+
+@pytest.mark.parametrize("e", [-126, -110, -90, -75, -61, 59])
+@pytest.mark.parametrize("D,H", [(64, 2), (128, 12), (128, 32)])
+def test_the_smallest_and_the_largest_scales(D, H, e):
+    """V scales from the smallest that the append makes, 2^-126, to 2^60: in one
+    tile, in both groups' tiles, and in parts of several CTAs."""
+    rng = np.random.default_rng(e + 200 + D)
+    page, n = 64, 20
+    codes = [model.nearest_codes(rng.standard_normal((n, page, D))), model.nearest_codes(rng.uniform(100, 448, (n, page, D)))]
+    scales = [np.ones((n, 1), np.float32) / 8, np.full((n, 1), 2.0 ** e, np.float32)]
+    for count in (1, 5, n, 60):
+        got, want, bound = run_weighted(codes, scales, np.arange(count) % n, np.round(rng.standard_normal(D) * 2) / 2,
+                                        1 / math.sqrt(D), H)
+        assert (np.abs(got - want) <= bound).all(), (count, np.abs(got / want - 1).max())
