@@ -421,9 +421,25 @@ def gqa_decode_paged_fp8(q, k_pages, v_pages, k_scale, v_scale, block_table, seq
         raise GQADecodeError(rc, "gqa_decode_paged_fp8")
 
 
+class _NoSize(Exception):
+    """No workspace size: unsupported sizes, or a device that could not be asked
+    just then. An exception, so that it is not kept."""
+
+
 @functools.lru_cache(maxsize=4096)
-def _paged_fp8_workspace_bytes(B, sq, H, G, D, page_size, most, device):
-    return int(_call(device, load().gqa_decode_paged_fp8_workspace_bytes, B, sq, H, G, D, page_size, most))
+def _known_paged_fp8_bytes(*sizes):
+    n = int(_call(sizes[-1], load().gqa_decode_paged_fp8_workspace_bytes, *sizes[:-1]))
+    if n == 0:
+        raise _NoSize
+    return n
+
+
+def _paged_fp8_workspace_bytes(*sizes):
+    """By B, sq, H, G, D, page_size, max_pages_per_seq and device."""
+    try:
+        return _known_paged_fp8_bytes(*sizes)
+    except _NoSize:
+        return 0
 
 
 def gqa_decode_paged_fp8_workspace_bytes(B, sq, H, G, D, page_size, max_pages_per_seq, device=None) -> int:

@@ -313,3 +313,13 @@ def test_host_threads_on_one_stream_do_not_share_a_workspace(monkeypatch):
     for turn in range(7):
         at = [mine[turn].data_ptr() for mine in got]
         assert len(set(at)) == n, turn
+
+
+def test_a_workspace_size_that_could_not_be_found_is_asked_for_again(monkeypatch):
+    """0 may mean that the device could not be asked just then."""
+    answers = iter([0, 4096])
+    monkeypatch.setattr(gq, "_call", lambda *a: next(answers))
+    sizes = (1, 1, 8, 2, 64, 16, 77777)
+    assert gq.gqa_decode_paged_fp8_workspace_bytes(*sizes, device=0) == 0
+    assert gq.gqa_decode_paged_fp8_workspace_bytes(*sizes, device=0) == 4096
+    assert gq.gqa_decode_paged_fp8_workspace_bytes(*sizes, device=0) == 4096
