@@ -15,6 +15,7 @@
 #include <mutex>
 #include <tuple>
 #include <utility>
+#include <vector>
 
 #include "gqa_decode.h"
 #include "gqa_launch.h"
@@ -44,7 +45,15 @@ std::map<int, DeviceInfo> g_devices;
 // split-KV arrival counters and partial slots; kind kPrefillWs the prefill's
 // split key-range partials, kept apart so that they never land on counters.
 constexpr int kDecodeWs = 0, kPrefillWs = 1;
-std::map<std::tuple<int, cudaStream_t, int>, std::pair<void*, size_t>> g_workspaces;
+// A buffer that is outgrown is kept until the stream's release: a graph captured
+// with it is still replayed, and another host thread may be about to launch with
+// it.
+struct OwnedWorkspace {
+    void* buf = nullptr;
+    size_t bytes = 0;
+    std::vector<void*> outgrown;
+};
+std::map<std::tuple<int, cudaStream_t, int>, OwnedWorkspace> g_workspaces;
 
 int device_info(DeviceInfo* out) {
     int dev = 0;
@@ -352,22 +361,19 @@ int stream_workspace(cudaStream_t stream, size_t need, void** ws, size_t* have, 
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e);
     std::lock_guard<std::mutex> lk(g_mu);
-    auto& slot = g_workspaces[{dev, stream, kind}];
-    if (slot.second < need) {
-        if (slot.first) {
-            // The old buffer may still be in use by work queued on this stream.
-            e = cudaStreamSynchronize(stream);
-            if (e != cudaSuccess) return cuda_fail(e);
-            cudaFree(slot.first);
-            slot = {nullptr, 0};
-        }
+    OwnedWorkspace& slot = g_workspaces[{dev, stream, kind}];
+    if (slot.bytes < need) {
+        // At least doubled, so that all that is outgrown is no more than what is used.
+        const size_t bytes = need > 2 * slot.bytes ? need : 2 * slot.bytes;
         void* p = nullptr;
-        e = cudaMalloc(&p, need);
+        e = cudaMalloc(&p, bytes);
         if (e != cudaSuccess) return cuda_fail(e);
-        slot = {p, need};
+        if (slot.buf) slot.outgrown.push_back(slot.buf);
+        slot.buf = p;
+        slot.bytes = bytes;
     }
-    *ws = slot.first;
-    *have = slot.second;
+    *ws = slot.buf;
+    *have = slot.bytes;
     return GQA_OK;
 }
 
@@ -573,20 +579,25 @@ int gqa_decode_release_workspace(cudaStream_t stream) {
     bool synced = false;
     for (int kind : {kDecodeWs, kPrefillWs}) {
         auto it = g_workspaces.find({dev, stream, kind});
-        if (it == g_workspaces.end()) continue;
-        // Work already queued on the stream may still use the buffer.
+        if (it == g_workspaces.end() || !it->second.buf) continue;
+        // Work already queued on the stream may still use the buffers.
         if (!synced) {
             e = cudaStreamSynchronize(stream);
             if (e != cudaSuccess) return cuda_fail(e);
             synced = true;
         }
-        void* buf = it->second.first;
-        g_workspaces.erase(it);
-        if (buf) {
-            e = cudaFree(buf);
-            if (e != cudaSuccess) return cuda_fail(e);
+        OwnedWorkspace& slot = it->second;
+        std::vector<void*> all;
+        all.swap(slot.outgrown);
+        all.push_back(slot.buf);
+        slot.buf = nullptr;
+        slot.bytes = 0;
+        for (void* p : all) {
+            const cudaError_t f = cudaFree(p);
+            if (e == cudaSuccess) e = f;
         }
     }
+    if (e != cudaSuccess) return cuda_fail(e);
     return GQA_OK;
 }
 

@@ -75,3 +75,42 @@ def test_host_threads_each_with_a_stream():
     assert gq.gqa_decode_check_error() == gq.GQA_OK
     for i, (dev, ref) in enumerate(cases):
         _check(dev, ref, f"thread {i}")
+
+
+def _bits(dev):
+    return dev["out"].view(torch.int16).clone(), dev["lse"].clone()
+
+
+def test_a_larger_call_leaves_the_workspace_of_a_captured_one():
+    """A graph captured on a stream is replayed after a larger call there has
+    outgrown the stream's buffer, decode and split prefill."""
+    scale = 1 / math.sqrt(D)
+    small, ref = _case(2501, 32, 8, 1, [1200])
+    large, _ = _case(2502, 64, 8, 4, [1200, 700, 900, 1100])
+    chunk, chunk_ref = _case(2503, 8, 2, 40, [1200])
+    wide, _ = _case(2504, 64, 8, 40, [1200, 1000])
+    s = torch.cuda.Stream()
+    with min_tiles(1), torch.cuda.stream(s):
+        for first, then in ((small, large), (chunk, wide)):
+            call = gq.gqa_decode if first is small else gq.gqa_prefill
+            args = [first[k] for k in "qkvl"] + [scale, first["out"], first["lse"]]
+            call(*args)
+            s.synchronize()
+            bits = _bits(first)
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                call(*args)
+            call(*[then[k] for k in "qkvl"], scale, then["out"], then["lse"])
+            other = torch.full((64 << 20,), 0xFF, dtype=torch.uint8, device="cuda")   # memory given back would be this
+            for _ in range(3):
+                first["out"].zero_()
+                graph.replay()
+            s.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(_bits(first), bits))
+            assert bool((other == 0xFF).all())
+            del graph
+    assert gq.gqa_decode_check_error() == gq.GQA_OK
+    gq.gqa_decode_release_workspace(s)
+    _check(small, ref, "decode")
+    _check(chunk, chunk_ref, "prefill")
+
