@@ -47,13 +47,15 @@ std::map<int, DeviceInfo> g_devices;
 constexpr int kDecodeWs = 0, kPrefillWs = 1;
 // A buffer that is outgrown is kept until the stream's release: a graph captured
 // with it is still replayed, and another host thread may be about to launch with
-// it.
+// it. `turn` is held by a call whose launches belong together, from the look-up
+// of its workspace to its last launch.
 struct OwnedWorkspace {
     void* buf = nullptr;
     size_t bytes = 0;
     std::vector<void*> outgrown;
+    std::mutex turn;
 };
-std::map<std::tuple<int, cudaStream_t, int>, OwnedWorkspace> g_workspaces;
+std::map<std::tuple<int, cudaStream_t, int>, OwnedWorkspace> g_workspaces;   // nodes are never erased
 
 int device_info(DeviceInfo* out) {
     int dev = 0;
@@ -355,13 +357,19 @@ int enqueue(const void* q, const void* k_cache, const void* v_cache, const int32
 }
 
 // The library-owned workspace of (current device, stream, kind), grown to
-// `need`.
-int stream_workspace(cudaStream_t stream, size_t need, void** ws, size_t* have, int kind = kDecodeWs) {
+// `need`. With `turn` the caller has it to itself until it lets go of that.
+int stream_workspace(cudaStream_t stream, size_t need, void** ws, size_t* have, int kind = kDecodeWs,
+                     std::unique_lock<std::mutex>* turn = nullptr) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e);
-    std::lock_guard<std::mutex> lk(g_mu);
+    std::unique_lock<std::mutex> lk(g_mu);
     OwnedWorkspace& slot = g_workspaces[{dev, stream, kind}];
+    if (turn) {
+        lk.unlock();   // the turn may take a while, other streams go on
+        *turn = std::unique_lock<std::mutex>(slot.turn);
+        lk.lock();
+    }
     if (slot.bytes < need) {
         // At least doubled, so that all that is outgrown is no more than what is used.
         const size_t bytes = need > 2 * slot.bytes ? need : 2 * slot.bytes;
@@ -517,8 +525,9 @@ int gqa_prefill(const void* q, const void* k_cache, const void* v_cache, const i
     void* ws = nullptr;
     size_t have = 0;
     const size_t need = prefill_workspace_bytes(D, items, (int)splits);
+    std::unique_lock<std::mutex> turn;   // the combine reads what the prefill kernel left
     if (need > 0) {
-        st = stream_workspace(stream, need, &ws, &have, kPrefillWs);
+        st = stream_workspace(stream, need, &ws, &have, kPrefillWs, &turn);
         if (st != GQA_OK) return st;
     }
     PrefillLaunchArgs a{};

@@ -83,7 +83,8 @@ extern "C" {
  * Decode attention for one step, using a workspace the library owns: one
  * grow-only device buffer per (device, stream), allocated with cudaMalloc on
  * the first call that needs more than the stream's buffer holds. Calls on the
- * same stream are ordered; calls on different streams use different buffers. A buffer that a larger call outgrows is kept until
+ * same stream are ordered, also those of several host threads; calls on different
+ * streams use different buffers. A buffer that a larger call outgrows is kept until
  * gqa_decode_release_workspace, for graphs that were captured with it. Graphs
  * captured on one stream share its buffer: their replays must not overlap.
  * Make one call per stream before capturing that stream into a CUDA graph, so

@@ -114,3 +114,40 @@ def test_a_larger_call_leaves_the_workspace_of_a_captured_one():
     _check(small, ref, "decode")
     _check(chunk, chunk_ref, "prefill")
 
+
+def test_host_threads_on_one_stream():
+    """Four threads on the current stream, decode steps and split prefill chunks of
+    unlike sizes: what one call leaves for its second launch is its own, and no
+    buffer goes away under another thread's call."""
+    cases = [_case(2601, 8, 2, 40, [1200]), _case(2602, 64, 8, 40, [1200, 600]), _case(2603, 32, 8, 1, [1200, 33]),
+             _case(2604, 16, 4, 70, [900])]
+    scale = 1 / math.sqrt(D)
+    errors, start = [], threading.Barrier(len(cases))
+    torch.cuda.synchronize()
+
+    def worker(i):
+        try:
+            dev, _ = cases[i]
+            call = gq.gqa_decode if i == 2 else gq.gqa_prefill
+            mine = [(torch.empty_like(dev["out"]), torch.empty_like(dev["lse"])) for _ in range(40)]
+            start.wait(60)
+            for out, lse in mine:
+                call(dev["q"], dev["k"], dev["v"], dev["l"], scale, out, lse)
+            torch.cuda.synchronize()
+            dev["out"], dev["lse"] = mine[0]
+            for out, lse in mine[1:]:
+                assert torch.equal(out.view(torch.int16), mine[0][0].view(torch.int16)) and torch.equal(lse, mine[0][1])
+        except Exception as e:
+            errors.append((i, repr(e)[:300]))
+
+    with min_tiles(1):
+        gq.gqa_decode_release_workspace()
+        threads = [threading.Thread(target=worker, args=(i,)) for i in range(len(cases))]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join(timeout=120)
+    assert not errors and not any(t.is_alive() for t in threads), errors
+    assert gq.gqa_decode_check_error() == gq.GQA_OK
+    for i, (dev, ref) in enumerate(cases):
+        _check(dev, ref, f"thread {i}")
