@@ -1141,19 +1141,18 @@ __global__ void __launch_bounds__(P8Shape<D, RP>::kThreads, 1)
                 float o[RH];
 #pragma unroll
                 for (int r = 0; r < RH; ++r) o[r] = 0.f;
+                // In units of the values; a row's factor comes later, times which this
+                // could fall below the normal numbers.
+                float unit = pow2i(ev) * (1.f / kP8ProbScale);
 #pragma unroll
-                for (int t = kP8Terms - 1; t >= 0; --t) {
+                for (int t = 0; t < kP8Terms; ++t) {
                     uint32_t u[RH];
                     tmem_ld_rows<RH>(o_tm + t * RP, u);
 #pragma unroll
-                    for (int r = 0; r < RH; ++r) o[r] = fmaf(o[r], 1.f / kP8TermStep, __uint_as_float(u[r]));
+                    for (int r = 0; r < RH; ++r) o[r] = fmaf(__uint_as_float(u[r]), unit, o[r]);
+                    unit *= 1.f / kP8TermStep;
                 }
                 tc_fence_before();
-                // In units of the values. By itself: times a row's factor as well it
-                // could fall below the normal numbers.
-                const float unit = pow2i(ev) * (1.f / kP8ProbScale);
-#pragma unroll
-                for (int r = 0; r < RH; ++r) o[r] *= unit;
                 // D = 64 products keep 16 of their rows in each warp's 32 lanes.
                 const bool mine = D == 128 || lane < 16;
                 const int dim = D == 128 ? tok : w4 * 16 + lane;
