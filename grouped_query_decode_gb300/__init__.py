@@ -548,8 +548,9 @@ def gqa_pages_fork(pools, src, block_table, seq_lens, ref_counts, page_size, blo
     """New row i goes on from old row src[i] (int32 [B]; outside [0, B): empty):
     full pages are shared, the partly filled last page stays with the lowest
     such row and is copied, in every pool, for the others; sequences that no
-    row goes on from give their pages back. The outputs are other tensors than
-    the inputs. counts (int32 [2]) = pages needed, pages that were free; the
+    row goes on from give their pages back. Holders outside the table keep full
+    pages only: the lowest row writes on in a partly filled one. The outputs are
+    other tensors than the inputs. counts (int32 [2]) = pages needed, pages that were free; the
     outputs are copies of the inputs if fewer are free than needed."""
     import torch
     dev, i32 = block_table.get_device(), torch.int32

@@ -16,7 +16,8 @@
 // TB/s). The schedulers issue 60 % of the time there, so instructions count: two
 // products to an instruction, packed maxima, no division by the page size (13.4
 // us without these). Up to 8 new tokens a warp takes a block by itself: one token of 64
-// sequences 2.4 us, which is latency (length, then page and tokens, then codes).
+// sequences 2.4 us, which is latency (length, then page and tokens, then codes);
+// of the 64 registers that leaves a thread at D 128, 28 bytes are spilled.
 #include <cuda_runtime.h>
 
 #include <cstdint>

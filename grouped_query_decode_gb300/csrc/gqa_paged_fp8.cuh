@@ -17,41 +17,50 @@
 //     step, 2^-11 of itself or 2^-25, where w is 1024..2048 for p = 1 and the
 //     largest scale. (Without the factors what lies below e5m2's least step,
 //     2^-16, was dropped: 2^17 keys with a hundredth of the weight behind a key
-//     with the rest came out 3 % low, 2^20 of them 22 %.) No conversion instruction is needed; an e4m3 split takes two
-//     per term and pair, and those, at a quarter of the rate, took half of a
-//     tile's time.
+//     with the rest came out 3 % low, 2^20 of them 22 %.) No conversion
+//     instruction is needed; an e4m3 split takes two per term and pair, and
+//     those, at a quarter of the rate, took half of a tile's time.
 // The extra columns cost nothing: up to N = 128 a product of M = 128 takes the
 // 64 cycles that reading its K or V rows takes.
 //
 // Softmax, one thread per token: x = s * scale2 * k_scale (base 2), p = 2^(x - m)
 // with a reference m per row that moves only when a score exceeds it by more
 // than 4 (then O is rescaled in tensor memory), so that tiles need no maximum
-// across threads: one vote. The sum l is kept per thread until the end. v_scale enters
-// p through a power of two 2^c that follows the largest scale seen.
+// across threads: one vote. The sum l is kept per thread until the end. v_scale
+// enters p through a power of two 2^c that follows the largest scale seen.
 //
-// Work: the tiles of all units, end to end, are shared equally by the CTAs
-// (one per SM; units of unlike lengths count a few tiles more for their end). A unit that crosses CTAs leaves (O, m, l) per CTA in the
-// workspace; the CTA that arrives last merges them. Per CTA: two groups of four
-// softmax warps (with 32 rows two such pairs, 16 rows each) take alternate
-// tiles. One warp brings K, another V (a TMA box per page, in the swizzle of
-// the operand layout; one warp issues a box in 65 cycles, two warps two); the
-// latter also fetches the blocks' scales, ahead of V by a chunk of tiles (behind
-// a saturated HBM a lookup of page and scale takes longer than a tile). Two warps issue the products.
-// Every wait is bounded, as in the other kernels.
+// Work: the tiles of all units, end to end, are shared equally by the CTAs (one
+// per SM; units of unlike lengths count a few tiles more for their end). A unit
+// that crosses CTAs leaves (O, m, l) per CTA in the workspace; the CTA that
+// arrives last merges them. Per CTA: two groups of four softmax warps (with 32
+// rows two such pairs, 16 rows each) take alternate tiles. One warp brings K,
+// another V (a TMA box per page, in the swizzle of the operand layout; one warp
+// issues a box in 65 cycles, two warps two); the latter also fetches the blocks'
+// scales, ahead of V by a chunk of tiles (behind a saturated HBM a lookup of page
+// and scale takes longer than a tile). Two warps issue the products. Every wait
+// is bounded, as in the other kernels.
 //
 // What bounds it. Bytes: the cache, once. A tile of 8 rows takes 0.3 us, one of 32
-// rows 0.65 to 0.70 us (a softmax warp's chain of load, vote, exponentials and
-// four terms is 2400 cycles, two groups at a time), against 0.62 to 0.74 us for
+// rows 0.70 to 0.75 us (a softmax warp's chain of load, vote, exponentials and
+// four terms is 2500 cycles, two groups at a time), against 0.62 to 0.74 us for
 // a tile's 32 KB from HBM shared by 128 to 152 SMs. Around the tiles: 2 us of
 // launch, 1.5 us of plan, 2 us until the first softmax, and where a unit is
 // split 4 to 6 us for its parts (stores, one atomic, the last arriver's merge).
-// Measured on one GB300 (HBM copy 6.77 TB/s), B x H/G heads, tokens, page:
-//   16 x 32/8, D 128, 4096, 64           25.2 us, 5.3 TB/s (6.6 TB/s at 16384 tokens)
-//   64 x 32/1, D 128, 8192, 32           33.5 us, 4.0 TB/s
-//   1 x 64/8, D 128, 131072, 16          52.5 us, 5.1 TB/s
-//   64 x 64/8, 4 new tokens, D 128, 512 to 32768, 64   318 us, 6.9 TB/s
-//   64 x 64/8, 4 new tokens, D 128, up to 4096, 64     77 us, 3.3 TB/s (8 rows 52 us)
-//   1 x 32/8, 64 new tokens, D 64, 4096, 64            23.4 us (4.7 MB: latency)
+// Every 32 rows walk their keys again, so chunks of a prompt are bound by the
+// softmax chain: a quarter of the bf16 rate from 512 new tokens on.
+// Measured on one GB300 (HBM copy 6.77 TB/s, SM clock 2070 MHz), B x H/G heads,
+// tokens, page; rates by the lengths that were read:
+//   16 x 32/8, D 128, 4096, 64           25.4 us, 5.3 TB/s (6.5 TB/s at 16384 tokens)
+//   64 x 32/1, D 128, 8192, 32           33.8 us, 4.0 TB/s
+//   1 x 64/8, D 128, 131072, 16          52.6 us, 5.1 TB/s
+//   64 x 64/8, 4 new tokens, D 128, 512 to 32768, 64   322 us, 6.5 TB/s (8 rows 6.9)
+//   64 x 64/8, 4 new tokens, D 128, up to 4096, 64     79.5 us, 3.15 TB/s (16 rows
+//                                        70 us, 8 rows 52 us)
+//   16 x 32/8, D 64, 16384, 64           75 us, 3.6 TB/s
+//   1 x 32/8, 64 new tokens, D 64, 4096, 64            23.7 us (4.7 MB: latency)
+//   4 x 32/8, 2048 new tokens, D 128, 8192, 64         2290 us, 420 TFLOP/s (the
+//                                        bf16 prefill kernel 851 us)
+// With 32 rows and D 128 the registers are one short: 8 bytes spilled, 20 read.
 // Tried and slower: asking for a barrier's phase ahead of its wait (MQA end +0.3
 // us), running the merge once without effect to fetch its instructions (+0.7 us),
 // 152 CTAs with uneven shares where 128 share equal units evenly (+2.8 us), the

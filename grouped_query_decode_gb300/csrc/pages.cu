@@ -573,7 +573,9 @@ int check_ws(void* ws, size_t bytes, int B, int num_pages) {
     return GQA_OK;
 }
 
-// Bytes that n copies of a page move at most, for the size of the grid.
+// The grid of a kernel that looks at `entries` table entries and then copies up
+// to n pages: a thread per entry and a warp per piece of a page, at most eight
+// CTAs per SM.
 unsigned move_grid(const PoolSet& set, long long n, long long entries, int sms) {
     long long warps = (entries + 31) / 32;
     for (int i = 0; i < set.n; ++i)

@@ -231,6 +231,8 @@ int gqa_prefill(const void* q, const void* k_cache, const void* v_cache, const i
  *
  * A NaN code in K or V at a position a row sees makes that row NaN (in V with
  * sq > 1 possibly in every column); codes at t >= seq_lens[b] are never used.
+ * Scores scale * q.k stay within 2^24 in magnitude, past which fp32 cannot tell
+ * their differences.
  * seq_lens and block_table stay as they are until the call has finished.
  */
 int gqa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
@@ -261,8 +263,9 @@ size_t gqa_decode_paged_fp8_workspace_bytes(int B, int sq, int H, int G, int D, 
  * the values that its block holds. Codes are round-to-nearest-even of x / scale; NaN
  * and infinities are stored as NaN codes and leave the scale alone.
  *
- * A page that receives tokens must belong to one sequence only (gqa_pages_fork
- * gives every sequence its own last page). No workspace.
+ * A page that receives tokens must belong to one sequence only, and to no holder
+ * outside the table (gqa_pages_fork gives every row of the table its own last
+ * page; see there for other holders). No workspace.
  */
 int gqa_append_paged_fp8(const void* k_new, const void* v_new, void* k_pages, void* v_pages,
                          float* k_scale, float* v_scale, const int32_t* block_table,
@@ -323,7 +326,10 @@ int gqa_pages_reserve(int32_t* block_table, const int32_t* seq_lens, int32_t* re
  * reserved behind it, stay with the lowest row that goes on from a sequence;
  * every other such row gets a copy of the partly filled page in a free page, in
  * the order of the rows. Sequences that no row goes on from give their pages
- * back. table_out, lens_out, refs_out do not overlap the inputs.
+ * back. Holders that ref_counts counts outside the table are not asked: where one
+ * holds a partly filled page (a prefix kept for later, say), the lowest row goes on
+ * in that page all the same. Give such a holder full pages only, or a copy of its
+ * last one (gqa_pages_copy). table_out, lens_out, refs_out do not overlap the inputs.
  * counts = {pages needed, pages that were free}; if fewer are free than needed,
  * the outputs are copies of the inputs and no page is copied.
  */
