@@ -363,9 +363,9 @@ def _kept_workspaces():
 def _workspace(nbytes, like, dev, stream):
     """A buffer for one call on the device of `like`, in the order of the call's
     stream. A call on the current stream takes the calling thread's own for that
-    stream, kept from call to call; a call that is being captured takes new memory of its graph, which
-    no other graph shares; one on a stream passed as an argument takes new
-    memory too."""
+    stream, kept from call to call; a call that is being captured takes new memory
+    of its graph, which no other graph shares; one on a stream passed as an
+    argument takes new memory too."""
     import torch
     if stream is None:
         if torch._C._cuda_getDevice() != dev or torch._C._cuda_isCurrentStreamCapturing():
@@ -550,8 +550,8 @@ def gqa_pages_fork(pools, src, block_table, seq_lens, ref_counts, page_size, blo
     such row and is copied, in every pool, for the others; sequences that no
     row goes on from give their pages back. Holders outside the table keep full
     pages only: the lowest row writes on in a partly filled one. The outputs are
-    other tensors than the inputs. counts (int32 [2]) = pages needed, pages that were free; the
-    outputs are copies of the inputs if fewer are free than needed."""
+    other tensors than the inputs. counts (int32 [2]) = pages needed, pages that
+    were free; the outputs are copies of the inputs if fewer are free than needed."""
     import torch
     dev, i32 = block_table.get_device(), torch.int32
     _check_all(dev, (("src", src, i32), ("block_table", block_table, i32), ("seq_lens", seq_lens, i32),
