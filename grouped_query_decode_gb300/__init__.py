@@ -50,6 +50,12 @@ class PagePoolT(ctypes.Structure):
                 ("layer_bytes", ctypes.c_size_t), ("layers", ctypes.c_int)]
 
 
+class RopeT(ctypes.Structure):
+    """Rotary positions, made by gqa_rope_init."""
+    _fields_ = [("dims", ctypes.c_int), ("interleaved", ctypes.c_int), ("gain", ctypes.c_double),
+                ("inv_freq", ctypes.c_double * 64)]
+
+
 class PlanT(ctypes.Structure):
     _fields_ = [("ctas", ctypes.c_int), ("tile_tokens", ctypes.c_int),
                 ("row_tiles", ctypes.c_int), ("stages", ctypes.c_int),
@@ -99,6 +105,19 @@ def load():
             lib.gqa_pages_free.restype = i32
             lib.gqa_pages_compact.argtypes = [vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, vp, sz, vp]
             lib.gqa_pages_compact.restype = i32
+            i64, f64 = ctypes.c_longlong, ctypes.c_double
+            lib.gqa_rope_init.argtypes = [vp, i32, i32, i32, f64, i32, f64, f64, f64, f64]
+            lib.gqa_rope_init.restype = i32
+            lib.gqa_rope.argtypes = [vp] * 6 + [i32] * 4 + [i64] * 4 + [i32, vp]
+            lib.gqa_rope.restype = i32
+            lib.gqa_append_paged.argtypes = [vp] * 10 + [i32] * 5 + [i64] * 4 + [i32] * 3 + [vp]
+            lib.gqa_append_paged.restype = i32
+            lib.gqa_prefill_packed.argtypes = [vp] * 4 + [f32, vp, vp] + [i32] * 5 + [i64] * 3 + [vp, sz, vp]
+            lib.gqa_prefill_packed.restype = i32
+            lib.gqa_prefill_paged.argtypes = [vp] * 6 + [f32, vp, vp] + [i32] * 5 + [i64] + [i32] * 3 + [vp, sz, vp]
+            lib.gqa_prefill_paged.restype = i32
+            lib.gqa_prefill_ragged_workspace_bytes.argtypes = [i32] * 5
+            lib.gqa_prefill_ragged_workspace_bytes.restype = sz
             lib.gqa_decode_noalloc.argtypes = [vp, vp, vp, vp, f32, vp, vp, *shape, vp]
             lib.gqa_decode_noalloc.restype = i32
             lib.gqa_decode_workspace_bytes.argtypes = shape
@@ -610,6 +629,242 @@ def gqa_pages_compact(pools, block_table, ref_counts, block_table_out, ref_count
                ws.data_ptr(), ws.numel(), _raw_stream(stream, dev))
     if rc != GQA_OK:
         raise GQADecodeError(rc, "gqa_pages_compact")
+
+
+# ------------------------------------------------- packed batches over bf16
+
+_SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "yarn": 4}
+
+
+def gqa_rope_init(D, dims=None, interleaved=False, base=10000.0, scaling="none", factor=1.0, original=0.0, low=1.0,
+                  high=4.0) -> RopeT:
+    """Rotary positions of the first `dims` (default: all D) elements of a head,
+    in pairs (i, i + dims / 2) or, interleaved, (2 i, 2 i + 1). scaling lengthens
+    the context by `factor`: "none", "linear", "base", "bands" or "yarn" (the last
+    two with the original context and the turns low and high between which pairs
+    are slowed in part). See include/gqa_decode.h."""
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling must be one of {', '.join(_SCALINGS)}")
+    rope = RopeT()
+    rc = load().gqa_rope_init(ctypes.byref(rope), D, D if dims is None else dims, bool(interleaved), float(base),
+                              _SCALINGS[scaling], float(factor), float(original), float(low), float(high))
+    if rc != GQA_OK:
+        raise GQADecodeError(rc, "gqa_rope_init")
+    return rope
+
+
+def _token_stride(name, t):
+    """Distance of the tokens of [N, heads, D], whose heads are dense."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [N, heads, D]")
+    N, heads, D = t.shape
+    if t.is_contiguous():
+        return heads * D
+    s = t.stride()
+    if s[2] != 1 or (heads > 1 and s[1] != D):
+        raise ValueError(f"{name} must have dense heads (only its tokens may be apart)")
+    return s[0] if N > 1 else heads * D
+
+
+def _check_strided(dev, named):
+    """dtype and device of (name, tensor, dtype) triples."""
+    for name, t, dt in named:
+        if t.dtype is not dt:
+            raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+        d = t.get_device()
+        if d < 0:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if d != dev:
+            raise ValueError(f"{name} is on cuda:{d}, others on cuda:{dev}: all tensors must be on one device")
+
+
+def _check_rope(rope):
+    if not isinstance(rope, RopeT):
+        raise TypeError("rope must come from gqa_rope_init")
+
+
+def gqa_rope(rope, q, k, positions, q_out, k_out, inverse=False, stream=None):
+    """Rotates q [N, H, D] and k [N, G, D] (bf16; either may be None) by
+    positions (int32 [N]) into q_out and k_out, which may be the inputs
+    themselves. inverse turns the other way (the transpose: the gradient's
+    operator). Tokens may be apart, as in views of a fused projection's rows."""
+    import torch
+    _check_rope(rope)
+    bf, named = torch.bfloat16, []
+    dev = positions.get_device()
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None) or (q is None and k is None):
+        raise ValueError("q comes with q_out and k with k_out, one of them at least")
+    if q is not None:
+        named += [("q", q, bf), ("q_out", q_out, bf)]
+    if k is not None:
+        named += [("k", k, bf), ("k_out", k_out, bf)]
+    _check_strided(dev, named)
+    _check_all(dev, (("positions", positions, torch.int32),))
+    strides = [_token_stride(name, t) for name, t, _ in named]
+    N, _, D = named[0][1].shape
+    for name, t, _ in named:
+        if t.shape[0] != N or t.shape[2] != D:
+            raise ValueError(f"{name} must be [N, heads, D] with the other tensors' N and D")
+    if positions.shape != (N,) or (q is not None and q_out.shape != q.shape) or (k is not None and k_out.shape != k.shape):
+        raise ValueError("positions must be [N], q_out like q, k_out like k")
+    qs, qos = (strides[0], strides[1]) if q is not None else (0, 0)
+    ks, kos = (strides[-2], strides[-1]) if k is not None else (0, 0)
+    rc = _call(dev, load().gqa_rope, ctypes.addressof(rope), None if q is None else q.data_ptr(),
+               None if k is None else k.data_ptr(), positions.data_ptr(), None if q is None else q_out.data_ptr(),
+               None if k is None else k_out.data_ptr(), N, 0 if q is None else q.shape[1],
+               0 if k is None else k.shape[1], D, qs, ks, qos, kos, 1 if inverse else 0, _raw_stream(stream, dev))
+    if rc != GQA_OK:
+        raise GQADecodeError(rc, "gqa_rope")
+
+
+def _paged_bf16_cache(k_pages, v_pages, block_table, seq_lens, cu):
+    """Checks the shapes of a paged bf16 cache and a packed batch; returns B,
+    num_pages, G, page_size, D and max_pages_per_seq."""
+    shape = k_pages.shape
+    if len(shape) != 4 or v_pages.shape != shape:
+        raise ValueError("k_pages / v_pages must be [num_pages, G, page_size, D]")
+    table = block_table.shape
+    if len(table) != 2 or seq_lens.shape != table[:1]:
+        raise ValueError("block_table must be [B, max_pages_per_seq] and seq_lens [B]")
+    if cu.shape != (table[0] + 1,):
+        raise ValueError("cu_new must be [B + 1]")
+    return (table[0], *shape, table[1])
+
+
+def gqa_append_paged(k_new, v_new, k_pages, v_pages, block_table, cu_new, seq_lens, rope=None, q=None, q_out=None,
+                     stream=None):
+    """Writes the new tokens k_new, v_new ([N, G, D] bf16, rows cu_new[b] to
+    cu_new[b + 1] of sequence b) to bf16 pages, at the last positions of
+    seq_lens[b]. With rope, keys are rotated on the way, and the queries q [N, H,
+    D] where given, into q_out (which may be q)."""
+    import torch
+    bf, i32 = torch.bfloat16, torch.int32
+    dev = k_new.get_device()
+    named = [("k_new", k_new, bf), ("v_new", v_new, bf)]
+    if (q is None) != (q_out is None):
+        raise ValueError("q comes with q_out")
+    if q is not None:
+        named += [("q", q, bf), ("q_out", q_out, bf)]
+    if rope is not None:
+        _check_rope(rope)
+    _check_strided(dev, named)
+    _check_all(dev, (("k_pages", k_pages, bf), ("v_pages", v_pages, bf), ("block_table", block_table, i32),
+                     ("cu_new", cu_new, i32), ("seq_lens", seq_lens, i32)))
+    B, num_pages, G, page_size, D, most = _paged_bf16_cache(k_pages, v_pages, block_table, seq_lens, cu_new)
+    strides = [_token_stride(name, t) for name, t, _ in named]
+    N = k_new.shape[0]
+    if k_new.shape[1:] != (G, D) or v_new.shape != k_new.shape:
+        raise ValueError("k_new / v_new must be [N, G, D]")
+    H = 0
+    if q is not None:
+        H = q.shape[1]
+        if q.shape != (N, H, D) or q_out.shape != q.shape:
+            raise ValueError("q / q_out must be [N, H, D]")
+    rc = _call(dev, load().gqa_append_paged, None if rope is None else ctypes.addressof(rope),
+               None if q is None else q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+               None if q is None else q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+               block_table.data_ptr(), cu_new.data_ptr(), seq_lens.data_ptr(), N, B, H, G, D,
+               strides[2] if H else 0, strides[0], strides[1], strides[3] if H else 0, page_size, num_pages, most,
+               _raw_stream(stream, dev))
+    if rc != GQA_OK:
+        raise GQADecodeError(rc, "gqa_append_paged")
+
+
+@functools.lru_cache(maxsize=4096)
+def _known_ragged_bytes(*sizes):
+    n = int(_call(sizes[-1], load().gqa_prefill_ragged_workspace_bytes, *sizes[:-1]))
+    if n == 0:
+        raise _NoSize
+    return n
+
+
+def _ragged_workspace_bytes(*sizes):
+    """By N, B, H, G, D and device."""
+    try:
+        return _known_ragged_bytes(*sizes)
+    except _NoSize:
+        return 0
+
+
+def gqa_prefill_ragged_workspace_bytes(N, B, H, G, D, device=None) -> int:
+    """Workspace bytes of gqa_prefill_packed and gqa_prefill_paged on a device
+    (0: unsupported sizes)."""
+    if device is None:
+        import torch
+        device = torch.cuda.current_device()
+    return _ragged_workspace_bytes(N, B, H, G, D, device)
+
+
+def _ragged_outputs(dev, q, out, lse, workspace):
+    """Checks q, out, lse and workspace of a packed batch; returns N, H, D."""
+    import torch
+    _check_strided(dev, (("q", q, torch.bfloat16),))
+    named = [("out", out, torch.bfloat16)]
+    if lse is not None:
+        named.append(("lse", lse, torch.float32))
+    if workspace is not None:
+        named.append(("workspace", workspace, torch.uint8))
+    _check_all(dev, named)
+    if q.dim() != 3:
+        raise ValueError("q must be [N, H, D]")
+    N, H, D = q.shape
+    if out.shape != q.shape or (lse is not None and lse.shape != (N, H)):
+        raise ValueError("out must be [N, H, D] and lse [N, H]")
+    return N, H, D
+
+
+def gqa_prefill_packed(q, k, v, cu_seqlens, scale, out, lse=None, stream=None, workspace=None):
+    """Causal attention of whole prompts that lie behind one another: q [N, H, D],
+    k and v [N, G, D] (tokens may be apart, as in views of a fused projection's
+    rows), cu_seqlens [B + 1] int32; out [N, H, D], lse [N, H]. Rows behind
+    cu_seqlens[B] are left as they are. The workspace is kept as for
+    gqa_decode_paged_fp8 when not given (gqa_prefill_ragged_workspace_bytes)."""
+    import torch
+    dev = q.get_device()
+    N, H, D = _ragged_outputs(dev, q, out, lse, workspace)
+    _check_strided(dev, (("k", k, torch.bfloat16), ("v", v, torch.bfloat16)))
+    _check_all(dev, (("cu_seqlens", cu_seqlens, torch.int32),))
+    qs, ks, vs = _token_stride("q", q), _token_stride("k", k), _token_stride("v", v)
+    G = k.shape[1]
+    if k.shape != (N, G, D) or v.shape != k.shape:
+        raise ValueError("k / v must be [N, G, D] with q's N and D")
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+        raise ValueError("cu_seqlens must be [B + 1]")
+    B = cu_seqlens.shape[0] - 1
+    if workspace is None:
+        workspace = _workspace(_ragged_workspace_bytes(N, B, H, G, D, dev) or 256, q, dev, stream)
+    rc = _call(dev, load().gqa_prefill_packed, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(),
+               float(scale), out.data_ptr(), None if lse is None else lse.data_ptr(), N, B, H, G, D, qs, ks, vs,
+               workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+    if rc != GQA_OK:
+        raise GQADecodeError(rc, "gqa_prefill_packed")
+
+
+def gqa_prefill_paged(q, k_pages, v_pages, block_table, cu_new, seq_lens, scale, out, lse=None, stream=None,
+                      workspace=None):
+    """Attention of chunks of any length, single tokens among them, over a paged
+    bf16 cache ([num_pages, G, page_size, D]): rows cu_new[b] to cu_new[b + 1] of
+    q [N, H, D] are the last tokens of seq_lens[b]. out [N, H, D], lse [N, H];
+    rows behind cu_new[B] are left as they are. Workspace as for
+    gqa_prefill_packed."""
+    import torch
+    bf, i32 = torch.bfloat16, torch.int32
+    dev = q.get_device()
+    N, H, D = _ragged_outputs(dev, q, out, lse, workspace)
+    _check_all(dev, (("k_pages", k_pages, bf), ("v_pages", v_pages, bf), ("block_table", block_table, i32),
+                     ("cu_new", cu_new, i32), ("seq_lens", seq_lens, i32)))
+    B, num_pages, G, page_size, Dk, most = _paged_bf16_cache(k_pages, v_pages, block_table, seq_lens, cu_new)
+    qs = _token_stride("q", q)
+    if Dk != D:
+        raise ValueError("q must be [N, H, D] with the pages' D")
+    if workspace is None:
+        workspace = _workspace(_ragged_workspace_bytes(N, B, H, G, D, dev) or 256, q, dev, stream)
+    rc = _call(dev, load().gqa_prefill_paged, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+               block_table.data_ptr(), cu_new.data_ptr(), seq_lens.data_ptr(), float(scale), out.data_ptr(),
+               None if lse is None else lse.data_ptr(), N, B, H, G, D, qs, page_size, num_pages, most,
+               workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+    if rc != GQA_OK:
+        raise GQADecodeError(rc, "gqa_prefill_paged")
 
 
 def gqa_decode_ex(q, k_cache, v_cache, seq_lens, scale, out, lse, workspace, stream=None):

@@ -361,6 +361,120 @@ int gqa_pages_compact(const gqa_page_pool_t* pools, int num_pools, const int32_t
                       size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Packed batches over bf16: the new tokens of B sequences, each with a number of
+ * its own, behind one another in tensors [N, heads, D]. cu[b] <= n < cu[b + 1]
+ * are the rows of sequence b (int32 [B + 1], device, ascending); a sequence may
+ * have none. Rows behind cu[B] (a batch padded to a captured size) are neither
+ * used nor written. Entries of cu are clamped to [0, N] and to their
+ * predecessor. One serving step is gqa_pages_reserve, gqa_append_paged (which
+ * rotates queries and keys) and gqa_prefill_paged.
+ *
+ * Inputs q, k, v take a stride: the distance of their tokens in elements, a
+ * multiple of 8 and at least heads * D, so that they may be views of one fused
+ * projection's rows. Tensors are 16-byte aligned, D is 64 or 128, H % G == 0.
+ * N = 0 enqueues nothing.
+ */
+
+/* Rotary positions. Pair i < dims / 2 of a head turns by t * inv_freq[i] radians
+ * at position t; the elements from `dims` on stay as they are. gain multiplies
+ * sine and cosine. */
+typedef struct gqa_rope_t {
+    int dims;            /* rotated elements of a head: even, 2..D */
+    int interleaved;     /* 1: pairs (2 i, 2 i + 1), 0: (i, i + dims / 2) */
+    double gain;
+    double inv_freq[64];
+} gqa_rope_t;
+
+/* How gqa_rope_init lengthens a context by `factor` (f = base^(-2 i / dims)):
+ *   PLAIN   f
+ *   LINEAR  f / factor
+ *   BASE    f with base * factor^(dims / (dims - 2))
+ *   BANDS   by the turns that a pair makes over `original` positions: f above
+ *           `high`, f / factor below `low`, in between the mean of both that is
+ *           linear in the turns
+ *   YARN    the same with a mean linear in the pair's index, between the pairs
+ *           that make `high` (rounded down) and `low` (rounded up) turns, and
+ *           gain = 1 + 0.1 ln(factor)
+ * factor >= 1, 0 < low < high, original > 0 where they are used. */
+#define GQA_ROPE_PLAIN 0
+#define GQA_ROPE_LINEAR 1
+#define GQA_ROPE_BASE 2
+#define GQA_ROPE_BANDS 3
+#define GQA_ROPE_YARN 4
+
+/* Fills *rope (host only); its fields may also be set by hand: gain and
+ * inv_freq finite, |inv_freq| <= 1e15. */
+int gqa_rope_init(gqa_rope_t* rope, int D, int dims, int interleaved, double base, int scaling, double factor,
+                  double original, double low, double high);
+
+/*
+ * Rotates q [N, H, D] and k [N, G, D] (either may be NULL) by positions[n]
+ * (int32 [N], device, any value) into q_out and k_out, which may be the inputs
+ * themselves, with the same stride, but not overlap them otherwise. inverse != 0
+ * turns the other way: the transpose, which is also the gradient's operator.
+ * Angles are exact modulo a turn (64-bit fixed point) to 2^-22 radians at every
+ * position; products are fp32, rounded once to bf16.
+ */
+int gqa_rope(const gqa_rope_t* rope, const void* q, const void* k, const int32_t* positions, void* q_out,
+             void* k_out, int N, int H, int G, int D, long long q_stride, long long k_stride,
+             long long q_out_stride, long long k_out_stride, int inverse, cudaStream_t stream);
+
+/*
+ * Writes new tokens to bf16 pages k_pages, v_pages [num_pages, G, page_size, D]:
+ * row cu_new[b] + s of k_new and v_new [N, G, D] goes to position T_b - n_b + s
+ * of sequence b (n_b = cu_new[b + 1] - cu_new[b] new tokens, T_b = seq_lens[b]
+ * counts them and is clamped to [0, max_pages_per_seq * page_size]). Positions
+ * below 0 and positions whose block-table entry is outside [0, num_pages) are
+ * not written. With rope, keys are rotated by their positions, and so are the
+ * queries q [N, H, D] where given, into q_out (which may be q, with its stride);
+ * without rope (NULL) q is copied. q NULL: keys and values only. Block table,
+ * page_size and page ownership as for gqa_append_paged_fp8; the arrays of a call
+ * overlap nowhere else. No workspace.
+ */
+int gqa_append_paged(const gqa_rope_t* rope, const void* q, const void* k_new, const void* v_new, void* q_out,
+                     void* k_pages, void* v_pages, const int32_t* block_table, const int32_t* cu_new,
+                     const int32_t* seq_lens, int N, int B, int H, int G, int D, long long q_stride,
+                     long long k_stride, long long v_stride, long long q_out_stride, int page_size, int num_pages,
+                     int max_pages_per_seq, cudaStream_t stream);
+
+/*
+ * Attention of whole prompts, without a cache: token s of a sequence attends to
+ * the sequence's tokens 0..s. q [N, H, D], k and v [N, G, D]; out [N, H, D] bf16
+ * and lse [N, H] (may be NULL) are dense. scale finite and > 0, H / G <= 128.
+ *
+ * gqa_prefill_paged: the same for chunks, with keys and values from pages
+ * (layouts, block table and page_size as for gqa_decode_paged): new token s of
+ * sequence b sits at position T_b - n_b + s and attends to positions up to its
+ * own. n_b may be 1 (a running sequence) or anything else, in one batch; a row
+ * with no visible key gets out = 0 and lse = -inf.
+ *
+ * Scores, sums and softmax statistics are fp32, probabilities are rounded to
+ * bf16 for the product with V. Positions that a row does not see never enter it,
+ * whatever they hold. A NaN or an infinity in V that a row sees makes its column
+ * of out NaN or infinite; in key tiles (128 tokens) that reach past the first
+ * row of a tile's limit it makes it NaN.
+ *
+ * The workspace is the caller's (256-byte aligned, no initialisation): calls
+ * that may overlap on the GPU, replays of different graphs among them, take
+ * different ones. cu, seq_lens and block_table stay as they are until the call
+ * has finished.
+ */
+int gqa_prefill_packed(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, float scale,
+                       void* out, float* lse, int N, int B, int H, int G, int D, long long q_stride,
+                       long long k_stride, long long v_stride, void* workspace, size_t workspace_bytes,
+                       cudaStream_t stream);
+
+int gqa_prefill_paged(const void* q, const void* k_pages, const void* v_pages, const int32_t* block_table,
+                      const int32_t* cu_new, const int32_t* seq_lens, float scale, void* out, float* lse, int N,
+                      int B, int H, int G, int D, long long q_stride, int page_size, int num_pages,
+                      int max_pages_per_seq, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes of both on the current device, for up to N rows and B sequences
+ * (0: unsupported sizes). */
+size_t gqa_prefill_ragged_workspace_bytes(int N, int B, int H, int G, int D);
+
+/*
  * Bytes of device workspace gqa_decode_ex needs for these sizes on the current
  * device: one 64-bit arrival counter per (sequence, KV head, 16-row tile),
  * then two partial-result slots (O[R][D] normalised by its own sum, running
