@@ -660,6 +660,25 @@ int encode_byte_map(CUtensorMap* map, const void* base, long long slabs, int row
     return GQA_OK;
 }
 
+int encode_page_map(CUtensorMap* map, const void* base, long long slabs, int rows, int D, int box_rows) {
+    return encode_cache_map(map, base, slabs, rows, D, box_rows);
+}
+
+int encode_rows_map(CUtensorMap* map, const void* base, int N, int heads, int D, long long stride, int box_heads,
+                    int box_tokens) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (!fn) return cuda_fail(cudaErrorNotSupported);
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)N};
+    cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
+    return GQA_OK;
+}
+
 template <template <int, int, bool> class F>
 int shape_query(int D, int mt, bool kv8) {
     if (kv8) return mt == 1 ? F<128, 1, true>::value : F<128, 2, true>::value;

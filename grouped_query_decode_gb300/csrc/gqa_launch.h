@@ -50,5 +50,11 @@ void wait_knobs(unsigned long long* timeout_ns, int* skip_tile);
 // cuTensorMapEncodeTiled of a 3-D uint8 tensor [slabs][rows][cols] (dense) with
 // boxes of box_rows x cols bytes and the swizzle that `cols` (64 or 128) spans.
 int encode_byte_map(CUtensorMap* map, const void* base, long long slabs, int rows, int cols, int box_rows);
+// The same of a bf16 cache [slabs][rows][D] with boxes of box_rows x 64 elements.
+int encode_page_map(CUtensorMap* map, const void* base, long long slabs, int rows, int D, int box_rows);
+// And of packed bf16 rows [N][heads][D], tokens `stride` elements apart, with boxes
+// of box_tokens x box_heads x 64 elements.
+int encode_rows_map(CUtensorMap* map, const void* base, int N, int heads, int D, long long stride, int box_heads,
+                    int box_tokens);
 
 }  // namespace gqa

@@ -1,0 +1,878 @@
+// Causal attention of packed batches (whole prompts, or chunks over a paged
+// cache) on the 5th-generation tensor cores, for sm_103a.
+//
+// A unit is (sequence, KV head, 2 * tq new tokens), tq = floor(128 / (H / G)): two
+// 128-row tiles A and B whose rows are the tokens' heads that read the KV head,
+// token by token, so K and V are read once for all of them. Per key tile of 128:
+//     S_X = Q_X K^T     M = 128, N = 128, K = D     (A, B operands in shared memory)
+//     O_X += P_X V      M = 128, N = D,   K = 128   (P in tensor memory)
+// with a running reference m per row that moves only when a score exceeds it by
+// more than 2^8 (then O_X is rescaled in tensor memory), fp32 sums, and P rounded
+// to bf16 over the columns of S_X that it came from.
+//
+// Work: gqa_ragged_plan.cuh. One CTA per SM walks the units of its share; parts
+// of units that shares cut leave (O, m, l) in the workspace, and the CTA that
+// arrives last merges them in the order of the parts.
+//
+// Warps: 0-3 and 4-7 softmax of A and B, a thread per row; 8-11 outputs; 12 issues
+// the products, always one of A, one of B, so that each tile's softmax runs behind
+// the other's products; 13 loads Q, K and V by TMA, a lane per page; 14 mends V
+// tiles that reach past the first row's limit; 15 plans and hands the units out
+// through a ring in shared memory. Every wait is bounded; after one has expired
+// the CTA runs through its units without work, so that the counters end at zero.
+//
+// V at positions that only some rows see: a masked key's weight is 0, and 0 times
+// NaN or infinity is not. In tiles past the first row's limit warp 14 zeroes what
+// no row sees, and takes out values that are not finite; a row that sees such a
+// value gets NaN in its column with the output.
+#pragma once
+
+#include <atomic>
+
+#include "gqa_device.cuh"
+#include "gqa_paged_fp8.cuh"
+#include "gqa_ragged.h"
+#include "gqa_ragged_plan.cuh"
+#include "tcgen05.cuh"
+
+namespace gqa {
+
+constexpr int kRgUnits = 4;              // ring of units
+constexpr int kRgThreads = 512;
+constexpr float kRgSlack = 8.0f;         // p <= 2^8 before the reference moves
+constexpr int kRgFirst = 64;             // keys whose weights are handed over ahead of the tile's others
+
+template <int D>
+struct RgShape {
+    static constexpr int kBlock = 128 * 128;              // 128 rows x 128 B, 128-byte swizzle
+    static constexpr int kBlocks = D / 64;
+    static constexpr int kTile = kBlocks * kBlock;        // Q, K or V of one tile
+    static constexpr int kStages = D == 128 ? 4 : 8;      // K and V tiles, in turn
+    static constexpr int kMlBytes = 2 * 128 * 8;
+    static constexpr int kBadBytes = kRgUnits * D * 4;
+    static constexpr int kUnitBytes = kRgUnits * 64;
+    static constexpr int kMiscBytes = 512;
+    static constexpr int kBars = 3 * kStages + 2 * 10 + 2 * kRgUnits + 1;
+    static constexpr int kSmemBytes =
+        1024 + 2 * kTile + kStages * kTile + kMlBytes + kBadBytes + kUnitBytes + kMiscBytes + 8 * kBars;
+    // Columns: S_A | S_B | O_A | O_B, with P over the first half of its S; D = 64
+    // has room for P apart (S_A | S_B | P_A | P_B | O_A | O_B), so that the next
+    // scores wait only until these have been read.
+    static constexpr bool kApart = D == 64;
+    static constexpr uint32_t kColS = 0, kColP = kApart ? 256 : 0, kStepP = kApart ? 64 : 128, kColO = kApart ? 384 : 256;
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
+};
+
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+#define RG_8(f, i) f(i), f(i + 1), f(i + 2), f(i + 3), f(i + 4), f(i + 5), f(i + 6), f(i + 7)
+#define RG_64(f) RG_8(f, 0), RG_8(f, 8), RG_8(f, 16), RG_8(f, 24), RG_8(f, 32), RG_8(f, 40), RG_8(f, 48), RG_8(f, 56)
+#define RG_OUT(i) "=f"(r[i])
+#define RG_BOTH(i) "+f"(r[i])
+
+// 64 fp32 columns of this thread's lane, under way until tmem_ld_wait has seen them.
+__device__ __forceinline__ void tmem_ld64_start(uint32_t taddr, float* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, "
+        "%36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, "
+        "%57, %58, %59, %60, %61, %62, %63}, [%64];"
+        : RG_64(RG_OUT)
+        : "r"(taddr));
+}
+// Waits for this thread's loads; the columns are named so that nothing reads them earlier.
+__device__ __forceinline__ void tmem_ld_wait(float* r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : RG_64(RG_BOTH));
+}
+
+// Maximum of 64 values, by eight chains.
+__device__ __forceinline__ float max64(const float* s) {
+    float t[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) t[k] = fmaxf(s[k], s[k + 8]);
+#pragma unroll
+    for (int i = 16; i < 64; i += 16)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t[k] = fmax3(t[k], s[i + k], s[i + 8 + k]);
+    return fmaxf(fmax3(t[0], t[1], t[2]), fmax3(fmax3(t[3], t[4], t[5]), t[6], t[7]));
+}
+
+// Weights 2^(s * scale + neg) of keys [K0, K1) into their columns of P, and their sums.
+template <int K0, int K1>
+__device__ __forceinline__ void rg_weights(const float* s, float2 scale, float2 neg, float2 (&sum)[4], uint32_t p_t) {
+#pragma unroll
+    for (int k = K0; k < K1; k += 32) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            const float2 z = fma_x2(make_float2(s[k + i], s[k + i + 1]), scale, neg);
+            const float2 e = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+            sum[(i / 2) & 3] = add_x2(sum[(i / 2) & 3], e);
+            pk[i / 2] = pack_bf16x2(e.x, e.y);
+        }
+        tmem_st16(p_t + k / 2, pk);
+    }
+}
+
+__device__ __forceinline__ RgSeq rg_sequence(const RaggedParams& p, int b) {
+    RgSeq s = {0, 0, 0};
+    if (b < p.B) {
+        s.start = clamp_len(__ldg(p.cu + b), p.N);
+        s.n = max(min(__ldg(p.cu + b + 1), p.N), s.start) - s.start;
+        s.T = p.table ? clamp_len(__ldg(p.lens + b), p.max_pages << p.page_shift) : s.n;
+    }
+    return s;
+}
+
+// Merges the parts of a unit: M = max m, L = sum l 2^(m - M), O = sum O 2^(m - M) / L,
+// part by part in their order. A warp per row.
+template <int D>
+__device__ __noinline__ void rg_merge(const RaggedParams& p, const RgUnit& u, int warp, int lane) {
+    constexpr int kPer = D / 32;
+    auto at = [&](int i) {
+        const int c = u.first + i;
+        // The first part is in the slot of its CTA's units that go on, or, where an
+        // earlier CTA had none, of those that came from before: its counter's.
+        return p.part + (size_t)(i == 0 ? u.counter : 2 * c) * rg_slot_floats(D);
+    };
+    for (int x = 0; x < 2; ++x) {
+        const int rows = u.tokens[x] * p.heads_per_group;
+        for (int row = warp; row < rows; row += 4) {
+            const int r = x * 128 + row;
+            float M = -INFINITY, L = 0.f, o[kPer] = {};
+            for (int i = 0; i < u.parts; ++i) {
+                const float* part = at(i);
+                const float m = __ldcg(part + 256 * D + r), l = __ldcg(part + 256 * D + 256 + r);
+                if (l == 0.f) continue;
+                const float top = fmaxf(M, m), a = fast_exp2(M - top), w = fast_exp2(m - top);
+                M = top;
+                L = L * a + l * w;
+                for (int k = 0; k < kPer; ++k) o[k] = o[k] * a + __ldcg(part + (size_t)r * D + lane * kPer + k) * w;
+            }
+            const int tok = p.by_heads(row);
+            const size_t orow = (size_t)(u.row0 + x * p.tq + tok) * p.H + (size_t)u.g * p.heads_per_group +
+                                (row - tok * p.heads_per_group);
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            uint16_t* dst = p.out + orow * D + lane * kPer;
+            for (int k = 0; k < kPer; k += 2)
+                *reinterpret_cast<uint32_t*>(dst + k) = L == 0.f ? 0u : pack_bf16x2(o[k] * inv, o[k + 1] * inv);
+            if (p.lse && lane == 0) p.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+        }
+    }
+}
+
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(kRgThreads, 1)
+    gqa_ragged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ RaggedParams p) {
+    using RS = RgShape<D>;
+    constexpr int S = RS::kStages;
+    constexpr uint32_t kBlock = RS::kBlock, kTile = RS::kTile;
+
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    const uint32_t q_s = base, ring_s = q_s + 2 * kTile;
+    unsigned char* gen = smem_raw + (ring_s + S * kTile - raw);
+    float2* const ml = reinterpret_cast<float2*>(gen);               // [2][128]
+    gen += RS::kMlBytes;
+    int* const bad = reinterpret_cast<int*>(gen);                    // [units][D]: first position with such a value
+    gen += RS::kBadBytes;
+    RgUnit* const units = reinterpret_cast<RgUnit*>(gen);
+    gen += RS::kUnitBytes;
+    uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gen);
+    volatile int* const abort_flag = reinterpret_cast<volatile int*>(gen + 4);
+    volatile int* const last_flag = reinterpret_cast<volatile int*>(gen + 8);
+    int* const bad_flag = reinterpret_cast<int*>(gen + 16);          // [units]
+    long long* const first_s = reinterpret_cast<long long*>(gen + 64);   // total; sequence and offset of the share's start
+    long long* const warp_sum = reinterpret_cast<long long*>(gen + 128); // [16]
+    gen += RS::kMiscBytes;
+    const uint32_t full = smem_addr(gen), empty = full + 8 * S, mended = empty + 8 * S;
+    const uint32_t q_full = mended + 8 * S, q_empty = q_full + 16, s_full = q_empty + 16, p_full = s_full + 16;
+    const uint32_t p_rest = p_full + 16, s_free = p_rest + 16, pv_done = s_free + 16;
+    const uint32_t o_full = pv_done + 16, o_empty = o_full + 16, ml_full = o_empty + 16, fin = ml_full + 16;
+    const uint32_t u_full = fin + 8, u_empty = u_full + 8 * kRgUnits;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint64_t tmo = p.wait_timeout_ns;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, 1 + (s & 1));    // V, in odd stages, has been seen by warp 14 too
+            mbar_init(mended + 8 * s, 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(q_full + 8 * x, 1);
+            mbar_init(q_empty + 8 * x, 1);
+            mbar_init(s_full + 8 * x, 1);
+            mbar_init(p_full + 8 * x, 4);
+            mbar_init(p_rest + 8 * x, 4);
+            mbar_init(s_free + 8 * x, 4);
+            mbar_init(pv_done + 8 * x, 1);
+            mbar_init(o_full + 8 * x, 1);
+            mbar_init(o_empty + 8 * x, 4);
+            mbar_init(ml_full + 8 * x, 4);
+        }
+        mbar_init(fin, 1);
+        for (int i = 0; i < kRgUnits; ++i) {
+            mbar_init(u_full + 8 * i, 1);
+            mbar_init(u_empty + 8 * i, 15);       // softmax and output warps, products, loads, mending
+        }
+        for (int i = 0; i < kRgUnits; ++i) bad_flag[i] = 0;
+        *abort_flag = 0;
+        first_s[1] = p.B;
+        fence_barrier_init();
+    }
+    if (warp == 12) {
+        tmem_alloc(smem_addr(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    if (warp == 13 && lane < 3) tma_prefetch_desc(lane == 0 ? &tm_q : lane == 1 ? &tm_k : &tm_v);
+    pdl_launch_dependents();
+    pdl_wait_primary();
+
+    // The line's length, and the sequence in which this CTA's share starts: every
+    // thread takes some sequences in a row.
+    const RgLine line = {p.tq, p.G};
+    {
+        const int per = (p.B + kRgThreads - 1) / kRgThreads;
+        const int b0 = min((int)threadIdx.x * per, p.B), b1 = min(b0 + per, p.B);
+        long long mine = 0;
+        for (int b = b0; b < b1; ++b) mine += line.head(rg_sequence(p, b)) * p.G;
+        long long sum = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        if (lane == 31) warp_sum[warp] = sum;
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        long long before = 0, total = 0;
+#pragma unroll
+        for (int w = 0; w < kRgThreads / 32; ++w) {
+            const long long y = warp_sum[w];
+            if (w < warp) before += y;
+            total += y;
+        }
+        long long at = before + sum - mine;
+        const RgShares sh = RgShares::of(total, gridDim.x);
+        const long long from = (int)blockIdx.x < sh.ctas ? sh.at(blockIdx.x) : total;
+        if (at <= from && from < at + mine)
+            for (int b = b0; b < b1; ++b) {
+                const long long y = line.head(rg_sequence(p, b)) * p.G;
+                if (from < at + y) {
+                    first_s[1] = b;
+                    first_s[2] = at;
+                    break;
+                }
+                at += y;
+            }
+        if (threadIdx.x == 0) first_s[0] = total;
+        __syncthreads();
+    }
+    const uint32_t tmem = *tmem_slot;
+
+    auto wait = [&](uint32_t bar, uint32_t parity) { return wait_phase(bar, parity & 1, abort_flag, p.status, tmo); };
+    // The next unit, for every lane of a warp. Waits on although the CTA has given
+    // up its work: units keep coming. False: none comes any more.
+    auto next_unit = [&](uint32_t n) {
+        const uint32_t bar = u_full + 8 * (n % kRgUnits), parity = (n / kRgUnits) & 1;
+        if (!mbar_try_wait(bar, parity)) {
+            const uint64_t t0 = global_timer_ns();
+            while (!mbar_try_wait(bar, parity))
+                if (global_timer_ns() - t0 > 8 * tmo) return false;
+        }
+        return true;
+    };
+
+    if (warp >= 12) {
+        fewer_registers<80>();
+        if (warp == 15) {
+            // ------------------------------------------------------------ plan
+            const RgShares sh = RgShares::of(first_s[0], gridDim.x);
+            const int c = blockIdx.x;
+            const long long to = c < sh.ctas ? sh.at(c + 1) : 0;
+            int b = (int)first_s[1];
+            long long at = first_s[2];
+            uint32_t n = 0;
+            int chunk = b;                          // lanes hold sequences chunk + lane
+            RgSeq mine = rg_sequence(p, chunk + lane);
+            const long long from = c < sh.ctas ? sh.at(c) : 0;
+            auto publish = [&](const RgUnit& u) {
+                bool ok = true;
+                if (lane == 0) {
+                    const uint64_t t0 = global_timer_ns();
+                    while (ok && !mbar_try_wait(u_empty + 8 * (n % kRgUnits), ((n / kRgUnits) & 1) ^ 1))
+                        ok = global_timer_ns() - t0 <= 4 * tmo;
+                    if (ok) {
+                        units[n % kRgUnits] = u;
+                        mbar_arrive(u_full + 8 * (n % kRgUnits));
+                    } else {
+                        *abort_flag = 1;
+                        atomicOr(p.status, kStatusTimeout);
+                    }
+                }
+                ++n;
+                return __shfl_sync(0xffffffffu, ok, 0) != 0;
+            };
+            bool ok = true;
+            for (bool first = true; ok && b < p.B && at < to; ++b) {
+                if (b >= chunk + 32) {
+                    chunk = b;
+                    mine = rg_sequence(p, chunk + lane);
+                }
+                RgSeq s;
+                s.start = __shfl_sync(0xffffffffu, mine.start, b - chunk);
+                s.n = __shfl_sync(0xffffffffu, mine.n, b - chunk);
+                s.T = __shfl_sync(0xffffffffu, mine.T, b - chunk);
+                const int pairs = line.pairs(s.n);
+                if (pairs == 0) continue;
+                const long long head = line.head(s);
+                int g = 0, pr = 0;
+                if (first) {
+                    g = (int)((from - at) / head);
+                    pr = line.pair_at(s, from - at - g * head);
+                    first = false;
+                }
+                for (; ok && g < p.G; ++g, pr = 0)
+                    for (; ok && pr < pairs; ++pr) {
+                        const long long unit = at + g * head + line.start(s, pr);
+                        if (unit >= to) {
+                            g = p.G;
+                            break;
+                        }
+                        RgUnit u;
+                        u.seq = b;
+                        u.g = g;
+                        if (rg_unit(line, sh, c, s, pr, unit, &u)) {
+                            if (u.slot >= 0 && lane == 0) tag_counter(p.counters + u.counter, p.tag);
+                            ok = publish(u);
+                        }
+                    }
+                at += head * p.G;
+            }
+            RgUnit none = {};
+            if (ok) publish(none);
+        } else if (warp == 13) {
+            // ----------------------------------------------------------- loads
+            const int page_rows = PAGED ? min(1 << p.page_shift, kRgTile) : kRgTile;
+            const int boxes = kRgTile / page_rows;
+            uint32_t it = 0, nq[2] = {0, 0};
+            // Copies issued: bit s, bit 16 + x; and the parity of the last of each.
+            uint32_t issued = 0, parity = 0;
+            auto note = [&](int bit, uint32_t phase) {
+                issued |= 1u << bit;
+                parity = (parity & ~(1u << bit)) | ((phase & 1) << bit);
+            };
+            for (uint32_t n = 0; next_unit(n); ++n) {
+                __syncwarp();
+                const RgUnit& u = units[n % kRgUnits];
+                if (!u.valid) break;
+                const int g = u.g, all = max(u.tiles[0], u.tiles[1]);
+                const int last = u.pos_last;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (u.tiles[x] == 0) continue;
+                    const bool ok = !*abort_flag && wait(q_empty + 8 * x, nq[x] ^ 1);
+                    if (ok) note(16 + x, nq[x]);
+                    ++nq[x];
+                    if (ok && lane == 0) {
+                        mbar_arrive_expect_tx(q_full + 8 * x, RS::kBlocks * p.tq * p.heads_per_group * 128);
+#pragma unroll
+                        for (int k = 0; k < RS::kBlocks; ++k)
+                            tma_load_3d(q_s + x * kTile + k * kBlock, &tm_q, q_full + 8 * x, k * 64,
+                                        g * p.heads_per_group, u.row0 + x * p.tq);
+                    }
+                }
+                // This lane's page of key tile j: its slab, or the one past the last.
+                auto slab = [&](int j) {
+                    int page = p.num_pages;
+                    if (lane < boxes) {
+                        const int t = (u.j0 + j) * kRgTile + lane * page_rows;
+                        if (t <= last) {
+                            const int e = __ldg(p.table + (size_t)u.seq * p.max_pages + (t >> p.page_shift));
+                            if ((unsigned)e < (unsigned)p.num_pages) page = e;
+                        }
+                    }
+                    return page == p.num_pages ? p.num_pages * p.G : page * p.G + g;
+                };
+                int now = PAGED && all > 0 ? slab(0) : 0;
+                for (int j = 0; j < all; ++j) {
+                    const int then = PAGED && j + 1 < all ? slab(j + 1) : 0;
+#pragma unroll
+                    for (int v = 0; v < 2; ++v, ++it) {
+                        const uint32_t s = it % S;
+                        const bool ok = !*abort_flag && wait(empty + 8 * s, (it / S) ^ 1);
+                        if (!__all_sync(0xffffffffu, ok)) continue;
+                        if (blockIdx.x == 0 && v == 0 && n == 0 && j == p.skip_tile) continue;   // injected fault
+                        note(s, it / S);
+                        if (lane == 0) mbar_arrive_expect_tx(full + 8 * s, kTile);
+                        __syncwarp();
+                        const uint32_t dst = ring_s + s * kTile;
+                        const CUtensorMap* tm = v ? &tm_v : &tm_k;
+                        if (PAGED) {
+                            const int row = ((u.j0 + j) * kRgTile) & ((1 << p.page_shift) - 1);
+                            if (lane < boxes)
+#pragma unroll
+                                for (int k = 0; k < RS::kBlocks; ++k)
+                                    tma_load_3d(dst + k * kBlock + lane * page_rows * 128, tm, full + 8 * s, k * 64,
+                                                boxes > 1 ? 0 : row, now);
+                        } else if (lane == 0) {
+#pragma unroll
+                            for (int k = 0; k < RS::kBlocks; ++k)
+                                tma_load_3d(dst + k * kBlock, tm, full + 8 * s, k * 64, g,
+                                            u.key0 + (u.j0 + j) * kRgTile);
+                        }
+                    }
+                    now = then;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(u_empty + 8 * (n % kRgUnits));
+            }
+            // Leave only once all copies have landed.
+            if (lane == 0)
+                for (int i = 0; i < 18; ++i) {
+                    if (!(issued >> i & 1)) continue;
+                    const uint32_t bar = i < 16 ? full + 8 * i : q_full + 8 * (i - 16);
+                    const uint64_t t0 = global_timer_ns();
+                    while (!mbar_try_wait(bar, parity >> i & 1))
+                        if (global_timer_ns() - t0 > tmo) break;
+                }
+        } else if (warp == 14) {
+            // ------------------------------------------------------- mending V
+            uint32_t it = 0;
+            for (uint32_t n = 0; next_unit(n); ++n) {
+                __syncwarp();
+                const RgUnit& u = units[n % kRgUnits];
+                if (!u.valid) break;
+                const int all = max(u.tiles[0], u.tiles[1]), slot = n % kRgUnits;
+                const int lim = u.pos0, last = u.pos_last, j0 = u.j0;
+                bool any = false;
+                for (int j = 0; j < all; ++j, it += 2) {
+                    const int t0 = (j0 + j) * kRgTile;
+                    const bool mend = t0 + kRgTile - 1 > lim;
+                    const uint32_t s = (it + 1) % S, v_s = ring_s + s * kTile;
+                    const bool ok = !*abort_flag && wait(full + 8 * s, (it + 1) / S);
+                    if (__all_sync(0xffffffffu, ok) && mend) {
+                        // Rows [r0, r1) are seen by some, those from r1 on by none.
+                        const int r0 = max(0, lim + 1 - t0), r1 = max(0, min(kRgTile, last + 1 - t0));
+                        auto chunk = [&](int r, int c) { return v_s + (c >> 3) * kBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
+                        constexpr int kChunks = D / 8;
+                        for (int i = r1 * kChunks + lane; i < kRgTile * kChunks; i += 32)
+                            st_shared_zero16(chunk(i / kChunks, i % kChunks));
+                        // x * 0 is NaN for what is not finite.
+                        uint32_t sum = 0;
+                        const uint32_t zero = 0;
+#pragma unroll 4
+                        for (int i = r0 * kChunks + lane; i < r1 * kChunks; i += 32) {
+                            uint32_t w[4];
+                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                         : "r"(chunk(i / kChunks, i % kChunks)));
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(w[k]), "r"(zero));
+                        }
+                        if (__any_sync(0xffffffffu, (sum & 0x7fff7fffu) != 0)) {
+                            int* const col = bad + slot * D;
+                            if (!any)
+                                for (int i = lane; i < D; i += 32) col[i] = 0x7fffffff;
+                            any = true;
+                            __syncwarp();
+                            for (int i = r0 * kChunks + lane; i < r1 * kChunks; i += 32) {
+                                const uint32_t a = chunk(i / kChunks, i % kChunks);
+                                for (int k = 0; k < 8; ++k) {
+                                    uint16_t e;
+                                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e) : "r"(a + 2 * k));
+                                    if ((e & 0x7f80) != 0x7f80) continue;
+                                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(a + 2 * k), "h"((uint16_t)0) : "memory");
+                                    atomicMin(col + (i % kChunks) * 8 + k, t0 + i / kChunks);
+                                }
+                            }
+                            __threadfence_block();
+                            __syncwarp();
+                            if (lane == 0) *reinterpret_cast<volatile int*>(bad_flag + slot) = 1 + (int)(n / kRgUnits);
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (mend) mbar_arrive(mended + 8 * s);
+                        mbar_arrive(empty + 8 * s);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(u_empty + 8 * (n % kRgUnits));
+            }
+        } else if (lane == 0) {
+            // -------------------------------------------------------- products
+            constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
+            constexpr uint32_t kIdescO = idesc_bf16_f32(128, D, false, true);
+            struct Now {
+                int a, b, all, j0, lim;          // key tiles of A, B, both
+                uint32_t it;
+            } u = {0, 0, 1, 0, 0, 0}, next = u;  // a unit without tiles leads in the first
+            uint32_t n = 0, it = 0, phases = 0, mends = 0;
+            bool ok = true, issued = false;
+            auto wait_next = [&](uint32_t bar, int bit, uint32_t flip) {
+                ok = ok && wait(bar, (phases >> bit) ^ flip);
+                phases ^= 1u << bit;
+            };
+            // The next unit with key tiles.
+            auto fetch = [&]() {
+                while (next_unit(n)) {
+                    const RgUnit& f = units[n % kRgUnits];
+                    if (!f.valid) return false;
+                    next = {f.tiles[0], f.tiles[1], max(f.tiles[0], f.tiles[1]), f.j0, f.pos0, it};
+                    mbar_arrive(u_empty + 8 * (n % kRgUnits));
+                    ++n;
+                    it += 2 * next.all;
+                    if (next.all > 0) return true;
+                }
+                return false;
+            };
+            constexpr uint64_t kDescK = smem_desc_base(16, 1024), kDescV = smem_desc_base(kBlock, 1024);
+            // S_X of the K tile at ring place i.
+            auto scores = [&](uint32_t i, int x, bool first, bool last, bool release) {
+                const uint32_t s = i % S;
+                if (first) wait_next(q_full + 8 * x, x, 0);
+                if (RS::kApart) wait_next(s_free + 8 * x, 6 + x, 1);
+                ok = ok && wait(full + 8 * s, i / S);
+                if (!ok) return;
+                tc_fence_after();
+                const uint64_t a = kDescK + ((q_s + x * kTile) >> 4), b = kDescK + ((ring_s + s * kTile) >> 4);
+                const uint32_t to = tmem + RS::kColS + x * 128;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = ((k >> 2) * kBlock + (k & 3) * 32) >> 4;
+                    umma_bf16(to, a + off, b + off, kIdescS, k > 0 ? 1u : 0u);
+                }
+                issued = true;
+                umma_commit(s_full + 8 * x);
+                if (last) umma_commit(q_empty + 8 * x);
+                if (release) umma_commit(empty + 8 * s);
+            };
+            // O_X += P_X V for the V tile at ring place i.
+            auto values = [&](uint32_t i, int x, bool fresh, bool mend, bool first, bool last, bool release) {
+                const uint32_t s = i % S;
+                if (fresh) {
+                    ok = ok && wait((mend ? mended : full) + 8 * s, mend ? mends >> s : i / S);
+                    if (mend) mends ^= 1u << s;
+                }
+                if (first) wait_next(o_empty + 8 * x, 4 + x, 1);
+                const uint64_t b = kDescV + ((ring_s + s * kTile) >> 4);
+                const uint32_t to = tmem + RS::kColO + x * D, a = tmem + RS::kColP + x * RS::kStepP;
+                ok = ok && wait(p_full + 8 * x, phases >> (2 + x));
+                if (!ok) return;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < kRgTile / 16; ++k) {
+                    if (k == kRgFirst / 16) {
+                        ok = wait(p_rest + 8 * x, phases >> (2 + x));
+                        if (!ok) return;
+                        tc_fence_after();
+                    }
+                    umma_bf16_ts(to, a + k * 8, b + k * (16 * 128 >> 4), kIdescO, (!first || k > 0) ? 1u : 0u);
+                }
+                phases ^= 4u << x;
+                if (RS::kApart) umma_commit(pv_done + 8 * x);
+                if (last) umma_commit(o_full + 8 * x);
+                if (release) umma_commit(empty + 8 * s);
+            };
+            bool have = true;
+            while (have) {
+                bool more = false;
+#pragma unroll 1
+                for (int j = 0; j < u.all; ++j) {
+                    const bool end = j + 1 == u.all;
+                    if (end) more = fetch();
+                    const bool mend = (u.j0 + j) * kRgTile + kRgTile - 1 > u.lim;
+#pragma unroll 1
+                    for (int x = 0; x < 2; ++x) {
+                        const int tiles = x ? u.b : u.a;
+                        // What S_X holds next: this unit's next tile, or the next unit's first.
+                        bool go = j + 1 < tiles, lead = false;
+                        uint32_t i = u.it + 2 * (j + 1);
+                        bool last = j + 2 == tiles, release = x == 1 || j + 1 >= u.b;
+                        if (!go && end && more) {
+                            const int t = x ? next.b : next.a;
+                            go = lead = t > 0;
+                            i = next.it;
+                            last = t == 1;
+                            release = x == 1 || next.b == 0;
+                        }
+                        if (RS::kApart && go) scores(i, x, lead, last, release);
+                        if (j < tiles)
+                            values(u.it + 2 * j + 1, x, x == 0 || j >= u.a, mend, j == 0, j + 1 == tiles, x == 1 || j >= u.b);
+                        if (!RS::kApart && go) scores(i, x, lead, last, release);
+                    }
+                }
+                u = next;
+                have = more;
+            }
+            if (issued) {
+                // Every product has completed once this flips.
+                umma_commit(fin);
+                const uint64_t t0 = global_timer_ns();
+                while (!mbar_try_wait(fin, 0))
+                    if (global_timer_ns() - t0 > tmo) {
+                        atomicOr(p.status, kStatusTimeout);
+                        break;
+                    }
+            }
+        }
+    } else if (warp >= 8) {
+        // ---------------------------------------------------------------- outputs
+        fewer_registers<80>();
+        const int row = threadIdx.x & 127;
+        const int tok = p.by_heads(row);
+        const bool in_tile = row < p.tq * p.heads_per_group;
+        uint32_t nt[2] = {0, 0};
+        for (uint32_t n = 0; next_unit(n); ++n) {
+            __syncwarp();
+            const RgUnit& u = units[n % kRgUnits];
+            if (!u.valid) break;
+            const int slot = u.slot;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                if (u.tokens[x] == 0) continue;
+                const bool some = u.tiles[x] > 0;
+                float m = -INFINITY, l = 0.f;
+                bool ok = true;
+                if (some) {
+                    ok = !*abort_flag && wait(ml_full + 8 * x, nt[x]) && wait(o_full + 8 * x, nt[x]);
+                    ok = __all_sync(0xffffffffu, ok);
+                    ++nt[x];
+                }
+                const bool valid = in_tile && tok < u.tokens[x];
+                if (ok) {
+                    tc_fence_after();
+                    if (some) {
+                        const float2 y = ml[x * 128 + row];
+                        m = y.x;
+                        l = y.y;
+                    }
+                    const bool flagged = *reinterpret_cast<volatile int*>(bad_flag + n % kRgUnits) == 1 + (int)(n / kRgUnits);
+                    const int lim = u.pos0 + x * p.tq + tok;
+                    const size_t orow = (size_t)(u.row0 + x * p.tq + tok) * p.H + (size_t)u.g * p.heads_per_group +
+                                        (row - tok * p.heads_per_group);
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    float* const part = p.part + (size_t)max(slot, 0) * rg_slot_floats(D);
+                    const int r = x * 128 + row;
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        if (some) {
+                            tmem_ld32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + RS::kColO + x * D + c, o);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = 0u;
+                        }
+                        if (c + 32 == D && some) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(o_empty + 8 * x);
+                        }
+                        if (l == 0.f)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = 0u;
+                        if (flagged)
+                            for (int i = 0; i < 32; ++i)
+                                if (bad[(n % kRgUnits) * D + c + i] <= lim) o[i] = 0x7fc00000u;
+                        if (valid && slot < 0) {
+                            uint4* const dst = reinterpret_cast<uint4*>(p.out + orow * D + c);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    w[i] = pack_bf16x2(__uint_as_float(o[8 * k + 2 * i]) * inv,
+                                                       __uint_as_float(o[8 * k + 2 * i + 1]) * inv);
+                                dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        } else if (valid && l != 0.f) {
+                            uint4* const dst = reinterpret_cast<uint4*>(part + (size_t)r * D + c);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        }
+                        __syncwarp();
+                    }
+                    if (valid) {
+                        if (slot >= 0) {
+                            part[256 * D + r] = m;
+                            part[256 * D + 256 + r] = l;
+                        } else if (p.lse) {
+                            p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                        }
+                    }
+                }
+            }
+            if (slot >= 0) {
+                // The last part to arrive merges all. The barrier orders the parts' stores
+                // before the arrival, which releases them.
+                named_sync(1, 128);
+                if (row == 0) *last_flag = arrive_last(p.counters + u.counter, p.tag, u.parts);
+                named_sync(1, 128);
+                if (*last_flag) rg_merge<D>(p, u, warp & 3, lane);
+                named_sync(1, 128);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(u_empty + 8 * (n % kRgUnits));
+        }
+    } else {
+        // ---------------------------------------------------------------- softmax
+        more_registers<176>();
+        const int x = warp >> 2, row = threadIdx.x & 127;
+        const int tok = p.by_heads(row);
+        const bool in_tile = row < p.tq * p.heads_per_group;
+        const uint32_t s_t = tmem + ((uint32_t)((warp & 3) * 32) << 16) + RS::kColS + x * 128;
+        const uint32_t o_t = tmem + ((uint32_t)((warp & 3) * 32) << 16) + RS::kColO + x * D;
+        const uint32_t p_t = tmem + ((uint32_t)((warp & 3) * 32) << 16) + RS::kColP + x * RS::kStepP;
+        uint32_t ns = 0, nu = 0, nd = 0;         // score tiles, units, products so far
+        for (uint32_t n = 0; next_unit(n); ++n) {
+            __syncwarp();
+            const RgUnit& u = units[n % kRgUnits];
+            if (!u.valid) break;
+            const int tiles = u.tiles[x], j0 = u.j0;
+            const int lim = in_tile && tok < u.tokens[x] ? u.pos0 + x * p.tq + tok : -1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(u_empty + 8 * (n % kRgUnits));
+            if (tiles == 0) continue;
+            const bool idle = __all_sync(0xffffffffu, lim < 0);      // no row of this warp sees anything
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < tiles; ++j, ++ns) {
+                bool ok = !*abort_flag && wait(s_full + 8 * x, ns);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) continue;
+                tc_fence_after();
+                if (idle) {
+                    if (RS::kApart) {
+                        // No arrival for this tile's P may count for the one before.
+                        if (lane == 0) mbar_arrive(s_free + 8 * x);
+                        if (nd > 0) ok = wait(pv_done + 8 * x, nd - 1);
+                        ++nd;
+                        if (!__all_sync(0xffffffffu, ok)) continue;
+                    }
+                    if (lane == 0) {
+                        mbar_arrive(p_full + 8 * x);
+                        mbar_arrive(p_rest + 8 * x);
+                    }
+                    continue;
+                }
+                float s[kRgTile];
+                tmem_ld64_start(s_t, s);
+                tmem_ld_wait(s);
+                tmem_ld64_start(s_t + 64, s + 64);
+                const int t0 = (j0 + j) * kRgTile;
+                const bool edge = t0 + kRgTile - 1 > lim;
+                if (edge) {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) s[i] = t0 + i <= lim ? s[i] : -INFINITY;
+                }
+                float top = max64(s);
+                tmem_ld_wait(s + 64);
+                if (RS::kApart) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s_free + 8 * x);
+                }
+                if (edge) {
+#pragma unroll
+                    for (int i = 64; i < kRgTile; ++i) s[i] = t0 + i <= lim ? s[i] : -INFINITY;
+                }
+                top = fmaxf(top, max64(s + 64)) * p.scale_log2;
+                const bool up = top > m + kRgSlack;
+                const float mn = up ? top : m, ref = mn == -INFINITY ? 0.f : mn;
+                const float2 scale = make_float2(p.scale_log2, p.scale_log2), neg = make_float2(-ref, -ref);
+                float2 sum[4] = {};
+                // With P apart, the product before has read it and O_X is settled only once
+                // it is done; otherwise these scores came after it.
+                if (RS::kApart) {
+                    if (nd > 0) ok = wait(pv_done + 8 * x, nd - 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    ++nd;
+                    if (!ok) continue;
+                    tc_fence_after();
+                }
+                if (j > 0 && __any_sync(0xffffffffu, up)) {
+                    const float a = up ? fast_exp2(m - ref) : 1.f;
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(o_t + c, o);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+                        tmem_st16(o_t + c, o);
+                    }
+                }
+                if (up) l *= fast_exp2(m - ref);
+                m = mn;
+                rg_weights<0, kRgFirst>(s, scale, neg, sum, p_t);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + 8 * x);
+                rg_weights<kRgFirst, kRgTile>(s, scale, neg, sum, p_t);
+                sum[0] = add_x2(add_x2(sum[0], sum[1]), add_x2(sum[2], sum[3]));
+                l += sum[0].x + sum[0].y;
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_rest + 8 * x);
+            }
+            // The unit before has been read from here once its O is given back.
+            if (!*abort_flag) wait(o_empty + 8 * x, nu ^ 1);
+            ml[x * 128 + row] = make_float2(m, l);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ml_full + 8 * x);
+            ++nu;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D, bool PAGED>
+cudaError_t launch_ragged(const RaggedLaunch& a) {
+    using RS = RgShape<D>;
+    // The shared-memory opt-in is per function and per device.
+    static std::atomic<unsigned long long> attr_set_mask{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(attr_set_mask.load() & bit)) {
+        e = cudaFuncSetAttribute(gqa_ragged_kernel<D, PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 RS::kSmemBytes);
+        if (e != cudaSuccess) return e;
+        attr_set_mask.fetch_or(bit);
+    }
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.grid);
+    cfg.blockDim = dim3(kRgThreads);
+    cfg.dynamicSmemBytes = RS::kSmemBytes;
+    cfg.stream = a.stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, gqa_ragged_kernel<D, PAGED>, a.tm_q, a.tm_k, a.tm_v, a.p);
+}
+
+}  // namespace gqa

@@ -1,0 +1,146 @@
+// How the attention of a packed batch is shared out over the CTAs. Plain
+// arithmetic, the same on the device and on the host.
+//
+// A unit is (sequence, KV head, pair of 128-row tiles): 2 * tq new tokens, each
+// with the H / G rows of its heads. Its length is the keys that its last token
+// sees, plus a pad for what its start and end cost. All units lie end to end,
+// sequence by sequence, KV head by KV head, and every CTA takes an equal share of
+// that line. Where a boundary between shares falls inside a unit, its key tiles
+// are cut there; the parts are merged afterwards.
+#pragma once
+
+#include <cstdint>
+
+#ifndef __CUDACC__
+#define __host__
+#define __device__
+#define __forceinline__ inline
+#endif
+
+namespace gqa {
+
+constexpr int kRgTile = 128;          // rows of a tile, and keys of a key tile
+constexpr int kRgPad = 128;           // what a unit counts beyond its keys
+constexpr int kRgMinShare = 512;      // least share of a CTA, in keys
+constexpr int kRgMinPart = 2;         // least key tiles of a part of a unit
+
+struct RgSeq {
+    int start, n, T;                  // first row, new tokens, keys
+};
+
+struct RgUnit {
+    int seq, g;
+    int row0;                         // first token's row
+    int tokens[2];                    // of tiles A and B
+    int pos0;                         // position of the first token (below 0: sees nothing)
+    int pos_last;                     // and of the last
+    int key0;                         // packed: row of the sequence's first token
+    int j0;                           // first key tile of this part
+    int tiles[2];                     // key tiles of this part that A and B see
+    int slot;                         // workspace slot of this part, -1: the unit is whole
+    int first, parts;                 // CTAs [first, first + parts) hold the unit's parts
+    int counter;                      // of the unit's arrivals
+    int valid;                        // 0: no more units
+};
+static_assert(sizeof(RgUnit) == 64, "a unit is read as 16-byte words");
+
+// Sizes that the line depends on: tokens of a tile, KV heads.
+struct RgLine {
+    int tq, G;
+
+    __host__ __device__ int pairs(int n) const { return (int)(((long long)n + 2 * tq - 1) / (2 * tq)); }
+    __host__ __device__ static int base(const RgSeq& s) { return s.T > s.n ? s.T - s.n : 0; }
+    // Where pair pr of a KV head starts, from the head's start.
+    __host__ __device__ long long start(const RgSeq& s, int pr) const {
+        return (long long)pr * (base(s) + kRgPad) + (long long)tq * pr * (pr + 1ll);
+    }
+    __host__ __device__ long long length(const RgSeq& s, int pr) const {
+        const long long seen = (pr + 1ll) * 2 * tq;
+        return base(s) + kRgPad + (seen < s.n ? seen : s.n);
+    }
+    // Of one KV head.
+    __host__ __device__ long long head(const RgSeq& s) const {
+        const int P = pairs(s.n);
+        return P == 0 ? 0 : start(s, P - 1) + length(s, P - 1);
+    }
+    __host__ __device__ int pair_at(const RgSeq& s, long long y) const {
+        int lo = 0, hi = pairs(s.n) - 1;
+        while (lo < hi) {
+            const int mid = lo + (hi - lo + 1) / 2;
+            if (start(s, mid) <= y) lo = mid; else hi = mid - 1;
+        }
+        return lo;
+    }
+};
+
+// The shares: CTA c takes [at(c), at(c + 1)) of the line.
+struct RgShares {
+    long long each, more;             // `more` CTAs take one key more
+    int ctas;
+
+    __host__ __device__ static RgShares of(long long total, int grid) {
+        long long c = total / kRgMinShare;
+        if (c > grid) c = grid;
+        if (c < 1) c = 1;
+        return {total / c, total % c, (int)c};
+    }
+    __host__ __device__ long long at(int c) const { return each * c + (c < more ? c : more); }
+    __host__ __device__ int holder(long long x) const {
+        const long long wide = more * (each + 1);
+        return (int)(x < wide ? x / (each + 1) : more + (x - wide) / each);
+    }
+};
+
+// Fills the part of unit (s, g, pr), which starts at `at` on the line, that CTA c
+// takes; false if it takes none.
+__host__ __device__ __forceinline__ bool rg_unit(const RgLine& line, const RgShares& sh, int c, const RgSeq& s, int pr,
+                                                 long long at, RgUnit* u) {
+    const int q2 = 2 * line.tq;
+    const int left = s.n - pr * q2;
+    const int a = left < line.tq ? left : line.tq;
+    const int b = left < q2 ? left - a : line.tq;
+    const int pos0 = s.T - s.n + pr * q2;
+    const int lim_a = pos0 + a - 1, lim_b = pos0 + a + b - 1;
+    const int tiles_a = lim_a < 0 ? 0 : lim_a / kRgTile + 1;
+    const int tiles_b = b == 0 || lim_b < 0 ? 0 : lim_b / kRgTile + 1;
+    const int tiles = tiles_b > tiles_a ? tiles_b : tiles_a;
+    const long long len = line.length(s, pr);
+    // Key tile that a boundary x cuts at. Parts below kRgMinPart tiles go to the neighbour.
+    auto cut = [&](long long x) {
+        const long long y = x - at;
+        if (y <= 0) return 0;
+        if (y >= len) return tiles;
+        const long long t = (y + kRgTile / 2) / kRgTile;
+        if (t < kRgMinPart) return 0;
+        return t > tiles - kRgMinPart ? tiles : (int)t;
+    };
+    const int j0 = cut(sh.at(c)), j1 = cut(sh.at(c + 1));
+    if (tiles == 0 ? sh.holder(at) != c : j0 >= j1) return false;
+    u->row0 = s.start + pr * q2;
+    u->tokens[0] = a;
+    u->tokens[1] = b;
+    u->pos0 = pos0;
+    u->pos_last = lim_b;
+    u->key0 = s.start;
+    u->j0 = j0;
+    const int ea = tiles_a < j1 ? tiles_a : j1, eb = tiles_b < j1 ? tiles_b : j1;
+    u->tiles[0] = ea > j0 ? ea - j0 : 0;
+    u->tiles[1] = eb > j0 ? eb - j0 : 0;
+    u->slot = -1;
+    u->first = c;
+    u->parts = 1;
+    u->counter = 0;
+    u->valid = 1;
+    if (tiles > 0 && (j0 > 0 || j1 < tiles)) {
+        int first = sh.holder(at), last = sh.holder(at + len - 1);
+        while (cut(sh.at(first + 1)) == 0) ++first;
+        while (cut(sh.at(last)) == tiles) --last;
+        u->slot = 2 * c + (at < sh.at(c) ? 0 : 1);
+        u->first = first;
+        u->parts = last - first + 1;
+        u->counter = 2 * first + (at < sh.at(first) ? 0 : 1);
+    }
+    return true;
+}
+
+}  // namespace gqa

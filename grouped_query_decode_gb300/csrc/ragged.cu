@@ -1,82 +1,16 @@
-// Attention of packed batches (gqa_prefill_packed, gqa_prefill_paged): a warp per
-// query row, 32 keys at a time, one key per lane for the scores and D / 32 columns
-// per lane for the product with V.
+// C ABI of the attention of packed batches (gqa_prefill_packed, gqa_prefill_paged):
+// argument checks, TMA descriptors and the launch. The kernels are in
+// gqa_ragged.cuh.
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
 #include "gqa_decode.h"
-#include "gqa_device.cuh"
 #include "gqa_launch.h"
+#include "gqa_ragged.h"
 
 namespace gqa {
 namespace {
-
-struct RaggedParams {
-    const uint16_t *q, *k, *v;
-    uint16_t* out;
-    float* lse;
-    const int32_t *cu, *lens, *table;    // lens, table: paged only
-    long long q_stride, k_stride, v_stride;
-    float scale;
-    int N, B, H, G, page_shift, num_pages, max_pages;
-};
-
-template <int D>
-__global__ void __launch_bounds__(256) ragged_kernel(const RaggedParams p) {
-    __shared__ float q_s[8][D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 8 + warp;
-    pdl_launch_dependents();
-    pdl_wait_primary();
-    if (row >= (long long)p.N * p.H) return;
-    const int n = (int)(row / p.H), h = (int)(row % p.H), g = h / (p.H / p.G);
-    int b = 0;
-    while (b < p.B && !(p.cu[b] <= n && n < p.cu[b + 1])) ++b;
-    if (b == p.B) return;
-    const int first = p.cu[b], end = min(p.cu[b + 1], p.N);
-    const int T = p.table ? clamp_len(p.lens[b], p.max_pages << p.page_shift) : end - first;
-    const int lim = T - end + n;
-    for (int d = lane; d < D; d += 32)
-        q_s[warp][d] = __uint_as_float((uint32_t)p.q[n * p.q_stride + h * D + d] << 16) * (p.scale * 1.4426950408889634f);
-    __syncwarp();
-    auto key = [&](int t) -> long long {      // element of position t's row in k and v, -1: reads as zeros
-        if (!p.table) return -2;
-        const int page = p.table[(size_t)b * p.max_pages + (t >> p.page_shift)];
-        if ((unsigned)page >= (unsigned)p.num_pages) return -1;
-        return ((((long long)page * p.G + g) << p.page_shift) + (t & ((1 << p.page_shift) - 1))) * D;
-    };
-    float m = -INFINITY, l = 0.f, o[D / 32] = {};
-    for (int t0 = 0; t0 <= lim; t0 += 32) {
-        const int t = t0 + lane;
-        const bool see = t <= lim;
-        const long long at = see ? key(t) : -1;
-        float x = see ? 0.f : -INFINITY;
-        if (see && at != -1) {
-            const uint16_t* k = p.table ? p.k + at : p.k + (first + t) * p.k_stride + g * D;
-            for (int d = 0; d < D; ++d) x = fmaf(__uint_as_float((uint32_t)k[d] << 16), q_s[warp][d], x);
-        }
-        float top = x;
-        for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-        const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.f : mn;
-        const float a = exp2f(m - base), e = see ? exp2f(x - base) : 0.f;
-        l = l * a + e;
-        m = mn;
-        for (int i = 0; i < D / 32; ++i) o[i] *= a;
-        for (int j = 0; j < 32 && t0 + j <= lim; ++j) {
-            const float pj = __shfl_sync(0xffffffffu, e, j);
-            const long long vj = __shfl_sync(0xffffffffu, at, j);
-            if (vj == -1) continue;
-            const uint16_t* v = p.table ? p.v + vj : p.v + (first + t0 + j) * p.v_stride + g * D;
-            for (int i = 0; i < D / 32; ++i)
-                o[i] = fmaf(pj, __uint_as_float((uint32_t)v[i * 32 + lane] << 16), o[i]);
-        }
-    }
-    for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
-    for (int i = 0; i < D / 32; ++i)
-        p.out[row * D + i * 32 + lane] = (uint16_t)pack_bf16x2(l == 0.f ? 0.f : o[i] / l, 0.f);
-    if (p.lse && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-}
 
 bool aligned(const void* x, unsigned mask) { return (reinterpret_cast<uintptr_t>(x) & mask) == 0; }
 
@@ -84,7 +18,7 @@ int check_sizes(int N, int B, int H, int G, int D) {
     if (N < 0 || B <= 0 || H <= 0 || G <= 0 || D <= 0) return GQA_ERR_INVALID_ARG;
     if (H % G != 0) return GQA_ERR_HEAD_RATIO;
     if (D != 64 && D != 128) return GQA_ERR_UNSUPPORTED;
-    if (H / G > 128 || (long long)N * H >= (1ll << 31) || B >= (1 << 24) || G >= (1 << 20)) return GQA_ERR_UNSUPPORTED;
+    if (H / G > 128 || (long long)N * H >= (1ll << 31) || B >= (1 << 24) || (long long)B * G >= (1 << 30)) return GQA_ERR_UNSUPPORTED;
     return GQA_OK;
 }
 
@@ -94,16 +28,45 @@ int check_rows(const void* x, long long stride, int heads, int D) {
     return stride >= (1ll << 38) ? GQA_ERR_UNSUPPORTED : GQA_OK;
 }
 
-size_t workspace_need(int N, int B, int H, int G, int D, int sms) { return 256; }
+// One CTA per SM; the device's plan gives work to as many as there is work for.
+size_t workspace_need(int D, int grid) { return rg_counter_bytes(grid) + sizeof(float) * 2 * grid * rg_slot_floats(D); }
 
-int launch(RaggedParams& p, int D, cudaStream_t stream) {
-    const long long rows = (long long)p.N * p.H;
-    const unsigned grid = (unsigned)((rows + 7) / 8);
-    if (D == 64)
-        ragged_kernel<64><<<grid, 256, 0, stream>>>(p);
-    else
-        ragged_kernel<128><<<grid, 256, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
+struct Call {
+    RaggedLaunch a = {};
+};
+
+// Fills what both calls share; q's descriptor, workspace and knobs.
+int begin(Call& c, const void* q, const int32_t* cu, float scale, void* out, float* lse, int N, int B, int H, int G,
+          int D, long long q_stride, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+    int sms;
+    RaggedParams& p = c.a.p;
+    int st = current_device(&sms, &p.status);
+    if (st != GQA_OK) return st;
+    c.a.grid = sms;
+    if (!workspace || workspace_bytes < workspace_need(D, sms) || !aligned(workspace, 255u)) return GQA_ERR_WORKSPACE;
+    const int r = H / G, tq = 128 / r;
+    if ((st = encode_rows_map(&c.a.tm_q, q, N, H, D, q_stride, r, tq)) != GQA_OK) return st;
+    p.cu = cu;
+    p.out = static_cast<uint16_t*>(out);
+    p.lse = lse;
+    p.counters = static_cast<unsigned long long*>(workspace);
+    p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + rg_counter_bytes(sms));
+    p.tag = call_tag();
+    wait_knobs(&p.wait_timeout_ns, &p.skip_tile);
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.N = N;
+    p.B = B;
+    p.H = H;
+    p.G = G;
+    p.heads_per_group = r;
+    p.tq = tq;
+    p.by_heads = FastDiv((unsigned)r);
+    c.a.stream = stream;
+    return GQA_OK;
+}
+
+int launch(const Call& c, int D, bool paged) {
+    const cudaError_t e = D == 64 ? launch_ragged_d64(c.a, paged) : launch_ragged_d128(c.a, paged);
     return e == cudaSuccess ? GQA_OK : remember_cuda_error(e);
 }
 
@@ -119,7 +82,7 @@ size_t gqa_prefill_ragged_workspace_bytes(int N, int B, int H, int G, int D) {
     int sms;
     unsigned* status;
     if (current_device(&sms, &status) != GQA_OK) return 0;
-    return workspace_need(N, B, H, G, D, sms);
+    return workspace_need(D, sms);
 }
 
 int gqa_prefill_packed(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, float scale,
@@ -134,28 +97,12 @@ int gqa_prefill_packed(const void* q, const void* k, const void* v, const int32_
         (st = check_rows(v, v_stride, G, D)) != GQA_OK)
         return st;
     if (!aligned(out, 15u) || !aligned(cu_seqlens, 3u) || !aligned(lse, 3u)) return GQA_ERR_MISALIGNED;
-    int sms;
-    unsigned* status;
-    st = current_device(&sms, &status);
+    Call c;
+    st = begin(c, q, cu_seqlens, scale, out, lse, N, B, H, G, D, q_stride, workspace, workspace_bytes, stream);
     if (st != GQA_OK) return st;
-    if (!workspace || workspace_bytes < workspace_need(N, B, H, G, D, sms) || !aligned(workspace, 255u))
-        return GQA_ERR_WORKSPACE;
-    RaggedParams p = {};
-    p.q = static_cast<const uint16_t*>(q);
-    p.k = static_cast<const uint16_t*>(k);
-    p.v = static_cast<const uint16_t*>(v);
-    p.out = static_cast<uint16_t*>(out);
-    p.lse = lse;
-    p.cu = cu_seqlens;
-    p.q_stride = q_stride;
-    p.k_stride = k_stride;
-    p.v_stride = v_stride;
-    p.scale = scale;
-    p.N = N;
-    p.B = B;
-    p.H = H;
-    p.G = G;
-    return launch(p, D, stream);
+    if ((st = encode_rows_map(&c.a.tm_k, k, N, G, D, k_stride, 1, 128)) != GQA_OK) return st;
+    if ((st = encode_rows_map(&c.a.tm_v, v, N, G, D, v_stride, 1, 128)) != GQA_OK) return st;
+    return launch(c, D, false);
 }
 
 int gqa_prefill_paged(const void* q, const void* k_pages, const void* v_pages, const int32_t* block_table,
@@ -175,31 +122,20 @@ int gqa_prefill_paged(const void* q, const void* k_pages, const void* v_pages, c
     if (!aligned(k_pages, 15u) || !aligned(v_pages, 15u) || !aligned(out, 15u) || !aligned(block_table, 3u) ||
         !aligned(cu_new, 3u) || !aligned(seq_lens, 3u) || !aligned(lse, 3u))
         return GQA_ERR_MISALIGNED;
-    int sms;
-    unsigned* status;
-    st = current_device(&sms, &status);
+    Call c;
+    st = begin(c, q, cu_new, scale, out, lse, N, B, H, G, D, q_stride, workspace, workspace_bytes, stream);
     if (st != GQA_OK) return st;
-    if (!workspace || workspace_bytes < workspace_need(N, B, H, G, D, sms) || !aligned(workspace, 255u))
-        return GQA_ERR_WORKSPACE;
-    RaggedParams p = {};
-    p.q = static_cast<const uint16_t*>(q);
-    p.k = static_cast<const uint16_t*>(k_pages);
-    p.v = static_cast<const uint16_t*>(v_pages);
-    p.out = static_cast<uint16_t*>(out);
-    p.lse = lse;
-    p.cu = cu_new;
+    const long long slabs = (long long)num_pages * G;
+    const int box = page_size < 128 ? page_size : 128;
+    if ((st = encode_page_map(&c.a.tm_k, k_pages, slabs, page_size, D, box)) != GQA_OK) return st;
+    if ((st = encode_page_map(&c.a.tm_v, v_pages, slabs, page_size, D, box)) != GQA_OK) return st;
+    RaggedParams& p = c.a.p;
     p.lens = seq_lens;
     p.table = block_table;
-    p.q_stride = q_stride;
-    p.scale = scale;
-    p.N = N;
-    p.B = B;
-    p.H = H;
-    p.G = G;
     p.page_shift = __builtin_ctz((unsigned)page_size);
     p.num_pages = num_pages;
     p.max_pages = max_pages_per_seq;
-    return launch(p, D, stream);
+    return launch(c, D, true);
 }
 
 }  // extern "C"

@@ -48,6 +48,12 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr, uint32_t lbo,
            ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
 }
 
+// The same without the address, to which (address >> 4) is added.
+__host__ __device__ constexpr uint64_t smem_desc_base(uint32_t lbo, uint32_t sbo) {
+    return ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) | ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) |
+           (2ull << 61);
+}
+
 // Instruction descriptor of kind::f16 with bf16 A and B and an fp32
 // accumulator; a_mn / b_mn select MN-major operands; M in {64, 128}, N a
 // multiple of 16 up to 256.

@@ -455,3 +455,22 @@ def test_a_captured_serving_step():
             assert ((k[T[b] - n:].double() - want[0]).abs() <= model.rotate_bound(*want)).all()
             model.check_rows(out[first:first + n], None, model.attention(q.cpu()[first:first + n], k, v, n, T[b], 0.1))
             first += n
+
+
+# ------------------------------------------------------- bounded waits
+
+def test_a_tile_that_never_comes():
+    """A load that is left out ends in a status, not in a hang, and leaves the
+    workspace so that the same call is right afterwards."""
+    b = Batch(8, 2, 128, [(1, 3000), (200, 900)], page=64, seed=50).run().check()
+    with env(GQA_DECODE_DEBUG_SKIP_TILE=0, GQA_DECODE_DEBUG_TIMEOUT_MS=50, GQA_DECODE_DEBUG_EPOCH=77):
+        b.call()
+        assert gq.gqa_decode_check_error() == gq.GQA_ERR_DEVICE_TIMEOUT
+    with env(GQA_DECODE_DEBUG_EPOCH=77):
+        for _ in range(2):
+            b.out.fill_(7)
+            b.lse.fill_(7)
+            b.call()
+            torch.cuda.synchronize()
+            assert gq.gqa_decode_check_error() == gq.GQA_OK
+            b.check()
