@@ -61,6 +61,7 @@ struct RgShape {
     static constexpr bool kApart = D == 64;
     static constexpr uint32_t kColS = 0, kColP = kApart ? 256 : 0, kStepP = kApart ? 64 : 128, kColO = kApart ? 384 : 256;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
+    static_assert(kStages * kTile >= (30 * 1024 + 256) * 4, "the merge's weights");
 };
 
 template <int N>
@@ -131,40 +132,103 @@ __device__ __forceinline__ RgSeq rg_sequence(const RaggedParams& p, int b) {
     return s;
 }
 
-// Merges the parts of a unit: M = max m, L = sum l 2^(m - M), O = sum O 2^(m - M) / L,
-// part by part in their order. A warp per row.
+template <int V>
+struct RgInt {
+    static constexpr int value = V;
+};
+
+// Merges the parts of a unit: M = max m, w = 2^(m - M), L = sum l w, O = sum O w / L,
+// part by part in their order, with all threads of the CTA. `weights` holds
+// kRgWeights floats, `inverse` 256.
+constexpr int kRgWeights = 30 * 1024;
 template <int D>
-__device__ __noinline__ void rg_merge(const RaggedParams& p, const RgUnit& u, int warp, int lane) {
-    constexpr int kPer = D / 32;
-    auto at = [&](int i) {
-        const int c = u.first + i;
-        // The first part is in the slot of its CTA's units that go on, or, where an
-        // earlier CTA had none, of those that came from before: its counter's.
-        return p.part + (size_t)(i == 0 ? u.counter : 2 * c) * rg_slot_floats(D);
+__device__ __forceinline__ void rg_merge(const RaggedParams& p, const RgUnit& u, float* weights, float* inverse) {
+    constexpr int kChunks = D / 4;
+    const int n = u.parts, rows_a = u.tokens[0] * p.heads_per_group, rows = rows_a + u.tokens[1] * p.heads_per_group;
+    // The first part's slot is its counter's; later ones continue from the CTA before.
+    auto part = [&](int i) { return p.part + (size_t)(i == 0 ? u.counter : 2 * (u.first + i)) * rg_slot_floats(D); };
+    auto out_row = [&](int r) {                  // r counts A's rows, then B's
+        const int x = r >= rows_a, tok = p.by_heads(x ? r - rows_a : r);
+        return (size_t)(u.row0 + x * p.tq + tok) * p.H + (size_t)u.g * p.heads_per_group +
+               ((x ? r - rows_a : r) - tok * p.heads_per_group);
     };
-    for (int x = 0; x < 2; ++x) {
-        const int rows = u.tokens[x] * p.heads_per_group;
-        for (int row = warp; row < rows; row += 4) {
-            const int r = x * 128 + row;
-            float M = -INFINITY, L = 0.f, o[kPer] = {};
-            for (int i = 0; i < u.parts; ++i) {
-                const float* part = at(i);
-                const float m = __ldcg(part + 256 * D + r), l = __ldcg(part + 256 * D + 256 + r);
-                if (l == 0.f) continue;
-                const float top = fmaxf(M, m), a = fast_exp2(M - top), w = fast_exp2(m - top);
-                M = top;
-                L = L * a + l * w;
-                for (int k = 0; k < kPer; ++k) o[k] = o[k] * a + __ldcg(part + (size_t)r * D + lane * kPer + k) * w;
+    auto slot_row = [&](int r) { return r < rows_a ? r : 128 + r - rows_a; };
+    const int block = min(rows, kRgWeights / n);  // rows whose weights fit
+    for (int r0 = 0; r0 < rows; r0 += block) {
+        const int r1 = min(rows, r0 + block);
+        // Lanes in groups of `width` take a row each, a lane some of its parts.
+        int width = 1;
+        while (width < n && width < 32) width *= 2;
+        const int lane = threadIdx.x & 31, k = lane % width;
+        for (int first = r0 + (int)(threadIdx.x >> 5) * (32 / width); first < r1; first += kRgThreads / width) {
+            const int r = first + lane / width, s = slot_row(min(r, r1 - 1));
+            float M = -INFINITY;
+            for (int i = k; i < n; i += width) M = fmaxf(M, __ldcg(part(i) + 256 * D + s));
+            for (int o = width / 2; o > 0; o /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            float L = 0.f;
+            for (int i = k; i < n; i += width) {
+                const float l = __ldcg(part(i) + 256 * D + 256 + s);
+                const float w = l == 0.f ? 0.f : fast_exp2(__ldcg(part(i) + 256 * D + s) - M);
+                if (r < r1) weights[(r - r0) * n + i] = w;
+                L += l * w;
             }
-            const int tok = p.by_heads(row);
-            const size_t orow = (size_t)(u.row0 + x * p.tq + tok) * p.H + (size_t)u.g * p.heads_per_group +
-                                (row - tok * p.heads_per_group);
-            const float inv = L == 0.f ? 0.f : 1.f / L;
-            uint16_t* dst = p.out + orow * D + lane * kPer;
-            for (int k = 0; k < kPer; k += 2)
-                *reinterpret_cast<uint32_t*>(dst + k) = L == 0.f ? 0u : pack_bf16x2(o[k] * inv, o[k + 1] * inv);
-            if (p.lse && lane == 0) p.lse[orow] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+            for (int o = width / 2; o > 0; o /= 2) L += __shfl_xor_sync(0xffffffffu, L, o);
+            if (k == 0 && r < r1) {
+                inverse[r - r0] = L == 0.f ? 0.f : 1.f / L;
+                if (p.lse) p.lse[out_row(r)] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+            }
         }
+        __syncthreads();
+        // A thread's four columns of some rows; I items and P parts of each under way at once.
+        auto sum = [&](auto items, auto parts) {
+            constexpr int I = decltype(items)::value, P = decltype(parts)::value;
+            for (int first = threadIdx.x; first < (r1 - r0) * kChunks; first += I * kRgThreads) {
+                float4 y[I];
+#pragma unroll
+                for (int j = 0; j < I; ++j) y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int i0 = 0; i0 < n; i0 += P) {
+                    float4 v[I][P];
+                    float w[I][P];
+#pragma unroll
+                    for (int j = 0; j < I; ++j)
+#pragma unroll
+                        for (int i = 0; i < P; ++i) {
+                            const int item = first + j * kRgThreads, r = item / kChunks;
+                            w[j][i] = 0.f;
+                            v[j][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (i0 + i < n && r < r1 - r0) {
+                                w[j][i] = weights[r * n + i0 + i];
+                                // Rows without a key in a part have left no O there.
+                                if (w[j][i] != 0.f)
+                                    v[j][i] = __ldcg(reinterpret_cast<const float4*>(part(i0 + i) + (size_t)slot_row(r0 + r) * D) +
+                                                     item % kChunks);
+                            }
+                        }
+#pragma unroll
+                    for (int j = 0; j < I; ++j)
+#pragma unroll
+                        for (int i = 0; i < P; ++i) {
+                            y[j].x = fmaf(v[j][i].x, w[j][i], y[j].x);
+                            y[j].y = fmaf(v[j][i].y, w[j][i], y[j].y);
+                            y[j].z = fmaf(v[j][i].z, w[j][i], y[j].z);
+                            y[j].w = fmaf(v[j][i].w, w[j][i], y[j].w);
+                        }
+                }
+#pragma unroll
+                for (int j = 0; j < I; ++j) {
+                    const int item = first + j * kRgThreads, r = item / kChunks;
+                    if (r >= r1 - r0) continue;
+                    const float f = inverse[r];
+                    *(reinterpret_cast<uint2*>(p.out + out_row(r0 + r) * D) + item % kChunks) =
+                        make_uint2(pack_bf16x2(y[j].x * f, y[j].y * f), pack_bf16x2(y[j].z * f, y[j].w * f));
+                }
+            }
+        };
+        if ((r1 - r0) * kChunks >= 4 * kRgThreads)
+            sum(RgInt<4>(), RgInt<2>());
+        else
+            sum(RgInt<1>(), RgInt<8>());
+        __syncthreads();
     }
 }
 
@@ -189,10 +253,11 @@ __global__ void __launch_bounds__(kRgThreads, 1)
     gen += RS::kUnitBytes;
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gen);
     volatile int* const abort_flag = reinterpret_cast<volatile int*>(gen + 4);
-    volatile int* const last_flag = reinterpret_cast<volatile int*>(gen + 8);
+    volatile int* const todos = reinterpret_cast<volatile int*>(gen + 8);
     int* const bad_flag = reinterpret_cast<int*>(gen + 16);          // [units]
     long long* const first_s = reinterpret_cast<long long*>(gen + 64);   // total; sequence and offset of the share's start
     long long* const warp_sum = reinterpret_cast<long long*>(gen + 128); // [16]
+    RgUnit* const todo = reinterpret_cast<RgUnit*>(gen + 256);       // [2]: units to merge
     gen += RS::kMiscBytes;
     const uint32_t full = smem_addr(gen), empty = full + 8 * S, mended = empty + 8 * S;
     const uint32_t q_full = mended + 8 * S, q_empty = q_full + 16, s_full = q_empty + 16, p_full = s_full + 16;
@@ -228,6 +293,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
         }
         for (int i = 0; i < kRgUnits; ++i) bad_flag[i] = 0;
         *abort_flag = 0;
+        *todos = 0;
         first_s[1] = p.B;
         fence_barrier_init();
     }
@@ -718,13 +784,11 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 }
             }
             if (slot >= 0) {
-                // The last part to arrive merges all. The barrier orders the parts' stores
-                // before the arrival, which releases them.
+                // The CTA whose part arrives last merges the unit, once it has no other work:
+                // its own part of a unit that goes on in the next CTA is its last one. The
+                // barrier orders the part's stores before the arrival, which releases them.
                 named_sync(1, 128);
-                if (row == 0) *last_flag = arrive_last(p.counters + u.counter, p.tag, u.parts);
-                named_sync(1, 128);
-                if (*last_flag) rg_merge<D>(p, u, warp & 3, lane);
-                named_sync(1, 128);
+                if (row == 0 && arrive_last(p.counters + u.counter, p.tag, u.parts)) todo[(*todos)++] = u;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(u_empty + 8 * (n % kRgUnits));
@@ -839,12 +903,17 @@ __global__ void __launch_bounds__(kRgThreads, 1)
         }
     }
 
+    // All threads merge, with as many registers as at the start.
+    __syncwarp();
+    if (warp < 8) fewer_registers<128>(); else more_registers<128>();
     tc_fence_before();
     __syncthreads();
     if (warp == 12) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    float* const scratch = reinterpret_cast<float*>(smem_raw + (ring_s - raw));     // all copies have landed
+    for (int i = 0; i < *todos; ++i) rg_merge<D>(p, todo[i], scratch, scratch + kRgWeights);
 }
 
 template <int D, bool PAGED>
