@@ -580,80 +580,100 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(u_empty + 8 * (n % kRgUnits));
             }
-        } else if (lane == 0) {
+        } else {
             // -------------------------------------------------------- products
+            // The warp waits as a whole and one thread issues; what the instructions
+            // take is made uniform (from a single thread's own registers every
+            // product waits for its operands' way to the uniform ones).
             constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
             constexpr uint32_t kIdescO = idesc_bf16_f32(128, D, false, true);
+            constexpr uint64_t kDescK = smem_desc_base(16, 1024), kDescV = smem_desc_base(kBlock, 1024);
             struct Now {
                 int a, b, all, j0, lim;          // key tiles of A, B, both
                 uint32_t it;
             } u = {0, 0, 1, 0, 0, 0}, next = u;  // a unit without tiles leads in the first
             uint32_t n = 0, it = 0, phases = 0, mends = 0;
             bool ok = true, issued = false;
+            const uint32_t tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
+            auto uniform = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
+            auto wait_warp = [&](uint32_t bar, uint32_t parity) {
+                if (ok) ok = __all_sync(0xffffffffu, wait(bar, parity)) != 0;
+            };
             auto wait_next = [&](uint32_t bar, int bit, uint32_t flip) {
-                ok = ok && wait(bar, (phases >> bit) ^ flip);
+                wait_warp(bar, (phases >> bit) ^ flip);
                 phases ^= 1u << bit;
             };
             // The next unit with key tiles.
             auto fetch = [&]() {
                 while (next_unit(n)) {
+                    __syncwarp();
                     const RgUnit& f = units[n % kRgUnits];
                     if (!f.valid) return false;
                     next = {f.tiles[0], f.tiles[1], max(f.tiles[0], f.tiles[1]), f.j0, f.pos0, it};
-                    mbar_arrive(u_empty + 8 * (n % kRgUnits));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(u_empty + 8 * (n % kRgUnits));
                     ++n;
                     it += 2 * next.all;
                     if (next.all > 0) return true;
                 }
                 return false;
             };
-            constexpr uint64_t kDescK = smem_desc_base(16, 1024), kDescV = smem_desc_base(kBlock, 1024);
             // S_X of the K tile at ring place i.
             auto scores = [&](uint32_t i, int x, bool first, bool last, bool release) {
                 const uint32_t s = i % S;
                 if (first) wait_next(q_full + 8 * x, x, 0);
                 if (RS::kApart) wait_next(s_free + 8 * x, 6 + x, 1);
-                ok = ok && wait(full + 8 * s, i / S);
+                wait_warp(full + 8 * s, i / S);
                 if (!ok) return;
                 tc_fence_after();
-                const uint64_t a = kDescK + ((q_s + x * kTile) >> 4), b = kDescK + ((ring_s + s * kTile) >> 4);
-                const uint32_t to = tmem + RS::kColS + x * 128;
+                const uint32_t su = uniform(s), xu = uniform(x), end = uniform(last | (release ? 2 : 0));
+                if (elect_one()) {
+                    const uint64_t a = kDescK + ((q_s + xu * kTile) >> 4), b = kDescK + ((ring_s + su * kTile) >> 4);
+                    const uint32_t to = tmem_u + RS::kColS + xu * 128;
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = ((k >> 2) * kBlock + (k & 3) * 32) >> 4;
-                    umma_bf16(to, a + off, b + off, kIdescS, k > 0 ? 1u : 0u);
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = ((k >> 2) * kBlock + (k & 3) * 32) >> 4;
+                        umma_bf16(to, a + off, b + off, kIdescS, k > 0 ? 1u : 0u);
+                    }
+                    umma_commit(s_full + 8 * xu);
+                    if (end & 1) umma_commit(q_empty + 8 * xu);
+                    if (end & 2) umma_commit(empty + 8 * su);
                 }
+                __syncwarp();
                 issued = true;
-                umma_commit(s_full + 8 * x);
-                if (last) umma_commit(q_empty + 8 * x);
-                if (release) umma_commit(empty + 8 * s);
             };
             // O_X += P_X V for the V tile at ring place i.
             auto values = [&](uint32_t i, int x, bool fresh, bool mend, bool first, bool last, bool release) {
                 const uint32_t s = i % S;
                 if (fresh) {
-                    ok = ok && wait((mend ? mended : full) + 8 * s, mend ? mends >> s : i / S);
+                    wait_warp((mend ? mended : full) + 8 * s, mend ? mends >> s : i / S);
                     if (mend) mends ^= 1u << s;
                 }
                 if (first) wait_next(o_empty + 8 * x, 4 + x, 1);
-                const uint64_t b = kDescV + ((ring_s + s * kTile) >> 4);
-                const uint32_t to = tmem + RS::kColO + x * D, a = tmem + RS::kColP + x * RS::kStepP;
-                ok = ok && wait(p_full + 8 * x, phases >> (2 + x));
+                const uint32_t su = uniform(s), xu = uniform(x), more = uniform(!first), end = uniform(last | (release ? 2 : 0));
+                const uint64_t b = kDescV + ((ring_s + su * kTile) >> 4);
+                const uint32_t to = tmem_u + RS::kColO + xu * D, a = tmem_u + RS::kColP + xu * RS::kStepP;
+                wait_warp(p_full + 8 * x, phases >> (2 + x));
                 if (!ok) return;
                 tc_fence_after();
+                if (elect_one())
 #pragma unroll
-                for (int k = 0; k < kRgTile / 16; ++k) {
-                    if (k == kRgFirst / 16) {
-                        ok = wait(p_rest + 8 * x, phases >> (2 + x));
-                        if (!ok) return;
-                        tc_fence_after();
-                    }
-                    umma_bf16_ts(to, a + k * 8, b + k * (16 * 128 >> 4), kIdescO, (!first || k > 0) ? 1u : 0u);
-                }
+                    for (int k = 0; k < kRgFirst / 16; ++k)
+                        umma_bf16_ts(to, a + k * 8, b + k * (16 * 128 >> 4), kIdescO, k > 0 ? 1u : more);
+                __syncwarp();
+                wait_warp(p_rest + 8 * x, phases >> (2 + x));
                 phases ^= 4u << x;
-                if (RS::kApart) umma_commit(pv_done + 8 * x);
-                if (last) umma_commit(o_full + 8 * x);
-                if (release) umma_commit(empty + 8 * s);
+                if (!ok) return;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = kRgFirst / 16; k < kRgTile / 16; ++k)
+                        umma_bf16_ts(to, a + k * 8, b + k * (16 * 128 >> 4), kIdescO, 1u);
+                    if (RS::kApart) umma_commit(pv_done + 8 * xu);
+                    if (end & 1) umma_commit(o_full + 8 * xu);
+                    if (end & 2) umma_commit(empty + 8 * su);
+                }
+                __syncwarp();
             };
             bool have = true;
             while (have) {
@@ -686,8 +706,8 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 u = next;
                 have = more;
             }
-            if (issued) {
-                // Every product has completed once this flips.
+            // elect_one picks the same thread each time: its commit covers all products.
+            if (issued && elect_one()) {
                 umma_commit(fin);
                 const uint64_t t0 = global_timer_ns();
                 while (!mbar_try_wait(fin, 0))
@@ -696,6 +716,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                         break;
                     }
             }
+            __syncwarp();
         }
     } else if (warp >= 8) {
         // ---------------------------------------------------------------- outputs
