@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(u_empty + 8 * (n % kRgUnits));
             }
-        } else {
+        } else if (elect_one()) {
             // -------------------------------------------------------- products
             // The warp waits as a whole and one thread issues; what the instructions
             // take is made uniform (from a single thread's own registers every
@@ -594,10 +594,10 @@ __global__ void __launch_bounds__(kRgThreads, 1)
             } u = {0, 0, 1, 0, 0, 0}, next = u;  // a unit without tiles leads in the first
             uint32_t n = 0, it = 0, phases = 0, mends = 0;
             bool ok = true, issued = false;
-            const uint32_t tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
-            auto uniform = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
+            const uint32_t tmem_u = tmem;
+            auto uniform = [](uint32_t v) { return v; };
             auto wait_warp = [&](uint32_t bar, uint32_t parity) {
-                if (ok) ok = __all_sync(0xffffffffu, wait(bar, parity)) != 0;
+                ok = ok && wait(bar, parity);
             };
             auto wait_next = [&](uint32_t bar, int bit, uint32_t flip) {
                 wait_warp(bar, (phases >> bit) ^ flip);
@@ -606,12 +606,10 @@ __global__ void __launch_bounds__(kRgThreads, 1)
             // The next unit with key tiles.
             auto fetch = [&]() {
                 while (next_unit(n)) {
-                    __syncwarp();
                     const RgUnit& f = units[n % kRgUnits];
                     if (!f.valid) return false;
                     next = {f.tiles[0], f.tiles[1], max(f.tiles[0], f.tiles[1]), f.j0, f.pos0, it};
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(u_empty + 8 * (n % kRgUnits));
+                    mbar_arrive(u_empty + 8 * (n % kRgUnits));
                     ++n;
                     it += 2 * next.all;
                     if (next.all > 0) return true;
@@ -627,7 +625,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t su = uniform(s), xu = uniform(x), end = uniform(last | (release ? 2 : 0));
-                if (elect_one()) {
+                {
                     const uint64_t a = kDescK + ((q_s + xu * kTile) >> 4), b = kDescK + ((ring_s + su * kTile) >> 4);
                     const uint32_t to = tmem_u + RS::kColS + xu * 128;
 #pragma unroll
@@ -639,7 +637,6 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                     if (end & 1) umma_commit(q_empty + 8 * xu);
                     if (end & 2) umma_commit(empty + 8 * su);
                 }
-                __syncwarp();
                 issued = true;
             };
             // O_X += P_X V for the V tile at ring place i.
@@ -656,16 +653,15 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 wait_warp(p_full + 8 * x, phases >> (2 + x));
                 if (!ok) return;
                 tc_fence_after();
-                if (elect_one())
+                
 #pragma unroll
                     for (int k = 0; k < kRgFirst / 16; ++k)
                         umma_bf16_ts(to, a + k * 8, b + k * (16 * 128 >> 4), kIdescO, k > 0 ? 1u : more);
-                __syncwarp();
                 wait_warp(p_rest + 8 * x, phases >> (2 + x));
                 phases ^= 4u << x;
                 if (!ok) return;
                 tc_fence_after();
-                if (elect_one()) {
+                {
 #pragma unroll
                     for (int k = kRgFirst / 16; k < kRgTile / 16; ++k)
                         umma_bf16_ts(to, a + k * 8, b + k * (16 * 128 >> 4), kIdescO, 1u);
@@ -673,7 +669,6 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                     if (end & 1) umma_commit(o_full + 8 * xu);
                     if (end & 2) umma_commit(empty + 8 * su);
                 }
-                __syncwarp();
             };
             bool have = true;
             while (have) {
@@ -707,7 +702,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 have = more;
             }
             // elect_one picks the same thread each time: its commit covers all products.
-            if (issued && elect_one()) {
+            if (issued) {
                 umma_commit(fin);
                 const uint64_t t0 = global_timer_ns();
                 while (!mbar_try_wait(fin, 0))
@@ -716,7 +711,6 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                         break;
                     }
             }
-            __syncwarp();
         }
     } else if (warp >= 8) {
         // ---------------------------------------------------------------- outputs
