@@ -52,7 +52,7 @@ struct RgShape {
     static constexpr int kBadBytes = kRgUnits * D * 4;
     static constexpr int kUnitBytes = kRgUnits * 64;
     static constexpr int kMiscBytes = 512;
-    static constexpr int kBars = 3 * kStages + 2 * 10 + 2 * kRgUnits + 1;
+    static constexpr int kBars = 3 * kStages + 2 * 10 + 2 * kRgUnits + 2;
     static constexpr int kSmemBytes =
         1024 + 2 * kTile + kStages * kTile + kMlBytes + kBadBytes + kUnitBytes + kMiscBytes + 8 * kBars;
     // Columns: S_A | S_B | O_A | O_B, with P over the first half of its S; D = 64
@@ -61,7 +61,7 @@ struct RgShape {
     static constexpr bool kApart = D == 64;
     static constexpr uint32_t kColS = 0, kColP = kApart ? 256 : 0, kStepP = kApart ? 64 : 128, kColO = kApart ? 384 : 256;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
-    static_assert(kStages * kTile >= (30 * 1024 + 256) * 4, "the merge's weights");
+    static_assert((2 + kStages) * kTile >= 1024 + 180 * (D * 4 + 4), "one row of all parts");
 };
 
 template <int N>
@@ -132,103 +132,115 @@ __device__ __forceinline__ RgSeq rg_sequence(const RaggedParams& p, int b) {
     return s;
 }
 
-template <int V>
-struct RgInt {
-    static constexpr int value = V;
-};
+// What a wait does when its phase has not completed yet: out of line, because
+// instruction fetches are what short units wait for.
+static __device__ __noinline__ bool rg_wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag, unsigned* status,
+                                          uint64_t tmo) {
+    return wait_phase(bar, parity, abort_flag, status, tmo);
+}
+__device__ __forceinline__ bool rg_wait_longer(uint32_t bar, uint32_t parity, uint64_t limit) {
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (global_timer_ns() - t0 > limit) return false;
+    return true;
+}
 
-// Merges the parts of a unit: M = max m, w = 2^(m - M), L = sum l w, O = sum O w / L,
-// part by part in their order, with all threads of the CTA. `weights` holds
-// kRgWeights floats, `inverse` 256.
-constexpr int kRgWeights = 30 * 1024;
+// 1-D copy into shared memory, completing bytes on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// Merges the parts of a unit with all threads of the CTA: M = max m, w = 2^(m - M),
+// L = sum l w, O = sum O w / L, part by part in their order. As many rows at a time
+// as `room` holds of all parts come into shared memory at once. This runs once or
+// twice per CTA, so its time is latency and instruction fetches: loops are short.
 template <int D>
-__device__ __forceinline__ void rg_merge(const RaggedParams& p, const RgUnit& u, float* weights, float* inverse) {
+__device__ __forceinline__ void rg_merge(const RaggedParams& p, const RgUnit& u, unsigned char* room, uint32_t room_bytes,
+                                         uint32_t bar, uint32_t& phase) {
     constexpr int kChunks = D / 4;
-    const int n = u.parts, rows_a = u.tokens[0] * p.heads_per_group, rows = rows_a + u.tokens[1] * p.heads_per_group;
-    // The first part's slot is its counter's; later ones continue from the CTA before.
-    auto part = [&](int i) { return p.part + (size_t)(i == 0 ? u.counter : 2 * (u.first + i)) * rg_slot_floats(D); };
-    auto out_row = [&](int r) {                  // r counts A's rows, then B's
-        const int x = r >= rows_a, tok = p.by_heads(x ? r - rows_a : r);
-        return (size_t)(u.row0 + x * p.tq + tok) * p.H + (size_t)u.g * p.heads_per_group +
-               ((x ? r - rows_a : r) - tok * p.heads_per_group);
-    };
-    auto slot_row = [&](int r) { return r < rows_a ? r : 128 + r - rows_a; };
-    const int block = min(rows, kRgWeights / n);  // rows whose weights fit
-    for (int r0 = 0; r0 < rows; r0 += block) {
-        const int r1 = min(rows, r0 + block);
-        // Lanes in groups of `width` take a row each, a lane some of its parts.
-        int width = 1;
-        while (width < n && width < 32) width *= 2;
-        const int lane = threadIdx.x & 31, k = lane % width;
-        for (int first = r0 + (int)(threadIdx.x >> 5) * (32 / width); first < r1; first += kRgThreads / width) {
-            const int r = first + lane / width, s = slot_row(min(r, r1 - 1));
-            float M = -INFINITY;
-            for (int i = k; i < n; i += width) M = fmaxf(M, __ldcg(part(i) + 256 * D + s));
-            for (int o = width / 2; o > 0; o /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            float L = 0.f;
-            for (int i = k; i < n; i += width) {
-                const float l = __ldcg(part(i) + 256 * D + 256 + s);
-                const float w = l == 0.f ? 0.f : fast_exp2(__ldcg(part(i) + 256 * D + s) - M);
-                if (r < r1) weights[(r - r0) * n + i] = w;
-                L += l * w;
-            }
-            for (int o = width / 2; o > 0; o /= 2) L += __shfl_xor_sync(0xffffffffu, L, o);
-            if (k == 0 && r < r1) {
-                inverse[r - r0] = L == 0.f ? 0.f : 1.f / L;
-                if (p.lse) p.lse[out_row(r)] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
-            }
-        }
-        __syncthreads();
-        // A thread's four columns of some rows; I items and P parts of each under way at once.
-        auto sum = [&](auto items, auto parts) {
-            constexpr int I = decltype(items)::value, P = decltype(parts)::value;
-            for (int first = threadIdx.x; first < (r1 - r0) * kChunks; first += I * kRgThreads) {
-                float4 y[I];
-#pragma unroll
-                for (int j = 0; j < I; ++j) y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int i0 = 0; i0 < n; i0 += P) {
-                    float4 v[I][P];
-                    float w[I][P];
-#pragma unroll
-                    for (int j = 0; j < I; ++j)
-#pragma unroll
-                        for (int i = 0; i < P; ++i) {
-                            const int item = first + j * kRgThreads, r = item / kChunks;
-                            w[j][i] = 0.f;
-                            v[j][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (i0 + i < n && r < r1 - r0) {
-                                w[j][i] = weights[r * n + i0 + i];
-                                // Rows without a key in a part have left no O there.
-                                if (w[j][i] != 0.f)
-                                    v[j][i] = __ldcg(reinterpret_cast<const float4*>(part(i0 + i) + (size_t)slot_row(r0 + r) * D) +
-                                                     item % kChunks);
-                            }
-                        }
-#pragma unroll
-                    for (int j = 0; j < I; ++j)
-#pragma unroll
-                        for (int i = 0; i < P; ++i) {
-                            y[j].x = fmaf(v[j][i].x, w[j][i], y[j].x);
-                            y[j].y = fmaf(v[j][i].y, w[j][i], y[j].y);
-                            y[j].z = fmaf(v[j][i].z, w[j][i], y[j].z);
-                            y[j].w = fmaf(v[j][i].w, w[j][i], y[j].w);
-                        }
-                }
-#pragma unroll
-                for (int j = 0; j < I; ++j) {
-                    const int item = first + j * kRgThreads, r = item / kChunks;
-                    if (r >= r1 - r0) continue;
-                    const float f = inverse[r];
-                    *(reinterpret_cast<uint2*>(p.out + out_row(r0 + r) * D) + item % kChunks) =
-                        make_uint2(pack_bf16x2(y[j].x * f, y[j].y * f), pack_bf16x2(y[j].z * f, y[j].w * f));
-                }
-            }
+    const int n = u.parts, lane = threadIdx.x & 31;
+    // Lanes in groups of `width` take a row each, a lane some of its parts.
+    int width = 1;
+    while (width < n && width < 32) width *= 2;
+    const int k = lane & (width - 1);
+    const int block = min(128, (int)((room_bytes - 1024) / (n * (D * 4 + 4))));
+    float* const inverse = reinterpret_cast<float*>(room);        // [128]
+    float* const weights = inverse + 128;                         // [block][n]
+    const uint32_t held = (512 + 4 * n * block + 127) & ~127u;    // O of the parts, [n][rows][D]
+#pragma unroll 1
+    for (int x = 0; x < 2; ++x) {
+        const int rows_x = u.tokens[x] * p.heads_per_group;
+        // The first part's slot is its counter's; later ones continue from the CTA before.
+        auto part = [&](int i) {
+            return p.part + (size_t)(i == 0 ? u.counter : 2 * (u.first + i)) * rg_slot_floats(D);
         };
-        if ((r1 - r0) * kChunks >= 4 * kRgThreads)
-            sum(RgInt<4>(), RgInt<2>());
-        else
-            sum(RgInt<1>(), RgInt<8>());
-        __syncthreads();
+        const size_t row_x = (size_t)(u.row0 + x * p.tq) * p.H + (size_t)u.g * p.heads_per_group;
+        auto out_row = [&](int r) {
+            const int tok = p.by_heads(r);
+            return row_x + (size_t)tok * p.H + (r - tok * p.heads_per_group);
+        };
+#pragma unroll 1
+        for (int r0 = 0; r0 < rows_x; r0 += block) {
+            const int rows = min(block, rows_x - r0);
+            if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, n * rows * D * 4);
+            __syncthreads();
+            asm volatile("fence.proxy.async;" ::: "memory");      // the parts were written by plain stores
+#pragma unroll 1
+            for (int i = threadIdx.x; i < n; i += kRgThreads)
+                bulk_load(smem_addr(room) + held + i * rows * D * 4, part(i) + (size_t)(x * 128 + r0) * D, rows * D * 4, bar);
+#pragma unroll 1
+            for (int first = (int)(threadIdx.x >> 5) * (32 / width); first < rows; first += kRgThreads / width) {
+                const int r = first + lane / width, s = 256 * D + x * 128 + r0 + min(r, rows - 1);
+                float M = -INFINITY, m = -INFINITY, l = 0.f, L = 0.f;
+#pragma unroll 1
+                for (int i = k; i < n; i += width) {
+                    m = __ldcg(part(i) + s);
+                    l = __ldcg(part(i) + s + 256);
+                    M = fmaxf(M, m);
+                }
+                for (int o = width / 2; o > 0; o /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll 1
+                for (int i = k; i < n; i += width) {
+                    if (n > width) {
+                        m = __ldcg(part(i) + s);
+                        l = __ldcg(part(i) + s + 256);
+                    }
+                    const float w = l == 0.f ? 0.f : fast_exp2(m - M);
+                    if (r < rows) weights[r * n + i] = w;
+                    L += l * w;
+                }
+                for (int o = width / 2; o > 0; o /= 2) L += __shfl_xor_sync(0xffffffffu, L, o);
+                if (k == 0 && r < rows) {
+                    inverse[r] = L == 0.f ? 0.f : 1.f / L;
+                    if (p.lse) p.lse[out_row(r0 + r)] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+                }
+            }
+            __syncthreads();
+            rg_wait_longer(bar, phase, p.wait_timeout_ns);
+            phase ^= 1;
+            const float4* const o = reinterpret_cast<const float4*>(room + held);
+#pragma unroll 1
+            for (int item = threadIdx.x; item < rows * kChunks; item += kRgThreads) {
+                const int r = item / kChunks;
+                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+                for (int i = 0; i < n; ++i) {
+                    const float w = weights[r * n + i];
+                    float4 v = o[i * rows * kChunks + item];
+                    if (w == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);     // a row without a key there has left no O
+                    y.x = fmaf(v.x, w, y.x);
+                    y.y = fmaf(v.y, w, y.y);
+                    y.z = fmaf(v.z, w, y.z);
+                    y.w = fmaf(v.w, w, y.w);
+                }
+                const float f = inverse[r];
+                *(reinterpret_cast<uint2*>(p.out + out_row(r0 + r) * D) + item % kChunks) =
+                    make_uint2(pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f));
+            }
+            __syncthreads();
+        }
     }
 }
 
@@ -255,7 +267,8 @@ __global__ void __launch_bounds__(kRgThreads, 1)
     volatile int* const abort_flag = reinterpret_cast<volatile int*>(gen + 4);
     volatile int* const todos = reinterpret_cast<volatile int*>(gen + 8);
     int* const bad_flag = reinterpret_cast<int*>(gen + 16);          // [units]
-    long long* const first_s = reinterpret_cast<long long*>(gen + 64);   // total; sequence and offset of the share's start
+    long long* const first_s = reinterpret_cast<long long*>(gen + 64);   // [1], [2]: sequence and offset of the share's start
+    RgShares* const shares = reinterpret_cast<RgShares*>(gen + 96);
     long long* const warp_sum = reinterpret_cast<long long*>(gen + 128); // [16]
     RgUnit* const todo = reinterpret_cast<RgUnit*>(gen + 256);       // [2]: units to merge
     gen += RS::kMiscBytes;
@@ -263,7 +276,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
     const uint32_t q_full = mended + 8 * S, q_empty = q_full + 16, s_full = q_empty + 16, p_full = s_full + 16;
     const uint32_t p_rest = p_full + 16, s_free = p_rest + 16, pv_done = s_free + 16;
     const uint32_t o_full = pv_done + 16, o_empty = o_full + 16, ml_full = o_empty + 16, fin = ml_full + 16;
-    const uint32_t u_full = fin + 8, u_empty = u_full + 8 * kRgUnits;
+    const uint32_t u_full = fin + 8, u_empty = u_full + 8 * kRgUnits, merge_bar = u_empty + 8 * kRgUnits;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t tmo = p.wait_timeout_ns;
@@ -287,6 +300,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
             mbar_init(ml_full + 8 * x, 4);
         }
         mbar_init(fin, 1);
+        mbar_init(merge_bar, 1);
         for (int i = 0; i < kRgUnits; ++i) {
             mbar_init(u_full + 8 * i, 1);
             mbar_init(u_empty + 8 * i, 15);       // softmax and output warps, products, loads, mending
@@ -312,6 +326,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
         const int per = (p.B + kRgThreads - 1) / kRgThreads;
         const int b0 = min((int)threadIdx.x * per, p.B), b1 = min(b0 + per, p.B);
         long long mine = 0;
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) mine += line.head(rg_sequence(p, b)) * p.G;
         long long sum = mine;
 #pragma unroll
@@ -331,9 +346,12 @@ __global__ void __launch_bounds__(kRgThreads, 1)
             total += y;
         }
         long long at = before + sum - mine;
-        const RgShares sh = RgShares::of(total, gridDim.x);
+        if (threadIdx.x == 0) *shares = RgShares::of(total, gridDim.x);
+        __syncthreads();
+        const RgShares sh = *shares;
         const long long from = (int)blockIdx.x < sh.ctas ? sh.at(blockIdx.x) : total;
         if (at <= from && from < at + mine)
+#pragma unroll 1
             for (int b = b0; b < b1; ++b) {
                 const long long y = line.head(rg_sequence(p, b)) * p.G;
                 if (from < at + y) {
@@ -343,29 +361,25 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 }
                 at += y;
             }
-        if (threadIdx.x == 0) first_s[0] = total;
         __syncthreads();
     }
     const uint32_t tmem = *tmem_slot;
 
-    auto wait = [&](uint32_t bar, uint32_t parity) { return wait_phase(bar, parity & 1, abort_flag, p.status, tmo); };
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        return mbar_try_wait(bar, parity & 1) || rg_wait_slow(bar, parity & 1, abort_flag, p.status, tmo);
+    };
     // The next unit, for every lane of a warp. Waits on although the CTA has given
     // up its work: units keep coming. False: none comes any more.
     auto next_unit = [&](uint32_t n) {
         const uint32_t bar = u_full + 8 * (n % kRgUnits), parity = (n / kRgUnits) & 1;
-        if (!mbar_try_wait(bar, parity)) {
-            const uint64_t t0 = global_timer_ns();
-            while (!mbar_try_wait(bar, parity))
-                if (global_timer_ns() - t0 > 8 * tmo) return false;
-        }
-        return true;
+        return mbar_try_wait(bar, parity) || rg_wait_longer(bar, parity, 8 * tmo);
     };
 
     if (warp >= 12) {
         fewer_registers<80>();
         if (warp == 15) {
             // ------------------------------------------------------------ plan
-            const RgShares sh = RgShares::of(first_s[0], gridDim.x);
+            const RgShares sh = *shares;
             const int c = blockIdx.x;
             const long long to = c < sh.ctas ? sh.at(c + 1) : 0;
             int b = (int)first_s[1];
@@ -377,9 +391,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
             auto publish = [&](const RgUnit& u) {
                 bool ok = true;
                 if (lane == 0) {
-                    const uint64_t t0 = global_timer_ns();
-                    while (ok && !mbar_try_wait(u_empty + 8 * (n % kRgUnits), ((n / kRgUnits) & 1) ^ 1))
-                        ok = global_timer_ns() - t0 <= 4 * tmo;
+                    ok = rg_wait_longer(u_empty + 8 * (n % kRgUnits), ((n / kRgUnits) & 1) ^ 1, 4 * tmo);
                     if (ok) {
                         units[n % kRgUnits] = u;
                         mbar_arrive(u_full + 8 * (n % kRgUnits));
@@ -406,7 +418,9 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 const long long head = line.head(s);
                 int g = 0, pr = 0;
                 if (first) {
-                    g = (int)((from - at) / head);
+                    g = min((int)((float)(from - at) / (float)head), p.G - 1);      // or the one beside it
+                    while (g * head > from - at) --g;
+                    while ((g + 1) * head <= from - at) ++g;
                     pr = line.pair_at(s, from - at - g * head);
                     first = false;
                 }
@@ -433,7 +447,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
             // ----------------------------------------------------------- loads
             const int page_rows = PAGED ? min(1 << p.page_shift, kRgTile) : kRgTile;
             const int boxes = kRgTile / page_rows;
-            uint32_t it = 0, nq[2] = {0, 0};
+            uint32_t it = 0, nq = 0;                 // nq: bit x, phases of Q_x
             // Copies issued: bit s, bit 16 + x; and the parity of the last of each.
             uint32_t issued = 0, parity = 0;
             auto note = [&](int bit, uint32_t phase) {
@@ -446,12 +460,12 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 if (!u.valid) break;
                 const int g = u.g, all = max(u.tiles[0], u.tiles[1]);
                 const int last = u.pos_last;
-#pragma unroll
+#pragma unroll 1
                 for (int x = 0; x < 2; ++x) {
                     if (u.tiles[x] == 0) continue;
-                    const bool ok = !*abort_flag && wait(q_empty + 8 * x, nq[x] ^ 1);
-                    if (ok) note(16 + x, nq[x]);
-                    ++nq[x];
+                    const bool ok = !*abort_flag && wait(q_empty + 8 * x, (nq >> x) ^ 1);
+                    if (ok) note(16 + x, nq >> x);
+                    nq ^= 1u << x;
                     if (ok && lane == 0) {
                         mbar_arrive_expect_tx(q_full + 8 * x, RS::kBlocks * p.tq * p.heads_per_group * 128);
 #pragma unroll
@@ -475,7 +489,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 int now = PAGED && all > 0 ? slab(0) : 0;
                 for (int j = 0; j < all; ++j) {
                     const int then = PAGED && j + 1 < all ? slab(j + 1) : 0;
-#pragma unroll
+#pragma unroll 1
                     for (int v = 0; v < 2; ++v, ++it) {
                         const uint32_t s = it % S;
                         const bool ok = !*abort_flag && wait(empty + 8 * s, (it / S) ^ 1);
@@ -510,9 +524,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 for (int i = 0; i < 18; ++i) {
                     if (!(issued >> i & 1)) continue;
                     const uint32_t bar = i < 16 ? full + 8 * i : q_full + 8 * (i - 16);
-                    const uint64_t t0 = global_timer_ns();
-                    while (!mbar_try_wait(bar, parity >> i & 1))
-                        if (global_timer_ns() - t0 > tmo) break;
+                    rg_wait_longer(bar, parity >> i & 1, tmo);
                 }
         } else if (warp == 14) {
             // ------------------------------------------------------- mending V
@@ -534,12 +546,13 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                         const int r0 = max(0, lim + 1 - t0), r1 = max(0, min(kRgTile, last + 1 - t0));
                         auto chunk = [&](int r, int c) { return v_s + (c >> 3) * kBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
                         constexpr int kChunks = D / 8;
+#pragma unroll 1
                         for (int i = r1 * kChunks + lane; i < kRgTile * kChunks; i += 32)
                             st_shared_zero16(chunk(i / kChunks, i % kChunks));
                         // x * 0 is NaN for what is not finite.
                         uint32_t sum = 0;
                         const uint32_t zero = 0;
-#pragma unroll 4
+#pragma unroll 2
                         for (int i = r0 * kChunks + lane; i < r1 * kChunks; i += 32) {
                             uint32_t w[4];
                             asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -552,11 +565,14 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                         if (__any_sync(0xffffffffu, (sum & 0x7fff7fffu) != 0)) {
                             int* const col = bad + slot * D;
                             if (!any)
+#pragma unroll 1
                                 for (int i = lane; i < D; i += 32) col[i] = 0x7fffffff;
                             any = true;
                             __syncwarp();
+#pragma unroll 1
                             for (int i = r0 * kChunks + lane; i < r1 * kChunks; i += 32) {
                                 const uint32_t a = chunk(i / kChunks, i % kChunks);
+#pragma unroll 1
                                 for (int k = 0; k < 8; ++k) {
                                     uint16_t e;
                                     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e) : "r"(a + 2 * k));
@@ -704,12 +720,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
             // elect_one picks the same thread each time: its commit covers all products.
             if (issued) {
                 umma_commit(fin);
-                const uint64_t t0 = global_timer_ns();
-                while (!mbar_try_wait(fin, 0))
-                    if (global_timer_ns() - t0 > tmo) {
-                        atomicOr(p.status, kStatusTimeout);
-                        break;
-                    }
+                if (!rg_wait_longer(fin, 0, tmo)) atomicOr(p.status, kStatusTimeout);
             }
         }
     } else if (warp >= 8) {
@@ -718,22 +729,22 @@ __global__ void __launch_bounds__(kRgThreads, 1)
         const int row = threadIdx.x & 127;
         const int tok = p.by_heads(row);
         const bool in_tile = row < p.tq * p.heads_per_group;
-        uint32_t nt[2] = {0, 0};
+        uint32_t nt = 0;                         // bit x: phases of O_x
         for (uint32_t n = 0; next_unit(n); ++n) {
             __syncwarp();
             const RgUnit& u = units[n % kRgUnits];
             if (!u.valid) break;
             const int slot = u.slot;
-#pragma unroll
+#pragma unroll 1
             for (int x = 0; x < 2; ++x) {
                 if (u.tokens[x] == 0) continue;
                 const bool some = u.tiles[x] > 0;
                 float m = -INFINITY, l = 0.f;
                 bool ok = true;
                 if (some) {
-                    ok = !*abort_flag && wait(ml_full + 8 * x, nt[x]) && wait(o_full + 8 * x, nt[x]);
+                    ok = !*abort_flag && wait(ml_full + 8 * x, nt >> x) && wait(o_full + 8 * x, nt >> x);
                     ok = __all_sync(0xffffffffu, ok);
-                    ++nt[x];
+                    nt ^= 1u << x;
                 }
                 const bool valid = in_tile && tok < u.tokens[x];
                 if (ok) {
@@ -767,9 +778,6 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                         if (l == 0.f)
 #pragma unroll
                             for (int i = 0; i < 32; ++i) o[i] = 0u;
-                        if (flagged)
-                            for (int i = 0; i < 32; ++i)
-                                if (bad[(n % kRgUnits) * D + c + i] <= lim) o[i] = 0x7fc00000u;
                         if (valid && slot < 0) {
                             uint4* const dst = reinterpret_cast<uint4*>(p.out + orow * D + c);
 #pragma unroll
@@ -787,6 +795,16 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                             for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                         }
                         __syncwarp();
+                    }
+                    if (flagged && valid && l != 0.f) {          // a value that is not finite, where the row sees it
+#pragma unroll 1
+                        for (int c = 0; c < D; ++c) {
+                            if (bad[(n % kRgUnits) * D + c] > lim) continue;
+                            if (slot < 0)
+                                p.out[orow * D + c] = 0x7fc0;
+                            else
+                                part[(size_t)r * D + c] = __uint_as_float(0x7fc00000u);
+                        }
                     }
                     if (valid) {
                         if (slot >= 0) {
@@ -817,8 +835,18 @@ __global__ void __launch_bounds__(kRgThreads, 1)
         const uint32_t s_t = tmem + ((uint32_t)((warp & 3) * 32) << 16) + RS::kColS + x * 128;
         const uint32_t o_t = tmem + ((uint32_t)((warp & 3) * 32) << 16) + RS::kColO + x * D;
         const uint32_t p_t = tmem + ((uint32_t)((warp & 3) * 32) << 16) + RS::kColP + x * RS::kStepP;
+        // No calls from here: a tile's scores are in registers.
+        auto wait_here = [&](uint32_t bar, uint32_t parity) {
+            return wait_phase(bar, parity & 1, abort_flag, p.status, tmo);
+        };
+        auto next_here = [&](uint32_t n) {
+            const uint64_t t0 = global_timer_ns();
+            while (!mbar_try_wait(u_full + 8 * (n % kRgUnits), (n / kRgUnits) & 1))
+                if (global_timer_ns() - t0 > 8 * tmo) return false;
+            return true;
+        };
         uint32_t ns = 0, nu = 0, nd = 0;         // score tiles, units, products so far
-        for (uint32_t n = 0; next_unit(n); ++n) {
+        for (uint32_t n = 0; next_here(n); ++n) {
             __syncwarp();
             const RgUnit& u = units[n % kRgUnits];
             if (!u.valid) break;
@@ -830,7 +858,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
             const bool idle = __all_sync(0xffffffffu, lim < 0);      // no row of this warp sees anything
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < tiles; ++j, ++ns) {
-                bool ok = !*abort_flag && wait(s_full + 8 * x, ns);
+                bool ok = !*abort_flag && wait_here(s_full + 8 * x, ns);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) continue;
                 tc_fence_after();
@@ -838,7 +866,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                     if (RS::kApart) {
                         // No arrival for this tile's P may count for the one before.
                         if (lane == 0) mbar_arrive(s_free + 8 * x);
-                        if (nd > 0) ok = wait(pv_done + 8 * x, nd - 1);
+                        if (nd > 0) ok = wait_here(pv_done + 8 * x, nd - 1);
                         ++nd;
                         if (!__all_sync(0xffffffffu, ok)) continue;
                     }
@@ -877,7 +905,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 // With P apart, the product before has read it and O_X is settled only once
                 // it is done; otherwise these scores came after it.
                 if (RS::kApart) {
-                    if (nd > 0) ok = wait(pv_done + 8 * x, nd - 1);
+                    if (nd > 0) ok = wait_here(pv_done + 8 * x, nd - 1);
                     ok = __all_sync(0xffffffffu, ok);
                     ++nd;
                     if (!ok) continue;
@@ -910,7 +938,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 if (lane == 0) mbar_arrive(p_rest + 8 * x);
             }
             // The unit before has been read from here once its O is given back.
-            if (!*abort_flag) wait(o_empty + 8 * x, nu ^ 1);
+            if (!*abort_flag) wait_here(o_empty + 8 * x, nu ^ 1);
             ml[x * 128 + row] = make_float2(m, l);
             __syncwarp();
             if (lane == 0) mbar_arrive(ml_full + 8 * x);
@@ -927,8 +955,11 @@ __global__ void __launch_bounds__(kRgThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-    float* const scratch = reinterpret_cast<float*>(smem_raw + (ring_s - raw));     // all copies have landed
-    for (int i = 0; i < *todos; ++i) rg_merge<D>(p, todo[i], scratch, scratch + kRgWeights);
+    // All copies have landed and all products are done: Q's and the ring's room is free.
+    uint32_t phase = 0;
+#pragma unroll 1
+    for (int i = 0; i < *todos; ++i)
+        rg_merge<D>(p, todo[i], smem_raw + (q_s - raw), (2 + S) * kTile, merge_bar, phase);
 }
 
 template <int D, bool PAGED>

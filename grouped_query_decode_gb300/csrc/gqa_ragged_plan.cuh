@@ -19,8 +19,9 @@
 
 namespace gqa {
 
-constexpr int kRgTile = 128;          // rows of a tile, and keys of a key tile
-constexpr int kRgPad = 128;           // what a unit counts beyond its keys
+constexpr int kRgTileShift = 7;
+constexpr int kRgTile = 1 << kRgTileShift;   // rows of a tile, and keys of a key tile
+constexpr int kRgPad = 256;           // what a unit counts beyond its keys
 constexpr int kRgMinShare = 512;      // least share of a CTA, in keys
 constexpr int kRgMinPart = 2;         // least key tiles of a part of a unit
 
@@ -48,11 +49,11 @@ static_assert(sizeof(RgUnit) == 64, "a unit is read as 16-byte words");
 struct RgLine {
     int tq, G;
 
-    __host__ __device__ int pairs(int n) const { return (int)(((long long)n + 2 * tq - 1) / (2 * tq)); }
-    __host__ __device__ static int base(const RgSeq& s) { return s.T > s.n ? s.T - s.n : 0; }
+    __host__ __device__ int pairs(int n) const { return (int)(((unsigned)n + 2u * tq - 1) / (2u * tq)); }
+    __host__ __device__ static long long base(const RgSeq& s) { return s.T > s.n ? s.T - s.n : 0; }
     // Where pair pr of a KV head starts, from the head's start.
     __host__ __device__ long long start(const RgSeq& s, int pr) const {
-        return (long long)pr * (base(s) + kRgPad) + (long long)tq * pr * (pr + 1ll);
+        return pr * (base(s) + kRgPad) + (long long)tq * pr * (pr + 1ll);
     }
     __host__ __device__ long long length(const RgSeq& s, int pr) const {
         const long long seen = (pr + 1ll) * 2 * tq;
@@ -82,13 +83,10 @@ struct RgShares {
         long long c = total / kRgMinShare;
         if (c > grid) c = grid;
         if (c < 1) c = 1;
-        return {total / c, total % c, (int)c};
+        const long long each = total / c;
+        return {each, total - each * c, (int)c};
     }
     __host__ __device__ long long at(int c) const { return each * c + (c < more ? c : more); }
-    __host__ __device__ int holder(long long x) const {
-        const long long wide = more * (each + 1);
-        return (int)(x < wide ? x / (each + 1) : more + (x - wide) / each);
-    }
 };
 
 // Fills the part of unit (s, g, pr), which starts at `at` on the line, that CTA c
@@ -101,8 +99,8 @@ __host__ __device__ __forceinline__ bool rg_unit(const RgLine& line, const RgSha
     const int b = left < q2 ? left - a : line.tq;
     const int pos0 = s.T - s.n + pr * q2;
     const int lim_a = pos0 + a - 1, lim_b = pos0 + a + b - 1;
-    const int tiles_a = lim_a < 0 ? 0 : lim_a / kRgTile + 1;
-    const int tiles_b = b == 0 || lim_b < 0 ? 0 : lim_b / kRgTile + 1;
+    const int tiles_a = lim_a < 0 ? 0 : (lim_a >> kRgTileShift) + 1;
+    const int tiles_b = b == 0 || lim_b < 0 ? 0 : (lim_b >> kRgTileShift) + 1;
     const int tiles = tiles_b > tiles_a ? tiles_b : tiles_a;
     const long long len = line.length(s, pr);
     // Key tile that a boundary x cuts at. Parts below kRgMinPart tiles go to the neighbour.
@@ -110,12 +108,12 @@ __host__ __device__ __forceinline__ bool rg_unit(const RgLine& line, const RgSha
         const long long y = x - at;
         if (y <= 0) return 0;
         if (y >= len) return tiles;
-        const long long t = (y + kRgTile / 2) / kRgTile;
+        const long long t = (y + kRgTile / 2) >> kRgTileShift;
         if (t < kRgMinPart) return 0;
         return t > tiles - kRgMinPart ? tiles : (int)t;
     };
     const int j0 = cut(sh.at(c)), j1 = cut(sh.at(c + 1));
-    if (tiles == 0 ? sh.holder(at) != c : j0 >= j1) return false;
+    if (tiles == 0 ? at < sh.at(c) || at >= sh.at(c + 1) : j0 >= j1) return false;
     u->row0 = s.start + pr * q2;
     u->tokens[0] = a;
     u->tokens[1] = b;
@@ -132,9 +130,9 @@ __host__ __device__ __forceinline__ bool rg_unit(const RgLine& line, const RgSha
     u->counter = 0;
     u->valid = 1;
     if (tiles > 0 && (j0 > 0 || j1 < tiles)) {
-        int first = sh.holder(at), last = sh.holder(at + len - 1);
-        while (cut(sh.at(first + 1)) == 0) ++first;
-        while (cut(sh.at(last)) == tiles) --last;
+        int first = c, last = c;                 // the CTAs with parts are neighbours
+        while (cut(sh.at(first)) > 0) --first;
+        while (cut(sh.at(last + 1)) < tiles) ++last;
         u->slot = 2 * c + (at < sh.at(c) ? 0 : 1);
         u->first = first;
         u->parts = last - first + 1;
