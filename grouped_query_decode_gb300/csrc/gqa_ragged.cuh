@@ -16,9 +16,9 @@
 //
 // Warps: 0-3 and 4-7 softmax of A and B, a thread per row; 8-11 outputs; 12 issues
 // the products, always one of A, one of B, so that each tile's softmax runs behind
-// the other's products; 13 loads Q, K and V by TMA, a lane per page; 14 mends V
-// tiles that reach past the first row's limit; 15 plans and hands the units out
-// through a ring in shared memory. Every wait is bounded; after one has expired
+// the other's products; 13 loads Q and K by TMA, a lane per page, 14 V, of which
+// it mends the tiles that reach past the first row's limit; 15 plans and hands the
+// units out through a ring in shared memory. Every wait is bounded; after one has expired
 // the CTA runs through its units without work, so that the counters end at zero.
 //
 // V at positions that only some rows see: a masked key's weight is 0, and 0 times
@@ -121,6 +121,19 @@ __device__ __forceinline__ void rg_weights(const float* s, float2 scale, float2 
         tmem_st16(p_t + k / 2, pk);
     }
 }
+
+// A unit with rows in tile A alone: its key tiles go to both pipelines in turn, so
+// that one tile's softmax runs behind the other's products; their two O are joined
+// with the output. Key tile of pipeline x's j-th step, and steps of pipeline x:
+struct RgSteps {
+    bool dual;
+    int a, b;
+    __device__ __forceinline__ explicit RgSteps(const RgUnit& u) {
+        dual = u.tokens[1] == 0 && u.tiles[0] > 1;
+        a = dual ? (u.tiles[0] + 1) / 2 : u.tiles[0];
+        b = dual ? u.tiles[0] / 2 : u.tiles[1];
+    }
+};
 
 __device__ __forceinline__ RgSeq rg_sequence(const RaggedParams& p, int b) {
     RgSeq s = {0, 0, 0};
@@ -284,7 +297,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(full + 8 * s, 1);
-            mbar_init(empty + 8 * s, 1 + (s & 1));    // V, in odd stages, has been seen by warp 14 too
+            mbar_init(empty + 8 * s, 1);
             mbar_init(mended + 8 * s, 1);
         }
         for (int x = 0; x < 2; ++x) {
@@ -303,7 +316,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
         mbar_init(merge_bar, 1);
         for (int i = 0; i < kRgUnits; ++i) {
             mbar_init(u_full + 8 * i, 1);
-            mbar_init(u_empty + 8 * i, 15);       // softmax and output warps, products, loads, mending
+            mbar_init(u_empty + 8 * i, 15);       // softmax and output warps, products, loads
         }
         for (int i = 0; i < kRgUnits; ++i) bad_flag[i] = 0;
         *abort_flag = 0;
@@ -379,75 +392,81 @@ __global__ void __launch_bounds__(kRgThreads, 1)
         fewer_registers<80>();
         if (warp == 15) {
             // ------------------------------------------------------------ plan
+            // Sequence b, whose units start at `at` on the line, KV head g, pair pr.
             const RgShares sh = *shares;
             const int c = blockIdx.x;
             const long long to = c < sh.ctas ? sh.at(c + 1) : 0;
-            int b = (int)first_s[1];
-            long long at = first_s[2];
-            uint32_t n = 0;
+            int b = (int)first_s[1], g = 0, pr = 0, pairs = 0;
+            long long at = first_s[2], head = 0;
             int chunk = b;                          // lanes hold sequences chunk + lane
-            RgSeq mine = rg_sequence(p, chunk + lane);
-            const long long from = c < sh.ctas ? sh.at(c) : 0;
-            auto publish = [&](const RgUnit& u) {
-                bool ok = true;
+            RgSeq mine = rg_sequence(p, chunk + lane), seq = {0, 0, 0};
+            bool inside = false, first = true;
+            auto plan = [&](RgUnit& u) {            // the next unit with a part for this CTA
+                while (true) {
+                    if (!inside) {
+                        for (; b < p.B && at < to; ++b) {
+                            if (b >= chunk + 32) {
+                                chunk = b;
+                                mine = rg_sequence(p, chunk + lane);
+                            }
+                            seq.n = __shfl_sync(0xffffffffu, mine.n, b - chunk);
+                            if (seq.n > 0) break;
+                        }
+                        if (b >= p.B || at >= to) return false;
+                        seq.start = __shfl_sync(0xffffffffu, mine.start, b - chunk);
+                        seq.T = __shfl_sync(0xffffffffu, mine.T, b - chunk);
+                        pairs = line.pairs(seq.n);
+                        head = line.head(seq);
+                        g = pr = 0;
+                        if (first) {
+                            const long long y = sh.at(c) - at;
+                            g = min((int)((float)y / (float)head), p.G - 1);       // or the one beside it
+                            while (g * head > y) --g;
+                            while ((g + 1) * head <= y) ++g;
+                            pr = line.pair_at(seq, y - g * head);
+                        }
+                        first = false;
+                        inside = true;
+                    }
+                    if (pr == pairs) {
+                        pr = 0;
+                        if (++g == p.G) {
+                            at += head * p.G;
+                            ++b;
+                            inside = false;
+                            continue;
+                        }
+                    }
+                    const long long unit = at + g * head + line.start(seq, pr);
+                    if (unit >= to) return false;
+                    u.seq = b;
+                    u.g = g;
+                    if (rg_unit(line, sh, c, seq, pr++, unit, &u)) return true;
+                }
+            };
+            bool more = true;
+            for (uint32_t n = 0; more; ++n) {
+                RgUnit u;
+                more = plan(u);
+                u.valid = more;                     // the last one handed out ends the list
                 if (lane == 0) {
-                    ok = rg_wait_longer(u_empty + 8 * (n % kRgUnits), ((n / kRgUnits) & 1) ^ 1, 4 * tmo);
-                    if (ok) {
-                        units[n % kRgUnits] = u;
-                        mbar_arrive(u_full + 8 * (n % kRgUnits));
-                    } else {
+                    if (more && u.slot >= 0) tag_counter(p.counters + u.counter, p.tag);
+                    if (!rg_wait_longer(u_empty + 8 * (n % kRgUnits), ((n / kRgUnits) & 1) ^ 1, 4 * tmo)) {
                         *abort_flag = 1;
                         atomicOr(p.status, kStatusTimeout);
                     }
+                    units[n % kRgUnits] = u;
+                    mbar_arrive(u_full + 8 * (n % kRgUnits));
                 }
-                ++n;
-                return __shfl_sync(0xffffffffu, ok, 0) != 0;
-            };
-            bool ok = true;
-            for (bool first = true; ok && b < p.B && at < to; ++b) {
-                if (b >= chunk + 32) {
-                    chunk = b;
-                    mine = rg_sequence(p, chunk + lane);
-                }
-                RgSeq s;
-                s.start = __shfl_sync(0xffffffffu, mine.start, b - chunk);
-                s.n = __shfl_sync(0xffffffffu, mine.n, b - chunk);
-                s.T = __shfl_sync(0xffffffffu, mine.T, b - chunk);
-                const int pairs = line.pairs(s.n);
-                if (pairs == 0) continue;
-                const long long head = line.head(s);
-                int g = 0, pr = 0;
-                if (first) {
-                    g = min((int)((float)(from - at) / (float)head), p.G - 1);      // or the one beside it
-                    while (g * head > from - at) --g;
-                    while ((g + 1) * head <= from - at) ++g;
-                    pr = line.pair_at(s, from - at - g * head);
-                    first = false;
-                }
-                for (; ok && g < p.G; ++g, pr = 0)
-                    for (; ok && pr < pairs; ++pr) {
-                        const long long unit = at + g * head + line.start(s, pr);
-                        if (unit >= to) {
-                            g = p.G;
-                            break;
-                        }
-                        RgUnit u;
-                        u.seq = b;
-                        u.g = g;
-                        if (rg_unit(line, sh, c, s, pr, unit, &u)) {
-                            if (u.slot >= 0 && lane == 0) tag_counter(p.counters + u.counter, p.tag);
-                            ok = publish(u);
-                        }
-                    }
-                at += head * p.G;
+                __syncwarp();
             }
-            RgUnit none = {};
-            if (ok) publish(none);
-        } else if (warp == 13) {
-            // ----------------------------------------------------------- loads
+        } else if (warp >= 13) {
+            // ------------- loads: Q and K from warp 13, V from warp 14, which mends it
+            const bool v_warp = warp == 14;
             const int page_rows = PAGED ? min(1 << p.page_shift, kRgTile) : kRgTile;
             const int boxes = kRgTile / page_rows;
-            uint32_t it = 0, nq = 0;                 // nq: bit x, phases of Q_x
+            const CUtensorMap* const tm = v_warp ? &tm_v : &tm_k;
+            uint32_t it = v_warp, nq = 0;            // ring place; phases of Q_x in bit x
             // Copies issued: bit s, bit 16 + x; and the parity of the last of each.
             uint32_t issued = 0, parity = 0;
             auto note = [&](int bit, uint32_t phase) {
@@ -458,20 +477,23 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 __syncwarp();
                 const RgUnit& u = units[n % kRgUnits];
                 if (!u.valid) break;
-                const int g = u.g, all = max(u.tiles[0], u.tiles[1]);
-                const int last = u.pos_last;
+                const int all = max(u.tiles[0], u.tiles[1]), last = u.pos_last, ug = u.g, lim = u.pos0;
+                bool any_bad = false;
+                if (!v_warp) {
+                    const bool dual = RgSteps(u).dual;       // both pipelines have tile A's rows
 #pragma unroll 1
-                for (int x = 0; x < 2; ++x) {
-                    if (u.tiles[x] == 0) continue;
-                    const bool ok = !*abort_flag && wait(q_empty + 8 * x, (nq >> x) ^ 1);
-                    if (ok) note(16 + x, nq >> x);
-                    nq ^= 1u << x;
-                    if (ok && lane == 0) {
-                        mbar_arrive_expect_tx(q_full + 8 * x, RS::kBlocks * p.tq * p.heads_per_group * 128);
+                    for (int x = 0; x < 2; ++x) {
+                        if ((x ? u.tiles[1] : u.tiles[0]) == 0 && !dual) continue;
+                        const bool ok = !*abort_flag && wait(q_empty + 8 * x, (nq >> x) ^ 1);
+                        if (ok) note(16 + x, nq >> x);
+                        nq ^= 1u << x;
+                        if (ok && lane == 0) {
+                            mbar_arrive_expect_tx(q_full + 8 * x, RS::kBlocks * p.tq * p.heads_per_group * 128);
 #pragma unroll
-                        for (int k = 0; k < RS::kBlocks; ++k)
-                            tma_load_3d(q_s + x * kTile + k * kBlock, &tm_q, q_full + 8 * x, k * 64,
-                                        g * p.heads_per_group, u.row0 + x * p.tq);
+                            for (int k = 0; k < RS::kBlocks; ++k)
+                                tma_load_3d(q_s + x * kTile + k * kBlock, &tm_q, q_full + 8 * x, k * 64,
+                                            ug * p.heads_per_group, u.row0 + (dual ? 0 : x * p.tq));
+                        }
                     }
                 }
                 // This lane's page of key tile j: its slab, or the one past the last.
@@ -484,139 +506,120 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                             if ((unsigned)e < (unsigned)p.num_pages) page = e;
                         }
                     }
-                    return page == p.num_pages ? p.num_pages * p.G : page * p.G + g;
+                    return page == p.num_pages ? p.num_pages * p.G : page * p.G + ug;
                 };
-                int now = PAGED && all > 0 ? slab(0) : 0;
-                for (int j = 0; j < all; ++j) {
-                    const int then = PAGED && j + 1 < all ? slab(j + 1) : 0;
+                int now = 0;
+                // With V, step j issues tile j and then sees tile j - 1 land, before the
+                // next copy goes to that one's stage.
 #pragma unroll 1
-                    for (int v = 0; v < 2; ++v, ++it) {
-                        const uint32_t s = it % S;
-                        const bool ok = !*abort_flag && wait(empty + 8 * s, (it / S) ^ 1);
-                        if (!__all_sync(0xffffffffu, ok)) continue;
-                        if (blockIdx.x == 0 && v == 0 && n == 0 && j == p.skip_tile) continue;   // injected fault
-                        note(s, it / S);
-                        if (lane == 0) mbar_arrive_expect_tx(full + 8 * s, kTile);
-                        __syncwarp();
-                        const uint32_t dst = ring_s + s * kTile;
-                        const CUtensorMap* tm = v ? &tm_v : &tm_k;
-                        if (PAGED) {
-                            const int row = ((u.j0 + j) * kRgTile) & ((1 << p.page_shift) - 1);
+                for (int j = 0; j < all + v_warp; ++j, it += 2) {
+                    const int t0 = (u.j0 + j) * kRgTile;
+                    if (j < all) {
+                        if (PAGED && j == 0) now = slab(0);
+                        const int then = PAGED && j + 1 < all ? slab(j + 1) : 0;
+                        const uint32_t s = it % S, bar = full + 8 * s;
+                        bool ok = !*abort_flag && wait(empty + 8 * s, (it / S) ^ 1);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (ok && !(blockIdx.x == 0 && !v_warp && n == 0 && j == p.skip_tile)) {     // injected fault
+                            note(s, it / S);
+                            if (lane == 0) mbar_arrive_expect_tx(bar, kTile);
+                            __syncwarp();
+                            const uint32_t dst = ring_s + s * kTile + lane * page_rows * 128;
                             if (lane < boxes)
 #pragma unroll
-                                for (int k = 0; k < RS::kBlocks; ++k)
-                                    tma_load_3d(dst + k * kBlock + lane * page_rows * 128, tm, full + 8 * s, k * 64,
-                                                boxes > 1 ? 0 : row, now);
-                        } else if (lane == 0) {
-#pragma unroll
-                            for (int k = 0; k < RS::kBlocks; ++k)
-                                tma_load_3d(dst + k * kBlock, tm, full + 8 * s, k * 64, g,
-                                            u.key0 + (u.j0 + j) * kRgTile);
+                                for (int k = 0; k < RS::kBlocks; ++k) {
+                                    if (PAGED)
+                                        tma_load_3d(dst + k * kBlock, tm, bar, k * 64,
+                                                    boxes > 1 ? 0 : t0 & ((1 << p.page_shift) - 1), now);
+                                    else
+                                        tma_load_3d(dst + k * kBlock, tm, bar, k * 64, ug, u.key0 + t0);
+                                }
                         }
+                        now = then;
                     }
-                    now = then;
+                    if (!v_warp || j == 0) continue;
+                    const int t1 = t0 - kRgTile;
+                    const uint32_t s = (it - 2) % S, v_s = ring_s + s * kTile;
+                    const bool ok = !*abort_flag && wait(full + 8 * s, (it - 2) / S);
+                    if (!__all_sync(0xffffffffu, ok) || t1 + kRgTile - 1 <= lim) continue;
+                    // Rows [r0, r1) are seen by some, those from r1 on by none.
+                    const int r0 = max(0, lim + 1 - t1), r1 = max(0, min(kRgTile, last + 1 - t1));
+                    auto chunk = [&](int r, int c) { return v_s + (c >> 3) * kBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
+                    constexpr int kChunks = D / 8;
+#pragma unroll 1
+                    for (int i = r1 * kChunks + lane; i < kRgTile * kChunks; i += 32)
+                        st_shared_zero16(chunk(i / kChunks, i % kChunks));
+                    // x * 0 is NaN for what is not finite.
+                    uint32_t sum = 0;
+                    const uint32_t zero = 0;
+#pragma unroll 2
+                    for (int i = r0 * kChunks + lane; i < r1 * kChunks; i += 32) {
+                        uint32_t w[4];
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                     : "r"(chunk(i / kChunks, i % kChunks)));
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(w[k]), "r"(zero));
+                    }
+                    if (__any_sync(0xffffffffu, (sum & 0x7fff7fffu) != 0)) {
+                        const int slot = n % kRgUnits;
+                        int* const col = bad + slot * D;
+                        if (!any_bad)
+#pragma unroll 1
+                            for (int i = lane; i < D; i += 32) col[i] = 0x7fffffff;
+                        any_bad = true;
+                        __syncwarp();
+#pragma unroll 1
+                        for (int i = r0 * kChunks + lane; i < r1 * kChunks; i += 32) {
+                            const uint32_t a = chunk(i / kChunks, i % kChunks);
+#pragma unroll 1
+                            for (int k = 0; k < 8; ++k) {
+                                uint16_t e;
+                                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e) : "r"(a + 2 * k));
+                                if ((e & 0x7f80) != 0x7f80) continue;
+                                asm volatile("st.shared.u16 [%0], %1;" ::"r"(a + 2 * k), "h"((uint16_t)0) : "memory");
+                                atomicMin(col + (i % kChunks) * 8 + k, t1 + i / kChunks);
+                            }
+                        }
+                        __threadfence_block();
+                        __syncwarp();
+                        if (lane == 0) *reinterpret_cast<volatile int*>(bad_flag + slot) = 1 + (int)(n / kRgUnits);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(mended + 8 * s);
                 }
+                if (v_warp) it -= 2;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(u_empty + 8 * (n % kRgUnits));
             }
             // Leave only once all copies have landed.
             if (lane == 0)
-                for (int i = 0; i < 18; ++i) {
-                    if (!(issued >> i & 1)) continue;
-                    const uint32_t bar = i < 16 ? full + 8 * i : q_full + 8 * (i - 16);
-                    rg_wait_longer(bar, parity >> i & 1, tmo);
-                }
-        } else if (warp == 14) {
-            // ------------------------------------------------------- mending V
-            uint32_t it = 0;
-            for (uint32_t n = 0; next_unit(n); ++n) {
-                __syncwarp();
-                const RgUnit& u = units[n % kRgUnits];
-                if (!u.valid) break;
-                const int all = max(u.tiles[0], u.tiles[1]), slot = n % kRgUnits;
-                const int lim = u.pos0, last = u.pos_last, j0 = u.j0;
-                bool any = false;
-                for (int j = 0; j < all; ++j, it += 2) {
-                    const int t0 = (j0 + j) * kRgTile;
-                    const bool mend = t0 + kRgTile - 1 > lim;
-                    const uint32_t s = (it + 1) % S, v_s = ring_s + s * kTile;
-                    const bool ok = !*abort_flag && wait(full + 8 * s, (it + 1) / S);
-                    if (__all_sync(0xffffffffu, ok) && mend) {
-                        // Rows [r0, r1) are seen by some, those from r1 on by none.
-                        const int r0 = max(0, lim + 1 - t0), r1 = max(0, min(kRgTile, last + 1 - t0));
-                        auto chunk = [&](int r, int c) { return v_s + (c >> 3) * kBlock + r * 128 + (((c & 7) ^ (r & 7)) << 4); };
-                        constexpr int kChunks = D / 8;
 #pragma unroll 1
-                        for (int i = r1 * kChunks + lane; i < kRgTile * kChunks; i += 32)
-                            st_shared_zero16(chunk(i / kChunks, i % kChunks));
-                        // x * 0 is NaN for what is not finite.
-                        uint32_t sum = 0;
-                        const uint32_t zero = 0;
-#pragma unroll 2
-                        for (int i = r0 * kChunks + lane; i < r1 * kChunks; i += 32) {
-                            uint32_t w[4];
-                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                                         : "r"(chunk(i / kChunks, i % kChunks)));
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(w[k]), "r"(zero));
-                        }
-                        if (__any_sync(0xffffffffu, (sum & 0x7fff7fffu) != 0)) {
-                            int* const col = bad + slot * D;
-                            if (!any)
-#pragma unroll 1
-                                for (int i = lane; i < D; i += 32) col[i] = 0x7fffffff;
-                            any = true;
-                            __syncwarp();
-#pragma unroll 1
-                            for (int i = r0 * kChunks + lane; i < r1 * kChunks; i += 32) {
-                                const uint32_t a = chunk(i / kChunks, i % kChunks);
-#pragma unroll 1
-                                for (int k = 0; k < 8; ++k) {
-                                    uint16_t e;
-                                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e) : "r"(a + 2 * k));
-                                    if ((e & 0x7f80) != 0x7f80) continue;
-                                    asm volatile("st.shared.u16 [%0], %1;" ::"r"(a + 2 * k), "h"((uint16_t)0) : "memory");
-                                    atomicMin(col + (i % kChunks) * 8 + k, t0 + i / kChunks);
-                                }
-                            }
-                            __threadfence_block();
-                            __syncwarp();
-                            if (lane == 0) *reinterpret_cast<volatile int*>(bad_flag + slot) = 1 + (int)(n / kRgUnits);
-                        }
-                        fence_proxy_async_smem();
-                    }
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (mend) mbar_arrive(mended + 8 * s);
-                        mbar_arrive(empty + 8 * s);
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(u_empty + 8 * (n % kRgUnits));
-            }
+                for (int i = 0; i < 18; ++i)
+                    if (issued >> i & 1)
+                        rg_wait_longer(i < 16 ? full + 8 * i : q_full + 8 * (i - 16), parity >> i & 1, tmo);
         } else if (elect_one()) {
             // -------------------------------------------------------- products
-            // The warp waits as a whole and one thread issues; what the instructions
-            // take is made uniform (from a single thread's own registers every
-            // product waits for its operands' way to the uniform ones).
+            // One thread, elected so that the compiler knows of no other: from a branch
+            // on the lane every product's operands were made uniform by themselves (the
+            // long prompt 1932 us, 1758 with a converged warp that elects for each batch
+            // of products, 1545 like this).
             constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
             constexpr uint32_t kIdescO = idesc_bf16_f32(128, D, false, true);
             constexpr uint64_t kDescK = smem_desc_base(16, 1024), kDescV = smem_desc_base(kBlock, 1024);
             struct Now {
-                int a, b, all, j0, lim;          // key tiles of A, B, both
-                uint32_t it;
-            } u = {0, 0, 1, 0, 0, 0}, next = u;  // a unit without tiles leads in the first
+                int a, b, all, j0, lim;          // steps of A, B, both
+                uint32_t it, dual;               // 0 or 1
+            } u = {0, 0, 1, 0, 0, 0, 0}, next = u;   // a unit without steps leads in the first
             uint32_t n = 0, it = 0, phases = 0, mends = 0;
             bool ok = true, issued = false;
-            const uint32_t tmem_u = tmem;
-            auto uniform = [](uint32_t v) { return v; };
-            auto wait_warp = [&](uint32_t bar, uint32_t parity) {
+            auto wait_one = [&](uint32_t bar, uint32_t parity) {
                 ok = ok && wait(bar, parity);
             };
             auto wait_next = [&](uint32_t bar, int bit, uint32_t flip) {
-                wait_warp(bar, (phases >> bit) ^ flip);
+                wait_one(bar, (phases >> bit) ^ flip);
                 phases ^= 1u << bit;
             };
             // The next unit with key tiles.
@@ -624,67 +627,61 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 while (next_unit(n)) {
                     const RgUnit& f = units[n % kRgUnits];
                     if (!f.valid) return false;
-                    next = {f.tiles[0], f.tiles[1], max(f.tiles[0], f.tiles[1]), f.j0, f.pos0, it};
+                    const RgSteps st(f);
+                    next = {st.a, st.b, max(st.a, st.b), f.j0, f.pos0, it, st.dual};
+                    it += 2 * max(f.tiles[0], f.tiles[1]);
                     mbar_arrive(u_empty + 8 * (n % kRgUnits));
                     ++n;
-                    it += 2 * next.all;
                     if (next.all > 0) return true;
                 }
                 return false;
             };
-            // S_X of the K tile at ring place i.
+            // S_X for the K tile at ring place i.
             auto scores = [&](uint32_t i, int x, bool first, bool last, bool release) {
                 const uint32_t s = i % S;
                 if (first) wait_next(q_full + 8 * x, x, 0);
                 if (RS::kApart) wait_next(s_free + 8 * x, 6 + x, 1);
-                wait_warp(full + 8 * s, i / S);
+                wait_one(full + 8 * s, i / S);
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t su = uniform(s), xu = uniform(x), end = uniform(last | (release ? 2 : 0));
-                {
-                    const uint64_t a = kDescK + ((q_s + xu * kTile) >> 4), b = kDescK + ((ring_s + su * kTile) >> 4);
-                    const uint32_t to = tmem_u + RS::kColS + xu * 128;
+                const uint64_t a = kDescK + ((q_s + x * kTile) >> 4), b = kDescK + ((ring_s + s * kTile) >> 4);
+                const uint32_t to = tmem + RS::kColS + x * 128;
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t off = ((k >> 2) * kBlock + (k & 3) * 32) >> 4;
-                        umma_bf16(to, a + off, b + off, kIdescS, k > 0 ? 1u : 0u);
-                    }
-                    umma_commit(s_full + 8 * xu);
-                    if (end & 1) umma_commit(q_empty + 8 * xu);
-                    if (end & 2) umma_commit(empty + 8 * su);
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = ((k >> 2) * kBlock + (k & 3) * 32) >> 4;
+                    umma_bf16(to, a + off, b + off, kIdescS, k > 0 ? 1u : 0u);
                 }
+                umma_commit(s_full + 8 * x);
+                if (last) umma_commit(q_empty + 8 * x);
+                if (release) umma_commit(empty + 8 * s);
                 issued = true;
             };
             // O_X += P_X V for the V tile at ring place i.
             auto values = [&](uint32_t i, int x, bool fresh, bool mend, bool first, bool last, bool release) {
                 const uint32_t s = i % S;
                 if (fresh) {
-                    wait_warp((mend ? mended : full) + 8 * s, mend ? mends >> s : i / S);
+                    wait_one((mend ? mended : full) + 8 * s, mend ? mends >> s : i / S);
                     if (mend) mends ^= 1u << s;
                 }
                 if (first) wait_next(o_empty + 8 * x, 4 + x, 1);
-                const uint32_t su = uniform(s), xu = uniform(x), more = uniform(!first), end = uniform(last | (release ? 2 : 0));
-                const uint64_t b = kDescV + ((ring_s + su * kTile) >> 4);
-                const uint32_t to = tmem_u + RS::kColO + xu * D, a = tmem_u + RS::kColP + xu * RS::kStepP;
-                wait_warp(p_full + 8 * x, phases >> (2 + x));
+                const uint64_t b = kDescV + ((ring_s + s * kTile) >> 4);
+                const uint32_t to = tmem + RS::kColO + x * D, a = tmem + RS::kColP + x * RS::kStepP;
+                wait_one(p_full + 8 * x, phases >> (2 + x));
                 if (!ok) return;
                 tc_fence_after();
-                
 #pragma unroll
-                    for (int k = 0; k < kRgFirst / 16; ++k)
-                        umma_bf16_ts(to, a + k * 8, b + k * (16 * 128 >> 4), kIdescO, k > 0 ? 1u : more);
-                wait_warp(p_rest + 8 * x, phases >> (2 + x));
+                for (int k = 0; k < kRgFirst / 16; ++k)
+                    umma_bf16_ts(to, a + k * 8, b + k * (16 * 128 >> 4), kIdescO, !first || k > 0 ? 1u : 0u);
+                wait_one(p_rest + 8 * x, phases >> (2 + x));
                 phases ^= 4u << x;
                 if (!ok) return;
                 tc_fence_after();
-                {
 #pragma unroll
-                    for (int k = kRgFirst / 16; k < kRgTile / 16; ++k)
-                        umma_bf16_ts(to, a + k * 8, b + k * (16 * 128 >> 4), kIdescO, 1u);
-                    if (RS::kApart) umma_commit(pv_done + 8 * xu);
-                    if (end & 1) umma_commit(o_full + 8 * xu);
-                    if (end & 2) umma_commit(empty + 8 * su);
-                }
+                for (int k = kRgFirst / 16; k < kRgTile / 16; ++k)
+                    umma_bf16_ts(to, a + k * 8, b + k * (16 * 128 >> 4), kIdescO, 1u);
+                if (RS::kApart) umma_commit(pv_done + 8 * x);
+                if (last) umma_commit(o_full + 8 * x);
+                if (release) umma_commit(empty + 8 * s);
             };
             bool have = true;
             while (have) {
@@ -693,24 +690,26 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 for (int j = 0; j < u.all; ++j) {
                     const bool end = j + 1 == u.all;
                     if (end) more = fetch();
-                    const bool mend = (u.j0 + j) * kRgTile + kRgTile - 1 > u.lim;
 #pragma unroll 1
                     for (int x = 0; x < 2; ++x) {
-                        const int tiles = x ? u.b : u.a;
-                        // What S_X holds next: this unit's next tile, or the next unit's first.
-                        bool go = j + 1 < tiles, lead = false;
-                        uint32_t i = u.it + 2 * (j + 1);
-                        bool last = j + 2 == tiles, release = x == 1 || j + 1 >= u.b;
+                        const int steps = x ? u.b : u.a;
+                        // What S_X holds next: this unit's next tile of X, or the next unit's first.
+                        bool go = j + 1 < steps, lead = false;
+                        const int v = (j << u.dual) + (x & u.dual);
+                        uint32_t i = u.it + 2 * v + (2 << u.dual);
+                        bool last = j + 2 == steps, release = u.dual || x == 1 || j + 1 >= u.b;
                         if (!go && end && more) {
-                            const int t = x ? next.b : next.a;
-                            go = lead = t > 0;
-                            i = next.it;
-                            last = t == 1;
-                            release = x == 1 || next.b == 0;
+                            const int to = x ? next.b : next.a;
+                            go = lead = to > 0;
+                            i = next.it + 2 * (x & next.dual);
+                            last = to == 1;
+                            release = next.dual || x == 1 || next.b == 0;
                         }
                         if (RS::kApart && go) scores(i, x, lead, last, release);
-                        if (j < tiles)
-                            values(u.it + 2 * j + 1, x, x == 0 || j >= u.a, mend, j == 0, j + 1 == tiles, x == 1 || j >= u.b);
+                        if (j < steps)
+                            values(u.it + 2 * v + 1, x, u.dual || x == 0 || j >= u.a,
+                                   (u.j0 + v) * kRgTile + kRgTile - 1 > u.lim, j == 0, j + 1 == steps,
+                                   u.dual || x == 1 || j >= u.b);
                         if (!RS::kApart && go) scores(i, x, lead, last, release);
                     }
                 }
@@ -738,13 +737,17 @@ __global__ void __launch_bounds__(kRgThreads, 1)
 #pragma unroll 1
             for (int x = 0; x < 2; ++x) {
                 if (u.tokens[x] == 0) continue;
-                const bool some = u.tiles[x] > 0;
-                float m = -INFINITY, l = 0.f;
+                const bool some = u.tiles[x] > 0, dual = RgSteps(u).dual;
+                float m = -INFINITY, l = 0.f, a0 = 1.f, a1 = 0.f;      // factors of O_A, O_B if both have the rows
                 bool ok = true;
                 if (some) {
                     ok = !*abort_flag && wait(ml_full + 8 * x, nt >> x) && wait(o_full + 8 * x, nt >> x);
-                    ok = __all_sync(0xffffffffu, ok);
                     nt ^= 1u << x;
+                    if (dual) {
+                        ok = ok && wait(ml_full + 8, nt >> 1) && wait(o_full + 8, nt >> 1);
+                        nt ^= 2u;
+                    }
+                    ok = __all_sync(0xffffffffu, ok);
                 }
                 const bool valid = in_tile && tok < u.tokens[x];
                 if (ok) {
@@ -753,6 +756,14 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                         const float2 y = ml[x * 128 + row];
                         m = y.x;
                         l = y.y;
+                        if (dual) {
+                            const float2 z = ml[128 + row];
+                            const float top = fmaxf(m, z.x);
+                            a0 = l == 0.f ? 0.f : fast_exp2(m - top);
+                            a1 = z.y == 0.f ? 0.f : fast_exp2(z.x - top);
+                            l = l * a0 + z.y * a1;
+                            m = top;
+                        }
                     }
                     const bool flagged = *reinterpret_cast<volatile int*>(bad_flag + n % kRgUnits) == 1 + (int)(n / kRgUnits);
                     const int lim = u.pos0 + x * p.tq + tok;
@@ -762,26 +773,38 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                     float* const part = p.part + (size_t)max(slot, 0) * rg_slot_floats(D);
                     const int r = x * 128 + row;
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        const uint32_t o_t = tmem + ((uint32_t)((warp & 3) * 32) << 16) + RS::kColO + c;
                         if (some) {
-                            tmem_ld32(tmem + ((uint32_t)((warp & 3) * 32) << 16) + RS::kColO + x * D + c, o);
+                            tmem_ld16(o_t + x * D, o);
                         } else {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = 0u;
+                            for (int i = 0; i < 16; ++i) o[i] = 0u;
                         }
-                        if (c + 32 == D && some) {
+                        if (dual) {
+                            uint32_t b[16];
+                            tmem_ld16(o_t + D, b);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                // A pipeline whose tiles showed the row nothing has no O for it.
+                                const float oa = a0 == 0.f ? 0.f : __uint_as_float(o[i]) * a0;
+                                o[i] = __float_as_uint(a1 == 0.f ? oa : fmaf(__uint_as_float(b[i]), a1, oa));
+                            }
+                        }
+                        if (c + 16 == D && some) {
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(o_empty + 8 * x);
+                            if (lane == 0 && dual) mbar_arrive(o_empty + 8);
                         }
                         if (l == 0.f)
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = 0u;
+                            for (int i = 0; i < 16; ++i) o[i] = 0u;
                         if (valid && slot < 0) {
                             uint4* const dst = reinterpret_cast<uint4*>(p.out + orow * D + c);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
+                            for (int k = 0; k < 2; ++k) {
                                 uint32_t w[4];
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
@@ -792,7 +815,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                         } else if (valid && l != 0.f) {
                             uint4* const dst = reinterpret_cast<uint4*>(part + (size_t)r * D + c);
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                            for (int k = 0; k < 4; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                         }
                         __syncwarp();
                     }
@@ -850,8 +873,10 @@ __global__ void __launch_bounds__(kRgThreads, 1)
             __syncwarp();
             const RgUnit& u = units[n % kRgUnits];
             if (!u.valid) break;
-            const int tiles = u.tiles[x], j0 = u.j0;
-            const int lim = in_tile && tok < u.tokens[x] ? u.pos0 + x * p.tq + tok : -1;
+            const RgSteps st(u);
+            const int tiles = x ? st.b : st.a, j0 = u.j0 + (st.dual ? x : 0), xr = st.dual ? 0 : x;
+            const bool dual = st.dual;
+            const int lim = in_tile && tok < u.tokens[xr] ? u.pos0 + xr * p.tq + tok : -1;
             __syncwarp();
             if (lane == 0) mbar_arrive(u_empty + 8 * (n % kRgUnits));
             if (tiles == 0) continue;
@@ -880,7 +905,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 tmem_ld64_start(s_t, s);
                 tmem_ld_wait(s);
                 tmem_ld64_start(s_t + 64, s + 64);
-                const int t0 = (j0 + j) * kRgTile;
+                const int t0 = (j0 + (dual ? 2 * j : j)) * kRgTile;
                 const bool edge = t0 + kRgTile - 1 > lim;
                 if (edge) {
 #pragma unroll

@@ -112,7 +112,15 @@ __host__ __device__ __forceinline__ bool rg_unit(const RgLine& line, const RgSha
         if (t < kRgMinPart) return 0;
         return t > tiles - kRgMinPart ? tiles : (int)t;
     };
-    const int j0 = cut(sh.at(c)), j1 = cut(sh.at(c + 1));
+    // The CTAs with parts of the unit are neighbours: where they begin and end.
+    int first = c, last = c, j0 = 0, j1 = 0;
+    for (int t; (t = cut(sh.at(first))) > 0; --first)
+        if (first == c) j0 = t;
+    for (;; ++last) {
+        const int t = cut(sh.at(last + 1));
+        if (last == c) j1 = t;
+        if (t == tiles) break;
+    }
     if (tiles == 0 ? at < sh.at(c) || at >= sh.at(c + 1) : j0 >= j1) return false;
     u->row0 = s.start + pr * q2;
     u->tokens[0] = a;
@@ -124,20 +132,12 @@ __host__ __device__ __forceinline__ bool rg_unit(const RgLine& line, const RgSha
     const int ea = tiles_a < j1 ? tiles_a : j1, eb = tiles_b < j1 ? tiles_b : j1;
     u->tiles[0] = ea > j0 ? ea - j0 : 0;
     u->tiles[1] = eb > j0 ? eb - j0 : 0;
-    u->slot = -1;
-    u->first = c;
-    u->parts = 1;
-    u->counter = 0;
     u->valid = 1;
-    if (tiles > 0 && (j0 > 0 || j1 < tiles)) {
-        int first = c, last = c;                 // the CTAs with parts are neighbours
-        while (cut(sh.at(first)) > 0) --first;
-        while (cut(sh.at(last + 1)) < tiles) ++last;
-        u->slot = 2 * c + (at < sh.at(c) ? 0 : 1);
-        u->first = first;
-        u->parts = last - first + 1;
-        u->counter = 2 * first + (at < sh.at(first) ? 0 : 1);
-    }
+    const bool whole = tiles == 0 || first == last;
+    u->slot = whole ? -1 : 2 * c + (at < sh.at(c) ? 0 : 1);
+    u->first = whole ? c : first;
+    u->parts = whole ? 1 : last - first + 1;
+    u->counter = whole ? 0 : 2 * first + (at < sh.at(first) ? 0 : 1);
     return true;
 }
 
