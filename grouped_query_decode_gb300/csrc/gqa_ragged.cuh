@@ -14,10 +14,10 @@
 // of units that shares cut leave (O, m, l) in the workspace, and the CTA that
 // arrives last merges them in the order of the parts.
 //
-// Warps: 0-3 and 4-7 softmax of A and B, a thread per row; 8-11 outputs; 12 issues
-// the products, always one of A, one of B, so that each tile's softmax runs behind
-// the other's products; 13 loads Q and K by TMA, a lane per page, 14 V, of which
-// it mends the tiles that reach past the first row's limit; 15 plans and hands the
+// Warps: 0-7 and 8-15 softmax of A and B, two threads per row, 64 keys of a tile
+// each; 16-19 outputs; 20 issues the products, always one of A, one of B, so that each tile's softmax runs behind
+// the other's products; 21 loads Q and K by TMA, a lane per page, 22 V, of which
+// it mends the tiles that reach past the first row's limit; 23 plans and hands the
 // units out through a ring in shared memory. Every wait is bounded; after one has expired
 // the CTA runs through its units without work, so that the counters end at zero.
 //
@@ -37,89 +37,44 @@
 
 namespace gqa {
 
-constexpr int kRgUnits = 4;              // ring of units
-constexpr int kRgThreads = 512;
+constexpr int kRgThreads = 768;
+constexpr int kRgOut = 16, kRgMma = 20, kRgLoadK = 21, kRgLoadV = 22, kRgPlan = 23;   // first warps of the roles
 constexpr float kRgSlack = 8.0f;         // p <= 2^8 before the reference moves
-constexpr int kRgFirst = 64;             // keys whose weights are handed over ahead of the tile's others
 
 template <int D>
 struct RgShape {
     static constexpr int kBlock = 128 * 128;              // 128 rows x 128 B, 128-byte swizzle
     static constexpr int kBlocks = D / 64;
     static constexpr int kTile = kBlocks * kBlock;        // Q, K or V of one tile
-    static constexpr int kStages = D == 128 ? 4 : 8;      // K and V tiles, in turn
-    static constexpr int kMlBytes = 2 * 128 * 8;
-    static constexpr int kBadBytes = kRgUnits * D * 4;
+    // K and V tiles in rings of their own, each filled by a warp of its own.
+    static constexpr int kStagesK = D == 128 ? 2 : 5, kStagesV = D == 128 ? 2 : 5, kStages = kStagesK + kStagesV;
+    static constexpr int kMlBytes = 2 * 128 * (8 + 8 + 4);
     static constexpr int kUnitBytes = kRgUnits * 64;
-    static constexpr int kMiscBytes = 512;
+    static constexpr int kMiscBytes = 384;
     static constexpr int kBars = 3 * kStages + 2 * 10 + 2 * kRgUnits + 2;
     static constexpr int kSmemBytes =
-        1024 + 2 * kTile + kStages * kTile + kMlBytes + kBadBytes + kUnitBytes + kMiscBytes + 8 * kBars;
-    // Columns: S_A | S_B | O_A | O_B, with P over the first half of its S; D = 64
+        2 * kTile + kStages * kTile + kMlBytes + kUnitBytes + kMiscBytes + 8 * kBars;
+    // Columns: S_A | S_B | O_A | O_B, with P over S, that of each 64 keys over the first
+    // half of their scores; D = 64
     // has room for P apart (S_A | S_B | P_A | P_B | O_A | O_B), so that the next
     // scores wait only until these have been read.
     static constexpr bool kApart = D == 64;
     static constexpr uint32_t kColS = 0, kColP = kApart ? 256 : 0, kStepP = kApart ? 64 : 128, kColO = kApart ? 384 : 256;
+    static constexpr uint32_t kHalfP = kApart ? 32 : 64;  // columns from the weights of the first 64 keys to the others'
     static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
     static_assert((2 + kStages) * kTile >= 1024 + 180 * (D * 4 + 4), "one row of all parts");
 };
 
-template <int N>
-__device__ __forceinline__ void more_registers() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void fewer_registers() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-#define RG_8(f, i) f(i), f(i + 1), f(i + 2), f(i + 3), f(i + 4), f(i + 5), f(i + 6), f(i + 7)
-#define RG_64(f) RG_8(f, 0), RG_8(f, 8), RG_8(f, 16), RG_8(f, 24), RG_8(f, 32), RG_8(f, 40), RG_8(f, 48), RG_8(f, 56)
-#define RG_OUT(i) "=f"(r[i])
-#define RG_BOTH(i) "+f"(r[i])
-
-// 64 fp32 columns of this thread's lane, under way until tmem_ld_wait has seen them.
-__device__ __forceinline__ void tmem_ld64_start(uint32_t taddr, float* r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, "
-        "%36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, "
-        "%57, %58, %59, %60, %61, %62, %63}, [%64];"
-        : RG_64(RG_OUT)
-        : "r"(taddr));
-}
-// Waits for this thread's loads; the columns are named so that nothing reads them earlier.
-__device__ __forceinline__ void tmem_ld_wait(float* r) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : RG_64(RG_BOTH));
-}
-
-// Maximum of 64 values, by eight chains.
-__device__ __forceinline__ float max64(const float* s) {
-    float t[8];
+// Maximum of 32 values, by four chains.
+__device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
+    float t[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) t[k] = fmaxf(s[k], s[k + 8]);
+    for (int k = 0; k < 4; ++k) t[k] = fmaxf(__uint_as_float(s[k]), __uint_as_float(s[k + 4]));
 #pragma unroll
-    for (int i = 16; i < 64; i += 16)
+    for (int i = 8; i < 32; i += 8)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) t[k] = fmax3(t[k], s[i + k], s[i + 8 + k]);
-    return fmaxf(fmax3(t[0], t[1], t[2]), fmax3(fmax3(t[3], t[4], t[5]), t[6], t[7]));
-}
-
-// Weights 2^(s * scale + neg) of keys [K0, K1) into their columns of P, and their sums.
-template <int K0, int K1>
-__device__ __forceinline__ void rg_weights(const float* s, float2 scale, float2 neg, float2 (&sum)[4], uint32_t p_t) {
-#pragma unroll
-    for (int k = K0; k < K1; k += 32) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-            const float2 z = fma_x2(make_float2(s[k + i], s[k + i + 1]), scale, neg);
-            const float2 e = make_float2(fast_exp2(z.x), fast_exp2(z.y));
-            sum[(i / 2) & 3] = add_x2(sum[(i / 2) & 3], e);
-            pk[i / 2] = pack_bf16x2(e.x, e.y);
-        }
-        tmem_st16(p_t + k / 2, pk);
-    }
+        for (int k = 0; k < 4; ++k) t[k] = fmax3(t[k], __uint_as_float(s[i + k]), __uint_as_float(s[i + 4 + k]));
+    return fmaxf(fmax3(t[0], t[1], t[2]), t[3]);
 }
 
 // A unit with rows in tile A alone: its key tiles go to both pipelines in turn, so
@@ -151,7 +106,7 @@ static __device__ __noinline__ bool rg_wait_slow(uint32_t bar, uint32_t parity, 
                                           uint64_t tmo) {
     return wait_phase(bar, parity, abort_flag, status, tmo);
 }
-__device__ __forceinline__ bool rg_wait_longer(uint32_t bar, uint32_t parity, uint64_t limit) {
+static __device__ __noinline__ bool rg_wait_longer(uint32_t bar, uint32_t parity, uint64_t limit) {
     const uint64_t t0 = global_timer_ns();
     while (!mbar_try_wait(bar, parity))
         if (global_timer_ns() - t0 > limit) return false;
@@ -262,18 +217,23 @@ __global__ void __launch_bounds__(kRgThreads, 1)
     gqa_ragged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ RaggedParams p) {
     using RS = RgShape<D>;
-    constexpr int S = RS::kStages;
+    constexpr int S = RS::kStages, SK = RS::kStagesK, SV = RS::kStagesV;       // V's stages follow K's
     constexpr uint32_t kBlock = RS::kBlock, kTile = RS::kTile;
 
     extern __shared__ __align__(1024) unsigned char smem_raw[];
+    // There is no static shared memory, so that the dynamic one starts on the 1024
+    // bytes of the swizzle atom.
     const uint32_t raw = smem_addr(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
-    const uint32_t q_s = base, ring_s = q_s + 2 * kTile;
-    unsigned char* gen = smem_raw + (ring_s + S * kTile - raw);
+    if (raw & 1023u) return;
+    const uint32_t q_s = raw, ring_s = q_s + 2 * kTile;
+    unsigned char* gen = smem_raw + (2 + S) * kTile;
     float2* const ml = reinterpret_cast<float2*>(gen);               // [2][128]
+    float* const top_s = reinterpret_cast<float*>(gen + 2048);       // [2][2][128]: maxima of each half of a tile
+    float* const sum_s = reinterpret_cast<float*>(gen + 4096);       // [2][128]: sums of the second halves
     gen += RS::kMlBytes;
-    int* const bad = reinterpret_cast<int*>(gen);                    // [units][D]: first position with such a value
-    gen += RS::kBadBytes;
+    // Per column the first position of a value that is not finite, in the workspace:
+    // it is hardly ever touched.
+    int* const bad = p.bad + (size_t)blockIdx.x * kRgUnits * D;      // [units][D]
     RgUnit* const units = reinterpret_cast<RgUnit*>(gen);
     gen += RS::kUnitBytes;
     uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(gen);
@@ -287,7 +247,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
     gen += RS::kMiscBytes;
     const uint32_t full = smem_addr(gen), empty = full + 8 * S, mended = empty + 8 * S;
     const uint32_t q_full = mended + 8 * S, q_empty = q_full + 16, s_full = q_empty + 16, p_full = s_full + 16;
-    const uint32_t p_rest = p_full + 16, s_free = p_rest + 16, pv_done = s_free + 16;
+    const uint32_t s_free = p_full + 16, pv_done = s_free + 16;
     const uint32_t o_full = pv_done + 16, o_empty = o_full + 16, ml_full = o_empty + 16, fin = ml_full + 16;
     const uint32_t u_full = fin + 8, u_empty = u_full + 8 * kRgUnits, merge_bar = u_empty + 8 * kRgUnits;
 
@@ -304,9 +264,8 @@ __global__ void __launch_bounds__(kRgThreads, 1)
             mbar_init(q_full + 8 * x, 1);
             mbar_init(q_empty + 8 * x, 1);
             mbar_init(s_full + 8 * x, 1);
-            mbar_init(p_full + 8 * x, 4);
-            mbar_init(p_rest + 8 * x, 4);
-            mbar_init(s_free + 8 * x, 4);
+            mbar_init(p_full + 8 * x, 8);
+            mbar_init(s_free + 8 * x, 8);
             mbar_init(pv_done + 8 * x, 1);
             mbar_init(o_full + 8 * x, 1);
             mbar_init(o_empty + 8 * x, 4);
@@ -316,7 +275,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
         mbar_init(merge_bar, 1);
         for (int i = 0; i < kRgUnits; ++i) {
             mbar_init(u_full + 8 * i, 1);
-            mbar_init(u_empty + 8 * i, 15);       // softmax and output warps, products, loads
+            mbar_init(u_empty + 8 * i, 23);       // softmax and output warps, products, loads
         }
         for (int i = 0; i < kRgUnits; ++i) bad_flag[i] = 0;
         *abort_flag = 0;
@@ -324,11 +283,11 @@ __global__ void __launch_bounds__(kRgThreads, 1)
         first_s[1] = p.B;
         fence_barrier_init();
     }
-    if (warp == 12) {
+    if (warp == kRgMma) {
         tmem_alloc(smem_addr(tmem_slot), 512);
         tmem_relinquish();
     }
-    if (warp == 13 && lane < 3) tma_prefetch_desc(lane == 0 ? &tm_q : lane == 1 ? &tm_k : &tm_v);
+    if (warp == kRgLoadK && lane < 3) tma_prefetch_desc(lane == 0 ? &tm_q : lane == 1 ? &tm_k : &tm_v);
     pdl_launch_dependents();
     pdl_wait_primary();
 
@@ -388,9 +347,8 @@ __global__ void __launch_bounds__(kRgThreads, 1)
         return mbar_try_wait(bar, parity) || rg_wait_longer(bar, parity, 8 * tmo);
     };
 
-    if (warp >= 12) {
-        fewer_registers<80>();
-        if (warp == 15) {
+    if (warp >= kRgMma) {
+        if (warp == kRgPlan) {
             // ------------------------------------------------------------ plan
             // Sequence b, whose units start at `at` on the line, KV head g, pair pr.
             const RgShares sh = *shares;
@@ -460,13 +418,14 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 }
                 __syncwarp();
             }
-        } else if (warp >= 13) {
+        } else if (warp >= kRgLoadK) {
             // ------------- loads: Q and K from warp 13, V from warp 14, which mends it
-            const bool v_warp = warp == 14;
+            const bool v_warp = warp == kRgLoadV;
             const int page_rows = PAGED ? min(1 << p.page_shift, kRgTile) : kRgTile;
             const int boxes = kRgTile / page_rows;
             const CUtensorMap* const tm = v_warp ? &tm_v : &tm_k;
-            uint32_t it = v_warp, nq = 0;            // ring place; phases of Q_x in bit x
+            const uint32_t stages = v_warp ? SV : SK, stage0 = v_warp ? SK : 0;
+            uint32_t stage = 0, turn = 0, nq = 0;    // stage of the ring, its parity; phases of Q_x in bit x
             // Copies issued: bit s, bit 16 + x; and the parity of the last of each.
             uint32_t issued = 0, parity = 0;
             auto note = [&](int bit, uint32_t phase) {
@@ -512,16 +471,16 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 // With V, step j issues tile j and then sees tile j - 1 land, before the
                 // next copy goes to that one's stage.
 #pragma unroll 1
-                for (int j = 0; j < all + v_warp; ++j, it += 2) {
+                for (int j = 0; j < all + v_warp; ++j) {
                     const int t0 = (u.j0 + j) * kRgTile;
                     if (j < all) {
                         if (PAGED && j == 0) now = slab(0);
                         const int then = PAGED && j + 1 < all ? slab(j + 1) : 0;
-                        const uint32_t s = it % S, bar = full + 8 * s;
-                        bool ok = !*abort_flag && wait(empty + 8 * s, (it / S) ^ 1);
+                        const uint32_t s = stage0 + stage, bar = full + 8 * s;
+                        bool ok = !*abort_flag && wait(empty + 8 * s, turn ^ 1);
                         ok = __all_sync(0xffffffffu, ok);
                         if (ok && !(blockIdx.x == 0 && !v_warp && n == 0 && j == p.skip_tile)) {     // injected fault
-                            note(s, it / S);
+                            note(s, turn);
                             if (lane == 0) mbar_arrive_expect_tx(bar, kTile);
                             __syncwarp();
                             const uint32_t dst = ring_s + s * kTile + lane * page_rows * 128;
@@ -537,10 +496,16 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                         }
                         now = then;
                     }
+                    // The tile before: its stage, and the parity of its turn.
+                    const uint32_t s = stage0 + (stage == 0 ? stages : stage) - 1, was = stage == 0 ? turn ^ 1 : turn;
+                    if (j < all && ++stage == stages) {
+                        stage = 0;
+                        turn ^= 1;
+                    }
                     if (!v_warp || j == 0) continue;
                     const int t1 = t0 - kRgTile;
-                    const uint32_t s = (it - 2) % S, v_s = ring_s + s * kTile;
-                    const bool ok = !*abort_flag && wait(full + 8 * s, (it - 2) / S);
+                    const uint32_t v_s = ring_s + s * kTile;
+                    const bool ok = !*abort_flag && wait(full + 8 * s, was);
                     if (!__all_sync(0xffffffffu, ok) || t1 + kRgTile - 1 <= lim) continue;
                     // Rows [r0, r1) are seen by some, those from r1 on by none.
                     const int r0 = max(0, lim + 1 - t1), r1 = max(0, min(kRgTile, last + 1 - t1));
@@ -567,8 +532,9 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                         int* const col = bad + slot * D;
                         if (!any_bad)
 #pragma unroll 1
-                            for (int i = lane; i < D; i += 32) col[i] = 0x7fffffff;
+                            for (int i = lane; i < D; i += 32) __stcg(col + i, 0x7fffffff);
                         any_bad = true;
+                        __threadfence();
                         __syncwarp();
 #pragma unroll 1
                         for (int i = r0 * kChunks + lane; i < r1 * kChunks; i += 32) {
@@ -582,7 +548,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                                 atomicMin(col + (i % kChunks) * 8 + k, t1 + i / kChunks);
                             }
                         }
-                        __threadfence_block();
+                        __threadfence();
                         __syncwarp();
                         if (lane == 0) *reinterpret_cast<volatile int*>(bad_flag + slot) = 1 + (int)(n / kRgUnits);
                     }
@@ -590,7 +556,6 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(mended + 8 * s);
                 }
-                if (v_warp) it -= 2;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(u_empty + 8 * (n % kRgUnits));
             }
@@ -629,19 +594,19 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                     if (!f.valid) return false;
                     const RgSteps st(f);
                     next = {st.a, st.b, max(st.a, st.b), f.j0, f.pos0, it, st.dual};
-                    it += 2 * max(f.tiles[0], f.tiles[1]);
+                    it += max(f.tiles[0], f.tiles[1]);
                     mbar_arrive(u_empty + 8 * (n % kRgUnits));
                     ++n;
                     if (next.all > 0) return true;
                 }
                 return false;
             };
-            // S_X for the K tile at ring place i.
+            // S_X for K tile i of all.
             auto scores = [&](uint32_t i, int x, bool first, bool last, bool release) {
-                const uint32_t s = i % S;
+                const uint32_t s = i % SK;
                 if (first) wait_next(q_full + 8 * x, x, 0);
                 if (RS::kApart) wait_next(s_free + 8 * x, 6 + x, 1);
-                wait_one(full + 8 * s, i / S);
+                wait_one(full + 8 * s, i / SK);
                 if (!ok) return;
                 tc_fence_after();
                 const uint64_t a = kDescK + ((q_s + x * kTile) >> 4), b = kDescK + ((ring_s + s * kTile) >> 4);
@@ -656,11 +621,11 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 if (release) umma_commit(empty + 8 * s);
                 issued = true;
             };
-            // O_X += P_X V for the V tile at ring place i.
+            // O_X += P_X V for V tile i of all.
             auto values = [&](uint32_t i, int x, bool fresh, bool mend, bool first, bool last, bool release) {
-                const uint32_t s = i % S;
+                const uint32_t s = SK + i % SV;
                 if (fresh) {
-                    wait_one((mend ? mended : full) + 8 * s, mend ? mends >> s : i / S);
+                    wait_one((mend ? mended : full) + 8 * s, mend ? mends >> s : i / SV);
                     if (mend) mends ^= 1u << s;
                 }
                 if (first) wait_next(o_empty + 8 * x, 4 + x, 1);
@@ -669,16 +634,11 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 wait_one(p_full + 8 * x, phases >> (2 + x));
                 if (!ok) return;
                 tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < kRgFirst / 16; ++k)
-                    umma_bf16_ts(to, a + k * 8, b + k * (16 * 128 >> 4), kIdescO, !first || k > 0 ? 1u : 0u);
-                wait_one(p_rest + 8 * x, phases >> (2 + x));
                 phases ^= 4u << x;
-                if (!ok) return;
-                tc_fence_after();
 #pragma unroll
-                for (int k = kRgFirst / 16; k < kRgTile / 16; ++k)
-                    umma_bf16_ts(to, a + k * 8, b + k * (16 * 128 >> 4), kIdescO, 1u);
+                for (int k = 0; k < kRgTile / 16; ++k)
+                    umma_bf16_ts(to, a + (k >> 2) * RS::kHalfP + (k & 3) * 8, b + k * (16 * 128 >> 4), kIdescO,
+                                 !first || k > 0 ? 1u : 0u);
                 if (RS::kApart) umma_commit(pv_done + 8 * x);
                 if (last) umma_commit(o_full + 8 * x);
                 if (release) umma_commit(empty + 8 * s);
@@ -696,18 +656,18 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                         // What S_X holds next: this unit's next tile of X, or the next unit's first.
                         bool go = j + 1 < steps, lead = false;
                         const int v = (j << u.dual) + (x & u.dual);
-                        uint32_t i = u.it + 2 * v + (2 << u.dual);
+                        uint32_t i = u.it + v + (1 << u.dual);
                         bool last = j + 2 == steps, release = u.dual || x == 1 || j + 1 >= u.b;
                         if (!go && end && more) {
                             const int to = x ? next.b : next.a;
                             go = lead = to > 0;
-                            i = next.it + 2 * (x & next.dual);
+                            i = next.it + (x & next.dual);
                             last = to == 1;
                             release = next.dual || x == 1 || next.b == 0;
                         }
                         if (RS::kApart && go) scores(i, x, lead, last, release);
                         if (j < steps)
-                            values(u.it + 2 * v + 1, x, u.dual || x == 0 || j >= u.a,
+                            values(u.it + v, x, u.dual || x == 0 || j >= u.a,
                                    (u.j0 + v) * kRgTile + kRgTile - 1 > u.lim, j == 0, j + 1 == steps,
                                    u.dual || x == 1 || j >= u.b);
                         if (!RS::kApart && go) scores(i, x, lead, last, release);
@@ -722,9 +682,8 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 if (!rg_wait_longer(fin, 0, tmo)) atomicOr(p.status, kStatusTimeout);
             }
         }
-    } else if (warp >= 8) {
+    } else if (warp >= kRgOut) {
         // ---------------------------------------------------------------- outputs
-        fewer_registers<80>();
         const int row = threadIdx.x & 127;
         const int tok = p.by_heads(row);
         const bool in_tile = row < p.tq * p.heads_per_group;
@@ -822,7 +781,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                     if (flagged && valid && l != 0.f) {          // a value that is not finite, where the row sees it
 #pragma unroll 1
                         for (int c = 0; c < D; ++c) {
-                            if (bad[(n % kRgUnits) * D + c] > lim) continue;
+                            if (__ldcg(bad + (n % kRgUnits) * D + c) > lim) continue;
                             if (slot < 0)
                                 p.out[orow * D + c] = 0x7fc0;
                             else
@@ -843,7 +802,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 // The CTA whose part arrives last merges the unit, once it has no other work:
                 // its own part of a unit that goes on in the next CTA is its last one. The
                 // barrier orders the part's stores before the arrival, which releases them.
-                named_sync(1, 128);
+                named_sync(9, 128);
                 if (row == 0 && arrive_last(p.counters + u.counter, p.tag, u.parts)) todo[(*todos)++] = u;
             }
             __syncwarp();
@@ -851,132 +810,135 @@ __global__ void __launch_bounds__(kRgThreads, 1)
         }
     } else {
         // ---------------------------------------------------------------- softmax
-        more_registers<176>();
-        const int x = warp >> 2, row = threadIdx.x & 127;
+        // Half h of tile X's keys. Nothing here is left out when a wait has expired: the
+        // two warps of the same rows meet at named barriers, which have no time limit.
+        const int x = warp >> 3, h = (warp >> 2) & 1, row = threadIdx.x & 127;
         const int tok = p.by_heads(row);
         const bool in_tile = row < p.tq * p.heads_per_group;
-        const uint32_t s_t = tmem + ((uint32_t)((warp & 3) * 32) << 16) + RS::kColS + x * 128;
-        const uint32_t o_t = tmem + ((uint32_t)((warp & 3) * 32) << 16) + RS::kColO + x * D;
-        const uint32_t p_t = tmem + ((uint32_t)((warp & 3) * 32) << 16) + RS::kColP + x * RS::kStepP;
-        // No calls from here: a tile's scores are in registers.
-        auto wait_here = [&](uint32_t bar, uint32_t parity) {
-            return wait_phase(bar, parity & 1, abort_flag, p.status, tmo);
-        };
-        auto next_here = [&](uint32_t n) {
-            const uint64_t t0 = global_timer_ns();
-            while (!mbar_try_wait(u_full + 8 * (n % kRgUnits), (n / kRgUnits) & 1))
-                if (global_timer_ns() - t0 > 8 * tmo) return false;
-            return true;
-        };
-        uint32_t ns = 0, nu = 0, nd = 0;         // score tiles, units, products so far
-        for (uint32_t n = 0; next_here(n); ++n) {
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t s_t = lanes + RS::kColS + x * 128 + h * 64, p_t = lanes + RS::kColP + x * RS::kStepP + h * RS::kHalfP;
+        const uint32_t o_t = lanes + RS::kColO + x * D + h * (D / 2);
+        const int pair = 1 + x * 4 + (warp & 3);
+        float* const my_top = top_s + (x * 2 + h) * 128 + row;
+        const float* const other_top = top_s + (x * 2 + (h ^ 1)) * 128 + row;
+        uint32_t ns = 0, nu = 0;                 // tiles, units so far
+        for (uint32_t n = 0; next_unit(n); ++n) {
             __syncwarp();
             const RgUnit& u = units[n % kRgUnits];
             if (!u.valid) break;
             const RgSteps st(u);
-            const int tiles = x ? st.b : st.a, j0 = u.j0 + (st.dual ? x : 0), xr = st.dual ? 0 : x;
-            const bool dual = st.dual;
+            const int tiles = x ? st.b : st.a, xr = st.dual ? 0 : x;
             const int lim = in_tile && tok < u.tokens[xr] ? u.pos0 + xr * p.tq + tok : -1;
+            int t0 = (u.j0 + (st.dual ? x : 0)) * kRgTile + h * 64;      // first key of this half
+            const int step = st.dual ? 2 * kRgTile : kRgTile;
             __syncwarp();
             if (lane == 0) mbar_arrive(u_empty + 8 * (n % kRgUnits));
             if (tiles == 0) continue;
             const bool idle = __all_sync(0xffffffffu, lim < 0);      // no row of this warp sees anything
             float m = -INFINITY, l = 0.f;
-            for (int j = 0; j < tiles; ++j, ++ns) {
-                bool ok = !*abort_flag && wait_here(s_full + 8 * x, ns);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) continue;
-                tc_fence_after();
-                if (idle) {
-                    if (RS::kApart) {
-                        // No arrival for this tile's P may count for the one before.
-                        if (lane == 0) mbar_arrive(s_free + 8 * x);
-                        if (nd > 0) ok = wait_here(pv_done + 8 * x, nd - 1);
-                        ++nd;
-                        if (!__all_sync(0xffffffffu, ok)) continue;
-                    }
-                    if (lane == 0) {
-                        mbar_arrive(p_full + 8 * x);
-                        mbar_arrive(p_rest + 8 * x);
-                    }
-                    continue;
-                }
-                float s[kRgTile];
-                tmem_ld64_start(s_t, s);
-                tmem_ld_wait(s);
-                tmem_ld64_start(s_t + 64, s + 64);
-                const int t0 = (j0 + (dual ? 2 * j : j)) * kRgTile;
-                const bool edge = t0 + kRgTile - 1 > lim;
-                if (edge) {
-#pragma unroll
-                    for (int i = 0; i < 64; ++i) s[i] = t0 + i <= lim ? s[i] : -INFINITY;
-                }
-                float top = max64(s);
-                tmem_ld_wait(s + 64);
-                if (RS::kApart) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(s_free + 8 * x);
-                }
-                if (edge) {
-#pragma unroll
-                    for (int i = 64; i < kRgTile; ++i) s[i] = t0 + i <= lim ? s[i] : -INFINITY;
-                }
-                top = fmaxf(top, max64(s + 64)) * p.scale_log2;
-                const bool up = top > m + kRgSlack;
-                const float mn = up ? top : m, ref = mn == -INFINITY ? 0.f : mn;
-                const float2 scale = make_float2(p.scale_log2, p.scale_log2), neg = make_float2(-ref, -ref);
-                float2 sum[4] = {};
-                // With P apart, the product before has read it and O_X is settled only once
-                // it is done; otherwise these scores came after it.
-                if (RS::kApart) {
-                    if (nd > 0) ok = wait_here(pv_done + 8 * x, nd - 1);
-                    ok = __all_sync(0xffffffffu, ok);
-                    ++nd;
-                    if (!ok) continue;
-                    tc_fence_after();
-                }
-                if (j > 0 && __any_sync(0xffffffffu, up)) {
-                    const float a = up ? fast_exp2(m - ref) : 1.f;
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(o_t + c, o);
+            for (int j = 0; j < tiles; ++j, ++ns, t0 += step) {
+                wait(s_full + 8 * x, ns);
+                __syncwarp();
+                tc_fence_after();
+                float ref = 0.f;
+                if (!idle) {
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < 64; c += 32) {
+                        uint32_t s[32];
+                        tmem_ld32(s_t + c, s);
+                        const int see = lim - t0 - c;
+                        if (see < 31) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
-                        tmem_st16(o_t + c, o);
+                            for (int i = 0; i < 32; ++i) s[i] = i <= see ? s[i] : 0xff800000u;
+                        }
+                        top = fmaxf(top, max32(s));
                     }
+                    *my_top = top;
+                    named_sync(pair, 64);
+                    top = fmaxf(top, *other_top) * p.scale_log2;
+                    const bool up = top > m + kRgSlack;
+                    const float mn = up ? top : m;
+                    ref = mn == -INFINITY ? 0.f : mn;
+                    // With P apart, the product before has read it and O_X is settled only once
+                    // it is done; otherwise these scores came after it.
+                    if (RS::kApart) {
+                        if (ns > 0) wait(pv_done + 8 * x, ns - 1);
+                        __syncwarp();
+                        tc_fence_after();
+                    }
+                    if (__any_sync(0xffffffffu, up)) {
+                        const float a = up ? fast_exp2(m - ref) : 1.f;
+                        if (j > 0)
+#pragma unroll 1
+                            for (int c = 0; c < D / 2; c += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(o_t + c, o);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+                                tmem_st16(o_t + c, o);
+                            }
+                        l *= a;
+                        m = mn;
+                    }
+                    const float2 scale = make_float2(p.scale_log2, p.scale_log2), neg = make_float2(-ref, -ref);
+                    float2 sum[2] = {};
+#pragma unroll 1
+                    for (int c = 0; c < 64; c += 32) {
+                        uint32_t s[32], w[16];
+                        tmem_ld32(s_t + c, s);
+                        if (RS::kApart && c == 32) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(s_free + 8 * x);
+                        }
+                        const int see = lim - t0 - c;
+                        if (see < 31) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) s[i] = i <= see ? s[i] : 0xff800000u;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float2 z = fma_x2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), scale, neg);
+                            const float2 e = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+                            sum[(i / 2) & 1] = add_x2(sum[(i / 2) & 1], e);
+                            w[i / 2] = pack_bf16x2(e.x, e.y);
+                        }
+                        tmem_st16(p_t + c / 2, w);
+                    }
+                    sum[0] = add_x2(sum[0], sum[1]);
+                    l += sum[0].x + sum[0].y;
+                    tmem_st_wait();
+                } else if (RS::kApart) {
+                    // No arrival for this tile's P may count for the one before.
+                    if (lane == 0) mbar_arrive(s_free + 8 * x);
+                    if (ns > 0) wait(pv_done + 8 * x, ns - 1);
                 }
-                if (up) l *= fast_exp2(m - ref);
-                m = mn;
-                rg_weights<0, kRgFirst>(s, scale, neg, sum, p_t);
-                tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + 8 * x);
-                rg_weights<kRgFirst, kRgTile>(s, scale, neg, sum, p_t);
-                sum[0] = add_x2(add_x2(sum[0], sum[1]), add_x2(sum[2], sum[3]));
-                l += sum[0].x + sum[0].y;
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_rest + 8 * x);
             }
-            // The unit before has been read from here once its O is given back.
-            if (!*abort_flag) wait_here(o_empty + 8 * x, nu ^ 1);
-            ml[x * 128 + row] = make_float2(m, l);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(ml_full + 8 * x);
+            if (!idle) {
+                if (h) sum_s[x * 128 + row] = l;
+                named_sync(pair, 64);
+                if (!h) l += sum_s[x * 128 + row];
+            }
+            if (!h) {
+                // The unit before has been read from here once its O is given back.
+                wait(o_empty + 8 * x, nu ^ 1);
+                ml[x * 128 + row] = make_float2(m, l);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ml_full + 8 * x);
+            }
             ++nu;
         }
     }
 
-    // All threads merge, with as many registers as at the start.
     __syncwarp();
-    if (warp < 8) fewer_registers<128>(); else more_registers<128>();
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == kRgMma) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -984,7 +946,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
     uint32_t phase = 0;
 #pragma unroll 1
     for (int i = 0; i < *todos; ++i)
-        rg_merge<D>(p, todo[i], smem_raw + (q_s - raw), (2 + S) * kTile, merge_bar, phase);
+        rg_merge<D>(p, todo[i], smem_raw, (2 + S) * kTile, merge_bar, phase);
 }
 
 template <int D, bool PAGED>

@@ -11,6 +11,8 @@
 
 namespace gqa {
 
+constexpr int kRgUnits = 4;              // units that a CTA has under way at most
+
 struct RaggedParams {
     const int32_t* cu;         // [B + 1]
     const int32_t* lens;       // [B], paged only
@@ -18,6 +20,7 @@ struct RaggedParams {
     uint16_t* out;             // [N, H, D] bf16
     float* lse;                // [N, H] or nullptr
     unsigned long long* counters;   // [grid][2]: arrivals of split units
+    int* bad;                  // [grid][kRgUnits][D]: first positions of values that are not finite
     float* part;               // [grid][2][slot]: O[256][D], m[256], l[256]
     unsigned long long tag;    // of this call, in the counters (48 bits)
     unsigned* status;
@@ -37,6 +40,7 @@ struct RaggedLaunch {
     cudaStream_t stream;
 };
 
+inline size_t rg_bad_bytes(int D, int grid) { return sizeof(int) * kRgUnits * (size_t)D * grid; }
 // A part's O, m and l: 256 rows of both tiles.
 __host__ __device__ constexpr size_t rg_slot_floats(int D) { return (size_t)256 * (D + 2); }
 inline size_t rg_counter_bytes(int grid) { return (sizeof(unsigned long long) * 2 * (size_t)grid + 255) & ~size_t(255); }

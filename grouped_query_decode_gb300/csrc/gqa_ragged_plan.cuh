@@ -55,9 +55,12 @@ struct RgLine {
     __host__ __device__ long long start(const RgSeq& s, int pr) const {
         return pr * (base(s) + kRgPad) + (long long)tq * pr * (pr + 1ll);
     }
+    // A key of a unit with rows in tile A alone counts three quarters: its tile takes
+    // 1.1 us, one of both row tiles 1.6 (a step of single tokens and chunks).
+    __host__ __device__ bool single(const RgSeq& s, int pr) const { return s.n - pr * 2 * tq <= tq; }
     __host__ __device__ long long length(const RgSeq& s, int pr) const {
-        const long long seen = (pr + 1ll) * 2 * tq;
-        return base(s) + kRgPad + (seen < s.n ? seen : s.n);
+        const long long seen = (pr + 1ll) * 2 * tq, keys = base(s) + (seen < s.n ? seen : s.n);
+        return (single(s, pr) ? keys - (keys >> 2) : keys) + kRgPad;
     }
     // Of one KV head.
     __host__ __device__ long long head(const RgSeq& s) const {
@@ -103,12 +106,13 @@ __host__ __device__ __forceinline__ bool rg_unit(const RgLine& line, const RgSha
     const int tiles_b = b == 0 || lim_b < 0 ? 0 : (lim_b >> kRgTileShift) + 1;
     const int tiles = tiles_b > tiles_a ? tiles_b : tiles_a;
     const long long len = line.length(s, pr);
+    const bool alone = line.single(s, pr);
     // Key tile that a boundary x cuts at. Parts below kRgMinPart tiles go to the neighbour.
     auto cut = [&](long long x) {
         const long long y = x - at;
         if (y <= 0) return 0;
         if (y >= len) return tiles;
-        const long long t = (y + kRgTile / 2) >> kRgTileShift;
+        const long long t = ((alone ? y + y * 85 / 256 : y) + kRgTile / 2) >> kRgTileShift;
         if (t < kRgMinPart) return 0;
         return t > tiles - kRgMinPart ? tiles : (int)t;
     };

@@ -29,7 +29,9 @@ int check_rows(const void* x, long long stride, int heads, int D) {
 }
 
 // One CTA per SM; the device's plan gives work to as many as there is work for.
-size_t workspace_need(int D, int grid) { return rg_counter_bytes(grid) + sizeof(float) * 2 * grid * rg_slot_floats(D); }
+size_t workspace_need(int D, int grid) {
+    return rg_counter_bytes(grid) + rg_bad_bytes(D, grid) + sizeof(float) * 2 * grid * rg_slot_floats(D);
+}
 
 struct Call {
     RaggedLaunch a = {};
@@ -50,7 +52,8 @@ int begin(Call& c, const void* q, const int32_t* cu, float scale, void* out, flo
     p.out = static_cast<uint16_t*>(out);
     p.lse = lse;
     p.counters = static_cast<unsigned long long*>(workspace);
-    p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + rg_counter_bytes(sms));
+    p.bad = reinterpret_cast<int*>(static_cast<char*>(workspace) + rg_counter_bytes(sms));
+    p.part = reinterpret_cast<float*>(reinterpret_cast<char*>(p.bad) + rg_bad_bytes(D, sms));
     p.tag = call_tag();
     wait_knobs(&p.wait_timeout_ns, &p.skip_tile);
     p.scale_log2 = scale * 1.4426950408889634f;

@@ -63,7 +63,7 @@ def check(plan, seqs, heads, G, grid=152):
                     at += max(u["tiles_a"], u["tiles_b"])
                     assert u["tiles_a"] == max(0, min(want[0], at) - u["j0"])
                     assert u["tiles_b"] == max(0, min(want[1], at) - u["j0"])
-                    load[u["cta"]] += max(u["tiles_a"], u["tiles_b"]) * 128 + 128
+                    load[u["cta"]] += max(u["tiles_a"], u["tiles_b"]) * (128 if tokens[1] else 96) + 256
                     assert u["parts"] == len(got) and u["first"] == got[0]["cta"]
                     if len(got) == 1:
                         assert u["slot"] == -1
