@@ -65,16 +65,39 @@ struct RgShape {
     static_assert((2 + kStages) * kTile >= 1024 + 180 * (D * 4 + 4), "one row of all parts");
 };
 
-// Maximum of 32 values, by four chains.
-__device__ __forceinline__ float max32(const uint32_t (&s)[32]) {
-    float t[4];
+// Scores of 16 keys, those from `see` + 1 on hidden.
+__device__ __forceinline__ void hide16(uint32_t (&s)[16], int see) {
+    if (see < 15) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) t[k] = fmaxf(__uint_as_float(s[k]), __uint_as_float(s[k + 4]));
+        for (int i = 0; i < 16; ++i) s[i] = i <= see ? s[i] : 0xff800000u;
+    }
+}
+
+// Weights 2^(s * scale + neg) of 16 keys, in pairs of bf16, their sums and the largest score.
+__device__ __forceinline__ void weights16(const uint32_t (&s)[16], float2 scale, float2 neg, float2 (&sum)[2],
+                                          float (&top)[2], uint32_t* w) {
 #pragma unroll
-    for (int i = 8; i < 32; i += 8)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) t[k] = fmax3(t[k], __uint_as_float(s[i + k]), __uint_as_float(s[i + 4 + k]));
-    return fmaxf(fmax3(t[0], t[1], t[2]), t[3]);
+    for (int i = 0; i < 16; i += 2) {
+        const float2 z = fma_x2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), scale, neg);
+        const float2 e = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+        sum[(i / 2) & 1] = add_x2(sum[(i / 2) & 1], e);
+        w[i / 2] = pack_bf16x2(e.x, e.y);
+        top[(i / 2) & 1] = fmax3(top[(i / 2) & 1], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+    }
+}
+
+// Whether any of a named barrier's 64 threads votes.
+__device__ __forceinline__ bool pair_any(int id, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 64, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(id)
+        : "memory");
+    return r != 0;
 }
 
 // A unit with rows in tile A alone: its key tiles go to both pipelines in turn, so
@@ -646,8 +669,49 @@ __global__ void __launch_bounds__(kRgThreads, 1)
             bool have = true;
             while (have) {
                 bool more = false;
+                int j = 0;
+                if (!RS::kApart && !u.dual && ok) {
+                    // Steps after which both tiles go on in this unit: what one thread spends on
+                    // instructions here, the tensor cores wait for.
+                    const int steady = min(u.a, u.b) - 1;
+                    uint32_t sv = u.it % SV, tv = (u.it / SV) & 1, sk = (u.it + 1) % SK, tk = ((u.it + 1) / SK) & 1;
 #pragma unroll 1
-                for (int j = 0; j < u.all; ++j) {
+                    for (; j < steady && ok; ++j) {
+                        const uint32_t v_lo = (ring_s + (SK + sv) * kTile) >> 4, k_lo = (ring_s + sk * kTile) >> 4;
+                        const bool mend = (u.j0 + j) * kRgTile + kRgTile - 1 > u.lim;
+                        wait_one((mend ? mended : full) + 8 * (SK + sv), mend ? mends >> (SK + sv) : tv);
+                        if (mend) mends ^= 1u << (SK + sv);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const uint32_t to = tmem + RS::kColO + x * D, a = tmem + RS::kColP + x * RS::kStepP;
+                            if (j == 0) wait_next(o_empty + 8 * x, 4 + x, 1);
+                            wait_one(p_full + 8 * x, phases >> (2 + x));
+                            phases ^= 4u << x;
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int k = 0; k < kRgTile / 16; ++k)
+                                umma_bf16_ts(to, a + (k >> 2) * RS::kHalfP + (k & 3) * 8, kDescV + (v_lo + k * (16 * 128 >> 4)),
+                                             kIdescO, j > 0 || k > 0 ? 1u : 0u);
+                            if (x == 1) umma_commit(empty + 8 * (SK + sv));
+                            if (x == 0) wait_one(full + 8 * sk, tk);
+                            if (!ok) break;
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint32_t off = ((k >> 2) * kBlock + (k & 3) * 32) >> 4;
+                                umma_bf16(tmem + RS::kColS + x * 128, kDescK + (((q_s + x * kTile) >> 4) + off), kDescK + (k_lo + off),
+                                          kIdescS, k > 0 ? 1u : 0u);
+                            }
+                            umma_commit(s_full + 8 * x);
+                            if (j + 2 == (x ? u.b : u.a)) umma_commit(q_empty + 8 * x);
+                            if (x == 1) umma_commit(empty + 8 * sk);
+                        }
+                        if (++sv == SV) sv = 0, tv ^= 1;
+                        if (++sk == SK) sk = 0, tk ^= 1;
+                    }
+                }
+#pragma unroll 1
+                for (; j < u.all; ++j) {
                     const bool end = j + 1 == u.all;
                     if (end) more = fetch();
 #pragma unroll 1
@@ -841,36 +905,39 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 wait(s_full + 8 * x, ns);
                 __syncwarp();
                 tc_fence_after();
-                float ref = 0.f;
-                if (!idle) {
-                    float top = -INFINITY;
+                bool settled = false;            // O_X holds all earlier keys, P is free
+                // The reference is the one of the tiles before as long as no score exceeds it by
+                // more than kRgSlack; otherwise (and with the first tile) the tile's maximum is
+                // taken first.
+                for (bool fresh = j == 0; !idle; fresh = true) {
+                    if (fresh) {
+                        float top = -INFINITY;
 #pragma unroll 1
-                    for (int c = 0; c < 64; c += 32) {
-                        uint32_t s[32];
-                        tmem_ld32(s_t + c, s);
-                        const int see = lim - t0 - c;
-                        if (see < 31) {
+                        for (int c = 0; c < 64; c += 16) {
+                            uint32_t s[16];
+                            tmem_ld16(s_t + c, s);
+                            hide16(s, lim - t0 - c);
+                            float t[2] = {top, top};
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) s[i] = i <= see ? s[i] : 0xff800000u;
+                            for (int i = 0; i < 16; i += 4) {
+                                t[0] = fmax3(t[0], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+                                t[1] = fmax3(t[1], __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
+                            }
+                            top = fmaxf(t[0], t[1]);
                         }
-                        top = fmaxf(top, max32(s));
-                    }
-                    *my_top = top;
-                    named_sync(pair, 64);
-                    top = fmaxf(top, *other_top) * p.scale_log2;
-                    const bool up = top > m + kRgSlack;
-                    const float mn = up ? top : m;
-                    ref = mn == -INFINITY ? 0.f : mn;
-                    // With P apart, the product before has read it and O_X is settled only once
-                    // it is done; otherwise these scores came after it.
-                    if (RS::kApart) {
-                        if (ns > 0) wait(pv_done + 8 * x, ns - 1);
-                        __syncwarp();
-                        tc_fence_after();
-                    }
-                    if (__any_sync(0xffffffffu, up)) {
-                        const float a = up ? fast_exp2(m - ref) : 1.f;
-                        if (j > 0)
+                        *my_top = top;
+                        named_sync(pair, 64);
+                        top = fmaxf(top, *other_top) * p.scale_log2;
+                        const bool up = top > m + kRgSlack;
+                        const float mn = up ? top : m;
+                        if (j > 0) {
+                            if (RS::kApart && !settled) {
+                                wait(pv_done + 8 * x, ns - 1);
+                                __syncwarp();
+                                tc_fence_after();
+                                settled = true;
+                            }
+                            const float a = up ? fast_exp2(m - mn) : 1.f;
 #pragma unroll 1
                             for (int c = 0; c < D / 2; c += 16) {
                                 uint32_t o[16];
@@ -879,38 +946,38 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                                 for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
                                 tmem_st16(o_t + c, o);
                             }
-                        l *= a;
+                            l *= a;
+                        }
                         m = mn;
                     }
+                    const float ref = m == -INFINITY ? 0.f : m;
                     const float2 scale = make_float2(p.scale_log2, p.scale_log2), neg = make_float2(-ref, -ref);
                     float2 sum[2] = {};
-#pragma unroll 1
-                    for (int c = 0; c < 64; c += 32) {
-                        uint32_t s[32], w[16];
-                        tmem_ld32(s_t + c, s);
-                        if (RS::kApart && c == 32) {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(s_free + 8 * x);
-                        }
-                        const int see = lim - t0 - c;
-                        if (see < 31) {
+                    float top[2] = {-INFINITY, -INFINITY};
+                    uint32_t w[32];
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) s[i] = i <= see ? s[i] : 0xff800000u;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
-                            const float2 z = fma_x2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), scale, neg);
-                            const float2 e = make_float2(fast_exp2(z.x), fast_exp2(z.y));
-                            sum[(i / 2) & 1] = add_x2(sum[(i / 2) & 1], e);
-                            w[i / 2] = pack_bf16x2(e.x, e.y);
-                        }
-                        tmem_st16(p_t + c / 2, w);
+                    for (int c = 0; c < 64; c += 16) {
+                        uint32_t s[16];
+                        tmem_ld16(s_t + c, s);
+                        hide16(s, lim - t0 - c);
+                        weights16(s, scale, neg, sum, top, w + c / 2);
                     }
+                    if (!fresh && pair_any(pair, fmaxf(top[0], top[1]) * p.scale_log2 > m + kRgSlack)) continue;
+                    if (RS::kApart) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(s_free + 8 * x);
+                        if (ns > 0 && !settled) wait(pv_done + 8 * x, ns - 1);
+                        __syncwarp();
+                        tc_fence_after();
+                    }
+                    tmem_st32(p_t, w);
                     sum[0] = add_x2(sum[0], sum[1]);
                     l += sum[0].x + sum[0].y;
                     tmem_st_wait();
-                } else if (RS::kApart) {
+                    break;
+                }
+                if (RS::kApart && idle) {
                     // No arrival for this tile's P may count for the one before.
                     if (lane == 0) mbar_arrive(s_free + 8 * x);
                     if (ns > 0) wait(pv_done + 8 * x, ns - 1);
