@@ -159,6 +159,7 @@ __device__ __forceinline__ void rg_merge(const RaggedParams& p, const RgUnit& u,
     const int block = min(128, (int)((room_bytes - 1024) / (n * (D * 4 + 4))));
     float* const inverse = reinterpret_cast<float*>(room);        // [128]
     float* const weights = inverse + 128;                         // [block][n]
+    asm volatile("fence.proxy.async;" ::: "memory");              // the parts were written by plain stores
     const uint32_t held = (512 + 4 * n * block + 127) & ~127u;    // O of the parts, [n][rows][D]
 #pragma unroll 1
     for (int x = 0; x < 2; ++x) {
@@ -177,7 +178,6 @@ __device__ __forceinline__ void rg_merge(const RaggedParams& p, const RgUnit& u,
             const int rows = min(block, rows_x - r0);
             if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, n * rows * D * 4);
             __syncthreads();
-            asm volatile("fence.proxy.async;" ::: "memory");      // the parts were written by plain stores
 #pragma unroll 1
             for (int i = threadIdx.x; i < n; i += kRgThreads)
                 bulk_load(smem_addr(room) + held + i * rows * D * 4, part(i) + (size_t)(x * 128 + r0) * D, rows * D * 4, bar);

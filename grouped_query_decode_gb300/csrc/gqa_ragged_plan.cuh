@@ -21,9 +21,9 @@ namespace gqa {
 
 constexpr int kRgTileShift = 7;
 constexpr int kRgTile = 1 << kRgTileShift;   // rows of a tile, and keys of a key tile
-constexpr int kRgPad = 256;           // what a unit counts beyond its keys
+constexpr int kRgPad = 384;           // what a unit counts beyond its keys
 constexpr int kRgMinShare = 512;      // least share of a CTA, in keys
-constexpr int kRgMinPart = 2;         // least key tiles of a part of a unit
+constexpr int kRgMinPart = 4;         // least key tiles of a part of a unit
 
 struct RgSeq {
     int start, n, T;                  // first row, new tokens, keys
