@@ -653,34 +653,40 @@ def gqa_rope_init(D, dims=None, interleaved=False, base=10000.0, scaling="none",
     return rope
 
 
-def _token_stride(name, t):
-    """Distance of the tokens of [N, heads, D], whose heads are dense."""
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [N, heads, D]")
-    N, heads, D = t.shape
-    if t.is_contiguous():
-        return heads * D
+def _row_stride(name, t, dt, dev, shape):
+    """Checks a packed tensor [N, heads, D] whose heads are dense; returns the
+    distance of its tokens in elements."""
+    if t.shape == shape and t.dtype is dt and t.get_device() == dev:      # the quick pass
+        s = t.stride()
+        if s[2] == 1 and s[1] == shape[2] and shape[0] > 1 and dev >= 0:
+            return s[0]
+    if t.dtype is not dt:
+        raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+    if t.get_device() < 0:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, others on cuda:{dev}: all tensors must be on one device")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, is {list(t.shape)}")
+    N, heads, D = shape
     s = t.stride()
-    if s[2] != 1 or (heads > 1 and s[1] != D):
+    if not t.is_contiguous() and (s[2] != 1 or (heads > 1 and s[1] != D)):
         raise ValueError(f"{name} must have dense heads (only its tokens may be apart)")
     return s[0] if N > 1 else heads * D
-
-
-def _check_strided(dev, named):
-    """dtype and device of (name, tensor, dtype) triples."""
-    for name, t, dt in named:
-        if t.dtype is not dt:
-            raise TypeError(f"{name} must be {dt}, got {t.dtype}")
-        d = t.get_device()
-        if d < 0:
-            raise TypeError(f"{name} must be a CUDA tensor")
-        if d != dev:
-            raise ValueError(f"{name} is on cuda:{d}, others on cuda:{dev}: all tensors must be on one device")
 
 
 def _check_rope(rope):
     if not isinstance(rope, RopeT):
         raise TypeError("rope must come from gqa_rope_init")
+
+
+def _launch(dev, fn, *args):
+    """_call for tensors that are there, so that CUDA is initialised."""
+    import torch
+    if torch._C._cuda_getDevice() == dev:
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
 
 
 def gqa_rope(rope, q, k, positions, q_out, k_out, inverse=False, stream=None):
@@ -690,29 +696,32 @@ def gqa_rope(rope, q, k, positions, q_out, k_out, inverse=False, stream=None):
     operator). Tokens may be apart, as in views of a fused projection's rows."""
     import torch
     _check_rope(rope)
-    bf, named = torch.bfloat16, []
-    dev = positions.get_device()
+    bf = torch.bfloat16
     if (q is None) != (q_out is None) or (k is None) != (k_out is None) or (q is None and k is None):
         raise ValueError("q comes with q_out and k with k_out, one of them at least")
+    dev = positions.get_device()
+    qp = qo = kp = ko = None
+    H = G = qs = qos = ks = kos = 0
+    for name, t in (("q", q), ("k", k)):
+        if t is not None and t.dim() != 3:
+            raise ValueError(f"{name} must be [N, heads, D]")
     if q is not None:
-        named += [("q", q, bf), ("q_out", q_out, bf)]
+        shape = q.shape
+        N, H, D = shape
+        qs, qos = _row_stride("q", q, bf, dev, shape), _row_stride("q_out", q_out, bf, dev, shape)
+        qp, qo = q.data_ptr(), q_out.data_ptr()
     if k is not None:
-        named += [("k", k, bf), ("k_out", k_out, bf)]
-    _check_strided(dev, named)
+        shape = k.shape
+        if q is not None and (shape[0] != N or shape[2] != D):
+            raise ValueError("k must be [N, heads, D] with q's N and D")
+        N, G, D = shape
+        ks, kos = _row_stride("k", k, bf, dev, shape), _row_stride("k_out", k_out, bf, dev, shape)
+        kp, ko = k.data_ptr(), k_out.data_ptr()
     _check_all(dev, (("positions", positions, torch.int32),))
-    strides = [_token_stride(name, t) for name, t, _ in named]
-    N, _, D = named[0][1].shape
-    for name, t, _ in named:
-        if t.shape[0] != N or t.shape[2] != D:
-            raise ValueError(f"{name} must be [N, heads, D] with the other tensors' N and D")
-    if positions.shape != (N,) or (q is not None and q_out.shape != q.shape) or (k is not None and k_out.shape != k.shape):
-        raise ValueError("positions must be [N], q_out like q, k_out like k")
-    qs, qos = (strides[0], strides[1]) if q is not None else (0, 0)
-    ks, kos = (strides[-2], strides[-1]) if k is not None else (0, 0)
-    rc = _call(dev, load().gqa_rope, ctypes.addressof(rope), None if q is None else q.data_ptr(),
-               None if k is None else k.data_ptr(), positions.data_ptr(), None if q is None else q_out.data_ptr(),
-               None if k is None else k_out.data_ptr(), N, 0 if q is None else q.shape[1],
-               0 if k is None else k.shape[1], D, qs, ks, qos, kos, 1 if inverse else 0, _raw_stream(stream, dev))
+    if positions.shape != (N,):
+        raise ValueError("positions must be [N]")
+    rc = _launch(dev, load().gqa_rope, ctypes.addressof(rope), qp, kp, positions.data_ptr(), qo, ko, N, H, G, D, qs, ks,
+                 qos, kos, 1 if inverse else 0, _raw_stream(stream, dev))
     if rc != GQA_OK:
         raise GQADecodeError(rc, "gqa_rope")
 
@@ -739,33 +748,30 @@ def gqa_append_paged(k_new, v_new, k_pages, v_pages, block_table, cu_new, seq_le
     D] where given, into q_out (which may be q)."""
     import torch
     bf, i32 = torch.bfloat16, torch.int32
-    dev = k_new.get_device()
-    named = [("k_new", k_new, bf), ("v_new", v_new, bf)]
     if (q is None) != (q_out is None):
         raise ValueError("q comes with q_out")
-    if q is not None:
-        named += [("q", q, bf), ("q_out", q_out, bf)]
     if rope is not None:
         _check_rope(rope)
-    _check_strided(dev, named)
+    dev = k_new.get_device()
     _check_all(dev, (("k_pages", k_pages, bf), ("v_pages", v_pages, bf), ("block_table", block_table, i32),
                      ("cu_new", cu_new, i32), ("seq_lens", seq_lens, i32)))
     B, num_pages, G, page_size, D, most = _paged_bf16_cache(k_pages, v_pages, block_table, seq_lens, cu_new)
-    strides = [_token_stride(name, t) for name, t, _ in named]
     N = k_new.shape[0]
-    if k_new.shape[1:] != (G, D) or v_new.shape != k_new.shape:
-        raise ValueError("k_new / v_new must be [N, G, D]")
-    H = 0
+    shape = (N, G, D)
+    ks, vs = _row_stride("k_new", k_new, bf, dev, shape), _row_stride("v_new", v_new, bf, dev, shape)
+    qp = qo = None
+    H = qs = qos = 0
     if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [N, H, D]")
         H = q.shape[1]
-        if q.shape != (N, H, D) or q_out.shape != q.shape:
-            raise ValueError("q / q_out must be [N, H, D]")
-    rc = _call(dev, load().gqa_append_paged, None if rope is None else ctypes.addressof(rope),
-               None if q is None else q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
-               None if q is None else q_out.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-               block_table.data_ptr(), cu_new.data_ptr(), seq_lens.data_ptr(), N, B, H, G, D,
-               strides[2] if H else 0, strides[0], strides[1], strides[3] if H else 0, page_size, num_pages, most,
-               _raw_stream(stream, dev))
+        shape = (N, H, D)
+        qs, qos = _row_stride("q", q, bf, dev, shape), _row_stride("q_out", q_out, bf, dev, shape)
+        qp, qo = q.data_ptr(), q_out.data_ptr()
+    rc = _launch(dev, load().gqa_append_paged, None if rope is None else ctypes.addressof(rope), qp, k_new.data_ptr(),
+                 v_new.data_ptr(), qo, k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+                 cu_new.data_ptr(), seq_lens.data_ptr(), N, B, H, G, D, qs, ks, vs, qos, page_size, num_pages, most,
+                 _raw_stream(stream, dev))
     if rc != GQA_OK:
         raise GQADecodeError(rc, "gqa_append_paged")
 
@@ -796,21 +802,21 @@ def gqa_prefill_ragged_workspace_bytes(N, B, H, G, D, device=None) -> int:
 
 
 def _ragged_outputs(dev, q, out, lse, workspace):
-    """Checks q, out, lse and workspace of a packed batch; returns N, H, D."""
+    """Checks q, out, lse and workspace of a packed batch; returns q's shape and
+    the distance of its tokens."""
     import torch
-    _check_strided(dev, (("q", q, torch.bfloat16),))
-    named = [("out", out, torch.bfloat16)]
-    if lse is not None:
-        named.append(("lse", lse, torch.float32))
-    if workspace is not None:
-        named.append(("workspace", workspace, torch.uint8))
-    _check_all(dev, named)
-    if q.dim() != 3:
+    shape = q.shape
+    if len(shape) != 3:
         raise ValueError("q must be [N, H, D]")
-    N, H, D = q.shape
-    if out.shape != q.shape or (lse is not None and lse.shape != (N, H)):
+    qs = _row_stride("q", q, torch.bfloat16, dev, shape)
+    _check_all(dev, (("out", out, torch.bfloat16),))
+    if lse is not None:
+        _check_all(dev, (("lse", lse, torch.float32),))
+    if workspace is not None:
+        _check_all(dev, (("workspace", workspace, torch.uint8),))
+    if out.shape != shape or (lse is not None and lse.shape != shape[:2]):
         raise ValueError("out must be [N, H, D] and lse [N, H]")
-    return N, H, D
+    return shape, qs
 
 
 def gqa_prefill_packed(q, k, v, cu_seqlens, scale, out, lse=None, stream=None, workspace=None):
@@ -820,22 +826,23 @@ def gqa_prefill_packed(q, k, v, cu_seqlens, scale, out, lse=None, stream=None, w
     cu_seqlens[B] are left as they are. The workspace is kept as for
     gqa_decode_paged_fp8 when not given (gqa_prefill_ragged_workspace_bytes)."""
     import torch
+    bf = torch.bfloat16
     dev = q.get_device()
-    N, H, D = _ragged_outputs(dev, q, out, lse, workspace)
-    _check_strided(dev, (("k", k, torch.bfloat16), ("v", v, torch.bfloat16)))
-    _check_all(dev, (("cu_seqlens", cu_seqlens, torch.int32),))
-    qs, ks, vs = _token_stride("q", q), _token_stride("k", k), _token_stride("v", v)
+    (N, H, D), qs = _ragged_outputs(dev, q, out, lse, workspace)
+    if k.dim() != 3:
+        raise ValueError("k must be [N, G, D]")
     G = k.shape[1]
-    if k.shape != (N, G, D) or v.shape != k.shape:
-        raise ValueError("k / v must be [N, G, D] with q's N and D")
+    shape = (N, G, D)
+    ks, vs = _row_stride("k", k, bf, dev, shape), _row_stride("v", v, bf, dev, shape)
+    _check_all(dev, (("cu_seqlens", cu_seqlens, torch.int32),))
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
         raise ValueError("cu_seqlens must be [B + 1]")
     B = cu_seqlens.shape[0] - 1
     if workspace is None:
         workspace = _workspace(_ragged_workspace_bytes(N, B, H, G, D, dev) or 256, q, dev, stream)
-    rc = _call(dev, load().gqa_prefill_packed, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(),
-               float(scale), out.data_ptr(), None if lse is None else lse.data_ptr(), N, B, H, G, D, qs, ks, vs,
-               workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+    rc = _launch(dev, load().gqa_prefill_packed, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(),
+                 float(scale), out.data_ptr(), None if lse is None else lse.data_ptr(), N, B, H, G, D, qs, ks, vs,
+                 workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
     if rc != GQA_OK:
         raise GQADecodeError(rc, "gqa_prefill_packed")
 
@@ -850,19 +857,18 @@ def gqa_prefill_paged(q, k_pages, v_pages, block_table, cu_new, seq_lens, scale,
     import torch
     bf, i32 = torch.bfloat16, torch.int32
     dev = q.get_device()
-    N, H, D = _ragged_outputs(dev, q, out, lse, workspace)
+    (N, H, D), qs = _ragged_outputs(dev, q, out, lse, workspace)
     _check_all(dev, (("k_pages", k_pages, bf), ("v_pages", v_pages, bf), ("block_table", block_table, i32),
                      ("cu_new", cu_new, i32), ("seq_lens", seq_lens, i32)))
     B, num_pages, G, page_size, Dk, most = _paged_bf16_cache(k_pages, v_pages, block_table, seq_lens, cu_new)
-    qs = _token_stride("q", q)
     if Dk != D:
         raise ValueError("q must be [N, H, D] with the pages' D")
     if workspace is None:
         workspace = _workspace(_ragged_workspace_bytes(N, B, H, G, D, dev) or 256, q, dev, stream)
-    rc = _call(dev, load().gqa_prefill_paged, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-               block_table.data_ptr(), cu_new.data_ptr(), seq_lens.data_ptr(), float(scale), out.data_ptr(),
-               None if lse is None else lse.data_ptr(), N, B, H, G, D, qs, page_size, num_pages, most,
-               workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
+    rc = _launch(dev, load().gqa_prefill_paged, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                 block_table.data_ptr(), cu_new.data_ptr(), seq_lens.data_ptr(), float(scale), out.data_ptr(),
+                 None if lse is None else lse.data_ptr(), N, B, H, G, D, qs, page_size, num_pages, most,
+                 workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
     if rc != GQA_OK:
         raise GQADecodeError(rc, "gqa_prefill_paged")
 

@@ -8,6 +8,7 @@
 #include "gqa_decode.h"
 #include "gqa_launch.h"
 #include "gqa_ragged.h"
+#include "gqa_ragged_plan.cuh"
 
 namespace gqa {
 namespace {
@@ -103,6 +104,11 @@ int gqa_prefill_packed(const void* q, const void* k, const void* v, const int32_
     Call c;
     st = begin(c, q, cu_seqlens, scale, out, lse, N, B, H, G, D, q_stride, workspace, workspace_bytes, stream);
     if (st != GQA_OK) return st;
+    // No more CTAs than the rows have work for: all in one sequence, and the most that
+    // cutting them into B leaves over.
+    const RgLine line = {c.a.p.tq, G};
+    const long long most = (line.head({0, N, N}) + (long long)B * (kRgPad + 2 * c.a.p.tq)) * G / kRgMinShare + 1;
+    if (most < c.a.grid) c.a.grid = (int)most;
     if ((st = encode_rows_map(&c.a.tm_k, k, N, G, D, k_stride, 1, 128)) != GQA_OK) return st;
     if ((st = encode_rows_map(&c.a.tm_v, v, N, G, D, v_stride, 1, 128)) != GQA_OK) return st;
     return launch(c, D, false);
