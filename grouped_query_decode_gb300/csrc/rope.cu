@@ -10,7 +10,11 @@
 // and pair and shared by all heads through shared memory; the products are fp32
 // and rounded once, to bf16.
 //
-// What bounds it: bytes, every row read and written once.
+// What bounds it: bytes, every row read and written once; 64 tokens take the launch
+// and one token's chain of dependent reads (2.6 us in a graph, the append 3.6).
+// Measured on one GB300 (copy 6.79 TB/s), 32/8 heads, D 128: 16384 tokens with half
+// of each head rotated 53.9 us, 6.2 TB/s; 5818 tokens of six sequences appended to
+// 64-token pages 28 us, 5.1 TB/s.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -25,7 +29,7 @@ namespace gqa {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeTokens = 8;           // tokens of a CTA, a warp each for angles and addresses
+constexpr int kRopeTokens = 4;           // tokens of a CTA, a warp each for angles and addresses
 constexpr int kMostPairs = 64;
 
 struct RopeParams {
@@ -252,8 +256,9 @@ int check_rows(const void* x, long long stride, int heads, int D) {
     return aligned(x, 15u) && (stride & 7) == 0 ? GQA_OK : GQA_ERR_MISALIGNED;
 }
 
-// Tokens of a CTA: one while that leaves SMs idle or with a wave to spare (a
-// token's rows are then spread over all of a CTA's threads), eight otherwise.
+// Tokens of a CTA: one while there are fewer than two waves of CTAs (a token's rows
+// are then spread over all of its threads), four where that still makes four waves.
+// 16384 tokens of 32/8 heads, D 128: 53.9 us with four, 57.2 with eight.
 int tokens_per_cta(int N, int sms) { return N >= sms * 8 * kRopeTokens ? kRopeTokens : N >= sms * 16 ? 2 : 1; }
 
 }  // namespace

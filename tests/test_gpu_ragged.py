@@ -4,6 +4,7 @@ sequences without new tokens, without keys and with fewer keys than new tokens,
 page sizes below and above a tile, NaN and infinities in masked places, views of
 fused projections, padded batches, captured graphs and streams that overlap."""
 import math
+import threading
 
 import pytest
 import torch
@@ -240,6 +241,36 @@ def test_malformed_offsets_stay_inside():
     assert gq.gqa_decode_check_error() == gq.GQA_OK
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_units_in_many_parts(D):
+    """Few tokens with many heads behind a long context: one unit over nearly all CTAs,
+    whose parts are merged a few rows at a time; and one with a part of its own per head."""
+    Batch(32, 1, D, [(8, 60000)], page=256, seed=60).run().check()
+    Batch(8, 2, D, [(1, 40000), (1, 3)], page=64, seed=61).run().check()
+    Batch(16, 1, D, [(13, 9000), (16, 700)], page=32, seed=62).run().check()
+
+
+def test_outputs_on_16_bytes():
+    """Outputs need no more than the 16 bytes that the header asks for; lse none but its own."""
+    b = Batch(8, 2, 64, [(130, 130), (5, 5)], seed=63).device()
+    buf = torch.full((b.out.numel() + 16,), 7.0, dtype=BF, device="cuda")
+    lse = torch.full((b.lse.numel() + 1,), 7.0, device="cuda")
+    b.out, b.lse = buf[8:8 + b.out.numel()].view(b.out.shape), lse[1:].view(b.lse.shape)
+    b.call()
+    b.check()
+    assert (buf[:8].float() == 7).all() and (buf[-8:].float() == 7).all() and lse[0] == 7
+
+
+def test_scores_without_any_key_left():
+    """Rows whose every visible key scores -inf weigh nothing: out 0, lse -inf, as rows that see nothing."""
+    b = Batch(4, 1, 64, [(40, 40)], seed=64)
+    b.q = b.q.abs() + 0.5
+    b.k[:3] = -math.inf
+    b.run()
+    assert (b.out[:3].float() == 0).all() and torch.isneginf(b.lse[:3]).all()
+    assert torch.isfinite(b.out[3:].float()).all()
+
+
 # -------------------------------------------------- NaN and masked positions
 
 @pytest.mark.parametrize("D,H,G", [(128, 8, 2), (64, 2, 2), (64, 3, 1)])
@@ -360,6 +391,31 @@ def test_streams_that_overlap():
     b.call(stream=streams[0])
     torch.cuda.synchronize()
     b.check()
+
+
+def test_host_threads_on_one_stream():
+    """Threads that share a stream share no workspace."""
+    batches = [Batch(8, 2, 128, [(3, 4000 + 500 * i), (40, 300)], page=32, seed=70 + i).device() for i in range(4)]
+    torch.cuda.synchronize()
+    stream, failed = torch.cuda.Stream(), []
+
+    def work(b):
+        try:
+            with torch.cuda.stream(stream):
+                for _ in range(20):
+                    b.call()
+        except Exception as e:          # noqa: BLE001 (reported below)
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(b,)) for b in batches]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for b in batches:
+        b.check()
 
 
 def test_no_tokens():
