@@ -51,7 +51,7 @@ struct RgShape {
     static constexpr int kMlBytes = 2 * 128 * (8 + 8 + 4);
     static constexpr int kUnitBytes = kRgUnits * 64;
     static constexpr int kMiscBytes = 384;
-    static constexpr int kBars = 3 * kStages + 2 * 10 + 2 * kRgUnits + 2;
+    static constexpr int kBars = 3 * kStages + 2 * 10 + 2 * kRgUnits + 3;
     static constexpr int kSmemBytes =
         2 * kTile + kStages * kTile + kMlBytes + kUnitBytes + kMiscBytes + 8 * kBars;
     // Columns: S_A | S_B | O_A | O_B, with P over S, that of each 64 keys over the first
@@ -62,8 +62,20 @@ struct RgShape {
     static constexpr uint32_t kColS = 0, kColP = kApart ? 256 : 0, kStepP = kApart ? 64 : 128, kColO = kApart ? 384 : 256;
     static constexpr uint32_t kHalfP = kApart ? 32 : 64;  // columns from the weights of the first 64 keys to the others'
     static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
-    static_assert((2 + kStages) * kTile >= 1024 + 180 * (D * 4 + 4), "one row of all parts");
+    static_assert((2 + kStages) * kTile >= 25 * 1024 + 2 * 160 * D * 4 + 256, "a merge's weights, and a row of 160 parts twice");
 };
+
+// Eight words to 32-byte aligned memory, or to 16-byte aligned.
+__device__ __forceinline__ void store32(void* to, const uint32_t* w, bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
 
 // Scores of 16 keys, those from `see` + 1 on hidden.
 __device__ __forceinline__ void hide16(uint32_t (&s)[16], int see) {
@@ -144,93 +156,97 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 // Merges the parts of a unit with all threads of the CTA: M = max m, w = 2^(m - M),
-// L = sum l w, O = sum O w / L, part by part in their order. As many rows at a time
-// as `room` holds of all parts come into shared memory at once. This runs once or
-// twice per CTA, so its time is latency and instruction fetches: loops are short.
+// L = sum l w, O = sum O w / L, part by part in their order. All parts of a block of
+// rows come into one half of `room` while the block before is summed from the other.
+// This runs once or twice per CTA, so its time is latency and instruction fetches:
+// loops are short. `bars`: two barriers, whose phases are bits of `phases`.
+constexpr uint32_t kRgWeightBytes = 24 * 1024;
 template <int D>
 __device__ __forceinline__ void rg_merge(const RaggedParams& p, const RgUnit& u, unsigned char* room, uint32_t room_bytes,
-                                         uint32_t bar, uint32_t& phase) {
+                                         uint32_t bars, uint32_t& phases) {
     constexpr int kChunks = D / 4;
-    const int n = u.parts, lane = threadIdx.x & 31;
-    // Lanes in groups of `width` take a row each, a lane some of its parts.
-    int width = 1;
-    while (width < n && width < 32) width *= 2;
-    const int k = lane & (width - 1);
-    const int block = min(128, (int)((room_bytes - 1024) / (n * (D * 4 + 4))));
-    float* const inverse = reinterpret_cast<float*>(room);        // [128]
-    float* const weights = inverse + 128;                         // [block][n]
+    const int n = u.parts, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rows_a = u.tokens[0] * p.heads_per_group, rows_all = rows_a + u.tokens[1] * p.heads_per_group;
+    float* const inverse = reinterpret_cast<float*>(room);        // [256]
+    float2* const weights = reinterpret_cast<float2*>(inverse + 256);   // [rows][n]: (m, l), then w in x
+    unsigned char* const held = room + 1024 + kRgWeightBytes;     // O of the parts, [n][rows][D], twice
+    const uint32_t half = (room_bytes - 1024 - kRgWeightBytes) / 2 & ~127u;
+    const int block = half / (n * D * 4), most = min(rows_all, (int)(kRgWeightBytes / (8 * n)));
+    // The first part's slot is its counter's; later ones continue from the CTA before.
+    auto part = [&](int i) { return p.part + (size_t)(i == 0 ? u.counter : 2 * (u.first + i)) * rg_slot_floats(D); };
+    // Rows count A's, then B's.
+    auto slot_row = [&](int r) { return r < rows_a ? r : 128 + r - rows_a; };
+    auto out_row = [&](int r) {
+        const int x = r >= rows_a, in = x ? r - rows_a : r, tok = p.by_heads(in);
+        return (size_t)(u.row0 + x * p.tq + tok) * p.H + (size_t)u.g * p.heads_per_group + (in - tok * p.heads_per_group);
+    };
     asm volatile("fence.proxy.async;" ::: "memory");              // the parts were written by plain stores
-    const uint32_t held = (512 + 4 * n * block + 127) & ~127u;    // O of the parts, [n][rows][D]
 #pragma unroll 1
-    for (int x = 0; x < 2; ++x) {
-        const int rows_x = u.tokens[x] * p.heads_per_group;
-        // The first part's slot is its counter's; later ones continue from the CTA before.
-        auto part = [&](int i) {
-            return p.part + (size_t)(i == 0 ? u.counter : 2 * (u.first + i)) * rg_slot_floats(D);
+    for (int w0 = 0; w0 < rows_all; w0 += most) {
+        const int w1 = min(rows_all, w0 + most);
+        auto end_of = [&](int r) { return min(min(r + block, w1), r < rows_a ? rows_a : rows_all); };   // of r's block
+        auto fetch = [&](int r, int b) {                          // by the last warp
+            const uint32_t bytes = (end_of(r) - r) * D * 4;
+            if (lane == 0) mbar_arrive_expect_tx(bars + 8 * b, n * bytes);
+            __syncwarp();
+#pragma unroll 1
+            for (int i = lane; i < n; i += 32)
+                bulk_load(smem_addr(held) + b * half + i * bytes, part(i) + (size_t)slot_row(r) * D, bytes, bars + 8 * b);
         };
-        const size_t row_x = (size_t)(u.row0 + x * p.tq) * p.H + (size_t)u.g * p.heads_per_group;
-        auto out_row = [&](int r) {
-            const int tok = p.by_heads(r);
-            return row_x + (size_t)tok * p.H + (r - tok * p.heads_per_group);
-        };
+        const bool feeds = warp == kRgThreads / 32 - 1;
+        if (feeds) fetch(w0, 0);
+#pragma unroll 2
+        for (int e = threadIdx.x; e < (w1 - w0) * n; e += kRgThreads) {
+            const int r = e / n, s = 256 * D + slot_row(w0 + r);
+            const float* const from = part(e - r * n);
+            weights[e] = make_float2(__ldcg(from + s), __ldcg(from + s + 256));
+        }
+        __syncthreads();
 #pragma unroll 1
-        for (int r0 = 0; r0 < rows_x; r0 += block) {
-            const int rows = min(block, rows_x - r0);
-            if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, n * rows * D * 4);
-            __syncthreads();
+        for (int r = w0 + (int)threadIdx.x; r < w1; r += kRgThreads) {
+            float2* const mine = weights + (r - w0) * n;
+            float M = -INFINITY, L = 0.f;
+#pragma unroll 2
+            for (int i = 0; i < n; ++i) M = fmaxf(M, mine[i].x);
 #pragma unroll 1
-            for (int i = threadIdx.x; i < n; i += kRgThreads)
-                bulk_load(smem_addr(room) + held + i * rows * D * 4, part(i) + (size_t)(x * 128 + r0) * D, rows * D * 4, bar);
-#pragma unroll 1
-            for (int first = (int)(threadIdx.x >> 5) * (32 / width); first < rows; first += kRgThreads / width) {
-                const int r = first + lane / width, s = 256 * D + x * 128 + r0 + min(r, rows - 1);
-                float M = -INFINITY, m = -INFINITY, l = 0.f, L = 0.f;
-#pragma unroll 1
-                for (int i = k; i < n; i += width) {
-                    m = __ldcg(part(i) + s);
-                    l = __ldcg(part(i) + s + 256);
-                    M = fmaxf(M, m);
-                }
-                for (int o = width / 2; o > 0; o /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-#pragma unroll 1
-                for (int i = k; i < n; i += width) {
-                    if (n > width) {
-                        m = __ldcg(part(i) + s);
-                        l = __ldcg(part(i) + s + 256);
-                    }
-                    const float w = l == 0.f ? 0.f : fast_exp2(m - M);
-                    if (r < rows) weights[r * n + i] = w;
-                    L += l * w;
-                }
-                for (int o = width / 2; o > 0; o /= 2) L += __shfl_xor_sync(0xffffffffu, L, o);
-                if (k == 0 && r < rows) {
-                    inverse[r] = L == 0.f ? 0.f : 1.f / L;
-                    if (p.lse) p.lse[out_row(r0 + r)] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
-                }
+            for (int i = 0; i < n; ++i) {
+                const float l = mine[i].y, w = l == 0.f ? 0.f : fast_exp2(mine[i].x - M);
+                mine[i].x = w;
+                L += l * w;
             }
-            __syncthreads();
-            rg_wait_longer(bar, phase, p.wait_timeout_ns);
-            phase ^= 1;
-            const float4* const o = reinterpret_cast<const float4*>(room + held);
+            inverse[r - w0] = L == 0.f ? 0.f : 1.f / L;
+            if (p.lse) p.lse[out_row(r)] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+        }
+        __syncthreads();
+        int b = 0;
 #pragma unroll 1
-            for (int item = threadIdx.x; item < rows * kChunks; item += kRgThreads) {
-                const int r = item / kChunks;
+        for (int r0 = w0; r0 < w1; b ^= 1) {
+            const int r1 = end_of(r0);
+            if (feeds && r1 < w1) fetch(r1, b ^ 1);
+            rg_wait_longer(bars + 8 * b, phases >> b & 1, p.wait_timeout_ns);
+            phases ^= 1u << b;
+            const float4* const o = reinterpret_cast<const float4*>(held + b * half);
+            const int items = (r1 - r0) * kChunks;
+#pragma unroll 1
+            for (int item = threadIdx.x; item < items; item += kRgThreads) {
+                const int r = r0 + item / kChunks;
                 float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
                 for (int i = 0; i < n; ++i) {
-                    const float w = weights[r * n + i];
-                    float4 v = o[i * rows * kChunks + item];
+                    const float w = weights[(r - w0) * n + i].x;
+                    float4 v = o[i * items + item];
                     if (w == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);     // a row without a key there has left no O
                     y.x = fmaf(v.x, w, y.x);
                     y.y = fmaf(v.y, w, y.y);
                     y.z = fmaf(v.z, w, y.z);
                     y.w = fmaf(v.w, w, y.w);
                 }
-                const float f = inverse[r];
-                *(reinterpret_cast<uint2*>(p.out + out_row(r0 + r) * D) + item % kChunks) =
+                const float f = inverse[r - w0];
+                *(reinterpret_cast<uint2*>(p.out + out_row(r) * D) + item % kChunks) =
                     make_uint2(pack_bf16x2(y.x * f, y.y * f), pack_bf16x2(y.z * f, y.w * f));
             }
             __syncthreads();
+            r0 = r1;
         }
     }
 }
@@ -296,6 +312,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
         }
         mbar_init(fin, 1);
         mbar_init(merge_bar, 1);
+        mbar_init(merge_bar + 8, 1);
         for (int i = 0; i < kRgUnits; ++i) {
             mbar_init(u_full + 8 * i, 1);
             mbar_init(u_empty + 8 * i, 23);       // softmax and output warps, products, loads
@@ -825,20 +842,14 @@ __global__ void __launch_bounds__(kRgThreads, 1)
 #pragma unroll
                             for (int i = 0; i < 16; ++i) o[i] = 0u;
                         if (valid && slot < 0) {
-                            uint4* const dst = reinterpret_cast<uint4*>(p.out + orow * D + c);
+                            uint32_t w[8];
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    w[i] = pack_bf16x2(__uint_as_float(o[8 * k + 2 * i]) * inv,
-                                                       __uint_as_float(o[8 * k + 2 * i + 1]) * inv);
-                                dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
+                            for (int i = 0; i < 8; ++i)
+                                w[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+                            store32(p.out + orow * D + c, w, p.wide);
                         } else if (valid && l != 0.f) {
-                            uint4* const dst = reinterpret_cast<uint4*>(part + (size_t)r * D + c);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                            store32(part + (size_t)r * D + c, o, true);
+                            store32(part + (size_t)r * D + c + 8, o + 8, true);
                         }
                         __syncwarp();
                     }
@@ -1010,10 +1021,10 @@ __global__ void __launch_bounds__(kRgThreads, 1)
         tmem_dealloc(tmem, 512);
     }
     // All copies have landed and all products are done: Q's and the ring's room is free.
-    uint32_t phase = 0;
+    uint32_t phases = 0;
 #pragma unroll 1
     for (int i = 0; i < *todos; ++i)
-        rg_merge<D>(p, todo[i], smem_raw, (2 + S) * kTile, merge_bar, phase);
+        rg_merge<D>(p, todo[i], smem_raw, (2 + S) * kTile, merge_bar, phases);
 }
 
 template <int D, bool PAGED>

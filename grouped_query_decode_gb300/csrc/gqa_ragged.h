@@ -29,6 +29,7 @@ struct RaggedParams {
     int N, B, H, G, heads_per_group, tq;   // tq: tokens of a 128-row tile
     FastDiv by_heads;          // by heads_per_group
     int page_shift, num_pages, max_pages;
+    int wide;                  // out is 32-byte aligned
     int skip_tile;             // fault injection for tests (-1: off)
 };
 

@@ -51,6 +51,7 @@ int begin(Call& c, const void* q, const int32_t* cu, float scale, void* out, flo
     if ((st = encode_rows_map(&c.a.tm_q, q, N, H, D, q_stride, r, tq)) != GQA_OK) return st;
     p.cu = cu;
     p.out = static_cast<uint16_t*>(out);
+    p.wide = aligned(out, 31u);
     p.lse = lse;
     p.counters = static_cast<unsigned long long*>(workspace);
     p.bad = reinterpret_cast<int*>(static_cast<char*>(workspace) + rg_counter_bytes(sms));
