@@ -293,31 +293,31 @@ __global__ void __launch_bounds__(kRgThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint64_t tmo = p.wait_timeout_ns;
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < S; ++s) {
-            mbar_init(full + 8 * s, 1);
-            mbar_init(empty + 8 * s, 1);
-            mbar_init(mended + 8 * s, 1);
-        }
-        for (int x = 0; x < 2; ++x) {
-            mbar_init(q_full + 8 * x, 1);
-            mbar_init(q_empty + 8 * x, 1);
-            mbar_init(s_full + 8 * x, 1);
-            mbar_init(p_full + 8 * x, 8);
-            mbar_init(s_free + 8 * x, 8);
-            mbar_init(pv_done + 8 * x, 1);
-            mbar_init(o_full + 8 * x, 1);
-            mbar_init(o_empty + 8 * x, 4);
-            mbar_init(ml_full + 8 * x, 4);
-        }
+    // Barriers, by threads of several warps.
+    if (warp == 0 && lane < S) {
+        mbar_init(full + 8 * lane, 1);
+        mbar_init(empty + 8 * lane, 1);
+        mbar_init(mended + 8 * lane, 1);
+        fence_barrier_init();
+    } else if (warp == 1 && lane < 2) {
+        mbar_init(q_full + 8 * lane, 1);
+        mbar_init(q_empty + 8 * lane, 1);
+        mbar_init(s_full + 8 * lane, 1);
+        mbar_init(p_full + 8 * lane, 8);
+        mbar_init(s_free + 8 * lane, 8);
+        mbar_init(pv_done + 8 * lane, 1);
+        mbar_init(o_full + 8 * lane, 1);
+        mbar_init(o_empty + 8 * lane, 4);
+        mbar_init(ml_full + 8 * lane, 4);
+        mbar_init(merge_bar + 8 * lane, 1);
+        fence_barrier_init();
+    } else if (warp == 2 && lane < kRgUnits) {
+        mbar_init(u_full + 8 * lane, 1);
+        mbar_init(u_empty + 8 * lane, 23);        // softmax and output warps, products, loads
+        bad_flag[lane] = 0;
+        fence_barrier_init();
+    } else if (warp == 3 && lane == 0) {
         mbar_init(fin, 1);
-        mbar_init(merge_bar, 1);
-        mbar_init(merge_bar + 8, 1);
-        for (int i = 0; i < kRgUnits; ++i) {
-            mbar_init(u_full + 8 * i, 1);
-            mbar_init(u_empty + 8 * i, 23);       // softmax and output warps, products, loads
-        }
-        for (int i = 0; i < kRgUnits; ++i) bad_flag[i] = 0;
         *abort_flag = 0;
         *todos = 0;
         first_s[1] = p.B;
@@ -331,10 +331,16 @@ __global__ void __launch_bounds__(kRgThreads, 1)
     pdl_launch_dependents();
     pdl_wait_primary();
 
-    // The line's length, and the sequence in which this CTA's share starts: every
-    // thread takes some sequences in a row.
+    // The line's length, and the sequence in which this CTA's share starts. With few
+    // sequences the planning warp finds them by itself, below (the others' start does
+    // not wait for it: a tiny prompt 13.1 -> 11.2 us); with more, every thread takes some in
+    // a row.
     const RgLine line = {p.tq, p.G};
-    {
+    const bool few = p.B <= 128;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (!few) {
         const int per = (p.B + kRgThreads - 1) / kRgThreads;
         const int b0 = min((int)threadIdx.x * per, p.B), b1 = min(b0 + per, p.B);
         long long mine = 0;
@@ -347,11 +353,9 @@ __global__ void __launch_bounds__(kRgThreads, 1)
             if (lane >= o) sum += y;
         }
         if (lane == 31) warp_sum[warp] = sum;
-        tc_fence_before();
         __syncthreads();
-        tc_fence_after();
         long long before = 0, total = 0;
-#pragma unroll
+#pragma unroll 4
         for (int w = 0; w < kRgThreads / 32; ++w) {
             const long long y = warp_sum[w];
             if (w < warp) before += y;
@@ -391,8 +395,35 @@ __global__ void __launch_bounds__(kRgThreads, 1)
         if (warp == kRgPlan) {
             // ------------------------------------------------------------ plan
             // Sequence b, whose units start at `at` on the line, KV head g, pair pr.
-            const RgShares sh = *shares;
             const int c = blockIdx.x;
+            if (few) {
+                long long total = 0;
+#pragma unroll 4
+                for (int b = lane; b < 128; b += 32) total += line.head(rg_sequence(p, b)) * p.G;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+                const RgShares sh = RgShares::of(total, gridDim.x);
+                const long long from = c < sh.ctas ? sh.at(c) : total;
+                long long at = 0;
+#pragma unroll 1
+                for (int b = 0; b < p.B; b += 32) {
+                    const long long y = line.head(rg_sequence(p, b + lane)) * p.G;
+                    long long sum = y;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const long long z = __shfl_up_sync(0xffffffffu, sum, o);
+                        if (lane >= o) sum += z;
+                    }
+                    if (at + sum - y <= from && from < at + sum) {
+                        first_s[1] = b + lane;
+                        first_s[2] = at + sum - y;
+                    }
+                    at += __shfl_sync(0xffffffffu, sum, 31);
+                }
+                if (lane == 0) *shares = sh;
+                __syncwarp();
+            }
+            const RgShares sh = *shares;
             const long long to = c < sh.ctas ? sh.at(c + 1) : 0;
             int b = (int)first_s[1], g = 0, pr = 0, pairs = 0;
             long long at = first_s[2], head = 0;

@@ -86,7 +86,8 @@ struct RgShares {
         long long c = total / kRgMinShare;
         if (c > grid) c = grid;
         if (c < 1) c = 1;
-        const long long each = total / c;
+        // (64-bit division takes long)
+        const long long each = total >> 31 == 0 ? (long long)((unsigned)total / (unsigned)c) : total / c;
         return {each, total - each * c, (int)c};
     }
     __host__ __device__ long long at(int c) const { return each * c + (c < more ? c : more); }
