@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 __syncwarp();
             }
         } else if (warp >= kRgLoadK) {
-            // ------------- loads: Q and K from warp 13, V from warp 14, which mends it
+            // --------------------- loads: Q and K by one warp, V by another, which mends it
             const bool v_warp = warp == kRgLoadV;
             const int page_rows = PAGED ? min(1 << p.page_shift, kRgTile) : kRgTile;
             const int boxes = kRgTile / page_rows;
@@ -658,19 +658,19 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 wait_one(bar, (phases >> bit) ^ flip);
                 phases ^= 1u << bit;
             };
-            // The next unit with key tiles.
+            // The next unit. One without key tiles is a step of its own, in which nothing but the
+            // unit behind it is taken up: this thread must not look further ahead before it has
+            // issued the last product of a unit that the output warps hold.
             auto fetch = [&]() {
-                while (next_unit(n)) {
-                    const RgUnit& f = units[n % kRgUnits];
-                    if (!f.valid) return false;
-                    const RgSteps st(f);
-                    next = {st.a, st.b, max(st.a, st.b), f.j0, f.pos0, it, st.dual};
-                    it += max(f.tiles[0], f.tiles[1]);
-                    mbar_arrive(u_empty + 8 * (n % kRgUnits));
-                    ++n;
-                    if (next.all > 0) return true;
-                }
-                return false;
+                if (!next_unit(n)) return false;
+                const RgUnit& f = units[n % kRgUnits];
+                if (!f.valid) return false;
+                const RgSteps st(f);
+                next = {st.a, st.b, max(max(st.a, st.b), 1), f.j0, f.pos0, it, st.dual};
+                it += max(f.tiles[0], f.tiles[1]);
+                mbar_arrive(u_empty + 8 * (n % kRgUnits));
+                ++n;
+                return true;
             };
             // S_X for K tile i of all.
             auto scores = [&](uint32_t i, int x, bool first, bool last, bool release) {

@@ -205,6 +205,14 @@ def test_paged_serving_batches():
         Batch(4 * G, G, D, seqs, page=page, behind=5, seed=11).run().check()
 
 
+@pytest.mark.parametrize("D,H,G,B,every", [(64, 32, 32, 128, 5), (128, 8, 2, 1000, 9), (128, 16, 16, 100, 100), (64, 4, 4, 700, 701)])
+def test_padded_batches(D, H, G, B, every):
+    """A batch padded with tokens of sequences without a key: runs of units in which there
+    is nothing to do, far longer than the list that hands units on."""
+    seqs = [(1, 300 + b) if (b + 1) % every == 0 else (1 + b % 3, 0) for b in range(B)]
+    Batch(H, G, D, seqs, page=32, behind=2, seed=64).run().check()
+
+
 def test_paged_unusable_entries_and_clamped_lengths():
     """Entries outside the pool read as zeros; lengths are cut to the table's."""
     b = Batch(8, 2, 64, [(3, 100), (1, 60), (4, 64)], page=16, seed=12, fill=2.0)
