@@ -617,7 +617,7 @@ const char* gqa_decode_strerror(int status) {
         case GQA_OK: return "ok";
         case GQA_ERR_INVALID_ARG: return "invalid argument (null pointer or non-positive size)";
         case GQA_ERR_HEAD_RATIO: return "H is not a multiple of G";
-        case GQA_ERR_UNSUPPORTED: return "unsupported shape (D must be 64 or 128; (H/G)*sq <= 32 except for gqa_decode, gqa_prefill and gqa_decode_paged_fp8; sizes as in the header)";
+        case GQA_ERR_UNSUPPORTED: return "unsupported shape (D must be 64 or 128; (H/G)*sq <= 32 except for gqa_decode, gqa_prefill, gqa_decode_paged_fp8 and packed batches; sizes as in the header)";
         case GQA_ERR_MISALIGNED: return "a tensor pointer is not 16-byte aligned";
         case GQA_ERR_WORKSPACE: return "workspace missing, too small or not 256-byte aligned";
         case GQA_ERR_CUDA: return "a CUDA call failed (see gqa_decode_last_cuda_error)";

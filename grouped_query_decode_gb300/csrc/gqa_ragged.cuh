@@ -15,16 +15,37 @@
 // arrives last merges them in the order of the parts.
 //
 // Warps: 0-7 and 8-15 softmax of A and B, two threads per row, 64 keys of a tile
-// each; 16-19 outputs; 20 issues the products, always one of A, one of B, so that each tile's softmax runs behind
-// the other's products; 21 loads Q and K by TMA, a lane per page, 22 V, of which
-// it mends the tiles that reach past the first row's limit; 23 plans and hands the
-// units out through a ring in shared memory. Every wait is bounded; after one has expired
-// the CTA runs through its units without work, so that the counters end at zero.
+// each; 16-19 outputs; 20 issues the products, always one of A, one of B, so that
+// each tile's softmax runs behind the other's products; 21 loads Q and K by TMA, a
+// lane per page, 22 V, of which it mends the tiles that reach past the first row's
+// limit; 23 plans and hands the units out through a ring in shared memory. Every
+// wait is bounded; after one has expired the CTA runs through its units without
+// work, so that the counters end at zero.
+//
+// Rounding: P to bf16, as the products take it (at most 2^-8 of each weight; out
+// differs from the formula in 64 bits by 2.0e-3 to 2.4e-3 of its norm, out rounded to
+// bf16 alone by 1.5e-3 to 1.7e-3), and out to bf16, once. Scores, m, l, O and the parts are fp32.
 //
 // V at positions that only some rows see: a masked key's weight is 0, and 0 times
-// NaN or infinity is not. In tiles past the first row's limit warp 14 zeroes what
+// NaN or infinity is not. In tiles past the first row's limit warp 22 zeroes what
 // no row sees, and takes out values that are not finite; a row that sees such a
 // value gets NaN in its column with the output.
+//
+// What bounds it, on one GB300 (copy 6.79 TB/s, bf16 products 1879 TFLOP/s):
+// - long prompts: 16384 tokens, 32/8 heads, D 128 take 1425 us back to back (the power
+//   cap holds the clock down) and 1307 us in a burst, 1.68 PFLOP/s; the products alone
+//   are 1171 us. Without its softmax the kernel took 1100 us, without its products 1120:
+//   both are nearly full, and what is left is their handing over to each other, about
+//   450 of a step's 3000 cycles (a step: one key tile with both row tiles).
+// - single tokens: HBM (64 sequences of up to 16384 keys 378 us, 6.7 TB/s).
+// - short sequences: 2 to 3 us at a unit's start and end, 4 us before a launch's first
+//   scores, 4 to 15 us for a merge (8 prompts of 1024, 16 heads, D 64 44 us, 10 at
+//   the roofline; chunks among single tokens 300 us, 146 at the roofline).
+//
+// Why this split of the warps: one softmax thread per row held 128 scores, and the 8
+// prompts took 54 us for 48 with two; one pipeline for units with one row tile, and
+// one warp that loaded K and V both and mended V between, took 475 us for the single
+// tokens' 381.
 #pragma once
 
 #include <atomic>
@@ -55,9 +76,8 @@ struct RgShape {
     static constexpr int kSmemBytes =
         2 * kTile + kStages * kTile + kMlBytes + kUnitBytes + kMiscBytes + 8 * kBars;
     // Columns: S_A | S_B | O_A | O_B, with P over S, that of each 64 keys over the first
-    // half of their scores; D = 64
-    // has room for P apart (S_A | S_B | P_A | P_B | O_A | O_B), so that the next
-    // scores wait only until these have been read.
+    // half of their scores; D = 64 has room for P apart (S_A | S_B | P_A | P_B | O_A |
+    // O_B), so that the next scores wait only until these have been read.
     static constexpr bool kApart = D == 64;
     static constexpr uint32_t kColS = 0, kColP = kApart ? 256 : 0, kStepP = kApart ? 64 : 128, kColO = kApart ? 384 : 256;
     static constexpr uint32_t kHalfP = kApart ? 32 : 64;  // columns from the weights of the first 64 keys to the others'
@@ -332,9 +352,9 @@ __global__ void __launch_bounds__(kRgThreads, 1)
     pdl_wait_primary();
 
     // The line's length, and the sequence in which this CTA's share starts. With few
-    // sequences the planning warp finds them by itself, below (the others' start does
-    // not wait for it: a tiny prompt 13.1 -> 11.2 us); with more, every thread takes some in
-    // a row.
+    // sequences the planning warp finds them by itself, below, and the others' start
+    // does not wait for it (a tiny prompt 13.1 -> 11.2 us); with more, every thread takes
+    // some in a row.
     const RgLine line = {p.tq, p.G};
     const bool few = p.B <= 128;
     tc_fence_before();
