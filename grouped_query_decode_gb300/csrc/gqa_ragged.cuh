@@ -61,6 +61,7 @@ namespace gqa {
 constexpr int kRgThreads = 768;
 constexpr int kRgOut = 16, kRgMma = 20, kRgLoadK = 21, kRgLoadV = 22, kRgPlan = 23;   // first warps of the roles
 constexpr float kRgSlack = 8.0f;         // p <= 2^8 before the reference moves
+constexpr uint64_t kRgTileNs = 16000;    // what a key tile may take at most (it takes 1600)
 
 template <int D>
 struct RgShape {
@@ -243,7 +244,7 @@ __device__ __forceinline__ void rg_merge(const RaggedParams& p, const RgUnit& u,
         for (int r0 = w0; r0 < w1; b ^= 1) {
             const int r1 = end_of(r0);
             if (feeds && r1 < w1) fetch(r1, b ^ 1);
-            rg_wait_longer(bars + 8 * b, phases >> b & 1, p.wait_timeout_ns);
+            if (!rg_wait_longer(bars + 8 * b, phases >> b & 1, p.wait_timeout_ns)) atomicOr(p.status, kStatusTimeout);
             phases ^= 1u << b;
             const float4* const o = reinterpret_cast<const float4*>(held + b * half);
             const int items = (r1 - r0) * kChunks;
@@ -283,7 +284,10 @@ __global__ void __launch_bounds__(kRgThreads, 1)
     // There is no static shared memory, so that the dynamic one starts on the 1024
     // bytes of the swizzle atom.
     const uint32_t raw = smem_addr(smem_raw);
-    if (raw & 1023u) return;
+    if (raw & 1023u) {
+        if (threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);
+        return;
+    }
     const uint32_t q_s = raw, ring_s = q_s + 2 * kTile;
     unsigned char* gen = smem_raw + (2 + S) * kTile;
     float2* const ml = reinterpret_cast<float2*>(gen);               // [2][128]
@@ -401,14 +405,15 @@ __global__ void __launch_bounds__(kRgThreads, 1)
     }
     const uint32_t tmem = *tmem_slot;
 
-    auto wait = [&](uint32_t bar, uint32_t parity) {
-        return mbar_try_wait(bar, parity & 1) || rg_wait_slow(bar, parity & 1, abort_flag, p.status, tmo);
+    auto wait = [&](uint32_t bar, uint32_t parity, uint64_t more = 0) {
+        return mbar_try_wait(bar, parity & 1) || rg_wait_slow(bar, parity & 1, abort_flag, p.status, tmo + more);
     };
     // The next unit, for every lane of a warp. Waits on although the CTA has given
-    // up its work: units keep coming. False: none comes any more.
+    // up its work: units keep coming, as long as the longest of them may take (69 s: 2^31
+    // keys are 25). False: none comes any more.
     auto next_unit = [&](uint32_t n) {
         const uint32_t bar = u_full + 8 * (n % kRgUnits), parity = (n / kRgUnits) & 1;
-        return mbar_try_wait(bar, parity) || rg_wait_longer(bar, parity, 8 * tmo);
+        return mbar_try_wait(bar, parity) || rg_wait_longer(bar, parity, 8 * tmo + (1ull << 36));
     };
 
     if (warp >= kRgMma) {
@@ -494,16 +499,19 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 }
             };
             bool more = true;
+            int longest = 0;                        // unit, in key tiles
             for (uint32_t n = 0; more; ++n) {
                 RgUnit u;
                 more = plan(u);
                 u.valid = more;                     // the last one handed out ends the list
                 if (lane == 0) {
                     if (more && u.slot >= 0) tag_counter(p.counters + u.counter, p.tag);
-                    if (!rg_wait_longer(u_empty + 8 * (n % kRgUnits), ((n / kRgUnits) & 1) ^ 1, 4 * tmo)) {
+                    if (!rg_wait_longer(u_empty + 8 * (n % kRgUnits), ((n / kRgUnits) & 1) ^ 1,
+                                        4 * tmo + kRgUnits * kRgTileNs * longest)) {
                         *abort_flag = 1;
                         atomicOr(p.status, kStatusTimeout);
                     }
+                    if (more) longest = max(longest, max(u.tiles[0], u.tiles[1]));
                     units[n % kRgUnits] = u;
                     mbar_arrive(u_full + 8 * (n % kRgUnits));
                 }
@@ -832,7 +840,8 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 float m = -INFINITY, l = 0.f, a0 = 1.f, a1 = 0.f;      // factors of O_A, O_B if both have the rows
                 bool ok = true;
                 if (some) {
-                    ok = !*abort_flag && wait(ml_full + 8 * x, nt >> x) && wait(o_full + 8 * x, nt >> x);
+                    const uint64_t whole = kRgTileNs * u.tiles[x];         // these wait for all of the unit
+                    ok = !*abort_flag && wait(ml_full + 8 * x, nt >> x, whole) && wait(o_full + 8 * x, nt >> x);
                     nt ^= 1u << x;
                     if (dual) {
                         ok = ok && wait(ml_full + 8, nt >> 1) && wait(o_full + 8, nt >> 1);

@@ -213,6 +213,29 @@ def test_padded_batches(D, H, G, B, every):
     Batch(H, G, D, seqs, page=32, behind=2, seed=64).run().check()
 
 
+def test_units_that_take_longer_than_a_wait():
+    """Units of 12 million keys, one to a CTA (their pages are one page, again and again), take
+    longer than a wait for a step is given here, 10 ms. Keys of zero: out is the mean
+    of equal values, lse the logarithm of the number of keys."""
+    H, G, D, page, pages = 128, 1, 64, 65536, 192
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    N, T = 2 * sms, page * pages
+    k = torch.zeros(1, G, page, D, dtype=BF, device="cuda")
+    v = (2.0 ** (torch.arange(D, device="cuda") % 7 - 3)).to(BF).expand_as(k).contiguous()
+    q = normal((N, H, D), torch.Generator().manual_seed(65)).cuda()
+    table = torch.zeros(1, pages, dtype=I32, device="cuda")
+    cu, lens = torch.tensor([0, N], dtype=I32, device="cuda"), torch.tensor([T], dtype=I32, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(N, H, device="cuda")
+    with env(GQA_DECODE_DEBUG_TIMEOUT_MS=10):
+        gq.gqa_prefill_paged(q, k, v, table, cu, lens, 0.125, out, lse)
+    torch.cuda.synchronize()
+    assert gq.gqa_decode_check_error() == gq.GQA_OK
+    assert torch.equal(out, v[0, 0, 0].expand_as(out))
+    want = torch.log(torch.arange(T - N + 1, T + 1, dtype=torch.float64))
+    # log2 and the product, 2^-23 each of at most 23.6 and 16.4
+    assert (lse.double().cpu() - want[:, None]).abs().max() < 1e-5
+
+
 def test_paged_unusable_entries_and_clamped_lengths():
     """Entries outside the pool read as zeros; lengths are cut to the table's."""
     b = Batch(8, 2, 64, [(3, 100), (1, 60), (4, 64)], page=16, seed=12, fill=2.0)
