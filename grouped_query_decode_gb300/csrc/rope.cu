@@ -256,6 +256,13 @@ int check_rows(const void* x, long long stride, int heads, int D) {
     return aligned(x, 15u) && (stride & 7) == 0 ? GQA_OK : GQA_ERR_MISALIGNED;
 }
 
+// A tensor and what it is rotated into: apart, or the same with the same stride.
+int check_pair(const void* x, long long stride, const void* out, long long out_stride, int N, int heads, int D) {
+    int st = check_rows(x, stride, heads, D);
+    if (st == GQA_OK) st = check_rows(out, out_stride, heads, D);
+    return st != GQA_OK || x != out || stride == out_stride || N == 1 ? st : GQA_ERR_INVALID_ARG;
+}
+
 // Tokens of a CTA: one while there are fewer than two waves of CTAs (a token's rows
 // are then spread over all of its threads), four where that still makes four waves.
 // 16384 tokens of 32/8 heads, D 128: 53.9 us with four, 57.2 with eight.
@@ -318,10 +325,8 @@ int gqa_rope(const gqa_rope_t* rope, const void* q, const void* k, const int32_t
     if (!k) G = 0;
     if ((long long)N * H + (long long)N * G >= (1ll << 31) || (long long)H + G >= (1 << 20)) return GQA_ERR_UNSUPPORTED;
     if (!aligned(positions, 3u)) return GQA_ERR_MISALIGNED;
-    if (q && ((st = check_rows(q, q_stride, H, D)) != GQA_OK || (st = check_rows(q_out, q_out_stride, H, D)) != GQA_OK))
-        return st;
-    if (k && ((st = check_rows(k, k_stride, G, D)) != GQA_OK || (st = check_rows(k_out, k_out_stride, G, D)) != GQA_OK))
-        return st;
+    if (q && (st = check_pair(q, q_stride, q_out, q_out_stride, N, H, D)) != GQA_OK) return st;
+    if (k && (st = check_pair(k, k_stride, k_out, k_out_stride, N, G, D)) != GQA_OK) return st;
     int sms;
     unsigned* status;
     st = current_device(&sms, &status);
@@ -368,8 +373,7 @@ int gqa_append_paged(const gqa_rope_t* rope, const void* q, const void* k_new, c
     if (!aligned(block_table, 3u) || !aligned(cu_new, 3u) || !aligned(seq_lens, 3u) || !aligned(k_pages, 15u) ||
         !aligned(v_pages, 15u))
         return GQA_ERR_MISALIGNED;
-    if (q && ((st = check_rows(q, q_stride, H, D)) != GQA_OK || (st = check_rows(q_out, q_out_stride, H, D)) != GQA_OK))
-        return st;
+    if (q && (st = check_pair(q, q_stride, q_out, q_out_stride, N, H, D)) != GQA_OK) return st;
     if ((st = check_rows(k_new, k_stride, G, D)) != GQA_OK || (st = check_rows(v_new, v_stride, G, D)) != GQA_OK)
         return st;
     int sms;

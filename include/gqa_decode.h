@@ -458,7 +458,7 @@ int gqa_append_paged(const gqa_rope_t* rope, const void* q, const void* k_new, c
  * The workspace is the caller's (256-byte aligned, no initialisation): calls
  * that may overlap on the GPU, replays of different graphs among them, take
  * different ones. cu, seq_lens and block_table stay as they are until the call
- * has finished.
+ * has finished; out, lse and workspace overlap no other array of the call.
  */
 int gqa_prefill_packed(const void* q, const void* k, const void* v, const int32_t* cu_seqlens, float scale,
                        void* out, float* lse, int N, int B, int H, int G, int D, long long q_stride,

@@ -72,6 +72,19 @@ def test_rope_refusals():
     assert call(r=r) == gq.GQA_ERR_INVALID_ARG
 
 
+def test_in_place_keeps_the_stride():
+    """Rotated into itself, a tensor has one stride: with two, tokens would overwrite others."""
+    lib = gq.load()
+    rope = ctypes.addressof(gq.gqa_rope_init(64))
+    args = lambda q, qo, qs, qos: (rope, q, None, 768, qo, None, 4, 8, 0, 64, qs, 0, qos, 0, 0, None)  # noqa: E731
+    assert lib.gqa_rope(*args(256, 256, 512, 640)) == gq.GQA_ERR_INVALID_ARG
+    key = lambda ks, kos: (rope, None, 256, 768, None, 256, 4, 0, 2, 64, 0, ks, 0, kos, 0, None)       # noqa: E731
+    assert lib.gqa_rope(*key(128, 256)) == gq.GQA_ERR_INVALID_ARG
+    append = lambda qs, qos: (rope, 256, 512, 768, 256, 1024, 1280, 1536, 1552, 1568, 4, 2, 8, 2, 64,  # noqa: E731
+                              qs, 128, 128, qos, 16, 4, 4, None)
+    assert lib.gqa_append_paged(*append(512, 640)) == gq.GQA_ERR_INVALID_ARG
+
+
 def test_append_refusals():
     lib = gq.load()
     rope = gq.gqa_rope_init(64)
