@@ -60,7 +60,7 @@ namespace gqa {
 
 constexpr int kRgThreads = 768;
 constexpr int kRgOut = 16, kRgMma = 20, kRgLoadK = 21, kRgLoadV = 22, kRgPlan = 23;   // first warps of the roles
-constexpr float kRgSlack = 8.0f;         // p <= 2^8 before the reference moves
+constexpr float kRgSlack = 256.0f;       // sum of 64 weights at which the reference moves
 constexpr uint64_t kRgTileNs = 16000;    // what a key tile may take at most (it takes 1600)
 
 template <int D>
@@ -106,16 +106,14 @@ __device__ __forceinline__ void hide16(uint32_t (&s)[16], int see) {
     }
 }
 
-// Weights 2^(s * scale + neg) of 16 keys, in pairs of bf16, their sums and the largest score.
-__device__ __forceinline__ void weights16(const uint32_t (&s)[16], float2 scale, float2 neg, float2 (&sum)[2],
-                                          float (&top)[2], uint32_t* w) {
+// Weights 2^(s * scale + neg) of 16 keys, in pairs of bf16, and their sums.
+__device__ __forceinline__ void weights16(const uint32_t (&s)[16], float2 scale, float2 neg, float2 (&sum)[2], uint32_t* w) {
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
         const float2 z = fma_x2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), scale, neg);
         const float2 e = make_float2(fast_exp2(z.x), fast_exp2(z.y));
         sum[(i / 2) & 1] = add_x2(sum[(i / 2) & 1], e);
         w[i / 2] = pack_bf16x2(e.x, e.y);
-        top[(i / 2) & 1] = fmax3(top[(i / 2) & 1], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
     }
 }
 
@@ -977,9 +975,9 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                 __syncwarp();
                 tc_fence_after();
                 bool settled = false;            // O_X holds all earlier keys, P is free
-                // The reference is the one of the tiles before as long as no score exceeds it by
-                // more than kRgSlack; otherwise (and with the first tile) the tile's maximum is
-                // taken first.
+                // The reference is the one of the tiles before as long as the weights' sum shows
+                // that no score exceeds it by much; otherwise (and with a row's first tile) the
+                // tile's maximum is taken first.
                 for (bool fresh = j == 0; !idle; fresh = true) {
                     if (fresh) {
                         float top = -INFINITY;
@@ -999,8 +997,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                         *my_top = top;
                         named_sync(pair, 64);
                         top = fmaxf(top, *other_top) * p.scale_log2;
-                        const bool up = top > m + kRgSlack;
-                        const float mn = up ? top : m;
+                        const float mn = fmaxf(top, m);
                         if (j > 0) {
                             if (RS::kApart && !settled) {
                                 wait(pv_done + 8 * x, ns - 1);
@@ -1008,7 +1005,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                                 tc_fence_after();
                                 settled = true;
                             }
-                            const float a = up ? fast_exp2(m - mn) : 1.f;
+                            const float a = mn > m ? fast_exp2(m - mn) : 1.f;
 #pragma unroll 1
                             for (int c = 0; c < D / 2; c += 16) {
                                 uint32_t o[16];
@@ -1024,16 +1021,17 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                     const float ref = m == -INFINITY ? 0.f : m;
                     const float2 scale = make_float2(p.scale_log2, p.scale_log2), neg = make_float2(-ref, -ref);
                     float2 sum[2] = {};
-                    float top[2] = {-INFINITY, -INFINITY};
                     uint32_t w[32];
 #pragma unroll
                     for (int c = 0; c < 64; c += 16) {
                         uint32_t s[16];
                         tmem_ld16(s_t + c, s);
                         hide16(s, lim - t0 - c);
-                        weights16(s, scale, neg, sum, top, w + c / 2);
+                        weights16(s, scale, neg, sum, w + c / 2);
                     }
-                    if (!fresh && pair_any(pair, fmaxf(top[0], top[1]) * p.scale_log2 > m + kRgSlack)) continue;
+                    sum[0] = add_x2(sum[0], sum[1]);
+                    const float all = sum[0].x + sum[0].y;
+                    if (!fresh && pair_any(pair, all > kRgSlack || (m == -INFINITY && t0 <= lim))) continue;
                     if (RS::kApart) {
                         tc_fence_before();
                         __syncwarp();
@@ -1043,8 +1041,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                         tc_fence_after();
                     }
                     tmem_st32(p_t, w);
-                    sum[0] = add_x2(sum[0], sum[1]);
-                    l += sum[0].x + sum[0].y;
+                    l += all;
                     tmem_st_wait();
                     break;
                 }
