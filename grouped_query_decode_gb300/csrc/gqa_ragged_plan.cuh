@@ -48,9 +48,14 @@ struct RgUnit {
 };
 static_assert(sizeof(RgUnit) == 64, "a unit is read as 16-byte words");
 
-// Sizes that the line depends on: tokens of a tile, KV heads.
+// Sizes that the line depends on: tokens of a tile, KV heads, and what a key of a unit
+// with rows in tile A alone counts, in eighths: its tiles go through both pipelines in
+// turn. Chunks among single tokens (48 sequences, 32/8 heads), D 128: 277 us with 6,
+// 260 with 5, 286 with 4; D 64: 240, 227, 212 and 249 with 3.
 struct RgLine {
-    int tq, G;
+    int tq, G, eighths;
+
+    __host__ __device__ static RgLine of(int tq, int G, int D) { return {tq, G, D == 128 ? 5 : 4}; }
 
     __host__ __device__ int pairs(int n) const { return (int)(((unsigned)n + 2u * tq - 1) / (2u * tq)); }
     __host__ __device__ static long long base(const RgSeq& s) { return s.T > s.n ? s.T - s.n : 0; }
@@ -58,13 +63,13 @@ struct RgLine {
     __host__ __device__ long long start(const RgSeq& s, int pr) const {
         return pr * (base(s) + kRgPad) + (long long)tq * pr * (pr + 1ll);
     }
-    // A key of a unit with rows in tile A alone counts three quarters: its tile takes
-    // 1.1 us, one of both row tiles 1.6 (a step of single tokens and chunks).
     __host__ __device__ bool single(const RgSeq& s, int pr) const { return s.n - pr * 2 * tq <= tq; }
     __host__ __device__ long long length(const RgSeq& s, int pr) const {
         const long long seen = (pr + 1ll) * 2 * tq, keys = base(s) + (seen < s.n ? seen : s.n);
-        return (single(s, pr) ? keys - (keys >> 2) : keys) + kRgPad;
+        return (single(s, pr) ? keys * eighths >> 3 : keys) + kRgPad;
     }
+    // Keys of such a unit by their length on the line (8 / 5 as 410 / 256).
+    __host__ __device__ long long keys_of(long long y) const { return eighths == 5 ? y * 410 >> 8 : 2 * y; }
     // Of one KV head.
     __host__ __device__ long long head(const RgSeq& s) const {
         const int P = pairs(s.n);
@@ -116,7 +121,7 @@ __host__ __device__ __forceinline__ bool rg_unit(const RgLine& line, const RgSha
         const long long y = x - at;
         if (y <= 0) return 0;
         if (y >= len) return tiles;
-        const long long t = ((alone ? y + y * 85 / 256 : y) + kRgTile / 2) >> kRgTileShift;
+        const long long t = ((alone ? line.keys_of(y) : y) + kRgTile / 2) >> kRgTileShift;
         if (t < kRgMinPart) return 0;
         return t > tiles - kRgMinPart ? tiles : (int)t;
     };

@@ -7,9 +7,9 @@
 
 using namespace gqa;
 
-extern "C" long long ragged_parts(const int* start, const int* n, const int* T, int B, int tq, int G, int grid, int* out,
-                                  long long most) {
-    const RgLine line = {tq, G};
+extern "C" long long ragged_parts(const int* start, const int* n, const int* T, int B, int tq, int G, int D, int grid,
+                                  int* out, long long most) {
+    const RgLine line = RgLine::of(tq, G, D);
     long long total = 0, count = 0;
     for (int b = 0; b < B; ++b) total += line.head({start[b], n[b], T[b]}) * G;
     const RgShares sh = RgShares::of(total, grid);

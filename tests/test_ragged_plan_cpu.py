@@ -22,23 +22,29 @@ def plan(tmp_path_factory):
                     os.path.join(ROOT, "tests", "ragged_plan_on_host.cpp"), "-o", so], check=True)
     lib = ctypes.CDLL(so)
     lib.ragged_parts.restype = ctypes.c_longlong
-    lib.ragged_parts.argtypes = [ctypes.c_void_p] * 3 + [ctypes.c_int] * 4 + [ctypes.c_void_p, ctypes.c_longlong]
+    lib.ragged_parts.argtypes = [ctypes.c_void_p] * 3 + [ctypes.c_int] * 5 + [ctypes.c_void_p, ctypes.c_longlong]
     return lib
 
 
-def parts_of(plan, seqs, heads, G, grid=152):
+def parts_of(plan, seqs, heads, G, grid=152, D=128):
     n, T = (np.array([s[i] for s in seqs], dtype=np.int32) for i in (0, 1))
     start = (np.cumsum(n) - n).astype(np.int32)
     tq = 128 // heads
     most = int(sum(-(-int(x) // (2 * tq)) for x in n)) * G + 2 * grid + 10
     out = np.zeros((most, 17), dtype=np.int32)
-    got = plan.ragged_parts(*(x.ctypes.data for x in (start, n, T)), len(seqs), tq, G, grid, out.ctypes.data, most)
+    got = plan.ragged_parts(*(x.ctypes.data for x in (start, n, T)), len(seqs), tq, G, D, grid, out.ctypes.data, most)
     assert got >= 0, got
     return [dict(zip(FIELDS, (int(v) for v in row))) for row in out[:got]], start, tq
 
 
 def check(plan, seqs, heads, G, grid=152):
-    parts, start, tq = parts_of(plan, seqs, heads, G, grid)
+    """Both head sizes; the load with D 128."""
+    one(plan, seqs, heads, G, grid, 64)
+    return one(plan, seqs, heads, G, grid, 128)
+
+
+def one(plan, seqs, heads, G, grid, D):
+    parts, start, tq = parts_of(plan, seqs, heads, G, grid, D)
     units = {}
     for u in parts:
         assert u["valid"] == 1
@@ -63,7 +69,7 @@ def check(plan, seqs, heads, G, grid=152):
                     at += max(u["tiles_a"], u["tiles_b"])
                     assert u["tiles_a"] == max(0, min(want[0], at) - u["j0"])
                     assert u["tiles_b"] == max(0, min(want[1], at) - u["j0"])
-                    load[u["cta"]] += max(u["tiles_a"], u["tiles_b"]) * (128 if tokens[1] else 96) + 256
+                    load[u["cta"]] += max(u["tiles_a"], u["tiles_b"]) * (128 if tokens[1] else 80) + 256
                     assert u["parts"] == len(got) and u["first"] == got[0]["cta"]
                     if len(got) == 1:
                         assert u["slot"] == -1
