@@ -34,15 +34,15 @@
 // value gets NaN in its column with the output.
 //
 // What bounds it, on one GB300 (copy 6.79 TB/s, bf16 products 1879 TFLOP/s):
-// - long prompts: 16384 tokens, 32/8 heads, D 128 take 1425 us back to back (the power
-//   cap holds the clock down) and 1307 us in a burst, 1.68 PFLOP/s; the products alone
-//   are 1171 us. Without its softmax the kernel took 1100 us, without its products 1120:
-//   both are nearly full, and what is left is their handing over to each other, about
-//   450 of a step's 3000 cycles (a step: one key tile with both row tiles).
-// - single tokens: HBM (64 sequences of up to 16384 keys 378 us, 6.7 TB/s).
+// - long prompts: 16384 tokens, 32/8 heads, D 128 take 1420 us back to back (the power
+//   cap holds the clock down) and 1296 us in a burst, 1.70 PFLOP/s; the products alone
+//   are 1171 us. Without its softmax an earlier form took 1100 us, without its products
+//   1120: both are nearly full, and what is left is their handing over to each other,
+//   some 450 of a step's 2900 cycles (a step: one key tile with both row tiles).
+// - single tokens: HBM (64 sequences of up to 16384 keys 386 us, 6.6 TB/s).
 // - short sequences: 2 to 3 us at a unit's start and end, 4 us before a launch's first
-//   scores, 4 to 15 us for a merge (8 prompts of 1024, 16 heads, D 64 44 us, 10 at
-//   the roofline; chunks among single tokens 300 us, 146 at the roofline).
+//   scores, 4 to 15 us for a merge (8 prompts of 1024, 16 heads, D 64 41 us, 10 at
+//   the roofline; chunks among single tokens 292 us, 146 at the roofline).
 //
 // Why this split of the warps: one softmax thread per row held 128 scores, and the 8
 // prompts took 54 us for 48 with two; one pipeline for units with one row tile, and
