@@ -14,7 +14,7 @@
 // and one token's chain of dependent reads (2.6 us in a graph, the append 3.6).
 // Measured on one GB300 (copy 6.79 TB/s), 32/8 heads, D 128: 16384 tokens with half
 // of each head rotated 53.9 us, 6.2 TB/s; 5818 tokens of six sequences appended to
-// 64-token pages 28 us, 5.1 TB/s.
+// 64-token pages 27 us, 5.3 TB/s (23000 of 24: 91 us, 6.6 TB/s).
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -63,8 +63,11 @@ __device__ int find_sequence(const int32_t* cu, int B, int n, int lane) {
     return lo;
 }
 
+// The append's rows come from three tensors and go through a table: eight CTAs on an SM
+// (32 registers) have more of them under way (24 chunks 95.6 us, 91.1 so); the rotation
+// alone loses by it (16384 tokens 54.1 us, 54.6).
 template <int D, bool APPEND>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, APPEND ? 8 : 6) rope_kernel(const __grid_constant__ RopeParams p) {
     __shared__ __align__(16) float cos_s[kRopeTokens][kMostPairs];
     __shared__ __align__(16) float sin_s[kRopeTokens][kMostPairs];
     __shared__ long long page_at[kRopeTokens];     // element of the token's row of KV head 0, -1: not written
@@ -263,10 +266,12 @@ int check_pair(const void* x, long long stride, const void* out, long long out_s
     return st != GQA_OK || x != out || stride == out_stride || N == 1 ? st : GQA_ERR_INVALID_ARG;
 }
 
-// Tokens of a CTA: one while there are fewer than two waves of CTAs (a token's rows
-// are then spread over all of its threads), four where that still makes four waves.
-// 16384 tokens of 32/8 heads, D 128: 53.9 us with four, 57.2 with eight.
-int tokens_per_cta(int N, int sms) { return N >= sms * 8 * kRopeTokens ? kRopeTokens : N >= sms * 16 ? 2 : 1; }
+// Tokens of a CTA: one while there are few (a token's rows are then spread over all of
+// its threads), two from sixteen CTAs per SM, `most` where that still makes sixteen. 16384
+// tokens rotated, 32/8 heads, D 128: 53.8 us with four, 55.8 with two, 57.2 with eight; 8192
+// 30.4 with four, 30.0 with two. 24 chunks appended: D 64 50.1 us with four, 51.6 with two;
+// D 128 94.8 with four, 91.1 with two.
+int tokens_per_cta(int N, int sms, int most) { return N >= sms * 16 * kRopeTokens ? most : N >= sms * 16 ? 2 : 1; }
 
 }  // namespace
 }  // namespace gqa
@@ -345,7 +350,7 @@ int gqa_rope(const gqa_rope_t* rope, const void* q, const void* k, const int32_t
     p.N = N;
     p.H = H;
     p.G = G;
-    p.tokens = tokens_per_cta(N, sms);
+    p.tokens = tokens_per_cta(N, sms, kRopeTokens);
     p.by_rows = FastDiv((unsigned)(H + G));
     const cudaError_t e = D == 64 ? launch_rope<64, false>(p, stream) : launch_rope<128, false>(p, stream);
     return e == cudaSuccess ? GQA_OK : remember_cuda_error(e);
@@ -402,7 +407,7 @@ int gqa_append_paged(const gqa_rope_t* rope, const void* q, const void* k_new, c
     p.page_shift = __builtin_ctz((unsigned)page_size);
     p.num_pages = num_pages;
     p.max_pages = max_pages_per_seq;
-    p.tokens = tokens_per_cta(N, sms);
+    p.tokens = tokens_per_cta(N, sms, D == 64 ? kRopeTokens : 2);
     p.by_rows = FastDiv((unsigned)(H + 2 * G));
     const cudaError_t e = D == 64 ? launch_rope<64, true>(p, stream) : launch_rope<128, true>(p, stream);
     return e == cudaSuccess ? GQA_OK : remember_cuda_error(e);
