@@ -21,10 +21,9 @@ namespace gqa {
 
 constexpr int kRgTileShift = 7;
 constexpr int kRgTile = 1 << kRgTileShift;   // rows of a tile, and keys of a key tile
-// What a unit counts beyond its keys, and the least key tiles of a part of a unit: with
-// a pad of 256 and parts of two tiles 8 prompts of 1024 (16 heads, D 64) took 49 us, 24
-// ragged ones (32/8 heads, D 128) 380 and one of 16384 1475; with these 46, 364 and 1440.
-constexpr int kRgPad = 384;
+// Least key tiles of a part of a unit. With two, and a pad of 256, 8 prompts of 1024 (16
+// heads, D 64) took 49 us, 24 ragged ones (32/8 heads, D 128) 380 and one of 16384 1475;
+// with four, and 384, 46, 364 and 1440.
 constexpr int kRgMinPart = 4;
 constexpr int kRgMinShare = 512;      // least share of a CTA, in keys: twice that was no faster
 
@@ -48,25 +47,30 @@ struct RgUnit {
 };
 static_assert(sizeof(RgUnit) == 64, "a unit is read as 16-byte words");
 
-// Sizes that the line depends on: tokens of a tile, KV heads, and what a key of a unit
-// with rows in tile A alone counts, in eighths: its tiles go through both pipelines in
-// turn. Chunks among single tokens (48 sequences, 32/8 heads), D 128: 277 us with 6,
-// 260 with 5, 286 with 4; D 64: 240, 227, 212 and 249 with 3.
+// Sizes that the line depends on: tokens of a tile, KV heads, and two weights.
+// eighths: what a key of a unit with rows in tile A alone counts; its tiles go through
+// both pipelines in turn. Chunks among single tokens (48 sequences, 32/8 heads), D 128:
+// 277 us with 6, 260 with 5, 286 with 4; D 64: 240, 227, 212 and 249 with 3.
+// pad: what a unit counts beyond its keys, for its start and end. 24 ragged prompts, D 128:
+// 339 us with 256, 331 with 384, 343 with 512; D 64: 280 with 256, 286 with 320, 291 with
+// 384 (16 heads of their own 158, 162, 166).
 struct RgLine {
-    int tq, G, eighths;
+    int tq, G, eighths, pad;
 
-    __host__ __device__ static RgLine of(int tq, int G, int D) { return {tq, G, D == 128 ? 5 : 4}; }
+    __host__ __device__ static RgLine of(int tq, int G, int D) {
+        return D == 128 ? RgLine{tq, G, 5, 384} : RgLine{tq, G, 4, 256};
+    }
 
     __host__ __device__ int pairs(int n) const { return (int)(((unsigned)n + 2u * tq - 1) / (2u * tq)); }
     __host__ __device__ static long long base(const RgSeq& s) { return s.T > s.n ? s.T - s.n : 0; }
     // Where pair pr of a KV head starts, from the head's start.
     __host__ __device__ long long start(const RgSeq& s, int pr) const {
-        return pr * (base(s) + kRgPad) + (long long)tq * pr * (pr + 1ll);
+        return pr * (base(s) + pad) + (long long)tq * pr * (pr + 1ll);
     }
     __host__ __device__ bool single(const RgSeq& s, int pr) const { return s.n - pr * 2 * tq <= tq; }
     __host__ __device__ long long length(const RgSeq& s, int pr) const {
         const long long seen = (pr + 1ll) * 2 * tq, keys = base(s) + (seen < s.n ? seen : s.n);
-        return (single(s, pr) ? keys * eighths >> 3 : keys) + kRgPad;
+        return (single(s, pr) ? keys * eighths >> 3 : keys) + pad;
     }
     // Keys of such a unit by their length on the line (8 / 5 as 410 / 256).
     __host__ __device__ long long keys_of(long long y) const { return eighths == 5 ? y * 410 >> 8 : 2 * y; }

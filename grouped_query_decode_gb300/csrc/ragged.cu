@@ -108,7 +108,7 @@ int gqa_prefill_packed(const void* q, const void* k, const void* v, const int32_
     // No more CTAs than the rows have work for: all in one sequence, and the most that
     // cutting them into B leaves over.
     const RgLine line = RgLine::of(c.a.p.tq, G, D);
-    const long long most = (line.head({0, N, N}) + (long long)B * (kRgPad + 2 * c.a.p.tq)) * G / kRgMinShare + 1;
+    const long long most = (line.head({0, N, N}) + (long long)B * (line.pad + 2 * c.a.p.tq)) * G / kRgMinShare + 1;
     if (most < c.a.grid) c.a.grid = (int)most;
     if ((st = encode_rows_map(&c.a.tm_k, k, N, G, D, k_stride, 1, 128)) != GQA_OK) return st;
     if ((st = encode_rows_map(&c.a.tm_v, v, N, G, D, v_stride, 1, 128)) != GQA_OK) return st;
