@@ -258,8 +258,7 @@ __device__ __forceinline__ void rg_merge(const RaggedParams& p, const RgUnit& u,
 #pragma unroll 2
                 for (int i = 0; i < n; ++i) {
                     const float w = weights[(r - w0) * n + i].x;
-                    float4 v = o[i * items + item];
-                    if (w == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);     // a row without a key there has left no O
+                    const float4 v = o[i * items + item];                  // 0 of it, too, keeps a NaN
                     y.x = fmaf(v.x, w, y.x);
                     y.y = fmaf(v.y, w, y.y);
                     y.z = fmaf(v.z, w, y.z);
@@ -869,6 +868,9 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                         }
                     }
                     const bool flagged = *reinterpret_cast<volatile int*>(bad_flag + n % kRgUnits) == 1 + (int)(n / kRgUnits);
+                    // A row that sees a key somewhere has an O wherever its tile has one, of zeros where
+                    // it sees none of the keys. Weights that are 0 (far below the row's largest
+                    // score) multiply it all the same, so that a NaN in V stays one.
                     const int lim = u.pos0 + x * p.tq + tok;
                     const size_t orow = (size_t)(u.row0 + x * p.tq + tok) * p.H + (size_t)u.g * p.heads_per_group +
                                         (row - tok * p.heads_per_group);
@@ -889,11 +891,8 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                             uint32_t b[16];
                             tmem_ld16(o_t + D, b);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                // A pipeline whose tiles showed the row nothing has no O for it.
-                                const float oa = a0 == 0.f ? 0.f : __uint_as_float(o[i]) * a0;
-                                o[i] = __float_as_uint(a1 == 0.f ? oa : fmaf(__uint_as_float(b[i]), a1, oa));
-                            }
+                            for (int i = 0; i < 16; ++i)
+                                o[i] = __float_as_uint(fmaf(__uint_as_float(b[i]), a1, __uint_as_float(o[i]) * a0));
                         }
                         if (c + 16 == D && some) {
                             tc_fence_before();
@@ -901,7 +900,7 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                             if (lane == 0) mbar_arrive(o_empty + 8 * x);
                             if (lane == 0 && dual) mbar_arrive(o_empty + 8);
                         }
-                        if (l == 0.f)
+                        if (lim < 0)
 #pragma unroll
                             for (int i = 0; i < 16; ++i) o[i] = 0u;
                         if (valid && slot < 0) {
@@ -910,13 +909,13 @@ __global__ void __launch_bounds__(kRgThreads, 1)
                             for (int i = 0; i < 8; ++i)
                                 w[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
                             store32(p.out + orow * D + c, w, p.wide);
-                        } else if (valid && l != 0.f) {
+                        } else if (valid) {
                             store32(part + (size_t)r * D + c, o, true);
                             store32(part + (size_t)r * D + c + 8, o + 8, true);
                         }
                         __syncwarp();
                     }
-                    if (flagged && valid && l != 0.f) {          // a value that is not finite, where the row sees it
+                    if (flagged && valid) {                      // a value that is not finite, where the row sees it
 #pragma unroll 1
                         for (int c = 0; c < D; ++c) {
                             if (__ldcg(bad + (n % kRgUnits) * D + c) > lim) continue;
