@@ -366,9 +366,13 @@ int gqa_pages_compact(const gqa_page_pool_t* pools, int num_pools, const int32_t
  * its own, behind one another in tensors [N, heads, D]. cu[b] <= n < cu[b + 1]
  * are the rows of sequence b (int32 [B + 1], device, ascending); a sequence may
  * have none. Rows behind cu[B] (a batch padded to a captured size) are neither
- * used nor written. Entries of cu are clamped to [0, N] and to their
- * predecessor. One serving step is gqa_pages_reserve, gqa_append_paged (which
- * rotates queries and keys) and gqa_prefill_paged.
+ * used nor written. Entries of cu below 0 count as 0, above N as N. cu has to
+ * ascend, which no call checks: where it does not, a row may lie in several
+ * sequences, and it is undefined which of them writes it and whether rows in one
+ * alone are written; still nothing outside the arrays is read or written, nor a
+ * row or a position that is in no sequence's range. One serving step is
+ * gqa_pages_reserve, gqa_append_paged (which rotates queries and keys) and
+ * gqa_prefill_paged.
  *
  * Inputs q, k, v take a stride: the distance of their tokens in elements, a
  * multiple of 8 and at least heads * D, so that they may be views of one fused
