@@ -24,6 +24,7 @@
 #include "gqa_device.cuh"
 #include "gqa_launch.h"
 #include "gqa_paged_fp8.h"
+#include "gqa_rope_step.h"
 
 namespace gqa {
 namespace {
@@ -240,15 +241,7 @@ void set_rope(RopeParams* p, const gqa_rope_t* r, bool inverse) {
     p->interleaved = r ? r->interleaved != 0 : 0;
     p->gain = r ? (float)r->gain : 1.f;
     p->sign = inverse ? -1.f : 1.f;
-    for (int i = 0; i < p->half; ++i) {
-        // inv_freq / 2 pi to 2^-64: the product with 1 / 2 pi and what it lacks.
-        constexpr double kInv = 0.15915494309189535, kInvRest = -9.839338337591243e-18;
-        const double turns = r->inv_freq[i] * kInv;
-        const double rest = std::fma(r->inv_freq[i], kInv, -turns) + r->inv_freq[i] * kInvRest;
-        const double part = turns - std::floor(turns);           // 1 for the smallest below 0
-        p->step[i] = (part < 1.0 ? (unsigned long long)std::ldexp(part, 64) : 0) +
-                     (unsigned long long)(long long)std::ldexp(rest, 64);   // |rest| < 2^-5
-    }
+    for (int i = 0; i < p->half; ++i) p->step[i] = rope_step(r->inv_freq[i]);
 }
 
 bool aligned(const void* x, unsigned mask) { return (reinterpret_cast<uintptr_t>(x) & mask) == 0; }
