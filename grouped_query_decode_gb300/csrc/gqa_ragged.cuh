@@ -74,7 +74,8 @@ struct RgShape {
     static constexpr int kStagesK = D == 128 ? 2 : 5, kStagesV = D == 128 ? 2 : 5, kStages = kStagesK + kStagesV;
     static constexpr int kMlBytes = 2 * 128 * (8 + 8 + 4);
     static constexpr int kUnitBytes = kRgUnits * 64;
-    static constexpr int kMiscBytes = 384;
+    static constexpr int kTodo = 128 + kRgThreads / 32 * 8;      // behind the warps' sums
+    static constexpr int kMiscBytes = kTodo + 2 * 64;
     static constexpr int kBars = 3 * kStages + 2 * 10 + 2 * kRgUnits + 3;
     static constexpr int kSmemBytes =
         2 * kTile + kStages * kTile + kMlBytes + kUnitBytes + kMiscBytes + 8 * kBars;
@@ -85,6 +86,7 @@ struct RgShape {
     static constexpr uint32_t kColS = 0, kColP = kApart ? 256 : 0, kStepP = kApart ? 64 : 128, kColO = kApart ? 384 : 256;
     static constexpr uint32_t kHalfP = kApart ? 32 : 64;  // columns from the weights of the first 64 keys to the others'
     static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
+    static_assert(16 + 4 * kRgUnits <= 64 && kTodo % 16 == 0, "flags of units; units as 16-byte words");
     static_assert((2 + kStages) * kTile >= 25 * 1024 + 2 * 160 * D * 4 + 256, "a merge's weights, and a row of 160 parts twice");
 };
 
@@ -307,8 +309,8 @@ __global__ void __launch_bounds__(kRgThreads, 1)
     int* const bad_flag = reinterpret_cast<int*>(gen + 16);          // [units]
     long long* const first_s = reinterpret_cast<long long*>(gen + 64);   // [1], [2]: sequence and offset of the share's start
     RgShares* const shares = reinterpret_cast<RgShares*>(gen + 96);
-    long long* const warp_sum = reinterpret_cast<long long*>(gen + 128); // [16]
-    RgUnit* const todo = reinterpret_cast<RgUnit*>(gen + 256);       // [2]: units to merge
+    long long* const warp_sum = reinterpret_cast<long long*>(gen + 128); // [warps]
+    RgUnit* const todo = reinterpret_cast<RgUnit*>(gen + RS::kTodo);     // [2]: units to merge
     gen += RS::kMiscBytes;
     const uint32_t full = smem_addr(gen), empty = full + 8 * S, mended = empty + 8 * S;
     const uint32_t q_full = mended + 8 * S, q_empty = q_full + 16, s_full = q_empty + 16, p_full = s_full + 16;
