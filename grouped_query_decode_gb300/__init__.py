@@ -776,18 +776,19 @@ def gqa_append_paged(k_new, v_new, k_pages, v_pages, block_table, cu_new, seq_le
         raise GQADecodeError(rc, "gqa_append_paged")
 
 
-@functools.lru_cache(maxsize=4096)
-def _known_ragged_bytes(*sizes):
-    n = int(_call(sizes[-1], load().gqa_prefill_ragged_workspace_bytes, *sizes[:-1]))
+@functools.lru_cache(maxsize=64)
+def _known_ragged_bytes(D, device):
+    n = int(_call(device, load().gqa_prefill_ragged_workspace_bytes, 1, 1, 1, 1, D))
     if n == 0:
         raise _NoSize
     return n
 
 
-def _ragged_workspace_bytes(*sizes):
-    """By N, B, H, G, D and device."""
+def _ragged_workspace_bytes(D, device):
+    """Of any sizes that the calls take: a packed batch's workspace depends on D and the
+    device's SMs alone, so that steps of changing sizes ask once."""
     try:
-        return _known_ragged_bytes(*sizes)
+        return _known_ragged_bytes(D, device)
     except _NoSize:
         return 0
 
@@ -798,7 +799,7 @@ def gqa_prefill_ragged_workspace_bytes(N, B, H, G, D, device=None) -> int:
     if device is None:
         import torch
         device = torch.cuda.current_device()
-    return _ragged_workspace_bytes(N, B, H, G, D, device)
+    return int(_call(device, load().gqa_prefill_ragged_workspace_bytes, N, B, H, G, D))
 
 
 def _ragged_outputs(dev, q, out, lse, workspace):
@@ -839,7 +840,7 @@ def gqa_prefill_packed(q, k, v, cu_seqlens, scale, out, lse=None, stream=None, w
         raise ValueError("cu_seqlens must be [B + 1]")
     B = cu_seqlens.shape[0] - 1
     if workspace is None:
-        workspace = _workspace(_ragged_workspace_bytes(N, B, H, G, D, dev) or 256, q, dev, stream)
+        workspace = _workspace(_ragged_workspace_bytes(D, dev) or 256, q, dev, stream)
     rc = _launch(dev, load().gqa_prefill_packed, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(),
                  float(scale), out.data_ptr(), None if lse is None else lse.data_ptr(), N, B, H, G, D, qs, ks, vs,
                  workspace.data_ptr(), workspace.numel(), _raw_stream(stream, dev))
@@ -864,7 +865,7 @@ def gqa_prefill_paged(q, k_pages, v_pages, block_table, cu_new, seq_lens, scale,
     if Dk != D:
         raise ValueError("q must be [N, H, D] with the pages' D")
     if workspace is None:
-        workspace = _workspace(_ragged_workspace_bytes(N, B, H, G, D, dev) or 256, q, dev, stream)
+        workspace = _workspace(_ragged_workspace_bytes(D, dev) or 256, q, dev, stream)
     rc = _launch(dev, load().gqa_prefill_paged, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
                  block_table.data_ptr(), cu_new.data_ptr(), seq_lens.data_ptr(), float(scale), out.data_ptr(),
                  None if lse is None else lse.data_ptr(), N, B, H, G, D, qs, page_size, num_pages, most,

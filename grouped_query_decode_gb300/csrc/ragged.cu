@@ -29,7 +29,8 @@ int check_rows(const void* x, long long stride, int heads, int D) {
     return stride >= (1ll << 38) ? GQA_ERR_UNSUPPORTED : GQA_OK;
 }
 
-// One CTA per SM; the device's plan gives work to as many as there is work for.
+// One CTA per SM; the device's plan gives work to as many as there is work for. The
+// binding relies on it that N, B, H and G do not matter.
 size_t workspace_need(int D, int grid) {
     return rg_counter_bytes(grid) + rg_bad_bytes(D, grid) + sizeof(float) * 2 * grid * rg_slot_floats(D);
 }
