@@ -3,6 +3,7 @@
 // gqa_ragged.cuh.
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 
 #include "gqa_decode.h"
@@ -14,6 +15,9 @@ namespace gqa {
 namespace {
 
 bool aligned(const void* x, unsigned mask) { return (reinterpret_cast<uintptr_t>(x) & mask) == 0; }
+
+constexpr float kLog2E = 1.4426950408889634f;     // exponentials are of base 2
+bool usable(float scale) { return scale > 0.f && std::isfinite(scale * kLog2E); }
 
 int check_sizes(int N, int B, int H, int G, int D) {
     if (N < 0 || B <= 0 || H <= 0 || G <= 0 || D <= 0) return GQA_ERR_INVALID_ARG;
@@ -59,7 +63,7 @@ int begin(Call& c, const void* q, const int32_t* cu, float scale, void* out, flo
     p.part = reinterpret_cast<float*>(reinterpret_cast<char*>(p.bad) + rg_bad_bytes(D, sms));
     p.tag = call_tag();
     wait_knobs(&p.wait_timeout_ns, &p.skip_tile);
-    p.scale_log2 = scale * 1.4426950408889634f;
+    p.scale_log2 = scale * kLog2E;
     p.N = N;
     p.B = B;
     p.H = H;
@@ -98,7 +102,7 @@ int gqa_prefill_packed(const void* q, const void* k, const void* v, const int32_
     int st = check_sizes(N, B, H, G, D);
     if (st != GQA_OK) return st;
     if (N == 0) return GQA_OK;              // tensors without rows have no address
-    if (!q || !k || !v || !cu_seqlens || !out || !(scale > 0.f) || scale > 3.0e38f) return GQA_ERR_INVALID_ARG;
+    if (!q || !k || !v || !cu_seqlens || !out || !usable(scale)) return GQA_ERR_INVALID_ARG;
     if ((st = check_rows(q, q_stride, H, D)) != GQA_OK || (st = check_rows(k, k_stride, G, D)) != GQA_OK ||
         (st = check_rows(v, v_stride, G, D)) != GQA_OK)
         return st;
@@ -123,7 +127,7 @@ int gqa_prefill_paged(const void* q, const void* k_pages, const void* v_pages, c
     int st = check_sizes(N, B, H, G, D);
     if (st != GQA_OK) return st;
     if (N == 0) return GQA_OK;              // tensors without rows have no address
-    if (!q || !k_pages || !v_pages || !block_table || !cu_new || !seq_lens || !out || !(scale > 0.f) || scale > 3.0e38f ||
+    if (!q || !k_pages || !v_pages || !block_table || !cu_new || !seq_lens || !out || !usable(scale) ||
         page_size <= 0 || num_pages <= 0 || max_pages_per_seq <= 0)
         return GQA_ERR_INVALID_ARG;
     if (page_size < 16 || page_size > 65536 || (page_size & (page_size - 1))) return GQA_ERR_UNSUPPORTED;

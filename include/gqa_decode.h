@@ -445,7 +445,8 @@ int gqa_append_paged(const gqa_rope_t* rope, const void* q, const void* k_new, c
 /*
  * Attention of whole prompts, without a cache: token s of a sequence attends to
  * the sequence's tokens 0..s. q [N, H, D], k and v [N, G, D]; out [N, H, D] bf16
- * and lse [N, H] (may be NULL) are dense. scale finite and > 0, H / G <= 128.
+ * and lse [N, H] (may be NULL) are dense. 0 < scale <= 2.35e38 (scale * log2(e)
+ * stays finite), H / G <= 128.
  *
  * gqa_prefill_paged: the same for chunks, with keys and values from pages
  * (layouts, block table and page_size as for gqa_decode_paged): new token s of
