@@ -366,7 +366,8 @@ int gqa_append_paged(const gqa_rope_t* rope, const void* q, const void* k_new, c
     if (st != GQA_OK) return st;
     if (!q) H = 0;
     if ((long long)max_pages_per_seq * page_size >= (1ll << 31) - 128 || (long long)num_pages * G >= (1ll << 31) ||
-        (long long)N * (H + 2ll * G) >= (1ll << 31) || H + 2ll * G >= (1 << 20))
+        (long long)N * (H + 2ll * G) >= (1ll << 31) || H + 2ll * G >= (1 << 20) ||
+        B >= (1ll << 31) - 33)                           // find_sequence counts B + 1 and 31 more
         return GQA_ERR_UNSUPPORTED;
     if (!aligned(block_table, 3u) || !aligned(cu_new, 3u) || !aligned(seq_lens, 3u) || !aligned(k_pages, 15u) ||
         !aligned(v_pages, 15u))
