@@ -40,9 +40,13 @@
 //   1120: both are nearly full, and what is left is their handing over to each other,
 //   some 450 of a step's 2900 cycles (a step: one key tile with both row tiles).
 // - single tokens: HBM (64 sequences of up to 16384 keys 386 us, 6.6 TB/s).
+// - D 64: the softmax's chain. A step's products are 1024 cycles, but scores, weights and
+//   the next scores follow one another, and a step takes 2800, as with D 128 (the long
+//   prompt 1192 us, 585 at the roofline; 24 ragged ones 286, 110 at the roofline).
 // - short sequences: 2 to 3 us at a unit's start and end, 4 us before a launch's first
 //   scores, 4 to 15 us for a merge (8 prompts of 1024, 16 heads, D 64 41 us, 10 at
-//   the roofline; chunks among single tokens 292 us, 146 at the roofline).
+//   the roofline; 64 single tokens of 1024 keys, D 64, 42, 20 at the roofline; chunks
+//   among single tokens 260 to 290 us by the order of the sequences, 146 at the roofline).
 //
 // Why this split of the warps: one softmax thread per row held 128 scores, and the 8
 // prompts took 54 us for 48 with two; one pipeline for units with one row tile, and

@@ -21,9 +21,13 @@ namespace gqa {
 
 constexpr int kRgTileShift = 7;
 constexpr int kRgTile = 1 << kRgTileShift;   // rows of a tile, and keys of a key tile
-// Least key tiles of a part of a unit. With two, and a pad of 256, 8 prompts of 1024 (16
-// heads, D 64) took 49 us, 24 ragged ones (32/8 heads, D 128) 380 and one of 16384 1475;
-// with four, and 384, 46, 364 and 1440.
+// The times of this file are of one batch in a captured graph, in three orders of its
+// sequences, one after another; calls from Python whose inputs change take up to 10 %
+// longer.
+//
+// Least key tiles of a part of a unit: 8 prompts of 1024 (16 heads, D 64) take 43.9 us
+// with two, 41.5 with four, 41.3 with six; 24 ragged ones (16 heads of their own, D 64)
+// 161, 161 and 164; with 32/8 heads and D 128, and one of 16384, no difference.
 constexpr int kRgMinPart = 4;
 constexpr int kRgMinShare = 512;      // least share of a CTA, in keys: twice that was no faster
 
@@ -49,11 +53,13 @@ static_assert(sizeof(RgUnit) == 64, "a unit is read as 16-byte words");
 
 // Sizes that the line depends on: tokens of a tile, KV heads, and two weights.
 // eighths: what a key of a unit with rows in tile A alone counts; its tiles go through
-// both pipelines in turn. Chunks among single tokens (48 sequences, 32/8 heads), D 128:
-// 277 us with 6, 260 with 5, 286 with 4; D 64: 240, 227, 212 and 249 with 3.
+// both pipelines in turn. (A single token's tiles wait for copies, a short chunk's for
+// products; one number serves both.) Chunks among single tokens (48 sequences, 32/8
+// heads), D 128: 276 us with 6, 259 with 5, 286 with 4; D 64: 238, 223, 212 and 249 with
+// 3 (16 heads of their own 273, 244, 224 and 241).
 // pad: what a unit counts beyond its keys, for its start and end. 24 ragged prompts, D 128:
-// 339 us with 256, 331 with 384, 343 with 512; D 64: 280 with 256, 286 with 320, 291 with
-// 384 (16 heads of their own 158, 162, 166).
+// 351 us with 256, 336 with 384, 348 with 512; D 64: 286 with 256, 293 with 320, 298 with
+// 384 (16 heads of their own 161, 164, 169).
 struct RgLine {
     int tq, G, eighths, pad;
 

@@ -146,7 +146,10 @@ __global__ void __launch_bounds__(kRopeThreads, APPEND ? 8 : 6) rope_kernel(cons
     };
 
     if (!p.interleaved && (p.half & 7)) {
-        // Halves that do not start on 16 bytes: a warp per row, through shared memory.
+        // Halves that do not start on 16 bytes: a warp per row, through shared memory. Half of
+        // the lanes copy, one row is under way, and pairs are read and written 2 bytes at a
+        // time: 16384 tokens, 32/8 heads, D 128, 50 elements rotated take 99 us, 48 take 53;
+        // 5818 tokens appended 42 us for 27.
         uint16_t* mine = row_s[warp];
         for (int item = warp; item < total; item += kRopeThreads / 32) {
             int w;
