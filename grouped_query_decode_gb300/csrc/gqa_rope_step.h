@@ -7,7 +7,7 @@ namespace gqa {
 
 // inv_freq / 2 pi modulo a turn, in units of 2^-64 turns. The magnitude is converted
 // and the sign applied to the result: minus a small frequency lies just below a whole
-// turn, where a double holds 2^-53 of it at best, 4e-7 radians after 2^31 positions.
+// turn, where a double is off by up to 2^-54 of it, 7e-7 radians after 2^31 positions.
 inline unsigned long long rope_step(double inv_freq) {
     // The product with 1 / 2 pi and what it lacks.
     constexpr double kInv = 0.15915494309189535, kInvRest = -9.839338337591243e-18;
